@@ -249,6 +249,127 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
                 cudaStream_t stream);
 
 /*
+ * Training-side operators: what produces the gradients that the owner's step
+ * and AdamW consume.  The DMuon pages train the models that these stand in
+ * (home page, "LLM Pretraining": gate, up and down projections in the Muon set,
+ * the output head in AdamW's) but do not write the operators out.
+ *
+ * Conventions beside those above:
+ *  - Activations, weights and gradients are bf16.  Products accumulate in fp32
+ *    on the tensor cores; an intermediate that feeds a second product (h, dgate,
+ *    dup, the gradient of the logits) is rounded to bf16 once, as its operand.
+ *  - A weight is a PyTorch parameter (out, in), contiguous.  It is 16-byte
+ *    aligned where its row length is a multiple of 8 (else it is copied to the
+ *    workspace, padded, on every call).
+ *  - A token matrix (x, y, dy, dx, hidden, dhidden) is `tokens` rows of `hidden`
+ *    elements, `ld` >= hidden elements apart.  Rows that are 16-byte aligned are
+ *    read and written in place; others are copied, or written with plain stores.
+ *  - tokens == 0 is legal: nothing is written except weight gradients, which are
+ *    set to zero.
+ *  - Limits: tokens <= 4194304, hidden and ffn <= 524288, vocab <= 4194304.
+ *  - Workspaces are 256-byte aligned; one sized for `tokens` serves fewer.
+ *    Device-side failures go to its error word (dmuon_stream_status); zero the
+ *    first 256 bytes once.
+ */
+
+/* Activation of the gated feed-forward block. */
+typedef enum {
+  DMUON_ACT_SILU = 0,      /* x * sigmoid(x) */
+  DMUON_ACT_GELU = 1,      /* x * Phi(x) */
+  DMUON_ACT_GELU_TANH = 2  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+} dmuon_activation;
+
+/* What the forward pass keeps of gate = x Wg^T and up = x Wu^T. */
+typedef enum {
+  DMUON_SAVE_NONE = 0,  /* nothing (inference) */
+  DMUON_SAVE_BF16 = 1,  /* both in bf16 */
+  DMUON_SAVE_ACT8 = 2   /* both in 8 bits (dmuon_act8_save's layout) */
+} dmuon_save;
+
+/*
+ * dmuon_act8_save / dmuon_act8_load -- an activation in 8 bits and back.
+ * Each row is cut into blocks of 32 columns (the last may be shorter); a block
+ * is stored as 8-bit codes and one bf16 scale:
+ *   scale = the smallest bf16 number >= max|x| / 127 (at least 2^-126); 0 for a
+ *           block of zeros
+ *   code  = x / scale rounded to the nearest integer, ties to even
+ * and comes back as code * scale, rounded to the output's type.  A block that
+ * holds a NaN or an infinity comes back as NaN throughout.
+ *   x, out   device, `rows` rows of `cols` elements, ld elements apart, F32 or BF16
+ *   codes    device, rows x cols int8, contiguous
+ *   scales   device, rows x ceil(cols / 32) bf16, contiguous
+ * One launch each; no workspace.
+ */
+int dmuon_act8_save(int64_t rows, int64_t cols, const void* x, int64_t x_ld, int x_dt,
+                    int8_t* codes, void* scales, cudaStream_t stream);
+int dmuon_act8_load(int64_t rows, int64_t cols, const int8_t* codes, const void* scales,
+                    void* out, int64_t out_ld, int out_dt, cudaStream_t stream);
+
+/* Sizes and kind of a gated feed-forward block. */
+typedef struct {
+  int64_t tokens, hidden, ffn;
+  int activation;  /* dmuon_activation */
+  int save;        /* dmuon_save: written by forward, read by backward */
+} dmuon_ffn_shape;
+
+/*
+ * dmuon_ffn_forward -- gated feed-forward block:
+ *   gate = x Wg^T,  up = x Wu^T,  h = act(gate) * up,  y = h Wd^T
+ * Both projections, the activation and the product run in one kernel.
+ *   w_gate, w_up  (ffn, hidden);  w_down  (hidden, ffn)
+ *   saved   host array of device pointers, contiguous (tokens, ffn) tensors:
+ *           SAVE_BF16 {gate, up}; SAVE_ACT8 {gate codes, gate scales, up codes,
+ *           up scales}; may be NULL for SAVE_NONE
+ */
+size_t dmuon_ffn_workspace_bytes(const dmuon_ffn_shape* shape, int backward);
+int dmuon_ffn_forward(const dmuon_ffn_shape* shape, const void* x, int64_t x_ld,
+                      const void* w_gate, const void* w_up, const void* w_down, void* y,
+                      int64_t y_ld, void* const* saved, void* workspace, size_t ws_bytes,
+                      cudaStream_t stream);
+
+/*
+ * dmuon_ffn_backward -- its gradients, from what forward kept:
+ *   dh = dy Wd,  dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *   dx = dgate Wg + dup Wu
+ *   dWg = dgate^T x,  dWu = dup^T x,  dWd = dy^T h
+ * (h is recomputed).  The weight gradients are written, not added to.
+ */
+int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_ld, const void* x,
+                       int64_t x_ld, const void* w_gate, const void* w_up, const void* w_down,
+                       void* const* saved, void* dx, int64_t dx_ld, void* dw_gate, void* dw_up,
+                       void* dw_down, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Sizes of an output head. */
+typedef struct {
+  int64_t tokens, hidden, vocab;
+} dmuon_xent_shape;
+
+/*
+ * dmuon_xent -- softmax cross entropy of the logits hidden W^T against one target
+ * per token, without keeping the logits:
+ *   lse[t] = log sum_v exp(hidden_t . W_v),  loss[t] = lse[t] - hidden_t . W_target[t]
+ * and, when asked, the gradients of sum_t grad_loss[t] * loss[t]:
+ *   dhidden = G W,  dW = G^T hidden,  G[t,v] = grad_loss[t] (exp(z[t,v] - lse[t]) - [v = target[t]])
+ *   target     device, int64 per token; a target outside [0, vocab) masks its
+ *              token: loss, lse and dhidden are 0 and nothing of its hidden row
+ *              (NaN of padding, say) reaches dW
+ *   grad_loss  device, fp32 per token (1/n for a mean over n tokens), or NULL
+ *              for the loss alone; then dhidden and dweight are NULL too
+ *   loss, lse  device, fp32 per token
+ *   dhidden    (tokens, hidden), rows dhidden_ld apart;  dweight (vocab, hidden)
+ * The logits never exist as a tensor: each piece of the vocabulary is reduced
+ * where it is computed.  For gradients the exponentials of a bounded number of
+ * tokens (about 2.2 GB of 16-bit values; at least 256 tokens) wait in the
+ * workspace; with more tokens than that, dW is summed over the pieces in fp32
+ * (4 * vocab * hidden bytes more workspace).
+ */
+size_t dmuon_xent_workspace_bytes(const dmuon_xent_shape* shape, int grads);
+int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden_ld,
+               const void* weight, const int64_t* target, const float* grad_loss, float* loss,
+               float* lse, void* dhidden, int64_t dhidden_ld, void* dweight, void* workspace,
+               size_t ws_bytes, cudaStream_t stream);
+
+/*
  * dmuon_stream_status -- synchronises `stream`, then reports (and clears) the
  * device error word kept in `workspace`: DMUON_OK, DMUON_ERR_TIMEOUT when a
  * bounded device wait gave up, DMUON_ERR_CUDA when the stream holds a CUDA

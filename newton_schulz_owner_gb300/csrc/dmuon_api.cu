@@ -3,6 +3,7 @@
 #include "dmuon.h"
 #include "launch.h"
 #include "tables.h"
+#include "train.h"
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -1130,6 +1131,19 @@ int run(const Request& R) {
 }
 
 }  // namespace
+
+int library_device(int* device, int* sms, int* max_clusters) {
+  DevInfo D;
+  const int st = device_info(&D);
+  if (st != DMUON_OK) return st;
+  if (cudaGetDevice(device) != cudaSuccess) return DMUON_ERR_CUDA;
+  *sms = D.sms;
+  *max_clusters = D.max_clusters;
+  return DMUON_OK;
+}
+
+TensorMapEncode library_tensor_map_encoder() { return tensor_map_encoder(); }
+
 }  // namespace dm
 
 namespace dm {

@@ -36,6 +36,7 @@
 // Pair tiles are handed out statically (tile = cluster + k * clusters), so all
 // roles of both CTAs walk the same sequence without talking to each other.
 #include "dmuon.h"
+#include "epi.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "tables.h"
@@ -64,7 +65,6 @@ constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;
-constexpr int kEpiBufBytes = 32 * 32 * 2;              // one 32 x 32 bf16 epilogue chunk
 constexpr int kEpiBytes = kEpiWarps * 2 * kEpiBufBytes;  // two chunk buffers per epilogue warp
 constexpr int kBarBytes = 512;
 constexpr size_t kSmemBytes =
@@ -72,9 +72,6 @@ constexpr size_t kSmemBytes =
 static_assert(kSmemBytes <= 232448, "dynamic shared memory above the sm_100 per-block limit");
 static_assert((2 * kStages + 5 + 2 * kEpiWarps) * 8 + 8 + 40 <= kBarBytes,
               "barrier area too small");
-// After a bounded wait gives up, wait this long before leaving so that copies
-// and MMAs already issued to this CTA's shared memory / TMEM have landed.
-constexpr long long kAbortSettleCycles = 400000;
 
 struct TileInfo {
   int bucket, mat, ti, tj;
@@ -162,16 +159,6 @@ DM_DEV int k_extent(const GemmArgs& g, const Bucket& B) {
 
 DM_DEV const void* tmap_of(const GemmArgs& g, const Bucket& B, int slot) {
   return g.tmaps + size_t(B.tmap + slot) * 128;
-}
-
-DM_DEV void raise_abort(int* err, volatile int* abort_flag) {
-  *abort_flag = 1;
-  atomicCAS(err, 0, int(DMUON_ERR_TIMEOUT));
-}
-
-DM_DEV uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&t);
 }
 
 // ------------------------------------------------------------------ roles
@@ -329,42 +316,9 @@ DM_DEV void mma_issuer(const GemmArgs& g, uint8_t* sA, uint8_t* sB, uint64_t* fu
 // A chunk goes through one of the warp's two 2 KB shared-memory buffers, laid
 // out as the TMA 64-byte swizzle expects (16-byte unit u of row i at byte
 // i*64 + ((u ^ ((i >> 1) & 3)) << 4)): each thread writes its whole row there
-// without bank conflicts, and one lane stores the chunk to global memory with
-// a TMA tensor store.  The a*X operand of B*X arrives the same way, by TMA
+// without bank conflicts (epi.cuh), and one lane stores the chunk to global memory
+// with a TMA tensor store.  The a*X operand of B*X arrives the same way, by TMA
 // loads issued ahead of time into the chunk's buffer.
-DM_DEV uint32_t epi_off(int row, int unit) {
-  return uint32_t(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
-}
-
-DM_DEV void epi_store_row(uint32_t buf, int row, const float (&o)[32]) {
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    st_shared_v4(buf + epi_off(row, u), pack_bf16x2(o[8 * u], o[8 * u + 1]),
-                 pack_bf16x2(o[8 * u + 2], o[8 * u + 3]), pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
-                 pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-}
-
-DM_DEV void epi_load_row(uint32_t buf, int row, float (&x)[32]) {
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    uint32_t w[4];
-    ld_shared_v4(buf + epi_off(row, u), w[0], w[1], w[2], w[3]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
-      x[8 * u + 2 * k] = f.x;
-      x[8 * u + 2 * k + 1] = f.y;
-    }
-  }
-}
-
-// Element (row, col) of a chunk buffer.
-DM_DEV void epi_store_elem(uint32_t buf, int row, int col, float v) {
-  const __nv_bfloat16 b = __float2bfloat16_rn(v);
-  st_shared_b16(buf + epi_off(row, col >> 3) + uint32_t((col & 7) * 2),
-                *reinterpret_cast<const uint16_t*>(&b));
-}
-
 DM_DEV const void* emap_of(const GemmArgs& g, const Bucket& B, int slot) {
   return g.tmaps + size_t(B.tmap + kSlots + slot) * 128;
 }

@@ -95,6 +95,24 @@ DM_DEV void tma_load_3d_u32(uint32_t smem_dst, const void* tmap, uint32_t bar, i
       : "memory");
 }
 
+// 2-D tiled load into this CTA's shared memory, completion counted on an mbarrier
+// that may live in the peer CTA of a pair (shared::cluster address).
+DM_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster, int c0,
+                             int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+// 2-D tiled store shared -> global; elements outside the tensor are dropped.
+DM_DEV void tma_store_2d(const void* tmap, uint32_t smem_src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_src), "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // 3-D tiled store shared -> global; elements outside the tensor are dropped.
 // Completion is tracked per thread with bulk async-groups.
 DM_DEV void tma_store_3d(const void* tmap, uint32_t smem_src, int c0, int c1, int c2) {

@@ -1,0 +1,117 @@
+// Tables and host-side launchers of the training-side operators: the gated
+// feed-forward block, softmax cross entropy over a vocabulary, and activations
+// kept in 8 bits.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace dm {
+
+// ------------------------------------------------------------------ shared with dmuon_api.cu
+// Status of the current device (DMUON_OK when it is usable), its SM count and
+// how many CTA pairs of the product kernels fit on it at once.
+int library_device(int* device, int* sms, int* max_clusters);
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncode library_tensor_map_encoder();
+
+// ------------------------------------------------------------------ tensor-core products
+// Elements of one 8-bit activation block (they share a bf16 scale).
+constexpr int kActBlock = 32;
+// Columns of the vocabulary whose exponentials share a reference maximum.
+constexpr int kXentGroup = 128;
+
+// What a product's epilogue does with the fp32 accumulator.
+enum LinEpi {
+  kLinStore = 0,    // C = bf16(acc), optionally through an fp32 running sum
+  kLinGlu = 1,      // h = act(gate) * up, gate / up kept as asked
+  kLinGluGrad = 2,  // acc = dh: dgate, dup and h from the kept gate / up
+  kLinXent = 3      // logits: group maxima and sums, exponentials kept as asked
+};
+enum LinKeep { kKeepNone = 0, kKeepBf16 = 1, kKeepAct8 = 2 };
+
+constexpr int kLinMaps = 12;     // tensor maps of one launch
+constexpr int kLinProblems = 3;  // products of one launch
+
+struct LinProblem {
+  int m, n;              // output rows / columns (kLinGlu: n = ffn, 128 of it per tile)
+  int tiles_m, tiles_n;
+  int kb0, kb1;          // K blocks from the first and the second operand pair
+  int tile_begin;        // first tile of this product in the launch
+  int a0, b0, a1, b1;    // operand maps (kLinGlu: b0 = gate's weight, b1 = up's)
+  int c_map;             // output map, or -1: c is written with plain stores
+  __nv_bfloat16* c;
+  long long c_ld;
+};
+
+struct LinArgs {
+  CUtensorMap maps[kLinMaps];
+  LinProblem prob[kLinProblems];
+  int n_prob;
+  int full_tiles;        // tiles computed whole; the rest in `split` parts along K
+  int split;
+  int total_units;       // full_tiles + split * (tiles - full_tiles)
+  float* partial;        // fp32 parts of the split tiles
+  int* arrived;          // arrivals per split tile and epilogue warp, zero between launches
+  int* err;
+  // kLinStore: fp32 running sum over launches (row pitch = n of the product)
+  float* sum;
+  int sum_read, sum_write;  // add what `sum` holds; write the sum there instead of C
+  // kLinGlu / kLinGluGrad
+  int act, keep;
+  int ffn;
+  int kept_vec;          // rows of the kept tensors allow 16-byte access
+  void *gate, *up;                          // bf16 values or 8-bit codes
+  __nv_bfloat16 *gate_scale, *up_scale;     // 8-bit block scales
+  int map_gate, map_up;                     // kLinGlu, bf16: output maps (kept_vec)
+  int map_dup, map_h;                       // kLinGluGrad: output maps beside c_map (dgate)
+  // kLinXent
+  const long long* target;
+  float* target_logit;   // one per token
+  float2* group_stat;    // (maximum, sum of exponentials) [group][token], pitch stat_ld
+  long long stat_ld;
+};
+
+size_t lin_partial_bytes();
+size_t lin_arrived_bytes();
+cudaError_t lin_prepare();  // once per device
+// Split the tiles of the last, partly filled wave along K (sets full_tiles ..
+// total_units from the products' tile counts).
+void lin_schedule(LinArgs& g, int clusters);
+cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
+                       cudaStream_t s);
+
+// ------------------------------------------------------------------ memory-bound kernels
+cudaError_t launch_act8_save(long long rows, long long cols, const void* x, long long ld,
+                             bool bf16, signed char* codes, __nv_bfloat16* scales,
+                             cudaStream_t s);
+cudaError_t launch_act8_load(long long rows, long long cols, const signed char* codes,
+                             const __nv_bfloat16* scales, void* out, long long ld, bool bf16,
+                             cudaStream_t s);
+// Copy rows x cols bf16 to rows of pitch `dst_ld` (a multiple of 8); a row whose
+// target lies outside [0, vocab) is written as zeros when `target` is given.
+cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16* src,
+                             long long src_ld, __nv_bfloat16* dst, long long dst_ld,
+                             const long long* target, long long vocab, cudaStream_t s);
+// Rows rows x cols of zeros (pitch ld).
+cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst, long long ld,
+                             cudaStream_t s);
+struct XentRows {
+  long long tokens, vocab;
+  const long long* target;
+  const float* grad_loss;   // null: no gradients
+  const float* target_logit;
+  const float2* group_stat;
+  long long stat_ld;
+  float *loss, *lse;
+};
+cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s);
+// Exponentials (fp16) to gradients of the logits (bf16), in place.
+cudaError_t launch_xent_grad(const XentRows& r, void* e, long long e_ld, cudaStream_t s);
+
+}  // namespace dm

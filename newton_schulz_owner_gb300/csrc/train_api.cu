@@ -1,0 +1,582 @@
+// C ABI of the training-side operators: argument checks, workspace layout, tensor
+// maps and launch sequences.  See include/dmuon.h.
+#include "dmuon.h"
+#include "launch.h"
+#include "train.h"
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+namespace dm {
+namespace {
+
+constexpr size_t kHdrBytes = 256;  // workspace header: device error word
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxDim = int64_t(1) << 19,
+                  kMaxVocab = int64_t(1) << 22;
+// Gradients of the logits are formed for as many tokens at a time as fit here
+// (a multiple of 256, at least 256); the loss alone keeps no logits and only
+// bounds the group statistics.
+constexpr size_t kLogitBytes = size_t(2200) << 20;
+constexpr int64_t kLossTokens = 16384;
+
+using bf16 = __nv_bfloat16;
+
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Ready the current device: the products' shared memory opt-in, once.
+int device_ready(int* max_clusters) {
+  int d = 0, sms = 0;
+  const int st = library_device(&d, &sms, max_clusters);
+  if (st != DMUON_OK) return st;
+  static std::mutex mu;
+  static bool ready[kMaxDevices] = {};
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ready[d]) {
+    if (lin_prepare() != cudaSuccess) return DMUON_ERR_CUDA;
+    ready[d] = true;
+  }
+  return DMUON_OK;
+}
+
+// Hands out 256-byte aligned pieces of a workspace (base may be null: sizes only).
+struct Carve {
+  unsigned char* base;
+  size_t used = 0;
+  explicit Carve(void* b) : base(static_cast<unsigned char*>(b)) {}
+  template <typename T>
+  T* take(size_t bytes) {
+    T* p = base == nullptr ? nullptr : reinterpret_cast<T*>(base + used);
+    used = align_up(used + bytes, 256);
+    return p;
+  }
+};
+
+// The part of every workspace that the products use.
+struct ProductSpace {
+  int* err;
+  int* arrived;
+  float* partial;
+};
+ProductSpace take_product_space(Carve& c) {
+  ProductSpace s;
+  s.err = c.take<int>(kHdrBytes);
+  s.arrived = c.take<int>(lin_arrived_bytes());
+  s.partial = c.take<float>(lin_partial_bytes());
+  return s;
+}
+
+// One launch under construction.
+struct Launch {
+  LinArgs g{};
+  int n_maps = 0;
+  bool ok = true;
+
+  explicit Launch(const ProductSpace& s) {
+    g.err = s.err;
+    g.arrived = s.arrived;
+    g.partial = s.partial;
+  }
+  int map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool output) {
+    const TensorMapEncode enc = library_tensor_map_encoder();
+    if (enc == nullptr || n_maps >= kLinMaps) {
+      ok = false;
+      return 0;
+    }
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint32_t box_in[2] = {64, 128}, box_out[2] = {32, 32}, es[2] = {1, 1};
+    ok = ok && enc(&g.maps[n_maps], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                   dims, strides, output ? box_out : box_in, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   output ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return n_maps++;
+  }
+  // An operand stored as `rows` rows of `cols` contiguous elements; whether it
+  // is K-major or MN-major, a box is 64 columns x 128 rows.
+  int operand(const bf16* p, int64_t cols, int64_t rows, int64_t ld) {
+    return map(p, cols, rows, ld, false);
+  }
+  int output(const bf16* p, int64_t cols, int64_t rows, int64_t ld) {
+    return map(p, cols, rows, ld, true);
+  }
+  LinProblem& problem(int64_t m, int64_t n, int64_t cols_per_tile, int64_t k0, int64_t k1) {
+    LinProblem& P = g.prob[g.n_prob++];
+    P.m = int(m);
+    P.n = int(n);
+    P.tiles_m = int(ceil_div(m, 256));
+    P.tiles_n = int(ceil_div(n, cols_per_tile));
+    P.kb0 = int(ceil_div(k0, 128));
+    P.kb1 = int(ceil_div(k1, 128));
+    P.c_map = -1;
+    return P;
+  }
+  // C: TMA where its rows allow it, plain stores otherwise.
+  void store_to(LinProblem& P, bf16* c, int64_t ld) {
+    P.c = c;
+    P.c_ld = ld;
+    if (aligned(c, 16) && ld % 8 == 0) P.c_map = output(c, P.n, P.m, ld);
+  }
+  int run(int epi, bool a_mn, bool b_mn, int clusters, cudaStream_t s) {
+    if (!ok) return DMUON_ERR_CUDA;
+    lin_schedule(g, clusters);
+    if (g.split > 1 &&
+        cudaMemsetAsync(g.arrived, 0, lin_arrived_bytes(), s) != cudaSuccess)
+      return DMUON_ERR_CUDA;
+    return launch_lin(g, epi, a_mn, b_mn, clusters, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
+  }
+};
+
+// A bf16 matrix as TMA can read it: where it lies, or copied to `copy`.
+int readable(const bf16* p, int64_t rows, int64_t cols, int64_t ld, bf16* copy, cudaStream_t s,
+             const bf16** out, int64_t* out_ld) {
+  if (aligned(p, 16) && ld % 8 == 0) {
+    *out = p;
+    *out_ld = ld;
+    return DMUON_OK;
+  }
+  *out = copy;
+  *out_ld = up8(cols);
+  return launch_copy_rows(rows, cols, p, ld, copy, *out_ld, nullptr, 0, s) == cudaSuccess
+             ? DMUON_OK
+             : DMUON_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ feed-forward block
+bool ffn_shape_ok(const dmuon_ffn_shape* s) {
+  return s != nullptr && s->tokens >= 0 && s->tokens <= kMaxTokens && s->hidden >= 1 &&
+         s->hidden <= kMaxDim && s->ffn >= 1 && s->ffn <= kMaxDim &&
+         s->activation >= DMUON_ACT_SILU && s->activation <= DMUON_ACT_GELU_TANH &&
+         s->save >= DMUON_SAVE_NONE && s->save <= DMUON_SAVE_ACT8;
+}
+
+struct FfnSpace {
+  ProductSpace ps;
+  bf16 *x, *dy, *h, *dgate, *dup, *w_gate, *w_up, *w_down;
+  size_t bytes;
+};
+FfnSpace ffn_space(const dmuon_ffn_shape& s, bool backward, void* ws) {
+  Carve c(ws);
+  FfnSpace f{};
+  const size_t t = size_t(s.tokens), d8 = size_t(up8(s.hidden)), f8 = size_t(up8(s.ffn));
+  f.ps = take_product_space(c);
+  f.x = c.take<bf16>(t * d8 * 2);
+  f.h = c.take<bf16>(t * f8 * 2);
+  if (backward) {
+    f.dy = c.take<bf16>(t * d8 * 2);
+    f.dgate = c.take<bf16>(t * f8 * 2);
+    f.dup = c.take<bf16>(t * f8 * 2);
+  }
+  if (s.hidden % 8 != 0) {
+    f.w_gate = c.take<bf16>(size_t(s.ffn) * d8 * 2);
+    f.w_up = c.take<bf16>(size_t(s.ffn) * d8 * 2);
+  }
+  if (s.ffn % 8 != 0) f.w_down = c.take<bf16>(size_t(s.hidden) * f8 * 2);
+  f.bytes = c.used;
+  return f;
+}
+
+struct FfnWeights {
+  const bf16 *gate, *up, *down;
+  int64_t ld_in, ld_down;  // row pitch of gate and up, of down
+};
+int ffn_weights(const dmuon_ffn_shape& s, const FfnSpace& f, const void* wg, const void* wu,
+                const void* wd, cudaStream_t st, FfnWeights* w) {
+  int e = readable(static_cast<const bf16*>(wg), s.ffn, s.hidden, s.hidden, f.w_gate, st, &w->gate,
+                   &w->ld_in);
+  if (e == DMUON_OK)
+    e = readable(static_cast<const bf16*>(wu), s.ffn, s.hidden, s.hidden, f.w_up, st, &w->up,
+                 &w->ld_in);
+  if (e == DMUON_OK)
+    e = readable(static_cast<const bf16*>(wd), s.hidden, s.ffn, s.ffn, f.w_down, st, &w->down,
+                 &w->ld_down);
+  return e;
+}
+
+// saved[] = {gate, up} in bf16, or {gate codes, gate scales, up codes, up scales}
+bool saved_ok(int save, void* const* saved) {
+  const int n = save == DMUON_SAVE_NONE ? 0 : save == DMUON_SAVE_BF16 ? 2 : 4;
+  if (n == 0) return true;
+  if (saved == nullptr) return false;
+  for (int i = 0; i < n; ++i)
+    if (saved[i] == nullptr) return false;
+  return true;
+}
+void use_saved(LinArgs& g, const dmuon_ffn_shape& s, void* const* saved) {
+  g.act = s.activation;
+  g.keep = s.save == DMUON_SAVE_BF16 ? kKeepBf16 : s.save == DMUON_SAVE_ACT8 ? kKeepAct8 : kKeepNone;
+  g.ffn = int(s.ffn);
+  if (g.keep == kKeepBf16) {
+    g.gate = saved[0];
+    g.up = saved[1];
+    g.kept_vec = s.ffn % 8 == 0 && aligned(g.gate, 16) && aligned(g.up, 16);
+  } else if (g.keep == kKeepAct8) {
+    g.gate = saved[0];
+    g.gate_scale = static_cast<bf16*>(saved[1]);
+    g.up = saved[2];
+    g.up_scale = static_cast<bf16*>(saved[3]);
+    g.kept_vec = s.ffn % 16 == 0 && aligned(g.gate, 16) && aligned(g.up, 16);
+  }
+}
+
+int ffn_weight_alignment(const dmuon_ffn_shape& s, const void* wg, const void* wu, const void* wd) {
+  if (s.hidden % 8 == 0 && (!aligned(wg, 16) || !aligned(wu, 16))) return DMUON_ERR_ALIGNMENT;
+  if (s.ffn % 8 == 0 && !aligned(wd, 16)) return DMUON_ERR_ALIGNMENT;
+  return DMUON_OK;
+}
+
+int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const void* wg,
+                const void* wu, const void* wd, void* y, int64_t y_ld, void* const* saved,
+                void* ws, cudaStream_t st) {
+  int clusters = 0;
+  int e = device_ready(&clusters);
+  if (e != DMUON_OK) return e;
+  const FfnSpace f = ffn_space(s, false, ws);
+  const int64_t f8 = up8(s.ffn);
+  FfnWeights w;
+  e = ffn_weights(s, f, wg, wu, wd, st, &w);
+  if (e != DMUON_OK) return e;
+  const bf16* xr;
+  int64_t xr_ld;
+  e = readable(static_cast<const bf16*>(x), s.tokens, s.hidden, x_ld, f.x, st, &xr, &xr_ld);
+  if (e != DMUON_OK) return e;
+  {
+    Launch L(f.ps);
+    LinProblem& P = L.problem(s.tokens, s.ffn, 128, s.hidden, 0);
+    P.a0 = L.operand(xr, s.hidden, s.tokens, xr_ld);
+    P.b0 = L.operand(w.gate, s.hidden, s.ffn, w.ld_in);
+    P.b1 = L.operand(w.up, s.hidden, s.ffn, w.ld_in);
+    P.c_map = L.output(f.h, s.ffn, s.tokens, f8);
+    use_saved(L.g, s, saved);
+    if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
+      L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
+      L.g.map_up = L.output(static_cast<bf16*>(L.g.up), s.ffn, s.tokens, s.ffn);
+    }
+    e = L.run(kLinGlu, false, false, clusters, st);
+    if (e != DMUON_OK) return e;
+  }
+  Launch L(f.ps);
+  LinProblem& P = L.problem(s.tokens, s.hidden, 256, s.ffn, 0);
+  P.a0 = L.operand(f.h, s.ffn, s.tokens, f8);
+  P.b0 = L.operand(w.down, s.ffn, s.hidden, w.ld_down);
+  L.store_to(P, static_cast<bf16*>(y), y_ld);
+  return L.run(kLinStore, false, false, clusters, st);
+}
+
+int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const void* x,
+                 int64_t x_ld, const void* wg, const void* wu, const void* wd,
+                 void* const* saved, void* dx, int64_t dx_ld, void* dwg, void* dwu, void* dwd,
+                 void* ws, cudaStream_t st) {
+  int clusters = 0;
+  int e = device_ready(&clusters);
+  if (e != DMUON_OK) return e;
+  if (s.tokens == 0) {  // sums over no token
+    if (launch_zero_rows(s.ffn, s.hidden, static_cast<bf16*>(dwg), s.hidden, st) != cudaSuccess ||
+        launch_zero_rows(s.ffn, s.hidden, static_cast<bf16*>(dwu), s.hidden, st) != cudaSuccess ||
+        launch_zero_rows(s.hidden, s.ffn, static_cast<bf16*>(dwd), s.ffn, st) != cudaSuccess)
+      return DMUON_ERR_CUDA;
+    return DMUON_OK;
+  }
+  const FfnSpace f = ffn_space(s, true, ws);
+  const int64_t f8 = up8(s.ffn);
+  FfnWeights w;
+  e = ffn_weights(s, f, wg, wu, wd, st, &w);
+  if (e != DMUON_OK) return e;
+  const bf16 *xr, *dyr;
+  int64_t xr_ld, dyr_ld;
+  e = readable(static_cast<const bf16*>(x), s.tokens, s.hidden, x_ld, f.x, st, &xr, &xr_ld);
+  if (e == DMUON_OK)
+    e = readable(static_cast<const bf16*>(dy), s.tokens, s.hidden, dy_ld, f.dy, st, &dyr, &dyr_ld);
+  if (e != DMUON_OK) return e;
+  {  // dh = dy Wd, and from it dgate, dup and h
+    Launch L(f.ps);
+    LinProblem& P = L.problem(s.tokens, s.ffn, 256, s.hidden, 0);
+    P.a0 = L.operand(dyr, s.hidden, s.tokens, dyr_ld);
+    P.b0 = L.operand(w.down, s.ffn, s.hidden, w.ld_down);
+    P.c_map = L.output(f.dgate, s.ffn, s.tokens, f8);
+    L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, f8);
+    L.g.map_h = L.output(f.h, s.ffn, s.tokens, f8);
+    use_saved(L.g, s, saved);
+    e = L.run(kLinGluGrad, false, true, clusters, st);
+    if (e != DMUON_OK) return e;
+  }
+  {  // dx = dgate Wg + dup Wu
+    Launch L(f.ps);
+    LinProblem& P = L.problem(s.tokens, s.hidden, 256, s.ffn, s.ffn);
+    P.a0 = L.operand(f.dgate, s.ffn, s.tokens, f8);
+    P.b0 = L.operand(w.gate, s.hidden, s.ffn, w.ld_in);
+    P.a1 = L.operand(f.dup, s.ffn, s.tokens, f8);
+    P.b1 = L.operand(w.up, s.hidden, s.ffn, w.ld_in);
+    L.store_to(P, static_cast<bf16*>(dx), dx_ld);
+    e = L.run(kLinStore, false, true, clusters, st);
+    if (e != DMUON_OK) return e;
+  }
+  // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
+  Launch L(f.ps);
+  const int mx = L.operand(xr, s.hidden, s.tokens, xr_ld);
+  const bf16* left[3] = {f.dgate, f.dup, dyr};
+  bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
+    LinProblem& P = L.problem(m, n, 256, s.tokens, 0);
+    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? f8 : dyr_ld);
+    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, f8);
+    L.store_to(P, out[i], n);
+  }
+  return L.run(kLinStore, true, true, clusters, st);
+}
+
+// ------------------------------------------------------------------ cross entropy
+bool xent_shape_ok(const dmuon_xent_shape* s) {
+  return s != nullptr && s->tokens >= 0 && s->tokens <= kMaxTokens && s->hidden >= 1 &&
+         s->hidden <= kMaxDim && s->vocab >= 1 && s->vocab <= kMaxVocab;
+}
+
+// Tokens worked on at a time.
+int64_t xent_piece(const dmuon_xent_shape& s, bool grads) {
+  int64_t most = kLossTokens;
+  if (grads)
+    most = std::max<int64_t>(256, int64_t(kLogitBytes / (size_t(up8(s.vocab)) * 2)) / 256 * 256);
+  return std::min(s.tokens, most);
+}
+
+struct XentSpace {
+  ProductSpace ps;
+  bf16 *hidden, *weight, *e;
+  float* target_logit;
+  float2* stat;
+  float* sum;
+  int64_t piece, stat_ld;
+  size_t bytes;
+};
+XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
+  Carve c(ws);
+  XentSpace x{};
+  const size_t d8 = size_t(up8(s.hidden)), groups = size_t(ceil_div(s.vocab, kXentGroup));
+  x.piece = xent_piece(s, grads);
+  x.stat_ld = (x.piece + 31) / 32 * 32;
+  x.ps = take_product_space(c);
+  x.hidden = c.take<bf16>(size_t(s.tokens) * d8 * 2);
+  x.target_logit = c.take<float>(size_t(s.tokens) * 4);
+  x.stat = c.take<float2>(groups * size_t(x.stat_ld) * sizeof(float2));
+  if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * d8 * 2);
+  if (grads) {
+    x.e = c.take<bf16>(size_t(x.piece) * size_t(up8(s.vocab)) * 2);
+    if (x.piece < s.tokens) x.sum = c.take<float>(size_t(s.vocab) * size_t(s.hidden) * 4);
+  }
+  x.bytes = c.used;
+  return x;
+}
+
+int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void* weight,
+         const int64_t* target, const float* grad_loss, float* loss, float* lse, void* dhidden,
+         int64_t dh_ld, void* dweight, void* ws, cudaStream_t st) {
+  const bool grads = grad_loss != nullptr;
+  int clusters = 0;
+  int e = device_ready(&clusters);
+  if (e != DMUON_OK) return e;
+  const XentSpace x = xent_space(s, grads, ws);
+  const int64_t v8 = up8(s.vocab);
+  const long long* tgt = reinterpret_cast<const long long*>(target);
+  const bf16 *w, *h;
+  int64_t w_ld, hr_ld;
+  e = readable(static_cast<const bf16*>(weight), s.vocab, s.hidden, s.hidden, x.weight, st, &w,
+               &w_ld);
+  if (e != DMUON_OK) return e;
+  if (grads) {
+    // masked rows become zeros, so that nothing they hold (NaN of padding, say)
+    // reaches the weight's gradient, which sums over rows
+    hr_ld = up8(s.hidden);
+    if (launch_copy_rows(s.tokens, s.hidden, static_cast<const bf16*>(hidden), h_ld, x.hidden,
+                         hr_ld, tgt, s.vocab, st) != cudaSuccess)
+      return DMUON_ERR_CUDA;
+    h = x.hidden;
+  } else {
+    e = readable(static_cast<const bf16*>(hidden), s.tokens, s.hidden, h_ld, x.hidden, st, &h,
+                 &hr_ld);
+    if (e != DMUON_OK) return e;
+  }
+  for (int64_t t0 = 0; t0 < s.tokens; t0 += x.piece) {
+    const int64_t n = std::min(x.piece, s.tokens - t0);
+    const bf16* hp = h + t0 * hr_ld;
+    XentRows R{};
+    R.tokens = n;
+    R.vocab = s.vocab;
+    R.target = tgt + t0;
+    R.grad_loss = grads ? grad_loss + t0 : nullptr;
+    R.target_logit = x.target_logit + t0;
+    R.group_stat = x.stat;
+    R.stat_ld = x.stat_ld;
+    R.loss = loss + t0;
+    R.lse = lse + t0;
+    {
+      Launch L(x.ps);
+      LinProblem& P = L.problem(n, s.vocab, 256, s.hidden, 0);
+      P.a0 = L.operand(hp, s.hidden, n, hr_ld);
+      P.b0 = L.operand(w, s.hidden, s.vocab, w_ld);
+      if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
+      L.g.target = tgt + t0;
+      L.g.target_logit = x.target_logit + t0;
+      L.g.group_stat = x.stat;
+      L.g.stat_ld = x.stat_ld;
+      e = L.run(kLinXent, false, false, clusters, st);
+      if (e != DMUON_OK) return e;
+    }
+    if (launch_xent_rows(R, st) != cudaSuccess) return DMUON_ERR_CUDA;
+    if (!grads) continue;
+    if (launch_xent_grad(R, x.e, v8, st) != cudaSuccess) return DMUON_ERR_CUDA;
+    {  // dhidden = G W
+      Launch L(x.ps);
+      LinProblem& P = L.problem(n, s.hidden, 256, s.vocab, 0);
+      P.a0 = L.operand(x.e, s.vocab, n, v8);
+      P.b0 = L.operand(w, s.hidden, s.vocab, w_ld);
+      L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
+      e = L.run(kLinStore, false, true, clusters, st);
+      if (e != DMUON_OK) return e;
+    }
+    // dweight += G^T h, in fp32 over the pieces
+    Launch L(x.ps);
+    LinProblem& P = L.problem(s.vocab, s.hidden, 256, n, 0);
+    P.a0 = L.operand(x.e, s.vocab, n, v8);
+    P.b0 = L.operand(hp, s.hidden, n, hr_ld);
+    L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
+    L.g.sum = x.sum;
+    L.g.sum_read = t0 > 0;
+    L.g.sum_write = t0 + n < s.tokens;
+    e = L.run(kLinStore, true, true, clusters, st);
+    if (e != DMUON_OK) return e;
+  }
+  return DMUON_OK;
+}
+
+}  // namespace
+}  // namespace dm
+
+extern "C" {
+
+using namespace dm;
+
+int dmuon_act8_save(int64_t rows, int64_t cols, const void* x, int64_t x_ld, int x_dt,
+                    int8_t* codes, void* scales, cudaStream_t stream) {
+  if (rows < 0 || cols < 0 || (x_dt != DMUON_F32 && x_dt != DMUON_BF16))
+    return DMUON_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return DMUON_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr || x_ld < cols)
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(x, x_dt == DMUON_BF16 ? 2 : 4) || !aligned(scales, 2)) return DMUON_ERR_ALIGNMENT;
+  if (ceil_div(cols, 2048) > INT32_MAX / rows) return DMUON_ERR_UNSUPPORTED;
+  int clusters = 0;
+  const int st = device_ready(&clusters);
+  if (st != DMUON_OK) return st;
+  return launch_act8_save(rows, cols, x, x_ld, x_dt == DMUON_BF16,
+                          reinterpret_cast<signed char*>(codes), static_cast<bf16*>(scales),
+                          stream) == cudaSuccess
+             ? DMUON_OK
+             : DMUON_ERR_CUDA;
+}
+
+int dmuon_act8_load(int64_t rows, int64_t cols, const int8_t* codes, const void* scales,
+                    void* out, int64_t out_ld, int out_dt, cudaStream_t stream) {
+  if (rows < 0 || cols < 0 || (out_dt != DMUON_F32 && out_dt != DMUON_BF16))
+    return DMUON_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return DMUON_OK;
+  if (out == nullptr || codes == nullptr || scales == nullptr || out_ld < cols)
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(out, out_dt == DMUON_BF16 ? 2 : 4) || !aligned(scales, 2))
+    return DMUON_ERR_ALIGNMENT;
+  if (ceil_div(cols, 2048) > INT32_MAX / rows) return DMUON_ERR_UNSUPPORTED;
+  int clusters = 0;
+  const int st = device_ready(&clusters);
+  if (st != DMUON_OK) return st;
+  return launch_act8_load(rows, cols, reinterpret_cast<const signed char*>(codes),
+                          static_cast<const bf16*>(scales), out, out_ld, out_dt == DMUON_BF16,
+                          stream) == cudaSuccess
+             ? DMUON_OK
+             : DMUON_ERR_CUDA;
+}
+
+size_t dmuon_ffn_workspace_bytes(const dmuon_ffn_shape* shape, int backward) {
+  if (!ffn_shape_ok(shape)) return 0;
+  return ffn_space(*shape, backward != 0, nullptr).bytes;
+}
+
+int dmuon_ffn_forward(const dmuon_ffn_shape* shape, const void* x, int64_t x_ld,
+                      const void* w_gate, const void* w_up, const void* w_down, void* y,
+                      int64_t y_ld, void* const* saved, void* workspace, size_t ws_bytes,
+                      cudaStream_t stream) {
+  if (!ffn_shape_ok(shape)) return DMUON_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return DMUON_OK;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr || y == nullptr ||
+      workspace == nullptr || x_ld < shape->hidden || y_ld < shape->hidden ||
+      !saved_ok(shape->save, saved))
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return DMUON_ERR_ALIGNMENT;
+  const int st = ffn_weight_alignment(*shape, w_gate, w_up, w_down);
+  if (st != DMUON_OK) return st;
+  if (ws_bytes < dmuon_ffn_workspace_bytes(shape, 0)) return DMUON_ERR_WORKSPACE;
+  return ffn_forward(*shape, x, x_ld, w_gate, w_up, w_down, y, y_ld, saved, workspace, stream);
+}
+
+int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_ld, const void* x,
+                       int64_t x_ld, const void* w_gate, const void* w_up, const void* w_down,
+                       void* const* saved, void* dx, int64_t dx_ld, void* dw_gate, void* dw_up,
+                       void* dw_down, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!ffn_shape_ok(shape) || shape->save == DMUON_SAVE_NONE) return DMUON_ERR_INVALID_ARG;
+  if (w_gate == nullptr || w_up == nullptr || w_down == nullptr || dw_gate == nullptr ||
+      dw_up == nullptr || dw_down == nullptr || workspace == nullptr)
+    return DMUON_ERR_INVALID_ARG;
+  if (shape->tokens > 0 &&
+      (dy == nullptr || x == nullptr || dx == nullptr || dy_ld < shape->hidden ||
+       x_ld < shape->hidden || dx_ld < shape->hidden || !saved_ok(shape->save, saved)))
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return DMUON_ERR_ALIGNMENT;
+  const int st = ffn_weight_alignment(*shape, w_gate, w_up, w_down);
+  if (st != DMUON_OK) return st;
+  if (ws_bytes < dmuon_ffn_workspace_bytes(shape, 1)) return DMUON_ERR_WORKSPACE;
+  return ffn_backward(*shape, dy, dy_ld, x, x_ld, w_gate, w_up, w_down, saved, dx, dx_ld, dw_gate,
+                      dw_up, dw_down, workspace, stream);
+}
+
+size_t dmuon_xent_workspace_bytes(const dmuon_xent_shape* shape, int grads) {
+  if (!xent_shape_ok(shape)) return 0;
+  return xent_space(*shape, grads != 0, nullptr).bytes;
+}
+
+int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden_ld,
+               const void* weight, const int64_t* target, const float* grad_loss, float* loss,
+               float* lse, void* dhidden, int64_t dhidden_ld, void* dweight, void* workspace,
+               size_t ws_bytes, cudaStream_t stream) {
+  if (!xent_shape_ok(shape) || weight == nullptr || workspace == nullptr)
+    return DMUON_ERR_INVALID_ARG;
+  const bool grads = grad_loss != nullptr || dhidden != nullptr || dweight != nullptr;
+  if (grads && dweight == nullptr) return DMUON_ERR_INVALID_ARG;
+  if (shape->tokens > 0) {
+    if (hidden == nullptr || target == nullptr || loss == nullptr || lse == nullptr ||
+        hidden_ld < shape->hidden)
+      return DMUON_ERR_INVALID_ARG;
+    if (grads && (grad_loss == nullptr || dhidden == nullptr || dhidden_ld < shape->hidden))
+      return DMUON_ERR_INVALID_ARG;
+  }
+  if (!aligned(workspace, 256) || (shape->hidden % 8 == 0 && !aligned(weight, 16)))
+    return DMUON_ERR_ALIGNMENT;
+  if (ws_bytes < dmuon_xent_workspace_bytes(shape, grads ? 1 : 0)) return DMUON_ERR_WORKSPACE;
+  if (shape->tokens == 0 && grads) {
+    int clusters = 0;
+    const int st = device_ready(&clusters);
+    if (st != DMUON_OK) return st;
+    return launch_zero_rows(shape->vocab, shape->hidden, static_cast<bf16*>(dweight),
+                            shape->hidden, stream) == cudaSuccess
+               ? DMUON_OK
+               : DMUON_ERR_CUDA;
+  }
+  if (shape->tokens == 0) return DMUON_OK;
+  return xent(*shape, hidden, hidden_ld, weight, target, grad_loss, loss, lse, dhidden, dhidden_ld,
+              dweight, workspace, stream);
+}
+
+}  // extern "C"

@@ -25,12 +25,17 @@ F32, BF16 = 0, 1
 NS_STANDARD, NS_GRAM, NS_GRAM_ALL = 0, 1, 2
 PACK_ALIGN_ELEMS = 128
 DEFAULT_ABC = (3.4445, -4.7750, 2.0315)
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+SAVE_NONE, SAVE_BF16, SAVE_ACT8 = 0, 1, 2
+ACT8_BLOCK = 32          # columns that share a scale
 
 EXPORTED = ("dmuon_plan", "dmuon_workspace_bytes", "dmuon_ns_variant_for", "dmuon_pack", "dmuon_ns_batched",
             "dmuon_unpack_update", "dmuon_muon_step", "dmuon_stream_status",
             "dmuon_debug_wait_timeout", "dmuon_ns_batched_noalloc", "dmuon_noalloc_status",
             "dmuon_adamw",
-            "dmuon_adamw_workspace_bytes", "dmuon_status_string", "dmuon_version",
+            "dmuon_adamw_workspace_bytes", "dmuon_act8_save", "dmuon_act8_load",
+            "dmuon_ffn_workspace_bytes", "dmuon_ffn_forward", "dmuon_ffn_backward",
+            "dmuon_xent_workspace_bytes", "dmuon_xent", "dmuon_status_string", "dmuon_version",
             "dmuon_launch_count", "dmuon_trace_begin", "dmuon_trace_end")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 # largest short side m and long side n of a matrix the library accepts
@@ -39,6 +44,15 @@ MAX_M, MAX_N = 32768, 1048576
 
 class Shape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class FfnShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("ffn", ctypes.c_int64),
+                ("activation", ctypes.c_int), ("save", ctypes.c_int)]
+
+
+class XentShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("vocab", ctypes.c_int64)]
 
 
 _vp, _i, _f, _sz, _i64p = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, \
@@ -73,6 +87,24 @@ _d = ctypes.c_double
 _lib.dmuon_adamw.argtypes = [_i, _i64p, _VPP, _i, _VPP, _i, _VPP, _VPP, _d, _d, _d, _d, _d, _i,
                              _vp, _sz, _vp]
 _lib.dmuon_adamw.restype = _i
+_int64 = ctypes.c_int64
+_FfnP, _XentP = ctypes.POINTER(FfnShape), ctypes.POINTER(XentShape)
+_lib.dmuon_act8_save.argtypes = [_int64, _int64, _vp, _int64, _i, _vp, _vp, _vp]
+_lib.dmuon_act8_save.restype = _i
+_lib.dmuon_act8_load.argtypes = [_int64, _int64, _vp, _vp, _vp, _int64, _i, _vp]
+_lib.dmuon_act8_load.restype = _i
+_lib.dmuon_ffn_workspace_bytes.argtypes = [_FfnP, _i]
+_lib.dmuon_ffn_workspace_bytes.restype = _sz
+_lib.dmuon_ffn_forward.argtypes = [_FfnP, _vp, _int64, _vp, _vp, _vp, _vp, _int64, _VPP, _vp, _sz, _vp]
+_lib.dmuon_ffn_forward.restype = _i
+_lib.dmuon_ffn_backward.argtypes = [_FfnP, _vp, _int64, _vp, _int64, _vp, _vp, _vp, _VPP, _vp, _int64,
+                                    _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.dmuon_ffn_backward.restype = _i
+_lib.dmuon_xent_workspace_bytes.argtypes = [_XentP, _i]
+_lib.dmuon_xent_workspace_bytes.restype = _sz
+_lib.dmuon_xent.argtypes = [_XentP, _vp, _int64, _vp, _vp, _vp, _vp, _vp, _vp, _int64, _vp, _vp, _sz,
+                            _vp]
+_lib.dmuon_xent.restype = _i
 _lib.dmuon_stream_status.argtypes = [_vp, _vp]
 _lib.dmuon_stream_status.restype = _i
 _lib.dmuon_debug_wait_timeout.argtypes = [_vp, _sz, _i, _vp]
@@ -325,6 +357,221 @@ class MuonOwner:
         r, c = self.shapes[i]
         o = self.offsets[i]
         return self.packed[o:o + r * c].view(r, c)
+
+    def status(self, stream=None) -> int:
+        return stream_status(self.workspace, stream)
+
+
+# ------------------------------------------------------------------ training-side operators
+def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
+    """Check a (rows, cols) bf16 token matrix; its row pitch in elements."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected bfloat16")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if rows <= 1 or cols == 0:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: the elements of a row must be contiguous")
+        return cols
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{what}: the elements of a row must be contiguous, rows must not overlap")
+    return t.stride(0)
+
+
+def _dense(t: torch.Tensor, dtype, shape, what: str) -> int:
+    """Check a contiguous CUDA tensor; its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _act8_blocks(cols: int) -> int:
+    return (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
+
+
+def act8_empty(rows: int, cols: int, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Uninitialised (codes, scales) of an 8-bit activation of shape (rows, cols)."""
+    return (torch.empty((rows, cols), dtype=torch.int8, device=device),
+            torch.empty((rows, _act8_blocks(cols)), dtype=torch.bfloat16, device=device))
+
+
+def _act8_args(t: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, where: str):
+    if t.dim() != 2:
+        raise ValueError(f"{where}: expected a 2-D tensor, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    dt = _dtype(t)
+    if not t.is_cuda or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{where}: expected a CUDA tensor whose rows are contiguous")
+    return (rows, cols, dt, t.stride(0) if rows > 1 else cols,
+            _dense(codes, torch.int8, (rows, cols), f"{where}: codes"),
+            _dense(scales, torch.bfloat16, (rows, _act8_blocks(cols)), f"{where}: scales"))
+
+
+def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Keep a 2-D activation (bf16 or fp32) as 8-bit codes, 32 columns to a scale."""
+    rows, cols, dt, ld, c, s = _act8_args(x, codes, scales, "act8_save")
+    _check(_lib.dmuon_act8_save(rows, cols, x.data_ptr(), ld, dt, c, s, _stream(stream)),
+           "dmuon_act8_save")
+
+
+def act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """Bring an 8-bit activation back into `out` (bf16 or fp32)."""
+    rows, cols, dt, ld, c, s = _act8_args(out, codes, scales, "act8_load")
+    _check(_lib.dmuon_act8_load(rows, cols, c, s, out.data_ptr(), ld, dt, _stream(stream)),
+           "dmuon_act8_load")
+
+
+class GatedFFN:
+    """Gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T and its backward
+    pass, for up to `max_tokens` tokens.  Holds the workspace; tensors are the
+    caller's, bf16, weights as PyTorch parameters (out, in).  The weight gradients
+    are those the owner's step takes for the gate, up and down projections.
+
+    `save` says what forward keeps for backward: SAVE_NONE, SAVE_BF16 or SAVE_ACT8
+    (see :meth:`empty_saved`).  `backward=False` sizes the workspace for forward only.
+    """
+
+    def __init__(self, max_tokens: int, hidden: int, ffn: int, activation: int = ACT_SILU,
+                 save: int = SAVE_BF16, backward: Optional[bool] = None, device="cuda"):
+        self.max_tokens, self.hidden, self.ffn = int(max_tokens), int(hidden), int(ffn)
+        self.activation, self.save = int(activation), int(save)
+        self.with_backward = self.save != SAVE_NONE if backward is None else bool(backward)
+        shape = self._shape(self.max_tokens)
+        nbytes = int(_lib.dmuon_ffn_workspace_bytes(ctypes.byref(shape), int(self.with_backward)))
+        if nbytes == 0:
+            raise DMuonError(ERR_INVALID_ARG, "dmuon_ffn_workspace_bytes")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+
+    def _shape(self, tokens: int) -> FfnShape:
+        return FfnShape(tokens, self.hidden, self.ffn, self.activation, self.save)
+
+    def empty_saved(self, tokens: int) -> Tuple[torch.Tensor, ...]:
+        """Uninitialised tensors for what forward keeps of `tokens` tokens: (),
+        (gate, up), or (gate codes, gate scales, up codes, up scales)."""
+        if self.save == SAVE_NONE:
+            return ()
+        dev = self.workspace.device
+        if self.save == SAVE_BF16:
+            return tuple(torch.empty((tokens, self.ffn), dtype=torch.bfloat16, device=dev)
+                         for _ in range(2))
+        return act8_empty(tokens, self.ffn, dev) + act8_empty(tokens, self.ffn, dev)
+
+    def _tokens(self, x: torch.Tensor) -> int:
+        t = x.shape[0] if x.dim() == 2 else -1
+        if t < 0 or t > self.max_tokens:
+            raise ValueError(f"x: expected (tokens <= {self.max_tokens}, {self.hidden}), "
+                             f"got {tuple(x.shape)}")
+        return t
+
+    def _weights(self, w_gate, w_up, w_down, what=""):
+        bf, d, f = torch.bfloat16, self.hidden, self.ffn
+        return (_dense(w_gate, bf, (f, d), what + "w_gate"), _dense(w_up, bf, (f, d), what + "w_up"),
+                _dense(w_down, bf, (d, f), what + "w_down"))
+
+    def _saved(self, saved, t: int):
+        saved = tuple(saved) if saved is not None else ()
+        want = {SAVE_NONE: 0, SAVE_BF16: 2, SAVE_ACT8: 4}[self.save]
+        if len(saved) != want:
+            raise ValueError(f"saved: expected {want} tensors, got {len(saved)}")
+        if self.save == SAVE_BF16:
+            kinds = [(torch.bfloat16, (t, self.ffn))] * 2
+        else:
+            kinds = [(torch.int8, (t, self.ffn)), (torch.bfloat16, (t, _act8_blocks(self.ffn)))] * 2
+        arr = (ctypes.c_void_p * 4)()
+        for i, s in enumerate(saved):
+            arr[i] = _dense(s, kinds[i][0], kinds[i][1], f"saved[{i}]")
+        return arr
+
+    def forward(self, x, w_gate, w_up, w_down, y, saved=None, stream=None) -> None:
+        """y <- block(x); x and y are (tokens, hidden), `saved` from :meth:`empty_saved`."""
+        t = self._tokens(x)
+        x_ld, y_ld = _bf16_rows(x, t, self.hidden, "x"), _bf16_rows(y, t, self.hidden, "y")
+        wg, wu, wd = self._weights(w_gate, w_up, w_down)
+        shape = self._shape(t)
+        _check(_lib.dmuon_ffn_forward(ctypes.byref(shape), x.data_ptr(), x_ld, wg, wu, wd,
+                                      y.data_ptr(), y_ld, self._saved(saved, t),
+                                      self.workspace.data_ptr(), self.workspace.numel(),
+                                      _stream(stream)), "dmuon_ffn_forward")
+
+    def backward(self, dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down,
+                 stream=None) -> None:
+        """Gradients of x and the three weights from dy and what forward kept."""
+        if not self.with_backward:
+            raise ValueError("this GatedFFN was made without a backward pass")
+        t = self._tokens(x)
+        d = self.hidden
+        dy_ld, x_ld = _bf16_rows(dy, t, d, "dy"), _bf16_rows(x, t, d, "x")
+        dx_ld = _bf16_rows(dx, t, d, "dx")
+        wg, wu, wd = self._weights(w_gate, w_up, w_down)
+        gg, gu, gd = self._weights(dw_gate, dw_up, dw_down, "d")
+        shape = self._shape(t)
+        _check(_lib.dmuon_ffn_backward(ctypes.byref(shape), dy.data_ptr(), dy_ld, x.data_ptr(),
+                                       x_ld, wg, wu, wd, self._saved(saved, t), dx.data_ptr(),
+                                       dx_ld, gg, gu, gd, self.workspace.data_ptr(),
+                                       self.workspace.numel(), _stream(stream)),
+               "dmuon_ffn_backward")
+
+    def status(self, stream=None) -> int:
+        return stream_status(self.workspace, stream)
+
+
+class LinearXent:
+    """Softmax cross entropy of hidden W^T against one target per token, for up to
+    `max_tokens` tokens, without keeping the logits; with `grads` also the
+    gradients of the hidden states and of the head W (vocab, hidden).  Holds the
+    workspace; hidden, W and their gradients are bf16, losses fp32, targets int64.
+    A target outside [0, vocab) masks its token.
+    """
+
+    def __init__(self, max_tokens: int, hidden: int, vocab: int, grads: bool = True,
+                 device="cuda"):
+        self.max_tokens, self.hidden, self.vocab = int(max_tokens), int(hidden), int(vocab)
+        self.grads = bool(grads)
+        shape = XentShape(self.max_tokens, self.hidden, self.vocab)
+        nbytes = int(_lib.dmuon_xent_workspace_bytes(ctypes.byref(shape), int(self.grads)))
+        if nbytes == 0:
+            raise DMuonError(ERR_INVALID_ARG, "dmuon_xent_workspace_bytes")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+
+    def _run(self, hidden, weight, target, grad_loss, loss, lse, dhidden, dweight, stream):
+        t, d = (hidden.shape[0] if hidden.dim() == 2 else -1), self.hidden
+        if t < 0 or t > self.max_tokens:
+            raise ValueError(f"hidden: expected (tokens <= {self.max_tokens}, {d}), "
+                             f"got {tuple(hidden.shape)}")
+        h_ld = _bf16_rows(hidden, t, d, "hidden")
+        w = _dense(weight, torch.bfloat16, (self.vocab, d), "weight")
+        tg = _dense(target, torch.int64, (t,), "target")
+        lo = _dense(loss, torch.float32, (t,), "loss")
+        ls = _dense(lse, torch.float32, (t,), "lse")
+        gl = dh = dw = None
+        dh_ld = 0
+        if grad_loss is not None:
+            gl = _dense(grad_loss, torch.float32, (t,), "grad_loss")
+            dh_ld, dh = _bf16_rows(dhidden, t, d, "dhidden"), dhidden.data_ptr()
+            dw = _dense(dweight, torch.bfloat16, (self.vocab, d), "dweight")
+        shape = XentShape(t, d, self.vocab)
+        _check(_lib.dmuon_xent(ctypes.byref(shape), hidden.data_ptr(), h_ld, w, tg, gl, lo, ls, dh,
+                               dh_ld, dw, self.workspace.data_ptr(), self.workspace.numel(),
+                               _stream(stream)), "dmuon_xent")
+
+    def loss(self, hidden, weight, target, loss, lse, stream=None) -> None:
+        """Per-token loss and log-sum-exp."""
+        self._run(hidden, weight, target, None, loss, lse, None, None, stream)
+
+    def loss_and_grads(self, hidden, weight, target, grad_loss, loss, lse, dhidden, dweight,
+                       stream=None) -> None:
+        """The same with the gradients of sum(grad_loss * loss)."""
+        if not self.grads:
+            raise ValueError("this LinearXent was made without gradients")
+        self._run(hidden, weight, target, grad_loss, loss, lse, dhidden, dweight, stream)
 
     def status(self, stream=None) -> int:
         return stream_status(self.workspace, stream)

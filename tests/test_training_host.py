@@ -1,0 +1,150 @@
+"""Host-side tests of the training-side operators' C ABI: workspace sizes, and bad
+arguments refused before anything touches a GPU (addresses here are never read)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def dm():
+    import os
+    from newton_schulz_owner_gb300 import build_lib
+    if not os.path.exists(build_lib.LIB):
+        build_lib.build()
+    from newton_schulz_owner_gb300 import dmuon
+    return dmuon
+
+
+P, W = 1 << 20, 1 << 30
+
+
+def ffn_bytes(dm, *a, backward=0):
+    return dm.lib().dmuon_ffn_workspace_bytes(ctypes.byref(dm.FfnShape(*a)), backward)
+
+
+def xent_bytes(dm, *a, grads=1):
+    return dm.lib().dmuon_xent_workspace_bytes(ctypes.byref(dm.XentShape(*a)), grads)
+
+
+def test_workspaces_grow_with_tokens_and_refuse_bad_shapes(dm):
+    for back in (0, 1):
+        sizes = [ffn_bytes(dm, t, 1537, 8961, dm.ACT_SILU, dm.SAVE_BF16, backward=back)
+                 for t in (0, 1, 2, 63, 64, 65, 300, 4096, 1 << 22)]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+        sizes = [xent_bytes(dm, t, 1537, 151936, grads=back)
+                 for t in (0, 1, 255, 256, 257, 7000, 8000, 20000, 1 << 22)]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+    # the logits of a long batch are not kept: the workspace stays far below them
+    assert xent_bytes(dm, 1 << 17, 4096, 128256) < (1 << 17) * 128256 * 2 / 4
+    for bad in [(-1, 8, 8, 0, 1), (1, 0, 8, 0, 1), (1, 8, 0, 0, 1), (1, 8, 8, 3, 1), (1, 8, 8, 0, 3),
+                (1, 8, 8, -1, 1), ((1 << 22) + 1, 8, 8, 0, 1), (1, (1 << 19) + 1, 8, 0, 1)]:
+        assert ffn_bytes(dm, *bad) == 0, bad
+    for bad in [(-1, 8, 8), (1, 0, 8), (1, 8, 0), (1, 8, (1 << 22) + 1), ((1 << 22) + 1, 8, 8)]:
+        assert xent_bytes(dm, *bad) == 0, bad
+    assert dm.lib().dmuon_ffn_workspace_bytes(None, 0) == 0
+    assert dm.lib().dmuon_xent_workspace_bytes(None, 0) == 0
+
+
+def test_ffn_refuses_bad_arguments(dm):
+    lib = dm.lib()
+    two = (ctypes.c_void_p * 4)(P, P, P, P)
+    hole = (ctypes.c_void_p * 4)(P, None, P, P)
+
+    def fwd(shape=(4, 64, 96, 0, 1), x=P, x_ld=64, wg=P, wu=P, wd=P, y=P, y_ld=64, saved=two, ws=W,
+            nb=None):
+        s = dm.FfnShape(*shape)
+        need = lib.dmuon_ffn_workspace_bytes(ctypes.byref(s), 0)
+        return lib.dmuon_ffn_forward(ctypes.byref(s), x, x_ld, wg, wu, wd, y, y_ld, saved, ws,
+                                     need if nb is None else need + nb, None)
+
+    def bwd(shape=(4, 64, 96, 0, 1), dy=P, x=P, wg=P, saved=two, dx=P, dx_ld=64, dwg=P, dwd=P, ws=W,
+            nb=None):
+        s = dm.FfnShape(*shape)
+        need = lib.dmuon_ffn_workspace_bytes(ctypes.byref(s), 1)
+        return lib.dmuon_ffn_backward(ctypes.byref(s), dy, 64, x, 64, wg, P, P, saved, dx, dx_ld,
+                                      dwg, P, dwd, ws, need if nb is None else need + nb, None)
+
+    bad = dm.ERR_INVALID_ARG
+    assert lib.dmuon_ffn_forward(None, P, 64, P, P, P, P, 64, two, W, 1 << 40, None) == bad
+    assert fwd(shape=(4, 64, 96, 5, 1)) == bad
+    assert fwd(shape=(4, 64, 96, 0, 9)) == bad
+    assert fwd(shape=(-1, 64, 96, 0, 1)) == bad
+    assert fwd(x=None) == bad and fwd(y=None) == bad and fwd(wu=None) == bad and fwd(ws=None) == bad
+    assert fwd(x_ld=63) == bad and fwd(y_ld=63) == bad
+    assert fwd(saved=None) == bad and fwd(saved=hole) == bad
+    assert fwd(wg=P + 2) == dm.ERR_ALIGNMENT and fwd(wd=P + 8) == dm.ERR_ALIGNMENT
+    assert fwd(ws=W + 16) == dm.ERR_ALIGNMENT
+    assert fwd(nb=-1) == dm.ERR_WORKSPACE
+    assert fwd(shape=(0, 64, 96, 0, 0), x=None, y=None) == dm.OK       # no tokens, nothing to do
+    assert bwd(shape=(4, 64, 96, 0, 0)) == bad                          # nothing was kept
+    assert bwd(dy=None) == bad and bwd(dx=None) == bad and bwd(dwg=None) == bad and bwd(dwd=None) == bad
+    assert bwd(dx_ld=10) == bad and bwd(saved=hole) == bad
+    assert bwd(wg=P + 2) == dm.ERR_ALIGNMENT
+    assert bwd(nb=-1) == dm.ERR_WORKSPACE
+
+
+def test_xent_refuses_bad_arguments(dm):
+    lib = dm.lib()
+
+    def call(shape=(4, 64, 96), h=P, ld=64, w=P, t=P, gl=P, loss=P, lse=P, dh=P, dh_ld=64, dw=P, ws=W,
+             nb=None):
+        s = dm.XentShape(*shape)
+        need = lib.dmuon_xent_workspace_bytes(ctypes.byref(s), 1)
+        return lib.dmuon_xent(ctypes.byref(s), h, ld, w, t, gl, loss, lse, dh, dh_ld, dw, ws,
+                              need if nb is None else need + nb, None)
+
+    bad = dm.ERR_INVALID_ARG
+    assert lib.dmuon_xent(None, P, 64, P, P, P, P, P, P, 64, P, W, 1 << 40, None) == bad
+    assert call(shape=(4, 64, 0)) == bad
+    for k in ("h", "w", "t", "gl", "loss", "lse", "dh", "dw", "ws"):
+        assert call(**{k: None}) == bad, k
+    assert call(ld=63) == bad and call(dh_ld=63) == bad
+    assert call(w=P + 2) == dm.ERR_ALIGNMENT and call(ws=W + 128) == dm.ERR_ALIGNMENT
+    assert call(nb=-1) == dm.ERR_WORKSPACE
+    assert call(shape=(0, 64, 96), gl=None, dh=None, dw=None, h=None) == dm.OK
+
+
+def test_act8_refuses_bad_arguments(dm):
+    lib = dm.lib()
+    bad = dm.ERR_INVALID_ARG
+    for f, a, b in [(lib.dmuon_act8_save, 2, (3, 3)), (lib.dmuon_act8_load, 4, (3, 3))]:
+        save = f is lib.dmuon_act8_save
+
+        def call(rows=3, cols=40, x=P, ld=40, dt=dm.BF16, codes=P, scales=P):
+            if save:
+                return f(rows, cols, x, ld, dt, codes, scales, None)
+            return f(rows, cols, codes, scales, x, ld, dt, None)
+
+        assert call(rows=-1) == bad and call(cols=-1) == bad and call(dt=2) == bad
+        assert call(x=None) == bad and call(codes=None) == bad and call(scales=None) == bad
+        assert call(ld=39) == bad
+        assert call(x=P + 1) == dm.ERR_ALIGNMENT and call(scales=P + 1) == dm.ERR_ALIGNMENT
+        assert call(x=P + 2, dt=dm.F32) == dm.ERR_ALIGNMENT
+        assert call(rows=1 << 31, cols=2049, ld=2049) == dm.ERR_UNSUPPORTED
+        assert call(rows=0, x=None) == dm.OK and call(cols=0, x=None) == dm.OK
+
+
+def test_binding_refuses_wrong_tensors(dm):
+    import torch
+    with pytest.raises(TypeError):
+        dm._bf16_rows(torch.zeros(2, 3), 2, 3, "x")
+    with pytest.raises(ValueError):
+        dm._bf16_rows(torch.zeros(2, 3, dtype=torch.bfloat16), 2, 4, "x")
+    with pytest.raises(ValueError):      # not on a GPU
+        dm._bf16_rows(torch.zeros(2, 3, dtype=torch.bfloat16), 2, 3, "x")
+    with pytest.raises(TypeError):
+        dm.act8_save(torch.zeros(2, 3, dtype=torch.float16), torch.zeros(2, 3, dtype=torch.int8),
+                     torch.zeros(2, 1, dtype=torch.bfloat16))
+    with pytest.raises(dm.DMuonError):
+        dm.GatedFFN(4, 0, 8, device="cpu")
+    with pytest.raises(dm.DMuonError):
+        dm.LinearXent(4, 8, 0, device="cpu")
+    op = dm.GatedFFN(4, 8, 8, save=dm.SAVE_NONE, device="cpu")
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        op.backward(x, x, x, x, x, (), x, x, x, x)
+    with pytest.raises(ValueError):
+        op.forward(torch.zeros(5, 8, dtype=torch.bfloat16), x, x, x, x)
+    head = dm.LinearXent(4, 8, 8, grads=False, device="cpu")
+    with pytest.raises(ValueError):
+        head.loss_and_grads(x, x, x, x, x, x, x, x)

@@ -66,8 +66,15 @@ static_assert(kSmemBytes <= 232448, "dynamic shared memory above the per-block l
 // a time, close to the fewest panels that 76 tiles can share.
 constexpr int kStrip = 8;
 
+// The tensor core's accumulation rounds toward zero, so a sum of K products loses
+// up to K/16 * 2^-25 of its size.  That is far below bf16 for an output that is
+// rounded to it, but not for the fp32 losses: the logits are accumulated in runs
+// of kRun stages (512 K-elements), each drained and added in registers, rounded
+// to nearest.  The drains hide behind the next run's MMAs.
+constexpr int kRun = 4;
+
 // Split parts a launch may have, and the size of one.
-constexpr int kMaxParts = 304;
+constexpr int kMaxParts = 152;
 constexpr size_t kPartFloats = size_t(kTile) * kTile;
 
 struct Unit {
@@ -164,43 +171,50 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sA, uint8_t* sB, uint64_t* ful
   const int clusters = int(cluster_count_x());
   int stage = 0;
   uint32_t phase = 0;
-  int it = 0;
-  for (int u = int(cluster_id_x()); u < g.total_units; u += clusters, ++it) {
+  int it = 0;  // accumulators handed to the epilogue so far
+  bool ok = true;
+  for (int u = int(cluster_id_x()); ok && u < g.total_units; u += clusters) {
     const Unit U = decode_unit(g, u);
-    const int acc = it & 1;
-    const uint32_t aph = uint32_t(it >> 1) & 1u;
-    if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, abort_flag)) {
-      raise_abort(g.err, abort_flag);
-      break;
-    }
-    tc_fence_after();
-    const uint32_t d = tmem_base + uint32_t(acc * kAccCols);
-    bool ok = true;
-    for (int kb = U.kb_lo; kb < U.kb_hi; ++kb) {
-      if (!mbar_wait_cluster(&full_bar[stage], phase, abort_flag)) {
+    for (int lo = U.kb_lo; ok && lo < U.kb_hi; ++it) {
+      const int hi = EPI == kLinXent ? min(lo + kRun, U.kb_hi) : U.kb_hi;
+      const int acc = it & 1;
+      const uint32_t aph = uint32_t(it >> 1) & 1u;
+      if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, abort_flag)) {
         raise_abort(g.err, abort_flag);
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint64_t ad = a_desc + uint64_t(stage * (kOpBytes >> 4));
-      const uint64_t bd = b_desc + uint64_t(stage * (kOpBytes >> 4));
+      const uint32_t d = tmem_base + uint32_t(acc * kAccCols);
+      for (int kb = lo; kb < hi; ++kb) {
+        if (!mbar_wait_cluster(&full_bar[stage], phase, abort_flag)) {
+          raise_abort(g.err, abort_flag);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = a_desc + uint64_t(stage * (kOpBytes >> 4));
+        const uint64_t bd = b_desc + uint64_t(stage * (kOpBytes >> 4));
 #pragma unroll
-      for (int k = 0; k < kK / 16; ++k) {
-        const uint64_t ao = A_MN ? uint64_t(k) * (2048u >> 4)
-                                 : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
-        const uint64_t bo = B_MN ? uint64_t(k) * (2048u >> 4)
-                                 : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
-        umma_bf16_pair(d, ad + ao, bd + bo, idesc, (kb > U.kb_lo || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kK / 16; ++k) {
+          const uint64_t ao = A_MN
+                                  ? uint64_t(k) * (2048u >> 4)
+                                  : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
+          const uint64_t bo = B_MN
+                                  ? uint64_t(k) * (2048u >> 4)
+                                  : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
+          umma_bf16_pair(d, ad + ao, bd + bo, idesc, (kb > lo || k > 0) ? 1u : 0u);
+        }
+        umma_commit_pair(&empty_bar[stage], 0x3);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      umma_commit_pair(&empty_bar[stage], 0x3);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      if (!ok) break;
+      umma_commit_pair(&tfull[acc], 0x3);
+      lo = hi;
     }
-    if (!ok) break;
-    umma_commit_pair(&tfull[acc], 0x3);
   }
   // every issued MMA must finish before TMEM and shared memory go away
   umma_commit_pair(drain_bar, 0x1);
@@ -466,6 +480,11 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
             continue;
           }
         }
+        if (g.scale != nullptr) {
+          const float f = *g.scale;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= f;
+        }
         if (P.c_map >= 0) put(P.c_map, v, c0, rg0);
         else if (r < P.m) store_row32(P.c + (long long)r * P.c_ld + c0, P.n - c0, false, v);
       }
@@ -526,49 +545,99 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
         put(g.map_dup, v, c0, rg0);
         put(g.map_h, up, c0, rg0);
       }
-    } else {  // kLinXent
-      const int g0 = U.tj * kTile + h * kXentGroup;  // first vocabulary entry of the group
-      if (g0 < P.n) {
-        float m = -INFINITY;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const int c0 = g0 + k * 32;
-          if (c0 >= P.n) break;
-          float v[32];
-          load_acc(k, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j < P.n) m = fmaxf(m, v[j]);
-        }
-        const long long t = r < P.m ? g.target[r] : -1;
-        const int d = t >= g0 && t < g0 + kXentGroup ? int(t - g0) : -1;
-        float s = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const int c0 = g0 + k * 32;
-          if (c0 >= P.n) break;
-          float v[32];
-          load_acc(k, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (k * 32 + j == d) g.target_logit[r] = v[j];
-            v[j] = c0 + j < P.n ? exp2f((v[j] - m) * 1.44269504f) : 0.f;
-            s += v[j];
-          }
-          if (P.c_map >= 0) {
-            uint32_t o[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __half2 p = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-              o[j] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            put_raw(P.c_map, o, c0, rg0);
-          }
-        }
-        if (r < P.m) g.group_stat[(long long)(g0 / kXentGroup) * g.stat_ld + r] = make_float2(m, s);
-      }
     }
     if (parts == nullptr) release();
+  }
+  // stores complete, and stop reading shared memory, before the CTA exits
+  if (lane == 0) bulk_wait_all();
+  __syncwarp();
+}
+
+// Logits of 32 tokens x 128 vocabulary entries per warp, in registers.
+DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
+                          uint32_t epi_smem, uint32_t tmem_base, volatile int* abort_flag) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, h = (warp - 2) >> 2, ew = warp - 2;
+  const uint32_t buf0 = epi_smem + uint32_t(ew * 2 * kEpiBufBytes);
+  const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
+  const int clusters = int(cluster_count_x());
+  const LinProblem& P = g.prob[0];
+  int it = 0;
+  bool ok = true;
+  for (int u = int(cluster_id_x()); ok && u < g.total_units; u += clusters) {
+    const Unit U = decode_unit(g, u);
+    const int rg0 = U.ti * kTile + int(rank) * kHalf + q * 32;
+    const int r = rg0 + lane;
+    const int g0 = U.tj * kTile + h * kXentGroup;  // first vocabulary entry of the group
+    float z[kXentGroup];
+#pragma unroll
+    for (int j = 0; j < kXentGroup; ++j) z[j] = 0.f;
+#pragma unroll 1
+    for (int lo = U.kb_lo; lo < U.kb_hi; lo += kRun, ++it) {
+      const int acc = it & 1;
+      int w = 1;
+      if (lane == 0) w = mbar_wait_cluster(&tfull[acc], uint32_t(it >> 1) & 1u, abort_flag) ? 1 : 0;
+      w = __shfl_sync(0xffffffffu, w, 0);
+      if (!w) {
+        if (lane == 0) raise_abort(g.err, abort_flag);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t = tmem_base + uint32_t(acc * kAccCols + h * kXentGroup) +
+                         (uint32_t(q * 32) << 16);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float v[16];
+        tmem_ld16(t + uint32_t(k * 16), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[k * 16 + j] += v[j];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty + uint32_t(acc) * 8u);
+    }
+    if (!ok || g0 >= P.n) continue;
+    const int n = P.n - g0;  // entries of the group that exist, if below 128
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kXentGroup; ++j)
+      if (j < n) m = fmaxf(m, z[j]);
+    const long long t = r < P.m ? g.target[r] : -1;
+    const int d = t >= g0 && t < g0 + kXentGroup && t < P.n ? int(t - g0) : -1;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int j = k * 32; j < k * 32 + 32; ++j) {
+        if (j == d) g.target_logit[r] = z[j];
+        z[j] = j < n ? exp2f((z[j] - m) * 1.44269504f) : 0.f;
+        s += z[j];
+      }
+      if (P.c_map >= 0 && k * 32 < n) {
+        const uint32_t buf = buf0 + uint32_t((k & 1) * kEpiBufBytes);
+        if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 p = __floats2half2_rn(z[k * 32 + 8 * i + 2 * j], z[k * 32 + 8 * i + 2 * j + 1]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          st_shared_v4(buf + epi_off(lane, i), o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&g.maps[P.c_map], buf, g0 + k * 32, rg0);
+          bulk_commit();
+        }
+      }
+    }
+    if (r < P.m) g.group_stat[(long long)(g0 / kXentGroup) * g.stat_ld + r] = make_float2(m, s);
   }
   // stores complete, and stop reading shared memory, before the CTA exits
   if (lane == 0) bulk_wait_all();
@@ -622,7 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
       mma_issuer<EPI, A_MN, B_MN>(g, sA, sB, full_bar, empty_bar, tfull, tempty, drain_bar,
                                   tmem_base, abort_flag);
   } else if (warp >= 2) {
-    epilogue<EPI>(g, rank, tfull, tempty, smem_u32(sE), tmem_base, abort_flag);
+    if constexpr (EPI == kLinXent)
+      epilogue_xent(g, rank, tfull, tempty, smem_u32(sE), tmem_base, abort_flag);
+    else
+      epilogue<EPI>(g, rank, tfull, tempty, smem_u32(sE), tmem_base, abort_flag);
   }
 
   __syncthreads();
@@ -671,15 +743,34 @@ cudaError_t lin_prepare() {
   return cudaSuccess;
 }
 
-void lin_schedule(LinArgs& g, int clusters) {
-  (void)clusters;
-  int tiles = 0;
+void lin_schedule(LinArgs& g, bool may_split, int clusters) {
+  int tiles = 0, kb = 0;
   for (int p = 0; p < g.n_prob; ++p) {
     g.prob[p].tile_begin = tiles;
     tiles += g.prob[p].tiles_m * g.prob[p].tiles_n;
+    const int k = g.prob[p].kb0 + g.prob[p].kb1;
+    kb = p == 0 || k < kb ? k : kb;
   }
   g.full_tiles = g.total_units = tiles;
   g.split = 1;
+  const int rest = tiles % clusters;
+  if (!may_split || rest == 0) return;
+  // Time of the last wave in K blocks (about 0.55 us each): a part costs its
+  // blocks plus about 4 for filling the pipeline and writing its accumulator,
+  // and the warp that joins S parts reads them at about 2 blocks each.
+  long long best = kb;
+  for (int s = 2; s * rest <= kMaxParts && 2 * s <= kb; ++s) {
+    const long long waves = ((long long)rest * s + clusters - 1) / clusters;
+    const long long cost = waves * ((kb + s - 1) / s + 4) + 2 * s;
+    if (cost < best) {
+      best = cost;
+      g.split = s;
+    }
+  }
+  if (g.split > 1) {
+    g.full_tiles = tiles - rest;
+    g.total_units = g.full_tiles + rest * g.split;
+  }
 }
 
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,

@@ -62,6 +62,7 @@ struct LinArgs {
   // kLinStore: fp32 running sum over launches (row pitch = n of the product)
   float* sum;
   int sum_read, sum_write;  // add what `sum` holds; write the sum there instead of C
+  const float* scale;    // C = scale * acc (device scalar), or null
   // kLinGlu / kLinGluGrad
   int act, keep;
   int ffn;
@@ -82,7 +83,7 @@ size_t lin_arrived_bytes();
 cudaError_t lin_prepare();  // once per device
 // Split the tiles of the last, partly filled wave along K (sets full_tiles ..
 // total_units from the products' tile counts).
-void lin_schedule(LinArgs& g, int clusters);
+void lin_schedule(LinArgs& g, bool may_split, int clusters);
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
                        cudaStream_t s);
 
@@ -105,11 +106,15 @@ struct XentRows {
   long long tokens, vocab;
   const long long* target;
   const float* grad_loss;   // null: no gradients
+  const float* grad_scale;  // G is formed of grad_loss / *grad_scale
   const float* target_logit;
   const float2* group_stat;
   long long stat_ld;
   float *loss, *lse;
 };
+// *scale = the largest |grad_loss| of the tokens that have a target (1 if that is 0).
+cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,
+                              long long vocab, float* scale, cudaStream_t s);
 cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s);
 // Exponentials (fp16) to gradients of the logits (bf16), in place.
 cudaError_t launch_xent_grad(const XentRows& r, void* e, long long e_ld, cudaStream_t s);

@@ -124,7 +124,7 @@ struct Launch {
   }
   int run(int epi, bool a_mn, bool b_mn, int clusters, cudaStream_t s) {
     if (!ok) return DMUON_ERR_CUDA;
-    lin_schedule(g, clusters);
+    lin_schedule(g, epi != kLinXent, clusters);
     if (g.split > 1 &&
         cudaMemsetAsync(g.arrived, 0, lin_arrived_bytes(), s) != cudaSuccess)
       return DMUON_ERR_CUDA;
@@ -348,7 +348,7 @@ int64_t xent_piece(const dmuon_xent_shape& s, bool grads) {
 struct XentSpace {
   ProductSpace ps;
   bf16 *hidden, *weight, *e;
-  float* target_logit;
+  float *target_logit, *grad_scale;
   float2* stat;
   float* sum;
   int64_t piece, stat_ld;
@@ -363,6 +363,7 @@ XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   x.ps = take_product_space(c);
   x.hidden = c.take<bf16>(size_t(s.tokens) * d8 * 2);
   x.target_logit = c.take<float>(size_t(s.tokens) * 4);
+  x.grad_scale = c.take<float>(4);
   x.stat = c.take<float2>(groups * size_t(x.stat_ld) * sizeof(float2));
   if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * d8 * 2);
   if (grads) {
@@ -393,7 +394,8 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     // reaches the weight's gradient, which sums over rows
     hr_ld = up8(s.hidden);
     if (launch_copy_rows(s.tokens, s.hidden, static_cast<const bf16*>(hidden), h_ld, x.hidden,
-                         hr_ld, tgt, s.vocab, st) != cudaSuccess)
+                         hr_ld, tgt, s.vocab, st) != cudaSuccess ||
+        launch_grad_scale(grad_loss, tgt, s.tokens, s.vocab, x.grad_scale, st) != cudaSuccess)
       return DMUON_ERR_CUDA;
     h = x.hidden;
   } else {
@@ -409,6 +411,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     R.vocab = s.vocab;
     R.target = tgt + t0;
     R.grad_loss = grads ? grad_loss + t0 : nullptr;
+    R.grad_scale = x.grad_scale;
     R.target_logit = x.target_logit + t0;
     R.group_stat = x.stat;
     R.stat_ld = x.stat_ld;
@@ -436,6 +439,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
       P.a0 = L.operand(x.e, s.vocab, n, v8);
       P.b0 = L.operand(w, s.hidden, s.vocab, w_ld);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
+      L.g.scale = x.grad_scale;
       e = L.run(kLinStore, false, true, clusters, st);
       if (e != DMUON_OK) return e;
     }
@@ -445,6 +449,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     P.a0 = L.operand(x.e, s.vocab, n, v8);
     P.b0 = L.operand(hp, s.hidden, n, hr_ld);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
+    L.g.scale = x.grad_scale;
     L.g.sum = x.sum;
     L.g.sum_read = t0 > 0;
     L.g.sum_write = t0 + n < s.tokens;

@@ -171,6 +171,26 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(long long cols, lon
   }
 }
 
+__global__ void __launch_bounds__(1024) grad_scale_kernel(const float* grad_loss,
+                                                          const long long* target,
+                                                          long long tokens, long long vocab,
+                                                          float* scale) {
+  __shared__ float top[32];
+  float m = 0.f;
+  for (long long t = threadIdx.x; t < tokens; t += 1024)
+    if (live_target(target, t, vocab)) m = fmaxf(m, fabsf(grad_loss[t]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = top[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x == 0) *scale = m > 0.f ? m : 1.f;
+  }
+}
+
 // One block per 32 tokens: 8 warps share the groups, lane = token.
 __global__ void __launch_bounds__(kThreads) xent_rows_kernel(const XentRows r) {
   __shared__ float sm[8][32], ss[8][32];
@@ -208,9 +228,11 @@ __global__ void __launch_bounds__(kThreads) xent_rows_kernel(const XentRows r) {
   r.lse[row] = live ? m + ls : 0.f;
 }
 
-// G = grad_loss * (exp(z - lse) - [entry is the target]).  exp(z - m) comes in
-// fp16, whose 11 bits leave the one rounding to bf16 here the only one that
-// shows; at the target the difference to 1 is taken as expm1(-loss).
+// G = grad_loss / scale * (exp(z - lse) - [entry is the target]).  exp(z - m)
+// comes in fp16, whose 11 bits leave the one rounding to bf16 here the only one
+// that shows; at the target the difference to 1 is taken as expm1(-loss).  With
+// equal weights (a mean) grad_loss / scale is 1, and the -1 of an unlikely target
+// is exact; the scale is put back in fp32 where the products are written.
 __global__ void __launch_bounds__(kThreads) xent_grad_kernel(const XentRows r, uint4* e,
                                                              long long e_ld, long long tiles) {
   const long long row = blockIdx.x / tiles;
@@ -222,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) xent_grad_kernel(const XentRows r, u
     *p = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const float gl = r.grad_loss[row];
+  const float gl = r.grad_loss[row] / *r.grad_scale;
   const float f = gl * exp2f((r.group_stat[(c0 / kXentGroup) * r.stat_ld + row].x - r.lse[row]) *
                              1.44269504f);
   const uint4 q = *p;
@@ -290,6 +312,12 @@ cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16
 cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst, long long ld,
                              cudaStream_t s) {
   return launch_copy_rows(rows, cols, nullptr, 8, dst, ld, nullptr, 0, s);
+}
+
+cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,
+                              long long vocab, float* scale, cudaStream_t s) {
+  grad_scale_kernel<<<1, 1024, 0, s>>>(grad_loss, target, tokens, vocab, scale);
+  return counted(cudaGetLastError());
 }
 
 cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s) {

@@ -16,6 +16,15 @@
 // Each operand is K-major (rows of K) or MN-major (rows of M or N), a template
 // parameter, so no operand is ever transposed in memory.
 //
+// Two orientations (template parameter SWAP).  Plainly, the tokens are M and a
+// tile holds 256 of them.  Swapped, the weight's rows are M and the tokens are N,
+// and a tile holds `nt` tokens, a multiple of 32 chosen to fit: with few tokens the
+// launch streams the weights at the memory's rate instead of multiplying padding
+// (a stage is then 32 KB of weights and nt/2 token rows, and more stages fit), and
+// a ragged count wastes less of its last tile.  The accumulator's lanes are then
+// the weight's rows; each 32 x 32 chunk is turned in shared memory, and from there
+// on both orientations share the epilogue code: a lane holds one token.
+//
 // The products are bound by the tensor cores, so the unit of work is the one
 // that needs the least operand traffic per MMA: a 256 x 256 tile on a pair of
 // SMs (tcgen05.mma.cta_group::2, M = N = 256, K = 16), each CTA staging its 128
@@ -28,9 +37,10 @@
 //
 // Tiles are handed out statically.  With T tiles on P pairs the last wave fills
 // only T mod P pairs; its tiles are split along K into parts that fill the
-// wave, the parts' fp32 accumulators go to the workspace, and the warp that
-// arrives last at a part of a tile adds them in order (so the result does not
-// depend on which one was last) and runs the epilogue.
+// wave; the parts' fp32 accumulators go to the workspace, and a second, fully
+// parallel launch adds them in order and runs the epilogue on the sums.  (Letting
+// the last arriving CTA of a tile do that in the first launch serialises the reads:
+// 12 parts of a 160 x 256 tile took 25 us longer.)
 #include "act8.cuh"
 #include "dmuon.h"
 #include "epi.cuh"
@@ -38,6 +48,7 @@
 #include "ptx.cuh"
 #include "train.h"
 
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,10 +58,10 @@ namespace {
 constexpr int kTile = 256;                 // tile rows and columns (CTA pair)
 constexpr int kHalf = 128;                 // one CTA's rows of A / columns of B
 constexpr int kK = 128;                    // K-elements per stage
-constexpr int kStages = 3;
-constexpr int kOpBytes = kHalf * kK * 2;   // 32 KB: one CTA's share of an operand
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kPairTx = 2 * kStageBytes;   // both CTAs' loads land on the leader's barrier
+constexpr int kStages = 3;                 // of 64 KB; swapped, as many as fit there
+constexpr int kMaxStages = 5;
+constexpr int kOpBytes = kHalf * kK * 2;   // 32 KB: one CTA's share of a 256-wide operand
+constexpr int kStageArea = kStages * 2 * kOpBytes;
 constexpr int kAtom = kOpBytes / 2;        // one TMA box: 64 K x 128 rows, or 64 MN x 128 K
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -58,8 +69,9 @@ constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;
 constexpr int kEpiBytes = kEpiWarps * 2 * kEpiBufBytes;
 constexpr int kBarBytes = 512;
-constexpr size_t kSmemBytes = size_t(kStages) * kStageBytes + kEpiBytes + 1024 + kBarBytes;
+constexpr size_t kSmemBytes = size_t(kStageArea) + kEpiBytes + 1024 + kBarBytes;
 static_assert(kSmemBytes <= 232448, "dynamic shared memory above the per-block limit");
+static_assert((2 * kMaxStages + 4 + 1 + 8) * 8 + 8 <= kBarBytes, "barrier area too small");
 
 // Tiles of a product are walked in strips of kStrip tile rows, columns outer,
 // rows inner: the pairs then work on about 8 row panels and 9 column panels at
@@ -73,9 +85,14 @@ constexpr int kStrip = 8;
 // to nearest.  The drains hide behind the next run's MMAs.
 constexpr int kRun = 4;
 
-// Split parts a launch may have, and the size of one.
-constexpr int kMaxParts = 152;
-constexpr size_t kPartFloats = size_t(kTile) * kTile;
+// Workspace of the split parts.
+constexpr size_t kPartialBytes = size_t(40) << 20;
+
+// The B operand's share of a stage: 128 columns, or half of the nt tokens.
+template <bool SWAP>
+DM_DEV int b_rows(const LinArgs& g) { return SWAP ? g.nt / 2 : kHalf; }
+template <bool SWAP>
+DM_DEV int stage_bytes(const LinArgs& g) { return kOpBytes + b_rows<SWAP>(g) * kK * 2; }
 
 struct Unit {
   int prob, ti, tj;
@@ -116,41 +133,53 @@ DM_DEV Unit decode_unit(const LinArgs& g, int u) {
 }
 
 // ------------------------------------------------------------------ roles
-template <int EPI, bool A_MN, bool B_MN>
-DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sA, uint8_t* sB,
-                     uint64_t* full_bar, uint64_t* empty_bar, volatile int* abort_flag) {
+template <int EPI, bool A_MN, bool B_MN, bool SWAP>
+DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t* full_bar,
+                     uint64_t* empty_bar, volatile int* abort_flag) {
   const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0);
   const int clusters = int(cluster_count_x());
+  const int stages = SWAP ? g.stages : kStages;
+  const int bytes = stage_bytes<SWAP>(g), brows = b_rows<SWAP>(g);
   int stage = 0;
   uint32_t phase = 0;
   for (int u = int(cluster_id_x()); u < g.total_units; u += clusters) {
     const Unit U = decode_unit(g, u);
     const LinProblem& P = g.prob[U.prob];
-    const int row0 = U.ti * kTile + int(rank) * kHalf;
-    const int col0 = EPI == kLinGlu ? U.tj * kHalf : U.tj * kTile + int(rank) * kHalf;
+    // kLinGlu: a plain tile's B half is the gate's (first CTA) or the up's rows; a
+    // swapped tile's A share is 64 rows of each
+    const int row0 = SWAP && EPI == kLinGlu ? U.ti * kHalf + int(rank) * 64
+                                            : U.ti * kTile + int(rank) * kHalf;
+    const int col0 = SWAP ? U.tj * g.nt + int(rank) * brows
+                          : (EPI == kLinGlu ? U.tj * kHalf : U.tj * kTile + int(rank) * kHalf);
     for (int kb = U.kb_lo; kb < U.kb_hi; ++kb) {
       const bool second = EPI != kLinGlu && kb >= P.kb0;
       const CUtensorMap* mapA = &g.maps[second ? P.a1 : P.a0];
       const CUtensorMap* mapB =
-          &g.maps[EPI == kLinGlu ? (rank == 0 ? P.b0 : P.b1) : (second ? P.b1 : P.b0)];
+          &g.maps[EPI == kLinGlu && !SWAP ? (rank == 0 ? P.b0 : P.b1) : (second ? P.b1 : P.b0)];
       const int k0 = (second ? kb - P.kb0 : kb) * kK;
       if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) {
         raise_abort(g.err, abort_flag);
         return;
       }
-      if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], kPairTx);
+      if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], uint32_t(2 * bytes));
       const uint32_t bar = leader_full + uint32_t(stage) * 8u;
-      uint8_t* a = sA + stage * kOpBytes;
-      uint8_t* b = sB + stage * kOpBytes;
+      uint8_t* a = sStage + stage * bytes;
+      uint8_t* b = a + kOpBytes;
       // rows, columns and K past the tensors' ends read as zeros
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (A_MN) tma_load_2d_pair(a + h * kAtom, mapA, bar, row0 + h * 64, k0);
-        else tma_load_2d_pair(a + h * kAtom, mapA, bar, k0 + h * 64, row0);
+        if (SWAP && EPI == kLinGlu) {
+          tma_load_2d_pair(a + h * kAtom, &g.maps[P.a0], bar, k0 + h * 64, row0);
+          tma_load_2d_pair(a + h * kAtom + kAtom / 2, &g.maps[P.a1], bar, k0 + h * 64, row0);
+        } else if (A_MN) {
+          tma_load_2d_pair(a + h * kAtom, mapA, bar, row0 + h * 64, k0);
+        } else {
+          tma_load_2d_pair(a + h * kAtom, mapA, bar, k0 + h * 64, row0);
+        }
         if (B_MN) tma_load_2d_pair(b + h * kAtom, mapB, bar, col0 + h * 64, k0);
-        else tma_load_2d_pair(b + h * kAtom, mapB, bar, k0 + h * 64, col0);
+        else tma_load_2d_pair(b + h * brows * 128, mapB, bar, k0 + h * 64, col0);
       }
-      if (++stage == kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -158,16 +187,20 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sA, uint8_t* sB,
   }
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sA, uint8_t* sB, uint64_t* full_bar,
-                       uint64_t* empty_bar, uint64_t* tfull, uint64_t* tempty,
-                       uint64_t* drain_bar, uint32_t tmem_base, volatile int* abort_flag) {
-  constexpr uint32_t idesc = idesc_bf16(kTile, kTile, A_MN, B_MN);
-  // K-major: two 64-element panels 16 KB apart, 32 bytes per K step inside a
-  // 128-byte row, 8-row groups 1 KB apart.  MN-major: 64-element atoms 16 KB
-  // apart (LBO), 8-row K groups 1 KB apart (SBO), 2 KB per K step.
-  const uint64_t a_desc = sdesc_sw128(smem_u32(sA), A_MN ? kAtom : 16, 1024);
-  const uint64_t b_desc = sdesc_sw128(smem_u32(sB), B_MN ? kAtom : 16, 1024);
+template <int EPI, bool A_MN, bool B_MN, bool SWAP>
+DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, uint64_t* empty_bar,
+                       uint64_t* tfull, uint64_t* tempty, uint64_t* drain_bar, uint32_t tmem_base,
+                       volatile int* abort_flag) {
+  const uint32_t idesc = idesc_bf16(kTile, SWAP ? g.nt : kTile, A_MN, B_MN);
+  // K-major: two 64-element panels, 32 bytes per K step inside a 128-byte row,
+  // 8-row groups 1 KB apart.  MN-major: 64-element atoms 16 KB apart (LBO), 8-row K
+  // groups 1 KB apart (SBO), 2 KB per K step.  Shared-memory addresses stay below
+  // 256 KB, so adding to the start-address field never carries out of it.
+  const uint64_t a_desc = sdesc_sw128(smem_u32(sStage), A_MN ? kAtom : 16, 1024);
+  const uint64_t b_desc = sdesc_sw128(smem_u32(sStage) + kOpBytes, B_MN ? kAtom : 16, 1024);
+  const uint32_t step = uint32_t(stage_bytes<SWAP>(g)) >> 4;
+  const uint32_t b_panel = uint32_t(b_rows<SWAP>(g)) * 128u >> 4;
+  const int stages = SWAP ? g.stages : kStages;
   const int clusters = int(cluster_count_x());
   int stage = 0;
   uint32_t phase = 0;
@@ -193,20 +226,19 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sA, uint8_t* sB, uint64_t* ful
           break;
         }
         tc_fence_after();
-        const uint64_t ad = a_desc + uint64_t(stage * (kOpBytes >> 4));
-        const uint64_t bd = b_desc + uint64_t(stage * (kOpBytes >> 4));
+        const uint64_t ad = a_desc + uint64_t(uint32_t(stage) * step);
+        const uint64_t bd = b_desc + uint64_t(uint32_t(stage) * step);
 #pragma unroll
         for (int k = 0; k < kK / 16; ++k) {
           const uint64_t ao = A_MN
                                   ? uint64_t(k) * (2048u >> 4)
                                   : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
-          const uint64_t bo = B_MN
-                                  ? uint64_t(k) * (2048u >> 4)
-                                  : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
+          const uint64_t bo = B_MN ? uint64_t(k) * (2048u >> 4)
+                                   : uint64_t(uint32_t(k >> 2) * b_panel) + uint64_t(k & 3) * (32u >> 4);
           umma_bf16_pair(d, ad + ao, bd + bo, idesc, (kb > lo || k > 0) ? 1u : 0u);
         }
         umma_commit_pair(&empty_bar[stage], 0x3);
-        if (++stage == kStages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -223,17 +255,19 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sA, uint8_t* sB, uint64_t* ful
 
 // ------------------------------------------------------------------ epilogue
 // act(x) and, for the gradient, act'(x), in fp32.
-DM_DEV float act_value(int act, float x) {
-  if (act == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
-  if (act == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
+template <int ACT>
+DM_DEV float act_value(float x) {
+  if (ACT == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
+  if (ACT == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
   return 0.5f * x * (1.f + tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x)));
 }
-DM_DEV void act_both(int act, float x, float& a, float& da) {
-  if (act == DMUON_ACT_SILU) {
+template <int ACT>
+DM_DEV void act_both(float x, float& a, float& da) {
+  if (ACT == DMUON_ACT_SILU) {
     const float s = __fdividef(1.f, 1.f + __expf(-x));
     a = x * s;
     da = s * fmaf(x, 1.f - s, 1.f);
-  } else if (act == DMUON_ACT_GELU) {
+  } else if (ACT == DMUON_ACT_GELU) {
     const float phi = 0.5f * (1.f + erff(x * 0.70710678f));
     a = x * phi;
     da = fmaf(x * 0.39894228f, __expf(-0.5f * x * x), phi);
@@ -242,6 +276,25 @@ DM_DEV void act_both(int act, float x, float& a, float& da) {
     const float half = 0.5f * (1.f + t);
     a = x * half;
     da = fmaf(0.5f * x * (1.f - t * t), 0.79788456f * fmaf(0.134145f * x, x, 1.f), half);
+  }
+}
+// a <- act(a) * b
+template <int ACT>
+DM_DEV void glu32(float (&a)[32], const float (&b)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) a[j] = act_value<ACT>(a[j]) * b[j];
+}
+// From dh, gate and up: v <- dup, ga <- dgate, up <- h
+template <int ACT>
+DM_DEV void glu_grad32(float (&v)[32], float (&ga)[32], float (&up)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float a, da;
+    act_both<ACT>(ga[j], a, da);
+    const float dh = v[j];
+    ga[j] = dh * up[j] * da;
+    up[j] *= a;
+    v[j] = dh * a;
   }
 }
 
@@ -271,28 +324,31 @@ DM_DEV void unpack8(const uint4& q, float* f) {
   }
 }
 
-// One row's block of 32 values in 8 bits; values past n are not written.
+// One row's block of 32 fp32 values in 8 bits; values past n are not written.  The
+// quotient is taken with the scale's rounded reciprocal: within 2e-5 of a step, far
+// below what the accumulation of the values leaves uncertain.
 DM_DEV void store_act8(signed char* codes, __nv_bfloat16* scale, int n, bool vec,
-                       const float (&v)[32]) {
-  float top = 0.f;
-  bool finite = true;
+                       float (&v)[32]) {
+  if (n < 32) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < n) {
-      top = fmaxf(top, fabsf(v[j]));
-      finite = finite && fabsf(v[j]) <= 3.402823466e38f;
-    }
-  const float s = act8_scale(top, finite);
-  const bool live = finite && s > 0.f;
+    for (int j = 0; j < 32; ++j)
+      if (j >= n) v[j] = 0.f;
+  }
+  float top = 0.f, bad = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    top = fmaxf(top, fabsf(v[j]));
+    bad = fmaf(v[j], 0.f, bad);  // NaN once a value is not finite
+  }
+  const float s = act8_scale(top, bad == 0.f);
+  const float r = bad == 0.f && s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
   uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    uint32_t p = 0;
+  for (int j = 0; j < 8; ++j) {
+    uint32_t c[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (live && j + k < n) p |= act8_code_f32(v[j + k], s) << (8 * k);
-    }
-    w[j / 4] = p;
+    for (int k = 0; k < 4; ++k) c[k] = act8_code_fast(bad == 0.f ? v[4 * j + k] : 0.f, r);
+    w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }
   if (vec && n >= 32) {
     reinterpret_cast<uint4*>(codes)[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -305,74 +361,122 @@ DM_DEV void store_act8(signed char* codes, __nv_bfloat16* scale, int n, bool vec
   *scale = __float2bfloat16_rn(s);
 }
 
-// 32 kept values of one row (columns c0 .. c0 + 31, n of them inside).
-DM_DEV void load_kept(const LinArgs& g, const void* base, const __nv_bfloat16* scales, int row,
-                      int c0, int n, float (&v)[32]) {
+// 32 kept values of one row (columns c0 .. c0 + 31, n of them inside), fetched as
+// stored: their loads are issued a chunk ahead of their use.
+struct Kept {
+  uint4 q[4];
+  float scale;
+};
+DM_DEV void fetch_kept(const LinArgs& g, const void* base, const __nv_bfloat16* scales, int row,
+                       int c0, int n, Kept& k) {
   if (g.keep == kKeepBf16) {
     const __nv_bfloat16* p =
         static_cast<const __nv_bfloat16*>(base) + (long long)row * g.ffn + c0;
     if (g.kept_vec && n >= 32) {
-      uint4 q[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) q[u] = reinterpret_cast<const uint4*>(p)[u];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) unpack8(q[u], v + 8 * u);
+      for (int u = 0; u < 4; ++u) k.q[u] = __ldcs(reinterpret_cast<const uint4*>(p) + u);
     } else {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+      uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = j < n ? __bfloat162float(p[j]) : 0.f;
+      for (int j = 0; j < 16; ++j)
+        w[j] = (2 * j < n ? uint32_t(e[2 * j]) : 0u) |
+               (2 * j + 1 < n ? uint32_t(e[2 * j + 1]) << 16 : 0u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k.q[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     }
   } else {
     const signed char* p = static_cast<const signed char*>(base) + (long long)row * g.ffn + c0;
     const int blocks = (g.ffn + kActBlock - 1) / kActBlock;
-    const float s = __bfloat162float(scales[(long long)row * blocks + c0 / kActBlock]);
+    k.scale = __bfloat162float(scales[(long long)row * blocks + c0 / kActBlock]);
     if (g.kept_vec && n >= 32) {
-      const uint4 q[2] = {reinterpret_cast<const uint4*>(p)[0],
-                          reinterpret_cast<const uint4*>(p)[1]};
-      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+      k.q[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+      k.q[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+    } else {
+      uint32_t w[8] = {};
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        v[j] = s * float((signed char)(w[j / 4] >> (8 * (j & 3))));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = j < n ? s * float(p[j]) : 0.f;
+        if (j < n) w[j / 4] |= uint32_t(uint8_t(p[j])) << (8 * (j & 3));
+      k.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      k.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
 }
+DM_DEV void kept_values(const LinArgs& g, const Kept& k, float (&v)[32]) {
+  if (g.keep == kKeepBf16) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) unpack8(k.q[u], v + 8 * u);
+  } else {
+    const uint32_t w[8] = {k.q[0].x, k.q[0].y, k.q[0].z, k.q[0].w,
+                           k.q[1].x, k.q[1].y, k.q[1].z, k.q[1].w};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = k.scale * float((signed char)(w[j / 4] >> (8 * (j & 3))));
+  }
+}
 
-template <int EPI>
+// A 32 x 32 fp32 chunk in a warp's 4 KB of shared memory, turned: lane i writes
+// element j of its row to word (j, i ^ j), lane j reads back (j, i ^ j) for every
+// i.  Both touch 32 banks per instruction.
+DM_DEV void turn_write(float* buf, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) buf[j * 32 + (lane ^ j)] = v[j];
+}
+DM_DEV void turn_read(const float* buf, int lane, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = buf[lane * 32 + (i ^ lane)];
+}
+
+// A swapped kLinGlu chunk has gate in the TMEM lanes of one warp and up in those of
+// another, which hands its part over: `ready` and `taken` are mbarriers that one
+// lane of the giving and of the receiving warp arrives on.
+struct Handover {
+  uint64_t *ready, *taken;
+  uint32_t parity;
+};
+
+template <int EPI, bool SWAP>
 DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
-                     uint32_t epi_smem, uint32_t tmem_base, volatile int* abort_flag) {
+                     uint8_t* epi, uint64_t* pair_bar, uint32_t tmem_base,
+                     volatile int* abort_flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3;          // TMEM lane quarter this warp may read
-  const int h = (warp - 2) >> 2;   // which half of the tile's columns
+  const int h = (warp - 2) >> 2;   // which half of the tile's columns (swapped: of its chunks)
   const int ew = warp - 2;
-  const uint32_t buf0 = epi_smem + uint32_t(ew * 2 * kEpiBufBytes);
+  // two 2 KB chunks to be stored; swapped, also the 4 KB in which a chunk is turned
+  float* turn = reinterpret_cast<float*>(epi + ew * 2 * kEpiBufBytes);
+  const uint32_t buf0 = smem_u32(turn);
   const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
   const int clusters = int(cluster_count_x());
-  const int r_loc = int(rank) * kHalf + q * 32;
+  const int chunks = SWAP ? g.nt / 32 : kAccCols / 32;  // 32-column chunks of the accumulator
   int stored = 0;  // chunks staged so far (their buffers alternate)
+  const int pair = h * 2 + (q & 1);
+  Handover ho{pair_bar + 2 * pair, pair_bar + 2 * pair + 1, 0u};
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    int w = 1;
+    if (lane == 0) {
+      w = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
+      if (!w) raise_abort(g.err, abort_flag);
+    }
+    return __shfl_sync(0xffffffffu, w, 0) != 0;
+  };
+  auto arrive_warp = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
-  // Write a 32 x 32 chunk (rows rg0.., columns c0..) of an output with m rows
-  // and n columns: through shared memory by TMA, which drops what lies outside.
-  auto put_raw = [&](int map, const uint32_t (&w)[16], int c0, int rg0) {
+  // Write a 32 x 32 chunk (rows rg0.., columns c0..) of an output through shared
+  // memory by TMA, which drops what lies outside.
+  auto put = [&](int map, const float (&o)[32], int c0, int rg0) {
     const uint32_t buf = buf0 + uint32_t((stored++ & 1) * kEpiBufBytes);
     if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
     __syncwarp();
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      st_shared_v4(buf + epi_off(lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    epi_store_row(buf, lane, o);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       tma_store_2d(&g.maps[map], buf, c0, rg0);
       bulk_commit();
     }
-  };
-  auto put = [&](int map, const float (&o)[32], int c0, int rg0) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-    put_raw(map, w, c0, rg0);
   };
 
   int it = 0;
@@ -381,6 +485,36 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     const LinProblem& P = g.prob[U.prob];
     const int acc = it & 1;
     const uint32_t aph = uint32_t(it >> 1) & 1u;
+    // This warp's chunk k (k = 0..3) sits at accumulator columns 32 col_of(k)..; it
+    // holds output rows row_of(k).. (one per lane) and columns c_of(k)...
+    auto col_of = [&](int k) {
+      if (SWAP) return 2 * k + h;
+      return EPI == kLinGlu ? (k >> 1) * 4 + h * 2 + (k & 1) : h * 4 + k;
+    };
+    auto row_of = [&](int k) {
+      return SWAP ? U.tj * g.nt + col_of(k) * 32 : U.ti * kTile + int(rank) * kHalf + q * 32;
+    };
+    auto c_of = [&](int k) {
+      if (SWAP)
+        return EPI == kLinGlu ? U.ti * kHalf + int(rank) * 64 + (q & 1) * 32
+                              : U.ti * kTile + int(rank) * kHalf + q * 32;
+      return EPI == kLinGlu ? U.tj * kHalf + h * 64 + (k & 1) * 32 : U.tj * kTile + (h * 4 + k) * 32;
+    };
+    constexpr int kChunks = EPI == kLinGlu && !SWAP ? 2 : 4;  // chunks to write (if inside)
+    auto inside = [&](int k) {
+      return col_of(k) < chunks && row_of(k) < P.rows && c_of(k) < P.cols;
+    };
+
+    Kept kept_g, kept_u;  // kLinGluGrad: the first chunk's, while the accumulator fills
+    auto fetch = [&](int k) {
+      const int r = row_of(k) + lane;
+      if (EPI == kLinGluGrad && k < kChunks && inside(k) && r < P.rows) {
+        fetch_kept(g, g.gate, g.gate_scale, r, c_of(k), P.cols - c_of(k), kept_g);
+        fetch_kept(g, g.up, g.up_scale, r, c_of(k), P.cols - c_of(k), kept_u);
+      }
+    };
+    if (EPI == kLinGluGrad && U.q < 0) fetch(0);
+
     int w = 1;
     if (lane == 0) w = mbar_wait_cluster(&tfull[acc], aph, abort_flag) ? 1 : 0;
     w = __shfl_sync(0xffffffffu, w, 0);
@@ -390,68 +524,58 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     }
     tc_fence_after();
     const uint32_t t_acc = tmem_base + uint32_t(acc * kAccCols) + (uint32_t(q * 32) << 16);
-    // this warp's four accumulator chunks: first tile column of chunk k
-    auto chunk_col = [&](int k) {
-      return EPI == kLinGlu ? (k >> 1) * kHalf + h * 64 + (k & 1) * 32 : h * 128 + k * 32;
-    };
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty + uint32_t(acc) * 8u);
     };
-    const float* parts = nullptr;  // this warp's first part, when the sum comes from the workspace
-    if (U.q >= 0) {
-      const size_t mine = (size_t(rank) * kEpiWarps + ew) * 4096;
-      float* dst = g.partial + size_t(U.q * g.split + U.part) * kPartFloats + mine;
+    if (U.q >= 0) {  // a part: the raw accumulator, for the joining launch
+      float* dst = g.partial + size_t(U.q * g.split + U.part) * (size_t(chunks) * 32 * kTile) + lane;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
+        if (col_of(k) >= chunks) break;
         float v[32];
-        tmem_ld32(t_acc + uint32_t(chunk_col(k)), v);
+        __syncwarp();
+        tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v);
         tmem_ld_wait();
+        float* p = dst + ((size_t(rank) * chunks + col_of(k)) * 4 + q) * 1024;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) dst[(k * 32 + j) * 32 + lane] = v[j];
+        for (int j = 0; j < 32; ++j) p[j * 32] = v[j];
       }
       release();
-      __threadfence();
-      __syncwarp();
-      int* counter = g.arrived + (U.q * 2 + int(rank)) * kEpiWarps + ew;
-      int before = 0;
-      if (lane == 0) before = atomicAdd(counter, 1);
-      before = __shfl_sync(0xffffffffu, before, 0);
-      if (before != g.split - 1) continue;
-      if (lane == 0) *counter = 0;  // ready for the next launch
-      __threadfence();
-      parts = g.partial + size_t(U.q) * g.split * kPartFloats + mine;
+      continue;
     }
+    // accumulator chunk k with the TMEM's lanes: a lane holds a row of the tile
+    auto load_raw = [&](int k, float (&v)[32]) {
+      __syncwarp();
+      tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v);
+      tmem_ld_wait();
+    };
+    // and with one output row per lane
     auto load_acc = [&](int k, float (&v)[32]) {
-      if (parts == nullptr) {
+      load_raw(k, v);
+      if (SWAP) {
+        if (lane == 0) bulk_wait_read<0>();  // no store still reads the buffer
         __syncwarp();
-        tmem_ld32(t_acc + uint32_t(chunk_col(k)), v);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __ldcg(parts + (k * 32 + j) * 32 + lane);
-        for (int p = 1; p < g.split; ++p) {
-          const float* src = parts + size_t(p) * kPartFloats;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (k * 32 + j) * 32 + lane);
-        }
+        turn_write(turn, lane, v);
+        __syncwarp();
+        turn_read(turn, lane, v);
+        __syncwarp();
       }
     };
-    const int rg0 = U.ti * kTile + r_loc;
-    const int r = rg0 + lane;
 
-    if constexpr (EPI == kLinStore) {
+    bool dead = false;
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int c0 = U.tj * kTile + chunk_col(k);
-        if (c0 >= P.n) break;
+    for (int k = 0; k < kChunks; ++k) {
+      if (!inside(k)) break;
+      const int c0 = c_of(k), rg0 = row_of(k), r = rg0 + lane, n = P.cols - c0;
+      if constexpr (EPI == kLinStore) {
         float v[32];
         load_acc(k, v);
-        if (g.sum != nullptr) {
-          float* sp = g.sum + (long long)r * P.n + c0;
-          const bool vec = (P.n & 3) == 0 && c0 + 32 <= P.n;
-          if (g.sum_read && r < P.m) {
+        if (!SWAP && g.sum != nullptr) {
+          float* sp = g.sum + (long long)r * P.cols + c0;
+          const bool vec = (P.cols & 3) == 0 && n >= 32;
+          if (g.sum_read && r < P.rows) {
             if (vec) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
@@ -461,11 +585,11 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (c0 + j < P.n) v[j] += sp[j];
+                if (j < n) v[j] += sp[j];
             }
           }
           if (g.sum_write) {
-            if (r < P.m) {
+            if (r < P.rows) {
               if (vec) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
@@ -474,7 +598,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
               } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (c0 + j < P.n) sp[j] = v[j];
+                  if (j < n) sp[j] = v[j];
               }
             }
             continue;
@@ -486,89 +610,128 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
           for (int j = 0; j < 32; ++j) v[j] *= f;
         }
         if (P.c_map >= 0) put(P.c_map, v, c0, rg0);
-        else if (r < P.m) store_row32(P.c + (long long)r * P.c_ld + c0, P.n - c0, false, v);
-      }
-    } else if constexpr (EPI == kLinGlu) {
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int c0 = U.tj * kHalf + chunk_col(k);
-        if (c0 >= P.n) break;
+        else if (r < P.rows) store_row32(P.c + (long long)r * P.c_ld + c0, n, false, v);
+      } else if constexpr (EPI == kLinGlu) {
         float a[32], b[32];
-        load_acc(k, a);
-        load_acc(k + 2, b);
+        if (SWAP) {
+          // gate's rows are the TMEM lanes of quarters 0 and 1, up's those of 2 and 3
+          if (q >= 2) {
+            load_raw(k, a);
+            turn_write(turn, lane, a);
+            arrive_warp(ho.ready);
+            dead = !wait_warp(ho.taken, ho.parity);
+            ho.parity ^= 1u;
+            if (dead) break;
+            continue;
+          }
+          load_acc(k, a);
+          dead = !wait_warp(ho.ready, ho.parity);
+          ho.parity ^= 1u;
+          if (dead) break;
+          turn_read(reinterpret_cast<const float*>(epi + (h * 4 + q) * 2 * kEpiBufBytes), lane, b);
+          arrive_warp(ho.taken);
+        } else {
+          load_acc(k, a);
+          load_acc(k + 2, b);
+        }
         if (g.keep == kKeepBf16) {
           if (g.kept_vec) {
             put(g.map_gate, a, c0, rg0);
             put(g.map_up, b, c0, rg0);
-          } else if (r < P.m) {
+          } else if (r < P.rows) {
             const long long at = (long long)r * g.ffn + c0;
-            store_row32(static_cast<__nv_bfloat16*>(g.gate) + at, P.n - c0, false, a);
-            store_row32(static_cast<__nv_bfloat16*>(g.up) + at, P.n - c0, false, b);
+            store_row32(static_cast<__nv_bfloat16*>(g.gate) + at, n, false, a);
+            store_row32(static_cast<__nv_bfloat16*>(g.up) + at, n, false, b);
           }
-        } else if (g.keep == kKeepAct8 && r < P.m) {
+        } else if (g.keep == kKeepAct8 && r < P.rows) {
           const long long at = (long long)r * g.ffn + c0;
           const long long sa =
               (long long)r * ((g.ffn + kActBlock - 1) / kActBlock) + c0 / kActBlock;
-          store_act8(static_cast<signed char*>(g.gate) + at, g.gate_scale + sa, P.n - c0,
+          store_act8(static_cast<signed char*>(g.gate) + at, g.gate_scale + sa, n,
                      g.kept_vec != 0, a);
-          store_act8(static_cast<signed char*>(g.up) + at, g.up_scale + sa, P.n - c0,
-                     g.kept_vec != 0, b);
+          store_act8(static_cast<signed char*>(g.up) + at, g.up_scale + sa, n, g.kept_vec != 0, b);
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) a[j] = act_value(g.act, a[j]) * b[j];
+        // one loop per activation: the three side by side in one loop overflow the
+        // instruction cache
+        if (g.act == DMUON_ACT_SILU) glu32<DMUON_ACT_SILU>(a, b);
+        else if (g.act == DMUON_ACT_GELU) glu32<DMUON_ACT_GELU>(a, b);
+        else glu32<DMUON_ACT_GELU_TANH>(a, b);
         put(P.c_map, a, c0, rg0);
-      }
-    } else if constexpr (EPI == kLinGluGrad) {
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int c0 = U.tj * kTile + chunk_col(k);
-        if (c0 >= P.n) break;
+      } else {  // kLinGluGrad
         float v[32], ga[32], up[32];
-        if (r < P.m) {
-          load_kept(g, g.gate, g.gate_scale, r, c0, P.n - c0, ga);
-          load_kept(g, g.up, g.up_scale, r, c0, P.n - c0, up);
+        if (r < P.rows) {
+          kept_values(g, kept_g, ga);
+          kept_values(g, kept_u, up);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) ga[j] = up[j] = 0.f;
         }
+        fetch(k + 1);
         load_acc(k, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float a, da;
-          act_both(g.act, ga[j], a, da);
-          const float dh = v[j];
-          ga[j] = dh * up[j] * da;  // dgate
-          up[j] *= a;               // h
-          v[j] = dh * a;            // dup
-        }
+        if (g.act == DMUON_ACT_SILU) glu_grad32<DMUON_ACT_SILU>(v, ga, up);
+        else if (g.act == DMUON_ACT_GELU) glu_grad32<DMUON_ACT_GELU>(v, ga, up);
+        else glu_grad32<DMUON_ACT_GELU_TANH>(v, ga, up);
         put(P.c_map, ga, c0, rg0);
         put(g.map_dup, v, c0, rg0);
         put(g.map_h, up, c0, rg0);
       }
     }
-    if (parts == nullptr) release();
+    if (dead) break;
+    release();
   }
   // stores complete, and stop reading shared memory, before the CTA exits
   if (lane == 0) bulk_wait_all();
   __syncwarp();
 }
 
-// Logits of 32 tokens x 128 vocabulary entries per warp, in registers.
+DM_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Logits of the cross entropy, accumulated in registers over runs of K.  A group of
+// vocabulary entries (128 plainly: the columns of a lane; 32 swapped: the lanes of
+// a warp) shares its maximum m: exp(z - m) = 2^((z - m) log2 e), exactly 1 at the
+// maximum, so that a certain token's loss and gradient come out exact.
+template <bool SWAP>
 DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
-                          uint32_t epi_smem, uint32_t tmem_base, volatile int* abort_flag) {
+                          uint8_t* epi, uint32_t tmem_base, volatile int* abort_flag) {
+  constexpr float kLog2e = 1.44269504f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3, h = (warp - 2) >> 2, ew = warp - 2;
-  const uint32_t buf0 = epi_smem + uint32_t(ew * 2 * kEpiBufBytes);
+  float* turn = reinterpret_cast<float*>(epi + ew * 2 * kEpiBufBytes);
+  const uint32_t buf0 = smem_u32(turn);
   const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
   const int clusters = int(cluster_count_x());
+  const int chunks = SWAP ? g.nt / 32 : kAccCols / 32;
   const LinProblem& P = g.prob[0];
   int it = 0;
   bool ok = true;
+
+  // 32 exponentials of one token, entries c0 .., to the workspace in fp16
+  auto put = [&](int which, const float* e, int c0, int rg0) {
+    const uint32_t buf = buf0 + uint32_t(which * kEpiBufBytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 p = __floats2half2_rn(e[8 * i + 2 * j], e[8 * i + 2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      st_shared_v4(buf + epi_off(lane, i), o[0], o[1], o[2], o[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&g.maps[P.c_map], buf, c0, rg0);
+      bulk_commit();
+    }
+  };
+
   for (int u = int(cluster_id_x()); ok && u < g.total_units; u += clusters) {
     const Unit U = decode_unit(g, u);
-    const int rg0 = U.ti * kTile + int(rank) * kHalf + q * 32;
-    const int r = rg0 + lane;
-    const int g0 = U.tj * kTile + h * kXentGroup;  // first vocabulary entry of the group
     float z[kXentGroup];
 #pragma unroll
     for (int j = 0; j < kXentGroup; ++j) z[j] = 0.f;
@@ -584,86 +747,129 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
         break;
       }
       tc_fence_after();
-      const uint32_t t = tmem_base + uint32_t(acc * kAccCols + h * kXentGroup) +
-                         (uint32_t(q * 32) << 16);
+      const uint32_t t = tmem_base + uint32_t(acc * kAccCols) + (uint32_t(q * 32) << 16);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float v[16];
-        tmem_ld16(t + uint32_t(k * 16), v);
-        tmem_ld_wait();
+        const int col = SWAP ? (2 * (k >> 1) + h) * 32 + (k & 1) * 16 : h * kXentGroup + k * 16;
+        if (!SWAP || 2 * (k >> 1) + h < chunks) {
+          float v[16];
+          tmem_ld16(t + uint32_t(col), v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[k * 16 + j] += v[j];
+          for (int j = 0; j < 16; ++j) z[k * 16 + j] += v[j];
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty + uint32_t(acc) * 8u);
     }
-    if (!ok || g0 >= P.n) continue;
-    const int n = P.n - g0;  // entries of the group that exist, if below 128
-    float m = -INFINITY;
+    if (!ok) break;
+    if constexpr (!SWAP) {
+      const int rg0 = U.ti * kTile + int(rank) * kHalf + q * 32, r = rg0 + lane;
+      const int g0 = U.tj * kTile + h * kXentGroup;  // first vocabulary entry of the group
+      if (g0 >= P.cols || rg0 >= P.rows) continue;
+      const long long t = r < P.rows ? g.target[r] : -1;
+      const int d = t >= g0 && t < g0 + kXentGroup && t < P.cols ? int(t - g0) : -1;
+      if (__any_sync(0xffffffffu, d >= 0)) {
 #pragma unroll
-    for (int j = 0; j < kXentGroup; ++j)
-      if (j < n) m = fmaxf(m, z[j]);
-    const long long t = r < P.m ? g.target[r] : -1;
-    const int d = t >= g0 && t < g0 + kXentGroup && t < P.n ? int(t - g0) : -1;
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-      for (int j = k * 32; j < k * 32 + 32; ++j) {
-        if (j == d) g.target_logit[r] = z[j];
-        z[j] = j < n ? exp2f((z[j] - m) * 1.44269504f) : 0.f;
-        s += z[j];
+        for (int j = 0; j < kXentGroup; ++j)
+          if (j == d) g.target_logit[r] = z[j];
       }
-      if (P.c_map >= 0 && k * 32 < n) {
-        const uint32_t buf = buf0 + uint32_t((k & 1) * kEpiBufBytes);
-        if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
-        __syncwarp();
+      const int n = P.cols - g0;
+      if (n < kXentGroup) {  // entries past the vocabulary weigh nothing
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[4];
+        for (int j = 0; j < kXentGroup; ++j)
+          if (j >= n) z[j] = -INFINITY;
+      }
+      float m = z[0];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 p = __floats2half2_rn(z[k * 32 + 8 * i + 2 * j], z[k * 32 + 8 * i + 2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&p);
-          }
-          st_shared_v4(buf + epi_off(lane, i), o[0], o[1], o[2], o[3]);
+      for (int j = 1; j < kXentGroup; ++j) m = fmaxf(m, z[j]);
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int j = k * 32; j < k * 32 + 32; ++j) {
+          z[j] = ex2((z[j] - m) * kLog2e);
+          s += z[j];
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&g.maps[P.c_map], buf, g0 + k * 32, rg0);
-          bulk_commit();
+        if (P.c_map >= 0 && k * 32 < n) {
+          if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
+          __syncwarp();
+          put(k & 1, z + k * 32, g0 + k * 32, rg0);
+        }
+      }
+      if (r < P.rows)
+        g.group_stat[(long long)(g0 / kXentGroup) * g.stat_ld + r] = make_float2(m, s);
+    } else {
+      const int c0 = U.ti * kTile + int(rank) * kHalf + q * 32;
+      if (c0 >= P.cols) continue;
+      const int n = P.cols - c0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rg0 = U.tj * g.nt + (2 * k + h) * 32, r = rg0 + lane;
+        if (2 * k + h < chunks && rg0 < P.rows) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = z[k * 32 + j];
+          if (P.c_map >= 0 && lane == 0) bulk_wait_read<0>();  // no store still reads the buffer
+          __syncwarp();
+          turn_write(turn, lane, v);
+          __syncwarp();
+          turn_read(turn, lane, v);
+          __syncwarp();
+          const long long t = r < P.rows ? g.target[r] : -1;
+          const int d = t >= c0 && t < c0 + 32 && t < P.cols ? int(t - c0) : -1;
+          if (__any_sync(0xffffffffu, d >= 0)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == d) g.target_logit[r] = v[j];
+          }
+          if (n < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j >= n) v[j] = -INFINITY;
+          }
+          float m = v[0];
+#pragma unroll
+          for (int j = 1; j < 32; ++j) m = fmaxf(m, v[j]);
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            v[j] = ex2((v[j] - m) * kLog2e);
+            s += v[j];
+          }
+          if (P.c_map >= 0) put(0, v, c0, rg0);
+          if (r < P.rows) g.group_stat[(long long)(c0 / 32) * g.stat_ld + r] = make_float2(m, s);
         }
       }
     }
-    if (r < P.m) g.group_stat[(long long)(g0 / kXentGroup) * g.stat_ld + r] = make_float2(m, s);
   }
   // stores complete, and stop reading shared memory, before the CTA exits
   if (lane == 0) bulk_wait_all();
   __syncwarp();
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool SWAP>
 __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_constant__ LinArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kOpBytes;
-  uint8_t* sE = sB + kStages * kOpBytes;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sE + kEpiBytes);
-  uint64_t* empty_bar = full_bar + kStages;
-  uint64_t* tfull = empty_bar + kStages;
+  uint8_t* sEpi = smem + kStageArea;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sEpi + kEpiBytes);
+  uint64_t* empty_bar = full_bar + kMaxStages;
+  uint64_t* tfull = empty_bar + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain_bar = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint64_t* pair_bar = drain_bar + 1;  // ready and taken of four warp pairs
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_bar + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  grid_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int b = 0; b < 8; ++b) mbar_init(&pair_bar[b], 1);  // one lane of a warp
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full_bar[s], 1);    // leader: its expect_tx; both CTAs' copies add bytes
       mbar_init(&empty_bar[s], 1);   // the leader's commit
     }
@@ -683,18 +889,19 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_wait();  // what follows reads what earlier launches wrote
 
   if (threadIdx.x == 0) {
-    producer<EPI, A_MN, B_MN>(g, rank, sA, sB, full_bar, empty_bar, abort_flag);
+    producer<EPI, A_MN, B_MN, SWAP>(g, rank, smem, full_bar, empty_bar, abort_flag);
   } else if (threadIdx.x == 32) {
     if (rank == 0)
-      mma_issuer<EPI, A_MN, B_MN>(g, sA, sB, full_bar, empty_bar, tfull, tempty, drain_bar,
-                                  tmem_base, abort_flag);
+      mma_issuer<EPI, A_MN, B_MN, SWAP>(g, smem, full_bar, empty_bar, tfull, tempty, drain_bar,
+                                        tmem_base, abort_flag);
   } else if (warp >= 2) {
     if constexpr (EPI == kLinXent)
-      epilogue_xent(g, rank, tfull, tempty, smem_u32(sE), tmem_base, abort_flag);
+      epilogue_xent<SWAP>(g, rank, tfull, tempty, sEpi, tmem_base, abort_flag);
     else
-      epilogue<EPI>(g, rank, tfull, tempty, smem_u32(sE), tmem_base, abort_flag);
+      epilogue<EPI, SWAP>(g, rank, tfull, tempty, sEpi, pair_bar, tmem_base, abort_flag);
   }
 
   __syncthreads();
@@ -711,36 +918,254 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   }
 }
 
+// ------------------------------------------------------------------ joining split tiles
+// A block of 128 threads takes one 32 x 32 chunk of a split tile (kLinGlu: gate's
+// and up's), adds the parts in order, turns it if need be, and runs the epilogue
+// with eight consecutive columns of a row per thread.  Bound by reading the parts
+// (from L2, mostly): eight columns x four parts are in flight per thread.
+DM_DEV void sum_parts(const float* p, size_t stride, int split, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  for (int s = 0; s < split; s += 4) {
+    float t[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[k][j] = s + k < split ? __ldcg(p + (s + k) * stride + j * 32) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += t[k][j];
+  }
+}
+DM_DEV void store_row8(__nv_bfloat16* dst, int n, bool vec, const float (&v)[8]) {
+  if (vec && n >= 8) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+// Eight values of a 32-value block (its four threads are neighbours in a warp; all
+// lanes of the warp take part).
+DM_DEV void store_act8_part(signed char* codes, __nv_bfloat16* scale, int n, bool vec, bool write,
+                            bool first, const float (&v)[8]) {
+  float top = 0.f, bad = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = j < n ? v[j] : 0.f;
+    top = fmaxf(top, fabsf(x));
+    bad = fmaf(x, 0.f, bad);
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    bad += __shfl_xor_sync(0xffffffffu, bad, o);
+  }
+  if (!write || n <= 0) return;
+  const float s = act8_scale(top, bad == 0.f);
+  const float r = bad == 0.f && s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j >> 2] |= (act8_code_fast(bad == 0.f ? v[j] : 0.f, r) & 0xFFu) << (8 * (j & 3));
+  if (vec && n >= 8) {
+    *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) codes[j] = (signed char)(w[j >> 2] >> (8 * (j & 3)));
+  }
+  if (first) *scale = __float2bfloat16_rn(s);
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ LinArgs g) {
+  __shared__ float t0[32][33], t1[EPI == kLinGlu ? 32 : 1][33];
+  grid_launch_dependents();
+  grid_wait();
+  const int chunks = g.swap ? g.nt / 32 : kAccCols / 32;
+  // chunk of the tile: CTA of the pair, column chunk, TMEM lane quarter
+  const int cols = EPI == kLinGlu && !g.swap ? chunks / 2 : chunks;
+  const int quarters = EPI == kLinGlu && g.swap ? 2 : 4;
+  int b = int(blockIdx.x);
+  const int q = b % quarters;
+  b /= quarters;
+  const int rank = b & 1;
+  b >>= 1;
+  const int col = b % cols;
+  b /= cols;  // split tile
+  const Unit U = decode_unit(g, g.full_tiles + b * g.split);
+  const LinProblem& P = g.prob[U.prob];
+  int row0, c0;
+  if (g.swap) {
+    row0 = U.tj * g.nt + col * 32;
+    c0 = EPI == kLinGlu ? U.ti * kHalf + rank * 64 + q * 32 : U.ti * kTile + rank * kHalf + q * 32;
+  } else {
+    row0 = U.ti * kTile + rank * kHalf + q * 32;
+    c0 = (EPI == kLinGlu ? U.tj * kHalf : U.tj * kTile) + col * 32;
+  }
+  if (row0 >= P.rows || c0 >= P.cols) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t stride = size_t(chunks) * 32 * kTile;
+  const float* base = g.partial + size_t(b) * g.split * stride + warp * 256 + lane;
+  auto chunk_at = [&](int cc, int qq) { return ((size_t(rank) * chunks + cc) * 4 + qq) * 1024; };
+  float v[8], u[8];
+  sum_parts(base + chunk_at(col, q), stride, g.split, v);
+  if (EPI == kLinGlu)
+    sum_parts(base + (g.swap ? chunk_at(col, q + 2) : chunk_at(col + cols, q)), stride, g.split, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // v[j]: TMEM lane `lane`, column 8 warp + j
+    const int i = g.swap ? warp * 8 + j : lane, k = g.swap ? lane : warp * 8 + j;
+    t0[i][k] = v[j];
+    if (EPI == kLinGlu) t1[i][k] = u[j];
+  }
+  __syncthreads();
+  const int tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 8;
+  const int r = row0 + tr, c = c0 + tc, n = P.cols - c;
+  const bool in = r < P.rows;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = t0[tr][tc + j];
+    if (EPI == kLinGlu) u[j] = t1[tr][tc + j];
+  }
+  const bool vec = P.c_map >= 0;
+  if (EPI == kLinStore) {
+    if (!in || n <= 0) return;
+    if (g.sum != nullptr) {
+      float* sp = g.sum + (long long)r * P.cols + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) {
+          if (g.sum_read) v[j] += sp[j];
+          if (g.sum_write) sp[j] = v[j];
+        }
+      if (g.sum_write) return;
+    }
+    if (g.scale != nullptr) {
+      const float f = *g.scale;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+    }
+    store_row8(P.c + (long long)r * P.c_ld + c, n, vec, v);
+  } else if (EPI == kLinGlu) {
+    const long long at = (long long)r * g.ffn + c;
+    if (g.keep == kKeepBf16 && in) {
+      store_row8(static_cast<__nv_bfloat16*>(g.gate) + at, n, g.kept_vec != 0, v);
+      store_row8(static_cast<__nv_bfloat16*>(g.up) + at, n, g.kept_vec != 0, u);
+    } else if (g.keep == kKeepAct8) {
+      const long long sa = (long long)r * ((g.ffn + kActBlock - 1) / kActBlock) + c0 / kActBlock;
+      store_act8_part(static_cast<signed char*>(g.gate) + at, g.gate_scale + sa, n,
+                      g.kept_vec != 0, in, tc == 0, v);
+      store_act8_part(static_cast<signed char*>(g.up) + at, g.up_scale + sa, n, g.kept_vec != 0,
+                      in, tc == 0, u);
+    }
+    if (!in || n <= 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = g.act == DMUON_ACT_SILU   ? act_value<DMUON_ACT_SILU>(v[j])
+                      : g.act == DMUON_ACT_GELU ? act_value<DMUON_ACT_GELU>(v[j])
+                                                : act_value<DMUON_ACT_GELU_TANH>(v[j]);
+      v[j] = a * u[j];
+    }
+    store_row8(P.c + (long long)r * P.c_ld + c, n, true, v);
+  } else {  // kLinGluGrad
+    if (!in || n <= 0) return;
+    const long long at = (long long)r * g.ffn + c;
+    float ga[8], up[8];
+    if (g.keep == kKeepBf16) {
+      const __nv_bfloat16* pg = static_cast<const __nv_bfloat16*>(g.gate) + at;
+      const __nv_bfloat16* pu = static_cast<const __nv_bfloat16*>(g.up) + at;
+      if (g.kept_vec && n >= 8) {
+        unpack8(*reinterpret_cast<const uint4*>(pg), ga);
+        unpack8(*reinterpret_cast<const uint4*>(pu), up);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ga[j] = j < n ? __bfloat162float(pg[j]) : 0.f;
+          up[j] = j < n ? __bfloat162float(pu[j]) : 0.f;
+        }
+      }
+    } else {
+      const long long sa = (long long)r * ((g.ffn + kActBlock - 1) / kActBlock) + c / kActBlock;
+      const float sg = __bfloat162float(g.gate_scale[sa]), su = __bfloat162float(g.up_scale[sa]);
+      const signed char* pg = static_cast<const signed char*>(g.gate) + at;
+      const signed char* pu = static_cast<const signed char*>(g.up) + at;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ga[j] = j < n ? sg * float(pg[j]) : 0.f;
+        up[j] = j < n ? su * float(pu[j]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float a, da;
+      if (g.act == DMUON_ACT_SILU) act_both<DMUON_ACT_SILU>(ga[j], a, da);
+      else if (g.act == DMUON_ACT_GELU) act_both<DMUON_ACT_GELU>(ga[j], a, da);
+      else act_both<DMUON_ACT_GELU_TANH>(ga[j], a, da);
+      const float dh = v[j];
+      ga[j] = dh * up[j] * da;
+      up[j] *= a;
+      v[j] = dh * a;
+    }
+    const long long to = (long long)r * P.c_ld + c;
+    store_row8(P.c + to, n, true, ga);
+    store_row8(g.dup + to, n, true, v);
+    store_row8(g.h + to, n, true, up);
+  }
+}
+
 using Kernel = void (*)(LinArgs);
-Kernel kernel_for(int epi, bool a_mn, bool b_mn) {
+Kernel kernel_for(int epi, bool a_mn, bool b_mn, bool swap) {
+  if (swap) {
+    if (b_mn) return nullptr;
+    switch (epi) {
+      case kLinGlu: return a_mn ? nullptr : pair_gemm_kernel<kLinGlu, false, false, true>;
+      case kLinGluGrad: return a_mn ? pair_gemm_kernel<kLinGluGrad, true, false, true> : nullptr;
+      case kLinXent: return a_mn ? nullptr : pair_gemm_kernel<kLinXent, false, false, true>;
+      case kLinStore:
+        return a_mn ? pair_gemm_kernel<kLinStore, true, false, true>
+                    : pair_gemm_kernel<kLinStore, false, false, true>;
+      default: return nullptr;
+    }
+  }
   switch (epi) {
-    case kLinGlu: return !a_mn && !b_mn ? pair_gemm_kernel<kLinGlu, false, false> : nullptr;
-    case kLinGluGrad: return !a_mn && b_mn ? pair_gemm_kernel<kLinGluGrad, false, true> : nullptr;
-    case kLinXent: return !a_mn && !b_mn ? pair_gemm_kernel<kLinXent, false, false> : nullptr;
+    case kLinGlu: return !a_mn && !b_mn ? pair_gemm_kernel<kLinGlu, false, false, false> : nullptr;
+    case kLinGluGrad:
+      return !a_mn && b_mn ? pair_gemm_kernel<kLinGluGrad, false, true, false> : nullptr;
+    case kLinXent:
+      return !a_mn && !b_mn ? pair_gemm_kernel<kLinXent, false, false, false> : nullptr;
     case kLinStore:
-      if (!a_mn) return b_mn ? pair_gemm_kernel<kLinStore, false, true>
-                             : pair_gemm_kernel<kLinStore, false, false>;
-      return b_mn ? pair_gemm_kernel<kLinStore, true, true> : nullptr;
+      if (!a_mn) return b_mn ? pair_gemm_kernel<kLinStore, false, true, false>
+                             : pair_gemm_kernel<kLinStore, false, false, false>;
+      return b_mn ? pair_gemm_kernel<kLinStore, true, true, false> : nullptr;
     default: return nullptr;
   }
 }
 
 }  // namespace
 
-size_t lin_partial_bytes() { return kMaxParts * kPartFloats * sizeof(float); }
-size_t lin_arrived_bytes() { return kMaxParts * 2 * kEpiWarps * sizeof(int); }
+size_t lin_partial_bytes() { return kPartialBytes; }
 
 cudaError_t lin_prepare() {
-  const struct { int epi; bool a, b; } all[] = {
-      {kLinGlu, false, false},   {kLinGluGrad, false, true}, {kLinXent, false, false},
-      {kLinStore, false, false}, {kLinStore, false, true},   {kLinStore, true, true}};
-  for (const auto& k : all) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel_for(k.epi, k.a, k.b),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(kSmemBytes));
-    if (e != cudaSuccess) return e;
-  }
+  for (int epi = kLinStore; epi <= kLinXent; ++epi)
+    for (int v = 0; v < 8; ++v) {
+      const Kernel k = kernel_for(epi, (v & 1) != 0, (v & 2) != 0, (v & 4) != 0);
+      if (k == nullptr) continue;
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 int(kSmemBytes));
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
+}
+
+bool lin_swaps(long long tokens, int* nt) {
+  const long long plain = (tokens + kTile - 1) / kTile;  // tiles of 256 tokens, either way
+  const long long fit = ((tokens + plain - 1) / plain + 31) / 32 * 32;
+  *nt = int(fit);
+  return plain * fit * 10 < plain * kTile * 9;
 }
 
 void lin_schedule(LinArgs& g, bool may_split, int clusters) {
@@ -751,17 +1176,26 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
     const int k = g.prob[p].kb0 + g.prob[p].kb1;
     kb = p == 0 || k < kb ? k : kb;
   }
+  g.stages = kStages;
+  if (g.swap) {
+    g.stages = kStageArea / (kOpBytes + g.nt / 2 * kK * 2);
+    if (g.stages > kMaxStages) g.stages = kMaxStages;
+  }
   g.full_tiles = g.total_units = tiles;
   g.split = 1;
   const int rest = tiles % clusters;
   if (!may_split || rest == 0) return;
-  // Time of the last wave in K blocks (about 0.55 us each): a part costs its
-  // blocks plus about 4 for filling the pipeline and writing its accumulator,
-  // and the warp that joins S parts reads them at about 2 blocks each.
-  long long best = kb;
-  for (int s = 2; s * rest <= kMaxParts && 2 * s <= kb; ++s) {
-    const long long waves = ((long long)rest * s + clusters - 1) / clusters;
-    const long long cost = waves * ((kb + s - 1) / s + 4) + 2 * s;
+  // Microseconds of the last wave.  A K block of a 256-wide tile takes a pair 0.55;
+  // of a narrow swapped one 0.75, its share of the memory's rate.  A part costs about
+  // 0.3 more (the pipeline stays filled from one to the next); joining costs a launch
+  // (4) and the parts' way to L2 and back (5 TB/s).
+  const int cols = g.swap ? g.nt : kTile;
+  const double t_kb = g.swap ? std::max(0.75, 0.55 * cols / 256) : 0.55;
+  const double part = double(cols) * kTile * sizeof(float);
+  double best = kb * t_kb + 0.3;
+  for (int s = 2; rest * s * part <= double(kPartialBytes) && 2 * s <= kb; ++s) {
+    const int waves = (rest * s + clusters - 1) / clusters;
+    const double cost = waves * ((kb + s - 1) / s * t_kb + 0.3) + 4 + 2 * rest * s * part / 5e6;
     if (cost < best) {
       best = cost;
       g.split = s;
@@ -776,7 +1210,7 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
                        cudaStream_t s) {
   if (g.total_units <= 0) return cudaSuccess;
-  const Kernel k = kernel_for(epi, a_mn, b_mn);
+  const Kernel k = kernel_for(epi, a_mn, b_mn, g.swap != 0);
   if (k == nullptr) return cudaErrorInvalidValue;
   const int clusters = g.total_units < max_clusters ? g.total_units : max_clusters;
   cudaLaunchConfig_t cfg{};
@@ -784,14 +1218,24 @@ cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return counted(cudaLaunchKernelEx(&cfg, k, g));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = counted(cudaLaunchKernelEx(&cfg, k, g));
+  if (e != cudaSuccess || g.split == 1) return e;
+  const int chunks = (g.swap ? g.nt : kAccCols) / 32;
+  const int tiles = (g.total_units - g.full_tiles) / g.split;
+  const int blocks = tiles * 2 * chunks * (epi == kLinGlu ? 2 : 4);
+  return launch_dependent(epi == kLinStore ? join_kernel<kLinStore>
+                          : epi == kLinGlu ? join_kernel<kLinGlu>
+                                           : join_kernel<kLinGluGrad>,
+                          unsigned(blocks), 128u, s, g);
 }
 
 }  // namespace dm

@@ -165,6 +165,13 @@ DM_DEV void prefetch_tensormap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
+// ------------------------------------------------------------------ dependent launches
+// A launch made dependent on the one before it in its stream may start while that
+// one still runs; it must wait before it touches memory.
+DM_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Let the next launch start its blocks where there is room for them.
+DM_DEV void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ------------------------------------------------------------------ tcgen05
 DM_DEV void tmem_alloc(uint32_t* slot_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "launch.h"
+
 namespace dm {
 
 // ------------------------------------------------------------------ shared with dmuon_api.cu
@@ -23,8 +25,9 @@ TensorMapEncode library_tensor_map_encoder();
 // ------------------------------------------------------------------ tensor-core products
 // Elements of one 8-bit activation block (they share a bf16 scale).
 constexpr int kActBlock = 32;
-// Columns of the vocabulary whose exponentials share a reference maximum.
-constexpr int kXentGroup = 128;
+// Vocabulary entries whose exponentials share a reference maximum (plain and
+// swapped orientation).
+constexpr int kXentGroup = 128, kXentGroupSwap = 32;
 
 // What a product's epilogue does with the fp32 accumulator.
 enum LinEpi {
@@ -39,11 +42,11 @@ constexpr int kLinMaps = 12;     // tensor maps of one launch
 constexpr int kLinProblems = 3;  // products of one launch
 
 struct LinProblem {
-  int m, n;              // output rows / columns (kLinGlu: n = ffn, 128 of it per tile)
-  int tiles_m, tiles_n;
+  int rows, cols;        // output extent (rows: tokens, except for weight gradients)
+  int tiles_m, tiles_n;  // tile grid of the product (swapped: m counts columns, n rows)
   int kb0, kb1;          // K blocks from the first and the second operand pair
   int tile_begin;        // first tile of this product in the launch
-  int a0, b0, a1, b1;    // operand maps (kLinGlu: b0 = gate's weight, b1 = up's)
+  int a0, b0, a1, b1;    // operand maps (kLinGlu: gate's weight b0, up's b1; swapped a0, a1)
   int c_map;             // output map, or -1: c is written with plain stores
   __nv_bfloat16* c;
   long long c_ld;
@@ -53,13 +56,13 @@ struct LinArgs {
   CUtensorMap maps[kLinMaps];
   LinProblem prob[kLinProblems];
   int n_prob;
+  int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;
   int total_units;       // full_tiles + split * (tiles - full_tiles)
   float* partial;        // fp32 parts of the split tiles
-  int* arrived;          // arrivals per split tile and epilogue warp, zero between launches
   int* err;
-  // kLinStore: fp32 running sum over launches (row pitch = n of the product)
+  // kLinStore: fp32 running sum over launches (row pitch = cols of the product)
   float* sum;
   int sum_read, sum_write;  // add what `sum` holds; write the sum there instead of C
   const float* scale;    // C = scale * acc (device scalar), or null
@@ -71,21 +74,40 @@ struct LinArgs {
   __nv_bfloat16 *gate_scale, *up_scale;     // 8-bit block scales
   int map_gate, map_up;                     // kLinGlu, bf16: output maps (kept_vec)
   int map_dup, map_h;                       // kLinGluGrad: output maps beside c_map (dgate)
+  __nv_bfloat16 *dup, *h;                   // and their tensors (pitch c_ld)
   // kLinXent
   const long long* target;
   float* target_logit;   // one per token
-  float2* group_stat;    // (maximum, sum of exponentials) [group][token], pitch stat_ld
-  long long stat_ld;
+  float2* group_stat;    // (max logit * log2 e, sum of 2^(logit * log2 e - that)) per
+  long long stat_ld;     // [group][token], pitch stat_ld
 };
 
 size_t lin_partial_bytes();
-size_t lin_arrived_bytes();
 cudaError_t lin_prepare();  // once per device
 // Split the tiles of the last, partly filled wave along K (sets full_tiles ..
 // total_units from the products' tile counts).
 void lin_schedule(LinArgs& g, bool may_split, int clusters);
+// Whether a product over `tokens` rows runs swapped, and its tokens per tile.
+bool lin_swaps(long long tokens, int* nt);
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
                        cudaStream_t s);
+
+// Launch a kernel that may start while the one before it in the stream still runs
+// (it calls grid_wait() before it touches memory).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads,
+                             cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return counted(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
+}
 
 // ------------------------------------------------------------------ memory-bound kernels
 cudaError_t launch_act8_save(long long rows, long long cols, const void* x, long long ld,
@@ -108,8 +130,9 @@ struct XentRows {
   const float* grad_loss;   // null: no gradients
   const float* grad_scale;  // G is formed of grad_loss / *grad_scale
   const float* target_logit;
-  const float2* group_stat;
+  const float2* group_stat;  // as LinArgs
   long long stat_ld;
+  int group;                // vocabulary entries per group
   float *loss, *lse;
 };
 // *scale = the largest |grad_loss| of the tokens that have a target (1 if that is 0).

@@ -20,12 +20,15 @@ constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxDim = int64_t(1) << 19,
 // bounds the group statistics.
 constexpr size_t kLogitBytes = size_t(2200) << 20;
 constexpr int64_t kLossTokens = 16384;
+// Above this many tokens a last tile of 256 wastes too little for lin_swaps().
+constexpr int64_t kSwapTokens = 1792;
 
 using bf16 = __nv_bfloat16;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Ready the current device: the products' shared memory opt-in, once.
@@ -59,13 +62,11 @@ struct Carve {
 // The part of every workspace that the products use.
 struct ProductSpace {
   int* err;
-  int* arrived;
   float* partial;
 };
 ProductSpace take_product_space(Carve& c) {
   ProductSpace s;
   s.err = c.take<int>(kHdrBytes);
-  s.arrived = c.take<int>(lin_arrived_bytes());
   s.partial = c.take<float>(lin_partial_bytes());
   return s;
 }
@@ -78,10 +79,10 @@ struct Launch {
 
   explicit Launch(const ProductSpace& s) {
     g.err = s.err;
-    g.arrived = s.arrived;
     g.partial = s.partial;
   }
-  int map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool output) {
+  int map(const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols, int box_rows,
+          CUtensorMapSwizzle swizzle) {
     const TensorMapEncode enc = library_tensor_map_encoder();
     if (enc == nullptr || n_maps >= kLinMaps) {
       ok = false;
@@ -89,45 +90,69 @@ struct Launch {
     }
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
-    const cuuint32_t box_in[2] = {64, 128}, box_out[2] = {32, 32}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)}, es[2] = {1, 1};
     ok = ok && enc(&g.maps[n_maps], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-                   dims, strides, output ? box_out : box_in, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   output ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     return n_maps++;
   }
   // An operand stored as `rows` rows of `cols` contiguous elements; whether it
-  // is K-major or MN-major, a box is 64 columns x 128 rows.
-  int operand(const bf16* p, int64_t cols, int64_t rows, int64_t ld) {
-    return map(p, cols, rows, ld, false);
+  // is K-major or MN-major, a box is 64 columns x 128 rows (fewer for the tokens of
+  // a swapped product and for the halves of a swapped kLinGlu tile).
+  int operand(const bf16* p, int64_t cols, int64_t rows, int64_t ld, int box_rows = 128) {
+    return map(p, cols, rows, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   int output(const bf16* p, int64_t cols, int64_t rows, int64_t ld) {
-    return map(p, cols, rows, ld, true);
+    return map(p, cols, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
-  LinProblem& problem(int64_t m, int64_t n, int64_t cols_per_tile, int64_t k0, int64_t k1) {
+  LinProblem& problem(int64_t rows, int64_t cols, int64_t k0, int64_t k1) {
     LinProblem& P = g.prob[g.n_prob++];
-    P.m = int(m);
-    P.n = int(n);
-    P.tiles_m = int(ceil_div(m, 256));
-    P.tiles_n = int(ceil_div(n, cols_per_tile));
+    P.rows = int(rows);
+    P.cols = int(cols);
+    P.tiles_m = int(ceil_div(rows, 256));
+    P.tiles_n = int(ceil_div(cols, 256));
     P.kb0 = int(ceil_div(k0, 128));
     P.kb1 = int(ceil_div(k1, 128));
     P.c_map = -1;
     return P;
   }
+  // A product tokens x weight, swapped where that fits the token count better.
+  LinProblem& token_problem(int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
+                            int64_t k1) {
+    LinProblem& P = problem(tokens, cols, k0, k1);
+    P.tiles_n = int(ceil_div(cols, cols_per_tile));
+    int nt = 0;
+    if (lin_swaps(tokens, &nt)) {
+      g.swap = 1;
+      g.nt = nt;
+      P.tiles_m = P.tiles_n;
+      P.tiles_n = int(ceil_div(tokens, nt));
+    }
+    return P;
+  }
+  // Operands of a token product: the tokens' rows of K, and the weight (rows of K,
+  // or for a weight read along its other axis rows of the output's columns).
+  void operands(LinProblem& P, const bf16* tok, int64_t k, int64_t tok_ld, const bf16* w,
+                int64_t w_cols, int64_t w_rows, int64_t w_ld, bool second = false) {
+    const int t = operand(tok, k, P.rows, tok_ld, g.swap ? g.nt / 2 : 128);
+    const int m = operand(w, w_cols, w_rows, w_ld);
+    (second ? P.a1 : P.a0) = g.swap ? m : t;
+    (second ? P.b1 : P.b0) = g.swap ? t : m;
+  }
   // C: TMA where its rows allow it, plain stores otherwise.
   void store_to(LinProblem& P, bf16* c, int64_t ld) {
     P.c = c;
     P.c_ld = ld;
-    if (aligned(c, 16) && ld % 8 == 0) P.c_map = output(c, P.n, P.m, ld);
+    if (aligned(c, 16) && ld % 8 == 0) P.c_map = output(c, P.cols, P.rows, ld);
+  }
+  // Run a token product; the weight's K is contiguous (k_major) or its columns are.
+  int run_token(int epi, bool k_major, int clusters, cudaStream_t s) {
+    return g.swap ? run(epi, !k_major, false, clusters, s) : run(epi, false, !k_major, clusters, s);
   }
   int run(int epi, bool a_mn, bool b_mn, int clusters, cudaStream_t s) {
     if (!ok) return DMUON_ERR_CUDA;
     lin_schedule(g, epi != kLinXent, clusters);
-    if (g.split > 1 &&
-        cudaMemsetAsync(g.arrived, 0, lin_arrived_bytes(), s) != cudaSuccess)
-      return DMUON_ERR_CUDA;
     return launch_lin(g, epi, a_mn, b_mn, clusters, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
   }
 };
@@ -247,25 +272,28 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   if (e != DMUON_OK) return e;
   {
     Launch L(f.ps);
-    LinProblem& P = L.problem(s.tokens, s.ffn, 128, s.hidden, 0);
-    P.a0 = L.operand(xr, s.hidden, s.tokens, xr_ld);
-    P.b0 = L.operand(w.gate, s.hidden, s.ffn, w.ld_in);
-    P.b1 = L.operand(w.up, s.hidden, s.ffn, w.ld_in);
-    P.c_map = L.output(f.h, s.ffn, s.tokens, f8);
+    LinProblem& P = L.token_problem(s.tokens, s.ffn, 128, s.hidden, 0);
+    const int t = L.operand(xr, s.hidden, s.tokens, xr_ld, L.g.swap ? L.g.nt / 2 : 128);
+    const int gate = L.operand(w.gate, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
+    const int up = L.operand(w.up, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
+    P.a0 = L.g.swap ? gate : t;
+    P.a1 = up;
+    P.b0 = L.g.swap ? t : gate;
+    P.b1 = up;
+    L.store_to(P, f.h, f8);
     use_saved(L.g, s, saved);
     if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
       L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
       L.g.map_up = L.output(static_cast<bf16*>(L.g.up), s.ffn, s.tokens, s.ffn);
     }
-    e = L.run(kLinGlu, false, false, clusters, st);
+    e = L.run_token(kLinGlu, true, clusters, st);
     if (e != DMUON_OK) return e;
   }
   Launch L(f.ps);
-  LinProblem& P = L.problem(s.tokens, s.hidden, 256, s.ffn, 0);
-  P.a0 = L.operand(f.h, s.ffn, s.tokens, f8);
-  P.b0 = L.operand(w.down, s.ffn, s.hidden, w.ld_down);
+  LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, 0);
+  L.operands(P, f.h, s.ffn, f8, w.down, s.ffn, s.hidden, w.ld_down);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
-  return L.run(kLinStore, false, false, clusters, st);
+  return L.run_token(kLinStore, true, clusters, st);
 }
 
 int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const void* x,
@@ -295,25 +323,24 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   if (e != DMUON_OK) return e;
   {  // dh = dy Wd, and from it dgate, dup and h
     Launch L(f.ps);
-    LinProblem& P = L.problem(s.tokens, s.ffn, 256, s.hidden, 0);
-    P.a0 = L.operand(dyr, s.hidden, s.tokens, dyr_ld);
-    P.b0 = L.operand(w.down, s.ffn, s.hidden, w.ld_down);
-    P.c_map = L.output(f.dgate, s.ffn, s.tokens, f8);
+    LinProblem& P = L.token_problem(s.tokens, s.ffn, 256, s.hidden, 0);
+    L.operands(P, dyr, s.hidden, dyr_ld, w.down, s.ffn, s.hidden, w.ld_down);
+    L.store_to(P, f.dgate, f8);
+    L.g.dup = f.dup;
+    L.g.h = f.h;
     L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, f8);
     L.g.map_h = L.output(f.h, s.ffn, s.tokens, f8);
     use_saved(L.g, s, saved);
-    e = L.run(kLinGluGrad, false, true, clusters, st);
+    e = L.run_token(kLinGluGrad, false, clusters, st);
     if (e != DMUON_OK) return e;
   }
   {  // dx = dgate Wg + dup Wu
     Launch L(f.ps);
-    LinProblem& P = L.problem(s.tokens, s.hidden, 256, s.ffn, s.ffn);
-    P.a0 = L.operand(f.dgate, s.ffn, s.tokens, f8);
-    P.b0 = L.operand(w.gate, s.hidden, s.ffn, w.ld_in);
-    P.a1 = L.operand(f.dup, s.ffn, s.tokens, f8);
-    P.b1 = L.operand(w.up, s.hidden, s.ffn, w.ld_in);
+    LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, s.ffn);
+    L.operands(P, f.dgate, s.ffn, f8, w.gate, s.hidden, s.ffn, w.ld_in);
+    L.operands(P, f.dup, s.ffn, f8, w.up, s.hidden, s.ffn, w.ld_in, true);
     L.store_to(P, static_cast<bf16*>(dx), dx_ld);
-    e = L.run(kLinStore, false, true, clusters, st);
+    e = L.run_token(kLinStore, false, clusters, st);
     if (e != DMUON_OK) return e;
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
@@ -323,7 +350,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
-    LinProblem& P = L.problem(m, n, 256, s.tokens, 0);
+    LinProblem& P = L.problem(m, n, s.tokens, 0);
     P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? f8 : dyr_ld);
     P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, f8);
     L.store_to(P, out[i], n);
@@ -351,20 +378,23 @@ struct XentSpace {
   float *target_logit, *grad_scale;
   float2* stat;
   float* sum;
-  int64_t piece, stat_ld;
+  int64_t piece;
   size_t bytes;
 };
 XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   Carve c(ws);
   XentSpace x{};
-  const size_t d8 = size_t(up8(s.hidden)), groups = size_t(ceil_div(s.vocab, kXentGroup));
+  const size_t d8 = size_t(up8(s.hidden));
   x.piece = xent_piece(s, grads);
-  x.stat_ld = (x.piece + 31) / 32 * 32;
   x.ps = take_product_space(c);
   x.hidden = c.take<bf16>(size_t(s.tokens) * d8 * 2);
   x.target_logit = c.take<float>(size_t(s.tokens) * 4);
   x.grad_scale = c.take<float>(4);
-  x.stat = c.take<float2>(groups * size_t(x.stat_ld) * sizeof(float2));
+  // swapped products have four times the groups, over at most kSwapTokens tokens
+  x.stat = c.take<float2>(
+      std::max(size_t(ceil_div(s.vocab, kXentGroup)) * size_t(up32(x.piece)),
+               size_t(ceil_div(s.vocab, kXentGroupSwap)) *
+                   size_t(std::min(up32(x.piece), kSwapTokens))) * sizeof(float2));
   if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * d8 * 2);
   if (grads) {
     x.e = c.take<bf16>(size_t(x.piece) * size_t(up8(s.vocab)) * 2);
@@ -414,20 +444,21 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     R.grad_scale = x.grad_scale;
     R.target_logit = x.target_logit + t0;
     R.group_stat = x.stat;
-    R.stat_ld = x.stat_ld;
+    R.stat_ld = up32(n);
     R.loss = loss + t0;
     R.lse = lse + t0;
     {
       Launch L(x.ps);
-      LinProblem& P = L.problem(n, s.vocab, 256, s.hidden, 0);
-      P.a0 = L.operand(hp, s.hidden, n, hr_ld);
-      P.b0 = L.operand(w, s.hidden, s.vocab, w_ld);
+      LinProblem& P = L.token_problem(n, s.vocab, 256, s.hidden, 0);
+      L.operands(P, hp, s.hidden, hr_ld, w, s.hidden, s.vocab, w_ld);
       if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
       L.g.target = tgt + t0;
       L.g.target_logit = x.target_logit + t0;
       L.g.group_stat = x.stat;
-      L.g.stat_ld = x.stat_ld;
-      e = L.run(kLinXent, false, false, clusters, st);
+      L.g.stat_ld = R.stat_ld;
+      if (L.g.swap && n > kSwapTokens) return DMUON_ERR_UNSUPPORTED;  // sized for fewer
+      R.group = L.g.swap ? kXentGroupSwap : kXentGroup;
+      e = L.run_token(kLinXent, true, clusters, st);
       if (e != DMUON_OK) return e;
     }
     if (launch_xent_rows(R, st) != cudaSuccess) return DMUON_ERR_CUDA;
@@ -435,17 +466,16 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     if (launch_xent_grad(R, x.e, v8, st) != cudaSuccess) return DMUON_ERR_CUDA;
     {  // dhidden = G W
       Launch L(x.ps);
-      LinProblem& P = L.problem(n, s.hidden, 256, s.vocab, 0);
-      P.a0 = L.operand(x.e, s.vocab, n, v8);
-      P.b0 = L.operand(w, s.hidden, s.vocab, w_ld);
+      LinProblem& P = L.token_problem(n, s.hidden, 256, s.vocab, 0);
+      L.operands(P, x.e, s.vocab, v8, w, s.hidden, s.vocab, w_ld);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
       L.g.scale = x.grad_scale;
-      e = L.run(kLinStore, false, true, clusters, st);
+      e = L.run_token(kLinStore, false, clusters, st);
       if (e != DMUON_OK) return e;
     }
     // dweight += G^T h, in fp32 over the pieces
     Launch L(x.ps);
-    LinProblem& P = L.problem(s.vocab, s.hidden, 256, n, 0);
+    LinProblem& P = L.problem(s.vocab, s.hidden, n, 0);
     P.a0 = L.operand(x.e, s.vocab, n, v8);
     P.b0 = L.operand(hp, s.hidden, n, hr_ld);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);

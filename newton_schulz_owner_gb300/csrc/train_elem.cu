@@ -55,74 +55,39 @@ DM_DEV void load8(const void* p, long long i, bool vec, int n, float (&f)[8]) {
   }
 }
 
-// Four neighbouring lanes hold a block: 8 values each.
+// Eight values of a block in 8 bits; the block's other values are in the three
+// lanes beside (all lanes of the warp take part).
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) act8_save_kernel(long long cols, long long tiles,
-                                                             const void* x, long long ld,
-                                                             bool vec_in, bool vec_out,
-                                                             signed char* codes,
-                                                             __nv_bfloat16* scales) {
-  const long long row = blockIdx.x / tiles;
-  const long long c0 = (blockIdx.x - row * tiles) * kVecCols + threadIdx.x * 8;
-  const int n = c0 < cols ? int(min(8ll, cols - c0)) : 0;
-  float v[8];
-  load8<BF16>(x, row * ld + c0, vec_in, n, v);
-  float top = 0.f;
-  bool finite = true;
+DM_DEV uint2 act8_pack(const float (&v)[8], float& s) {
+  float top = 0.f, bad = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     top = fmaxf(top, fabsf(v[k]));
-    finite = finite && fabsf(v[k]) <= 3.402823466e38f;
+    bad = fmaf(v[k], 0.f, bad);  // NaN once a value is not finite
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    finite = __shfl_xor_sync(0xffffffffu, int(finite), o) && finite;
+    bad += __shfl_xor_sync(0xffffffffu, bad, o);
   }
-  if (n == 0) return;
-  const float s = act8_scale(top, finite);
-  const bool live = finite && s > 0.f;
-  const float r = BF16 && live ? __fdiv_rn(1.f, s) : 0.f;
+  s = act8_scale(top, bad == 0.f);
   uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (live) w[k >> 2] |= (BF16 ? act8_code_bf16(v[k], r) : act8_code_f32(v[k], s)) << (8 * (k & 3));
-  signed char* dst = codes + row * cols + c0;
-  if (vec_out && n >= 8) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  } else {
+  if (bad == 0.f && s > 0.f) {
+    const float r = __fdiv_rn(1.f, s);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) dst[k] = (signed char)(w[k >> 2] >> (8 * (k & 3)));
+      w[k >> 2] |= (BF16 ? act8_code_bf16(v[k], r) : act8_code_f32(v[k], s)) << (8 * (k & 3));
   }
-  if ((threadIdx.x & 3) == 0)
-    scales[row * ((cols + kActBlock - 1) / kActBlock) + c0 / kActBlock] = __float2bfloat16_rn(s);
+  return make_uint2(w[0], w[1]);
 }
-
+DM_DEV void act8_unpack(const uint2& q, float s, float (&f)[8]) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = s * float((signed char)(w[k >> 2] >> (8 * (k & 3))));
+}
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) act8_load_kernel(long long cols, long long tiles,
-                                                             const signed char* codes,
-                                                             const __nv_bfloat16* scales,
-                                                             void* out, long long ld, bool vec_in,
-                                                             bool vec_out) {
-  const long long row = blockIdx.x / tiles;
-  const long long c0 = (blockIdx.x - row * tiles) * kVecCols + threadIdx.x * 8;
-  if (c0 >= cols) return;
-  const int n = int(min(8ll, cols - c0));
-  const float s = __bfloat162float(scales[row * ((cols + kActBlock - 1) / kActBlock) + c0 / kActBlock]);
-  const signed char* src = codes + row * cols + c0;
-  float f[8];
-  if (vec_in && n >= 8) {
-    const uint2 q = *reinterpret_cast<const uint2*>(src);
-    const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = s * float((signed char)(w[k >> 2] >> (8 * (k & 3))));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = k < n ? s * float(src[k]) : 0.f;
-  }
-  const long long at = row * ld + c0;
-  if (vec_out && n >= 8) {
+DM_DEV void store8(void* out, long long at, bool vec, int n, const float (&f)[8]) {
+  if (vec && n >= 8) {
     if (BF16) {
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) = pack8(f);
     } else {
@@ -140,6 +105,112 @@ __global__ void __launch_bounds__(kThreads) act8_load_kernel(long long cols, lon
   }
 }
 
+// Any shape and pitch: a block covers kVecCols columns of one row.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) act8_save_kernel(long long cols, unsigned tiles,
+                                                             const void* x, long long ld,
+                                                             bool vec_in, bool vec_out,
+                                                             signed char* codes,
+                                                             __nv_bfloat16* scales) {
+  grid_launch_dependents();
+  grid_wait();
+  const long long row = blockIdx.x / tiles;
+  const long long c0 = (long long)(blockIdx.x - unsigned(row) * tiles) * kVecCols + threadIdx.x * 8;
+  const int n = c0 < cols ? int(min(8ll, cols - c0)) : 0;
+  float v[8], s;
+  load8<BF16>(x, row * ld + c0, vec_in, n, v);
+  const uint2 w = act8_pack<BF16>(v, s);
+  if (n == 0) return;
+  signed char* dst = codes + row * cols + c0;
+  if (vec_out && n >= 8) {
+    *reinterpret_cast<uint2*>(dst) = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) dst[k] = (signed char)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+  }
+  if ((threadIdx.x & 3) == 0)
+    scales[row * ((cols + kActBlock - 1) / kActBlock) + c0 / kActBlock] = __float2bfloat16_rn(s);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) act8_load_kernel(long long cols, unsigned tiles,
+                                                             const signed char* codes,
+                                                             const __nv_bfloat16* scales,
+                                                             void* out, long long ld, bool vec_in,
+                                                             bool vec_out) {
+  grid_launch_dependents();
+  grid_wait();
+  const long long row = blockIdx.x / tiles;
+  const long long c0 = (long long)(blockIdx.x - unsigned(row) * tiles) * kVecCols + threadIdx.x * 8;
+  if (c0 >= cols) return;
+  const int n = int(min(8ll, cols - c0));
+  const float s = __bfloat162float(scales[row * ((cols + kActBlock - 1) / kActBlock) + c0 / kActBlock]);
+  const signed char* src = codes + row * cols + c0;
+  float f[8];
+  if (vec_in && n >= 8) {
+    act8_unpack(*reinterpret_cast<const uint2*>(src), s, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < n ? s * float(src[k]) : 0.f;
+  }
+  store8<BF16>(out, row * ld + c0, vec_out, n, f);
+}
+
+// Contiguous rows of whole blocks: the matrix is one run of blocks, and a thread
+// keeps kUnits 16-byte loads in flight.
+constexpr int kUnits = 4;
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) act8_save_flat_kernel(long long units, const void* x,
+                                                                  uint2* codes,
+                                                                  __nv_bfloat16* scales) {
+  grid_launch_dependents();
+  grid_wait();
+  const long long u0 = (long long)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  float v[kUnits][8];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k)
+    load8<BF16>(x, (u0 + k * kThreads) * 8, true, u0 + k * kThreads < units ? 8 : 0, v[k]);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const long long u = u0 + k * kThreads;
+    float s;
+    const uint2 w = act8_pack<BF16>(v[k], s);
+    if (u < units) {
+      codes[u] = w;
+      if ((threadIdx.x & 3) == 0) scales[u / 4] = __float2bfloat16_rn(s);
+    }
+  }
+}
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) act8_load_flat_kernel(long long units,
+                                                                  const uint2* codes,
+                                                                  const __nv_bfloat16* scales,
+                                                                  void* out) {
+  grid_launch_dependents();
+  grid_wait();
+  const long long u0 = (long long)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  uint2 q[kUnits];
+  float s[kUnits];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const long long u = u0 + k * kThreads;
+    if (u < units) {
+      q[k] = codes[u];
+      s[k] = __bfloat162float(scales[u / 4]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const long long u = u0 + k * kThreads;
+    if (u < units) {
+      float f[8];
+      act8_unpack(q[k], s[k], f);
+      store8<BF16>(out, u * 8, true, 8, f);
+    }
+  }
+}
+
 DM_DEV bool live_target(const long long* target, long long row, long long vocab) {
   if (target == nullptr) return true;
   const long long t = target[row];
@@ -154,6 +225,8 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(long long cols, lon
                                                              const long long* target,
                                                              long long vocab, bool vec_in,
                                                              bool vec_out) {
+  grid_launch_dependents();
+  grid_wait();
   const long long row = blockIdx.x / tiles;
   const long long c0 = (blockIdx.x - row * tiles) * kVecCols + threadIdx.x * 8;
   if (c0 >= cols) return;
@@ -176,6 +249,8 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* grad_loss
                                                           long long tokens, long long vocab,
                                                           float* scale) {
   __shared__ float top[32];
+  grid_launch_dependents();
+  grid_wait();
   float m = 0.f;
   for (long long t = threadIdx.x; t < tokens; t += 1024)
     if (live_target(target, t, vocab)) m = fmaxf(m, fabsf(grad_loss[t]));
@@ -191,41 +266,64 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* grad_loss
   }
 }
 
-// One block per 32 tokens: 8 warps share the groups, lane = token.
-__global__ void __launch_bounds__(kThreads) xent_rows_kernel(const XentRows r) {
-  __shared__ float sm[8][32], ss[8][32];
+// lse and loss from the groups' maxima and sums.  A block takes `tb` tokens (a power
+// of two up to 32, few when there are few tokens, so that the groups spread over
+// many blocks): lane % tb is the token, everything else strides over the groups
+// with four loads in flight.  Partial results join in a fixed order.
+constexpr int kRowThreads = 1024;
+// maximum and sum of up to N pairs; pairs at the common maximum add as they are, so
+// that a NaN beside an infinity stays
+DM_DEV float weigh(float m, float s, float top) {
+  return m == top ? s : s * exp2f((m - top) * 1.44269504f);
+}
+DM_DEV void join(float& m, float& s, float pm, float ps) {
+  const float top = fmaxf(m, pm);
+  s = weigh(m, s, top) + weigh(pm, ps, top);
+  m = top;
+}
+__global__ void __launch_bounds__(kRowThreads) xent_rows_kernel(const XentRows r, int tb) {
+  __shared__ float sm[kRowThreads / 32][32], ss[kRowThreads / 32][32];
+  grid_launch_dependents();
+  grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long row = (long long)blockIdx.x * 32 + lane;
+  const long long row = (long long)blockIdx.x * tb + (lane & (tb - 1));
   const bool in = row < r.tokens;
-  const long long groups = (r.vocab + kXentGroup - 1) / kXentGroup;
-  // running maximum and sum of exponentials relative to it
+  const long long groups = (r.vocab + r.group - 1) / r.group;
+  const int step = kRowThreads / tb;
   float m = -INFINITY, s = 0.f;
   if (in)
-    for (long long g = w; g < groups; g += 8) {
-      const float2 p = r.group_stat[g * r.stat_ld + row];
-      if (p.x > m) {
-        s = s * exp2f((m - p.x) * 1.44269504f) + p.y;
-        m = p.x;
-      } else {
-        // groups with the same infinity keep their sum, so that a NaN in it stays
-        s += p.x == m ? p.y : p.y * exp2f((p.x - m) * 1.44269504f);
+    for (long long g = w * (32 / tb) + lane / tb; g < groups; g += 4 * step) {
+      float2 p[4];
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[k] = g + k * step < groups ? r.group_stat[(g + k * step) * r.stat_ld + row]
+                                     : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, p[k].x);
       }
+      s = weigh(m, s, top);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += weigh(p[k].x, p[k].y, top);
+      m = top;
     }
+  for (int o = tb; o < 32; o <<= 1)
+    join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
   sm[w][lane] = m;
   ss[w][lane] = s;
   __syncthreads();
-  if (w != 0 || !in) return;
-  m = sm[0][lane];
+  // warp w joins the warps' results of token w of the block: lane = warp
+  if (w >= tb) return;
+  m = sm[lane][w];
+  s = ss[lane][w];
 #pragma unroll
-  for (int k = 1; k < 8; ++k) m = fmaxf(m, sm[k][lane]);
-  s = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    s += sm[k][lane] == m ? ss[k][lane] : ss[k][lane] * exp2f((sm[k][lane] - m) * 1.44269504f);
-  const bool live = live_target(r.target, row, r.vocab);
+  for (int o = 1; o < 32; o <<= 1)
+    join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+  const long long t = (long long)blockIdx.x * tb + w;
+  if (lane != 0 || t >= r.tokens) return;
+  const bool live = live_target(r.target, t, r.vocab);
   const float ls = logf(s);
-  r.loss[row] = live ? (m - r.target_logit[row]) + ls : 0.f;
-  r.lse[row] = live ? m + ls : 0.f;
+  r.loss[t] = live ? (m - r.target_logit[t]) + ls : 0.f;
+  r.lse[t] = live ? m + ls : 0.f;
 }
 
 // G = grad_loss / scale * (exp(z - lse) - [entry is the target]).  exp(z - m)
@@ -233,36 +331,53 @@ __global__ void __launch_bounds__(kThreads) xent_rows_kernel(const XentRows r) {
 // that shows; at the target the difference to 1 is taken as expm1(-loss).  With
 // equal weights (a mean) grad_loss / scale is 1, and the -1 of an unlikely target
 // is exact; the scale is put back in fp32 where the products are written.
+// A block takes kGradCols columns of one row, four 16-byte loads in flight a thread.
+constexpr int kGradCols = 4 * kVecCols;
 __global__ void __launch_bounds__(kThreads) xent_grad_kernel(const XentRows r, uint4* e,
-                                                             long long e_ld, long long tiles) {
+                                                             long long e_ld, unsigned tiles) {
+  grid_launch_dependents();
+  grid_wait();
   const long long row = blockIdx.x / tiles;
-  const long long c0 = (blockIdx.x - row * tiles) * kVecCols + threadIdx.x * 8;
-  if (c0 >= r.vocab) return;
+  const long long c0 = (long long)(blockIdx.x - unsigned(row) * tiles) * kGradCols + threadIdx.x * 8;
   uint4* p = e + (row * e_ld + c0) / 8;
-  const long long t = r.target[row];
-  if (t < 0 || t >= r.vocab) {
-    *p = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const float gl = r.grad_loss[row] / *r.grad_scale;
-  const float f = gl * exp2f((r.group_stat[(c0 / kXentGroup) * r.stat_ld + row].x - r.lse[row]) *
-                             1.44269504f);
-  const uint4 q = *p;
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  float v[8];
+  uint4 q[4];
+  float m[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-    v[2 * k] = x.x * f;
-    v[2 * k + 1] = x.y * f;
+    const long long c = c0 + k * kVecCols;
+    if (c < r.vocab) {
+      q[k] = p[k * kThreads];
+      m[k] = r.group_stat[(unsigned(c) / unsigned(r.group)) * r.stat_ld + row].x;
+    }
   }
-  if (t >= c0 && t < c0 + 8) {
-    const float at = gl * expm1f(-r.loss[row]);
+  const long long t = r.target[row];
+  const bool live = t >= 0 && t < r.vocab;
+  const float gl = live ? r.grad_loss[row] / *r.grad_scale : 0.f, lse = r.lse[row];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c0 + k == t) v[k] = at;
+  for (int k = 0; k < 4; ++k) {
+    const long long c = c0 + k * kVecCols;
+    if (c >= r.vocab) break;
+    if (!live) {
+      p[k * kThreads] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const float f = gl * exp2f((m[k] - lse) * 1.44269504f);
+    const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[2 * j] = x.x * f;
+      v[2 * j + 1] = x.y * f;
+    }
+    if (t >= c && t < c + 8) {
+      const float at = gl * expm1f(-r.loss[row]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j == t) v[j] = at;
+    }
+    p[k * kThreads] = pack8(v);
   }
-  *p = pack8(v);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -273,29 +388,35 @@ long long tiles_of(long long cols) { return (cols + kVecCols - 1) / kVecCols; }
 cudaError_t launch_act8_save(long long rows, long long cols, const void* x, long long ld,
                              bool bf16, signed char* codes, __nv_bfloat16* scales,
                              cudaStream_t s) {
-  const long long tiles = tiles_of(cols);
   const bool vin = aligned16(x) && ld % 8 == 0;
   const bool vout = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
-  const unsigned grid = unsigned(rows * tiles);
-  if (bf16)
-    act8_save_kernel<true><<<grid, kThreads, 0, s>>>(cols, tiles, x, ld, vin, vout, codes, scales);
-  else
-    act8_save_kernel<false><<<grid, kThreads, 0, s>>>(cols, tiles, x, ld, vin, vout, codes, scales);
-  return counted(cudaGetLastError());
+  if (vin && vout && ld == cols && cols % kActBlock == 0) {
+    const long long units = rows * cols / 8;
+    return launch_dependent(bf16 ? act8_save_flat_kernel<true> : act8_save_flat_kernel<false>,
+                            unsigned((units + kThreads * kUnits - 1) / (kThreads * kUnits)),
+                            kThreads, s, units, x, reinterpret_cast<uint2*>(codes), scales);
+  }
+  const unsigned tiles = unsigned(tiles_of(cols));
+  return launch_dependent(bf16 ? act8_save_kernel<true> : act8_save_kernel<false>,
+                          unsigned(rows) * tiles, kThreads, s, cols, tiles, x, ld, vin, vout, codes,
+                          scales);
 }
 
 cudaError_t launch_act8_load(long long rows, long long cols, const signed char* codes,
                              const __nv_bfloat16* scales, void* out, long long ld, bool bf16,
                              cudaStream_t s) {
-  const long long tiles = tiles_of(cols);
   const bool vin = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
   const bool vout = aligned16(out) && ld % 8 == 0;
-  const unsigned grid = unsigned(rows * tiles);
-  if (bf16)
-    act8_load_kernel<true><<<grid, kThreads, 0, s>>>(cols, tiles, codes, scales, out, ld, vin, vout);
-  else
-    act8_load_kernel<false><<<grid, kThreads, 0, s>>>(cols, tiles, codes, scales, out, ld, vin, vout);
-  return counted(cudaGetLastError());
+  if (vin && vout && ld == cols && cols % kActBlock == 0) {
+    const long long units = rows * cols / 8;
+    return launch_dependent(bf16 ? act8_load_flat_kernel<true> : act8_load_flat_kernel<false>,
+                            unsigned((units + kThreads * kUnits - 1) / (kThreads * kUnits)),
+                            kThreads, s, units, reinterpret_cast<const uint2*>(codes), scales, out);
+  }
+  const unsigned tiles = unsigned(tiles_of(cols));
+  return launch_dependent(bf16 ? act8_load_kernel<true> : act8_load_kernel<false>,
+                          unsigned(rows) * tiles, kThreads, s, cols, tiles, codes, scales, out, ld,
+                          vin, vout);
 }
 
 cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16* src,
@@ -303,10 +424,9 @@ cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16
                              const long long* target, long long vocab, cudaStream_t s) {
   const long long tiles = tiles_of(cols);
   if (rows <= 0 || cols <= 0) return cudaSuccess;
-  copy_rows_kernel<<<unsigned(rows * tiles), kThreads, 0, s>>>(
-      cols, tiles, src, src_ld, dst, dst_ld, target, vocab, aligned16(src) && src_ld % 8 == 0,
-      aligned16(dst) && dst_ld % 8 == 0);
-  return counted(cudaGetLastError());
+  return launch_dependent(copy_rows_kernel, unsigned(rows * tiles), kThreads, s, cols, tiles, src,
+                          src_ld, dst, dst_ld, target, vocab, aligned16(src) && src_ld % 8 == 0,
+                          aligned16(dst) && dst_ld % 8 == 0);
 }
 
 cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst, long long ld,
@@ -316,20 +436,20 @@ cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst,
 
 cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,
                               long long vocab, float* scale, cudaStream_t s) {
-  grad_scale_kernel<<<1, 1024, 0, s>>>(grad_loss, target, tokens, vocab, scale);
-  return counted(cudaGetLastError());
+  return launch_dependent(grad_scale_kernel, 1u, 1024u, s, grad_loss, target, tokens, vocab, scale);
 }
 
 cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s) {
-  xent_rows_kernel<<<unsigned((r.tokens + 31) / 32), kThreads, 0, s>>>(r);
-  return counted(cudaGetLastError());
+  int tb = 32;
+  while (tb > 1 && r.tokens < 152ll * tb) tb >>= 1;
+  return launch_dependent(xent_rows_kernel, unsigned((r.tokens + tb - 1) / tb), kRowThreads, s, r,
+                          tb);
 }
 
 cudaError_t launch_xent_grad(const XentRows& r, void* e, long long e_ld, cudaStream_t s) {
-  const long long tiles = tiles_of(r.vocab);
-  xent_grad_kernel<<<unsigned(r.tokens * tiles), kThreads, 0, s>>>(r, static_cast<uint4*>(e), e_ld,
-                                                                   tiles);
-  return counted(cudaGetLastError());
+  const unsigned tiles = unsigned((r.vocab + kGradCols - 1) / kGradCols);
+  return launch_dependent(xent_grad_kernel, unsigned(r.tokens) * tiles, kThreads, s, r,
+                          static_cast<uint4*>(e), e_ld, tiles);
 }
 
 }  // namespace dm

@@ -180,7 +180,8 @@ def check_kept(dm, op, saved, fwd, c, f):
 
 
 FFN_SHAPES = [(1, 8, 8), (1, 64, 128), (2, 100, 33), (17, 256, 129), (64, 129, 257), (65, 512, 384),
-              (255, 72, 100), (256, 128, 128), (257, 520, 136), (513, 264, 640), (300, 1000, 2050)]
+              (255, 72, 100), (256, 128, 128), (257, 520, 136), (513, 264, 640), (300, 1000, 2050),
+              (33, 4096, 330), (97, 2048, 900), (250, 2900, 520), (700, 640, 1100)]
 
 
 @pytest.mark.parametrize("t,d,f", FFN_SHAPES)
@@ -308,7 +309,8 @@ def loss_bound(h, w, lse):
 
 
 XENT_SHAPES = [(1, 8, 8), (1, 64, 1), (2, 100, 127), (17, 256, 128), (64, 129, 129), (65, 72, 1000),
-               (255, 64, 256), (256, 520, 257), (257, 128, 3001), (40, 512, 20011)]
+               (255, 64, 256), (256, 520, 257), (257, 128, 3001), (40, 512, 20011),
+               (33, 1500, 9000), (520, 1100, 4000)]
 
 
 @pytest.mark.parametrize("t,d,v", XENT_SHAPES)

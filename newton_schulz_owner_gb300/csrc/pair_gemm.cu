@@ -57,12 +57,9 @@ namespace {
 
 constexpr int kTile = 256;                 // tile rows and columns (CTA pair)
 constexpr int kHalf = 128;                 // one CTA's rows of A / columns of B
-constexpr int kK = 128;                    // K-elements per stage
 constexpr int kStages = 3;                 // of 64 KB; swapped, as many as fit there
-constexpr int kMaxStages = 5;
-constexpr int kOpBytes = kHalf * kK * 2;   // 32 KB: one CTA's share of a 256-wide operand
-constexpr int kStageArea = kStages * 2 * kOpBytes;
-constexpr int kAtom = kOpBytes / 2;        // one TMA box: 64 K x 128 rows, or 64 MN x 128 K
+constexpr int kMaxStages = 10;
+constexpr int kStageArea = kStages * 65536;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kTmemCols = 512;
@@ -81,24 +78,42 @@ constexpr int kStrip = 8;
 // The tensor core's accumulation rounds toward zero, so a sum of K products loses
 // up to K/16 * 2^-25 of its size.  That is far below bf16 for an output that is
 // rounded to it, but not for the fp32 losses: the logits are accumulated in runs
-// of kRun stages (512 K-elements), each drained and added in registers, rounded
+// of 512 K-elements, each drained and added in registers, rounded
 // to nearest.  The drains hide behind the next run's MMAs.
-constexpr int kRun = 4;
+constexpr int kRunElems = 512;
 
 // Workspace of the split parts.
 constexpr size_t kPartialBytes = size_t(40) << 20;
 
-// The B operand's share of a stage: 128 columns, or half of the nt tokens.
+// A stage: K-elements, this CTA's 128 rows of A and its half of B's columns (128,
+// or nt/2 tokens).  Plainly 128 K-elements, which halves the barrier round trips;
+// swapped, where the bytes in flight bound the rate at which weights stream, 64, so
+// that a smaller part of the stages is being consumed.
 template <bool SWAP>
-DM_DEV int b_rows(const LinArgs& g) { return SWAP ? g.nt / 2 : kHalf; }
-template <bool SWAP>
-DM_DEV int stage_bytes(const LinArgs& g) { return kOpBytes + b_rows<SWAP>(g) * kK * 2; }
+struct Stage {
+  static constexpr int k = SWAP ? kLinKSwap : kLinK;
+  static constexpr int a_bytes = kHalf * k * 2;
+  static constexpr int panels = k / 64;  // spans of a 128-byte swizzled row
+  static DM_DEV int b_rows(const LinArgs& g) { return SWAP ? g.nt / 2 : kHalf; }
+  static DM_DEV int bytes(const LinArgs& g) { return a_bytes + b_rows(g) * k * 2; }
+  static DM_DEV int count(const LinArgs& g) { return SWAP ? g.stages : kStages; }
+};
 
 struct Unit {
   int prob, ti, tj;
   int kb_lo, kb_hi;  // K blocks of this unit
   int q, part;       // split tile (0-based) and part; q < 0: a whole tile
 };
+
+// n / d with d's magic number (lin_magic), n < 2^31: the epilogue decodes a tile per
+// few thousand cycles, and hardware division would take a third of that.
+DM_DEV int divide(int n, int d, unsigned magic) {
+  int q = int(__umulhi(unsigned(n), magic));
+  const int r = n - q * d;
+  if (r < 0) --q;
+  else if (r >= d) ++q;
+  return q;
+}
 
 DM_DEV Unit decode_unit(const LinArgs& g, int u) {
   Unit U;
@@ -107,7 +122,7 @@ DM_DEV Unit decode_unit(const LinArgs& g, int u) {
   U.part = 0;
   if (u >= g.full_tiles) {
     const int r = u - g.full_tiles;
-    U.q = r / g.split;
+    U.q = divide(r, g.split, g.split_magic);
     U.part = r - U.q * g.split;
     t = g.full_tiles + U.q;
   }
@@ -117,17 +132,17 @@ DM_DEV Unit decode_unit(const LinArgs& g, int u) {
   U.prob = p;
   const int local = t - P.tile_begin;
   const int per = kStrip * P.tiles_n;
-  const int strip = local / per;
-  const int rows = min(kStrip, P.tiles_m - strip * kStrip);
+  const int strip = divide(local, per, P.strip_magic);
   const int r = local - strip * per;
-  U.tj = r / rows;
+  const int rows = min(kStrip, P.tiles_m - strip * kStrip);
+  U.tj = rows == kStrip ? r / kStrip : divide(r, rows, P.last_magic);
   U.ti = strip * kStrip + (r - U.tj * rows);
   const int kb = P.kb0 + P.kb1;
   U.kb_lo = 0;
   U.kb_hi = kb;
   if (U.q >= 0) {
-    U.kb_lo = int((long long)kb * U.part / g.split);
-    U.kb_hi = int((long long)kb * (U.part + 1) / g.split);
+    U.kb_lo = divide(kb * U.part, g.split, g.split_magic);
+    U.kb_hi = divide(kb * (U.part + 1), g.split, g.split_magic);
   }
   return U;
 }
@@ -138,8 +153,9 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
                      uint64_t* empty_bar, volatile int* abort_flag) {
   const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0);
   const int clusters = int(cluster_count_x());
-  const int stages = SWAP ? g.stages : kStages;
-  const int bytes = stage_bytes<SWAP>(g), brows = b_rows<SWAP>(g);
+  using St = Stage<SWAP>;
+  const int stages = St::count(g), bytes = St::bytes(g), brows = St::b_rows(g);
+  constexpr int a_box = St::k * 128;  // 64 MN-elements of k rows, or (two panels) 128 rows
   int stage = 0;
   uint32_t phase = 0;
   for (int u = int(cluster_id_x()); u < g.total_units; u += clusters) {
@@ -156,7 +172,7 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
       const CUtensorMap* mapA = &g.maps[second ? P.a1 : P.a0];
       const CUtensorMap* mapB =
           &g.maps[EPI == kLinGlu && !SWAP ? (rank == 0 ? P.b0 : P.b1) : (second ? P.b1 : P.b0)];
-      const int k0 = (second ? kb - P.kb0 : kb) * kK;
+      const int k0 = (second ? kb - P.kb0 : kb) * St::k;
       if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) {
         raise_abort(g.err, abort_flag);
         return;
@@ -164,20 +180,27 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
       if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], uint32_t(2 * bytes));
       const uint32_t bar = leader_full + uint32_t(stage) * 8u;
       uint8_t* a = sStage + stage * bytes;
-      uint8_t* b = a + kOpBytes;
+      uint8_t* b = a + St::a_bytes;
       // rows, columns and K past the tensors' ends read as zeros
+      if (A_MN) {
+        tma_load_2d_pair(a, mapA, bar, row0, k0);
+        tma_load_2d_pair(a + a_box, mapA, bar, row0 + 64, k0);
+      }
+      if (B_MN) {
+        tma_load_2d_pair(b, mapB, bar, col0, k0);
+        tma_load_2d_pair(b + a_box, mapB, bar, col0 + 64, k0);
+      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (SWAP && EPI == kLinGlu) {
-          tma_load_2d_pair(a + h * kAtom, &g.maps[P.a0], bar, k0 + h * 64, row0);
-          tma_load_2d_pair(a + h * kAtom + kAtom / 2, &g.maps[P.a1], bar, k0 + h * 64, row0);
-        } else if (A_MN) {
-          tma_load_2d_pair(a + h * kAtom, mapA, bar, row0 + h * 64, k0);
-        } else {
-          tma_load_2d_pair(a + h * kAtom, mapA, bar, k0 + h * 64, row0);
+      for (int h = 0; h < St::panels; ++h) {
+        if (!A_MN) {
+          if (SWAP && EPI == kLinGlu) {
+            tma_load_2d_pair(a + h * 16384, &g.maps[P.a0], bar, k0 + h * 64, row0);
+            tma_load_2d_pair(a + h * 16384 + 8192, &g.maps[P.a1], bar, k0 + h * 64, row0);
+          } else {
+            tma_load_2d_pair(a + h * 16384, mapA, bar, k0 + h * 64, row0);
+          }
         }
-        if (B_MN) tma_load_2d_pair(b + h * kAtom, mapB, bar, col0 + h * 64, k0);
-        else tma_load_2d_pair(b + h * brows * 128, mapB, bar, k0 + h * 64, col0);
+        if (!B_MN) tma_load_2d_pair(b + h * brows * 128, mapB, bar, k0 + h * 64, col0);
       }
       if (++stage == stages) {
         stage = 0;
@@ -192,15 +215,17 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
                        uint64_t* tfull, uint64_t* tempty, uint64_t* drain_bar, uint32_t tmem_base,
                        volatile int* abort_flag) {
   const uint32_t idesc = idesc_bf16(kTile, SWAP ? g.nt : kTile, A_MN, B_MN);
-  // K-major: two 64-element panels, 32 bytes per K step inside a 128-byte row,
-  // 8-row groups 1 KB apart.  MN-major: 64-element atoms 16 KB apart (LBO), 8-row K
-  // groups 1 KB apart (SBO), 2 KB per K step.  Shared-memory addresses stay below
-  // 256 KB, so adding to the start-address field never carries out of it.
-  const uint64_t a_desc = sdesc_sw128(smem_u32(sStage), A_MN ? kAtom : 16, 1024);
-  const uint64_t b_desc = sdesc_sw128(smem_u32(sStage) + kOpBytes, B_MN ? kAtom : 16, 1024);
-  const uint32_t step = uint32_t(stage_bytes<SWAP>(g)) >> 4;
-  const uint32_t b_panel = uint32_t(b_rows<SWAP>(g)) * 128u >> 4;
-  const int stages = SWAP ? g.stages : kStages;
+  // K-major: 64-element panels, 32 bytes per K step inside a 128-byte row, 8-row
+  // groups 1 KB apart.  MN-major: 64-element atoms of the stage's K rows apart (LBO),
+  // 8-row K groups 1 KB apart (SBO), 2 KB per K step.  Shared-memory addresses stay
+  // below 256 KB, so adding to the start-address field never carries out of it.
+  using St = Stage<SWAP>;
+  constexpr int atom = St::k * 128;
+  const uint64_t a_desc = sdesc_sw128(smem_u32(sStage), A_MN ? atom : 16, 1024);
+  const uint64_t b_desc = sdesc_sw128(smem_u32(sStage) + St::a_bytes, B_MN ? atom : 16, 1024);
+  const uint32_t step = uint32_t(St::bytes(g)) >> 4;
+  const uint32_t b_panel = uint32_t(St::b_rows(g)) * 128u >> 4;
+  const int stages = St::count(g);
   const int clusters = int(cluster_count_x());
   int stage = 0;
   uint32_t phase = 0;
@@ -209,7 +234,7 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
   for (int u = int(cluster_id_x()); ok && u < g.total_units; u += clusters) {
     const Unit U = decode_unit(g, u);
     for (int lo = U.kb_lo; ok && lo < U.kb_hi; ++it) {
-      const int hi = EPI == kLinXent ? min(lo + kRun, U.kb_hi) : U.kb_hi;
+      const int hi = EPI == kLinXent ? min(lo + kRunElems / St::k, U.kb_hi) : U.kb_hi;
       const int acc = it & 1;
       const uint32_t aph = uint32_t(it >> 1) & 1u;
       if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, abort_flag)) {
@@ -229,10 +254,10 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
         const uint64_t ad = a_desc + uint64_t(uint32_t(stage) * step);
         const uint64_t bd = b_desc + uint64_t(uint32_t(stage) * step);
 #pragma unroll
-        for (int k = 0; k < kK / 16; ++k) {
+        for (int k = 0; k < St::k / 16; ++k) {
           const uint64_t ao = A_MN
                                   ? uint64_t(k) * (2048u >> 4)
-                                  : uint64_t(k >> 2) * (kAtom >> 4) + uint64_t(k & 3) * (32u >> 4);
+                                  : uint64_t(k >> 2) * (16384u >> 4) + uint64_t(k & 3) * (32u >> 4);
           const uint64_t bo = B_MN ? uint64_t(k) * (2048u >> 4)
                                    : uint64_t(uint32_t(k >> 2) * b_panel) + uint64_t(k & 3) * (32u >> 4);
           umma_bf16_pair(d, ad + ao, bd + bo, idesc, (kb > lo || k > 0) ? 1u : 0u);
@@ -286,9 +311,9 @@ DM_DEV void glu32(float (&a)[32], const float (&b)[32]) {
 }
 // From dh, gate and up: v <- dup, ga <- dgate, up <- h
 template <int ACT>
-DM_DEV void glu_grad32(float (&v)[32], float (&ga)[32], float (&up)[32]) {
+DM_DEV void glu_grad16(float* v, float (&ga)[16], float (&up)[16]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
+  for (int j = 0; j < 16; ++j) {
     float a, da;
     act_both<ACT>(ga[j], a, da);
     const float dh = v[j];
@@ -402,15 +427,14 @@ DM_DEV void fetch_kept(const LinArgs& g, const void* base, const __nv_bfloat16* 
     }
   }
 }
-DM_DEV void kept_values(const LinArgs& g, const Kept& k, float (&v)[32]) {
+DM_DEV void kept_values(const LinArgs& g, const Kept& k, int half, float (&v)[16]) {
   if (g.keep == kKeepBf16) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) unpack8(k.q[u], v + 8 * u);
+    unpack8(k.q[2 * half], v);
+    unpack8(k.q[2 * half + 1], v + 8);
   } else {
-    const uint32_t w[8] = {k.q[0].x, k.q[0].y, k.q[0].z, k.q[0].w,
-                           k.q[1].x, k.q[1].y, k.q[1].z, k.q[1].w};
+    const uint32_t w[4] = {k.q[half].x, k.q[half].y, k.q[half].z, k.q[half].w};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = k.scale * float((signed char)(w[j / 4] >> (8 * (j & 3))));
+    for (int j = 0; j < 16; ++j) v[j] = k.scale * float((signed char)(w[j / 4] >> (8 * (j & 3))));
   }
 }
 
@@ -464,19 +488,44 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     if (lane == 0) mbar_arrive(bar);
   };
 
+  // kLinStore, plain: 32 x 64 chunks in the warp's 4 KB (128-byte rows: half the TMA
+  // requests of 32 x 32 ones)
+  auto put_wide = [&](int map, const uint32_t (&w)[32], int c0, int rg0) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      st_shared_v4(buf0 + uint32_t(lane * 128 + ((u ^ (lane & 7)) << 4)), w[4 * u], w[4 * u + 1],
+                   w[4 * u + 2], w[4 * u + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&g.maps[map], buf0, c0, rg0);
+      bulk_commit();
+    }
+  };
+
   // Write a 32 x 32 chunk (rows rg0.., columns c0..) of an output through shared
   // memory by TMA, which drops what lies outside.
-  auto put = [&](int map, const float (&o)[32], int c0, int rg0) {
+  auto put_packed = [&](int map, const uint32_t (&w)[16], int c0, int rg0) {
     const uint32_t buf = buf0 + uint32_t((stored++ & 1) * kEpiBufBytes);
     if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
     __syncwarp();
-    epi_store_row(buf, lane, o);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      st_shared_v4(buf + epi_off(lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       tma_store_2d(&g.maps[map], buf, c0, rg0);
       bulk_commit();
     }
+  };
+  auto put = [&](int map, const float (&o)[32], int c0, int rg0) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+    put_packed(map, w, c0, rg0);
   };
 
   int it = 0;
@@ -527,7 +576,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_tempty + uint32_t(acc) * 8u);
+      if (lane == 0) mbar_arrive_remote(leader_tempty + uint32_t(acc) * 8u);
     };
     if (U.q >= 0) {  // a part: the raw accumulator, for the joining launch
       float* dst = g.partial + size_t(U.q * g.split + U.part) * (size_t(chunks) * 32 * kTile) + lane;
@@ -564,6 +613,32 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       }
     };
 
+    if constexpr (EPI == kLinStore && !SWAP) {
+      if (g.sum == nullptr && P.c_map >= 0) {
+        const float f = g.scale != nullptr ? *g.scale : 1.f;
+        const bool second = inside(2);
+#pragma unroll 1
+        for (int k = 0; k < 4; k += 2) {
+          if (!inside(k)) break;
+          uint32_t w[32];
+          __syncwarp();
+          float v0[32], v1[32];
+          tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v0);
+          tmem_ld32(t_acc + uint32_t(col_of(k) * 32 + 32), v1);
+          tmem_ld_wait();
+          // the accumulator is free as soon as it is in registers
+          if (k == 2 || !second) release();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            w[j] = pack_bf16x2(v0[2 * j] * f, v0[2 * j + 1] * f);
+            w[16 + j] = pack_bf16x2(v1[2 * j] * f, v1[2 * j + 1] * f);
+          }
+          put_wide(P.c_map, w, c_of(k), row_of(k));
+        }
+        if (!inside(0)) release();
+        continue;
+      }
+    }
     bool dead = false;
 #pragma unroll 1
     for (int k = 0; k < kChunks; ++k) {
@@ -609,8 +684,8 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= f;
         }
-        if (P.c_map >= 0) put(P.c_map, v, c0, rg0);
-        else if (r < P.rows) store_row32(P.c + (long long)r * P.c_ld + c0, n, false, v);
+        if (SWAP && P.c_map >= 0) put(P.c_map, v, c0, rg0);
+        else if (r < P.rows) store_row32(P.c + (long long)r * P.c_ld + c0, n, P.c_map >= 0, v);
       } else if constexpr (EPI == kLinGlu) {
         float a[32], b[32];
         if (SWAP) {
@@ -658,22 +733,31 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
         else glu32<DMUON_ACT_GELU_TANH>(a, b);
         put(P.c_map, a, c0, rg0);
       } else {  // kLinGluGrad
-        float v[32], ga[32], up[32];
-        if (r < P.rows) {
-          kept_values(g, kept_g, ga);
-          kept_values(g, kept_u, up);
-        } else {
+        float v[32];
+        load_acc(k, v);
+        if (r >= P.rows) kept_g = kept_u = Kept{};
+        // in halves of 16 columns, packed as they are done, to stay within the registers
+        uint32_t pg[16], pd[16], ph[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) ga[j] = up[j] = 0.f;
+        for (int half = 0; half < 2; ++half) {
+          float ga[16], up[16];
+          kept_values(g, kept_g, half, ga);
+          kept_values(g, kept_u, half, up);
+          float* vh = v + 16 * half;
+          if (g.act == DMUON_ACT_SILU) glu_grad16<DMUON_ACT_SILU>(vh, ga, up);
+          else if (g.act == DMUON_ACT_GELU) glu_grad16<DMUON_ACT_GELU>(vh, ga, up);
+          else glu_grad16<DMUON_ACT_GELU_TANH>(vh, ga, up);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            pg[8 * half + j] = pack_bf16x2(ga[2 * j], ga[2 * j + 1]);
+            pd[8 * half + j] = pack_bf16x2(vh[2 * j], vh[2 * j + 1]);
+            ph[8 * half + j] = pack_bf16x2(up[2 * j], up[2 * j + 1]);
+          }
         }
         fetch(k + 1);
-        load_acc(k, v);
-        if (g.act == DMUON_ACT_SILU) glu_grad32<DMUON_ACT_SILU>(v, ga, up);
-        else if (g.act == DMUON_ACT_GELU) glu_grad32<DMUON_ACT_GELU>(v, ga, up);
-        else glu_grad32<DMUON_ACT_GELU_TANH>(v, ga, up);
-        put(P.c_map, ga, c0, rg0);
-        put(g.map_dup, v, c0, rg0);
-        put(g.map_h, up, c0, rg0);
+        put_packed(P.c_map, pg, c0, rg0);
+        put_packed(g.map_dup, pd, c0, rg0);
+        put_packed(g.map_h, ph, c0, rg0);
       }
     }
     if (dead) break;
@@ -736,7 +820,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
 #pragma unroll
     for (int j = 0; j < kXentGroup; ++j) z[j] = 0.f;
 #pragma unroll 1
-    for (int lo = U.kb_lo; lo < U.kb_hi; lo += kRun, ++it) {
+    for (int lo = U.kb_lo; lo < U.kb_hi; lo += kRunElems / Stage<SWAP>::k, ++it) {
       const int acc = it & 1;
       int w = 1;
       if (lane == 0) w = mbar_wait_cluster(&tfull[acc], uint32_t(it >> 1) & 1u, abort_flag) ? 1 : 0;
@@ -761,7 +845,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_tempty + uint32_t(acc) * 8u);
+      if (lane == 0) mbar_arrive_remote(leader_tempty + uint32_t(acc) * 8u);
     }
     if (!ok) break;
     if constexpr (!SWAP) {
@@ -1168,6 +1252,11 @@ bool lin_swaps(long long tokens, int* nt) {
   return plain * fit * 10 < plain * kTile * 9;
 }
 
+// floor(2^32 / d) or one more: the quotient's estimate is off by one at most.
+static unsigned lin_magic(int d) {
+  return d <= 1 ? 0xFFFFFFFFu : unsigned((0x100000000ull + unsigned(d) - 1) / unsigned(d));
+}
+
 void lin_schedule(LinArgs& g, bool may_split, int clusters) {
   int tiles = 0, kb = 0;
   for (int p = 0; p < g.n_prob; ++p) {
@@ -1175,22 +1264,25 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
     tiles += g.prob[p].tiles_m * g.prob[p].tiles_n;
     const int k = g.prob[p].kb0 + g.prob[p].kb1;
     kb = p == 0 || k < kb ? k : kb;
+    g.prob[p].strip_magic = lin_magic(kStrip * g.prob[p].tiles_n);
+    g.prob[p].last_magic = lin_magic(g.prob[p].tiles_m % kStrip);
   }
   g.stages = kStages;
   if (g.swap) {
-    g.stages = kStageArea / (kOpBytes + g.nt / 2 * kK * 2);
+    g.stages = kStageArea / (kHalf * kLinKSwap * 2 + g.nt / 2 * kLinKSwap * 2);
     if (g.stages > kMaxStages) g.stages = kMaxStages;
   }
   g.full_tiles = g.total_units = tiles;
   g.split = 1;
+  g.split_magic = lin_magic(1);
   const int rest = tiles % clusters;
   if (!may_split || rest == 0) return;
-  // Microseconds of the last wave.  A K block of a 256-wide tile takes a pair 0.55;
+  // Microseconds of the last wave.  128 K-elements of a 256-wide tile take a pair 0.55;
   // of a narrow swapped one 0.75, its share of the memory's rate.  A part costs about
   // 0.3 more (the pipeline stays filled from one to the next); joining costs a launch
   // (4) and the parts' way to L2 and back (5 TB/s).
   const int cols = g.swap ? g.nt : kTile;
-  const double t_kb = g.swap ? std::max(0.75, 0.55 * cols / 256) : 0.55;
+  const double t_kb = g.swap ? 0.5 * std::max(0.75, 0.55 * cols / 256) : 0.55;
   const double part = double(cols) * kTile * sizeof(float);
   double best = kb * t_kb + 0.3;
   for (int s = 2; rest * s * part <= double(kPartialBytes) && 2 * s <= kb; ++s) {
@@ -1201,6 +1293,7 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
       g.split = s;
     }
   }
+  g.split_magic = lin_magic(g.split);
   if (g.split > 1) {
     g.full_tiles = tiles - rest;
     g.total_units = g.full_tiles + rest * g.split;

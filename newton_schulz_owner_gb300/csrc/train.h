@@ -38,6 +38,8 @@ enum LinEpi {
 };
 enum LinKeep { kKeepNone = 0, kKeepBf16 = 1, kKeepAct8 = 2 };
 
+// K-elements of a pipeline stage, the unit of kb0 and kb1 (plain and swapped).
+constexpr int kLinK = 128, kLinKSwap = 64;
 constexpr int kLinMaps = 12;     // tensor maps of one launch
 constexpr int kLinProblems = 3;  // products of one launch
 
@@ -46,6 +48,7 @@ struct LinProblem {
   int tiles_m, tiles_n;  // tile grid of the product (swapped: m counts columns, n rows)
   int kb0, kb1;          // K blocks from the first and the second operand pair
   int tile_begin;        // first tile of this product in the launch
+  unsigned strip_magic, last_magic;  // division by the tiles of a strip, by the last strip's rows
   int a0, b0, a1, b1;    // operand maps (kLinGlu: gate's weight b0, up's b1; swapped a0, a1)
   int c_map;             // output map, or -1: c is written with plain stores
   __nv_bfloat16* c;
@@ -59,6 +62,7 @@ struct LinArgs {
   int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;
+  unsigned split_magic;
   int total_units;       // full_tiles + split * (tiles - full_tiles)
   float* partial;        // fp32 parts of the split tiles
   int* err;

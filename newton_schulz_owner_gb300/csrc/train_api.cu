@@ -97,14 +97,15 @@ struct Launch {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     return n_maps++;
   }
-  // An operand stored as `rows` rows of `cols` contiguous elements; whether it
-  // is K-major or MN-major, a box is 64 columns x 128 rows (fewer for the tokens of
-  // a swapped product and for the halves of a swapped kLinGlu tile).
+  // An operand stored as `rows` rows of `cols` contiguous elements; whether it is
+  // K-major or MN-major, a box is 64 columns x 128 rows (swapped: half the tile's
+  // tokens, the stage's 64 K rows of an MN-major weight, 64 rows each of gate and up).
   int operand(const bf16* p, int64_t cols, int64_t rows, int64_t ld, int box_rows = 128) {
     return map(p, cols, rows, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   }
-  int output(const bf16* p, int64_t cols, int64_t rows, int64_t ld) {
-    return map(p, cols, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  int output(const bf16* p, int64_t cols, int64_t rows, int64_t ld, bool wide = false) {
+    return wide ? map(p, cols, rows, ld, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)
+                : map(p, cols, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   LinProblem& problem(int64_t rows, int64_t cols, int64_t k0, int64_t k1) {
     LinProblem& P = g.prob[g.n_prob++];
@@ -112,8 +113,8 @@ struct Launch {
     P.cols = int(cols);
     P.tiles_m = int(ceil_div(rows, 256));
     P.tiles_n = int(ceil_div(cols, 256));
-    P.kb0 = int(ceil_div(k0, 128));
-    P.kb1 = int(ceil_div(k1, 128));
+    P.kb0 = int(ceil_div(k0, kLinK));
+    P.kb1 = int(ceil_div(k1, kLinK));
     P.c_map = -1;
     return P;
   }
@@ -128,23 +129,26 @@ struct Launch {
       g.nt = nt;
       P.tiles_m = P.tiles_n;
       P.tiles_n = int(ceil_div(tokens, nt));
+      P.kb0 = int(ceil_div(k0, kLinKSwap));
+      P.kb1 = int(ceil_div(k1, kLinKSwap));
     }
     return P;
   }
   // Operands of a token product: the tokens' rows of K, and the weight (rows of K,
   // or for a weight read along its other axis rows of the output's columns).
   void operands(LinProblem& P, const bf16* tok, int64_t k, int64_t tok_ld, const bf16* w,
-                int64_t w_cols, int64_t w_rows, int64_t w_ld, bool second = false) {
+                int64_t w_cols, int64_t w_rows, int64_t w_ld, bool k_major, bool second = false) {
     const int t = operand(tok, k, P.rows, tok_ld, g.swap ? g.nt / 2 : 128);
-    const int m = operand(w, w_cols, w_rows, w_ld);
+    const int m = operand(w, w_cols, w_rows, w_ld, g.swap && !k_major ? kLinKSwap : 128);
     (second ? P.a1 : P.a0) = g.swap ? m : t;
     (second ? P.b1 : P.b0) = g.swap ? t : m;
   }
   // C: TMA where its rows allow it, plain stores otherwise.
-  void store_to(LinProblem& P, bf16* c, int64_t ld) {
+  void store_to(LinProblem& P, bf16* c, int64_t ld, bool store_epilogue = true) {
     P.c = c;
     P.c_ld = ld;
-    if (aligned(c, 16) && ld % 8 == 0) P.c_map = output(c, P.cols, P.rows, ld);
+    if (aligned(c, 16) && ld % 8 == 0)
+      P.c_map = output(c, P.cols, P.rows, ld, store_epilogue && !g.swap);
   }
   // Run a token product; the weight's K is contiguous (k_major) or its columns are.
   int run_token(int epi, bool k_major, int clusters, cudaStream_t s) {
@@ -280,7 +284,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     P.a1 = up;
     P.b0 = L.g.swap ? t : gate;
     P.b1 = up;
-    L.store_to(P, f.h, f8);
+    L.store_to(P, f.h, f8, false);
     use_saved(L.g, s, saved);
     if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
       L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
@@ -291,7 +295,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   }
   Launch L(f.ps);
   LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, 0);
-  L.operands(P, f.h, s.ffn, f8, w.down, s.ffn, s.hidden, w.ld_down);
+  L.operands(P, f.h, s.ffn, f8, w.down, s.ffn, s.hidden, w.ld_down, true);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
   return L.run_token(kLinStore, true, clusters, st);
 }
@@ -324,8 +328,8 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   {  // dh = dy Wd, and from it dgate, dup and h
     Launch L(f.ps);
     LinProblem& P = L.token_problem(s.tokens, s.ffn, 256, s.hidden, 0);
-    L.operands(P, dyr, s.hidden, dyr_ld, w.down, s.ffn, s.hidden, w.ld_down);
-    L.store_to(P, f.dgate, f8);
+    L.operands(P, dyr, s.hidden, dyr_ld, w.down, s.ffn, s.hidden, w.ld_down, false);
+    L.store_to(P, f.dgate, f8, false);
     L.g.dup = f.dup;
     L.g.h = f.h;
     L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, f8);
@@ -337,8 +341,8 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   {  // dx = dgate Wg + dup Wu
     Launch L(f.ps);
     LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, s.ffn);
-    L.operands(P, f.dgate, s.ffn, f8, w.gate, s.hidden, s.ffn, w.ld_in);
-    L.operands(P, f.dup, s.ffn, f8, w.up, s.hidden, s.ffn, w.ld_in, true);
+    L.operands(P, f.dgate, s.ffn, f8, w.gate, s.hidden, s.ffn, w.ld_in, false);
+    L.operands(P, f.dup, s.ffn, f8, w.up, s.hidden, s.ffn, w.ld_in, false, true);
     L.store_to(P, static_cast<bf16*>(dx), dx_ld);
     e = L.run_token(kLinStore, false, clusters, st);
     if (e != DMUON_OK) return e;
@@ -450,7 +454,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     {
       Launch L(x.ps);
       LinProblem& P = L.token_problem(n, s.vocab, 256, s.hidden, 0);
-      L.operands(P, hp, s.hidden, hr_ld, w, s.hidden, s.vocab, w_ld);
+      L.operands(P, hp, s.hidden, hr_ld, w, s.hidden, s.vocab, w_ld, true);
       if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
       L.g.target = tgt + t0;
       L.g.target_logit = x.target_logit + t0;
@@ -467,7 +471,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     {  // dhidden = G W
       Launch L(x.ps);
       LinProblem& P = L.token_problem(n, s.hidden, 256, s.vocab, 0);
-      L.operands(P, x.e, s.vocab, v8, w, s.hidden, s.vocab, w_ld);
+      L.operands(P, x.e, s.vocab, v8, w, s.hidden, s.vocab, w_ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
       L.g.scale = x.grad_scale;
       e = L.run_token(kLinStore, false, clusters, st);

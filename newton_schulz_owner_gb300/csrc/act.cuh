@@ -1,0 +1,33 @@
+// Activations of the gated feed-forward block.
+#pragma once
+#include "dmuon.h"
+#include "ptx.cuh"
+
+namespace dm {
+
+// act(x) and, for the gradient, act'(x), in fp32.
+template <int ACT>
+DM_DEV float act_value(float x) {
+  if (ACT == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
+  if (ACT == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
+  return 0.5f * x * (1.f + tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x)));
+}
+template <int ACT>
+DM_DEV void act_both(float x, float& a, float& da) {
+  if (ACT == DMUON_ACT_SILU) {
+    const float s = __fdividef(1.f, 1.f + __expf(-x));
+    a = x * s;
+    da = s * fmaf(x, 1.f - s, 1.f);
+  } else if (ACT == DMUON_ACT_GELU) {
+    const float phi = 0.5f * (1.f + erff(x * 0.70710678f));
+    a = x * phi;
+    da = fmaf(x * 0.39894228f, __expf(-0.5f * x * x), phi);
+  } else {
+    const float t = tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x));
+    const float half = 0.5f * (1.f + t);
+    a = x * half;
+    da = fmaf(0.5f * x * (1.f - t * t), 0.79788456f * fmaf(0.134145f * x, x, 1.f), half);
+  }
+}
+
+}  // namespace dm

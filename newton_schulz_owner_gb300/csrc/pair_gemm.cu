@@ -41,6 +41,7 @@
 // parallel launch adds them in order and runs the epilogue on the sums.  (Letting
 // the last arriving CTA of a tile do that in the first launch serialises the reads:
 // 12 parts of a 160 x 256 tile took 25 us longer.)
+#include "act.cuh"
 #include "act8.cuh"
 #include "dmuon.h"
 #include "epi.cuh"
@@ -279,30 +280,6 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
 }
 
 // ------------------------------------------------------------------ epilogue
-// act(x) and, for the gradient, act'(x), in fp32.
-template <int ACT>
-DM_DEV float act_value(float x) {
-  if (ACT == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
-  if (ACT == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
-  return 0.5f * x * (1.f + tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x)));
-}
-template <int ACT>
-DM_DEV void act_both(float x, float& a, float& da) {
-  if (ACT == DMUON_ACT_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-x));
-    a = x * s;
-    da = s * fmaf(x, 1.f - s, 1.f);
-  } else if (ACT == DMUON_ACT_GELU) {
-    const float phi = 0.5f * (1.f + erff(x * 0.70710678f));
-    a = x * phi;
-    da = fmaf(x * 0.39894228f, __expf(-0.5f * x * x), phi);
-  } else {
-    const float t = tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x));
-    const float half = 0.5f * (1.f + t);
-    a = x * half;
-    da = fmaf(0.5f * x * (1.f - t * t), 0.79788456f * fmaf(0.134145f * x, x, 1.f), half);
-  }
-}
 // a <- act(a) * b
 template <int ACT>
 DM_DEV void glu32(float (&a)[32], const float (&b)[32]) {
@@ -1003,24 +980,45 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ joining split tiles
-// A block of 128 threads takes one 32 x 32 chunk of a split tile (kLinGlu: gate's
+// A block of 256 threads takes one 32 x 32 chunk of a split tile (kLinGlu: gate's
 // and up's), adds the parts in order, turns it if need be, and runs the epilogue
-// with eight consecutive columns of a row per thread.  Bound by reading the parts
-// (from L2, mostly): eight columns x four parts are in flight per thread.
-DM_DEV void sum_parts(const float* p, size_t stride, int split, float (&v)[8]) {
+// with eight consecutive columns of a row per thread of its first half.  Bound by
+// the latency of reading the parts (from L2, mostly): a thread keeps its four
+// elements of eight parts in flight.
+constexpr int kJoinThreads = 256;
+DM_DEV float load_part(const float* p) {  // not moved: eight parts' loads go out together
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+DM_DEV void sum_parts(const float* p, size_t stride, int split, float (&v)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  for (int s = 0; s < split; s += 4) {
-    float t[4][8];
+  for (int j = 0; j < 4; ++j) v[j] = 0.f;
+  int s = 0;
+  for (; s + 8 <= split; s += 8) {
+    float t[8][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[k][j] = s + k < split ? __ldcg(p + (s + k) * stride + j * 32) : 0.f;
+      for (int j = 0; j < 4; ++j) t[k][j] = load_part(p + (s + k) * stride + j * 32);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += t[k][j];
+      for (int j = 0; j < 4; ++j) v[j] += t[k][j];
   }
+  float t[8][4];
+#pragma unroll
+  for (int k = 0; k < 7; ++k)
+    if (s + k < split) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[k][j] = load_part(p + (s + k) * stride + j * 32);
+    }
+#pragma unroll
+  for (int k = 0; k < 7; ++k)
+    if (s + k < split) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[k][j];
+    }
 }
 DM_DEV void store_row8(__nv_bfloat16* dst, int n, bool vec, const float (&v)[8]) {
   if (vec && n >= 8) {
@@ -1066,7 +1064,7 @@ DM_DEV void store_act8_part(signed char* codes, __nv_bfloat16* scale, int n, boo
 }
 
 template <int EPI>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ LinArgs g) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ LinArgs g) {
   __shared__ float t0[32][33], t1[EPI == kLinGlu ? 32 : 1][33];
   grid_launch_dependents();
   grid_wait();
@@ -1094,19 +1092,21 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ LinAr
   if (row0 >= P.rows || c0 >= P.cols) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t stride = size_t(chunks) * 32 * kTile;
-  const float* base = g.partial + size_t(b) * g.split * stride + warp * 256 + lane;
+  const float* base = g.partial + size_t(b) * g.split * stride + warp * 128 + lane;
   auto chunk_at = [&](int cc, int qq) { return ((size_t(rank) * chunks + cc) * 4 + qq) * 1024; };
-  float v[8], u[8];
-  sum_parts(base + chunk_at(col, q), stride, g.split, v);
+  float sv[4], su[4];
+  sum_parts(base + chunk_at(col, q), stride, g.split, sv);
   if (EPI == kLinGlu)
-    sum_parts(base + (g.swap ? chunk_at(col, q + 2) : chunk_at(col + cols, q)), stride, g.split, u);
+    sum_parts(base + (g.swap ? chunk_at(col, q + 2) : chunk_at(col + cols, q)), stride, g.split, su);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {  // v[j]: TMEM lane `lane`, column 8 warp + j
-    const int i = g.swap ? warp * 8 + j : lane, k = g.swap ? lane : warp * 8 + j;
-    t0[i][k] = v[j];
-    if (EPI == kLinGlu) t1[i][k] = u[j];
+  for (int j = 0; j < 4; ++j) {  // sv[j]: TMEM lane `lane`, column 4 warp + j
+    const int i = g.swap ? warp * 4 + j : lane, k = g.swap ? lane : warp * 4 + j;
+    t0[i][k] = sv[j];
+    if (EPI == kLinGlu) t1[i][k] = su[j];
   }
   __syncthreads();
+  if (threadIdx.x >= 128) return;
+  float v[8], u[8];
   const int tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 8;
   const int r = row0 + tr, c = c0 + tc, n = P.cols - c;
   const bool in = r < P.rows;
@@ -1245,11 +1245,15 @@ cudaError_t lin_prepare() {
   return cudaSuccess;
 }
 
-bool lin_swaps(long long tokens, int* nt) {
+// Swapped where that saves a tenth of the padded rows: at 7/8 of them it measured 3 to 7%
+// faster (block of 4096/14336, 400 to 1100 tokens), at all of them 2% slower.  The
+// cross entropy's epilogue costs more swapped: there a fifth (at 7/8 of the rows 1 to
+// 4% slower with 200 to 777 tokens, at 5/8 7% faster with 300).
+bool lin_swaps(long long tokens, int epi, int* nt) {
   const long long plain = (tokens + kTile - 1) / kTile;  // tiles of 256 tokens, either way
   const long long fit = ((tokens + plain - 1) / plain + 31) / 32 * 32;
   *nt = int(fit);
-  return plain * fit * 10 < plain * kTile * 9;
+  return epi == kLinXent ? fit * 5 < kTile * 4 : fit * 10 < kTile * 9;
 }
 
 // floor(2^32 / d) or one more: the quotient's estimate is off by one at most.
@@ -1328,7 +1332,7 @@ cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_
   return launch_dependent(epi == kLinStore ? join_kernel<kLinStore>
                           : epi == kLinGlu ? join_kernel<kLinGlu>
                                            : join_kernel<kLinGluGrad>,
-                          unsigned(blocks), 128u, s, g);
+                          unsigned(blocks), unsigned(kJoinThreads), s, g);
 }
 
 }  // namespace dm

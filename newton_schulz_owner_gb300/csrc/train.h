@@ -92,7 +92,7 @@ cudaError_t lin_prepare();  // once per device
 // total_units from the products' tile counts).
 void lin_schedule(LinArgs& g, bool may_split, int clusters);
 // Whether a product over `tokens` rows runs swapped, and its tokens per tile.
-bool lin_swaps(long long tokens, int* nt);
+bool lin_swaps(long long tokens, int epi, int* nt);
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
                        cudaStream_t s);
 
@@ -112,6 +112,17 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned thr
   cfg.numAttrs = 1;
   return counted(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
 }
+
+// ------------------------------------------------------------------ few tokens
+constexpr int kThinTokens = 8;
+struct ThinArgs {
+  const __nv_bfloat16 *x, *w0, *w1;  // w1: up's weight
+  long long x_ld, w_ld, out_ld;
+  __nv_bfloat16 *out, *gate, *up;    // gate, up: kept projections (contiguous) or null
+  int tokens, k, cols, act;
+};
+// out = x w0^T, or act(x w0^T) * (x w1^T); k a multiple of 8, rows 16-byte aligned.
+cudaError_t launch_thin(const ThinArgs& g, bool glu, cudaStream_t s);
 
 // ------------------------------------------------------------------ memory-bound kernels
 cudaError_t launch_act8_save(long long rows, long long cols, const void* x, long long ld,

@@ -119,12 +119,12 @@ struct Launch {
     return P;
   }
   // A product tokens x weight, swapped where that fits the token count better.
-  LinProblem& token_problem(int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
+  LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
                             int64_t k1) {
     LinProblem& P = problem(tokens, cols, k0, k1);
     P.tiles_n = int(ceil_div(cols, cols_per_tile));
     int nt = 0;
-    if (lin_swaps(tokens, &nt)) {
+    if (lin_swaps(tokens, epi, &nt)) {
       g.swap = 1;
       g.nt = nt;
       P.tiles_m = P.tiles_n;
@@ -274,9 +274,43 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   int64_t xr_ld;
   e = readable(static_cast<const bf16*>(x), s.tokens, s.hidden, x_ld, f.x, st, &xr, &xr_ld);
   if (e != DMUON_OK) return e;
+  // Few tokens: weights streamed without tiles (8-bit blocks span more columns than
+  // such a block computes).
+  if (s.tokens <= kThinTokens && s.hidden % 8 == 0 && s.ffn % 8 == 0 &&
+      s.save != DMUON_SAVE_ACT8) {
+    ThinArgs a{};
+    a.x = xr;
+    a.x_ld = xr_ld;
+    a.w0 = w.gate;
+    a.w1 = w.up;
+    a.w_ld = w.ld_in;
+    a.out = f.h;
+    a.out_ld = f8;
+    if (s.save == DMUON_SAVE_BF16) {
+      a.gate = static_cast<bf16*>(saved[0]);
+      a.up = static_cast<bf16*>(saved[1]);
+    }
+    a.tokens = int(s.tokens);
+    a.k = int(s.hidden);
+    a.cols = int(s.ffn);
+    a.act = s.activation;
+    ThinArgs b{};
+    b.x = f.h;
+    b.x_ld = f8;
+    b.w0 = w.down;
+    b.w_ld = w.ld_down;
+    b.out = static_cast<bf16*>(y);
+    b.out_ld = y_ld;
+    b.tokens = a.tokens;
+    b.k = int(s.ffn);
+    b.cols = int(s.hidden);
+    return launch_thin(a, true, st) == cudaSuccess && launch_thin(b, false, st) == cudaSuccess
+               ? DMUON_OK
+               : DMUON_ERR_CUDA;
+  }
   {
     Launch L(f.ps);
-    LinProblem& P = L.token_problem(s.tokens, s.ffn, 128, s.hidden, 0);
+    LinProblem& P = L.token_problem(kLinGlu, s.tokens, s.ffn, 128, s.hidden, 0);
     const int t = L.operand(xr, s.hidden, s.tokens, xr_ld, L.g.swap ? L.g.nt / 2 : 128);
     const int gate = L.operand(w.gate, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
     const int up = L.operand(w.up, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
@@ -294,7 +328,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     if (e != DMUON_OK) return e;
   }
   Launch L(f.ps);
-  LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, 0);
+  LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, 0);
   L.operands(P, f.h, s.ffn, f8, w.down, s.ffn, s.hidden, w.ld_down, true);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
   return L.run_token(kLinStore, true, clusters, st);
@@ -327,7 +361,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   if (e != DMUON_OK) return e;
   {  // dh = dy Wd, and from it dgate, dup and h
     Launch L(f.ps);
-    LinProblem& P = L.token_problem(s.tokens, s.ffn, 256, s.hidden, 0);
+    LinProblem& P = L.token_problem(kLinGluGrad, s.tokens, s.ffn, 256, s.hidden, 0);
     L.operands(P, dyr, s.hidden, dyr_ld, w.down, s.ffn, s.hidden, w.ld_down, false);
     L.store_to(P, f.dgate, f8, false);
     L.g.dup = f.dup;
@@ -340,7 +374,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   }
   {  // dx = dgate Wg + dup Wu
     Launch L(f.ps);
-    LinProblem& P = L.token_problem(s.tokens, s.hidden, 256, s.ffn, s.ffn);
+    LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, s.ffn);
     L.operands(P, f.dgate, s.ffn, f8, w.gate, s.hidden, s.ffn, w.ld_in, false);
     L.operands(P, f.dup, s.ffn, f8, w.up, s.hidden, s.ffn, w.ld_in, false, true);
     L.store_to(P, static_cast<bf16*>(dx), dx_ld);
@@ -453,7 +487,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     R.lse = lse + t0;
     {
       Launch L(x.ps);
-      LinProblem& P = L.token_problem(n, s.vocab, 256, s.hidden, 0);
+      LinProblem& P = L.token_problem(kLinXent, n, s.vocab, 256, s.hidden, 0);
       L.operands(P, hp, s.hidden, hr_ld, w, s.hidden, s.vocab, w_ld, true);
       if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
       L.g.target = tgt + t0;
@@ -470,7 +504,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     if (launch_xent_grad(R, x.e, v8, st) != cudaSuccess) return DMUON_ERR_CUDA;
     {  // dhidden = G W
       Launch L(x.ps);
-      LinProblem& P = L.token_problem(n, s.hidden, 256, s.vocab, 0);
+      LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, s.vocab, 0);
       L.operands(P, x.e, s.vocab, v8, w, s.hidden, s.vocab, w_ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
       L.g.scale = x.grad_scale;

@@ -179,7 +179,7 @@ def check_kept(dm, op, saved, fwd, c, f):
             assert np.all(np.abs(c * wide - fwd[name]) <= 0.51 * wide), name
 
 
-FFN_SHAPES = [(1, 8, 8), (1, 64, 128), (2, 100, 33), (17, 256, 129), (64, 129, 257), (65, 512, 384),
+FFN_SHAPES = [(1, 8, 8), (1, 64, 128), (3, 1032, 40), (8, 200, 1000), (5, 36, 64), (2, 100, 33), (17, 256, 129), (64, 129, 257), (65, 512, 384),
               (255, 72, 100), (256, 128, 128), (257, 520, 136), (513, 264, 640), (300, 1000, 2050),
               (33, 4096, 330), (97, 2048, 900), (250, 2900, 520), (700, 640, 1100)]
 

@@ -5,12 +5,13 @@
 
 namespace dm {
 
-// act(x) and, for the gradient, act'(x), in fp32.
+// act(x) and, for the gradient, act'(x), in fp32.  The tanh form is taken as
+// x * sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)): (1 + tanh y) / 2 = sigmoid(2 y).
 template <int ACT>
 DM_DEV float act_value(float x) {
   if (ACT == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
   if (ACT == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
-  return 0.5f * x * (1.f + tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x)));
+  return x * __fdividef(1.f, 1.f + __expf(-1.59576912f * fmaf(0.044715f * x * x, x, x)));
 }
 template <int ACT>
 DM_DEV void act_both(float x, float& a, float& da) {
@@ -23,10 +24,9 @@ DM_DEV void act_both(float x, float& a, float& da) {
     a = x * phi;
     da = fmaf(x * 0.39894228f, __expf(-0.5f * x * x), phi);
   } else {
-    const float t = tanhf(0.79788456f * fmaf(0.044715f * x * x, x, x));
-    const float half = 0.5f * (1.f + t);
-    a = x * half;
-    da = fmaf(0.5f * x * (1.f - t * t), 0.79788456f * fmaf(0.134145f * x, x, 1.f), half);
+    const float s = __fdividef(1.f, 1.f + __expf(-1.59576912f * fmaf(0.044715f * x * x, x, x)));
+    a = x * s;
+    da = fmaf(x * s * (1.f - s), 1.59576912f * fmaf(0.134145f * x, x, 1.f), s);
   }
 }
 

@@ -326,11 +326,10 @@ DM_DEV void unpack8(const uint4& q, float* f) {
   }
 }
 
-// One row's block of 32 fp32 values in 8 bits; values past n are not written.  The
+// One row's block of 32 fp32 values in 8 bits; values past n count as zeros.  The
 // quotient is taken with the scale's rounded reciprocal: within 2e-5 of a step, far
 // below what the accumulation of the values leaves uncertain.
-DM_DEV void store_act8(signed char* codes, __nv_bfloat16* scale, int n, bool vec,
-                       float (&v)[32]) {
+DM_DEV float act8_block(float (&v)[32], int n, uint32_t (&w)[8]) {
   if (n < 32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -344,7 +343,6 @@ DM_DEV void store_act8(signed char* codes, __nv_bfloat16* scale, int n, bool vec
   }
   const float s = act8_scale(top, bad == 0.f);
   const float r = bad == 0.f && s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-  uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     uint32_t c[4];
@@ -352,15 +350,7 @@ DM_DEV void store_act8(signed char* codes, __nv_bfloat16* scale, int n, bool vec
     for (int k = 0; k < 4; ++k) c[k] = act8_code_fast(bad == 0.f ? v[4 * j + k] : 0.f, r);
     w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }
-  if (vec && n >= 32) {
-    reinterpret_cast<uint4*>(codes)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(codes)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) codes[j] = (signed char)(w[j / 4] >> (8 * (j & 3)));
-  }
-  *scale = __float2bfloat16_rn(s);
+  return s;
 }
 
 // 32 kept values of one row (columns c0 .. c0 + 31, n of them inside), fetched as
@@ -503,6 +493,34 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
     put_packed(map, w, c0, rg0);
+  };
+  // and one in 8 bits: the codes by TMA too (32-byte rows; written by the lanes, they
+  // would be 64 scattered pieces), the scales as they are
+  auto put_act8 = [&](int map, void* codes, __nv_bfloat16* scales, float (&o)[32], int c0, int rg0,
+                      int n, bool in) {
+    uint32_t w[8];
+    const float s = act8_block(o, n, w);
+    const long long row = rg0 + lane;
+    if (in)
+      scales[row * ((g.ffn + kActBlock - 1) / kActBlock) + c0 / kActBlock] = __float2bfloat16_rn(s);
+    if (g.kept_vec) {
+      const uint32_t buf = buf0 + uint32_t((stored++ & 1) * kEpiBufBytes);
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+      st_shared_v4(buf + uint32_t(lane * 32), w[0], w[1], w[2], w[3]);
+      st_shared_v4(buf + uint32_t(lane * 32 + 16), w[4], w[5], w[6], w[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&g.maps[map], buf, c0, rg0);
+        bulk_commit();
+      }
+    } else if (in) {
+      signed char* dst = static_cast<signed char*>(codes) + row * g.ffn + c0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) dst[j] = (signed char)(w[j / 4] >> (8 * (j & 3)));
+    }
   };
 
   int it = 0;
@@ -666,7 +684,8 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       } else if constexpr (EPI == kLinGlu) {
         float a[32], b[32];
         if (SWAP) {
-          // gate's rows are the TMEM lanes of quarters 0 and 1, up's those of 2 and 3
+          // gate's rows are the TMEM lanes of quarters 0 and 1, up's those of 2 and 3, whose
+          // warp turns its chunk for the other one
           if (q >= 2) {
             load_raw(k, a);
             turn_write(turn, lane, a);
@@ -680,6 +699,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
           dead = !wait_warp(ho.ready, ho.parity);
           ho.parity ^= 1u;
           if (dead) break;
+          // quarter q's warp is number (q + 2) % 4 of its half: the partner's is number q
           turn_read(reinterpret_cast<const float*>(epi + (h * 4 + q) * 2 * kEpiBufBytes), lane, b);
           arrive_warp(ho.taken);
         } else {
@@ -695,13 +715,9 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
             store_row32(static_cast<__nv_bfloat16*>(g.gate) + at, n, false, a);
             store_row32(static_cast<__nv_bfloat16*>(g.up) + at, n, false, b);
           }
-        } else if (g.keep == kKeepAct8 && r < P.rows) {
-          const long long at = (long long)r * g.ffn + c0;
-          const long long sa =
-              (long long)r * ((g.ffn + kActBlock - 1) / kActBlock) + c0 / kActBlock;
-          store_act8(static_cast<signed char*>(g.gate) + at, g.gate_scale + sa, n,
-                     g.kept_vec != 0, a);
-          store_act8(static_cast<signed char*>(g.up) + at, g.up_scale + sa, n, g.kept_vec != 0, b);
+        } else if (g.keep == kKeepAct8) {
+          put_act8(g.map_gate, g.gate, g.gate_scale, a, c0, rg0, n, r < P.rows);
+          put_act8(g.map_up, g.up, g.up_scale, b, c0, rg0, n, r < P.rows);
         }
         // one loop per activation: the three side by side in one loop overflow the
         // instruction cache
@@ -1281,17 +1297,20 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
   g.split_magic = lin_magic(1);
   const int rest = tiles % clusters;
   if (!may_split || rest == 0) return;
-  // Microseconds of the last wave.  128 K-elements of a 256-wide tile take a pair 0.55;
-  // of a narrow swapped one 0.75, its share of the memory's rate.  A part costs about
-  // 0.3 more (the pipeline stays filled from one to the next); joining costs a launch
-  // (4) and the parts' way to L2 and back (5 TB/s).
+  // Microseconds of the last wave.  Per 128 K-elements a pair moves 64 KB plus 256
+  // bytes per column of its tile through each SM's shared memory (in by TMA, out to the
+  // tensor core) at about 243 GB/s: 0.54 for 256 columns.  With few tokens the weights'
+  // way from HBM takes longer, 0.75 shared by the token tiles that use them.  A part
+  // costs about 0.3 more (the pipeline stays filled from one to the next); joining costs
+  // a launch (3) and the parts' way to L2 and back (5 TB/s).
   const int cols = g.swap ? g.nt : kTile;
-  const double t_kb = g.swap ? 0.5 * std::max(0.75, 0.55 * cols / 256) : 0.55;
+  double t_kb = (65536 + 256.0 * cols) / 243e3;
+  if (g.swap) t_kb = 0.5 * std::max(t_kb, 0.75 / g.prob[0].tiles_n);
   const double part = double(cols) * kTile * sizeof(float);
   double best = kb * t_kb + 0.3;
   for (int s = 2; rest * s * part <= double(kPartialBytes) && 2 * s <= kb; ++s) {
     const int waves = (rest * s + clusters - 1) / clusters;
-    const double cost = waves * ((kb + s - 1) / s * t_kb + 0.3) + 4 + 2 * rest * s * part / 5e6;
+    const double cost = waves * ((kb + s - 1) / s * t_kb + 0.3) + 3 + 2 * rest * s * part / 5e6;
     if (cost < best) {
       best = cost;
       g.split = s;

@@ -82,17 +82,18 @@ struct Launch {
     g.partial = s.partial;
   }
   int map(const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols, int box_rows,
-          CUtensorMapSwizzle swizzle) {
+          CUtensorMapSwizzle swizzle, int elem = 2) {
     const TensorMapEncode enc = library_tensor_map_encoder();
     if (enc == nullptr || n_maps >= kLinMaps) {
       ok = false;
       return 0;
     }
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * cuuint64_t(elem)};
     const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)}, es[2] = {1, 1};
-    ok = ok && enc(&g.maps[n_maps], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+    ok = ok && enc(&g.maps[n_maps],
+                   elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     return n_maps++;
@@ -106,6 +107,9 @@ struct Launch {
   int output(const bf16* p, int64_t cols, int64_t rows, int64_t ld, bool wide = false) {
     return wide ? map(p, cols, rows, ld, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)
                 : map(p, cols, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  int output_codes(const void* p, int64_t cols, int64_t rows) {
+    return map(p, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE, 1);
   }
   LinProblem& problem(int64_t rows, int64_t cols, int64_t k0, int64_t k1) {
     LinProblem& P = g.prob[g.n_prob++];
@@ -323,6 +327,9 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
       L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
       L.g.map_up = L.output(static_cast<bf16*>(L.g.up), s.ffn, s.tokens, s.ffn);
+    } else if (L.g.keep == kKeepAct8 && L.g.kept_vec) {
+      L.g.map_gate = L.output_codes(L.g.gate, s.ffn, s.tokens);
+      L.g.map_up = L.output_codes(L.g.up, s.ffn, s.tokens);
     }
     e = L.run_token(kLinGlu, true, clusters, st);
     if (e != DMUON_OK) return e;

@@ -944,6 +944,8 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kLinMaps && int(threadIdx.x) - 64 < g.n_maps)
+    prefetch_tensormap(&g.maps[threadIdx.x - 64]);
   if (threadIdx.x == 0) {
     for (int b = 0; b < 8; ++b) mbar_init(&pair_bar[b], 1);  // one lane of a warp
     for (int s = 0; s < kMaxStages; ++s) {

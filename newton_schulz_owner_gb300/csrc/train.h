@@ -58,7 +58,7 @@ struct LinProblem {
 struct LinArgs {
   CUtensorMap maps[kLinMaps];
   LinProblem prob[kLinProblems];
-  int n_prob;
+  int n_prob, n_maps;
   int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;

@@ -160,6 +160,7 @@ struct Launch {
   }
   int run(int epi, bool a_mn, bool b_mn, int clusters, cudaStream_t s) {
     if (!ok) return DMUON_ERR_CUDA;
+    g.n_maps = n_maps;
     lin_schedule(g, epi != kLinXent, clusters);
     return launch_lin(g, epi, a_mn, b_mn, clusters, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
   }

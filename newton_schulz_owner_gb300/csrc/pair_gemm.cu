@@ -300,22 +300,6 @@ DM_DEV void glu_grad16(float* v, float (&ga)[16], float (&up)[16]) {
   }
 }
 
-// 32 values of one row, as bf16, at dst: 16-byte stores where allowed.
-DM_DEV void store_row32(__nv_bfloat16* dst, int n, bool vec, const float (&v)[32]) {
-  if (vec && n >= 32) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      reinterpret_cast<uint4*>(dst)[u] =
-          make_uint4(pack_bf16x2(v[8 * u], v[8 * u + 1]), pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
-                     pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
-                     pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
-  }
-}
-
 DM_DEV void unpack8(const uint4& q, float* f) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -488,6 +472,22 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       bulk_commit();
     }
   };
+  // Where rows are not 16-byte aligned TMA cannot write them: the chunk still goes
+  // through shared memory, and the warp writes it row by row, 64 bytes at a time.
+  auto put_plain = [&](__nv_bfloat16* dst, long long ld, const float (&o)[32], int c0, int rg0,
+                       int rows, int n) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    epi_store_row(buf0, lane, o);
+    __syncwarp();
+    const int last = min(32, rows - rg0);
+    dst += (long long)rg0 * ld + c0 + lane;
+    if (lane < n)
+      for (int i = 0; i < last; ++i)
+        reinterpret_cast<uint16_t*>(dst)[i * ld] = ld_shared_b16(
+            buf0 + epi_off(i, lane >> 3) + uint32_t((lane & 7) * 2));
+    __syncwarp();
+  };
   auto put = [&](int map, const float (&o)[32], int c0, int rg0) {
     uint32_t w[16];
 #pragma unroll
@@ -515,11 +515,18 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
         tma_store_2d(&g.maps[map], buf, c0, rg0);
         bulk_commit();
       }
-    } else if (in) {
-      signed char* dst = static_cast<signed char*>(codes) + row * g.ffn + c0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) dst[j] = (signed char)(w[j / 4] >> (8 * (j & 3)));
+    } else {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      st_shared_v4(buf0 + uint32_t(lane * 32), w[0], w[1], w[2], w[3]);
+      st_shared_v4(buf0 + uint32_t(lane * 32 + 16), w[4], w[5], w[6], w[7]);
+      __syncwarp();
+      const unsigned rows = __popc(__ballot_sync(0xffffffffu, in));
+      signed char* dst = static_cast<signed char*>(codes) + (long long)rg0 * g.ffn + c0 + lane;
+      const signed char* src = reinterpret_cast<const signed char*>(turn) + lane;
+      if (lane < n)
+        for (unsigned i = 0; i < rows; ++i) dst[(long long)i * g.ffn] = src[i * 32];
+      __syncwarp();
     }
   };
 
@@ -680,7 +687,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
           for (int j = 0; j < 32; ++j) v[j] *= f;
         }
         if (SWAP && P.c_map >= 0) put(P.c_map, v, c0, rg0);
-        else if (r < P.rows) store_row32(P.c + (long long)r * P.c_ld + c0, n, P.c_map >= 0, v);
+        else put_plain(P.c, P.c_ld, v, c0, rg0, P.rows, n);
       } else if constexpr (EPI == kLinGlu) {
         float a[32], b[32];
         if (SWAP) {
@@ -710,10 +717,9 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
           if (g.kept_vec) {
             put(g.map_gate, a, c0, rg0);
             put(g.map_up, b, c0, rg0);
-          } else if (r < P.rows) {
-            const long long at = (long long)r * g.ffn + c0;
-            store_row32(static_cast<__nv_bfloat16*>(g.gate) + at, n, false, a);
-            store_row32(static_cast<__nv_bfloat16*>(g.up) + at, n, false, b);
+          } else {
+            put_plain(static_cast<__nv_bfloat16*>(g.gate), g.ffn, a, c0, rg0, P.rows, n);
+            put_plain(static_cast<__nv_bfloat16*>(g.up), g.ffn, b, c0, rg0, P.rows, n);
           }
         } else if (g.keep == kKeepAct8) {
           put_act8(g.map_gate, g.gate, g.gate_scale, a, c0, rg0, n, r < P.rows);

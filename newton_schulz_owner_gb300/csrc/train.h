@@ -131,14 +131,33 @@ cudaError_t launch_act8_save(long long rows, long long cols, const void* x, long
 cudaError_t launch_act8_load(long long rows, long long cols, const signed char* codes,
                              const __nv_bfloat16* scales, void* out, long long ld, bool bf16,
                              cudaStream_t s);
-// Copy rows x cols bf16 to rows of pitch `dst_ld` (a multiple of 8); a row whose
-// target lies outside [0, vocab) is written as zeros when `target` is given.
-cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16* src,
-                             long long src_ld, __nv_bfloat16* dst, long long dst_ld,
-                             const long long* target, long long vocab, cudaStream_t s);
-// Rows rows x cols of zeros (pitch ld).
-cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst, long long ld,
-                             cudaStream_t s);
+// Copies of bf16 matrices (src null: zeros), one launch; with `target`, rows of the
+// first whose target lies outside [0, vocab) become zeros.
+struct CopyArgs {
+  static constexpr int kMost = 5;
+  struct Mat {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    long long rows, cols, src_ld, dst_ld;
+    unsigned block_begin;
+    int src_vec, dst_vec;  // 16-byte aligned rows
+  };
+  Mat mat[kMost];
+  int n;
+  const long long* target;
+  long long vocab;
+  void add(const __nv_bfloat16* src, long long src_ld, __nv_bfloat16* dst, long long dst_ld,
+           long long rows, long long cols) {
+    Mat& M = mat[n++];
+    M.src = src;
+    M.dst = dst;
+    M.rows = rows;
+    M.cols = cols;
+    M.src_ld = src_ld;
+    M.dst_ld = dst_ld;
+  }
+};
+cudaError_t launch_copy_rows(CopyArgs& g, cudaStream_t s);
 struct XentRows {
   long long tokens, vocab;
   const long long* target;

@@ -166,19 +166,19 @@ struct Launch {
   }
 };
 
-// A bf16 matrix as TMA can read it: where it lies, or copied to `copy`.
-int readable(const bf16* p, int64_t rows, int64_t cols, int64_t ld, bf16* copy, cudaStream_t s,
-             const bf16** out, int64_t* out_ld) {
-  if (aligned(p, 16) && ld % 8 == 0) {
-    *out = p;
-    *out_ld = ld;
-    return DMUON_OK;
-  }
-  *out = copy;
-  *out_ld = up8(cols);
-  return launch_copy_rows(rows, cols, p, ld, copy, *out_ld, nullptr, 0, s) == cudaSuccess
-             ? DMUON_OK
-             : DMUON_ERR_CUDA;
+// A bf16 matrix as TMA can read it: where it lies, or (noted in `c`) copied to `copy`.
+struct Readable {
+  const bf16* p;
+  int64_t ld;
+};
+Readable readable(CopyArgs& c, const void* p, int64_t rows, int64_t cols, int64_t ld, bf16* copy) {
+  const bf16* src = static_cast<const bf16*>(p);
+  if (aligned(src, 16) && ld % 8 == 0) return {src, ld};
+  c.add(src, ld, copy, up8(cols), rows, cols);
+  return {copy, up8(cols)};
+}
+int run_copies(CopyArgs& c, cudaStream_t s) {
+  return c.n == 0 || launch_copy_rows(c, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ feed-forward block
@@ -216,20 +216,13 @@ FfnSpace ffn_space(const dmuon_ffn_shape& s, bool backward, void* ws) {
 }
 
 struct FfnWeights {
-  const bf16 *gate, *up, *down;
-  int64_t ld_in, ld_down;  // row pitch of gate and up, of down
+  Readable gate, up, down;
 };
-int ffn_weights(const dmuon_ffn_shape& s, const FfnSpace& f, const void* wg, const void* wu,
-                const void* wd, cudaStream_t st, FfnWeights* w) {
-  int e = readable(static_cast<const bf16*>(wg), s.ffn, s.hidden, s.hidden, f.w_gate, st, &w->gate,
-                   &w->ld_in);
-  if (e == DMUON_OK)
-    e = readable(static_cast<const bf16*>(wu), s.ffn, s.hidden, s.hidden, f.w_up, st, &w->up,
-                 &w->ld_in);
-  if (e == DMUON_OK)
-    e = readable(static_cast<const bf16*>(wd), s.hidden, s.ffn, s.ffn, f.w_down, st, &w->down,
-                 &w->ld_down);
-  return e;
+FfnWeights ffn_weights(CopyArgs& c, const dmuon_ffn_shape& s, const FfnSpace& f, const void* wg,
+                       const void* wu, const void* wd) {
+  return {readable(c, wg, s.ffn, s.hidden, s.hidden, f.w_gate),
+          readable(c, wu, s.ffn, s.hidden, s.hidden, f.w_up),
+          readable(c, wd, s.hidden, s.ffn, s.ffn, f.w_down)};
 }
 
 // saved[] = {gate, up} in bf16, or {gate codes, gate scales, up codes, up scales}
@@ -272,23 +265,23 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   if (e != DMUON_OK) return e;
   const FfnSpace f = ffn_space(s, false, ws);
   const int64_t f8 = up8(s.ffn);
-  FfnWeights w;
-  e = ffn_weights(s, f, wg, wu, wd, st, &w);
+  CopyArgs copies{};
+  const FfnWeights w = ffn_weights(copies, s, f, wg, wu, wd);
+  const Readable xr = readable(copies, x, s.tokens, s.hidden, x_ld, f.x);
+  e = run_copies(copies, st);
   if (e != DMUON_OK) return e;
-  const bf16* xr;
-  int64_t xr_ld;
-  e = readable(static_cast<const bf16*>(x), s.tokens, s.hidden, x_ld, f.x, st, &xr, &xr_ld);
-  if (e != DMUON_OK) return e;
-  // Few tokens: weights streamed without tiles (8-bit blocks span more columns than
-  // such a block computes).
+  // Few tokens: weights streamed without tiles: one token through 4096/14336 61 us
+  // against 75 with tiles, eight 62 against 75 (with 16 or 32, sharing the weights'
+  // registers among more tokens, 89 and 138 against 76).  8-bit blocks span more columns
+  // than a block computes.
   if (s.tokens <= kThinTokens && s.hidden % 8 == 0 && s.ffn % 8 == 0 &&
       s.save != DMUON_SAVE_ACT8) {
     ThinArgs a{};
-    a.x = xr;
-    a.x_ld = xr_ld;
-    a.w0 = w.gate;
-    a.w1 = w.up;
-    a.w_ld = w.ld_in;
+    a.x = xr.p;
+    a.x_ld = xr.ld;
+    a.w0 = w.gate.p;
+    a.w1 = w.up.p;
+    a.w_ld = w.gate.ld;
     a.out = f.h;
     a.out_ld = f8;
     if (s.save == DMUON_SAVE_BF16) {
@@ -302,8 +295,8 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     ThinArgs b{};
     b.x = f.h;
     b.x_ld = f8;
-    b.w0 = w.down;
-    b.w_ld = w.ld_down;
+    b.w0 = w.down.p;
+    b.w_ld = w.down.ld;
     b.out = static_cast<bf16*>(y);
     b.out_ld = y_ld;
     b.tokens = a.tokens;
@@ -316,9 +309,9 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   {
     Launch L(f.ps);
     LinProblem& P = L.token_problem(kLinGlu, s.tokens, s.ffn, 128, s.hidden, 0);
-    const int t = L.operand(xr, s.hidden, s.tokens, xr_ld, L.g.swap ? L.g.nt / 2 : 128);
-    const int gate = L.operand(w.gate, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
-    const int up = L.operand(w.up, s.hidden, s.ffn, w.ld_in, L.g.swap ? 64 : 128);
+    const int t = L.operand(xr.p, s.hidden, s.tokens, xr.ld, L.g.swap ? L.g.nt / 2 : 128);
+    const int gate = L.operand(w.gate.p, s.hidden, s.ffn, w.gate.ld, L.g.swap ? 64 : 128);
+    const int up = L.operand(w.up.p, s.hidden, s.ffn, w.up.ld, L.g.swap ? 64 : 128);
     P.a0 = L.g.swap ? gate : t;
     P.a1 = up;
     P.b0 = L.g.swap ? t : gate;
@@ -337,7 +330,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   }
   Launch L(f.ps);
   LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, 0);
-  L.operands(P, f.h, s.ffn, f8, w.down, s.ffn, s.hidden, w.ld_down, true);
+  L.operands(P, f.h, s.ffn, f8, w.down.p, s.ffn, s.hidden, w.down.ld, true);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
   return L.run_token(kLinStore, true, clusters, st);
 }
@@ -350,27 +343,24 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   int e = device_ready(&clusters);
   if (e != DMUON_OK) return e;
   if (s.tokens == 0) {  // sums over no token
-    if (launch_zero_rows(s.ffn, s.hidden, static_cast<bf16*>(dwg), s.hidden, st) != cudaSuccess ||
-        launch_zero_rows(s.ffn, s.hidden, static_cast<bf16*>(dwu), s.hidden, st) != cudaSuccess ||
-        launch_zero_rows(s.hidden, s.ffn, static_cast<bf16*>(dwd), s.ffn, st) != cudaSuccess)
-      return DMUON_ERR_CUDA;
-    return DMUON_OK;
+    CopyArgs zeros{};
+    zeros.add(nullptr, 8, static_cast<bf16*>(dwg), s.hidden, s.ffn, s.hidden);
+    zeros.add(nullptr, 8, static_cast<bf16*>(dwu), s.hidden, s.ffn, s.hidden);
+    zeros.add(nullptr, 8, static_cast<bf16*>(dwd), s.ffn, s.hidden, s.ffn);
+    return run_copies(zeros, st);
   }
   const FfnSpace f = ffn_space(s, true, ws);
   const int64_t f8 = up8(s.ffn);
-  FfnWeights w;
-  e = ffn_weights(s, f, wg, wu, wd, st, &w);
-  if (e != DMUON_OK) return e;
-  const bf16 *xr, *dyr;
-  int64_t xr_ld, dyr_ld;
-  e = readable(static_cast<const bf16*>(x), s.tokens, s.hidden, x_ld, f.x, st, &xr, &xr_ld);
-  if (e == DMUON_OK)
-    e = readable(static_cast<const bf16*>(dy), s.tokens, s.hidden, dy_ld, f.dy, st, &dyr, &dyr_ld);
+  CopyArgs copies{};
+  const FfnWeights w = ffn_weights(copies, s, f, wg, wu, wd);
+  const Readable xr = readable(copies, x, s.tokens, s.hidden, x_ld, f.x);
+  const Readable dyr = readable(copies, dy, s.tokens, s.hidden, dy_ld, f.dy);
+  e = run_copies(copies, st);
   if (e != DMUON_OK) return e;
   {  // dh = dy Wd, and from it dgate, dup and h
     Launch L(f.ps);
     LinProblem& P = L.token_problem(kLinGluGrad, s.tokens, s.ffn, 256, s.hidden, 0);
-    L.operands(P, dyr, s.hidden, dyr_ld, w.down, s.ffn, s.hidden, w.ld_down, false);
+    L.operands(P, dyr.p, s.hidden, dyr.ld, w.down.p, s.ffn, s.hidden, w.down.ld, false);
     L.store_to(P, f.dgate, f8, false);
     L.g.dup = f.dup;
     L.g.h = f.h;
@@ -383,21 +373,21 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   {  // dx = dgate Wg + dup Wu
     Launch L(f.ps);
     LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, s.ffn);
-    L.operands(P, f.dgate, s.ffn, f8, w.gate, s.hidden, s.ffn, w.ld_in, false);
-    L.operands(P, f.dup, s.ffn, f8, w.up, s.hidden, s.ffn, w.ld_in, false, true);
+    L.operands(P, f.dgate, s.ffn, f8, w.gate.p, s.hidden, s.ffn, w.gate.ld, false);
+    L.operands(P, f.dup, s.ffn, f8, w.up.p, s.hidden, s.ffn, w.up.ld, false, true);
     L.store_to(P, static_cast<bf16*>(dx), dx_ld);
     e = L.run_token(kLinStore, false, clusters, st);
     if (e != DMUON_OK) return e;
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
   Launch L(f.ps);
-  const int mx = L.operand(xr, s.hidden, s.tokens, xr_ld);
-  const bf16* left[3] = {f.dgate, f.dup, dyr};
+  const int mx = L.operand(xr.p, s.hidden, s.tokens, xr.ld);
+  const bf16* left[3] = {f.dgate, f.dup, dyr.p};
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
     LinProblem& P = L.problem(m, n, s.tokens, 0);
-    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? f8 : dyr_ld);
+    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? f8 : dyr.ld);
     P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, f8);
     L.store_to(P, out[i], n);
   }
@@ -460,28 +450,27 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
   const XentSpace x = xent_space(s, grads, ws);
   const int64_t v8 = up8(s.vocab);
   const long long* tgt = reinterpret_cast<const long long*>(target);
-  const bf16 *w, *h;
-  int64_t w_ld, hr_ld;
-  e = readable(static_cast<const bf16*>(weight), s.vocab, s.hidden, s.hidden, x.weight, st, &w,
-               &w_ld);
-  if (e != DMUON_OK) return e;
+  CopyArgs copies{};
+  Readable h;
   if (grads) {
     // masked rows become zeros, so that nothing they hold (NaN of padding, say)
     // reaches the weight's gradient, which sums over rows
-    hr_ld = up8(s.hidden);
-    if (launch_copy_rows(s.tokens, s.hidden, static_cast<const bf16*>(hidden), h_ld, x.hidden,
-                         hr_ld, tgt, s.vocab, st) != cudaSuccess ||
-        launch_grad_scale(grad_loss, tgt, s.tokens, s.vocab, x.grad_scale, st) != cudaSuccess)
-      return DMUON_ERR_CUDA;
-    h = x.hidden;
+    copies.target = tgt;
+    copies.vocab = s.vocab;
+    h = {x.hidden, up8(s.hidden)};
+    copies.add(static_cast<const bf16*>(hidden), h_ld, x.hidden, h.ld, s.tokens, s.hidden);
   } else {
-    e = readable(static_cast<const bf16*>(hidden), s.tokens, s.hidden, h_ld, x.hidden, st, &h,
-                 &hr_ld);
-    if (e != DMUON_OK) return e;
+    h = readable(copies, hidden, s.tokens, s.hidden, h_ld, x.hidden);
   }
+  const Readable w = readable(copies, weight, s.vocab, s.hidden, s.hidden, x.weight);
+  e = run_copies(copies, st);
+  if (e != DMUON_OK) return e;
+  if (grads &&
+      launch_grad_scale(grad_loss, tgt, s.tokens, s.vocab, x.grad_scale, st) != cudaSuccess)
+    return DMUON_ERR_CUDA;
   for (int64_t t0 = 0; t0 < s.tokens; t0 += x.piece) {
     const int64_t n = std::min(x.piece, s.tokens - t0);
-    const bf16* hp = h + t0 * hr_ld;
+    const bf16* hp = h.p + t0 * h.ld;
     XentRows R{};
     R.tokens = n;
     R.vocab = s.vocab;
@@ -496,7 +485,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     {
       Launch L(x.ps);
       LinProblem& P = L.token_problem(kLinXent, n, s.vocab, 256, s.hidden, 0);
-      L.operands(P, hp, s.hidden, hr_ld, w, s.hidden, s.vocab, w_ld, true);
+      L.operands(P, hp, s.hidden, h.ld, w.p, s.hidden, s.vocab, w.ld, true);
       if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
       L.g.target = tgt + t0;
       L.g.target_logit = x.target_logit + t0;
@@ -513,7 +502,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     {  // dhidden = G W
       Launch L(x.ps);
       LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, s.vocab, 0);
-      L.operands(P, x.e, s.vocab, v8, w, s.hidden, s.vocab, w_ld, false);
+      L.operands(P, x.e, s.vocab, v8, w.p, s.hidden, s.vocab, w.ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
       L.g.scale = x.grad_scale;
       e = L.run_token(kLinStore, false, clusters, st);
@@ -523,7 +512,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     Launch L(x.ps);
     LinProblem& P = L.problem(s.vocab, s.hidden, n, 0);
     P.a0 = L.operand(x.e, s.vocab, n, v8);
-    P.b0 = L.operand(hp, s.hidden, n, hr_ld);
+    P.b0 = L.operand(hp, s.hidden, n, h.ld);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
     L.g.scale = x.grad_scale;
     L.g.sum = x.sum;
@@ -650,10 +639,9 @@ int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden
     int clusters = 0;
     const int st = device_ready(&clusters);
     if (st != DMUON_OK) return st;
-    return launch_zero_rows(shape->vocab, shape->hidden, static_cast<bf16*>(dweight),
-                            shape->hidden, stream) == cudaSuccess
-               ? DMUON_OK
-               : DMUON_ERR_CUDA;
+    CopyArgs zeros{};
+    zeros.add(nullptr, 8, static_cast<bf16*>(dweight), shape->hidden, shape->vocab, shape->hidden);
+    return run_copies(zeros, stream);
   }
   if (shape->tokens == 0) return DMUON_OK;
   return xent(*shape, hidden, hidden_ld, weight, target, grad_loss, loss, lse, dhidden, dhidden_ld,

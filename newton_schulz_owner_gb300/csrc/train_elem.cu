@@ -217,30 +217,74 @@ DM_DEV bool live_target(const long long* target, long long row, long long vocab)
   return t >= 0 && t < vocab;
 }
 
-// src == nullptr: zeros.
-__global__ void __launch_bounds__(kThreads) copy_rows_kernel(long long cols, long long tiles,
-                                                             const __nv_bfloat16* src,
-                                                             long long src_ld,
-                                                             __nv_bfloat16* dst, long long dst_ld,
-                                                             const long long* target,
-                                                             long long vocab, bool vec_in,
-                                                             bool vec_out) {
+// Eight bf16 elements at p, which is 2-byte aligned, from the two 16-byte words around
+// them.
+DM_DEV uint4 load8_shifted(const __nv_bfloat16* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const unsigned skip = unsigned(at & 15u);  // bytes, even
+  const uint4* q = reinterpret_cast<const uint4*>(at - skip);
+  const uint4 lo = q[0];
+  if (skip == 0) return lo;
+  const uint4 hi = q[1];
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const unsigned bits = (skip & 3u) * 8u;
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t a = 0, b = 0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (skip / 4 == unsigned(s)) {
+        a = w[k + s];
+        b = w[k + s + 1];
+      }
+    o[k] = __funnelshift_r(a, b, bits);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Up to CopyArgs::kMost matrices to rows that TMA can read, one launch.  A thread
+// moves 8 columns; the threads run through rows and columns alike, so that narrow
+// matrices fill them too.  src == nullptr: zeros.
+__global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_constant__ CopyArgs g) {
   grid_launch_dependents();
   grid_wait();
-  const long long row = blockIdx.x / tiles;
-  const long long c0 = (blockIdx.x - row * tiles) * kVecCols + threadIdx.x * 8;
-  if (c0 >= cols) return;
-  const int n = int(min(8ll, cols - c0));
-  float f[8] = {};
-  if (src != nullptr && live_target(target, row, vocab))
-    load8<true>(src, row * src_ld + c0, vec_in, n, f);
-  __nv_bfloat16* d = dst + row * dst_ld + c0;
-  if (vec_out && n >= 8) {
-    *reinterpret_cast<uint4*>(d) = pack8(f);
-  } else {
+  int m = 0;
+  while (m + 1 < g.n && blockIdx.x >= g.mat[m + 1].block_begin) ++m;
+  const CopyArgs::Mat& M = g.mat[m];
+  const unsigned per_row = unsigned((M.cols + 7) / 8);
+  const unsigned long long u0 =
+      (unsigned long long)(blockIdx.x - M.block_begin) * (4 * kThreads) + threadIdx.x;
+  const unsigned long long units = (unsigned long long)M.rows * per_row;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) d[k] = __float2bfloat16_rn(f[k]);
+  for (int k = 0; k < 4; ++k) {
+    const unsigned long long u = u0 + k * kThreads;
+    if (u >= units) return;
+    const long long row = units <= 0xFFFFFFFFull ? (long long)(unsigned(u) / per_row)
+                                                 : (long long)(u / per_row);
+    const long long c0 = ((long long)u - row * per_row) * 8;
+    const int n = int(min(8ll, M.cols - c0));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (M.src != nullptr && (m > 0 || live_target(g.target, row, g.vocab))) {
+      const __nv_bfloat16* p = M.src + row * M.src_ld + c0;
+      // the words around eight elements of an inner row lie inside the matrix
+      if (n == 8 && (M.src_vec || (row > 0 && row + 1 < M.rows))) {
+        v = load8_shifted(p);
+      } else {
+        float f[8];
+        load8<true>(p, 0, false, n, f);
+        v = pack8(f);
+      }
+    }
+    __nv_bfloat16* d = M.dst + row * M.dst_ld + c0;
+    if (M.dst_vec && n == 8) {
+      *reinterpret_cast<uint4*>(d) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) reinterpret_cast<uint16_t*>(d)[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+    }
   }
 }
 
@@ -419,19 +463,18 @@ cudaError_t launch_act8_load(long long rows, long long cols, const signed char* 
                           vin, vout);
 }
 
-cudaError_t launch_copy_rows(long long rows, long long cols, const __nv_bfloat16* src,
-                             long long src_ld, __nv_bfloat16* dst, long long dst_ld,
-                             const long long* target, long long vocab, cudaStream_t s) {
-  const long long tiles = tiles_of(cols);
-  if (rows <= 0 || cols <= 0) return cudaSuccess;
-  return launch_dependent(copy_rows_kernel, unsigned(rows * tiles), kThreads, s, cols, tiles, src,
-                          src_ld, dst, dst_ld, target, vocab, aligned16(src) && src_ld % 8 == 0,
-                          aligned16(dst) && dst_ld % 8 == 0);
-}
-
-cudaError_t launch_zero_rows(long long rows, long long cols, __nv_bfloat16* dst, long long ld,
-                             cudaStream_t s) {
-  return launch_copy_rows(rows, cols, nullptr, 8, dst, ld, nullptr, 0, s);
+cudaError_t launch_copy_rows(CopyArgs& g, cudaStream_t s) {
+  unsigned blocks = 0;
+  for (int m = 0; m < g.n; ++m) {
+    CopyArgs::Mat& M = g.mat[m];
+    M.block_begin = blocks;
+    M.src_vec = aligned16(M.src) && M.src_ld % 8 == 0;
+    M.dst_vec = aligned16(M.dst) && M.dst_ld % 8 == 0;
+    const long long units = M.rows * ((M.cols + 7) / 8);
+    blocks += unsigned((units + 4 * kThreads - 1) / (4 * kThreads));
+  }
+  if (blocks == 0) return cudaSuccess;
+  return launch_dependent(copy_rows_kernel, blocks, unsigned(kThreads), s, g);
 }
 
 cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,

@@ -47,6 +47,7 @@
 #include "epi.cuh"
 #include "launch.h"
 #include "ptx.cuh"
+#include "shift.cuh"
 #include "train.h"
 
 #include <algorithm>
@@ -338,19 +339,23 @@ DM_DEV float act8_block(float (&v)[32], int n, uint32_t (&w)[8]) {
 }
 
 // 32 kept values of one row (columns c0 .. c0 + 31, n of them inside), fetched as
-// stored: their loads are issued a chunk ahead of their use.
+// stored: their loads are issued a chunk ahead of their use.  `inner`: neither the
+// first nor the last row, so that the aligned words around an unaligned piece of it
+// lie inside the tensor.
 struct Kept {
   uint4 q[4];
   float scale;
 };
 DM_DEV void fetch_kept(const LinArgs& g, const void* base, const __nv_bfloat16* scales, int row,
-                       int c0, int n, Kept& k) {
+                       int c0, int n, bool inner, Kept& k) {
   if (g.keep == kKeepBf16) {
     const __nv_bfloat16* p =
         static_cast<const __nv_bfloat16*>(base) + (long long)row * g.ffn + c0;
     if (g.kept_vec && n >= 32) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) k.q[u] = __ldcs(reinterpret_cast<const uint4*>(p) + u);
+    } else if (inner && n >= 32) {
+      load_shifted<4>(p, k.q);
     } else {
       const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
       uint32_t w[16];
@@ -368,6 +373,11 @@ DM_DEV void fetch_kept(const LinArgs& g, const void* base, const __nv_bfloat16* 
     if (g.kept_vec && n >= 32) {
       k.q[0] = __ldcs(reinterpret_cast<const uint4*>(p));
       k.q[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+    } else if (inner && n >= 32) {
+      uint4 t[2];
+      load_shifted<2>(p, t);
+      k.q[0] = t[0];
+      k.q[1] = t[1];
     } else {
       uint32_t w[8] = {};
 #pragma unroll
@@ -560,8 +570,9 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     auto fetch = [&](int k) {
       const int r = row_of(k) + lane;
       if (EPI == kLinGluGrad && k < kChunks && inside(k) && r < P.rows) {
-        fetch_kept(g, g.gate, g.gate_scale, r, c_of(k), P.cols - c_of(k), kept_g);
-        fetch_kept(g, g.up, g.up_scale, r, c_of(k), P.cols - c_of(k), kept_u);
+        const bool inner = r > 0 && r + 1 < P.rows;
+        fetch_kept(g, g.gate, g.gate_scale, r, c_of(k), P.cols - c_of(k), inner, kept_g);
+        fetch_kept(g, g.up, g.up_scale, r, c_of(k), P.cols - c_of(k), inner, kept_u);
       }
     };
     if (EPI == kLinGluGrad && U.q < 0) fetch(0);
@@ -792,9 +803,9 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
   int it = 0;
   bool ok = true;
 
-  // 32 exponentials of one token, entries c0 .., to the workspace in fp16
-  auto put = [&](int which, const float* e, int c0, int rg0) {
-    const uint32_t buf = buf0 + uint32_t(which * kEpiBufBytes);
+  // swapped: 32 exponentials of one token, entries c0 .., to the workspace in fp16
+  auto put = [&](const float* e, int c0, int rg0) {
+    const uint32_t buf = buf0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t o[4];
@@ -875,10 +886,28 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
           z[j] = ex2((z[j] - m) * kLog2e);
           s += z[j];
         }
-        if (P.c_map >= 0 && k * 32 < n) {
-          if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
+        // 64 entries of each token at a time: 128-byte rows
+        if (P.c_map >= 0 && (k & 1) && (k - 1) * 32 < n) {
+          if (lane == 0) bulk_wait_read<0>();  // the store that last read the buffer
           __syncwarp();
-          put(k & 1, z + k * 32, g0 + k * 32, rg0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 p = __floats2half2_rn(z[(k - 1) * 32 + 8 * i + 2 * j],
+                                                  z[(k - 1) * 32 + 8 * i + 2 * j + 1]);
+              o[j] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            st_shared_v4(buf0 + uint32_t(lane * 128 + ((i ^ (lane & 7)) << 4)), o[0], o[1], o[2],
+                         o[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&g.maps[P.c_map], buf0, g0 + (k - 1) * 32, rg0);
+            bulk_commit();
+          }
         }
       }
       if (r < P.rows)
@@ -921,7 +950,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
             v[j] = ex2((v[j] - m) * kLog2e);
             s += v[j];
           }
-          if (P.c_map >= 0) put(0, v, c0, rg0);
+          if (P.c_map >= 0) put(v, c0, rg0);
           if (r < P.rows) g.group_stat[(long long)(c0 / 32) * g.stat_ld + r] = make_float2(m, s);
         }
       }

@@ -27,7 +27,10 @@ using bf16 = __nv_bfloat16;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+// Row pitch of what the workspace holds: whole 128-byte lines, so that a box row of a
+// TMA copy touches one (with rows of 16-byte multiples only, 390 us against 304 for the
+// logits of 2443 tokens, 2259 x 50119).
+int64_t pitch(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -174,8 +177,8 @@ struct Readable {
 Readable readable(CopyArgs& c, const void* p, int64_t rows, int64_t cols, int64_t ld, bf16* copy) {
   const bf16* src = static_cast<const bf16*>(p);
   if (aligned(src, 16) && ld % 8 == 0) return {src, ld};
-  c.add(src, ld, copy, up8(cols), rows, cols);
-  return {copy, up8(cols)};
+  c.add(src, ld, copy, pitch(cols), rows, cols);
+  return {copy, pitch(cols)};
 }
 int run_copies(CopyArgs& c, cudaStream_t s) {
   return c.n == 0 || launch_copy_rows(c, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
@@ -197,20 +200,20 @@ struct FfnSpace {
 FfnSpace ffn_space(const dmuon_ffn_shape& s, bool backward, void* ws) {
   Carve c(ws);
   FfnSpace f{};
-  const size_t t = size_t(s.tokens), d8 = size_t(up8(s.hidden)), f8 = size_t(up8(s.ffn));
+  const size_t t = size_t(s.tokens), dp = size_t(pitch(s.hidden)), fp = size_t(pitch(s.ffn));
   f.ps = take_product_space(c);
-  f.x = c.take<bf16>(t * d8 * 2);
-  f.h = c.take<bf16>(t * f8 * 2);
+  f.x = c.take<bf16>(t * dp * 2);
+  f.h = c.take<bf16>(t * fp * 2);
   if (backward) {
-    f.dy = c.take<bf16>(t * d8 * 2);
-    f.dgate = c.take<bf16>(t * f8 * 2);
-    f.dup = c.take<bf16>(t * f8 * 2);
+    f.dy = c.take<bf16>(t * dp * 2);
+    f.dgate = c.take<bf16>(t * fp * 2);
+    f.dup = c.take<bf16>(t * fp * 2);
   }
   if (s.hidden % 8 != 0) {
-    f.w_gate = c.take<bf16>(size_t(s.ffn) * d8 * 2);
-    f.w_up = c.take<bf16>(size_t(s.ffn) * d8 * 2);
+    f.w_gate = c.take<bf16>(size_t(s.ffn) * dp * 2);
+    f.w_up = c.take<bf16>(size_t(s.ffn) * dp * 2);
   }
-  if (s.ffn % 8 != 0) f.w_down = c.take<bf16>(size_t(s.hidden) * f8 * 2);
+  if (s.ffn % 8 != 0) f.w_down = c.take<bf16>(size_t(s.hidden) * fp * 2);
   f.bytes = c.used;
   return f;
 }
@@ -264,7 +267,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   int e = device_ready(&clusters);
   if (e != DMUON_OK) return e;
   const FfnSpace f = ffn_space(s, false, ws);
-  const int64_t f8 = up8(s.ffn);
+  const int64_t fp = pitch(s.ffn);
   CopyArgs copies{};
   const FfnWeights w = ffn_weights(copies, s, f, wg, wu, wd);
   const Readable xr = readable(copies, x, s.tokens, s.hidden, x_ld, f.x);
@@ -283,7 +286,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     a.w1 = w.up.p;
     a.w_ld = w.gate.ld;
     a.out = f.h;
-    a.out_ld = f8;
+    a.out_ld = fp;
     if (s.save == DMUON_SAVE_BF16) {
       a.gate = static_cast<bf16*>(saved[0]);
       a.up = static_cast<bf16*>(saved[1]);
@@ -294,7 +297,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     a.act = s.activation;
     ThinArgs b{};
     b.x = f.h;
-    b.x_ld = f8;
+    b.x_ld = fp;
     b.w0 = w.down.p;
     b.w_ld = w.down.ld;
     b.out = static_cast<bf16*>(y);
@@ -316,7 +319,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     P.a1 = up;
     P.b0 = L.g.swap ? t : gate;
     P.b1 = up;
-    L.store_to(P, f.h, f8, false);
+    L.store_to(P, f.h, fp, false);
     use_saved(L.g, s, saved);
     if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
       L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
@@ -330,7 +333,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   }
   Launch L(f.ps);
   LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, 0);
-  L.operands(P, f.h, s.ffn, f8, w.down.p, s.ffn, s.hidden, w.down.ld, true);
+  L.operands(P, f.h, s.ffn, fp, w.down.p, s.ffn, s.hidden, w.down.ld, true);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
   return L.run_token(kLinStore, true, clusters, st);
 }
@@ -350,7 +353,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     return run_copies(zeros, st);
   }
   const FfnSpace f = ffn_space(s, true, ws);
-  const int64_t f8 = up8(s.ffn);
+  const int64_t fp = pitch(s.ffn);
   CopyArgs copies{};
   const FfnWeights w = ffn_weights(copies, s, f, wg, wu, wd);
   const Readable xr = readable(copies, x, s.tokens, s.hidden, x_ld, f.x);
@@ -361,11 +364,11 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     Launch L(f.ps);
     LinProblem& P = L.token_problem(kLinGluGrad, s.tokens, s.ffn, 256, s.hidden, 0);
     L.operands(P, dyr.p, s.hidden, dyr.ld, w.down.p, s.ffn, s.hidden, w.down.ld, false);
-    L.store_to(P, f.dgate, f8, false);
+    L.store_to(P, f.dgate, fp, false);
     L.g.dup = f.dup;
     L.g.h = f.h;
-    L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, f8);
-    L.g.map_h = L.output(f.h, s.ffn, s.tokens, f8);
+    L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, fp);
+    L.g.map_h = L.output(f.h, s.ffn, s.tokens, fp);
     use_saved(L.g, s, saved);
     e = L.run_token(kLinGluGrad, false, clusters, st);
     if (e != DMUON_OK) return e;
@@ -373,8 +376,8 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   {  // dx = dgate Wg + dup Wu
     Launch L(f.ps);
     LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, s.ffn);
-    L.operands(P, f.dgate, s.ffn, f8, w.gate.p, s.hidden, s.ffn, w.gate.ld, false);
-    L.operands(P, f.dup, s.ffn, f8, w.up.p, s.hidden, s.ffn, w.up.ld, false, true);
+    L.operands(P, f.dgate, s.ffn, fp, w.gate.p, s.hidden, s.ffn, w.gate.ld, false);
+    L.operands(P, f.dup, s.ffn, fp, w.up.p, s.hidden, s.ffn, w.up.ld, false, true);
     L.store_to(P, static_cast<bf16*>(dx), dx_ld);
     e = L.run_token(kLinStore, false, clusters, st);
     if (e != DMUON_OK) return e;
@@ -387,8 +390,8 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
     LinProblem& P = L.problem(m, n, s.tokens, 0);
-    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? f8 : dyr.ld);
-    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, f8);
+    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld);
+    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, fp);
     L.store_to(P, out[i], n);
   }
   return L.run(kLinStore, true, true, clusters, st);
@@ -404,7 +407,7 @@ bool xent_shape_ok(const dmuon_xent_shape* s) {
 int64_t xent_piece(const dmuon_xent_shape& s, bool grads) {
   int64_t most = kLossTokens;
   if (grads)
-    most = std::max<int64_t>(256, int64_t(kLogitBytes / (size_t(up8(s.vocab)) * 2)) / 256 * 256);
+    most = std::max<int64_t>(256, int64_t(kLogitBytes / (size_t(pitch(s.vocab)) * 2)) / 256 * 256);
   return std::min(s.tokens, most);
 }
 
@@ -420,10 +423,10 @@ struct XentSpace {
 XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   Carve c(ws);
   XentSpace x{};
-  const size_t d8 = size_t(up8(s.hidden));
+  const size_t dp = size_t(pitch(s.hidden));
   x.piece = xent_piece(s, grads);
   x.ps = take_product_space(c);
-  x.hidden = c.take<bf16>(size_t(s.tokens) * d8 * 2);
+  x.hidden = c.take<bf16>(size_t(s.tokens) * dp * 2);
   x.target_logit = c.take<float>(size_t(s.tokens) * 4);
   x.grad_scale = c.take<float>(4);
   // swapped products have four times the groups, over at most kSwapTokens tokens
@@ -431,9 +434,9 @@ XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
       std::max(size_t(ceil_div(s.vocab, kXentGroup)) * size_t(up32(x.piece)),
                size_t(ceil_div(s.vocab, kXentGroupSwap)) *
                    size_t(std::min(up32(x.piece), kSwapTokens))) * sizeof(float2));
-  if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * d8 * 2);
+  if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * dp * 2);
   if (grads) {
-    x.e = c.take<bf16>(size_t(x.piece) * size_t(up8(s.vocab)) * 2);
+    x.e = c.take<bf16>(size_t(x.piece) * size_t(pitch(s.vocab)) * 2);
     if (x.piece < s.tokens) x.sum = c.take<float>(size_t(s.vocab) * size_t(s.hidden) * 4);
   }
   x.bytes = c.used;
@@ -448,7 +451,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
   int e = device_ready(&clusters);
   if (e != DMUON_OK) return e;
   const XentSpace x = xent_space(s, grads, ws);
-  const int64_t v8 = up8(s.vocab);
+  const int64_t vp = pitch(s.vocab);
   const long long* tgt = reinterpret_cast<const long long*>(target);
   CopyArgs copies{};
   Readable h;
@@ -457,7 +460,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     // reaches the weight's gradient, which sums over rows
     copies.target = tgt;
     copies.vocab = s.vocab;
-    h = {x.hidden, up8(s.hidden)};
+    h = {x.hidden, pitch(s.hidden)};
     copies.add(static_cast<const bf16*>(hidden), h_ld, x.hidden, h.ld, s.tokens, s.hidden);
   } else {
     h = readable(copies, hidden, s.tokens, s.hidden, h_ld, x.hidden);
@@ -486,7 +489,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
       Launch L(x.ps);
       LinProblem& P = L.token_problem(kLinXent, n, s.vocab, 256, s.hidden, 0);
       L.operands(P, hp, s.hidden, h.ld, w.p, s.hidden, s.vocab, w.ld, true);
-      if (grads) P.c_map = L.output(x.e, s.vocab, n, v8);
+      if (grads) P.c_map = L.output(x.e, s.vocab, n, vp, !L.g.swap);
       L.g.target = tgt + t0;
       L.g.target_logit = x.target_logit + t0;
       L.g.group_stat = x.stat;
@@ -498,11 +501,11 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     }
     if (launch_xent_rows(R, st) != cudaSuccess) return DMUON_ERR_CUDA;
     if (!grads) continue;
-    if (launch_xent_grad(R, x.e, v8, st) != cudaSuccess) return DMUON_ERR_CUDA;
+    if (launch_xent_grad(R, x.e, vp, st) != cudaSuccess) return DMUON_ERR_CUDA;
     {  // dhidden = G W
       Launch L(x.ps);
       LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, s.vocab, 0);
-      L.operands(P, x.e, s.vocab, v8, w.p, s.hidden, s.vocab, w.ld, false);
+      L.operands(P, x.e, s.vocab, vp, w.p, s.hidden, s.vocab, w.ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
       L.g.scale = x.grad_scale;
       e = L.run_token(kLinStore, false, clusters, st);
@@ -511,7 +514,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     // dweight += G^T h, in fp32 over the pieces
     Launch L(x.ps);
     LinProblem& P = L.problem(s.vocab, s.hidden, n, 0);
-    P.a0 = L.operand(x.e, s.vocab, n, v8);
+    P.a0 = L.operand(x.e, s.vocab, n, vp);
     P.b0 = L.operand(hp, s.hidden, n, h.ld);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
     L.g.scale = x.grad_scale;

@@ -4,6 +4,7 @@
 #include "act8.cuh"
 #include "dmuon.h"
 #include "launch.h"
+#include "shift.cuh"
 #include "train.h"
 
 #include <cuda_fp16.h>
@@ -217,32 +218,6 @@ DM_DEV bool live_target(const long long* target, long long row, long long vocab)
   return t >= 0 && t < vocab;
 }
 
-// Eight bf16 elements at p, which is 2-byte aligned, from the two 16-byte words around
-// them.
-DM_DEV uint4 load8_shifted(const __nv_bfloat16* p) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const unsigned skip = unsigned(at & 15u);  // bytes, even
-  const uint4* q = reinterpret_cast<const uint4*>(at - skip);
-  const uint4 lo = q[0];
-  if (skip == 0) return lo;
-  const uint4 hi = q[1];
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const unsigned bits = (skip & 3u) * 8u;
-  uint32_t o[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t a = 0, b = 0;
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      if (skip / 4 == unsigned(s)) {
-        a = w[k + s];
-        b = w[k + s + 1];
-      }
-    o[k] = __funnelshift_r(a, b, bits);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // Up to CopyArgs::kMost matrices to rows that TMA can read, one launch.  A thread
 // moves 8 columns; the threads run through rows and columns alike, so that narrow
 // matrices fill them too.  src == nullptr: zeros.
@@ -269,7 +244,9 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_consta
       const __nv_bfloat16* p = M.src + row * M.src_ld + c0;
       // the words around eight elements of an inner row lie inside the matrix
       if (n == 8 && (M.src_vec || (row > 0 && row + 1 < M.rows))) {
-        v = load8_shifted(p);
+        uint4 q[1];
+        load_shifted<1>(p, q);
+        v = q[0];
       } else {
         float f[8];
         load8<true>(p, 0, false, n, f);

@@ -5,18 +5,25 @@
 
 namespace dm {
 
+DM_DEV float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+DM_DEV float sigmoid(float x) { return fast_rcp(1.f + __expf(-x)); }
+
 // act(x) and, for the gradient, act'(x), in fp32.  The tanh form is taken as
 // x * sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)): (1 + tanh y) / 2 = sigmoid(2 y).
 template <int ACT>
 DM_DEV float act_value(float x) {
-  if (ACT == DMUON_ACT_SILU) return x * __fdividef(1.f, 1.f + __expf(-x));
+  if (ACT == DMUON_ACT_SILU) return x * sigmoid(x);
   if (ACT == DMUON_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678f));
-  return x * __fdividef(1.f, 1.f + __expf(-1.59576912f * fmaf(0.044715f * x * x, x, x)));
+  return x * sigmoid(1.59576912f * fmaf(0.044715f * x * x, x, x));
 }
 template <int ACT>
 DM_DEV void act_both(float x, float& a, float& da) {
   if (ACT == DMUON_ACT_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-x));
+    const float s = sigmoid(x);
     a = x * s;
     da = s * fmaf(x, 1.f - s, 1.f);
   } else if (ACT == DMUON_ACT_GELU) {
@@ -24,7 +31,7 @@ DM_DEV void act_both(float x, float& a, float& da) {
     a = x * phi;
     da = fmaf(x * 0.39894228f, __expf(-0.5f * x * x), phi);
   } else {
-    const float s = __fdividef(1.f, 1.f + __expf(-1.59576912f * fmaf(0.044715f * x * x, x, x)));
+    const float s = sigmoid(1.59576912f * fmaf(0.044715f * x * x, x, x));
     a = x * s;
     da = fmaf(x * s * (1.f - s), 1.59576912f * fmaf(0.134145f * x, x, 1.f), s);
   }

@@ -59,16 +59,21 @@ namespace {
 
 constexpr int kTile = 256;                 // tile rows and columns (CTA pair)
 constexpr int kHalf = 128;                 // one CTA's rows of A / columns of B
-constexpr int kStages = 3;                 // of 64 KB; swapped, as many as fit there
 constexpr int kMaxStages = 10;
-constexpr int kStageArea = kStages * 65536;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;
-constexpr int kEpiBytes = kEpiWarps * 2 * kEpiBufBytes;
 constexpr int kBarBytes = 512;
-constexpr size_t kSmemBytes = size_t(kStageArea) + kEpiBytes + 1024 + kBarBytes;
+// Stages and, for each epilogue warp, 4 KB in which chunks are turned or wait to be
+// stored; kLinGluGrad takes 32 KB less of stages and gives each warp another 4 KB, for
+// the gate's and up's chunks on their way in.
+__host__ __device__ constexpr int stage_area(int epi) { return (epi == kLinGluGrad ? 160 : 192) << 10; }
+__host__ __device__ constexpr int warp_bytes(int epi) { return epi == kLinGluGrad ? 8192 : 4096; }
+constexpr size_t kSmemBytes = size_t(224 << 10) + 1024 + kBarBytes;
+static_assert(stage_area(kLinStore) + kEpiWarps * warp_bytes(kLinStore) == 224 << 10 &&
+                  stage_area(kLinGluGrad) + kEpiWarps * warp_bytes(kLinGluGrad) == 224 << 10,
+              "shared memory layout");
 static_assert(kSmemBytes <= 232448, "dynamic shared memory above the per-block limit");
 static_assert((2 * kMaxStages + 4 + 1 + 8) * 8 + 8 <= kBarBytes, "barrier area too small");
 
@@ -90,15 +95,18 @@ constexpr size_t kPartialBytes = size_t(40) << 20;
 // A stage: K-elements, this CTA's 128 rows of A and its half of B's columns (128,
 // or nt/2 tokens).  Plainly 128 K-elements, which halves the barrier round trips;
 // swapped, where the bytes in flight bound the rate at which weights stream, 64, so
-// that a smaller part of the stages is being consumed.
-template <bool SWAP>
+// that a smaller part of the stages is being consumed (and for kLinGluGrad, whose
+// stages have 160 KB).
+template <int EPI, bool SWAP>
 struct Stage {
-  static constexpr int k = SWAP ? kLinKSwap : kLinK;
+  static constexpr int k = lin_stage_k(EPI, SWAP);
   static constexpr int a_bytes = kHalf * k * 2;
   static constexpr int panels = k / 64;  // spans of a 128-byte swizzled row
   static DM_DEV int b_rows(const LinArgs& g) { return SWAP ? g.nt / 2 : kHalf; }
   static DM_DEV int bytes(const LinArgs& g) { return a_bytes + b_rows(g) * k * 2; }
-  static DM_DEV int count(const LinArgs& g) { return SWAP ? g.stages : kStages; }
+  static DM_DEV int count(const LinArgs& g) {
+    return SWAP ? g.stages : stage_area(EPI) / (2 * a_bytes);
+  }
 };
 
 struct Unit {
@@ -155,7 +163,7 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
                      uint64_t* empty_bar, volatile int* abort_flag) {
   const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0);
   const int clusters = int(cluster_count_x());
-  using St = Stage<SWAP>;
+  using St = Stage<EPI, SWAP>;
   const int stages = St::count(g), bytes = St::bytes(g), brows = St::b_rows(g);
   constexpr int a_box = St::k * 128;  // 64 MN-elements of k rows, or (two panels) 128 rows
   int stage = 0;
@@ -221,7 +229,7 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
   // groups 1 KB apart.  MN-major: 64-element atoms of the stage's K rows apart (LBO),
   // 8-row K groups 1 KB apart (SBO), 2 KB per K step.  Shared-memory addresses stay
   // below 256 KB, so adding to the start-address field never carries out of it.
-  using St = Stage<SWAP>;
+  using St = Stage<EPI, SWAP>;
   constexpr int atom = St::k * 128;
   const uint64_t a_desc = sdesc_sw128(smem_u32(sStage), A_MN ? atom : 16, 1024);
   const uint64_t b_desc = sdesc_sw128(smem_u32(sStage) + St::a_bytes, B_MN ? atom : 16, 1024);
@@ -395,7 +403,7 @@ DM_DEV void kept_values(const LinArgs& g, const Kept& k, int half, float (&v)[16
   } else {
     const uint32_t w[4] = {k.q[half].x, k.q[half].y, k.q[half].z, k.q[half].w};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = k.scale * float((signed char)(w[j / 4] >> (8 * (j & 3))));
+    for (int j = 0; j < 16; ++j) v[j] = k.scale * act8_int(w[j / 4], j & 3);
   }
 }
 
@@ -419,6 +427,55 @@ struct Handover {
   uint32_t parity;
 };
 
+// Where an epilogue warp's 32 x 32 chunks lie.  Chunk k (0..3) sits at the
+// accumulator's columns 32 col(k).. and the warp's quarter of the TMEM lanes; it holds
+// the output's rows row(k).. and columns c(k)...
+template <int EPI, bool SWAP>
+struct Chunks {
+  const LinArgs& g;
+  const LinProblem& P;
+  int ti, tj, rank, q, h, chunks;
+  DM_DEV Chunks(const LinArgs& g_, const Unit& U, int rank_, int q_, int h_)
+      : g(g_), P(g_.prob[U.prob]), ti(U.ti), tj(U.tj), rank(rank_), q(q_), h(h_),
+        chunks(SWAP ? g_.nt / 32 : kAccCols / 32) {}
+  DM_DEV int col(int k) const {
+    if (SWAP) return 2 * k + h;
+    return EPI == kLinGlu ? (k >> 1) * 4 + h * 2 + (k & 1) : h * 4 + k;
+  }
+  DM_DEV int row(int k) const {
+    return SWAP ? tj * g.nt + col(k) * 32 : ti * kTile + rank * kHalf + q * 32;
+  }
+  DM_DEV int c(int k) const {
+    if (SWAP)
+      return EPI == kLinGlu ? ti * kHalf + rank * 64 + (q & 1) * 32
+                            : ti * kTile + rank * kHalf + q * 32;
+    return EPI == kLinGlu ? tj * kHalf + h * 64 + (k & 1) * 32 : tj * kTile + (h * 4 + k) * 32;
+  }
+  static constexpr int count = EPI == kLinGlu && !SWAP ? 2 : 4;  // chunks to write (if inside)
+  DM_DEV bool inside(int k) const {
+    return k < count && col(k) < chunks && row(k) < P.rows && c(k) < P.cols;
+  }
+};
+
+// A split tile's part: the raw accumulator, for the joining launch.
+template <int EPI, bool SWAP>
+DM_DEV void store_part(const Chunks<EPI, SWAP>& G, const Unit& U, uint32_t t_acc, int lane) {
+  float* dst = G.g.partial +
+               size_t(U.q * G.g.split + U.part) * (size_t(G.chunks) * 32 * kTile) + lane;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int col = G.col(k);
+    if (col >= G.chunks) break;
+    float v[32];
+    __syncwarp();
+    tmem_ld32(t_acc + uint32_t(col * 32), v);
+    tmem_ld_wait();
+    float* p = dst + ((size_t(G.rank) * G.chunks + col) * 4 + G.q) * 1024;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) p[j * 32] = v[j];
+  }
+}
+
 template <int EPI, bool SWAP>
 DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
                      uint8_t* epi, uint64_t* pair_bar, uint32_t tmem_base,
@@ -428,11 +485,10 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
   const int h = (warp - 2) >> 2;   // which half of the tile's columns (swapped: of its chunks)
   const int ew = warp - 2;
   // two 2 KB chunks to be stored; swapped, also the 4 KB in which a chunk is turned
-  float* turn = reinterpret_cast<float*>(epi + ew * 2 * kEpiBufBytes);
+  float* turn = reinterpret_cast<float*>(epi + ew * warp_bytes(kLinStore));
   const uint32_t buf0 = smem_u32(turn);
   const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
   const int clusters = int(cluster_count_x());
-  const int chunks = SWAP ? g.nt / 32 : kAccCols / 32;  // 32-column chunks of the accumulator
   int stored = 0;  // chunks staged so far (their buffers alternate)
   const int pair = h * 2 + (q & 1);
   Handover ho{pair_bar + 2 * pair, pair_bar + 2 * pair + 1, 0u};
@@ -546,37 +602,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     const LinProblem& P = g.prob[U.prob];
     const int acc = it & 1;
     const uint32_t aph = uint32_t(it >> 1) & 1u;
-    // This warp's chunk k (k = 0..3) sits at accumulator columns 32 col_of(k)..; it
-    // holds output rows row_of(k).. (one per lane) and columns c_of(k)...
-    auto col_of = [&](int k) {
-      if (SWAP) return 2 * k + h;
-      return EPI == kLinGlu ? (k >> 1) * 4 + h * 2 + (k & 1) : h * 4 + k;
-    };
-    auto row_of = [&](int k) {
-      return SWAP ? U.tj * g.nt + col_of(k) * 32 : U.ti * kTile + int(rank) * kHalf + q * 32;
-    };
-    auto c_of = [&](int k) {
-      if (SWAP)
-        return EPI == kLinGlu ? U.ti * kHalf + int(rank) * 64 + (q & 1) * 32
-                              : U.ti * kTile + int(rank) * kHalf + q * 32;
-      return EPI == kLinGlu ? U.tj * kHalf + h * 64 + (k & 1) * 32 : U.tj * kTile + (h * 4 + k) * 32;
-    };
-    constexpr int kChunks = EPI == kLinGlu && !SWAP ? 2 : 4;  // chunks to write (if inside)
-    auto inside = [&](int k) {
-      return col_of(k) < chunks && row_of(k) < P.rows && c_of(k) < P.cols;
-    };
-
-    Kept kept_g, kept_u;  // kLinGluGrad: the first chunk's, while the accumulator fills
-    auto fetch = [&](int k) {
-      const int r = row_of(k) + lane;
-      if (EPI == kLinGluGrad && k < kChunks && inside(k) && r < P.rows) {
-        const bool inner = r > 0 && r + 1 < P.rows;
-        fetch_kept(g, g.gate, g.gate_scale, r, c_of(k), P.cols - c_of(k), inner, kept_g);
-        fetch_kept(g, g.up, g.up_scale, r, c_of(k), P.cols - c_of(k), inner, kept_u);
-      }
-    };
-    if (EPI == kLinGluGrad && U.q < 0) fetch(0);
-
+    const Chunks<EPI, SWAP> G(g, U, int(rank), q, h);
     int w = 1;
     if (lane == 0) w = mbar_wait_cluster(&tfull[acc], aph, abort_flag) ? 1 : 0;
     w = __shfl_sync(0xffffffffu, w, 0);
@@ -591,26 +617,15 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(leader_tempty + uint32_t(acc) * 8u);
     };
-    if (U.q >= 0) {  // a part: the raw accumulator, for the joining launch
-      float* dst = g.partial + size_t(U.q * g.split + U.part) * (size_t(chunks) * 32 * kTile) + lane;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        if (col_of(k) >= chunks) break;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v);
-        tmem_ld_wait();
-        float* p = dst + ((size_t(rank) * chunks + col_of(k)) * 4 + q) * 1024;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) p[j * 32] = v[j];
-      }
+    if (U.q >= 0) {
+      store_part(G, U, t_acc, lane);
       release();
       continue;
     }
     // accumulator chunk k with the TMEM's lanes: a lane holds a row of the tile
     auto load_raw = [&](int k, float (&v)[32]) {
       __syncwarp();
-      tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v);
+      tmem_ld32(t_acc + uint32_t(G.col(k) * 32), v);
       tmem_ld_wait();
     };
     // and with one output row per lane
@@ -629,15 +644,15 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     if constexpr (EPI == kLinStore && !SWAP) {
       if (g.sum == nullptr && P.c_map >= 0) {
         const float f = g.scale != nullptr ? *g.scale : 1.f;
-        const bool second = inside(2);
+        const bool second = G.inside(2);
 #pragma unroll 1
         for (int k = 0; k < 4; k += 2) {
-          if (!inside(k)) break;
+          if (!G.inside(k)) break;
           uint32_t w[32];
           __syncwarp();
           float v0[32], v1[32];
-          tmem_ld32(t_acc + uint32_t(col_of(k) * 32), v0);
-          tmem_ld32(t_acc + uint32_t(col_of(k) * 32 + 32), v1);
+          tmem_ld32(t_acc + uint32_t(G.col(k) * 32), v0);
+          tmem_ld32(t_acc + uint32_t(G.col(k) * 32 + 32), v1);
           tmem_ld_wait();
           // the accumulator is free as soon as it is in registers
           if (k == 2 || !second) release();
@@ -646,17 +661,17 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
             w[j] = pack_bf16x2(v0[2 * j] * f, v0[2 * j + 1] * f);
             w[16 + j] = pack_bf16x2(v1[2 * j] * f, v1[2 * j + 1] * f);
           }
-          put_wide(P.c_map, w, c_of(k), row_of(k));
+          put_wide(P.c_map, w, G.c(k), G.row(k));
         }
-        if (!inside(0)) release();
+        if (!G.inside(0)) release();
         continue;
       }
     }
     bool dead = false;
 #pragma unroll 1
-    for (int k = 0; k < kChunks; ++k) {
-      if (!inside(k)) break;
-      const int c0 = c_of(k), rg0 = row_of(k), r = rg0 + lane, n = P.cols - c0;
+    for (int k = 0; k < G.count; ++k) {
+      if (!G.inside(k)) break;
+      const int c0 = G.c(k), rg0 = G.row(k), r = rg0 + lane, n = P.cols - c0;
       if constexpr (EPI == kLinStore) {
         float v[32];
         load_acc(k, v);
@@ -699,7 +714,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
         }
         if (SWAP && P.c_map >= 0) put(P.c_map, v, c0, rg0);
         else put_plain(P.c, P.c_ld, v, c0, rg0, P.rows, n);
-      } else if constexpr (EPI == kLinGlu) {
+      } else {  // kLinGlu
         float a[32], b[32];
         if (SWAP) {
           // gate's rows are the TMEM lanes of quarters 0 and 1, up's those of 2 and 3, whose
@@ -718,7 +733,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
           ho.parity ^= 1u;
           if (dead) break;
           // quarter q's warp is number (q + 2) % 4 of its half: the partner's is number q
-          turn_read(reinterpret_cast<const float*>(epi + (h * 4 + q) * 2 * kEpiBufBytes), lane, b);
+          turn_read(reinterpret_cast<const float*>(epi + (h * 4 + q) * warp_bytes(EPI)), lane, b);
           arrive_warp(ho.taken);
         } else {
           load_acc(k, a);
@@ -742,37 +757,185 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
         else if (g.act == DMUON_ACT_GELU) glu32<DMUON_ACT_GELU>(a, b);
         else glu32<DMUON_ACT_GELU_TANH>(a, b);
         put(P.c_map, a, c0, rg0);
-      } else {  // kLinGluGrad
-        float v[32];
-        load_acc(k, v);
-        if (r >= P.rows) kept_g = kept_u = Kept{};
-        // in halves of 16 columns, packed as they are done, to stay within the registers
-        uint32_t pg[16], pd[16], ph[16];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float ga[16], up[16];
-          kept_values(g, kept_g, half, ga);
-          kept_values(g, kept_u, half, up);
-          float* vh = v + 16 * half;
-          if (g.act == DMUON_ACT_SILU) glu_grad16<DMUON_ACT_SILU>(vh, ga, up);
-          else if (g.act == DMUON_ACT_GELU) glu_grad16<DMUON_ACT_GELU>(vh, ga, up);
-          else glu_grad16<DMUON_ACT_GELU_TANH>(vh, ga, up);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            pg[8 * half + j] = pack_bf16x2(ga[2 * j], ga[2 * j + 1]);
-            pd[8 * half + j] = pack_bf16x2(vh[2 * j], vh[2 * j + 1]);
-            ph[8 * half + j] = pack_bf16x2(up[2 * j], up[2 * j + 1]);
-          }
-        }
-        fetch(k + 1);
-        put_packed(P.c_map, pg, c0, rg0);
-        put_packed(g.map_dup, pd, c0, rg0);
-        put_packed(g.map_h, ph, c0, rg0);
       }
     }
     if (dead) break;
     release();
   }
+  // stores complete, and stop reading shared memory, before the CTA exits
+  if (lane == 0) bulk_wait_all();
+  __syncwarp();
+}
+
+// kLinGluGrad.  The kept gate and up of a chunk come in by TMA, a chunk ahead, and the
+// three outputs leave by TMA.  (With lanes reading their own rows from global memory the
+// loads took 17000 of a tile's 45000 cycles, and reading and writing 8 rows x 64 bytes an
+// instruction was no better: 86 us against 59 for 2048 tokens, 1536/8960.)  Rows that
+// are not 16-byte aligned are read by the lanes.
+template <bool SWAP>
+DM_DEV void epilogue_grad(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
+                          uint8_t* epi, uint64_t* kept_bars, uint32_t tmem_base,
+                          volatile int* abort_flag) {
+  using Geo = Chunks<kLinGluGrad, SWAP>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, h = (warp - 2) >> 2, ew = warp - 2;
+  float* turn = reinterpret_cast<float*>(epi + ew * warp_bytes(kLinGluGrad));
+  const uint32_t buf0 = smem_u32(turn), kept0 = buf0 + 4096u;
+  uint64_t* kept_bar = kept_bars + ew;
+  const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
+  const int clusters = int(cluster_count_x());
+  const bool act8 = g.keep == kKeepAct8, vec = g.kept_vec != 0;
+  const int blocks = (g.ffn + kActBlock - 1) / kActBlock;
+  int stored = 0;
+  uint32_t kept_parity = 0;
+  bool fetched = false;  // a chunk's gate and up are on their way
+
+  // every lane is done with what the buffer held
+  auto fetch = [&](const Geo& G, int k) {
+    if (!vec || !G.inside(k)) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kept_bar, act8 ? 2048u : 4096u);
+      tma_load_2d_u32(kept0, &g.maps[g.map_gate], smem_u32(kept_bar), G.c(k), G.row(k));
+      tma_load_2d_u32(kept0 + 2048u, &g.maps[g.map_up], smem_u32(kept_bar), G.c(k), G.row(k));
+    }
+    fetched = true;
+  };
+  auto read_kept = [&](Kept& kg, Kept& ku) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (act8 && i >= 2) break;
+      const uint32_t at = kept0 + (act8 ? uint32_t(lane * 32 + i * 16) : epi_off(lane, i));
+      ld_shared_v4(at, kg.q[i].x, kg.q[i].y, kg.q[i].z, kg.q[i].w);
+      ld_shared_v4(at + 2048u, ku.q[i].x, ku.q[i].y, ku.q[i].z, ku.q[i].w);
+    }
+    __syncwarp();
+  };
+  auto put = [&](int map, const uint32_t (&w)[16], int c0, int rg0) {
+    const uint32_t buf = buf0 + uint32_t((stored++ & 1) * kEpiBufBytes);
+    if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      st_shared_v4(buf + epi_off(lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&g.maps[map], buf, c0, rg0);
+      bulk_commit();
+    }
+  };
+
+  int it = 0;
+  for (int u = int(cluster_id_x()); u < g.total_units; u += clusters, ++it) {
+    const Unit U = decode_unit(g, u);
+    const Geo G(g, U, int(rank), q, h);
+    const LinProblem& P = G.P;
+    const int acc = it & 1;
+    if (U.q < 0 && !fetched) fetch(G, 0);
+    // block scales, as stored: a plain tile's four of a row lie side by side
+    uint2 scale4[2] = {};
+    const bool four = act8 && vec && !SWAP && blocks % 4 == 0 && G.inside(0);
+    if (four && U.q < 0 && G.row(0) + lane < P.rows) {
+      const long long at = (long long)(G.row(0) + lane) * blocks + G.c(0) / kActBlock;
+      scale4[0] = *reinterpret_cast<const uint2*>(g.gate_scale + at);
+      scale4[1] = *reinterpret_cast<const uint2*>(g.up_scale + at);
+    }
+    int w = 1;
+    if (lane == 0) w = mbar_wait_cluster(&tfull[acc], uint32_t(it >> 1) & 1u, abort_flag) ? 1 : 0;
+    w = __shfl_sync(0xffffffffu, w, 0);
+    if (!w) {
+      if (lane == 0) raise_abort(g.err, abort_flag);
+      break;
+    }
+    tc_fence_after();
+    const uint32_t t_acc = tmem_base + uint32_t(acc * kAccCols) + (uint32_t(q * 32) << 16);
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(leader_tempty + uint32_t(acc) * 8u);
+    };
+    if (U.q >= 0) {
+      store_part(G, U, t_acc, lane);
+      release();
+      continue;
+    }
+    bool dead = false;
+#pragma unroll 1
+    for (int k = 0; k < 4 && G.inside(k); ++k) {
+      const int c0 = G.c(k), rg0 = G.row(k), r = rg0 + lane, n = P.cols - c0;
+      Kept kg{}, ku{};
+      if (vec) {
+        int kw = 1;
+        if (lane == 0) {
+          kw = mbar_wait(kept_bar, kept_parity, abort_flag) ? 1 : 0;
+          if (!kw) raise_abort(g.err, abort_flag);
+        }
+        dead = __shfl_sync(0xffffffffu, kw, 0) == 0;
+        if (dead) break;
+        kept_parity ^= 1u;
+        read_kept(kg, ku);
+        if (four) {
+          const uint32_t sg = k & 2 ? scale4[0].y : scale4[0].x;
+          const uint32_t su = k & 2 ? scale4[1].y : scale4[1].x;
+          kg.scale = __uint_as_float(k & 1 ? sg & 0xFFFF0000u : sg << 16);
+          ku.scale = __uint_as_float(k & 1 ? su & 0xFFFF0000u : su << 16);
+        } else if (act8 && r < P.rows) {
+          const long long at = (long long)r * blocks + c0 / kActBlock;
+          kg.scale = __bfloat162float(g.gate_scale[at]);
+          ku.scale = __bfloat162float(g.up_scale[at]);
+        }
+        fetched = false;
+        if (G.inside(k + 1)) {
+          fetch(G, k + 1);
+        } else if (u + clusters < g.total_units) {
+          const Unit N = decode_unit(g, u + clusters);
+          if (N.q < 0) fetch(Geo(g, N, int(rank), q, h), 0);
+        }
+      } else if (r < P.rows) {
+        const bool inner = r > 0 && r + 1 < P.rows;
+        fetch_kept(g, g.gate, g.gate_scale, r, c0, n, inner, kg);
+        fetch_kept(g, g.up, g.up_scale, r, c0, n, inner, ku);
+      }
+      float v[32];
+      __syncwarp();
+      tmem_ld32(t_acc + uint32_t(G.col(k) * 32), v);
+      tmem_ld_wait();
+      if (!G.inside(k + 1)) release();  // the accumulator is in registers
+      if (SWAP) {
+        if (lane == 0) bulk_wait_read<0>();  // no store still reads the buffer
+        __syncwarp();
+        turn_write(turn, lane, v);
+        __syncwarp();
+        turn_read(turn, lane, v);
+        __syncwarp();
+      }
+      // in halves of 16 columns, packed as they are done, to stay within the registers
+      uint32_t pg[16], pd[16], ph[16];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float ga[16], up[16];
+        kept_values(g, kg, half, ga);
+        kept_values(g, ku, half, up);
+        float* vh = v + 16 * half;
+        if (g.act == DMUON_ACT_SILU) glu_grad16<DMUON_ACT_SILU>(vh, ga, up);
+        else if (g.act == DMUON_ACT_GELU) glu_grad16<DMUON_ACT_GELU>(vh, ga, up);
+        else glu_grad16<DMUON_ACT_GELU_TANH>(vh, ga, up);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          pg[8 * half + j] = pack_bf16x2(ga[2 * j], ga[2 * j + 1]);
+          pd[8 * half + j] = pack_bf16x2(vh[2 * j], vh[2 * j + 1]);
+          ph[8 * half + j] = pack_bf16x2(up[2 * j], up[2 * j + 1]);
+        }
+      }
+      put(P.c_map, pg, c0, rg0);
+      put(g.map_dup, pd, c0, rg0);
+      put(g.map_h, ph, c0, rg0);
+    }
+    if (dead) break;
+    if (!G.inside(0)) release();
+  }
+  // a fetch that nobody waited for (after an abort) must land before the CTA exits
+  if (fetched && lane == 0) (void)mbar_wait(kept_bar, kept_parity, nullptr, kAbortSettleCycles);
   // stores complete, and stop reading shared memory, before the CTA exits
   if (lane == 0) bulk_wait_all();
   __syncwarp();
@@ -794,7 +957,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
   constexpr float kLog2e = 1.44269504f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3, h = (warp - 2) >> 2, ew = warp - 2;
-  float* turn = reinterpret_cast<float*>(epi + ew * 2 * kEpiBufBytes);
+  float* turn = reinterpret_cast<float*>(epi + ew * warp_bytes(kLinStore));
   const uint32_t buf0 = smem_u32(turn);
   const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
   const int clusters = int(cluster_count_x());
@@ -830,7 +993,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
 #pragma unroll
     for (int j = 0; j < kXentGroup; ++j) z[j] = 0.f;
 #pragma unroll 1
-    for (int lo = U.kb_lo; lo < U.kb_hi; lo += kRunElems / Stage<SWAP>::k, ++it) {
+    for (int lo = U.kb_lo; lo < U.kb_hi; lo += kRunElems / Stage<kLinXent, SWAP>::k, ++it) {
       const int acc = it & 1;
       int w = 1;
       if (lane == 0) w = mbar_wait_cluster(&tfull[acc], uint32_t(it >> 1) & 1u, abort_flag) ? 1 : 0;
@@ -966,13 +1129,14 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sEpi = smem + kStageArea;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sEpi + kEpiBytes);
+  uint8_t* sEpi = smem + stage_area(EPI);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sEpi + kEpiWarps * warp_bytes(EPI));
   uint64_t* empty_bar = full_bar + kMaxStages;
   uint64_t* tfull = empty_bar + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain_bar = tempty + 2;
-  uint64_t* pair_bar = drain_bar + 1;  // ready and taken of four warp pairs
+  // ready and taken of four warp pairs (kLinGlu), or one per epilogue warp (kLinGluGrad)
+  uint64_t* pair_bar = drain_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_bar + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -1014,6 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   } else if (warp >= 2) {
     if constexpr (EPI == kLinXent)
       epilogue_xent<SWAP>(g, rank, tfull, tempty, sEpi, tmem_base, abort_flag);
+    else if constexpr (EPI == kLinGluGrad)
+      epilogue_grad<SWAP>(g, rank, tfull, tempty, sEpi, pair_bar, tmem_base, abort_flag);
     else
       epilogue<EPI, SWAP>(g, rank, tfull, tempty, sEpi, pair_bar, tmem_base, abort_flag);
   }
@@ -1314,7 +1480,7 @@ static unsigned lin_magic(int d) {
   return d <= 1 ? 0xFFFFFFFFu : unsigned((0x100000000ull + unsigned(d) - 1) / unsigned(d));
 }
 
-void lin_schedule(LinArgs& g, bool may_split, int clusters) {
+void lin_schedule(LinArgs& g, int epi, int clusters) {
   int tiles = 0, kb = 0;
   for (int p = 0; p < g.n_prob; ++p) {
     g.prob[p].tile_begin = tiles;
@@ -1324,16 +1490,15 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
     g.prob[p].strip_magic = lin_magic(kStrip * g.prob[p].tiles_n);
     g.prob[p].last_magic = lin_magic(g.prob[p].tiles_m % kStrip);
   }
-  g.stages = kStages;
   if (g.swap) {
-    g.stages = kStageArea / (kHalf * kLinKSwap * 2 + g.nt / 2 * kLinKSwap * 2);
+    g.stages = stage_area(epi) / ((kHalf + g.nt / 2) * lin_stage_k(epi, true) * 2);
     if (g.stages > kMaxStages) g.stages = kMaxStages;
   }
   g.full_tiles = g.total_units = tiles;
   g.split = 1;
   g.split_magic = lin_magic(1);
   const int rest = tiles % clusters;
-  if (!may_split || rest == 0) return;
+  if (epi == kLinXent || rest == 0) return;
   // Microseconds of the last wave.  Per 128 K-elements a pair moves 64 KB plus 256
   // bytes per column of its tile through each SM's shared memory (in by TMA, out to the
   // tensor core) at about 243 GB/s: 0.54 for 256 columns.  With few tokens the weights'
@@ -1342,7 +1507,8 @@ void lin_schedule(LinArgs& g, bool may_split, int clusters) {
   // a launch (3) and the parts' way to L2 and back (5 TB/s).
   const int cols = g.swap ? g.nt : kTile;
   double t_kb = (65536 + 256.0 * cols) / 243e3;
-  if (g.swap) t_kb = 0.5 * std::max(t_kb, 0.75 / g.prob[0].tiles_n);
+  if (g.swap) t_kb = std::max(t_kb, 0.75 / g.prob[0].tiles_n);
+  t_kb *= lin_stage_k(epi, g.swap != 0) / 128.0;
   const double part = double(cols) * kTile * sizeof(float);
   double best = kb * t_kb + 0.3;
   for (int s = 2; rest * s * part <= double(kPartialBytes) && 2 * s <= kb; ++s) {

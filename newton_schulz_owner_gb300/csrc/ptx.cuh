@@ -95,6 +95,14 @@ DM_DEV void tma_load_3d_u32(uint32_t smem_dst, const void* tmap, uint32_t bar, i
       : "memory");
 }
 
+// 2-D tiled load, destination and barrier given as shared::cta addresses.
+DM_DEV void tma_load_2d_u32(uint32_t smem_dst, const void* tmap, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
 // 2-D tiled load into this CTA's shared memory, completion counted on an mbarrier
 // that may live in the peer CTA of a pair (shared::cluster address).
 DM_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster, int c0,

@@ -38,8 +38,10 @@ enum LinEpi {
 };
 enum LinKeep { kKeepNone = 0, kKeepBf16 = 1, kKeepAct8 = 2 };
 
-// K-elements of a pipeline stage, the unit of kb0 and kb1 (plain and swapped).
-constexpr int kLinK = 128, kLinKSwap = 64;
+// K-elements of a pipeline stage, the unit of kb0 and kb1.
+__host__ __device__ constexpr int lin_stage_k(int epi, bool swap) {
+  return swap || epi == kLinGluGrad ? 64 : 128;
+}
 constexpr int kLinMaps = 12;     // tensor maps of one launch
 constexpr int kLinProblems = 3;  // products of one launch
 
@@ -76,7 +78,7 @@ struct LinArgs {
   int kept_vec;          // rows of the kept tensors allow 16-byte access
   void *gate, *up;                          // bf16 values or 8-bit codes
   __nv_bfloat16 *gate_scale, *up_scale;     // 8-bit block scales
-  int map_gate, map_up;                     // kLinGlu, bf16: output maps (kept_vec)
+  int map_gate, map_up;                     // their maps, 32 x 32 boxes (kept_vec)
   int map_dup, map_h;                       // kLinGluGrad: output maps beside c_map (dgate)
   __nv_bfloat16 *dup, *h;                   // and their tensors (pitch c_ld)
   // kLinXent
@@ -90,7 +92,7 @@ size_t lin_partial_bytes();
 cudaError_t lin_prepare();  // once per device
 // Split the tiles of the last, partly filled wave along K (sets full_tiles ..
 // total_units from the products' tile counts).
-void lin_schedule(LinArgs& g, bool may_split, int clusters);
+void lin_schedule(LinArgs& g, int epi, int clusters);
 // Whether a product over `tokens` rows runs swapped, and its tokens per tile.
 bool lin_swaps(long long tokens, int epi, int* nt);
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,

@@ -78,6 +78,7 @@ ProductSpace take_product_space(Carve& c) {
 struct Launch {
   LinArgs g{};
   int n_maps = 0;
+  int k_box = 128;  // K rows in a box of an MN-major weight: a stage's
   bool ok = true;
 
   explicit Launch(const ProductSpace& s) {
@@ -114,30 +115,32 @@ struct Launch {
   int output_codes(const void* p, int64_t cols, int64_t rows) {
     return map(p, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE, 1);
   }
-  LinProblem& problem(int64_t rows, int64_t cols, int64_t k0, int64_t k1) {
+  LinProblem& problem(int epi, int64_t rows, int64_t cols, int64_t k0, int64_t k1) {
+    const int k = lin_stage_k(epi, g.swap != 0);
     LinProblem& P = g.prob[g.n_prob++];
     P.rows = int(rows);
     P.cols = int(cols);
     P.tiles_m = int(ceil_div(rows, 256));
     P.tiles_n = int(ceil_div(cols, 256));
-    P.kb0 = int(ceil_div(k0, kLinK));
-    P.kb1 = int(ceil_div(k1, kLinK));
+    P.kb0 = int(ceil_div(k0, k));
+    P.kb1 = int(ceil_div(k1, k));
     P.c_map = -1;
     return P;
   }
   // A product tokens x weight, swapped where that fits the token count better.
   LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
                             int64_t k1) {
-    LinProblem& P = problem(tokens, cols, k0, k1);
-    P.tiles_n = int(ceil_div(cols, cols_per_tile));
     int nt = 0;
     if (lin_swaps(tokens, epi, &nt)) {
       g.swap = 1;
       g.nt = nt;
+    }
+    k_box = lin_stage_k(epi, g.swap != 0);
+    LinProblem& P = problem(epi, tokens, cols, k0, k1);
+    P.tiles_n = int(ceil_div(cols, cols_per_tile));
+    if (g.swap) {
       P.tiles_m = P.tiles_n;
       P.tiles_n = int(ceil_div(tokens, nt));
-      P.kb0 = int(ceil_div(k0, kLinKSwap));
-      P.kb1 = int(ceil_div(k1, kLinKSwap));
     }
     return P;
   }
@@ -146,9 +149,20 @@ struct Launch {
   void operands(LinProblem& P, const bf16* tok, int64_t k, int64_t tok_ld, const bf16* w,
                 int64_t w_cols, int64_t w_rows, int64_t w_ld, bool k_major, bool second = false) {
     const int t = operand(tok, k, P.rows, tok_ld, g.swap ? g.nt / 2 : 128);
-    const int m = operand(w, w_cols, w_rows, w_ld, g.swap && !k_major ? kLinKSwap : 128);
+    const int m = operand(w, w_cols, w_rows, w_ld, k_major ? 128 : k_box);
     (second ? P.a1 : P.a0) = g.swap ? m : t;
     (second ? P.b1 : P.b0) = g.swap ? t : m;
+  }
+  // The kept gate and up, read and written in 32 x 32 chunks.
+  void kept_maps(const dmuon_ffn_shape& s) {
+    if (!g.kept_vec) return;
+    const bool codes = g.keep == kKeepAct8;
+    for (int i = 0; i < 2; ++i) {
+      const void* p = i == 0 ? g.gate : g.up;
+      (i == 0 ? g.map_gate : g.map_up) =
+          codes ? output_codes(p, s.ffn, s.tokens)
+                : output(static_cast<const bf16*>(p), s.ffn, s.tokens, s.ffn);
+    }
   }
   // C: TMA where its rows allow it, plain stores otherwise.
   void store_to(LinProblem& P, bf16* c, int64_t ld, bool store_epilogue = true) {
@@ -164,7 +178,7 @@ struct Launch {
   int run(int epi, bool a_mn, bool b_mn, int clusters, cudaStream_t s) {
     if (!ok) return DMUON_ERR_CUDA;
     g.n_maps = n_maps;
-    lin_schedule(g, epi != kLinXent, clusters);
+    lin_schedule(g, epi, clusters);
     return launch_lin(g, epi, a_mn, b_mn, clusters, s) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
   }
 };
@@ -250,7 +264,8 @@ void use_saved(LinArgs& g, const dmuon_ffn_shape& s, void* const* saved) {
     g.gate_scale = static_cast<bf16*>(saved[1]);
     g.up = saved[2];
     g.up_scale = static_cast<bf16*>(saved[3]);
-    g.kept_vec = s.ffn % 16 == 0 && aligned(g.gate, 16) && aligned(g.up, 16);
+    g.kept_vec = s.ffn % 16 == 0 && aligned(g.gate, 16) && aligned(g.up, 16) &&
+                 aligned(g.gate_scale, 8) && aligned(g.up_scale, 8);
   }
 }
 
@@ -321,13 +336,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     P.b1 = up;
     L.store_to(P, f.h, fp, false);
     use_saved(L.g, s, saved);
-    if (L.g.keep == kKeepBf16 && L.g.kept_vec) {
-      L.g.map_gate = L.output(static_cast<bf16*>(L.g.gate), s.ffn, s.tokens, s.ffn);
-      L.g.map_up = L.output(static_cast<bf16*>(L.g.up), s.ffn, s.tokens, s.ffn);
-    } else if (L.g.keep == kKeepAct8 && L.g.kept_vec) {
-      L.g.map_gate = L.output_codes(L.g.gate, s.ffn, s.tokens);
-      L.g.map_up = L.output_codes(L.g.up, s.ffn, s.tokens);
-    }
+    L.kept_maps(s);
     e = L.run_token(kLinGlu, true, clusters, st);
     if (e != DMUON_OK) return e;
   }
@@ -370,6 +379,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     L.g.map_dup = L.output(f.dup, s.ffn, s.tokens, fp);
     L.g.map_h = L.output(f.h, s.ffn, s.tokens, fp);
     use_saved(L.g, s, saved);
+    L.kept_maps(s);
     e = L.run_token(kLinGluGrad, false, clusters, st);
     if (e != DMUON_OK) return e;
   }
@@ -389,7 +399,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
-    LinProblem& P = L.problem(m, n, s.tokens, 0);
+    LinProblem& P = L.problem(kLinStore, m, n, s.tokens, 0);
     P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld);
     P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, fp);
     L.store_to(P, out[i], n);
@@ -513,7 +523,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     }
     // dweight += G^T h, in fp32 over the pieces
     Launch L(x.ps);
-    LinProblem& P = L.problem(s.vocab, s.hidden, n, 0);
+    LinProblem& P = L.problem(kLinStore, s.vocab, s.hidden, n, 0);
     P.a0 = L.operand(x.e, s.vocab, n, vp);
     P.b0 = L.operand(hp, s.hidden, n, h.ld);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);

@@ -84,7 +84,7 @@ DM_DEV uint2 act8_pack(const float (&v)[8], float& s) {
 DM_DEV void act8_unpack(const uint2& q, float s, float (&f)[8]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = s * float((signed char)(w[k >> 2] >> (8 * (k & 3))));
+  for (int k = 0; k < 8; ++k) f[k] = s * act8_int(w[k >> 2], k & 3);
 }
 template <bool BF16>
 DM_DEV void store8(void* out, long long at, bool vec, int n, const float (&f)[8]) {

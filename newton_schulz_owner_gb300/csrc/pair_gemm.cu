@@ -20,8 +20,8 @@
 // tile holds 256 of them.  Swapped, the weight's rows are M and the tokens are N,
 // and a tile holds `nt` tokens, a multiple of 32 chosen to fit: with few tokens the
 // launch streams the weights at the memory's rate instead of multiplying padding
-// (a stage is then 32 KB of weights and nt/2 token rows, and more stages fit), and
-// a ragged count wastes less of its last tile.  The accumulator's lanes are then
+// (a stage is then 16 KB of weights and nt/2 token rows, and up to ten fit), and a
+// ragged count wastes less of its last tile.  The accumulator's lanes are then
 // the weight's rows; each 32 x 32 chunk is turned in shared memory, and from there
 // on both orientations share the epilogue code: a lane holds one token.
 //
@@ -40,7 +40,12 @@
 // wave; the parts' fp32 accumulators go to the workspace, and a second, fully
 // parallel launch adds them in order and runs the epilogue on the sums.  (Letting
 // the last arriving CTA of a tile do that in the first launch serialises the reads:
-// 12 parts of a 160 x 256 tile took 25 us longer.)
+// dx of 301 tokens, 1536/8960, took 46 us that way and takes 22 + 4 this way.)
+//
+// Measured alone on one GB300 (2070 MHz, before the power cap bites): gate and up of
+// 8192 tokens, 4096/14336, 0.99 ms (1.94 PFLOP/s; cuBLAS's best product 1.90), the
+// down projection 0.50 ms; sustained, the backward's products run at 1.70 to 1.76
+// PFLOP/s (cuBLAS sustained 1.73).
 #include "act.cuh"
 #include "act8.cuh"
 #include "dmuon.h"
@@ -84,9 +89,10 @@ constexpr int kStrip = 8;
 
 // The tensor core's accumulation rounds toward zero, so a sum of K products loses
 // up to K/16 * 2^-25 of its size.  That is far below bf16 for an output that is
-// rounded to it, but not for the fp32 losses: the logits are accumulated in runs
-// of 512 K-elements, each drained and added in registers, rounded
-// to nearest.  The drains hide behind the next run's MMAs.
+// rounded to it, but not for the fp32 losses: the logits are accumulated in runs of
+// 512 K-elements, each drained and added in registers, rounded to nearest (error of
+// 777 tokens' losses against 64 bits 2.7e-6 without, 3.6e-7 with; fp32 products on the
+// CUDA cores 6e-7).  The drains hide behind the next run's MMAs: 1% of the time.
 constexpr int kRunElems = 512;
 
 // Workspace of the split parts.
@@ -346,54 +352,47 @@ DM_DEV float act8_block(float (&v)[32], int n, uint32_t (&w)[8]) {
   return s;
 }
 
-// 32 kept values of one row (columns c0 .. c0 + 31, n of them inside), fetched as
-// stored: their loads are issued a chunk ahead of their use.  `inner`: neither the
-// first nor the last row, so that the aligned words around an unaligned piece of it
-// lie inside the tensor.
+// 32 kept values of one row (columns c0 .. c0 + 31, n of them inside), as stored.
 struct Kept {
   uint4 q[4];
   float scale;
 };
+// From rows that are not 16-byte aligned.  `inner`: neither the first nor the last row,
+// so that the aligned words around a whole piece of it lie inside the tensor.
 DM_DEV void fetch_kept(const LinArgs& g, const void* base, const __nv_bfloat16* scales, int row,
                        int c0, int n, bool inner, Kept& k) {
+  const long long at = (long long)row * g.ffn + c0;
   if (g.keep == kKeepBf16) {
-    const __nv_bfloat16* p =
-        static_cast<const __nv_bfloat16*>(base) + (long long)row * g.ffn + c0;
-    if (g.kept_vec && n >= 32) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) k.q[u] = __ldcs(reinterpret_cast<const uint4*>(p) + u);
-    } else if (inner && n >= 32) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if (inner && n >= 32) {
       load_shifted<4>(p, k.q);
-    } else {
-      const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
-      uint32_t w[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = (2 * j < n ? uint32_t(e[2 * j]) : 0u) |
-               (2 * j + 1 < n ? uint32_t(e[2 * j + 1]) << 16 : 0u);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) k.q[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+      return;
     }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      w[j] = (2 * j < n ? uint32_t(p[2 * j]) : 0u) |
+             (2 * j + 1 < n ? uint32_t(p[2 * j + 1]) << 16 : 0u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      k.q[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
   } else {
-    const signed char* p = static_cast<const signed char*>(base) + (long long)row * g.ffn + c0;
+    const uint8_t* p = static_cast<const uint8_t*>(base) + at;
     const int blocks = (g.ffn + kActBlock - 1) / kActBlock;
     k.scale = __bfloat162float(scales[(long long)row * blocks + c0 / kActBlock]);
-    if (g.kept_vec && n >= 32) {
-      k.q[0] = __ldcs(reinterpret_cast<const uint4*>(p));
-      k.q[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
-    } else if (inner && n >= 32) {
+    if (inner && n >= 32) {
       uint4 t[2];
       load_shifted<2>(p, t);
       k.q[0] = t[0];
       k.q[1] = t[1];
-    } else {
-      uint32_t w[8] = {};
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) w[j / 4] |= uint32_t(uint8_t(p[j])) << (8 * (j & 3));
-      k.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      k.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      return;
     }
+    uint32_t w[8] = {};
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) w[j / 4] |= uint32_t(p[j]) << (8 * (j & 3));
+    k.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    k.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 DM_DEV void kept_values(const LinArgs& g, const Kept& k, int half, float (&v)[16]) {
@@ -1464,15 +1463,16 @@ cudaError_t lin_prepare() {
   return cudaSuccess;
 }
 
-// Swapped where that saves a tenth of the padded rows: at 7/8 of them it measured 3 to 7%
-// faster (block of 4096/14336, 400 to 1100 tokens), at all of them 2% slower.  The
-// cross entropy's epilogue costs more swapped: there a fifth (at 7/8 of the rows 1 to
-// 4% slower with 200 to 777 tokens, at 5/8 7% faster with 300).
+// Swapped where that saves a tenth of the padded rows: at 7/8 of them it measured 3 to
+// 7% faster (block of 4096/14336, 400 to 1100 tokens), at all of them 2% slower.  The
+// cross entropy's epilogue costs more swapped: there a fifth (at 7/8 of the rows 1 to 4%
+// slower with 200 to 777 tokens, at 5/8 7% faster with 300).
 bool lin_swaps(long long tokens, int epi, int* nt) {
   const long long plain = (tokens + kTile - 1) / kTile;  // tiles of 256 tokens, either way
   const long long fit = ((tokens + plain - 1) / plain + 31) / 32 * 32;
   *nt = int(fit);
-  return epi == kLinXent ? fit * 5 < kTile * 4 : fit * 10 < kTile * 9;
+  return epi == kLinXent ? tokens <= kXentSwapTokens && fit * 5 < kTile * 4
+                         : fit * 10 < kTile * 9;
 }
 
 // floor(2^32 / d) or one more: the quotient's estimate is off by one at most.

@@ -28,6 +28,8 @@ constexpr int kActBlock = 32;
 // Vocabulary entries whose exponentials share a reference maximum (plain and
 // swapped orientation).
 constexpr int kXentGroup = 128, kXentGroupSwap = 32;
+// The most tokens for which the logits run swapped (a workspace is sized by it).
+constexpr int kXentSwapTokens = 1024;
 
 // What a product's epilogue does with the fp32 accumulator.
 enum LinEpi {

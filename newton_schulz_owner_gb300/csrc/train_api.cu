@@ -20,8 +20,6 @@ constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxDim = int64_t(1) << 19,
 // bounds the group statistics.
 constexpr size_t kLogitBytes = size_t(2200) << 20;
 constexpr int64_t kLossTokens = 16384;
-// Above this many tokens a last tile of 256 wastes too little for lin_swaps().
-constexpr int64_t kSwapTokens = 1792;
 
 using bf16 = __nv_bfloat16;
 
@@ -439,11 +437,11 @@ XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   x.hidden = c.take<bf16>(size_t(s.tokens) * dp * 2);
   x.target_logit = c.take<float>(size_t(s.tokens) * 4);
   x.grad_scale = c.take<float>(4);
-  // swapped products have four times the groups, over at most kSwapTokens tokens
+  // swapped products have four times the groups, over at most kXentSwapTokens tokens
   x.stat = c.take<float2>(
       std::max(size_t(ceil_div(s.vocab, kXentGroup)) * size_t(up32(x.piece)),
                size_t(ceil_div(s.vocab, kXentGroupSwap)) *
-                   size_t(std::min(up32(x.piece), kSwapTokens))) * sizeof(float2));
+                   size_t(std::min<int64_t>(up32(x.piece), kXentSwapTokens))) * sizeof(float2));
   if (s.hidden % 8 != 0) x.weight = c.take<bf16>(size_t(s.vocab) * dp * 2);
   if (grads) {
     x.e = c.take<bf16>(size_t(x.piece) * size_t(pitch(s.vocab)) * 2);
@@ -504,7 +502,6 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
       L.g.target_logit = x.target_logit + t0;
       L.g.group_stat = x.stat;
       L.g.stat_ld = R.stat_ld;
-      if (L.g.swap && n > kSwapTokens) return DMUON_ERR_UNSUPPORTED;  // sized for fewer
       R.group = L.g.swap ? kXentGroupSwap : kXentGroup;
       e = L.run_token(kLinXent, true, clusters, st);
       if (e != DMUON_OK) return e;

@@ -11,6 +11,10 @@
 // Wg and the same 8 of Wu fill the 16) or per 16 output columns, so the blocks are
 // small and spread evenly; against tiles of 256 rows (pair_gemm.cu) nothing has to be
 // split along K and joined by another launch.
+// Measured for one token, 4096/14336: 38 us for 235 MB of Wg and Wu (6.2 TB/s, 0.92 of
+// the copy rate), 19 us for 117 MB of Wd.  Many blocks with two steps in flight beat
+// fewer with four or eight for the first (38 against 43 and 40 us); the second, with few
+// blocks, wants 16 warps of four (19 against 23 with eight, 20 with eight warps).
 #include "dmuon.h"
 #include "act.cuh"
 #include "launch.h"
@@ -19,8 +23,6 @@
 
 namespace dm {
 namespace {
-
-constexpr int kDepth = 4;
 
 DM_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                      uint32_t b1) {
@@ -31,7 +33,7 @@ DM_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool GLU, int WARPS>
+template <bool GLU, int WARPS, int kDepth>
 __global__ void __launch_bounds__(WARPS * 32) thin_kernel(const ThinArgs g) {
   __shared__ float red[WARPS][16][9];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,8 +117,8 @@ __global__ void __launch_bounds__(WARPS * 32) thin_kernel(const ThinArgs g) {
 
 cudaError_t launch_thin(const ThinArgs& g, bool glu, cudaStream_t s) {
   if (glu)
-    return launch_dependent(thin_kernel<true, 8>, unsigned((g.cols + 7) / 8), 256u, s, g);
-  return launch_dependent(thin_kernel<false, 16>, unsigned((g.cols + 15) / 16), 512u, s, g);
+    return launch_dependent(thin_kernel<true, 8, 2>, unsigned((g.cols + 7) / 8), 256u, s, g);
+  return launch_dependent(thin_kernel<false, 16, 4>, unsigned((g.cols + 15) / 16), 512u, s, g);
 }
 
 }  // namespace dm

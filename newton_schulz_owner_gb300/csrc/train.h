@@ -136,7 +136,8 @@ cudaError_t launch_act8_load(long long rows, long long cols, const signed char* 
                              const __nv_bfloat16* scales, void* out, long long ld, bool bf16,
                              cudaStream_t s);
 // Copies of bf16 matrices (src null: zeros), one launch; with `target`, rows of the
-// first whose target lies outside [0, vocab) become zeros.
+// first whose target lies outside [0, vocab) become zeros; with `grad_loss` also the
+// scale that the gradients of the logits are formed relative to.
 struct CopyArgs {
   static constexpr int kMost = 5;
   struct Mat {
@@ -150,6 +151,9 @@ struct CopyArgs {
   int n;
   const long long* target;
   long long vocab;
+  const float* grad_loss;  // of `tokens` tokens
+  long long tokens;
+  float* grad_scale;       // out: largest |grad_loss| of tokens with a target, 1 if 0
   void add(const __nv_bfloat16* src, long long src_ld, __nv_bfloat16* dst, long long dst_ld,
            long long rows, long long cols) {
     Mat& M = mat[n++];
@@ -173,9 +177,6 @@ struct XentRows {
   int group;                // vocabulary entries per group
   float *loss, *lse;
 };
-// *scale = the largest |grad_loss| of the tokens that have a target (1 if that is 0).
-cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,
-                              long long vocab, float* scale, cudaStream_t s);
 cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s);
 // Exponentials (fp16) to gradients of the logits (bf16), in place.
 cudaError_t launch_xent_grad(const XentRows& r, void* e, long long e_ld, cudaStream_t s);

@@ -468,6 +468,9 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     // reaches the weight's gradient, which sums over rows
     copies.target = tgt;
     copies.vocab = s.vocab;
+    copies.grad_loss = grad_loss;
+    copies.tokens = s.tokens;
+    copies.grad_scale = x.grad_scale;
     h = {x.hidden, pitch(s.hidden)};
     copies.add(static_cast<const bf16*>(hidden), h_ld, x.hidden, h.ld, s.tokens, s.hidden);
   } else {
@@ -476,9 +479,6 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
   const Readable w = readable(copies, weight, s.vocab, s.hidden, s.hidden, x.weight);
   e = run_copies(copies, st);
   if (e != DMUON_OK) return e;
-  if (grads &&
-      launch_grad_scale(grad_loss, tgt, s.tokens, s.vocab, x.grad_scale, st) != cudaSuccess)
-    return DMUON_ERR_CUDA;
   for (int64_t t0 = 0; t0 < s.tokens; t0 += x.piece) {
     const int64_t n = std::min(x.piece, s.tokens - t0);
     const bf16* hp = h.p + t0 * h.ld;

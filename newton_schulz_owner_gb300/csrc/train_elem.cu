@@ -218,12 +218,34 @@ DM_DEV bool live_target(const long long* target, long long row, long long vocab)
   return t >= 0 && t < vocab;
 }
 
+// The largest |grad_loss| of the tokens that have a target (1 if that is 0), by one block.
+DM_DEV void grad_scale(const CopyArgs& g) {
+  __shared__ float top[kThreads / 32];
+  float m = 0.f;
+#pragma unroll 4
+  for (long long t = threadIdx.x; t < g.tokens; t += kThreads)
+    if (live_target(g.target, t, g.vocab)) m = fmaxf(m, fabsf(g.grad_loss[t]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, top[w]);
+    *g.grad_scale = m > 0.f ? m : 1.f;
+  }
+}
+
 // Up to CopyArgs::kMost matrices to rows that TMA can read, one launch.  A thread
 // moves 8 columns; the threads run through rows and columns alike, so that narrow
 // matrices fill them too.  src == nullptr: zeros.
 __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_constant__ CopyArgs g) {
   grid_launch_dependents();
   grid_wait();
+  if (g.grad_loss != nullptr && blockIdx.x + 1 == gridDim.x) {  // an extra block
+    grad_scale(g);
+    return;
+  }
   int m = 0;
   while (m + 1 < g.n && blockIdx.x >= g.mat[m + 1].block_begin) ++m;
   const CopyArgs::Mat& M = g.mat[m];
@@ -262,28 +284,6 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_consta
       for (int j = 0; j < 8; ++j)
         if (j < n) reinterpret_cast<uint16_t*>(d)[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
     }
-  }
-}
-
-__global__ void __launch_bounds__(1024) grad_scale_kernel(const float* grad_loss,
-                                                          const long long* target,
-                                                          long long tokens, long long vocab,
-                                                          float* scale) {
-  __shared__ float top[32];
-  grid_launch_dependents();
-  grid_wait();
-  float m = 0.f;
-  for (long long t = threadIdx.x; t < tokens; t += 1024)
-    if (live_target(target, t, vocab)) m = fmaxf(m, fabsf(grad_loss[t]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    m = top[threadIdx.x];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (threadIdx.x == 0) *scale = m > 0.f ? m : 1.f;
   }
 }
 
@@ -450,13 +450,9 @@ cudaError_t launch_copy_rows(CopyArgs& g, cudaStream_t s) {
     const long long units = M.rows * ((M.cols + 7) / 8);
     blocks += unsigned((units + 4 * kThreads - 1) / (4 * kThreads));
   }
+  if (g.grad_loss != nullptr) ++blocks;
   if (blocks == 0) return cudaSuccess;
   return launch_dependent(copy_rows_kernel, blocks, unsigned(kThreads), s, g);
-}
-
-cudaError_t launch_grad_scale(const float* grad_loss, const long long* target, long long tokens,
-                              long long vocab, float* scale, cudaStream_t s) {
-  return launch_dependent(grad_scale_kernel, 1u, 1024u, s, grad_loss, target, tokens, vocab, scale);
 }
 
 cudaError_t launch_xent_rows(const XentRows& r, cudaStream_t s) {

@@ -193,7 +193,9 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
         raise_abort(g.err, abort_flag);
         return;
       }
-      if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], uint32_t(2 * bytes));
+      if (rank == 0)
+        mbar_arrive_expect_tx(&full_bar[stage],
+                              uint32_t(A_MN && B_MN ? 8 * 128 * g.k_rows : 2 * bytes));
       const uint32_t bar = leader_full + uint32_t(stage) * 8u;
       uint8_t* a = sStage + stage * bytes;
       uint8_t* b = a + St::a_bytes;
@@ -271,6 +273,7 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
         const uint64_t bd = b_desc + uint64_t(uint32_t(stage) * step);
 #pragma unroll
         for (int k = 0; k < St::k / 16; ++k) {
+          if (A_MN && B_MN && k * 16 >= g.k_rows) break;
           const uint64_t ao = A_MN
                                   ? uint64_t(k) * (2048u >> 4)
                                   : uint64_t(k >> 2) * (16384u >> 4) + uint64_t(k & 3) * (32u >> 4);

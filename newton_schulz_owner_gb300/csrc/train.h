@@ -64,6 +64,7 @@ struct LinArgs {
   LinProblem prob[kLinProblems];
   int n_prob, n_maps;
   int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
+  int k_rows;            // weight gradients: tokens per K block (128, or all if fewer)
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;
   unsigned split_magic;

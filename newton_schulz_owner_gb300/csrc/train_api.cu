@@ -125,6 +125,13 @@ struct Launch {
     P.c_map = -1;
     return P;
   }
+  // Tokens in a K block of a weight gradient.  A box takes TMA as long for rows past the
+  // tensor's end as for rows inside, so with few tokens it has just their number (5
+  // tokens, 3584 x 152064: 212 us with boxes of 128 rows, 167 with 16).
+  int token_rows(int64_t tokens) {
+    g.k_rows = tokens <= 64 ? int(ceil_div(tokens, 16) * 16) : 128;
+    return g.k_rows;
+  }
   // A product tokens x weight, swapped where that fits the token count better.
   LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
                             int64_t k1) {
@@ -392,14 +399,15 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
   Launch L(f.ps);
-  const int mx = L.operand(xr.p, s.hidden, s.tokens, xr.ld);
+  const int box = L.token_rows(s.tokens);
+  const int mx = L.operand(xr.p, s.hidden, s.tokens, xr.ld, box);
   const bf16* left[3] = {f.dgate, f.dup, dyr.p};
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
     LinProblem& P = L.problem(kLinStore, m, n, s.tokens, 0);
-    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld);
-    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, fp);
+    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld, box);
+    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, fp, box);
     L.store_to(P, out[i], n);
   }
   return L.run(kLinStore, true, true, clusters, st);
@@ -521,8 +529,9 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     // dweight += G^T h, in fp32 over the pieces
     Launch L(x.ps);
     LinProblem& P = L.problem(kLinStore, s.vocab, s.hidden, n, 0);
-    P.a0 = L.operand(x.e, s.vocab, n, vp);
-    P.b0 = L.operand(hp, s.hidden, n, h.ld);
+    const int box = L.token_rows(n);
+    P.a0 = L.operand(x.e, s.vocab, n, vp, box);
+    P.b0 = L.operand(hp, s.hidden, n, h.ld, box);
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
     L.g.scale = x.grad_scale;
     L.g.sum = x.sum;

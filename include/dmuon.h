@@ -270,6 +270,10 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
  *  - Workspaces are 256-byte aligned; one sized for `tokens` serves fewer.
  *    Device-side failures go to its error word (dmuon_stream_status); zero the
  *    first 256 bytes once.
+ *  - Every element lies at a multiple of its size (2 bytes for bf16, 4 for fp32, 8
+ *    for targets); DMUON_ERR_ALIGNMENT otherwise.
+ *  - The calls can be captured into a CUDA graph; make one call on the device
+ *    before the first capture.
  */
 
 /* Activation of the gated feed-forward block. */

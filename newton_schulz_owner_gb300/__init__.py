@@ -1,4 +1,6 @@
-"""DMuon owner-side Muon step on GB300 (sm_103a).
+"""DMuon owner-side Muon step on GB300 (sm_103a), and the operators that make the
+gradients it takes (gated feed-forward block, cross entropy over a vocabulary, 8-bit
+activations).
 
 The compute path lives in the C-ABI library ``libdmuon.so`` (CUDA kernels for
 sm_103a, declared in ``include/dmuon.h``); :mod:`newton_schulz_owner_gb300.dmuon`

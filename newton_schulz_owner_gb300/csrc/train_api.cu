@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 namespace dm {
@@ -31,6 +32,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t pitch(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool all_aligned(size_t a, std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned(p, a)) return false;
+  return true;
+}
 
 // Ready the current device: the products' shared memory opt-in, once.
 int device_ready(int* max_clusters) {
@@ -274,7 +280,12 @@ void use_saved(LinArgs& g, const dmuon_ffn_shape& s, void* const* saved) {
   }
 }
 
-int ffn_weight_alignment(const dmuon_ffn_shape& s, const void* wg, const void* wu, const void* wd) {
+// Every bf16 element at an even address; weights at 16 bytes where rows allow TMA.
+int ffn_alignment(const dmuon_ffn_shape& s, const void* wg, const void* wu, const void* wd,
+                  void* const* saved, std::initializer_list<const void*> others) {
+  if (!all_aligned(2, {wg, wu, wd}) || !all_aligned(2, others)) return DMUON_ERR_ALIGNMENT;
+  if (s.save == DMUON_SAVE_BF16 && !all_aligned(2, {saved[0], saved[1]})) return DMUON_ERR_ALIGNMENT;
+  if (s.save == DMUON_SAVE_ACT8 && !all_aligned(2, {saved[1], saved[3]})) return DMUON_ERR_ALIGNMENT;
   if (s.hidden % 8 == 0 && (!aligned(wg, 16) || !aligned(wu, 16))) return DMUON_ERR_ALIGNMENT;
   if (s.ffn % 8 == 0 && !aligned(wd, 16)) return DMUON_ERR_ALIGNMENT;
   return DMUON_OK;
@@ -605,7 +616,7 @@ int dmuon_ffn_forward(const dmuon_ffn_shape* shape, const void* x, int64_t x_ld,
       !saved_ok(shape->save, saved))
     return DMUON_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return DMUON_ERR_ALIGNMENT;
-  const int st = ffn_weight_alignment(*shape, w_gate, w_up, w_down);
+  const int st = ffn_alignment(*shape, w_gate, w_up, w_down, saved, {x, y});
   if (st != DMUON_OK) return st;
   if (ws_bytes < dmuon_ffn_workspace_bytes(shape, 0)) return DMUON_ERR_WORKSPACE;
   return ffn_forward(*shape, x, x_ld, w_gate, w_up, w_down, y, y_ld, saved, workspace, stream);
@@ -624,7 +635,12 @@ int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_
        x_ld < shape->hidden || dx_ld < shape->hidden || !saved_ok(shape->save, saved)))
     return DMUON_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return DMUON_ERR_ALIGNMENT;
-  const int st = ffn_weight_alignment(*shape, w_gate, w_up, w_down);
+  const dmuon_ffn_shape& sh = *shape;
+  void* const none[4] = {};
+  const int st = sh.tokens > 0 ? ffn_alignment(sh, w_gate, w_up, w_down, saved,
+                                               {dy, x, dx, dw_gate, dw_up, dw_down})
+                               : ffn_alignment(sh, w_gate, w_up, w_down, none,
+                                               {dw_gate, dw_up, dw_down});
   if (st != DMUON_OK) return st;
   if (ws_bytes < dmuon_ffn_workspace_bytes(shape, 1)) return DMUON_ERR_WORKSPACE;
   return ffn_backward(*shape, dy, dy_ld, x, x_ld, w_gate, w_up, w_down, saved, dx, dx_ld, dw_gate,
@@ -651,7 +667,12 @@ int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden
     if (grads && (grad_loss == nullptr || dhidden == nullptr || dhidden_ld < shape->hidden))
       return DMUON_ERR_INVALID_ARG;
   }
-  if (!aligned(workspace, 256) || (shape->hidden % 8 == 0 && !aligned(weight, 16)))
+  if (!aligned(workspace, 256) || !aligned(weight, shape->hidden % 8 == 0 ? 16 : 2) ||
+      !aligned(dweight, 2))
+    return DMUON_ERR_ALIGNMENT;
+  if (shape->tokens > 0 &&
+      (!all_aligned(2, {hidden, dhidden}) || !all_aligned(4, {loss, lse, grad_loss}) ||
+       !aligned(target, 8)))
     return DMUON_ERR_ALIGNMENT;
   if (ws_bytes < dmuon_xent_workspace_bytes(shape, grads ? 1 : 0)) return DMUON_ERR_WORKSPACE;
   if (shape->tokens == 0 && grads) {

@@ -74,6 +74,13 @@ def test_ffn_refuses_bad_arguments(dm):
     assert fwd(saved=None) == bad and fwd(saved=hole) == bad
     assert fwd(wg=P + 2) == dm.ERR_ALIGNMENT and fwd(wd=P + 8) == dm.ERR_ALIGNMENT
     assert fwd(ws=W + 16) == dm.ERR_ALIGNMENT
+    odd = (ctypes.c_void_p * 4)(P + 1, P, P, P)
+    assert fwd(x=P + 1) == dm.ERR_ALIGNMENT and fwd(y=P + 1) == dm.ERR_ALIGNMENT
+    assert fwd(saved=odd) == dm.ERR_ALIGNMENT and bwd(saved=odd) == dm.ERR_ALIGNMENT
+    assert fwd(shape=(4, 65, 96, 0, 1), x_ld=65, y_ld=65, wg=P + 1) == dm.ERR_ALIGNMENT
+    scale = (ctypes.c_void_p * 4)(P, P + 1, P, P)
+    assert fwd(shape=(4, 64, 96, 0, 2), saved=scale) == dm.ERR_ALIGNMENT
+    assert bwd(dy=P + 1) == dm.ERR_ALIGNMENT and bwd(dwd=P + 1) == dm.ERR_ALIGNMENT
     assert fwd(nb=-1) == dm.ERR_WORKSPACE
     assert fwd(shape=(0, 64, 96, 0, 0), x=None, y=None) == dm.OK       # no tokens, nothing to do
     assert bwd(shape=(4, 64, 96, 0, 0)) == bad                          # nothing was kept
@@ -100,6 +107,9 @@ def test_xent_refuses_bad_arguments(dm):
         assert call(**{k: None}) == bad, k
     assert call(ld=63) == bad and call(dh_ld=63) == bad
     assert call(w=P + 2) == dm.ERR_ALIGNMENT and call(ws=W + 128) == dm.ERR_ALIGNMENT
+    for k, v in {"h": P + 1, "t": P + 4, "gl": P + 2, "loss": P + 2, "lse": P + 1, "dh": P + 1,
+                 "dw": P + 1}.items():
+        assert call(**{k: v}) == dm.ERR_ALIGNMENT, k
     assert call(nb=-1) == dm.ERR_WORKSPACE
     assert call(shape=(0, 64, 96), gl=None, dh=None, dw=None, h=None) == dm.OK
 

@@ -33,7 +33,9 @@ DM_DEV void act_both(float x, float& a, float& da) {
   } else {
     const float s = sigmoid(1.59576912f * fmaf(0.044715f * x * x, x, x));
     a = x * s;
-    da = fmaf(x * s * (1.f - s), 1.59576912f * fmaf(0.134145f * x, x, 1.f), s);
+    // the polynomial is bounded: past 1e19 it overflows where s (1 - s) is 0
+    const float poly = fminf(fmaf(0.134145f * x, x, 1.f), 1e30f);
+    da = fmaf(x * s * (1.f - s), 1.59576912f * poly, s);
   }
 }
 

@@ -270,6 +270,33 @@ def test_ffn_nan_stays_in_its_token(dm):
     assert bad[5] and int(bad.sum()) == 1 and torch.isnan(y[5]).all()
 
 
+def test_ffn_gradient_at_saturated_gates(dm):
+    """Kept gates of any finite size: act' is 0 or 1 there, whatever its terms overflow to."""
+    t, d, f = 40, 64, 96
+    c = ffn_case(16, t, d, f)
+    gate, up = Draw(17)((t, f)), Draw(18)((t, f))
+    big = torch.tensor([40.0, 1e4, 1e13, 1e20, 3e38], device="cuda").to(torch.bfloat16)
+    gate[::2, :5], gate[1::2, 5:10] = -big, -big       # act = act' = 0
+    up[:, 10:15], gate[:, 10:15] = 0, big              # act' = 1, h = 0
+    c["dy"][:] = c["dy"].abs()
+    c["wd"][:, 10:15] = 0                               # and dup = dh act = 0
+    for kind, n in ACTS.items():
+        op = dm.GatedFFN(t, d, f, activation=n)
+        ref = oracle.ffn_backward(np64(c["dy"]), np64(c["x"]), np64(c["wg"]), np64(c["wu"]),
+                                  np64(c["wd"]), np64(gate), np64(up), kind)
+        dx = torch.empty_like(c["x"])
+        dw = [torch.empty_like(c[k]) for k in ("wg", "wu", "wd")]
+        op.backward(c["dy"], c["x"], c["wg"], c["wu"], c["wd"], (gate, up), dx, *dw)
+        assert op.status() == dm.OK
+        a, da = oracle.act(kind, np64(gate))
+        dh, ax = np64(c["dy"]) @ np64(c["wd"]), np.abs(np64(c["x"]))
+        dg, du = np.abs(dh * np64(up) * da), np.abs(dh * a)
+        near(dx, ref["dx"], kind, dg @ np.abs(np64(c["wg"])) + du @ np.abs(np64(c["wu"])))
+        near(dw[0], ref["dw_gate"], kind, dg.T @ ax)
+        near(dw[1], ref["dw_up"], kind, du.T @ ax)
+        near(dw[2], ref["dw_down"], kind, np.abs(np64(c["dy"])).T @ np.abs(a * np64(up)))
+
+
 def test_ffn_no_tokens(dm):
     op = dm.GatedFFN(4, 64, 96)
     c = ffn_case(15, 4, 64, 96)

@@ -218,13 +218,18 @@ DM_DEV bool live_target(const long long* target, long long row, long long vocab)
   return t >= 0 && t < vocab;
 }
 
-// The largest |grad_loss| of the tokens that have a target (1 if that is 0), by one block.
+// The largest finite |grad_loss| of the tokens that have a target (1 if that is 0), by one
+// block.  An infinite one stays infinite relative to it and spoils only its own token's
+// gradients, which an infinite scale would spread over all.
 DM_DEV void grad_scale(const CopyArgs& g) {
   __shared__ float top[kThreads / 32];
   float m = 0.f;
 #pragma unroll 4
   for (long long t = threadIdx.x; t < g.tokens; t += kThreads)
-    if (live_target(g.target, t, g.vocab)) m = fmaxf(m, fabsf(g.grad_loss[t]));
+    if (live_target(g.target, t, g.vocab)) {
+      const float f = fabsf(g.grad_loss[t]);
+      if (f < INFINITY) m = fmaxf(m, f);
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;

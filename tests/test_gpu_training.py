@@ -430,6 +430,28 @@ def test_xent_nan_and_infinite_logits_stay_in_their_token(dm):
     assert bad[3] and bad[9] and int(bad.sum()) == 2
 
 
+def test_xent_infinite_weight_of_one_token(dm):
+    """An overflowed grad_loss reaches its own row of dhidden and every row of dweight
+    that its token weighs in, no other row of dhidden."""
+    t, d, v = 70, 64, 300
+    h, w, target, gl = xent_case(27, t, d, v)
+    op = dm.LinearXent(t, d, v)
+    outs = []
+    for bad in (0.0, float("inf"), float("nan")):
+        gl[5] = bad
+        loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        op.loss_and_grads(h, w, target, gl, loss, lse, dh, dw)
+        assert op.status() == dm.OK
+        outs.append((loss, lse, dh, dw))
+    others = torch.arange(t, device="cuda") != 5
+    assert not outs[0][2][5].any() and torch.isfinite(outs[0][3]).all()
+    for loss, lse, dh, dw in outs[1:]:
+        assert torch.equal(loss, outs[0][0]) and torch.equal(lse, outs[0][1])
+        assert torch.equal(dh[others], outs[0][2][others])
+        assert not torch.isfinite(dh[5]).any() and not torch.isfinite(dw).any()
+
+
 def test_xent_in_several_pieces(dm):
     """A vocabulary so large that 300 tokens take two pieces (256 tokens at a time)."""
     t, d, v = 300, 8, 1 << 22

@@ -487,6 +487,106 @@ def test_xent_no_tokens(dm):
     assert op.status() == dm.OK and not dw.any()
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_act8_offsets_past_32_bits(dm):
+    rows, cols = 70000, 65536                 # 4.6e9 elements
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = Draw(31)((3, cols))
+    codes, scales = dm.act8_empty(rows, cols)
+    dm.act8_save(x, codes, scales)
+    small = dm.act8_empty(3, cols)
+    dm.act8_save(x[-3:], *small)
+    assert torch.equal(codes[-3:], small[0]) and torch.equal(scales[-3:], small[1])
+    assert not codes[:-3].any() and not scales[:-3].any()
+    want = torch.empty_like(x[-3:])
+    dm.act8_load(*small, want)
+    x.fill_(SENTINEL)
+    dm.act8_load(codes, scales, x)
+    assert torch.equal(x[-3:], want) and not x[:-3].any()
+    del codes, scales
+    # three rows of odd length, 2^32 elements and more between the first and the last
+    wide = x.view(-1).as_strided((3, 2049), (2200000001, 1))
+    wide.copy_(Draw(32)((3, 2049)))
+    codes, scales = dm.act8_empty(3, 2049)
+    dm.act8_save(wide, codes, scales)
+    want_c, want_s = oracle.act8_codes(np64(wide))
+    assert np.array_equal(np64(codes), want_c) and np.array_equal(np64(scales), want_s)
+    wide.fill_(SENTINEL)
+    dm.act8_load(codes, scales, wide)
+    back = oracle.act8_values(want_c, want_s)
+    assert np.all(np.abs(np64(wide) - back) <= U * np.abs(back))
+
+
+@pytest.mark.parametrize("save", [1, 2])
+@pytest.mark.parametrize("f", [18944, 18949])
+def test_ffn_offsets_past_32_bits(dm, save, f):
+    """More than 2^31 kept elements, 2^32 bytes of each: only the last tokens weigh."""
+    t, d, n = 120000, 64, 300
+    c = ffn_case(33, n, d, f)
+    op = dm.GatedFFN(t, d, f, save=save)
+    x, dy = (torch.zeros((t, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-n:], dy[-n:] = c["x"], c["dy"]
+    y, saved = torch.empty_like(x), op.empty_saved(t)
+    op.forward(x, c["wg"], c["wu"], c["wd"], y, saved)
+    assert op.status() == dm.OK and not y[:-n].any()
+    fwd = oracle.ffn_forward(np64(c["x"]), np64(c["wg"]), np64(c["wu"]), np64(c["wd"]))
+    near(y[-n:], fwd["y"], "y", np.abs(fwd["h"]) @ np.abs(np64(c["wd"])).T)
+    last = tuple(s[-n:] for s in saved)
+    check_kept(dm, op, last, fwd, c, f)
+    gate, up = kept_values(op, dm, last, n)
+    ref = oracle.ffn_backward(np64(c["dy"]), np64(c["x"]), np64(c["wg"]), np64(c["wu"]),
+                              np64(c["wd"]), gate, up)
+    dw = [torch.empty_like(c[k]) for k in ("wg", "wu", "wd")]
+    op.backward(dy, x, c["wg"], c["wu"], c["wd"], saved, y, *dw)
+    assert op.status() == dm.OK and not y[:-n].any()
+    a, da = oracle.act("silu", gate)
+    dh, ax = np64(c["dy"]) @ np64(c["wd"]), np.abs(np64(c["x"]))
+    dg, du = np.abs(dh * up * da), np.abs(dh * a)
+    near(y[-n:], ref["dx"], "dx", dg @ np.abs(np64(c["wg"])) + du @ np.abs(np64(c["wu"])))
+    near(dw[0], ref["dw_gate"], "dw_gate", dg.T @ ax)
+    near(dw[1], ref["dw_up"], "dw_up", du.T @ ax)
+    near(dw[2], ref["dw_down"], "dw_down", np.abs(np64(c["dy"])).T @ np.abs(a * up))
+
+
+@pytest.mark.parametrize("t", [40, 300])
+@pytest.mark.parametrize("d", [1032, 1033])
+def test_xent_offsets_past_32_bits(dm, t, d):
+    """A head of 4.3e9 elements, zero but for its last rows, which hold the targets;
+    300 tokens take two pieces."""
+    v, n = 1 << 22, 500
+    h, tail, target, gl = xent_case(34, t, d, n, 2.0)
+    tail = (tail.float() * 4).to(torch.bfloat16)
+    w = torch.zeros((v, d), dtype=torch.bfloat16, device="cuda")
+    w[-n:] = tail
+    op = dm.LinearXent(t, d, v)
+    loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    op.loss_and_grads(h, w, target + (v - n), gl, loss, lse, dh, dw)
+    assert op.status() == dm.OK
+    hd, wd, gd = np64(h), np64(tail), np64(gl)
+    z = hd @ wd.T
+    norm = np.log(np.exp(z).sum(1) + (v - n))
+    at = np.arange(t), target.cpu().numpy()
+    bound = loss_bound(hd, wd, norm)
+    assert np.all(np.abs(np64(lse) - norm) <= bound)
+    assert np.all(np.abs(np64(loss) - (norm - z[at])) <= bound)
+    p = np.exp(z - norm[:, None])
+    p[at] -= 1
+    g = gd[:, None] * p
+    # what the roundings leave is in grad_mass: 1.25 |G| and 2^-16 grad_loss of each entry
+    room = gd[:, None] * (1.25 * np.abs(p) + 2.0 ** -16)
+    near(dh, g @ wd, "dhidden", room @ np.abs(wd))
+    near(dw[-n:], g.T @ hd, "dweight", room.T @ np.abs(hd))
+    rest = (gd * np.exp(-norm)) @ hd           # the same for every zero row
+    first = np64(dw[0])
+    assert np.all(np.abs(first - rest) <= 1.01 * U * np.abs(rest)
+                  + U * ((gd * np.exp(-norm) * 1.25 + gd * 2.0 ** -25) @ np.abs(hd)))
+    # all the same, but for those whose exponentials are taken relative to a tail row
+    same = (v - n) // 256 * 256
+    for lo in range(0, same, 1 << 19):
+        assert (dw[lo:min(lo + (1 << 19), same)] == dw[0]).all()
+
+
 # ------------------------------------------------------------------ streams, graphs, repeats
 def test_results_repeat_bit_for_bit_on_another_stream_and_in_a_graph(dm):
     t, d, f, v = 333, 256, 520, 2000

@@ -185,9 +185,10 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
                           : (EPI == kLinGlu ? U.tj * kHalf : U.tj * kTile + int(rank) * kHalf);
     for (int kb = U.kb_lo; kb < U.kb_hi; ++kb) {
       const bool second = EPI != kLinGlu && kb >= P.kb0;
-      const CUtensorMap* mapA = &g.maps[second ? P.a1 : P.a0];
-      const CUtensorMap* mapB =
-          &g.maps[EPI == kLinGlu && !SWAP ? (rank == 0 ? P.b0 : P.b1) : (second ? P.b1 : P.b0)];
+      const bool tail = A_MN && B_MN && kb == P.kb0 - 1;
+      const CUtensorMap* mapA = &g.maps[second || tail ? P.a1 : P.a0];
+      const CUtensorMap* mapB = &g.maps[EPI == kLinGlu && !SWAP ? (rank == 0 ? P.b0 : P.b1)
+                                                                : (second || tail ? P.b1 : P.b0)];
       const int k0 = (second ? kb - P.kb0 : kb) * St::k;
       if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) {
         raise_abort(g.err, abort_flag);
@@ -195,7 +196,7 @@ DM_DEV void producer(const LinArgs& g, uint32_t rank, uint8_t* sStage, uint64_t*
       }
       if (rank == 0)
         mbar_arrive_expect_tx(&full_bar[stage],
-                              uint32_t(A_MN && B_MN ? 8 * 128 * g.k_rows : 2 * bytes));
+                              uint32_t(tail ? 8 * 128 * g.k_tail : 2 * bytes));
       const uint32_t bar = leader_full + uint32_t(stage) * 8u;
       uint8_t* a = sStage + stage * bytes;
       uint8_t* b = a + St::a_bytes;
@@ -251,6 +252,7 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
   bool ok = true;
   for (int u = int(cluster_id_x()); ok && u < g.total_units; u += clusters) {
     const Unit U = decode_unit(g, u);
+    const int last = g.prob[U.prob].kb0 - 1;
     for (int lo = U.kb_lo; ok && lo < U.kb_hi; ++it) {
       const int hi = EPI == kLinXent ? min(lo + kRunElems / St::k, U.kb_hi) : U.kb_hi;
       const int acc = it & 1;
@@ -271,9 +273,10 @@ DM_DEV void mma_issuer(const LinArgs& g, uint8_t* sStage, uint64_t* full_bar, ui
         tc_fence_after();
         const uint64_t ad = a_desc + uint64_t(uint32_t(stage) * step);
         const uint64_t bd = b_desc + uint64_t(uint32_t(stage) * step);
+        const int k_rows = A_MN && B_MN && kb == last ? g.k_tail : St::k;
 #pragma unroll
         for (int k = 0; k < St::k / 16; ++k) {
-          if (A_MN && B_MN && k * 16 >= g.k_rows) break;
+          if (A_MN && B_MN && k * 16 >= k_rows) break;
           const uint64_t ao = A_MN
                                   ? uint64_t(k) * (2048u >> 4)
                                   : uint64_t(k >> 2) * (16384u >> 4) + uint64_t(k & 3) * (32u >> 4);

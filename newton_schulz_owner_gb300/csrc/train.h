@@ -44,7 +44,7 @@ enum LinKeep { kKeepNone = 0, kKeepBf16 = 1, kKeepAct8 = 2 };
 __host__ __device__ constexpr int lin_stage_k(int epi, bool swap) {
   return swap || epi == kLinGluGrad ? 64 : 128;
 }
-constexpr int kLinMaps = 12;     // tensor maps of one launch
+constexpr int kLinMaps = 13;     // tensor maps of one launch
 constexpr int kLinProblems = 3;  // products of one launch
 
 struct LinProblem {
@@ -53,7 +53,8 @@ struct LinProblem {
   int kb0, kb1;          // K blocks from the first and the second operand pair
   int tile_begin;        // first tile of this product in the launch
   unsigned strip_magic, last_magic;  // division by the tiles of a strip, by the last strip's rows
-  int a0, b0, a1, b1;    // operand maps (kLinGlu: gate's weight b0, up's b1; swapped a0, a1)
+  int a0, b0, a1, b1;    // operand maps (kLinGlu: gate's weight b0, up's b1; swapped a0, a1;
+                         // weight gradients: a1, b1 for the last K block)
   int c_map;             // output map, or -1: c is written with plain stores
   __nv_bfloat16* c;
   long long c_ld;
@@ -64,7 +65,7 @@ struct LinArgs {
   LinProblem prob[kLinProblems];
   int n_prob, n_maps;
   int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
-  int k_rows;            // weight gradients: tokens per K block (128, or all if fewer)
+  int k_tail;            // weight gradients: tokens in the last K block (a multiple of 16)
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;
   unsigned split_magic;
@@ -87,8 +88,8 @@ struct LinArgs {
   // kLinXent
   const long long* target;
   float* target_logit;   // one per token
-  float2* group_stat;    // (max logit * log2 e, sum of 2^(logit * log2 e - that)) per
-  long long stat_ld;     // [group][token], pitch stat_ld
+  float2* group_stat;    // (max logit, sum of exp(logit - that)) per [group][token]
+  long long stat_ld;     // pitch of a group
 };
 
 size_t lin_partial_bytes();

@@ -131,12 +131,26 @@ struct Launch {
     P.c_map = -1;
     return P;
   }
-  // Tokens in a K block of a weight gradient.  A box takes TMA as long for rows past the
-  // tensor's end as for rows inside, so with few tokens it has just their number (5
-  // tokens, 3584 x 152064: 212 us with boxes of 128 rows, 167 with 16).
-  int token_rows(int64_t tokens) {
-    g.k_rows = tokens <= 64 ? int(ceil_div(tokens, 16) * 16) : 128;
-    return g.k_rows;
+  // A weight gradient: rows x cols = left^T right, summed over the tokens.  A box takes
+  // TMA as long for rows past the tensor's end as for rows inside, so the last K block has
+  // maps of its own, with just its rows (5 tokens, 3584 x 152064: 212 us with boxes of 128
+  // rows, 167 with 16).
+  struct TokenOperand {
+    int body, tail;
+  };
+  TokenOperand token_operand(const bf16* p, int64_t cols, int64_t tokens, int64_t ld) {
+    g.k_tail = int(ceil_div((tokens - 1) % 128 + 1, 16) * 16);
+    const int tail = operand(p, cols, tokens, ld, g.k_tail);
+    return {tokens <= 128 || g.k_tail == 128 ? tail : operand(p, cols, tokens, ld), tail};
+  }
+  LinProblem& weight_problem(int64_t rows, int64_t cols, int64_t tokens, TokenOperand left,
+                             TokenOperand right) {
+    LinProblem& P = problem(kLinStore, rows, cols, tokens, 0);
+    P.a0 = left.body;
+    P.a1 = left.tail;
+    P.b0 = right.body;
+    P.b1 = right.tail;
+    return P;
   }
   // A product tokens x weight, swapped where that fits the token count better.
   LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
@@ -410,16 +424,14 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
   Launch L(f.ps);
-  const int box = L.token_rows(s.tokens);
-  const int mx = L.operand(xr.p, s.hidden, s.tokens, xr.ld, box);
+  const Launch::TokenOperand ox = L.token_operand(xr.p, s.hidden, s.tokens, xr.ld),
+                             oh = L.token_operand(f.h, s.ffn, s.tokens, fp);
   const bf16* left[3] = {f.dgate, f.dup, dyr.p};
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
   for (int i = 0; i < 3; ++i) {
     const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
-    LinProblem& P = L.problem(kLinStore, m, n, s.tokens, 0);
-    P.a0 = L.operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld, box);
-    P.b0 = i < 2 ? mx : L.operand(f.h, s.ffn, s.tokens, fp, box);
-    L.store_to(P, out[i], n);
+    const Launch::TokenOperand ol = L.token_operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld);
+    L.store_to(L.weight_problem(m, n, s.tokens, ol, i < 2 ? ox : oh), out[i], n);
   }
   return L.run(kLinStore, true, true, clusters, st);
 }
@@ -539,10 +551,8 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     }
     // dweight += G^T h, in fp32 over the pieces
     Launch L(x.ps);
-    LinProblem& P = L.problem(kLinStore, s.vocab, s.hidden, n, 0);
-    const int box = L.token_rows(n);
-    P.a0 = L.operand(x.e, s.vocab, n, vp, box);
-    P.b0 = L.operand(hp, s.hidden, n, h.ld, box);
+    LinProblem& P = L.weight_problem(s.vocab, s.hidden, n, L.token_operand(x.e, s.vocab, n, vp),
+                                     L.token_operand(hp, s.hidden, n, h.ld));
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
     L.g.scale = x.grad_scale;
     L.g.sum = x.sum;

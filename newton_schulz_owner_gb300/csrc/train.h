@@ -38,6 +38,12 @@ enum LinEpi {
   kLinGluGrad = 2,  // acc = dh: dgate, dup and h from the kept gate / up
   kLinXent = 3      // logits: group maxima and sums, exponentials kept as asked
 };
+// What a product may load while the launch before it still runs.
+enum LinEarly {
+  kEarlyNone = 0,     // nothing: a call's first product
+  kEarlyWeights = 1,  // the weight operand
+  kEarlyAll = 2       // weight gradients: both operands are older than that launch
+};
 enum LinKeep { kKeepNone = 0, kKeepBf16 = 1, kKeepAct8 = 2 };
 
 // K-elements of a pipeline stage, the unit of kb0 and kb1.
@@ -65,6 +71,7 @@ struct LinArgs {
   LinProblem prob[kLinProblems];
   int n_prob, n_maps;
   int swap, nt, stages;  // swapped orientation: tokens per tile, pipeline stages
+  int early;             // LinEarly
   int k_tail;            // weight gradients: tokens in the last K block (a multiple of 16)
   int full_tiles;        // tiles computed whole; the rest in `split` parts along K
   int split;
@@ -103,7 +110,7 @@ cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_
                        cudaStream_t s);
 
 // Launch a kernel that may start while the one before it in the stream still runs
-// (it calls grid_wait() before it touches memory).
+// (it calls grid_wait() before it writes, or reads what that one writes).
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads,
                              cudaStream_t s, A... args) {

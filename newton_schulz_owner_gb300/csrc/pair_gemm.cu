@@ -1501,16 +1501,22 @@ cudaError_t lin_prepare() {
   return cudaSuccess;
 }
 
-// Swapped where that saves a tenth of the padded rows: at 7/8 of them it measured 3 to
-// 7% faster (block of 4096/14336, 400 to 1100 tokens), at all of them 2% slower.  The
-// cross entropy's epilogue costs more swapped: there a fifth (at 7/8 of the rows 1 to 4%
-// slower with 200 to 777 tokens, at 5/8 7% faster with 300).
-bool lin_swaps(long long tokens, int epi, int* nt) {
+// Swapped where that saves a tenth of the padded rows: at 7/8 of them a block of
+// 4096/14336 measured 7% faster with 448 tokens and 1% with 224 (1536/8960: 1% and 10%
+// slower, backward 2% faster and the same); at all of them both are within 2% of the other.
+// The cross entropy's epilogue costs more swapped, once a tile, while what swapping saves
+// grows with K: with several token tiles it breaks even at K (256 - nt) = 150e3 (320 tokens:
+// K = 1024 76 us against 69, 1536 138 both ways, 2560 173 against 193), with one, where the
+// weights' way from memory hides most of either, at 250e3 to 330e3.  Up to 32 tokens it wins
+// throughout (one token, K = 1536: 92 us against 127).
+bool lin_swaps(long long tokens, int epi, long long k, int* nt) {
   const long long plain = (tokens + kTile - 1) / kTile;  // tiles of 256 tokens, either way
   const long long fit = ((tokens + plain - 1) / plain + 31) / 32 * 32;
   *nt = int(fit);
-  return epi == kLinXent ? tokens <= kXentSwapTokens && fit * 5 < kTile * 4
-                         : fit * 10 < kTile * 9;
+  if (epi == kLinXent)
+    return tokens <= kXentSwapTokens &&
+           (fit <= 32 || k * (kTile - fit) >= (plain == 1 ? 300000 : 160000));
+  return fit * 10 < kTile * 9;
 }
 
 // floor(2^32 / d) or one more: the quotient's estimate is off by one at most.

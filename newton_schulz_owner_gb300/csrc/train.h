@@ -104,8 +104,8 @@ cudaError_t lin_prepare();  // once per device
 // Split the tiles of the last, partly filled wave along K (sets full_tiles ..
 // total_units from the products' tile counts).
 void lin_schedule(LinArgs& g, int epi, int clusters);
-// Whether a product over `tokens` rows runs swapped, and its tokens per tile.
-bool lin_swaps(long long tokens, int epi, int* nt);
+// Whether a product over `tokens` rows and k K-elements runs swapped, and its tokens per tile.
+bool lin_swaps(long long tokens, int epi, long long k, int* nt);
 cudaError_t launch_lin(const LinArgs& g, int epi, bool a_mn, bool b_mn, int max_clusters,
                        cudaStream_t s);
 

@@ -157,7 +157,7 @@ struct Launch {
   LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
                             int64_t k1) {
     int nt = 0;
-    if (lin_swaps(tokens, epi, &nt)) {
+    if (lin_swaps(tokens, epi, k0 + k1, &nt)) {
       g.swap = 1;
       g.nt = nt;
     }

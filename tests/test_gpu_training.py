@@ -369,6 +369,15 @@ def test_xent(dm, t, d, v, grads):
         assert hr.intact() and dh.intact()
 
 
+@pytest.mark.parametrize("t,d,v", [(64, 2048, 300), (160, 3592, 520), (300, 2056, 700),
+                                   (350, 2600, 1000), (1000, 3400, 300)])
+@pytest.mark.parametrize("grads", [False, True])
+def test_xent_long_rows(dm, t, d, v, grads):
+    """Rows long enough for the orientation with the vocabulary along the tile's rows, with
+    one token tile and several, of 64 to 256 tokens."""
+    test_xent(dm, t, d, v, grads)
+
+
 def test_xent_masked_rows_leave_no_trace(dm):
     """NaN and infinities in masked rows: every other result as if they were not there."""
     t, d, v = 300, 128, 1500

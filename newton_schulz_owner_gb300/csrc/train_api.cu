@@ -319,9 +319,9 @@ int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const voi
   const Readable xr = readable(copies, x, s.tokens, s.hidden, x_ld, f.x);
   e = run_copies(copies, st);
   if (e != DMUON_OK) return e;
-  // Few tokens: weights streamed without tiles: one token through 4096/14336 61 us
-  // against 75 with tiles, eight 62 against 75 (with 16 or 32, sharing the weights'
-  // registers among more tokens, 89 and 138 against 76).  8-bit blocks span more columns
+  // Few tokens: weights streamed without tiles: eight tokens through 4096/14336 59 us, one
+  // 56, against 73 with tiles (with 16 or 32, sharing the weights' registers among more
+  // tokens, 89 and 138 against 73; 1536/8960, eight, 24 against 29).  8-bit blocks span more columns
   // than a block computes.
   if (s.tokens <= kThinTokens && s.hidden % 8 == 0 && s.ffn % 8 == 0 &&
       s.save != DMUON_SAVE_ACT8) {

@@ -578,6 +578,9 @@ class LinearXent:
         """The same with the gradients of sum(grad_loss * loss)."""
         if not self.grads:
             raise ValueError("this LinearXent was made without gradients")
+        for name, t in (("grad_loss", grad_loss), ("dhidden", dhidden), ("dweight", dweight)):
+            if t is None:
+                raise TypeError(f"{name}: expected a tensor, got None")
         self._run(hidden, weight, target, grad_loss, loss, lse, dhidden, dweight, stream)
 
     def status(self, stream=None) -> int:

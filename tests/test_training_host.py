@@ -158,3 +158,16 @@ def test_binding_refuses_wrong_tensors(dm):
     head = dm.LinearXent(4, 8, 8, grads=False, device="cpu")
     with pytest.raises(ValueError):
         head.loss_and_grads(x, x, x, x, x, x, x, x)
+
+
+def test_binding_refuses_gradients_without_their_tensors(dm):
+    """A missing grad_loss is not a call for the loss alone: the gradients would stay as they were."""
+    import torch
+    head = dm.LinearXent(4, 8, 8, device="cpu")
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    each = torch.zeros(4)
+    args = dict(hidden=x, weight=x, target=torch.zeros(4, dtype=torch.int64), grad_loss=each, loss=each,
+                lse=each, dhidden=x, dweight=x)
+    for name in ("grad_loss", "dhidden", "dweight"):
+        with pytest.raises(TypeError, match=name):
+            head.loss_and_grads(**{**args, name: None})

@@ -272,6 +272,7 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
  *    first 256 bytes once.
  *  - Every element lies at a multiple of its size (2 bytes for bf16, 4 for fp32, 8
  *    for targets); DMUON_ERR_ALIGNMENT otherwise.
+ *  - Every address is one of the current device, on which the kernels launch.
  *  - The calls can be captured into a CUDA graph; make one call on the device
  *    before the first capture.
  */

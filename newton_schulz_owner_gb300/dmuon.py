@@ -369,14 +369,36 @@ class MuonOwner:
 
 
 # ------------------------------------------------------------------ training-side operators
-def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
-    """Check a (rows, cols) bf16 token matrix; its row pitch in elements."""
+# Tensors and workspace lie on the current device.
+def _current_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _launch_device(t: torch.Tensor, what: str) -> int:
+    """Index of the device that `t` lies on, which has to be the current one: that is where
+    the library launches."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _same_device(t: torch.Tensor, dev: Optional[int], what: str) -> None:
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what}: expected a tensor on cuda:{dev}, got one on {t.device}")
+
+
+def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str, dev: Optional[int] = None) -> int:
+    """Check a (rows, cols) bf16 token matrix (on device `dev`); its row pitch in elements."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected bfloat16")
     if t.shape != (rows, cols):
         raise ValueError(f"{what}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
+    _same_device(t, dev, what)
     ld, unit = t.stride()
     if rows <= 1 or cols == 0:
         ld = cols
@@ -385,14 +407,15 @@ def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
     return ld
 
 
-def _dense(t: torch.Tensor, dtype, shape, what: str) -> int:
-    """Check a contiguous CUDA tensor; its address."""
+def _dense(t: torch.Tensor, dtype, shape, what: str, dev: Optional[int] = None) -> int:
+    """Check a contiguous CUDA tensor (on device `dev`); its address."""
     if t.dtype != dtype:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous CUDA tensor")
+    _same_device(t, dev, what)
     return t.data_ptr()
 
 
@@ -416,8 +439,9 @@ def _act8_args(t: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, where
         ld = cols
     if not t.is_cuda or (cols > 1 and unit != 1) or ld < cols:
         raise ValueError(f"{where}: expected a CUDA tensor whose rows are contiguous")
-    return (rows, cols, dt, ld, _dense(codes, torch.int8, (rows, cols), "codes"),
-            _dense(scales, torch.bfloat16, (rows, _act8_blocks(cols)), "scales"))
+    dev = _launch_device(t, where)
+    return (rows, cols, dt, ld, _dense(codes, torch.int8, (rows, cols), "codes", dev),
+            _dense(scales, torch.bfloat16, (rows, _act8_blocks(cols)), "scales", dev))
 
 
 def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
@@ -477,12 +501,13 @@ class GatedFFN:
                              f"got {tuple(x.shape)}")
         return t
 
-    def _weights(self, w_gate, w_up, w_down, what=""):
+    def _weights(self, dev: int, w_gate, w_up, w_down, what=""):
         bf, d, f = torch.bfloat16, self.hidden, self.ffn
-        return (_dense(w_gate, bf, (f, d), what + "w_gate"), _dense(w_up, bf, (f, d), what + "w_up"),
-                _dense(w_down, bf, (d, f), what + "w_down"))
+        return (_dense(w_gate, bf, (f, d), what + "w_gate", dev),
+                _dense(w_up, bf, (f, d), what + "w_up", dev),
+                _dense(w_down, bf, (d, f), what + "w_down", dev))
 
-    def _saved(self, saved, t: int):
+    def _saved(self, saved, t: int, dev: int):
         saved = tuple(saved) if saved is not None else ()
         want = {SAVE_NONE: 0, SAVE_BF16: 2, SAVE_ACT8: 4}[self.save]
         if len(saved) != want:
@@ -493,17 +518,18 @@ class GatedFFN:
             kinds = [(torch.int8, (t, self.ffn)), (torch.bfloat16, (t, _act8_blocks(self.ffn)))] * 2
         arr = (ctypes.c_void_p * 4)()
         for i, s in enumerate(saved):
-            arr[i] = _dense(s, kinds[i][0], kinds[i][1], f"saved[{i}]")
+            arr[i] = _dense(s, kinds[i][0], kinds[i][1], f"saved[{i}]", dev)
         return arr
 
     def forward(self, x, w_gate, w_up, w_down, y, saved=None, stream=None) -> None:
         """y <- block(x); x and y are (tokens, hidden), `saved` from :meth:`empty_saved`."""
         t = self._tokens(x)
-        x_ld, y_ld = _bf16_rows(x, t, self.hidden, "x"), _bf16_rows(y, t, self.hidden, "y")
-        wg, wu, wd = self._weights(w_gate, w_up, w_down)
+        dev = _launch_device(self.workspace, "the workspace")
+        x_ld, y_ld = (_bf16_rows(v, t, self.hidden, n, dev) for v, n in ((x, "x"), (y, "y")))
+        wg, wu, wd = self._weights(dev, w_gate, w_up, w_down)
         shape = self._shape(t)
         _check(_lib.dmuon_ffn_forward(ctypes.byref(shape), x.data_ptr(), x_ld, wg, wu, wd,
-                                      y.data_ptr(), y_ld, self._saved(saved, t),
+                                      y.data_ptr(), y_ld, self._saved(saved, t, dev),
                                       self.workspace.data_ptr(), self.workspace.numel(),
                                       _stream(stream)), "dmuon_ffn_forward")
 
@@ -513,14 +539,14 @@ class GatedFFN:
         if not self.with_backward:
             raise ValueError("this GatedFFN was made without a backward pass")
         t = self._tokens(x)
-        d = self.hidden
-        dy_ld, x_ld = _bf16_rows(dy, t, d, "dy"), _bf16_rows(x, t, d, "x")
-        dx_ld = _bf16_rows(dx, t, d, "dx")
-        wg, wu, wd = self._weights(w_gate, w_up, w_down)
-        gg, gu, gd = self._weights(dw_gate, dw_up, dw_down, "d")
+        d, dev = self.hidden, _launch_device(self.workspace, "the workspace")
+        dy_ld, x_ld = _bf16_rows(dy, t, d, "dy", dev), _bf16_rows(x, t, d, "x", dev)
+        dx_ld = _bf16_rows(dx, t, d, "dx", dev)
+        wg, wu, wd = self._weights(dev, w_gate, w_up, w_down)
+        gg, gu, gd = self._weights(dev, dw_gate, dw_up, dw_down, "d")
         shape = self._shape(t)
         _check(_lib.dmuon_ffn_backward(ctypes.byref(shape), dy.data_ptr(), dy_ld, x.data_ptr(),
-                                       x_ld, wg, wu, wd, self._saved(saved, t), dx.data_ptr(),
+                                       x_ld, wg, wu, wd, self._saved(saved, t, dev), dx.data_ptr(),
                                        dx_ld, gg, gu, gd, self.workspace.data_ptr(),
                                        self.workspace.numel(), _stream(stream)),
                "dmuon_ffn_backward")
@@ -553,17 +579,18 @@ class LinearXent:
         if t < 0 or t > self.max_tokens:
             raise ValueError(f"hidden: expected (tokens <= {self.max_tokens}, {d}), "
                              f"got {tuple(hidden.shape)}")
-        h_ld = _bf16_rows(hidden, t, d, "hidden")
-        w = _dense(weight, torch.bfloat16, (self.vocab, d), "weight")
-        tg = _dense(target, torch.int64, (t,), "target")
-        lo = _dense(loss, torch.float32, (t,), "loss")
-        ls = _dense(lse, torch.float32, (t,), "lse")
+        dev = _launch_device(self.workspace, "the workspace")
+        h_ld = _bf16_rows(hidden, t, d, "hidden", dev)
+        w = _dense(weight, torch.bfloat16, (self.vocab, d), "weight", dev)
+        tg = _dense(target, torch.int64, (t,), "target", dev)
+        lo = _dense(loss, torch.float32, (t,), "loss", dev)
+        ls = _dense(lse, torch.float32, (t,), "lse", dev)
         gl = dh = dw = None
         dh_ld = 0
         if grad_loss is not None:
-            gl = _dense(grad_loss, torch.float32, (t,), "grad_loss")
-            dh_ld, dh = _bf16_rows(dhidden, t, d, "dhidden"), dhidden.data_ptr()
-            dw = _dense(dweight, torch.bfloat16, (self.vocab, d), "dweight")
+            gl = _dense(grad_loss, torch.float32, (t,), "grad_loss", dev)
+            dh_ld, dh = _bf16_rows(dhidden, t, d, "dhidden", dev), dhidden.data_ptr()
+            dw = _dense(dweight, torch.bfloat16, (self.vocab, d), "dweight", dev)
         shape = XentShape(t, d, self.vocab)
         _check(_lib.dmuon_xent(ctypes.byref(shape), hidden.data_ptr(), h_ld, w, tg, gl, lo, ls, dh,
                                dh_ld, dw, self.workspace.data_ptr(), self.workspace.numel(),

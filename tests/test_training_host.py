@@ -171,3 +171,83 @@ def test_binding_refuses_gradients_without_their_tensors(dm):
     for name in ("grad_loss", "dhidden", "dweight"):
         with pytest.raises(TypeError, match=name):
             head.loss_and_grads(**{**args, name: None})
+
+
+class OnDevice:
+    """As much of a contiguous CUDA tensor as the binding looks at."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index):
+        import torch
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype, index
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return P
+
+
+def test_binding_refuses_tensors_on_other_devices(dm, monkeypatch):
+    """A launch goes to the current device: the workspace and every tensor have to lie there."""
+    import torch
+    bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
+    calls = []
+    monkeypatch.setattr(dm, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(dm, "_raw_stream", None)
+    for name in ("dmuon_ffn_forward", "dmuon_ffn_backward", "dmuon_xent", "dmuon_act8_save",
+                 "dmuon_act8_load"):
+        monkeypatch.setattr(dm._lib, name, lambda *a, name=name: calls.append(name) or 0)
+
+    block = dm.GatedFFN(4, 8, 16, save=dm.SAVE_ACT8, device="cpu")
+    head = dm.LinearXent(4, 8, 32, device="cpu")
+    x = lambda: OnDevice((4, 8), bf, 0)
+    ws = dict(w_gate=((16, 8), bf), w_up=((16, 8), bf), w_down=((8, 16), bf))
+    saved = [OnDevice((4, 16), i8, 0), OnDevice((4, 1), bf, 0)] * 2
+    cases = [
+        (block.forward, dict(x=x(), y=x(), saved=saved, **{k: OnDevice(*v, 0) for k, v in ws.items()})),
+        (block.backward, dict(x=x(), dy=x(), dx=x(), saved=saved,
+                              **{k: OnDevice(*v, 0) for k, v in ws.items()},
+                              **{"d" + k: OnDevice(*v, 0) for k, v in ws.items()})),
+        (head.loss_and_grads, dict(hidden=x(), dhidden=x(), weight=OnDevice((32, 8), bf, 0),
+                                   dweight=OnDevice((32, 8), bf, 0),
+                                   target=OnDevice((4,), torch.int64, 0),
+                                   **{k: OnDevice((4,), f32, 0) for k in ("grad_loss", "loss", "lse")})),
+        (dm.act8_save, dict(x=OnDevice((4, 40), bf, 0), codes=OnDevice((4, 40), i8, 0),
+                            scales=OnDevice((4, 2), bf, 0))),
+        (dm.act8_load, dict(out=OnDevice((4, 40), f32, 0), codes=OnDevice((4, 40), i8, 0),
+                            scales=OnDevice((4, 2), bf, 0)))]
+    for op in (block, head):
+        op.workspace = OnDevice((op.workspace.numel(),), torch.uint8, 0)
+    for f, args in cases:
+        f(**args, stream=1)
+        assert len(calls) == 1 and calls.pop()          # all on the current device: launched
+        for name, v in args.items():
+            parts = range(4) if name == "saved" else [None]
+            for i in parts:
+                t = v if i is None else v[i]
+                away = OnDevice(t.shape, t.dtype, 1)
+                moved = away if i is None else [away if j == i else s for j, s in enumerate(v)]
+                with pytest.raises(ValueError, match="cuda:1"):
+                    f(**{**args, name: moved}, stream=1)
+    for op, (f, args) in ((block, cases[0]), (block, cases[1]), (head, cases[2])):
+        here = op.workspace
+        op.workspace = OnDevice(here.shape, torch.uint8, 1)
+        with pytest.raises(ValueError, match="workspace is on cuda:1"):
+            f(**args, stream=1)
+        op.workspace = here
+    assert not calls

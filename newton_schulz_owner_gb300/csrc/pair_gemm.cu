@@ -979,7 +979,9 @@ DM_DEV float ex2(float x) {
 // Logits of the cross entropy, accumulated in registers over runs of K.  A group of
 // vocabulary entries (128 plainly: the columns of a lane; 32 swapped: the lanes of
 // a warp) shares its maximum m: exp(z - m) = 2^((z - m) log2 e), exactly 1 at the
-// maximum, so that a certain token's loss and gradient come out exact.
+// maximum, so that a certain token's loss and gradient come out exact.  m is at least
+// the lowest finite number, so that a group whose logits are all -infinity weighs nothing.
+constexpr float kLowest = -3.40282347e38f;
 template <bool SWAP>
 DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
                           uint8_t* epi, uint32_t tmem_base, volatile int* abort_flag) {
@@ -1067,7 +1069,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
         for (int j = 0; j < kXentGroup; ++j)
           if (j >= n) z[j] = -INFINITY;
       }
-      float m = z[0];
+      float m = fmaxf(z[0], kLowest);
 #pragma unroll
       for (int j = 1; j < kXentGroup; ++j) m = fmaxf(m, z[j]);
       float s = 0.f;
@@ -1133,7 +1135,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
             for (int j = 0; j < 32; ++j)
               if (j >= n) v[j] = -INFINITY;
           }
-          float m = v[0];
+          float m = fmaxf(v[0], kLowest);
 #pragma unroll
           for (int j = 1; j < 32; ++j) m = fmaxf(m, v[j]);
           float s = 0.f;

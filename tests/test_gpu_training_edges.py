@@ -1,0 +1,75 @@
+"""GPU tests of the training-side operators where a wrong result hides behind a large norm:
+losses near zero against their own size, entries far below their neighbours, logits at
+minus infinity, gates where the normal CDF is small, sums over millions of elements.
+Their fp64 forms are in oracle/training_oracle.py; u = 2^-8 is bf16's unit roundoff."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def dm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import os
+    from newton_schulz_owner_gb300 import build_lib
+    if not os.path.exists(build_lib.LIB):
+        build_lib.build()
+    from newton_schulz_owner_gb300 import dmuon
+    return dmuon
+
+
+def np64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def normal(seed, shape, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").mul_(std).to(dtype)
+
+
+def run_xent(dm, h, w, target, gl=None):
+    t = h.shape[0]
+    op = dm.LinearXent(t, h.shape[1], w.shape[0], grads=gl is not None)
+    out = dict(loss=torch.full((t,), 7.0, device="cuda"), lse=torch.full((t,), 7.0, device="cuda"))
+    if gl is None:
+        op.loss(h, w, target, out["loss"], out["lse"])
+    else:
+        out.update(dhidden=torch.full_like(h, 7.0), dweight=torch.full_like(w, 7.0))
+        op.loss_and_grads(h, w, target, gl, out["loss"], out["lse"], out["dhidden"], out["dweight"])
+    assert op.status() == dm.OK
+    return out
+
+
+# ------------------------------------------------------------------ logits at minus infinity
+@pytest.mark.parametrize("t,d", [(5, 64), (300, 64), (300, 2048)])
+@pytest.mark.parametrize("v,gone", [(700, (128, 384)), (700, (32, 64)), (515, (512, 515)), (130, (0, 128))])
+def test_xent_entries_at_minus_infinity_weigh_nothing(dm, t, d, v, gone):
+    """Whole groups of neighbouring entries (the last, shorter one too) whose logits fall
+    below fp32's range: every result as if their rows were not there, in both orientations."""
+    h, w = normal(41, (t, d)), normal(42, (v, d), d ** -0.5)
+    h[:, 0] = 8.0
+    w[gone[0]:gone[1]] = 0
+    w[gone[0]:gone[1], 0] = -3e38                  # 8 * -3e38: the product is below fp32's range
+    rest = [i for i in range(v) if not gone[0] <= i < gone[1]]
+    r = np.random.default_rng(43)
+    at = r.integers(0, len(rest), t)
+    target = torch.tensor(np.asarray(rest)[at], device="cuda")
+    gl = torch.full((t,), 1.0 / t, device="cuda")
+    ref = oracle.xent(np64(h), np64(w)[rest], at, np64(gl))
+    # the bounds of test_gpu_training.py: fp32 losses, gradients with one operand rounded
+    hd, wd = np64(h), np64(w)[rest]
+    bound = 2.0 ** -21 * (np.abs(hd) @ np.abs(wd).T).max(1) + 2.0 ** -20 * (1 + np.abs(ref["lse"]))
+    for grads in (None, gl):
+        out = run_xent(dm, h, w, target, grads)
+        assert np.all(np.abs(np64(out["loss"]) - ref["loss"]) <= bound)
+        assert np.all(np.abs(np64(out["lse"]) - ref["lse"]) <= bound)
+    assert not out["dweight"][gone[0]:gone[1]].any()
+    for got, want in ((out["dhidden"], ref["dhidden"]), (out["dweight"][rest], ref["dweight"])):
+        assert np.linalg.norm(np64(got) - want) <= 2 * U * np.linalg.norm(want)

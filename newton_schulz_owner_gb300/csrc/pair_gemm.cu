@@ -11,8 +11,8 @@
 //                h = act(gate) * up again
 //   kLinXent     acc = logits of 256 tokens x 256 vocabulary entries; writes,
 //                per token and group of 128 entries, max m and sum of
-//                exp(z - m), the target's logit, and exp(z - m) itself in fp16
-//                when gradients are wanted
+//                exp(z - m), the target's logit, and kXentScale exp(z - m) itself
+//                in fp16 when gradients are wanted
 // Each operand is K-major (rows of K) or MN-major (rows of M or N), a template
 // parameter, so no operand is ever transposed in memory.
 //
@@ -1005,7 +1005,8 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __half2 p = __floats2half2_rn(e[8 * i + 2 * j], e[8 * i + 2 * j + 1]);
+        const __half2 p = __floats2half2_rn(e[8 * i + 2 * j] * kXentScale,
+                                            e[8 * i + 2 * j + 1] * kXentScale);
         o[j] = *reinterpret_cast<const uint32_t*>(&p);
       }
       st_shared_v4(buf + epi_off(lane, i), o[0], o[1], o[2], o[3]);
@@ -1089,8 +1090,8 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __half2 p = __floats2half2_rn(z[(k - 1) * 32 + 8 * i + 2 * j],
-                                                  z[(k - 1) * 32 + 8 * i + 2 * j + 1]);
+              const __half2 p = __floats2half2_rn(z[(k - 1) * 32 + 8 * i + 2 * j] * kXentScale,
+                                                  z[(k - 1) * 32 + 8 * i + 2 * j + 1] * kXentScale);
               o[j] = *reinterpret_cast<const uint32_t*>(&p);
             }
             st_shared_v4(buf0 + uint32_t(lane * 128 + ((i ^ (lane & 7)) << 4)), o[0], o[1], o[2],

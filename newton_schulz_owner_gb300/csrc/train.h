@@ -28,6 +28,10 @@ constexpr int kActBlock = 32;
 // Vocabulary entries whose exponentials share a reference maximum (plain and
 // swapped orientation).
 constexpr int kXentGroup = 128, kXentGroupSwap = 32;
+// Exponentials wait in fp16 times this, the largest power of two that keeps 1 finite: 11 bits
+// down to 2^-29 of their group's largest (e^-20; without it 2^-14, e^-9.7), 2^-40 absolute
+// below.
+constexpr float kXentScale = 32768.f;
 // The most tokens for which the logits run swapped (a workspace is sized by it).
 constexpr int kXentSwapTokens = 1024;
 

@@ -352,11 +352,12 @@ __global__ void __launch_bounds__(kRowThreads) xent_rows_kernel(const XentRows r
   r.lse[t] = live ? m + ls : 0.f;
 }
 
-// G = grad_loss / scale * (exp(z - lse) - [entry is the target]).  exp(z - m)
-// comes in fp16, whose 11 bits leave the one rounding to bf16 here the only one
-// that shows; at the target the difference to 1 is taken as expm1(-loss).  With
-// equal weights (a mean) grad_loss / scale is 1, and the -1 of an unlikely target
-// is exact; the scale is put back in fp32 where the products are written.
+// G = grad_loss / scale * (exp(z - lse) - [entry is the target]).  kXentScale exp(z - m)
+// comes in fp16: 2^-11 of an entry's G beside the 2^-8 of rounding it to bf16 here, down to
+// 2^-29 of its group's largest, and 2^-40 of that one's G below.  At the target the
+// difference to 1 is taken as expm1(-loss).  With equal weights (a mean) grad_loss / scale
+// is 1, and the -1 of an unlikely target is exact; the scale is put back in fp32 where the
+// products are written.
 // A block takes kGradCols columns of one row, four 16-byte loads in flight a thread.
 constexpr int kGradCols = 4 * kVecCols;
 __global__ void __launch_bounds__(kThreads) xent_grad_kernel(const XentRows r, uint4* e,
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) xent_grad_kernel(const XentRows r, u
       p[k * kThreads] = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
-    const float f = gl * exp2f((m[k] - lse) * 1.44269504f);
+    const float f = gl * (1.f / kXentScale) * exp2f((m[k] - lse) * 1.44269504f);
     const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
     float v[8];
 #pragma unroll

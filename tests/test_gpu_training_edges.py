@@ -47,6 +47,21 @@ def run_xent(dm, h, w, target, gl=None):
     return out
 
 
+def xent64(h, w, target):
+    """loss, lse and softmax minus one-hot without cancellation, in 64 bits."""
+    z = h @ w.T
+    at = np.arange(len(h)), target
+    zt = z[at].copy()
+    z[at] = -np.inf
+    top = z.max(1)
+    others = np.log(np.exp(z - top[:, None]).sum(1)) + top
+    loss = np.logaddexp(0, others - zt)
+    loss = np.where(others < zt, np.log1p(np.exp(np.minimum(others - zt, 0))), loss)
+    g = np.exp(z - (zt + loss)[:, None])
+    g[at] = np.expm1(-loss)
+    return loss, zt + loss, g
+
+
 # ------------------------------------------------------------------ logits at minus infinity
 @pytest.mark.parametrize("t,d", [(5, 64), (300, 64), (300, 2048)])
 @pytest.mark.parametrize("v,gone", [(700, (128, 384)), (700, (32, 64)), (515, (512, 515)), (130, (0, 128))])
@@ -73,3 +88,23 @@ def test_xent_entries_at_minus_infinity_weigh_nothing(dm, t, d, v, gone):
     assert not out["dweight"][gone[0]:gone[1]].any()
     for got, want in ((out["dhidden"], ref["dhidden"]), (out["dweight"][rest], ref["dweight"])):
         assert np.linalg.norm(np64(got) - want) <= 2 * U * np.linalg.norm(want)
+
+
+# ------------------------------------------------------------------ entries far below their group
+@pytest.mark.parametrize("t", [40, 300])
+@pytest.mark.parametrize("v", [31, 120, 300])
+def test_xent_gradient_of_entries_far_below_their_neighbours(dm, t, v):
+    """Neighbouring entries whose logits spread over 20: each row of dweight against its own
+    size (the exponentials keep 11 bits down to e^-20 of their group's largest)."""
+    d = 64
+    w = torch.zeros((v, d), dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = -(torch.arange(v, device="cuda") * 7 % 31).to(torch.bfloat16) * (19.5 / 30)
+    w[:, 1] = normal(61, (v,), 0.01)
+    h = normal(62, (t, d))
+    h[:, 0] = 1.0
+    target = torch.full((t,), 5, dtype=torch.int64, device="cuda")
+    hd, wd, tg = np64(h), np64(w), target.cpu().numpy()
+    g = xent64(hd, wd, tg)[2]
+    out = run_xent(dm, h, w, target, torch.ones(t, device="cuda"))
+    err = np.abs(np64(out["dweight"]) - g.T @ hd)
+    assert np.all(err <= U * np.abs(g.T @ hd) + 1.25 * U * (np.abs(g).T @ np.abs(hd)))

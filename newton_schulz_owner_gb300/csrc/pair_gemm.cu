@@ -11,7 +11,7 @@
 //                h = act(gate) * up again
 //   kLinXent     acc = logits of 256 tokens x 256 vocabulary entries; writes,
 //                per token and group of 128 entries, max m and sum of
-//                exp(z - m), the target's logit, and kXentScale exp(z - m) itself
+//                exp(z - m) without the target, and kXentScale exp(z - m) itself
 //                in fp16 when gradients are wanted
 // Each operand is K-major (rows of K) or MN-major (rows of M or N), a template
 // parameter, so no operand is ever transposed in memory.
@@ -91,8 +91,9 @@ constexpr int kStrip = 8;
 // up to K/16 * 2^-25 of its size.  That is far below bf16 for an output that is
 // rounded to it, but not for the fp32 losses: the logits are accumulated in runs of
 // 512 K-elements, each drained and added in registers, rounded to nearest (error of
-// 777 tokens' losses against 64 bits 2.7e-6 without, 3.6e-7 with; fp32 products on the
-// CUDA cores 6e-7).  The drains hide behind the next run's MMAs: 1% of the time.
+// 777 tokens' losses against 64 bits 2.7e-6 without, 3.6e-7 with, and 1.0e-7 with the
+// target's logit, a sum of one sign, summed apart in xent_rows_kernel; fp32 products on
+// the CUDA cores 6e-7).  The drains hide behind the next run's MMAs: 1% of the time.
 constexpr int kRunElems = 512;
 
 // Workspace of the split parts.
@@ -978,9 +979,10 @@ DM_DEV float ex2(float x) {
 
 // Logits of the cross entropy, accumulated in registers over runs of K.  A group of
 // vocabulary entries (128 plainly: the columns of a lane; 32 swapped: the lanes of
-// a warp) shares its maximum m: exp(z - m) = 2^((z - m) log2 e), exactly 1 at the
-// maximum, so that a certain token's loss and gradient come out exact.  m is at least
-// the lowest finite number, so that a group whose logits are all -infinity weighs nothing.
+// a warp) shares its maximum m: exp(z - m) = 2^((z - m) log2 e).  A token's target takes
+// no part (its logit counts as -infinity): the loss of a token that is sure of it is the
+// weight of the others, which would be lost beside the target's 1.  m is at least the
+// lowest finite number, so that a group whose logits are all -infinity weighs nothing.
 constexpr float kLowest = -3.40282347e38f;
 template <bool SWAP>
 DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t* tempty,
@@ -1062,7 +1064,7 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
       if (__any_sync(0xffffffffu, d >= 0)) {
 #pragma unroll
         for (int j = 0; j < kXentGroup; ++j)
-          if (j == d) g.target_logit[r] = z[j];
+          if (j == d) z[j] = -INFINITY;
       }
       const int n = P.cols - g0;
       if (n < kXentGroup) {  // entries past the vocabulary weigh nothing
@@ -1122,15 +1124,12 @@ DM_DEV void epilogue_xent(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
           __syncwarp();
           turn_write(turn, lane, v);
           __syncwarp();
+          if (r < P.rows) {  // the target, in the word from which this lane reads it
+            const unsigned long long d = (unsigned long long)(g.target[r] - c0);
+            if (d < 32) st_shared_f32(buf0 + uint32_t(lane * 32 + (int(d) ^ lane)) * 4u, -INFINITY);
+          }
           turn_read(turn, lane, v);
           __syncwarp();
-          const long long t = r < P.rows ? g.target[r] : -1;
-          const int d = t >= c0 && t < c0 + 32 && t < P.cols ? int(t - c0) : -1;
-          if (__any_sync(0xffffffffu, d >= 0)) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == d) g.target_logit[r] = v[j];
-          }
           if (n < 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)

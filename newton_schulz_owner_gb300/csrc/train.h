@@ -98,8 +98,8 @@ struct LinArgs {
   __nv_bfloat16 *dup, *h;                   // and their tensors (pitch c_ld)
   // kLinXent
   const long long* target;
-  float* target_logit;   // one per token
-  float2* group_stat;    // (max logit, sum of exp(logit - that)) per [group][token]
+  float2* group_stat;    // (max logit, sum of exp(logit - that)) per [group][token], the
+                         // token's target left out
   long long stat_ld;     // pitch of a group
 };
 
@@ -184,7 +184,9 @@ struct XentRows {
   const long long* target;
   const float* grad_loss;   // null: no gradients
   const float* grad_scale;  // G is formed of grad_loss / *grad_scale
-  const float* target_logit;
+  const __nv_bfloat16 *hidden, *weight;  // rows of k elements, 16-byte aligned
+  long long hidden_ld, weight_ld;
+  int k;
   const float2* group_stat;  // as LinArgs
   long long stat_ld;
   int group;                // vocabulary entries per group

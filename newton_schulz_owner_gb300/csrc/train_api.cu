@@ -454,7 +454,7 @@ int64_t xent_piece(const dmuon_xent_shape& s, bool grads) {
 struct XentSpace {
   ProductSpace ps;
   bf16 *hidden, *weight, *e;
-  float *target_logit, *grad_scale;
+  float* grad_scale;
   float2* stat;
   float* sum;
   int64_t piece;
@@ -467,7 +467,6 @@ XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   x.piece = xent_piece(s, grads);
   x.ps = take_product_space(c);
   x.hidden = c.take<bf16>(size_t(s.tokens) * dp * 2);
-  x.target_logit = c.take<float>(size_t(s.tokens) * 4);
   x.grad_scale = c.take<float>(4);
   // swapped products have four times the groups, over at most kXentSwapTokens tokens
   x.stat = c.take<float2>(
@@ -520,7 +519,11 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     R.target = tgt + t0;
     R.grad_loss = grads ? grad_loss + t0 : nullptr;
     R.grad_scale = x.grad_scale;
-    R.target_logit = x.target_logit + t0;
+    R.hidden = hp;
+    R.hidden_ld = h.ld;
+    R.weight = w.p;
+    R.weight_ld = w.ld;
+    R.k = int(s.hidden);
     R.group_stat = x.stat;
     R.stat_ld = up32(n);
     R.loss = loss + t0;
@@ -531,7 +534,6 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
       L.operands(P, hp, s.hidden, h.ld, w.p, s.hidden, s.vocab, w.ld, true);
       if (grads) P.c_map = L.output(x.e, s.vocab, n, vp, !L.g.swap);
       L.g.target = tgt + t0;
-      L.g.target_logit = x.target_logit + t0;
       L.g.group_stat = x.stat;
       L.g.stat_ld = R.stat_ld;
       R.group = L.g.swap ? kXentGroupSwap : kXentGroup;

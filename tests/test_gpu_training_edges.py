@@ -108,3 +108,73 @@ def test_xent_gradient_of_entries_far_below_their_neighbours(dm, t, v):
     out = run_xent(dm, h, w, target, torch.ones(t, device="cuda"))
     err = np.abs(np64(out["dweight"]) - g.T @ hd)
     assert np.all(err <= U * np.abs(g.T @ hd) + 1.25 * U * (np.abs(g).T @ np.abs(hd)))
+
+
+# ------------------------------------------------------------------ sure tokens
+def sure_case(seed, t, d, v, lo=1e-5, hi=1e-1):
+    """Tokens whose loss runs from `hi` down to `lo`: the hidden state is pulled towards the
+    target's row until that logit is as far above all others together."""
+    h, w = normal(seed, (t, d)).double(), normal(seed + 1, (v, d), d ** -0.5)
+    wd = w.double()
+    r = np.random.default_rng(seed)
+    target = torch.from_numpy(r.integers(0, v, t)).cuda()
+    rows = wd[target]
+    rows = rows / rows.square().sum(1, keepdim=True)
+    want = torch.logspace(np.log10(hi), np.log10(lo), t, device="cuda", dtype=torch.float64)
+    if t == 1:
+        want = torch.tensor([1e-3], device="cuda", dtype=torch.float64)
+    at = torch.arange(t, device="cuda")
+    for _ in range(20):                            # others move a little with the pull
+        z = h @ wd.T
+        zt = z[at, target].clone()
+        z[at, target] = -float("inf")
+        h = h + rows * (torch.logsumexp(z, 1) - zt - torch.log(torch.expm1(want)))[:, None]
+    return h.to(torch.bfloat16), w, target
+
+
+SURE = [(1, 64, 300), (1, 4096, 5000), (3, 1024, 40), (40, 4096, 300), (64, 512, 129), (300, 64, 5000),
+        (300, 2048, 700), (300, 4096, 260), (600, 1000, 2000)]
+
+
+@pytest.mark.parametrize("t,d,v", SURE)
+@pytest.mark.parametrize("seed", [51, 52])
+def test_xent_of_sure_tokens_relative_to_the_loss(dm, t, d, v, seed):
+    """loss = log(1 + sum of exp(z_v - z_target)), so its relative error is that of the
+    exponentials: 2e-6 for their arithmetic and the difference's rounding, and 2^-22 of their
+    terms' sizes for the other entries' logits.  Nothing is granted for the target's own
+    logit, a sum of one sign of 5 to 25, nor for the sum that 1 is added to."""
+    h, w, target = sure_case(seed, t, d, v)
+    hd, wd, tg = np64(h), np64(w), target.cpu().numpy()
+    loss, lse, g = xent64(hd, wd, tg)
+    assert loss.max() < 0.2 and loss.min() > 5e-6
+    others = np.abs(hd) @ np.abs(wd).T
+    others[np.arange(t), tg] = 0
+    rel = 2e-6 + 2.0 ** -22 * others.max(1)
+    gl = torch.full((t,), 1.0 / t, device="cuda")
+    for grads in (None, gl):
+        out = run_xent(dm, h, w, target, grads)
+        err = np.abs(np64(out["loss"]) - loss)
+        assert np.all(err <= rel * loss), (err / loss).max()
+        assert np.all(np.abs(np64(out["lse"]) - lse) <= 3e-7 * np.abs(lse))
+    # gradients, element by element: G's entries and the outputs are rounded once each
+    g /= t
+    for got, want, mass in ((out["dhidden"], g @ wd, np.abs(g) @ np.abs(wd)),
+                            (out["dweight"], g.T @ hd, np.abs(g).T @ np.abs(hd))):
+        assert np.all(np.abs(np64(got) - want) <= U * np.abs(want) + 1.25 * U * mass)
+
+
+def test_xent_gradient_rows_of_sure_tokens_balance(dm):
+    """Two entries, 10 to 20 apart: G is (-p, p) with p = exp(-gap) whatever the gap."""
+    t, d = 40, 64
+    w = torch.zeros((2, d), dtype=torch.bfloat16, device="cuda")
+    w[0, 0] = 1.0
+    w[1, 1] = 1.0
+    h = torch.zeros((t, d), dtype=torch.bfloat16, device="cuda")
+    gap = torch.linspace(10, 20, t, device="cuda").to(torch.bfloat16)
+    h[:, 0] = gap
+    target = torch.zeros(t, dtype=torch.int64, device="cuda")
+    out = run_xent(dm, h, w, target, torch.ones(t, device="cuda"))
+    p = 1 / (1 + np.exp(np64(gap)))
+    assert np.all(np.abs(np64(out["loss"]) + np.log1p(-p)) <= 1e-6 * p)
+    for col, sign in ((0, -1), (1, 1)):
+        assert np.all(np.abs(np64(out["dhidden"])[:, col] - sign * p) <= 2 * U * p)

@@ -366,7 +366,8 @@ typedef struct {
  * where it is computed.  For gradients the exponentials of a bounded number of
  * tokens (about 2.2 GB of 16-bit values; at least 256 tokens) wait in the
  * workspace; with more tokens than that, dW is summed over the pieces in fp32
- * (4 * vocab * hidden bytes more workspace).
+ * (4 * vocab * hidden bytes more workspace).  A workspace sized with `grads` serves
+ * the loss alone too.
  */
 size_t dmuon_xent_workspace_bytes(const dmuon_xent_shape* shape, int grads);
 int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden_ld,

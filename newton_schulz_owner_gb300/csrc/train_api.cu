@@ -662,7 +662,10 @@ int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_
 
 size_t dmuon_xent_workspace_bytes(const dmuon_xent_shape* shape, int grads) {
   if (!xent_shape_ok(shape)) return 0;
-  return xent_space(*shape, grads != 0, nullptr).bytes;
+  // one for gradients serves the loss alone too, which takes more tokens at a time (a vast
+  // vocabulary's group statistics of 16384 tokens outweigh what gradients keep)
+  const size_t loss = xent_space(*shape, false, nullptr).bytes;
+  return grads != 0 ? std::max(loss, xent_space(*shape, true, nullptr).bytes) : loss;
 }
 
 int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden_ld,

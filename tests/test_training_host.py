@@ -251,3 +251,10 @@ def test_binding_refuses_tensors_on_other_devices(dm, monkeypatch):
             f(**args, stream=1)
         op.workspace = here
     assert not calls
+
+
+def test_a_workspace_for_gradients_serves_the_loss_alone(dm):
+    for t in (1, 300, 1024, 16384, 1 << 18):
+        for d in (8, 64, 65, 4096):
+            for v in (1, 1000, 151936, 1 << 20, 1 << 22):
+                assert xent_bytes(dm, t, d, v, grads=1) >= xent_bytes(dm, t, d, v, grads=0), (t, d, v)

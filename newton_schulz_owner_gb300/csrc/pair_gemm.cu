@@ -971,12 +971,6 @@ DM_DEV void epilogue_grad(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint
   __syncwarp();
 }
 
-DM_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Logits of the cross entropy, accumulated in registers over runs of K.  A group of
 // vocabulary entries (128 plainly: the columns of a lane; 32 swapped: the lanes of
 // a warp) shares its maximum m: exp(z - m) = 2^((z - m) log2 e).  A token's target takes

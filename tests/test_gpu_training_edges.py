@@ -178,3 +178,49 @@ def test_xent_gradient_rows_of_sure_tokens_balance(dm):
     assert np.all(np.abs(np64(out["loss"]) + np.log1p(-p)) <= 1e-6 * p)
     for col, sign in ((0, -1), (1, 1)):
         assert np.all(np.abs(np64(out["dhidden"])[:, col] - sign * p) <= 2 * U * p)
+
+
+# ------------------------------------------------------------------ small values of the normal CDF
+GATES = [-0.5, -1.0, -2.0, -3.0, -4.0, -4.75, -5.0, -5.5, -5.75, -6.0, -7.0, -8.0, -9.0, -10.0, 0.25, 3.0, 6.0]
+
+
+def gelu64(g):
+    """x Phi(x) and its derivative without cancellation (Phi through erfc)."""
+    import math
+    phi = np.array([0.5 * math.erfc(-x / math.sqrt(2)) for x in g])
+    return g * phi, phi + g * np.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+
+
+@pytest.mark.parametrize("t", [1, 9, 40, 300])
+def test_gelu_of_negative_gates_relative_to_its_size(dm, t):
+    """Every product of the block is with one row of an identity, so y is act(gate) rounded
+    twice (h, y), dw_gate's first column act'(gate) and dw_up's act(gate) likewise."""
+    gates = torch.tensor(GATES, device="cuda").to(torch.bfloat16)
+    n = len(GATES)
+    d = f = 64
+    eye = torch.eye(d, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((t, d), dtype=torch.bfloat16, device="cuda")
+    x[0, :n], x[0, 63] = gates, 1.0
+    w_up = torch.zeros((f, d), dtype=torch.bfloat16, device="cuda")
+    w_up[:, 63] = 1.0                                              # up = 1
+    op = dm.GatedFFN(t, d, f, activation=dm.ACT_GELU)
+    saved, y = op.empty_saved(t), torch.empty_like(x)
+    op.forward(x, eye, w_up, eye, y, saved)
+    a, da = gelu64(np64(gates))
+    assert np.all(np.abs(np64(y[0, :n]) - a) <= 1.01 * U * np.abs(a))
+    # the gradients of one live token, whose x and dy are the first unit vector
+    x.zero_()
+    x[0, 0] = 1.0
+    dy = x.clone()
+    w_down = torch.zeros((d, f), dtype=torch.bfloat16, device="cuda")
+    w_down[0] = 1.0                                                # dh = 1
+    gate, up = torch.zeros((t, f), dtype=torch.bfloat16, device="cuda"), torch.ones(
+        (t, f), dtype=torch.bfloat16, device="cuda")
+    gate[0, :n] = gates
+    dx, dw = torch.empty_like(x), [torch.empty_like(eye) for _ in range(3)]
+    op.backward(dy, x, eye, w_up, w_down, (gate, up), dx, *dw)
+    assert op.status() == dm.OK
+    # act' crosses zero near -0.75: there two terms of half its size each cancel
+    assert np.all(np.abs(np64(dw[0][:n, 0]) - da) <= 1.01 * U * np.abs(da) + 1e-6 * np.exp(-0.5 * np64(gates) ** 2))
+    assert np.all(np.abs(np64(dw[1][:n, 0]) - a) <= 1.01 * U * np.abs(a))
+    assert np.all(np.abs(np64(dw[2][0, :n]) - a) <= 1.01 * U * np.abs(a))

@@ -258,6 +258,11 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
  *  - Activations, weights and gradients are bf16.  Products accumulate in fp32
  *    on the tensor cores; an intermediate that feeds a second product (h, dgate,
  *    dup, the gradient of the logits) is rounded to bf16 once, as its operand.
+ *    The tensor cores' accumulation truncates: a sum of K terms of one sign comes out
+ *    up to K * 2^-27.5 short.  Sums over tokens are cut at 65536 of them and sums over
+ *    more than 262144 vocabulary entries into parts of at most 131072, added in fp32;
+ *    sums over hidden and ffn are whole, so that near the limits of those (2.7e-3 at
+ *    524288, and dx sums over 2 ffn) truncation nears the rounding to bf16.
  *  - A weight is a PyTorch parameter (out, in), contiguous.  It is 16-byte
  *    aligned where its row length is a multiple of 8 (else it is copied to the
  *    workspace, padded, on every call).
@@ -337,7 +342,8 @@ int dmuon_ffn_forward(const dmuon_ffn_shape* shape, const void* x, int64_t x_ld,
  *   dh = dy Wd,  dgate = dh * up * act'(gate),  dup = dh * act(gate)
  *   dx = dgate Wg + dup Wu
  *   dWg = dgate^T x,  dWu = dup^T x,  dWd = dy^T h
- * (h is recomputed).  The weight gradients are written, not added to.
+ * (h is recomputed).  The weight gradients are written, not added to.  With more than
+ * 65536 tokens the workspace also holds their fp32 sums (12 * hidden * ffn bytes).
  */
 int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_ld, const void* x,
                        int64_t x_ld, const void* w_gate, const void* w_up, const void* w_down,
@@ -364,7 +370,7 @@ typedef struct {
  *   dhidden    (tokens, hidden), rows dhidden_ld apart;  dweight (vocab, hidden)
  * The logits never exist as a tensor: each piece of the vocabulary is reduced
  * where it is computed.  For gradients the exponentials of a bounded number of
- * tokens (about 2.2 GB of 16-bit values; at least 256 tokens) wait in the
+ * tokens (about 2.2 GB of 16-bit values; at least 256, at most 65536 tokens) wait in the
  * workspace; with more tokens than that, dW is summed over the pieces in fp32
  * (4 * vocab * hidden bytes more workspace).  A workspace sized with `grads` serves
  * the loss alone too.

@@ -87,9 +87,11 @@ static_assert((2 * kMaxStages + 4 + 1 + 8) * 8 + 8 <= kBarBytes, "barrier area t
 // a time, close to the fewest panels that 76 tiles can share.
 constexpr int kStrip = 8;
 
-// The tensor core's accumulation rounds toward zero, so a sum of K products loses
-// up to K/16 * 2^-25 of its size.  That is far below bf16 for an output that is
-// rounded to it, but not for the fp32 losses: the logits are accumulated in runs of
+// The tensor core's accumulation rounds toward zero, so a sum of K terms of one sign
+// comes out short: of 2^20, 3.1e-3 to 5.4e-3 of the sum were missing, which is K * 2^-28.4
+// to K * 2^-27.5.  Below K = 2^18 that is at most a third of rounding an output to bf16
+// (longer sums are cut, train_api.cu), but not for the fp32 losses: the logits are
+// accumulated in runs of
 // 512 K-elements, each drained and added in registers, rounded to nearest (error of
 // 777 tokens' losses against 64 bits 2.7e-6 without, 3.6e-7 with, and 1.0e-7 with the
 // target's logit, a sum of one sign, summed apart in xent_rows_kernel; fp32 products on
@@ -672,7 +674,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     };
 
     if constexpr (EPI == kLinStore && !SWAP) {
-      if (g.sum == nullptr && P.c_map >= 0) {
+      if (P.sum == nullptr && P.c_map >= 0) {
         const float f = g.scale != nullptr ? *g.scale : 1.f;
         const bool second = G.inside(2);
 #pragma unroll 1
@@ -705,8 +707,8 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       if constexpr (EPI == kLinStore) {
         float v[32];
         load_acc(k, v);
-        if (!SWAP && g.sum != nullptr) {
-          float* sp = g.sum + (long long)r * P.cols + c0;
+        if (P.sum != nullptr) {
+          float* sp = P.sum + (long long)r * P.cols + c0;
           const bool vec = (P.cols & 3) == 0 && n >= 32;
           if (g.sum_read && r < P.rows) {
             if (vec) {
@@ -1370,8 +1372,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const bool vec = P.c_map >= 0;
   if (EPI == kLinStore) {
     if (!in || n <= 0) return;
-    if (g.sum != nullptr) {
-      float* sp = g.sum + (long long)r * P.cols + c;
+    if (P.sum != nullptr) {
+      float* sp = P.sum + (long long)r * P.cols + c;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < n) {

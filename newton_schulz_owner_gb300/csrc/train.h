@@ -68,6 +68,7 @@ struct LinProblem {
   int c_map;             // output map, or -1: c is written with plain stores
   __nv_bfloat16* c;
   long long c_ld;
+  float* sum;            // kLinStore: fp32 running sum over launches (row pitch = cols), or null
 };
 
 struct LinArgs {
@@ -83,9 +84,7 @@ struct LinArgs {
   int total_units;       // full_tiles + split * (tiles - full_tiles)
   float* partial;        // fp32 parts of the split tiles
   int* err;
-  // kLinStore: fp32 running sum over launches (row pitch = cols of the product)
-  float* sum;
-  int sum_read, sum_write;  // add what `sum` holds; write the sum there instead of C
+  int sum_read, sum_write;  // add what the products' sums hold; write there instead of C
   const float* scale;    // C = scale * acc (device scalar), or null
   // kLinGlu / kLinGluGrad
   int act, keep;

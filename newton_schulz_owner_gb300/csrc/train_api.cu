@@ -21,6 +21,12 @@ constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxDim = int64_t(1) << 19,
 // bounds the group statistics.
 constexpr size_t kLogitBytes = size_t(2200) << 20;
 constexpr int64_t kLossTokens = 16384;
+// The tensor core's truncation takes up to K * 2^-27.5 of a sum of one sign (pair_gemm.cu).
+// Sums over tokens are cut at 2^16 of them (2^20 at once: 5.4e-3 of a weight gradient
+// missing, more than its rounding to bf16; of 2^16, a sixteenth of that), the parts added in
+// fp32.  A sum over more than 2^18 vocabulary entries is cut into parts of at most 2^17;
+// usual vocabularies stay whole (152064: up to 8e-4, a fifth of the rounding).
+constexpr int64_t kSumTokens = 1 << 16, kVocabWhole = 1 << 18, kVocabPart = 1 << 17;
 
 using bf16 = __nv_bfloat16;
 
@@ -153,6 +159,13 @@ struct Launch {
     P.b1 = right.tail;
     return P;
   }
+  // One part of a sum over several launches, kept in `sum` from the first to the last.
+  void part_of(LinProblem& P, float* sum, bool first, bool last) {
+    if (first && last) return;
+    P.sum = sum;
+    g.sum_read = !first;
+    g.sum_write = !last;
+  }
   // A product tokens x weight, swapped where that fits the token count better.
   LinProblem& token_problem(int epi, int64_t tokens, int64_t cols, int cols_per_tile, int64_t k0,
                             int64_t k1) {
@@ -235,6 +248,7 @@ bool ffn_shape_ok(const dmuon_ffn_shape* s) {
 struct FfnSpace {
   ProductSpace ps;
   bf16 *x, *dy, *h, *dgate, *dup, *w_gate, *w_up, *w_down;
+  float* sum[3];
   size_t bytes;
 };
 FfnSpace ffn_space(const dmuon_ffn_shape& s, bool backward, void* ws) {
@@ -248,6 +262,8 @@ FfnSpace ffn_space(const dmuon_ffn_shape& s, bool backward, void* ws) {
     f.dy = c.take<bf16>(t * dp * 2);
     f.dgate = c.take<bf16>(t * fp * 2);
     f.dup = c.take<bf16>(t * fp * 2);
+    if (s.tokens > kSumTokens)
+      for (float*& sum : f.sum) sum = c.take<float>(size_t(s.ffn) * size_t(s.hidden) * 4);
   }
   if (s.hidden % 8 != 0) {
     f.w_gate = c.take<bf16>(size_t(s.ffn) * dp * 2);
@@ -424,17 +440,25 @@ int ffn_backward(const dmuon_ffn_shape& s, const void* dy, int64_t dy_ld, const 
     if (e != DMUON_OK) return e;
   }
   // dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
-  Launch L(f.ps, kEarlyAll);
-  const Launch::TokenOperand ox = L.token_operand(xr.p, s.hidden, s.tokens, xr.ld),
-                             oh = L.token_operand(f.h, s.ffn, s.tokens, fp);
   const bf16* left[3] = {f.dgate, f.dup, dyr.p};
   bf16* out[3] = {static_cast<bf16*>(dwg), static_cast<bf16*>(dwu), static_cast<bf16*>(dwd)};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
-    const Launch::TokenOperand ol = L.token_operand(left[i], m, s.tokens, i < 2 ? fp : dyr.ld);
-    L.store_to(L.weight_problem(m, n, s.tokens, ol, i < 2 ? ox : oh), out[i], n);
+  for (int64_t t0 = 0; t0 < s.tokens; t0 += kSumTokens) {
+    const int64_t t = std::min(kSumTokens, s.tokens - t0);
+    Launch L(f.ps, kEarlyAll);
+    const Launch::TokenOperand ox = L.token_operand(xr.p + t0 * xr.ld, s.hidden, t, xr.ld),
+                               oh = L.token_operand(f.h + t0 * fp, s.ffn, t, fp);
+    for (int i = 0; i < 3; ++i) {
+      const int64_t m = i < 2 ? s.ffn : s.hidden, n = i < 2 ? s.hidden : s.ffn;
+      const int64_t ld = i < 2 ? fp : dyr.ld;
+      const Launch::TokenOperand ol = L.token_operand(left[i] + t0 * ld, m, t, ld);
+      LinProblem& P = L.weight_problem(m, n, t, ol, i < 2 ? ox : oh);
+      L.store_to(P, out[i], n);
+      L.part_of(P, f.sum[i], t0 == 0, t0 + t == s.tokens);
+    }
+    e = L.run(kLinStore, true, true, clusters, st);
+    if (e != DMUON_OK) return e;
   }
-  return L.run(kLinStore, true, true, clusters, st);
+  return DMUON_OK;
 }
 
 // ------------------------------------------------------------------ cross entropy
@@ -447,7 +471,9 @@ bool xent_shape_ok(const dmuon_xent_shape* s) {
 int64_t xent_piece(const dmuon_xent_shape& s, bool grads) {
   int64_t most = kLossTokens;
   if (grads)
-    most = std::max<int64_t>(256, int64_t(kLogitBytes / (size_t(pitch(s.vocab)) * 2)) / 256 * 256);
+    most = std::min(kSumTokens,
+                    std::max<int64_t>(256, int64_t(kLogitBytes / (size_t(pitch(s.vocab)) * 2)) /
+                                               256 * 256));
   return std::min(s.tokens, most);
 }
 
@@ -456,7 +482,7 @@ struct XentSpace {
   bf16 *hidden, *weight, *e;
   float* grad_scale;
   float2* stat;
-  float* sum;
+  float *sum, *hidden_sum;
   int64_t piece;
   size_t bytes;
 };
@@ -477,6 +503,8 @@ XentSpace xent_space(const dmuon_xent_shape& s, bool grads, void* ws) {
   if (grads) {
     x.e = c.take<bf16>(size_t(x.piece) * size_t(pitch(s.vocab)) * 2);
     if (x.piece < s.tokens) x.sum = c.take<float>(size_t(s.vocab) * size_t(s.hidden) * 4);
+    if (s.vocab > kVocabWhole)
+      x.hidden_sum = c.take<float>(size_t(x.piece) * size_t(s.hidden) * 4);
   }
   x.bytes = c.used;
   return x;
@@ -543,11 +571,16 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
     if (launch_xent_rows(R, st) != cudaSuccess) return DMUON_ERR_CUDA;
     if (!grads) continue;
     if (launch_xent_grad(R, x.e, vp, st) != cudaSuccess) return DMUON_ERR_CUDA;
-    {  // dhidden = G W
+    // dhidden = G W
+    const int64_t cuts = s.vocab > kVocabWhole ? ceil_div(s.vocab, kVocabPart) : 1;
+    const int64_t span = pitch(ceil_div(s.vocab, cuts));
+    for (int64_t v0 = 0; v0 < s.vocab; v0 += span) {
+      const int64_t k = std::min(span, s.vocab - v0);
       Launch L(x.ps, kEarlyWeights);
-      LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, s.vocab, 0);
-      L.operands(P, x.e, s.vocab, vp, w.p, s.hidden, s.vocab, w.ld, false);
+      LinProblem& P = L.token_problem(kLinStore, n, s.hidden, 256, k, 0);
+      L.operands(P, x.e + v0, k, vp, w.p + v0 * w.ld, s.hidden, k, w.ld, false);
       L.store_to(P, static_cast<bf16*>(dhidden) + t0 * dh_ld, dh_ld);
+      L.part_of(P, x.hidden_sum, v0 == 0, v0 + k == s.vocab);
       L.g.scale = x.grad_scale;
       e = L.run_token(kLinStore, false, clusters, st);
       if (e != DMUON_OK) return e;
@@ -558,9 +591,7 @@ int xent(const dmuon_xent_shape& s, const void* hidden, int64_t h_ld, const void
                                      L.token_operand(hp, s.hidden, n, h.ld));
     L.store_to(P, static_cast<bf16*>(dweight), s.hidden);
     L.g.scale = x.grad_scale;
-    L.g.sum = x.sum;
-    L.g.sum_read = t0 > 0;
-    L.g.sum_write = t0 + n < s.tokens;
+    L.part_of(P, x.sum, t0 == 0, t0 + n == s.tokens);
     e = L.run(kLinStore, true, true, clusters, st);
     if (e != DMUON_OK) return e;
   }

@@ -224,3 +224,126 @@ def test_gelu_of_negative_gates_relative_to_its_size(dm, t):
     assert np.all(np.abs(np64(dw[0][:n, 0]) - da) <= 1.01 * U * np.abs(da) + 1e-6 * np.exp(-0.5 * np64(gates) ** 2))
     assert np.all(np.abs(np64(dw[1][:n, 0]) - a) <= 1.01 * U * np.abs(a))
     assert np.all(np.abs(np64(dw[2][0, :n]) - a) <= 1.01 * U * np.abs(a))
+
+
+# ------------------------------------------------------------------ sums over millions of elements
+# The accumulator truncates, a bias that no averaging removes.  Allowed of it: 2^-11 of the
+# terms' sizes, here at most twice the result's.  The operands' roundings average out over
+# millions; the output's is at most u / sqrt(3) as a relative norm.  0.58 u + 0.25 u < u.
+LONG = U
+
+
+def far(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("t", [20, 256, 300])
+@pytest.mark.parametrize("d", [64, 72, 33])
+def test_xent_hidden_gradient_over_millions_of_entries(dm, t, d):
+    """A vocabulary at the limit, weights of one sign: dhidden is a sum of four million terms
+    (300 tokens: in two pieces)."""
+    v = 1 << 22
+    h, w = normal(71, (t, d), 0.1), normal(72, (v, d)).abs_()
+    target = torch.arange(t, device="cuda") * 13001
+    gl = torch.ones(t, device="cuda")
+    out = run_xent(dm, h, w, target, gl)
+    want = torch.empty((t, d), dtype=torch.float64, device="cuda")
+    for lo in range(0, t, 64):
+        z = h[lo:lo + 64].double() @ w.double().T
+        z = torch.softmax(z, 1)
+        z[torch.arange(len(z), device="cuda"), target[lo:lo + 64]] -= 1
+        want[lo:lo + 64] = z @ w.double()
+        del z
+    assert far(out["dhidden"], want) <= LONG
+
+
+@pytest.mark.parametrize("d,f", [(64, 64), (40, 33)])
+def test_ffn_weight_gradients_over_millions_of_tokens(dm, d, f):
+    """All tokens at the limit of four million, every term of the sums positive."""
+    t = 1 << 22
+    x, dy = normal(73, (t, d)).abs_(), normal(74, (t, d)).abs_()
+    wg, wu, wd = (normal(75 + i, s, 0.1).abs_() for i, s in enumerate([(f, d), (f, d), (d, f)]))
+    gate, up = normal(78, (t, f)).abs_(), normal(79, (t, f)).abs_()
+    op = dm.GatedFFN(t, d, f)
+    dx, dw = torch.empty_like(x), [torch.empty_like(w) for w in (wg, wu, wd)]
+    op.backward(dy, x, wg, wu, wd, (gate, up), dx, *dw)
+    assert op.status() == dm.OK
+    want = [torch.zeros(w.shape, dtype=torch.float64, device="cuda") for w in (wg, wu, wd)]
+    for lo in range(0, t, 1 << 18):
+        s = slice(lo, lo + (1 << 18))
+        g, u, y, xs = gate[s].double(), up[s].double(), dy[s].double(), x[s].double()
+        sg = torch.sigmoid(g)
+        dh = y @ wd.double()
+        want[0] += (dh * u * (sg + g * sg * (1 - sg))).T @ xs
+        want[1] += (dh * g * sg).T @ xs
+        want[2] += y.T @ (g * sg * u)
+    for got, ref in zip(dw, want):
+        assert far(got, ref) <= LONG
+
+
+def test_xent_weight_gradient_over_millions_of_tokens(dm):
+    """A small vocabulary and four million tokens, hidden states of one sign; the rows that are
+    no token's target are sums of one sign."""
+    t, d, v = 1 << 22, 64, 40
+    h, w = normal(81, (t, d)).abs_(), normal(82, (v, d), 0.05)
+    target = torch.zeros(t, dtype=torch.int64, device="cuda")
+    out = run_xent(dm, h, w, target, torch.full((t,), 2.0 ** -22, device="cuda"))
+    want = torch.zeros((v, d), dtype=torch.float64, device="cuda")
+    for lo in range(0, t, 1 << 18):
+        hs = h[lo:lo + (1 << 18)].double()
+        p = torch.softmax(hs @ w.double().T, 1)
+        p[:, 0] -= 1
+        want += p.T @ hs * 2.0 ** -22
+    assert far(out["dweight"], want) <= LONG
+    assert far(out["dweight"][1:], want[1:]) <= LONG
+
+
+def kinds(shape, seed):
+    """A positive matrix whose rows repeat four random ones, and these in 64 bits."""
+    four = normal(seed, (4, shape[1])).abs_()
+    return four.expand(shape[0] // 4, 4, shape[1]).reshape(shape), four.double()
+
+
+def bias(got, want):
+    """Mean relative error: roundings to bf16, 2^-8 / sqrt(3) each, average out over the
+    thousands of elements of a row; what truncation takes does not."""
+    return abs(float(((got.double() - want) / want).mean()))
+
+
+# 2^-11 for the truncation (above), and four times what the roundings leave
+BIAS = 2.0 ** -11 + 1e-4
+
+
+def test_xent_hidden_gradient_of_full_tiles_is_not_biased(dm):
+    """A million entries, hidden states and tiles so many that each sums all of them: with
+    hidden states of zero every entry weighs 2^-20, exactly."""
+    t, d, v = 1024, 5120, 1 << 20
+    w, four = kinds((v, d), 83)
+    w[0] = 0
+    target = torch.zeros(t, dtype=torch.int64, device="cuda")
+    out = run_xent(dm, torch.zeros((t, d), dtype=torch.bfloat16, device="cuda"), w, target,
+                   torch.ones(t, device="cuda"))
+    assert bias(out["dhidden"], (four.sum(0) * (v // 4) - four[0]) / v) <= BIAS
+
+
+def test_xent_weight_gradient_of_full_tiles_is_not_biased(dm):
+    t, d, v = 1 << 20, 5120, 1024
+    h, four = kinds((t, d), 84)
+    target = torch.zeros(t, dtype=torch.int64, device="cuda")
+    out = run_xent(dm, h, torch.zeros((v, d), dtype=torch.bfloat16, device="cuda"), target,
+                   torch.full((t,), 2.0 ** -20, device="cuda"))
+    assert bias(out["dweight"][1:], four.mean(0) / v) <= BIAS
+
+
+def test_ffn_weight_gradients_of_full_tiles_are_not_biased(dm):
+    t, d, f = 1 << 20, 1024, 1792
+    (x, x4), (dy, dy4), (gate, g4), (up, u4) = (kinds((t, n), 85 + i) for i, n in enumerate((d, d, f, f)))
+    wg, wu, wd = (normal(89 + i, s, 0.1).abs_() for i, s in enumerate([(f, d), (f, d), (d, f)]))
+    op = dm.GatedFFN(t, d, f)
+    dx, dw = torch.empty_like(x), [torch.empty_like(w) for w in (wg, wu, wd)]
+    op.backward(dy, x, wg, wu, wd, (gate, up), dx, *dw)
+    assert op.status() == dm.OK
+    sg, dh = torch.sigmoid(g4), dy4 @ wd.double()
+    a = g4 * sg
+    for got, left, right in zip(dw, (dh * u4 * (sg + a * (1 - sg)), dh * a, dy4), (x4, x4, a * u4)):
+        assert bias(got, left.T @ right * (t // 4)) <= BIAS

@@ -269,6 +269,8 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
  *  - A token matrix (x, y, dy, dx, hidden, dhidden) is `tokens` rows of `hidden`
  *    elements, `ld` >= hidden elements apart.  Rows that are 16-byte aligned are
  *    read and written in place; others are copied, or written with plain stores.
+ *  - An output shares no memory with another tensor of the call, except that y may be
+ *    x and dhidden may be hidden (dx over dy or x: DMUON_ERR_INVALID_ARG).
  *  - tokens == 0 is legal: nothing is written except weight gradients, which are
  *    set to zero.
  *  - Limits: tokens <= 4194304, hidden and ffn <= 524288, vocab <= 4194304.

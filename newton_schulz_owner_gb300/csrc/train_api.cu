@@ -322,6 +322,19 @@ int ffn_alignment(const dmuon_ffn_shape& s, const void* wg, const void* wu, cons
   return DMUON_OK;
 }
 
+// Whether two bf16 matrices of one size may share an element.
+bool overlap(const void* a, int64_t a_ld, const void* b, int64_t b_ld, int64_t rows, int64_t cols) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  if (pa + (uintptr_t(rows - 1) * uintptr_t(a_ld) + uintptr_t(cols)) * 2 <= pb ||
+      pb + (uintptr_t(rows - 1) * uintptr_t(b_ld) + uintptr_t(cols)) * 2 <= pa)
+    return false;
+  if (rows == 1 || a_ld != b_ld) return true;
+  // rows of one pitch: columns may lie side by side
+  const int64_t apart = (int64_t(pb) - int64_t(pa)) / 2 % a_ld;
+  const int64_t at = apart < 0 ? apart + a_ld : apart;
+  return at < cols || at + cols > a_ld;
+}
+
 int ffn_forward(const dmuon_ffn_shape& s, const void* x, int64_t x_ld, const void* wg,
                 const void* wu, const void* wd, void* y, int64_t y_ld, void* const* saved,
                 void* ws, cudaStream_t st) {
@@ -687,6 +700,10 @@ int dmuon_ffn_backward(const dmuon_ffn_shape* shape, const void* dy, int64_t dy_
                                                {dw_gate, dw_up, dw_down});
   if (st != DMUON_OK) return st;
   if (ws_bytes < dmuon_ffn_workspace_bytes(shape, 1)) return DMUON_ERR_WORKSPACE;
+  // dx is written before, and while, the weight gradients read dy and x
+  if (sh.tokens > 0 && (overlap(dx, dx_ld, dy, dy_ld, sh.tokens, sh.hidden) ||
+                        overlap(dx, dx_ld, x, x_ld, sh.tokens, sh.hidden)))
+    return DMUON_ERR_INVALID_ARG;
   return ffn_backward(*shape, dy, dy_ld, x, x_ld, w_gate, w_up, w_down, saved, dx, dx_ld, dw_gate,
                       dw_up, dw_down, workspace, stream);
 }

@@ -347,3 +347,24 @@ def test_ffn_weight_gradients_of_full_tiles_are_not_biased(dm):
     a = g4 * sg
     for got, left, right in zip(dw, (dh * u4 * (sg + a * (1 - sg)), dh * a, dy4), (x4, x4, a * u4)):
         assert bias(got, left.T @ right * (t // 4)) <= BIAS
+
+
+# ------------------------------------------------------------------ results in place
+@pytest.mark.parametrize("t,d,f", [(1, 64, 96), (3, 65, 96), (40, 64, 96), (300, 136, 264), (600, 64, 96)])
+def test_forward_and_hidden_gradient_in_place(dm, t, d, f):
+    """y may be x, dhidden may be hidden: the same bits as into tensors of their own."""
+    x = normal(98, (t, d))
+    ws = [normal(99 + i, s, s[1] ** -0.5) for i, s in enumerate([(f, d), (f, d), (d, f)])]
+    op = dm.GatedFFN(t, d, f, save=dm.SAVE_NONE)
+    y, place = torch.empty_like(x), x.clone()
+    op.forward(x, *ws, y)
+    op.forward(place, *ws, place)
+    assert torch.equal(y, place)
+    head, target, gl = normal(103, (500, d)), torch.arange(t, device="cuda") % 500, torch.ones(t, device="cuda")
+    want = run_xent(dm, x, head, target, gl)
+    place = x.clone()
+    op = dm.LinearXent(t, d, 500)
+    loss, lse, dw = torch.empty(t, device="cuda"), torch.empty(t, device="cuda"), torch.empty_like(head)
+    op.loss_and_grads(place, head, target, gl, loss, lse, place, dw)
+    assert op.status() == dm.OK
+    assert torch.equal(place, want["dhidden"]) and torch.equal(dw, want["dweight"])

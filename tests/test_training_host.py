@@ -258,3 +258,40 @@ def test_a_workspace_for_gradients_serves_the_loss_alone(dm):
         for d in (8, 64, 65, 4096):
             for v in (1, 1000, 151936, 1 << 20, 1 << 22):
                 assert xent_bytes(dm, t, d, v, grads=1) >= xent_bytes(dm, t, d, v, grads=0), (t, d, v)
+
+
+def test_ffn_backward_refuses_dx_over_its_inputs(dm):
+    """The weight gradients read x and dy after dx is written (and while it is)."""
+    lib, t, d, f = dm.lib(), 4, 64, 96
+    at = {n: (i + 2) << 24 for i, n in enumerate(("dy", "x", "dx", "wg", "wu", "wd", "gate", "up", "gg",
+                                                  "gu", "gd"))}
+
+    def call(dy_ld=d, x_ld=d, dx_ld=d, shape=(t, d, f, 0, 1), **move):
+        a = {**at, **move}
+        s = dm.FfnShape(*shape)
+        need = lib.dmuon_ffn_workspace_bytes(ctypes.byref(s), 1)
+        saved = (ctypes.c_void_p * 4)(a["gate"], a["up"], None, None)
+        return lib.dmuon_ffn_backward(ctypes.byref(s), a["dy"], dy_ld, a["x"], x_ld, a["wg"], a["wu"],
+                                      a["wd"], saved, a["dx"], dx_ld, a["gg"], a["gu"], a["gd"], W,
+                                      need, None)
+
+    import torch
+    if torch.cuda.is_available():       # these addresses must not reach one
+        pytest.skip("needs a machine without a GPU")
+    fine = call()
+    assert fine not in (dm.OK, dm.ERR_INVALID_ARG)          # past the checks, and no GPU
+    size = t * d * 2
+    for name in ("dy", "x"):
+        for shift in (0, 2, -2, 16, size - 2, 2 - size):
+            assert call(dx=at[name] + shift) == dm.ERR_INVALID_ARG, (name, shift)
+        for shift in (size, -size, size + 16):
+            assert call(dx=at[name] + shift) == fine, (name, shift)
+        # columns side by side in rows of one pitch share nothing
+        wide = dict(dy_ld=3 * d, x_ld=3 * d, dx_ld=3 * d)
+        for shift in (d, 2 * d, -d, -2 * d):
+            assert call(dx=at[name] + 2 * shift, **wide) == fine, (name, shift)
+        for shift in (d - 1, 2 * d + 1, 1 - d, 3 * d, -3 * d):
+            assert call(dx=at[name] + 2 * shift, **wide) == dm.ERR_INVALID_ARG, (name, shift)
+    one = dict(shape=(1, d, f, 0, 1))
+    assert call(dx=at["x"] + 2 * d, dx_ld=1 << 20, **one) == fine      # one row has no pitch
+    assert call(dx=at["x"] + 2 * d - 2, dx_ld=1 << 20, **one) == dm.ERR_INVALID_ARG

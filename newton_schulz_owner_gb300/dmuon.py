@@ -370,24 +370,30 @@ class MuonOwner:
 
 # ------------------------------------------------------------------ training-side operators
 # Tensors and workspace lie on the current device.
-def _current_device() -> int:
-    return torch.cuda.current_device()
+# current device without torch.cuda's check that CUDA is initialised (a tensor on one shows it)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch_device(t: torch.Tensor, what: str) -> int:
     """Index of the device that `t` lies on, which has to be the current one: that is where
     the library launches."""
-    dev = t.get_device()
+    dev = t.get_device()            # -1: not on a GPU
     if dev < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if dev != _current_device():
-        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    now = _current_device()
+    if dev != now:
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{now}")
     return dev
 
 
-def _same_device(t: torch.Tensor, dev: Optional[int], what: str) -> None:
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{what}: expected a tensor on cuda:{dev}, got one on {t.device}")
+def _launch_stream(stream, dev: int) -> int:
+    """_stream(stream), where `dev` is known to be the current device."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _elsewhere(t: torch.Tensor, dev: Optional[int], what: str) -> ValueError:
+    return ValueError(f"{what}: expected a CUDA tensor" +
+                      (f" on cuda:{dev}, got one on {t.device}" if dev is not None else ""))
 
 
 def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str, dev: Optional[int] = None) -> int:
@@ -396,9 +402,9 @@ def _bf16_rows(t: torch.Tensor, rows: int, cols: int, what: str, dev: Optional[i
         raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected bfloat16")
     if t.shape != (rows, cols):
         raise ValueError(f"{what}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    _same_device(t, dev, what)
+    at = t.get_device()
+    if at < 0 or at != (at if dev is None else dev):
+        raise _elsewhere(t, dev, what)
     ld, unit = t.stride()
     if rows <= 1 or cols == 0:
         ld = cols
@@ -413,9 +419,11 @@ def _dense(t: torch.Tensor, dtype, shape, what: str, dev: Optional[int] = None) 
         raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous CUDA tensor")
-    _same_device(t, dev, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    at = t.get_device()
+    if at < 0 or at != (at if dev is None else dev):
+        raise _elsewhere(t, dev, what)
     return t.data_ptr()
 
 
@@ -437,24 +445,24 @@ def _act8_args(t: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, where
     ld, unit = t.stride()
     if rows <= 1:
         ld = cols
-    if not t.is_cuda or (cols > 1 and unit != 1) or ld < cols:
-        raise ValueError(f"{where}: expected a CUDA tensor whose rows are contiguous")
+    if (cols > 1 and unit != 1) or ld < cols:
+        raise ValueError(f"{where}: expected a tensor whose rows are contiguous")
     dev = _launch_device(t, where)
-    return (rows, cols, dt, ld, _dense(codes, torch.int8, (rows, cols), "codes", dev),
+    return (dev, rows, cols, dt, ld, _dense(codes, torch.int8, (rows, cols), "codes", dev),
             _dense(scales, torch.bfloat16, (rows, _act8_blocks(cols)), "scales", dev))
 
 
 def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """Keep a 2-D activation (bf16 or fp32) as 8-bit codes, 32 columns to a scale."""
-    rows, cols, dt, ld, c, s = _act8_args(x, codes, scales, "act8_save")
-    _check(_lib.dmuon_act8_save(rows, cols, x.data_ptr(), ld, dt, c, s, _stream(stream)),
+    dev, rows, cols, dt, ld, c, s = _act8_args(x, codes, scales, "act8_save")
+    _check(_lib.dmuon_act8_save(rows, cols, x.data_ptr(), ld, dt, c, s, _launch_stream(stream, dev)),
            "dmuon_act8_save")
 
 
 def act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """Bring an 8-bit activation back into `out` (bf16 or fp32)."""
-    rows, cols, dt, ld, c, s = _act8_args(out, codes, scales, "act8_load")
-    _check(_lib.dmuon_act8_load(rows, cols, c, s, out.data_ptr(), ld, dt, _stream(stream)),
+    dev, rows, cols, dt, ld, c, s = _act8_args(out, codes, scales, "act8_load")
+    _check(_lib.dmuon_act8_load(rows, cols, c, s, out.data_ptr(), ld, dt, _launch_stream(stream, dev)),
            "dmuon_act8_load")
 
 
@@ -531,7 +539,7 @@ class GatedFFN:
         _check(_lib.dmuon_ffn_forward(ctypes.byref(shape), x.data_ptr(), x_ld, wg, wu, wd,
                                       y.data_ptr(), y_ld, self._saved(saved, t, dev),
                                       self.workspace.data_ptr(), self.workspace.numel(),
-                                      _stream(stream)), "dmuon_ffn_forward")
+                                      _launch_stream(stream, dev)), "dmuon_ffn_forward")
 
     def backward(self, dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down,
                  stream=None) -> None:
@@ -548,7 +556,7 @@ class GatedFFN:
         _check(_lib.dmuon_ffn_backward(ctypes.byref(shape), dy.data_ptr(), dy_ld, x.data_ptr(),
                                        x_ld, wg, wu, wd, self._saved(saved, t, dev), dx.data_ptr(),
                                        dx_ld, gg, gu, gd, self.workspace.data_ptr(),
-                                       self.workspace.numel(), _stream(stream)),
+                                       self.workspace.numel(), _launch_stream(stream, dev)),
                "dmuon_ffn_backward")
 
     def status(self, stream=None) -> int:
@@ -594,7 +602,7 @@ class LinearXent:
         shape = XentShape(t, d, self.vocab)
         _check(_lib.dmuon_xent(ctypes.byref(shape), hidden.data_ptr(), h_ld, w, tg, gl, lo, ls, dh,
                                dh_ld, dw, self.workspace.data_ptr(), self.workspace.numel(),
-                               _stream(stream)), "dmuon_xent")
+                               _launch_stream(stream, dev)), "dmuon_xent")
 
     def loss(self, hidden, weight, target, loss, lse, stream=None) -> None:
         """Per-token loss and log-sum-exp."""

@@ -368,3 +368,52 @@ def test_forward_and_hidden_gradient_in_place(dm, t, d, f):
     op.loss_and_grads(place, head, target, gl, loss, lse, place, dw)
     assert op.status() == dm.OK
     assert torch.equal(place, want["dhidden"]) and torch.equal(dw, want["dweight"])
+
+
+# ------------------------------------------------------------------ the orientations' ranges
+@pytest.mark.parametrize("t", [1030, 1100, 1290, 1344, 1345, 1540, 1568, 1569])
+def test_ffn_with_five_to_seven_token_tiles(dm, t):
+    """Products with the weight's rows as the tile's rows run up to 1568 tokens; sizes on both
+    sides of where the orientation changes, forward and backward."""
+    d, f = 200, 392
+    x, dy = normal(91, (t, d)), normal(92, (t, d), 1e-2)
+    wg, wu, wd = (normal(93 + i, s, s[1] ** -0.5) for i, s in enumerate([(f, d), (f, d), (d, f)]))
+    for save in (dm.SAVE_BF16, dm.SAVE_ACT8):
+        op = dm.GatedFFN(t, d, f, save=save)
+        saved, y = op.empty_saved(t), torch.full_like(x, 7.0)
+        op.forward(x, wg, wu, wd, y, saved)
+        dx, dw = torch.full_like(x, 7.0), [torch.full_like(w, 7.0) for w in (wg, wu, wd)]
+        op.backward(dy, x, wg, wu, wd, saved, dx, *dw)
+        assert op.status() == dm.OK
+        fwd = oracle.ffn_forward(np64(x), np64(wg), np64(wu), np64(wd))
+        if save == dm.SAVE_BF16:
+            gate, up = np64(saved[0]), np64(saved[1])
+        else:
+            gate, up = (oracle.act8_values(np64(saved[i]), np64(saved[i + 1])) for i in (0, 2))
+        ref = oracle.ffn_backward(np64(dy), np64(x), np64(wg), np64(wu), np64(wd), gate, up)
+        a, da = oracle.act("silu", gate)
+        dh, ax = np64(dy) @ np64(wd), np.abs(np64(x))
+        dg, du = np.abs(dh * up * da), np.abs(dh * a)
+        for got, want, mass in (
+                (y, fwd["y"], np.abs(fwd["h"]) @ np.abs(np64(wd)).T),
+                (dx, ref["dx"], dg @ np.abs(np64(wg)) + du @ np.abs(np64(wu))),
+                (dw[0], ref["dw_gate"], dg.T @ ax), (dw[1], ref["dw_up"], du.T @ ax),
+                (dw[2], ref["dw_down"], np.abs(np64(dy)).T @ np.abs(a * up))):
+            err = np.abs(np64(got) - want)
+            assert np.all(err <= U * np.abs(want) + 1.01 * U * mass)
+
+
+@pytest.mark.parametrize("t", [1030, 1100, 1290, 1568, 1569])
+def test_xent_gradients_with_five_to_seven_token_tiles(dm, t):
+    d, v = 136, 900
+    h, w = normal(95, (t, d), 2.0), normal(96, (v, d), d ** -0.5)
+    target = torch.from_numpy(np.random.default_rng(97).integers(0, v, t)).cuda()
+    hd, wd, tg = np64(h), np64(w), target.cpu().numpy()
+    loss, lse, g = xent64(hd, wd, tg)
+    out = run_xent(dm, h, w, target, torch.ones(t, device="cuda"))
+    bound = 2.0 ** -21 * (np.abs(hd) @ np.abs(wd).T).max(1) + 2.0 ** -20 * (1 + np.abs(lse))
+    assert np.all(np.abs(np64(out["loss"]) - loss) <= bound)
+    assert np.all(np.abs(np64(out["lse"]) - lse) <= bound)
+    for got, want, mass in ((out["dhidden"], g @ wd, np.abs(g) @ np.abs(wd)),
+                            (out["dweight"], g.T @ hd, np.abs(g).T @ np.abs(hd))):
+        assert np.all(np.abs(np64(got) - want) <= U * np.abs(want) + 1.26 * U * mass)

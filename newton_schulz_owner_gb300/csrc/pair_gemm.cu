@@ -674,7 +674,7 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
     };
 
     if constexpr (EPI == kLinStore && !SWAP) {
-      if (P.sum == nullptr && P.c_map >= 0) {
+      if (g.sum == nullptr && P.c_map >= 0) {
         const float f = g.scale != nullptr ? *g.scale : 1.f;
         const bool second = G.inside(2);
 #pragma unroll 1
@@ -707,8 +707,8 @@ DM_DEV void epilogue(const LinArgs& g, uint32_t rank, uint64_t* tfull, uint64_t*
       if constexpr (EPI == kLinStore) {
         float v[32];
         load_acc(k, v);
-        if (P.sum != nullptr) {
-          float* sp = P.sum + (long long)r * P.cols + c0;
+        if (!SWAP && g.sum != nullptr) {
+          float* sp = g.sum + P.sum_at + (long long)r * P.cols + c0;
           const bool vec = (P.cols & 3) == 0 && n >= 32;
           if (g.sum_read && r < P.rows) {
             if (vec) {
@@ -1372,8 +1372,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const bool vec = P.c_map >= 0;
   if (EPI == kLinStore) {
     if (!in || n <= 0) return;
-    if (P.sum != nullptr) {
-      float* sp = P.sum + (long long)r * P.cols + c;
+    if (g.sum != nullptr) {
+      float* sp = g.sum + P.sum_at + (long long)r * P.cols + c;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < n) {

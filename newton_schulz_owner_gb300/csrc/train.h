@@ -68,7 +68,7 @@ struct LinProblem {
   int c_map;             // output map, or -1: c is written with plain stores
   __nv_bfloat16* c;
   long long c_ld;
-  float* sum;            // kLinStore: fp32 running sum over launches (row pitch = cols), or null
+  long long sum_at;      // where its running sum starts in LinArgs::sum
 };
 
 struct LinArgs {
@@ -84,7 +84,10 @@ struct LinArgs {
   int total_units;       // full_tiles + split * (tiles - full_tiles)
   float* partial;        // fp32 parts of the split tiles
   int* err;
-  int sum_read, sum_write;  // add what the products' sums hold; write there instead of C
+  // kLinStore, plain: fp32 running sums over launches (row pitch = cols of the product).  One
+  // address for all products: testing one of each product's own costs 0.3 us a launch.
+  float* sum;
+  int sum_read, sum_write;  // add what a sum holds; write there instead of C
   const float* scale;    // C = scale * acc (device scalar), or null
   // kLinGlu / kLinGluGrad
   int act, keep;

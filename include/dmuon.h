@@ -268,7 +268,8 @@ int dmuon_adamw(int n, const int64_t* numel, void* const* param, int param_dt,
  *    workspace, padded, on every call).
  *  - A token matrix (x, y, dy, dx, hidden, dhidden) is `tokens` rows of `hidden`
  *    elements, `ld` >= hidden elements apart.  Rows that are 16-byte aligned are
- *    read and written in place; others are copied, or written with plain stores.
+ *    read and written in place; others are copied, or written with plain stores.  For
+ *    gradients `hidden` is always copied (masked rows become zeros).
  *  - An output shares no memory with another tensor of the call, except that y may be
  *    x and dhidden may be hidden (dx over dy or x: DMUON_ERR_INVALID_ARG).
  *  - tokens == 0 is legal: nothing is written except weight gradients, which are

@@ -385,6 +385,132 @@ int dmuon_xent(const dmuon_xent_shape* shape, const void* hidden, int64_t hidden
                size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Token mixing: the norms and rotation of queries and keys, and linear attention.
+ *
+ * Conventions beside those of the training-side operators above:
+ *  - A tensor of heads has `tokens` x `heads` rows of `dim` contiguous bf16 elements; element
+ *    (t, h, i) lies at data[t * token_stride + h * head_stride + i].  Any order of tokens and
+ *    heads and any padding will do, and parts of one packed projection; rows do not overlap.
+ *  - Sums, states, decays, angles and frequencies are fp32 or finer.
+ *  - tokens == 0 is legal; limits: tokens <= 4194304, heads <= 65536.
+ */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;  /* elements */
+} dmuon_heads;
+
+/* Sizes of the query and key heads. */
+typedef struct {
+  int64_t tokens, q_heads, k_heads;  /* k_heads may be 0 */
+  int64_t head_dim;    /* a multiple of 8, at most 256 */
+  int64_t rotary_dim;  /* the first elements of a head that turn: a multiple of 8, 0 for none */
+  int interleaved;     /* pairs (2i, 2i + 1) if nonzero, else (i, i + rotary_dim / 2) */
+  float eps;           /* >= 0 */
+} dmuon_qk_shape;
+
+/*
+ * dmuon_qk_norm_rope -- norm and rotation of every query and key head, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * w           over the head_dim elements of a head
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i]
+ *                                               for pair i of the first rotary_dim elements
+ *   w_q, w_k   device, bf16 gains, head_dim each; NULL: gains of 1
+ *   inv_freq   device, fp32, rotary_dim / 2 angles per position
+ *   position   device, int32 per token (any value)
+ * The angle is taken modulo a turn in 64-bit fixed point, so that far positions lose nothing:
+ * sines and cosines are within 2^-21 for any position.  Squares are summed in fp32 (elements
+ * beyond 1e18 overflow).  An output may be its own input (q_out = q, k_out = k); a NaN or an
+ * infinity reaches its own head only.  One launch; no workspace.  Rows at 8-byte addresses move
+ * in 8-byte pieces, others element by element.
+ */
+int dmuon_qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* q, const dmuon_heads* k,
+                       const void* w_q, const void* w_k, const float* inv_freq,
+                       const int32_t* position, const dmuon_heads* q_out,
+                       const dmuon_heads* k_out, cudaStream_t stream);
+
+/*
+ * dmuon_qk_norm_rope_backward -- its gradients, from its inputs q and k:
+ *   g = dout turned back,  n = x / sqrt(mean(x^2) + eps)
+ *   dw = sum over tokens and heads of g n
+ *   dx = (g w - n mean(g w n)) / sqrt(mean(x^2) + eps)
+ *   dw_q, dw_k  device, bf16, head_dim each, written, not added to; NULL: not wanted
+ * dq may be dq_out, and dk dk_out.  tokens == 0 sets dw_q and dw_k to zero.
+ */
+size_t dmuon_qk_norm_rope_workspace_bytes(const dmuon_qk_shape* shape);
+int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const dmuon_heads* dq_out,
+                                const dmuon_heads* dk_out, const dmuon_heads* q,
+                                const dmuon_heads* k, const void* w_q, const void* w_k,
+                                const float* inv_freq, const int32_t* position,
+                                const dmuon_heads* dq, const dmuon_heads* dk, void* dw_q,
+                                void* dw_k, void* workspace, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/* Sizes of a linear attention. */
+typedef struct {
+  int64_t tokens, sequences;     /* of all sequences together; 1 <= sequences <= 65536 */
+  int64_t heads;
+  int64_t key_dim, value_dim;    /* multiples of 8, at most 128 */
+  float scale;                   /* not 0 */
+} dmuon_linattn_shape;
+
+/*
+ * dmuon_linattn_forward -- causal linear attention with a decay for each head, per sequence:
+ *   S_t = exp(log_decay) S_{t-1} + k_t v_t^T,   out_t = scale q_t S_t
+ *   log_decay    device, fp32 per head, <= 0 (0: no decay, -infinity: each token for itself)
+ *   offsets      device, int32, sequences + 1: sequence s is tokens offsets[s] ..
+ *                offsets[s + 1] - 1 (sequences may be empty); NULL: one sequence of all
+ *                tokens.  Tokens before the first and after the last sequence are not touched;
+ *                offsets are cut to 0 .. tokens.
+ *   state        device, fp32, contiguous (sequences, heads, key_dim, value_dim): S before the
+ *                first token of each sequence; NULL: zeros
+ *   final_state  the same after the last token; NULL: not wanted.  May be `state`.
+ * Tokens are taken in blocks of 128 counted from their sequence's start.  The weighted scores of
+ * a block, the state that enters it and the keys times their decay are rounded to bf16 as
+ * operands of products that accumulate in fp32; with final_state the keys are kept to 16 bits, so
+ * that the state is within 2^-16 of the sum of its terms' magnitudes.
+ * A NaN or an infinity in v reaches all tokens of its block of its sequence and those after it
+ * (one in k its own token and those after, one in q its own); no other sequence or head.
+ * Rows of heads are 16-byte aligned (strides multiples of 8 elements), DMUON_ERR_ALIGNMENT
+ * otherwise; so are states.
+ */
+size_t dmuon_linattn_workspace_bytes(const dmuon_linattn_shape* shape, int backward);
+int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q,
+                          const dmuon_heads* k, const dmuon_heads* v, const float* log_decay,
+                          const int32_t* offsets, const float* state, float* final_state,
+                          const dmuon_heads* out, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/*
+ * dmuon_linattn_backward -- its gradients (nothing is kept by forward):
+ *   dfinal_state  gradient of final_state, or NULL for zeros
+ *   dstate        gradient of state, or NULL: not wanted.  May be dfinal_state.
+ * With g_t = scale dout_t and D_t the gradient of S_t, both along the sequence:
+ *   D_t = q_t g_t^T + exp(log_decay) D_{t+1},   dq_t = S_t g_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
+ * A NaN or an infinity in q, k, v or dout may reach all gradients of its sequence and head.
+ */
+int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* dout,
+                           const dmuon_heads* q, const dmuon_heads* k, const dmuon_heads* v,
+                           const float* log_decay, const int32_t* offsets, const float* state,
+                           const float* dfinal_state, const dmuon_heads* dq,
+                           const dmuon_heads* dk, const dmuon_heads* dv, float* dstate,
+                           void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * dmuon_linattn_step -- one token for each of `tokens` streams (shape.sequences is not used):
+ * row r reads the state of slot[r], writes the state after its token and its output, all in
+ * fp32 but for the bf16 output.
+ *   slot       device, int32 per row, or NULL: row r has slot r.  A slot outside [0, slots)
+ *              skips its row (padding): nothing of it is read or written.  Rows that share a
+ *              slot are taken one after another in their order.
+ *   state      device, fp32, contiguous (slots, heads, key_dim, value_dim)
+ *   new_state  the same; may be `state` (in place).  Slots that no row names are not written.
+ * One launch; no workspace.
+ */
+int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
+                       const dmuon_heads* k, const dmuon_heads* v, const float* log_decay,
+                       const int32_t* slot, int64_t slots, const float* state, float* new_state,
+                       const dmuon_heads* out, cudaStream_t stream);
+
+/*
  * dmuon_stream_status -- synchronises `stream`, then reports (and clears) the
  * device error word kept in `workspace`: DMUON_OK, DMUON_ERR_TIMEOUT when a
  * bounded device wait gave up, DMUON_ERR_CUDA when the stream holds a CUDA

@@ -1,0 +1,78 @@
+// Host-side launchers of the operators that mix tokens: the norms and rotation of query
+// and key heads, and linear attention with a decay for each head.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "train.h"
+
+namespace dm {
+
+// Rows of heads: element (t, h, i) at p[t * ts + h * hs + i].
+struct Heads {
+  __nv_bfloat16* p;
+  long long ts, hs;
+};
+
+// ------------------------------------------------------------------ norms and rotation
+struct RopeArgs {
+  // [0]: queries, [1]: keys.  Forward: x -> out.  Backward: x and dy -> out = dx.
+  Heads x[2], dy[2], out[2];
+  const __nv_bfloat16* w[2];
+  const float* inv_freq;
+  const int32_t* position;
+  int tokens, heads[2], dim, rotary;
+  float eps;
+  int parts;                  // warps that share a token's heads
+  float* partial;             // backward: sums of the gains' gradients, one row per block
+  __nv_bfloat16* dw[2];       // or null
+};
+constexpr int kRopeBlocks = 1216;  // most blocks of a backward launch
+// vec: every row lies at an 8-byte address.
+cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, int sms,
+                        cudaStream_t s);
+
+// ------------------------------------------------------------------ linear attention
+// One sweep over every sequence, along time or against it (mix_kernel in linattn.cu):
+//   along:    S_t = a S_{t-1} + k_t v_t^T,  out_t = scale q_t S_t         a = exp(log_decay)
+//   against:  R_t = a R_{t+1} + ...,        out_t = scale q_t (R_{t+1} a^0 + k_t v_t^T ...)
+struct LinAttnArgs {
+  CUtensorMap q, k, v, o;     // loads: 64 x 1 x 128 boxes; o: stores of 32 x 1 x 32
+  const float* log_decay;
+  const int32_t* offsets;
+  int sequences, heads, tokens, dk, dv;
+  float scale;
+  int against;
+  const float* state_in;      // or null
+  float* state_out;           // or null
+  float in_scale, out_scale;  // of the state on its way in and out
+  int st_row, st_col;         // element strides of a state (row: the keys' side)
+  Heads out;
+  int split;                  // CTAs of a cluster, which share a sequence of a head
+  float* local;               // their states on the way to one another
+  int* err;
+};
+constexpr int kMixBlock = 128;   // tokens taken at a time
+constexpr int kMixMaxSplit = 8;
+constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a CTA
+constexpr int64_t kMixMaxLocals = 640;  // CTAs of a launch whose sequences are shared
+cudaError_t linattn_prepare();  // once per device
+cudaError_t launch_linattn(const LinAttnArgs& g, cudaStream_t s);
+
+struct LinStepArgs {
+  Heads q, k, v, out;
+  const float* log_decay;
+  const int32_t* slot;
+  long long slots;
+  const float* state;
+  float* new_state;
+  int rows, heads, dk, dv;
+  float scale;
+};
+cudaError_t launch_linattn_step(const LinStepArgs& g, cudaStream_t s);
+
+}  // namespace dm

@@ -1,0 +1,444 @@
+// C ABI of the operators that mix tokens: argument checks, tensor maps and launch sequences.
+// See include/dmuon.h.
+#include "dmuon.h"
+#include "launch.h"
+#include "mix.h"
+#include "train.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+#include <mutex>
+
+namespace dm {
+namespace {
+
+constexpr size_t kHdrBytes = 256;  // workspace header: device error word
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxHeads = int64_t(1) << 16,
+                  kMaxSequences = int64_t(1) << 16;
+
+using bf16 = __nv_bfloat16;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Ready the current device: the kernels' shared memory opt-in, once.
+int device_ready(int* sms) {
+  int d = 0, clusters = 0;
+  const int st = library_device(&d, sms, &clusters);
+  if (st != DMUON_OK) return st;
+  static std::mutex mu;
+  static bool ready[kMaxDevices] = {};
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ready[d]) {
+    if (linattn_prepare() != cudaSuccess) return DMUON_ERR_CUDA;
+    ready[d] = true;
+  }
+  return DMUON_OK;
+}
+
+// ------------------------------------------------------------------ tensors of heads
+// A tensor's rows with strides that also hold where there is one token or one head only.
+struct Rows {
+  uintptr_t p;
+  int64_t tokens, heads, dim, ts, hs;
+  uintptr_t end() const {
+    return p + uintptr_t((tokens - 1) * ts + (heads - 1) * hs + dim) * 2;
+  }
+};
+// Fills r; false: a null pointer, or rows that may overlap.
+bool rows_of(const dmuon_heads* h, int64_t tokens, int64_t heads, int64_t dim, Rows* r) {
+  if (h == nullptr || h->data == nullptr) return false;
+  constexpr int64_t kMost = int64_t(1) << 38;  // of a stride, in elements
+  *r = Rows{reinterpret_cast<uintptr_t>(h->data), tokens, heads, dim, h->token_stride,
+            h->head_stride};
+  if (heads == 1) r->hs = dim;
+  if (tokens == 1) r->ts = heads == 1 ? dim : r->hs;
+  if (r->hs < dim || r->ts < dim || r->hs > kMost || r->ts > kMost) return false;
+  if (tokens == 1 || heads == 1) return true;
+  return r->ts >= (heads - 1) * r->hs + dim || r->hs >= (tokens - 1) * r->ts + dim;
+}
+// Whether two tensors of the same tokens (heads and dims may differ) may share an element.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.end() <= b.p || b.end() <= a.p) return false;
+  // a stride over one row is any stride
+  if ((a.tokens > 1 && a.ts != b.ts) || (a.heads > 1 && b.heads > 1 && a.hs != b.hs)) return true;
+  const int64_t ts = a.tokens > 1 ? a.ts : int64_t(1) << 40, hs = a.heads > 1 ? a.hs : b.hs;
+  // parts of one packed tensor: b's place against a's as whole strides, outer and inner, and a
+  // rest.  Element (t, h, x) of a is (t', h', x') of b where
+  //   apart = (t - t') ts + (h - h') hs + (x - x')
+  const int64_t apart = (int64_t(b.p) - int64_t(a.p)) / 2;
+  const bool by_token = ts >= hs;
+  const int64_t s1 = by_token ? ts : hs, s2 = by_token ? hs : ts;
+  const int64_t a1 = by_token ? a.tokens : a.heads, b1 = by_token ? b.tokens : b.heads;
+  const int64_t a2 = by_token ? a.heads : a.tokens, b2 = by_token ? b.heads : b.tokens;
+  auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+  const int64_t k1 = floor_div(apart, s1);
+  for (int64_t i = k1; i <= k1 + 1; ++i) {
+    if (i <= -b1 || i >= a1) continue;
+    const int64_t rest = apart - i * s1, k2 = floor_div(rest, s2);
+    for (int64_t j = k2; j <= k2 + 1; ++j) {
+      if (j <= -b2 || j >= a2) continue;
+      const int64_t x = rest - j * s2;
+      if (x < a.dim && -x < b.dim) return true;
+    }
+  }
+  return false;
+}
+bool same(const Rows& a, const Rows& b) {
+  return a.p == b.p && (a.tokens == 1 || a.ts == b.ts) && (a.heads == 1 || a.hs == b.hs);
+}
+bool rows_aligned(const Rows& r, size_t bytes) {
+  return r.p % bytes == 0 && r.ts * 2 % int64_t(bytes) == 0 && r.hs * 2 % int64_t(bytes) == 0;
+}
+Heads device_heads(const Rows& r) { return {reinterpret_cast<bf16*>(r.p), r.ts, r.hs}; }
+
+// ------------------------------------------------------------------ norms and rotation
+bool qk_shape_ok(const dmuon_qk_shape* s) {
+  return s != nullptr && s->tokens >= 0 && s->tokens <= kMaxTokens && s->q_heads >= 1 &&
+         s->q_heads <= kMaxHeads && s->k_heads >= 0 && s->k_heads <= kMaxHeads &&
+         s->head_dim >= 8 && s->head_dim <= 256 && s->head_dim % 8 == 0 && s->rotary_dim >= 0 &&
+         s->rotary_dim <= s->head_dim && s->rotary_dim % 8 == 0 && s->eps >= 0.f &&
+         std::isfinite(s->eps);
+}
+size_t qk_workspace(const dmuon_qk_shape& s) {
+  return kHdrBytes + size_t(kRopeBlocks) * 2 * size_t(s.head_dim) * sizeof(float);
+}
+
+// Forward (dout null) and backward.
+int qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* const x[2],
+                 const dmuon_heads* const dout[2], const dmuon_heads* const out[2],
+                 const void* const w[2], const float* inv_freq, const int32_t* position,
+                 void* const dw[2], float* partial, cudaStream_t st) {
+  const dmuon_qk_shape& s = *shape;
+  const int64_t heads[2] = {s.q_heads, s.k_heads};
+  if (s.rotary_dim > 0 && (inv_freq == nullptr || (position == nullptr && s.tokens > 0)))
+    return DMUON_ERR_INVALID_ARG;
+  const bool backward = partial != nullptr;
+  RopeArgs g{};
+  bool vec = true;
+  Rows xr[2], dr[2], orow[2];
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0 || s.tokens == 0) continue;
+    if (!rows_of(x[i], s.tokens, heads[i], s.head_dim, &xr[i]) ||
+        !rows_of(out[i], s.tokens, heads[i], s.head_dim, &orow[i]) ||
+        (backward && !rows_of(dout[i], s.tokens, heads[i], s.head_dim, &dr[i])))
+      return DMUON_ERR_INVALID_ARG;
+  }
+  if (!aligned(w[0], 2) || !aligned(w[1], 2) || !aligned(inv_freq, 4) || !aligned(position, 4) ||
+      !aligned(dw[0], 2) || !aligned(dw[1], 2))
+    return DMUON_ERR_ALIGNMENT;
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0 || s.tokens == 0) continue;
+    if (xr[i].p % 2 != 0 || orow[i].p % 2 != 0 || (backward && dr[i].p % 2 != 0))
+      return DMUON_ERR_ALIGNMENT;
+    vec = vec && rows_aligned(xr[i], 8) && rows_aligned(orow[i], 8) &&
+          (!backward || rows_aligned(dr[i], 8));
+    g.x[i] = device_heads(xr[i]);
+    g.out[i] = device_heads(orow[i]);
+    if (backward) g.dy[i] = device_heads(dr[i]);
+  }
+  // an output is its own input, or apart from every input and the other output
+  if (s.tokens > 0) {
+    for (int i = 0; i < 2; ++i) {
+      if (heads[i] == 0) continue;
+      for (int j = 0; j < 2; ++j) {
+        if (heads[j] == 0) continue;
+        if (backward) {
+          if (overlap(orow[i], xr[j])) return DMUON_ERR_INVALID_ARG;
+          if (!(i == j && same(orow[i], dr[j])) && overlap(orow[i], dr[j]))
+            return DMUON_ERR_INVALID_ARG;
+        } else if (!(i == j && same(orow[i], xr[j])) && overlap(orow[i], xr[j])) {
+          return DMUON_ERR_INVALID_ARG;
+        }
+        if (i < j && overlap(orow[i], orow[j])) return DMUON_ERR_INVALID_ARG;
+      }
+    }
+  }
+  if (s.tokens == 0 && !backward) return DMUON_OK;
+  int sms = 0;
+  const int e = device_ready(&sms);
+  if (e != DMUON_OK) return e;
+  for (int i = 0; i < 2; ++i) {
+    g.w[i] = static_cast<const bf16*>(w[i]);
+    g.dw[i] = static_cast<bf16*>(dw[i]);
+    g.heads[i] = int(heads[i]);
+  }
+  g.inv_freq = inv_freq;
+  g.position = position;
+  g.tokens = int(s.tokens);
+  g.dim = int(s.head_dim);
+  g.rotary = int(s.rotary_dim);
+  g.eps = s.eps;
+  g.partial = dw[0] != nullptr || dw[1] != nullptr ? partial : nullptr;
+  return launch_rope(g, backward, s.interleaved != 0, vec, sms, st) == cudaSuccess
+             ? DMUON_OK
+             : DMUON_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ linear attention
+bool linattn_shape_ok(const dmuon_linattn_shape* s) {
+  return s != nullptr && s->tokens >= 0 && s->tokens <= kMaxTokens && s->sequences >= 1 &&
+         s->sequences <= kMaxSequences && s->heads >= 1 && s->heads <= kMaxHeads &&
+         s->key_dim >= 8 && s->key_dim <= 128 && s->key_dim % 8 == 0 && s->value_dim >= 8 &&
+         s->value_dim <= 128 && s->value_dim % 8 == 0 && std::isfinite(s->scale) &&
+         s->scale != 0.f && s->sequences * s->heads <= (int64_t(1) << 27);
+}
+
+// CTAs that share a sequence of a head.
+int choose_split(const dmuon_linattn_shape& s, int sms) {
+  const int64_t blocks = ceil_div(ceil_div(s.tokens, s.sequences), kMixBlock);
+  const int64_t items = s.sequences * s.heads;
+  int best = 1;
+  double least = 0;
+  for (int c = 1; c <= kMixMaxSplit; c *= 2) {
+    if (c > 1 && (c > blocks || items * c > kMixMaxLocals)) break;
+    const double per = double(ceil_div(blocks, c));
+    const double cost = double(ceil_div(items * c, sms)) * (per * (c > 1 ? 1.5 : 1.0) + 2);
+    if (c == 1 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
+}
+// The workspace serves any split of any number of tokens and sequences up to the shape's.
+size_t linattn_workspace(const dmuon_linattn_shape& s) {
+  const int64_t locals = std::min(s.sequences * s.heads * kMixMaxSplit, kMixMaxLocals);
+  return kHdrBytes + size_t(locals) * kMixLocalBytes;
+}
+
+bool tile_map(CUtensorMap* m, const Rows& r, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+  const TensorMapEncode enc = library_tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(r.dim), cuuint64_t(r.heads), cuuint64_t(r.tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(r.hs) * 2, cuuint64_t(r.ts) * 2};
+  const cuuint32_t box[3] = {cuuint32_t(box_cols), 1, cuuint32_t(box_rows)}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, reinterpret_cast<void*>(r.p), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One sweep: out of (q, k, v), key width q.dim, value width v.dim.
+struct Sweep {
+  const Rows *q, *k, *v, *out;
+  bool against;
+  const float* state_in;
+  float* state_out;
+  bool transposed;  // the caller's state is (value, key)
+  float in_scale, out_scale;
+};
+int run_sweep(const dmuon_linattn_shape& s, const Sweep& w, const float* log_decay,
+              const int32_t* offsets, int split, void* ws, cudaStream_t st) {
+  LinAttnArgs g{};
+  if (!tile_map(&g.q, *w.q, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tile_map(&g.k, *w.k, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tile_map(&g.v, *w.v, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tile_map(&g.o, *w.out, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return DMUON_ERR_CUDA;
+  g.log_decay = log_decay;
+  g.offsets = offsets;
+  g.sequences = int(s.sequences);
+  g.heads = int(s.heads);
+  g.tokens = int(s.tokens);
+  g.dk = int(w.q->dim);
+  g.dv = int(w.v->dim);
+  g.scale = s.scale;
+  g.against = w.against;
+  g.state_in = w.state_in;
+  g.state_out = w.state_out;
+  g.in_scale = w.in_scale;
+  g.out_scale = w.out_scale;
+  g.st_row = w.transposed ? 1 : g.dv;
+  g.st_col = w.transposed ? g.dk : 1;
+  g.out = device_heads(*w.out);
+  g.split = split;
+  g.err = static_cast<int*>(ws);
+  g.local = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHdrBytes);
+  return launch_linattn(g, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
+}
+
+// Rows of a tensor of the call, checked; `status` keeps the first failure.
+Rows checked(const dmuon_heads* h, const dmuon_linattn_shape& s, int64_t dim, int* status) {
+  Rows r{};
+  if (!rows_of(h, s.tokens, s.heads, dim, &r)) *status = DMUON_ERR_INVALID_ARG;
+  else if (*status == DMUON_OK && !rows_aligned(r, 16)) *status = DMUON_ERR_ALIGNMENT;
+  return r;
+}
+int check_common(const dmuon_linattn_shape* s, const float* log_decay, const int32_t* offsets,
+                 const float* a, const float* b, void* ws, size_t ws_bytes) {
+  if (!linattn_shape_ok(s) || log_decay == nullptr || ws == nullptr ||
+      (offsets == nullptr && s->sequences != 1))
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !aligned(log_decay, 4) || !aligned(offsets, 4) || !aligned(a, 16) ||
+      !aligned(b, 16))
+    return DMUON_ERR_ALIGNMENT;
+  if (ws_bytes < linattn_workspace(*s)) return DMUON_ERR_WORKSPACE;
+  return DMUON_OK;
+}
+
+}  // namespace
+}  // namespace dm
+
+using namespace dm;
+
+extern "C" {
+
+int dmuon_qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* q, const dmuon_heads* k,
+                       const void* w_q, const void* w_k, const float* inv_freq,
+                       const int32_t* position, const dmuon_heads* q_out,
+                       const dmuon_heads* k_out, cudaStream_t stream) {
+  if (!qk_shape_ok(shape)) return DMUON_ERR_INVALID_ARG;
+  const dmuon_heads *x[2] = {q, k}, *none[2] = {}, *out[2] = {q_out, k_out};
+  const void* w[2] = {w_q, w_k};
+  void* dw[2] = {};
+  return qk_norm_rope(shape, x, none, out, w, inv_freq, position, dw, nullptr, stream);
+}
+
+size_t dmuon_qk_norm_rope_workspace_bytes(const dmuon_qk_shape* shape) {
+  return qk_shape_ok(shape) ? qk_workspace(*shape) : 0;
+}
+
+int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const dmuon_heads* dq_out,
+                                const dmuon_heads* dk_out, const dmuon_heads* q,
+                                const dmuon_heads* k, const void* w_q, const void* w_k,
+                                const float* inv_freq, const int32_t* position,
+                                const dmuon_heads* dq, const dmuon_heads* dk, void* dw_q,
+                                void* dw_k, void* workspace, size_t ws_bytes,
+                                cudaStream_t stream) {
+  if (!qk_shape_ok(shape) || workspace == nullptr) return DMUON_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return DMUON_ERR_ALIGNMENT;
+  if (ws_bytes < qk_workspace(*shape)) return DMUON_ERR_WORKSPACE;
+  const dmuon_heads *x[2] = {q, k}, *dout[2] = {dq_out, dk_out}, *out[2] = {dq, dk};
+  const void* w[2] = {w_q, w_k};
+  void* dw[2] = {dw_q, shape->k_heads > 0 ? dw_k : nullptr};
+  float* partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kHdrBytes);
+  return qk_norm_rope(shape, x, dout, out, w, inv_freq, position, dw, partial, stream);
+}
+
+size_t dmuon_linattn_workspace_bytes(const dmuon_linattn_shape* shape, int backward) {
+  (void)backward;
+  return linattn_shape_ok(shape) ? linattn_workspace(*shape) : 0;
+}
+
+int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q,
+                          const dmuon_heads* k, const dmuon_heads* v, const float* log_decay,
+                          const int32_t* offsets, const float* state, float* final_state,
+                          const dmuon_heads* out, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream) {
+  int e = check_common(shape, log_decay, offsets, state, final_state, workspace, ws_bytes);
+  if (e != DMUON_OK) return e;
+  const dmuon_linattn_shape& s = *shape;
+  if (s.tokens == 0 && final_state == nullptr) return DMUON_OK;
+  // without tokens the states still pass through: a tensor of one token that no sequence has
+  dmuon_linattn_shape one = s;
+  dmuon_heads dummy{workspace, s.heads * 128, 128};
+  if (s.tokens == 0) {
+    one.tokens = 1;
+    q = k = v = out = &dummy;
+  }
+  const Rows qr = checked(q, one, s.key_dim, &e), kr = checked(k, one, s.key_dim, &e),
+             vr = checked(v, one, s.value_dim, &e), orow = checked(out, one, s.value_dim, &e);
+  if (e != DMUON_OK) return e;
+  if (s.tokens > 0 && (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)))
+    return DMUON_ERR_INVALID_ARG;
+  int sms = 0;
+  e = device_ready(&sms);
+  if (e != DMUON_OK) return e;
+  const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, 1.f, 1.f};
+  return run_sweep(s, w, log_decay, offsets, choose_split(s, sms), workspace, stream);
+}
+
+int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* dout,
+                           const dmuon_heads* q, const dmuon_heads* k, const dmuon_heads* v,
+                           const float* log_decay, const int32_t* offsets, const float* state,
+                           const float* dfinal_state, const dmuon_heads* dq,
+                           const dmuon_heads* dk, const dmuon_heads* dv, float* dstate,
+                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  int e = check_common(shape, log_decay, offsets, state, dfinal_state, workspace, ws_bytes);
+  if (e != DMUON_OK) return e;
+  if (!aligned(dstate, 16)) return DMUON_ERR_ALIGNMENT;
+  const dmuon_linattn_shape& s = *shape;
+  if (s.tokens == 0 && dstate == nullptr) return DMUON_OK;
+  dmuon_linattn_shape one = s;
+  dmuon_heads dummy{workspace, s.heads * 128, 128};
+  if (s.tokens == 0) {
+    one.tokens = 1;
+    dout = q = k = v = dq = dk = dv = &dummy;
+  }
+  const Rows dor = checked(dout, one, s.value_dim, &e), qr = checked(q, one, s.key_dim, &e),
+             kr = checked(k, one, s.key_dim, &e), vr = checked(v, one, s.value_dim, &e),
+             dqr = checked(dq, one, s.key_dim, &e), dkr = checked(dk, one, s.key_dim, &e),
+             dvr = checked(dv, one, s.value_dim, &e);
+  if (e != DMUON_OK) return e;
+  if (s.tokens > 0) {
+    for (const Rows* o : {&dqr, &dkr, &dvr})
+      for (const Rows* i : {&dor, &qr, &kr, &vr})
+        if (overlap(*o, *i)) return DMUON_ERR_INVALID_ARG;
+    if (overlap(dqr, dkr) || overlap(dqr, dvr) || overlap(dkr, dvr)) return DMUON_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  e = device_ready(&sms);
+  if (e != DMUON_OK) return e;
+  const int split = choose_split(s, sms);
+  const float inv = 1.f / s.scale;
+  // dk reads dfinal_state before dv's sweep may write dstate over it
+  const Sweep sweeps[3] = {
+      {&dor, &vr, &kr, &dqr, false, state, nullptr, true, 1.f, 1.f},
+      {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, inv, 1.f},
+      {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, inv, s.scale}};
+  for (int i = s.tokens > 0 ? 0 : 2; i < 3; ++i) {
+    e = run_sweep(s, sweeps[i], log_decay, offsets, split, workspace, stream);
+    if (e != DMUON_OK) return e;
+  }
+  return DMUON_OK;
+}
+
+int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
+                       const dmuon_heads* k, const dmuon_heads* v, const float* log_decay,
+                       const int32_t* slot, int64_t slots, const float* state, float* new_state,
+                       const dmuon_heads* out, cudaStream_t stream) {
+  if (!linattn_shape_ok(shape) || log_decay == nullptr || slots < 0) return DMUON_ERR_INVALID_ARG;
+  const dmuon_linattn_shape& s = *shape;
+  if (s.tokens == 0) return DMUON_OK;
+  if (state == nullptr || new_state == nullptr || (slot == nullptr && slots < s.tokens))
+    return DMUON_ERR_INVALID_ARG;
+  if (!aligned(state, 16) || !aligned(new_state, 16) || !aligned(log_decay, 4) || !aligned(slot, 4))
+    return DMUON_ERR_ALIGNMENT;
+  LinStepArgs g{};
+  Rows qr, kr, vr, orow;
+  if (!rows_of(q, s.tokens, s.heads, s.key_dim, &qr) ||
+      !rows_of(k, s.tokens, s.heads, s.key_dim, &kr) ||
+      !rows_of(v, s.tokens, s.heads, s.value_dim, &vr) ||
+      !rows_of(out, s.tokens, s.heads, s.value_dim, &orow))
+    return DMUON_ERR_INVALID_ARG;
+  for (const Rows* r : {&qr, &kr, &vr, &orow})
+    if (r->p % 2 != 0) return DMUON_ERR_ALIGNMENT;
+  if (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)) return DMUON_ERR_INVALID_ARG;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(state), b = reinterpret_cast<uintptr_t>(new_state),
+                  bytes = uintptr_t(slots) * uintptr_t(s.heads * s.key_dim * s.value_dim) * 4;
+  if (a != b && a < b + bytes && b < a + bytes) return DMUON_ERR_INVALID_ARG;
+  if (s.tokens * s.heads * ceil_div(s.value_dim, 32) > INT32_MAX) return DMUON_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int e = device_ready(&sms);
+  if (e != DMUON_OK) return e;
+  g.q = device_heads(qr);
+  g.k = device_heads(kr);
+  g.v = device_heads(vr);
+  g.out = device_heads(orow);
+  g.log_decay = log_decay;
+  g.slot = slot;
+  g.slots = slots;
+  g.state = state;
+  g.new_state = new_state;
+  g.rows = int(s.tokens);
+  g.heads = int(s.heads);
+  g.dk = int(s.key_dim);
+  g.dv = int(s.value_dim);
+  g.scale = s.scale;
+  return launch_linattn_step(g, stream) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
+}
+
+}  // extern "C"

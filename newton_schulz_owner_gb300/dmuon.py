@@ -35,7 +35,10 @@ EXPORTED = ("dmuon_plan", "dmuon_workspace_bytes", "dmuon_ns_variant_for", "dmuo
             "dmuon_adamw",
             "dmuon_adamw_workspace_bytes", "dmuon_act8_save", "dmuon_act8_load",
             "dmuon_ffn_workspace_bytes", "dmuon_ffn_forward", "dmuon_ffn_backward",
-            "dmuon_xent_workspace_bytes", "dmuon_xent", "dmuon_status_string", "dmuon_version",
+            "dmuon_xent_workspace_bytes", "dmuon_xent", "dmuon_qk_norm_rope",
+            "dmuon_qk_norm_rope_workspace_bytes", "dmuon_qk_norm_rope_backward",
+            "dmuon_linattn_workspace_bytes", "dmuon_linattn_forward", "dmuon_linattn_backward",
+            "dmuon_linattn_step", "dmuon_status_string", "dmuon_version",
             "dmuon_launch_count", "dmuon_trace_begin", "dmuon_trace_end")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 # largest short side m and long side n of a matrix the library accepts
@@ -53,6 +56,17 @@ class FfnShape(ctypes.Structure):
 
 class XentShape(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("vocab", ctypes.c_int64)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("rotary_dim", ctypes.c_int64),
+                ("interleaved", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class LinattnShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("sequences", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("key_dim", ctypes.c_int64), ("value_dim", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
 _vp, _i, _f, _sz, _i64p = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, \
@@ -105,6 +119,21 @@ _lib.dmuon_xent_workspace_bytes.restype = _sz
 _lib.dmuon_xent.argtypes = [_XentP, _vp, _int64, _vp, _vp, _vp, _vp, _vp, _vp, _int64, _vp, _vp, _sz,
                             _vp]
 _lib.dmuon_xent.restype = _i
+# a dmuon_heads is three 64-bit words; a call's tensors are passed from one array of them
+_lib.dmuon_qk_norm_rope.argtypes = [_vp] * 9 + [_vp]
+_lib.dmuon_qk_norm_rope.restype = _i
+_lib.dmuon_qk_norm_rope_workspace_bytes.argtypes = [_vp]
+_lib.dmuon_qk_norm_rope_workspace_bytes.restype = _sz
+_lib.dmuon_qk_norm_rope_backward.argtypes = [_vp] * 14 + [_sz, _vp]
+_lib.dmuon_qk_norm_rope_backward.restype = _i
+_lib.dmuon_linattn_workspace_bytes.argtypes = [_vp, _i]
+_lib.dmuon_linattn_workspace_bytes.restype = _sz
+_lib.dmuon_linattn_forward.argtypes = [_vp] * 10 + [_sz, _vp]
+_lib.dmuon_linattn_forward.restype = _i
+_lib.dmuon_linattn_backward.argtypes = [_vp] * 14 + [_sz, _vp]
+_lib.dmuon_linattn_backward.restype = _i
+_lib.dmuon_linattn_step.argtypes = [_vp] * 6 + [_int64] + [_vp] * 4
+_lib.dmuon_linattn_step.restype = _i
 _lib.dmuon_stream_status.argtypes = [_vp, _vp]
 _lib.dmuon_stream_status.restype = _i
 _lib.dmuon_debug_wait_timeout.argtypes = [_vp, _sz, _i, _vp]
@@ -617,6 +646,214 @@ class LinearXent:
             if t is None:
                 raise TypeError(f"{name}: expected a tensor, got None")
         self._run(hidden, weight, target, grad_loss, loss, lse, dhidden, dweight, stream)
+
+    def status(self, stream=None) -> int:
+        return stream_status(self.workspace, stream)
+
+
+# ------------------------------------------------------------------ token mixing
+_HEADS = {n: ctypes.c_int64 * (3 * n) for n in (4, 6, 7)}      # n dmuon_heads
+
+
+def _heads(t: torch.Tensor, shape, what: str, dev: int):
+    """Check a (tokens, heads, dim) bf16 tensor on device `dev`; the words of its dmuon_heads."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected bfloat16")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise _elsewhere(t, dev, what)
+    token, head, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{what}: the elements of a head must be contiguous")
+    return t.data_ptr(), token, head
+
+
+class QKNormRope:
+    """Root-mean-square norm of every query and key head with a gain per element, then the
+    rotation of its first `rotary_dim` elements by position, and their backward pass.
+
+    Queries are (tokens, q_heads, head_dim), keys (tokens, k_heads, head_dim), bf16, any strides
+    between tokens and heads (slices of one packed projection, say); outputs may be the inputs.
+    Gains are bf16 (head_dim,) or None for ones, `inv_freq` fp32 (rotary_dim / 2,), positions
+    int32 (tokens,).  `k_heads` = 0 takes queries alone (pass None for keys).
+    """
+
+    def __init__(self, max_tokens: int, q_heads: int, k_heads: int, head_dim: int,
+                 rotary_dim: Optional[int] = None, eps: float = 1e-6, interleaved: bool = False,
+                 backward: bool = True, device="cuda"):
+        self.max_tokens, self.q_heads, self.k_heads = int(max_tokens), int(q_heads), int(k_heads)
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        self.eps, self.interleaved, self.with_backward = float(eps), bool(interleaved), bool(backward)
+        shape = self._shape(self.max_tokens)
+        nbytes = int(_lib.dmuon_qk_norm_rope_workspace_bytes(ctypes.byref(shape)))
+        if nbytes == 0:
+            raise DMuonError(ERR_INVALID_ARG, "dmuon_qk_norm_rope_workspace_bytes")
+        self.workspace = torch.empty(nbytes if self.with_backward else 256, dtype=torch.uint8,
+                                     device=device)
+        self.workspace[:256].zero_()
+
+    def _shape(self, tokens: int) -> QkShape:
+        return QkShape(tokens, self.q_heads, self.k_heads, self.head_dim, self.rotary_dim,
+                       self.interleaved, self.eps)
+
+    def _begin(self, q):
+        t = q.shape[0] if q.dim() == 3 else -1
+        if t < 0 or t > self.max_tokens:
+            raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.q_heads}, "
+                             f"{self.head_dim}), got {tuple(q.shape)}")
+        dev = _launch_device(self.workspace, "the workspace")
+        return t, dev, (t, self.q_heads, self.head_dim), (t, self.k_heads, self.head_dim)
+
+    def _key(self, k, shape, what, dev):
+        if self.k_heads == 0:
+            if k is not None:
+                raise ValueError(f"{what}: expected None without key heads")
+            return 0, 0, 0
+        return _heads(k, shape, what, dev)
+
+    def _rest(self, w_q, w_k, inv_freq, position, t, dev):
+        d = self.head_dim
+        wq = None if w_q is None else _dense(w_q, torch.bfloat16, (d,), "w_q", dev)
+        wk = None if w_k is None else _dense(w_k, torch.bfloat16, (d,), "w_k", dev)
+        if self.rotary_dim == 0:
+            return wq, wk, None, None
+        return (wq, wk, _dense(inv_freq, torch.float32, (self.rotary_dim // 2,), "inv_freq", dev),
+                _dense(position, torch.int32, (t,), "position", dev))
+
+    def forward(self, q, k, w_q, w_k, inv_freq, position, q_out, k_out, stream=None) -> None:
+        """q_out, k_out <- the normalised and rotated q and k."""
+        t, dev, qs, ks = self._begin(q)
+        h = _HEADS[4](*_heads(q, qs, "q", dev), *self._key(k, ks, "k", dev),
+                      *_heads(q_out, qs, "q_out", dev), *self._key(k_out, ks, "k_out", dev))
+        at = ctypes.addressof(h)
+        _check(_lib.dmuon_qk_norm_rope(ctypes.byref(self._shape(t)), at, at + 24,
+                                       *self._rest(w_q, w_k, inv_freq, position, t, dev), at + 48,
+                                       at + 72, _launch_stream(stream, dev)), "dmuon_qk_norm_rope")
+
+    def backward(self, dq_out, dk_out, q, k, w_q, w_k, inv_freq, position, dq, dk, dw_q=None,
+                 dw_k=None, stream=None) -> None:
+        """Gradients of q, k (forward's inputs) and the gains from those of the outputs; a gain's
+        gradient may be None (not wanted)."""
+        if not self.with_backward:
+            raise ValueError("this QKNormRope was made without a backward pass")
+        t, dev, qs, ks = self._begin(q)
+        h = _HEADS[6](*_heads(dq_out, qs, "dq_out", dev), *self._key(dk_out, ks, "dk_out", dev),
+                      *_heads(q, qs, "q", dev), *self._key(k, ks, "k", dev),
+                      *_heads(dq, qs, "dq", dev), *self._key(dk, ks, "dk", dev))
+        at, d = ctypes.addressof(h), self.head_dim
+        gq = None if dw_q is None else _dense(dw_q, torch.bfloat16, (d,), "dw_q", dev)
+        gk = None if dw_k is None else _dense(dw_k, torch.bfloat16, (d,), "dw_k", dev)
+        _check(_lib.dmuon_qk_norm_rope_backward(
+            ctypes.byref(self._shape(t)), at, at + 24, at + 48, at + 72,
+            *self._rest(w_q, w_k, inv_freq, position, t, dev), at + 96, at + 120, gq, gk,
+            self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
+            "dmuon_qk_norm_rope_backward")
+
+    def status(self, stream=None) -> int:
+        return stream_status(self.workspace, stream)
+
+
+class LinearAttention:
+    """Causal linear attention with a decay for each head over packed sequences,
+    S_t = exp(log_decay) S_(t-1) + k_t v_t^T, out_t = scale q_t S_t, its backward pass, and the
+    step of single tokens, for up to `max_tokens` tokens and `max_sequences` sequences at a time.
+
+    q and k are (tokens, heads, key_dim), v and out (tokens, heads, value_dim), bf16, any strides
+    between tokens and heads; `log_decay` fp32 (heads,), <= 0; states fp32
+    (sequences, heads, key_dim, value_dim).  `offsets` int32 (sequences + 1,) says where sequences
+    begin and end; None: one sequence.  `scale` is key_dim ** -0.5 unless given.
+    """
+
+    def __init__(self, max_tokens: int, heads: int, key_dim: int, value_dim: Optional[int] = None,
+                 max_sequences: int = 1, scale: Optional[float] = None, backward: bool = True,
+                 device="cuda"):
+        self.max_tokens, self.heads, self.key_dim = int(max_tokens), int(heads), int(key_dim)
+        self.value_dim = self.key_dim if value_dim is None else int(value_dim)
+        self.max_sequences, self.with_backward = int(max_sequences), bool(backward)
+        self.scale = max(1, self.key_dim) ** -0.5 if scale is None else float(scale)
+        shape = self._shape(self.max_tokens, self.max_sequences)
+        nbytes = int(_lib.dmuon_linattn_workspace_bytes(ctypes.byref(shape), int(self.with_backward)))
+        if nbytes == 0:
+            raise DMuonError(ERR_INVALID_ARG, "dmuon_linattn_workspace_bytes")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+
+    def _shape(self, tokens: int, sequences: int) -> LinattnShape:
+        return LinattnShape(tokens, sequences, self.heads, self.key_dim, self.value_dim, self.scale)
+
+    def _begin(self, q, offsets=None):
+        t = q.shape[0] if q.dim() == 3 else -1
+        if t < 0 or t > self.max_tokens:
+            raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.heads}, "
+                             f"{self.key_dim}), got {tuple(q.shape)}")
+        dev = _launch_device(self.workspace, "the workspace")
+        n, off = 1, None
+        if offsets is not None:
+            n = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+            if n < 1 or n > self.max_sequences:
+                raise ValueError(f"offsets: expected (sequences + 1 <= {self.max_sequences + 1},), "
+                                 f"got {tuple(offsets.shape)}")
+            off = _dense(offsets, torch.int32, (n + 1,), "offsets", dev)
+        return t, n, off, dev, (t, self.heads, self.key_dim), (t, self.heads, self.value_dim)
+
+    def _state(self, state, n, what, dev):
+        return None if state is None else _dense(
+            state, torch.float32, (n, self.heads, self.key_dim, self.value_dim), what, dev)
+
+    def forward(self, q, k, v, log_decay, out, offsets=None, state=None, final_state=None,
+                stream=None) -> None:
+        """out <- the mixed values; from `state` (None: zeros) and to `final_state` if given
+        (which may be `state`)."""
+        t, n, off, dev, ks, vs = self._begin(q, offsets)
+        h = _HEADS[4](*_heads(q, ks, "q", dev), *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev),
+                      *_heads(out, vs, "out", dev))
+        at = ctypes.addressof(h)
+        _check(_lib.dmuon_linattn_forward(
+            ctypes.byref(self._shape(t, n)), at, at + 24, at + 48,
+            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), off,
+            self._state(state, n, "state", dev), self._state(final_state, n, "final_state", dev),
+            at + 72, self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
+            "dmuon_linattn_forward")
+
+    def backward(self, dout, q, k, v, log_decay, dq, dk, dv, offsets=None, state=None,
+                 dfinal_state=None, dstate=None, stream=None) -> None:
+        """Gradients of q, k, v and (if `dstate` is given) of `state`, from those of out and
+        (None: zeros) of final_state."""
+        if not self.with_backward:
+            raise ValueError("this LinearAttention was made without a backward pass")
+        t, n, off, dev, ks, vs = self._begin(q, offsets)
+        h = _HEADS[7](*_heads(dout, vs, "dout", dev), *_heads(q, ks, "q", dev),
+                      *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev), *_heads(dq, ks, "dq", dev),
+                      *_heads(dk, ks, "dk", dev), *_heads(dv, vs, "dv", dev))
+        at = ctypes.addressof(h)
+        _check(_lib.dmuon_linattn_backward(
+            ctypes.byref(self._shape(t, n)), at, at + 24, at + 48, at + 72,
+            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), off,
+            self._state(state, n, "state", dev), self._state(dfinal_state, n, "dfinal_state", dev),
+            at + 96, at + 120, at + 144, self._state(dstate, n, "dstate", dev),
+            self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
+            "dmuon_linattn_backward")
+
+    def step(self, q, k, v, log_decay, state, out, new_state=None, slots=None, stream=None) -> None:
+        """One token for each of q.shape[0] streams: row r reads state[slots[r]] (None: state[r])
+        and writes the state after its token to the same place of `new_state` (None: of `state`).
+        A slot outside the states skips its row; rows that share one are taken in their order."""
+        t, _, _, dev, ks, vs = self._begin(q)
+        if state.dim() != 4:
+            raise ValueError(f"state: expected 4 dimensions, got {tuple(state.shape)}")
+        n = state.shape[0]
+        st = self._state(state, n, "state", dev)
+        new = st if new_state is None else self._state(new_state, n, "new_state", dev)
+        sl = None if slots is None else _dense(slots, torch.int32, (t,), "slots", dev)
+        h = _HEADS[4](*_heads(q, ks, "q", dev), *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev),
+                      *_heads(out, vs, "out", dev))
+        at = ctypes.addressof(h)
+        _check(_lib.dmuon_linattn_step(
+            ctypes.byref(self._shape(t, 1)), at, at + 24, at + 48,
+            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), sl, n, st, new,
+            at + 72, _launch_stream(stream, dev)), "dmuon_linattn_step")
 
     def status(self, stream=None) -> int:
         return stream_status(self.workspace, stream)

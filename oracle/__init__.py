@@ -16,3 +16,6 @@ from .muon_oracle import (  # noqa: F401
 from .training_oracle import (  # noqa: F401
     ACT8_BLOCK, act8_codes, act8_values, act, ffn_forward, ffn_backward, xent,
 )
+from .mixing_oracle import (  # noqa: F401
+    norm_rope, norm_rope_backward, linattn, linattn_backward,
+)

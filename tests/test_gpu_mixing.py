@@ -1,0 +1,663 @@
+"""GPU parity of the operators that mix tokens (norms and rotation of query and key heads, linear
+attention with a decay for each head, their gradients, the step of single tokens) against their
+fp64 forms, at the sizes, strides, sequences and decays where they can go wrong.
+
+Tolerances.  u = 2^-8 is bf16's half step relative to the value.
+Norm and rotation: computed in fp32 and rounded once.  rsqrt, sine and cosine are within 2^-21,
+a handful of fp32 operations adds 2^-22 each: |error| <= u |value| + 2^-19 (|a| + |b|), a and b
+the pair before the turn.  The gains' gradients add at most 2^14 terms one after another in any
+lane: u |value| + 2^-10 sum |terms| at worst, 2^-14 of it for the sizes here (fewer than 1024 one
+after another).
+Linear attention: the weighted scores, the entering state and the decayed keys are rounded to bf16
+once, the output once.  Element by element
+  |error| <= u |value| + 2.1 u mass,   mass = scale sum_s a^(t-s) (|q_t| . |k_s|) |v_s| + |q| |S|
+(the state's share has two roundings, the scores' one; 0.1: second order and accumulation); of
+independent roundings the relative Frobenius error is about sqrt(4) u 0.43, at most 2 u.
+States: keys keep 16 bits, half a step of each of two roundings, 2^-16 of every term; products of a
+block are truncated to 2^-20 of their sum, blocks add in fp32: 1.25 * 2^-16 mass.
+Single tokens: fp32 throughout, d products one after another: state 2^-22, output u |value| +
+2^-17 mass."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def dm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import os
+    from newton_schulz_owner_gb300 import build_lib
+    if not os.path.exists(build_lib.LIB):
+        build_lib.build()
+    from newton_schulz_owner_gb300 import dmuon
+    return dmuon
+
+
+def np64(t):
+    return None if t is None else t.detach().to(torch.float64).cpu().numpy()
+
+
+class Draw:
+    def __init__(self, seed):
+        self.g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def __call__(self, shape, std=1.0, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=self.g, device="cuda").mul_(std).to(dtype)
+
+
+SENTINEL = 7.0
+
+
+class Place:
+    """A (tokens, heads, dim) tensor inside a buffer of sentinels.  "rows": token after token,
+    packed beside `others` more dims; "heads": head after head; "mixed": the heads' slices of
+    several tensors interleaved.  `off` elements in."""
+
+    def __init__(self, tokens, heads, dim, layout="rows", off=0, pad=0, fill=None):
+        if layout == "rows":
+            ts, hs = heads * dim + pad, dim
+        elif layout == "heads":
+            ts, hs = dim + pad, tokens * (dim + pad) + pad
+        else:
+            ts, hs = heads * (3 * dim + pad) + pad, 3 * dim + pad
+        size = off + (max(tokens, 1) - 1) * ts + (heads - 1) * hs + dim + 8
+        self.buf = torch.full((size,), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        self.at = ((tokens, heads, dim), (ts, hs, 1), off)
+        self.t = self.buf.as_strided(*self.at)
+        if fill is not None:
+            self.t.copy_(fill)
+
+    def intact(self):
+        seen = self.buf.clone()
+        seen.as_strided(*self.at).fill_(SENTINEL)
+        return bool((seen == SENTINEL).all())
+
+
+LAYOUTS = [("rows", 0, 0), ("rows", 8, 64), ("heads", 16, 8), ("mixed", 8, 0)]
+
+
+def no_worse(got, ref, bound, what):
+    got = np64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == ref.shape, what
+    assert np.all(np.isfinite(got)), what
+    over = np.abs(got - ref) - bound
+    assert np.all(over <= 0), (what, float(over.max()), np.unravel_index(over.argmax(), over.shape))
+
+
+# ------------------------------------------------------------------ norms and rotation
+def rope_reference(dim, rotary, base=10000.0):
+    i = torch.arange(rotary // 2, device="cuda", dtype=torch.float64)
+    return (base ** (-2 * i / max(1, rotary))).float()
+
+
+def rope_bound(x, w, eps, y):
+    """u |y| + 2^-19 of the pair's magnitudes (at most sqrt(2) the largest of a head)."""
+    n = np.abs(x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps) * w)
+    return U * np.abs(y) + 2.0 ** -18 * n.max(axis=-1, keepdims=True)
+
+
+ROPE = [(1, 32, 8, 128, 128), (3, 1, 1, 8, 8), (5, 3, 2, 64, 32), (70, 12, 2, 128, 64),
+        (33, 5, 5, 96, 96), (9, 7, 3, 256, 256), (300, 28, 4, 80, 0), (2, 4, 0, 128, 128),
+        (2100, 3, 1, 40, 24), (17, 40, 40, 16, 8)]
+
+
+@pytest.mark.parametrize("tokens,hq,hk,dim,rotary", ROPE)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("layout,off,pad", LAYOUTS + [("rows", 3, 5), ("heads", 4, 4)])
+def test_norm_rope_both_ways(dm, tokens, hq, hk, dim, rotary, interleaved, layout, off, pad):
+    """Forward and gradients, aligned or not, gains or none."""
+    d, eps = Draw(tokens + dim), 1e-5
+    f = rope_reference(dim, rotary)
+    pos = torch.randint(-50, 200000, (tokens,), generator=d.g, device="cuda", dtype=torch.int32)
+    op = dm.QKNormRope(tokens + 2, hq, hk, dim, rotary, eps=eps, interleaved=interleaved)
+    place = lambda h, std=None: None if h == 0 else Place(
+        tokens, h, dim, layout, off, pad, None if std is None else d((tokens, h, dim), std))
+    tens = lambda p: None if p is None else p.t
+    x = [place(hq, 1.7), place(hk, 0.01)]
+    w = [d((dim,), 0.5), None if tokens == 5 else d((dim,), 2.0)]
+    out = [place(hq), place(hk)]
+    op.forward(*map(tens, x), *w, f, pos, *map(tens, out))
+    g = [place(hq, 1.0), place(hk, 1e-3)]
+    dx = [place(hq), place(hk)]
+    dw = [torch.full((dim,), SENTINEL, dtype=torch.bfloat16, device="cuda") for _ in w]
+    if w[1] is None or hk == 0:
+        dw[1] = None
+    op.backward(*map(tens, g), *map(tens, x), *w, f, pos, *map(tens, dx), *dw)
+    for i in range(2):
+        if x[i] is None:
+            continue
+        xn, wn = np64(x[i].t), np64(w[i]) if w[i] is not None else np.ones(dim)
+        y = oracle.norm_rope(xn, wn, np64(f), np64(pos), eps, interleaved)
+        no_worse(out[i].t, y, rope_bound(xn, wn, eps, y), f"out {i}")
+        gn = np64(g[i].t)
+        want, want_w = oracle.norm_rope_backward(gn, xn, wn, np64(f), np64(pos), eps, interleaved)
+        r = 1 / np.sqrt(np.mean(xn * xn, axis=-1, keepdims=True) + eps)
+        n, top = np.abs(xn * r), np.abs(gn).max(axis=-1, keepdims=True) * np.sqrt(2)
+        most = np.abs(wn).max()
+        no_worse(dx[i].t, want, U * np.abs(want) + 2.0 ** -18 * r * top * most * (
+            1 + n * n.max(axis=-1, keepdims=True)), f"dx {i}")
+        if dw[i] is not None:
+            terms = np.sum(top * n, axis=(0, 1))
+            no_worse(dw[i], want_w, U * np.abs(want_w) + 2.0 ** -14 * terms, f"dw {i}")
+        assert all(p.intact() for p in (x[i], out[i], g[i], dx[i]))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_far_positions(dm, interleaved):
+    """The angle loses nothing up to the ends of int32, with frequencies above one turn too."""
+    pos = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 1 << 24, -1, 0], dtype=torch.int32,
+                       device="cuda")
+    f = torch.tensor([1.0, 0.3337, 6.5, 100.25, 1e-7, 2.0 ** -20, 0.0, 0.77], device="cuda")
+    op = dm.QKNormRope(6, 3, 1, 16, interleaved=interleaved, eps=0.0)
+    q, k = Draw(1)((6, 3, 16)), Draw(2)((6, 1, 16))
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    op.forward(q, k, None, None, f, pos, qo, ko)
+    one = np.ones(16)
+    for x, y in ((q, qo), (k, ko)):
+        want = oracle.norm_rope(np64(x), one, np64(f), np64(pos), 0.0, interleaved)
+        # position * frequency is exact in the reference to 2^-53 * 2^31 * 100 = 2^-15
+        slack = 2.0 ** -15 * np.abs(np64(x)).max()
+        no_worse(y, want, rope_bound(np64(x), one, 0.0, want) + slack * 4, "far")
+
+
+def test_norm_rope_in_place_and_packed(dm):
+    """q and k as slices of one projection, normalised where they lie; v is not touched."""
+    t, hq, hk, d = 77, 8, 2, 64
+    qkv = Draw(3)((t, (hq + 2 * hk) * d))
+    keep = qkv.clone()
+    q, k = qkv[:, :hq * d].view(t, hq, d), qkv[:, hq * d:(hq + hk) * d].view(t, hk, d)
+    w, f = Draw(4)((d,)), rope_reference(d, d)
+    pos = torch.arange(t, device="cuda", dtype=torch.int32)
+    op = dm.QKNormRope(t, hq, hk, d)
+    want = [torch.empty((t, h, d), dtype=torch.bfloat16, device="cuda") for h in (hq, hk)]
+    op.forward(q, k, w, w, f, pos, *want)
+    op.forward(q, k, w, w, f, pos, q, k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(qkv[:, (hq + hk) * d:], keep[:, (hq + hk) * d:])
+    # gradients over the outputs' gradients
+    g = [Draw(5)(x.shape) for x in want]
+    x = [keep[:, :hq * d].view(t, hq, d), keep[:, hq * d:(hq + hk) * d].view(t, hk, d)]
+    dx, dw = [torch.empty_like(v) for v in want], [torch.empty_like(w) for _ in want]
+    op.backward(*g, *x, w, w, f, pos, *dx, *dw)
+    dw2 = [torch.empty_like(w) for _ in want]
+    op.backward(*g, *x, w, w, f, pos, *g, *dw2)
+    assert all(torch.equal(a, b) for a, b in zip(g + dw2, dx + dw))
+
+
+def test_norm_rope_bad_values_stay_in_their_head(dm):
+    q, k = Draw(6)((4, 3, 64)), Draw(7)((4, 2, 64))
+    f, pos = rope_reference(64, 64), torch.arange(4, device="cuda", dtype=torch.int32)
+    op = dm.QKNormRope(4, 3, 2, 64)
+    run = lambda: [x for x in (torch.empty_like(q), torch.empty_like(k))]
+    a, b = run(), run()
+    op.forward(q, k, None, None, f, pos, *a)
+    q[1, 2, 5] = float("nan")
+    k[3, 0, 63] = float("inf")
+    op.forward(q, k, None, None, f, pos, *b)
+    assert bool(b[0][1, 2].isnan().all()) and bool(b[1][3, 0, 63].isnan())
+    a[0][1, 2] = 0
+    b[0][1, 2] = 0
+    a[1][3, 0] = 0
+    b[1][3, 0] = 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_norm_rope_zero_tokens_and_zero_rows(dm):
+    op = dm.QKNormRope(8, 2, 2, 64)
+    f = rope_reference(64, 64)
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    op.forward(e, e, None, None, f, none, e, e)
+    dw = [torch.full((64,), SENTINEL, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    op.backward(e, e, e, e, None, None, f, none, e, e, *dw)
+    assert not dw[0].any() and not dw[1].any()
+    z = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(3, device="cuda", dtype=torch.int32)
+    y = [torch.empty_like(z), torch.empty_like(z)]
+    op.forward(z, z, None, None, f, pos, *y)
+    assert not y[0].any() and not y[1].any()
+
+
+# ------------------------------------------------------------------ linear attention
+def mix_case(seed, tokens, heads, dk, dv, sequences, states, layout=("rows", 0, 0)):
+    d = Draw(seed)
+    lay, off, pad = layout
+    c = {}
+    for n, w in (("q", dk), ("k", dk), ("v", dv), ("dout", dv)):
+        c[n] = Place(tokens, heads, w, lay, off, pad, d((tokens, heads, w)))
+    for n, w in (("out", dv), ("dq", dk), ("dk", dk), ("dv", dv)):
+        c["to_" + n] = Place(tokens, heads, w, lay, off, pad)
+    g = -torch.exp2(-8 * torch.rand(heads, generator=d.g, device="cuda"))
+    if heads > 2:
+        g[1] = 0.0
+        g[2] = -float("inf")
+    if heads > 3:
+        g[3] = -20.0
+    c["g"] = g
+    n = len(sequences) - 1 if sequences is not None else 1
+    c["offsets"] = None if sequences is None else torch.tensor(sequences, dtype=torch.int32,
+                                                                device="cuda")
+    shape = (n, heads, dk, dv)
+    c["state"] = d(shape, 3.0, torch.float32) if states else None
+    c["dfinal"] = d(shape, 1.0, torch.float32) if states else None
+    c["final"], c["dstate"] = (torch.full(shape, SENTINEL, device="cuda") if states else None
+                               for _ in range(2))
+    return c
+
+
+def near_mix(got, ref, mass, what, live=None):
+    got = np64(got)
+    if live is not None:
+        got, ref, mass = got[live], ref[live], mass[live]
+    if ref.size == 0:
+        return
+    no_worse(got, ref, U * np.abs(ref) + 2.1 * U * mass, what)
+    lim = 2 * U if ref.size >= 1000 else 3 * U
+    assert np.linalg.norm(got - ref) <= lim * np.linalg.norm(ref), \
+        (what, np.linalg.norm(got - ref) / np.linalg.norm(ref))
+
+
+def mix_check(dm, c, scale, what):
+    tokens, heads, dk = c["q"].t.shape
+    dv = c["v"].t.shape[2]
+    n = 1 if c["offsets"] is None else len(c["offsets"]) - 1
+    op = dm.LinearAttention(tokens, heads, dk, dv, max_sequences=n, scale=scale)
+    q, k, v, dout = (c[x].t for x in ("q", "k", "v", "dout"))
+    op.forward(q, k, v, c["g"], c["to_out"].t, offsets=c["offsets"], state=c["state"],
+               final_state=c["final"])
+    op.backward(dout, q, k, v, c["g"], c["to_dq"].t, c["to_dk"].t, c["to_dv"].t,
+                offsets=c["offsets"], state=c["state"], dfinal_state=c["dfinal"],
+                dstate=c["dstate"])
+    assert op.status() == dm.OK
+    off = None if c["offsets"] is None else c["offsets"].tolist()
+    live = np.zeros(tokens, bool)
+    for b, e in ([(0, tokens)] if off is None else zip(off, off[1:])):
+        live[b:e] = True
+    a = [np64(x) for x in (q, k, v, dout)]
+    g, st, df = np64(c["g"]), np64(c["state"]), np64(c["dfinal"])
+    mag = [np.abs(x) for x in a]
+    ab = lambda x: None if x is None else np.abs(x)
+    ref = oracle.linattn(a[0], a[1], a[2], g, scale, off, st)
+    mass = oracle.linattn(mag[0], mag[1], mag[2], g, abs(scale), off, ab(st))
+    near_mix(c["to_out"].t, ref["out"], mass["out"], what + " out", live)
+    back = oracle.linattn_backward(a[3], a[0], a[1], a[2], g, scale, off, st, df)
+    bmass = oracle.linattn_backward(mag[3], mag[0], mag[1], mag[2], g, abs(scale), off, ab(st), ab(df))
+    for x in ("dq", "dk", "dv"):
+        near_mix(c["to_" + x].t, back[x], bmass[x], what + " " + x, live)
+    if st is not None:
+        tiny = 2.0 ** -100
+        no_worse(c["final"], ref["state"], 1.25 * 2.0 ** -16 * mass["state"] + tiny, what + " final")
+        no_worse(c["dstate"], back["dstate"], 1.25 * 2.0 ** -16 * bmass["dstate"] + tiny,
+                 what + " dstate")
+    for x in ("to_out", "to_dq", "to_dk", "to_dv"):
+        assert c[x].intact(), (what, x)
+        if not live.all():
+            assert bool((c[x].t[torch.from_numpy(~live).cuda()] == SENTINEL).all()), (what, x)
+    return op
+
+
+DIMS = [(128, 128), (64, 64), (64, 128), (128, 64), (8, 8), (40, 96), (120, 24), (72, 128)]
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("tokens", [1, 2, 127, 128, 129, 300])
+def test_linattn_one_sequence(dm, dk, dv, tokens):
+    c = mix_case(tokens + dk, tokens, 5, dk, dv, None, tokens != 2)
+    mix_check(dm, c, dk ** -0.5, f"{dk} {dv} {tokens}")
+
+
+RAGGED = [[0, 0, 1, 129, 129, 385, 400], [5, 6, 7, 135, 300], [0, 128, 256, 384], [3, 3], [17, 400, 400]]
+
+
+@pytest.mark.parametrize("offsets", RAGGED)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (64, 128), (24, 112)])
+@pytest.mark.parametrize("states", [False, True])
+def test_linattn_packed_sequences(dm, offsets, dk, dv, states):
+    """Empty sequences, single tokens, ends inside a block; rows of no sequence hold NaN, and
+    stay as they were in the outputs."""
+    c = mix_case(7, 400, 4, dk, dv, offsets, states)
+    dead = torch.ones(400, dtype=torch.bool, device="cuda")
+    dead[offsets[0]:offsets[-1]] = False
+    for x in ("q", "k", "v", "dout"):
+        c[x].t[dead] = float("nan")
+    for x in ("q", "k", "v", "dout"):      # the reference never looks at them
+        c[x].t[dead] = float("nan")
+    clean = {x: c[x].t.clone() for x in ("q", "k", "v", "dout")}
+    mix_check(dm, c, -0.4, f"{offsets}")
+    assert all(torch.equal(torch.nan_to_num(clean[x]), torch.nan_to_num(c[x].t)) for x in clean)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS[1:])
+def test_linattn_strides(dm, layout):
+    mix_check(dm, mix_case(8, 333, 3, 64, 128, [0, 100, 333], True, layout), 0.2, str(layout))
+
+
+@pytest.mark.parametrize("tokens,heads", [(1500, 1), (1024, 3), (2600, 4)])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+def test_linattn_long_sequences_of_few_heads(dm, tokens, heads, dk, dv):
+    """Sequences that several CTAs share."""
+    mix_check(dm, mix_case(9, tokens, heads, dk, dv, None, True), 0.1, f"{tokens} {heads}")
+
+
+def test_linattn_many_sequences(dm):
+    rng = np.random.default_rng(3)
+    ends = np.concatenate([[0], np.cumsum(rng.integers(0, 9, 200))]).tolist()
+    mix_check(dm, mix_case(10, ends[-1], 3, 64, 64, ends, True), 1.0, "many")
+
+
+def test_linattn_states_in_place(dm):
+    c = mix_case(11, 1300, 2, 128, 128, None, True)
+    op = dm.LinearAttention(1300, 2, 128)
+    args = [c[x].t for x in ("q", "k", "v")] + [c["g"]]
+    op.forward(*args, c["to_out"].t, state=c["state"], final_state=c["final"])
+    s, out = c["state"].clone(), torch.empty_like(c["v"].t)
+    op.forward(*args, out, state=s, final_state=s)
+    assert torch.equal(s, c["final"]) and torch.equal(out, c["to_out"].t)
+    grads = [c[x].t for x in ("to_dq", "to_dk", "to_dv")]
+    op.backward(c["dout"].t, *args, *grads, state=c["state"], dfinal_state=c["dfinal"],
+                dstate=c["dstate"])
+    d, again = c["dfinal"].clone(), [torch.empty_like(x) for x in grads]
+    op.backward(c["dout"].t, *args, *again, state=c["state"], dfinal_state=d, dstate=d)
+    assert torch.equal(d, c["dstate"]) and all(torch.equal(a, b) for a, b in zip(again, grads))
+
+
+def test_linattn_bad_values_stay_in_their_sequence_and_head(dm):
+    off = [0, 50, 300, 420]
+    a, b = (mix_case(12, 420, 3, 128, 128, off, True) for _ in range(2))
+    for x in (a, b):
+        x["g"].fill_(-0.05)
+    for x, at in (("q", (60, 1, 3)), ("k", (61, 1, 0)), ("v", (200, 1, 127)), ("dout", (250, 1, 9))):
+        b[x].t[at] = float("nan")
+    op = dm.LinearAttention(420, 3, 128, max_sequences=3)
+    for x in (a, b):
+        args = [x[n].t for n in ("q", "k", "v")] + [x["g"]]
+        op.forward(*args, x["to_out"].t, offsets=x["offsets"], state=x["state"], final_state=x["final"])
+        op.backward(x["dout"].t, *args, *(x[n].t for n in ("to_dq", "to_dk", "to_dv")),
+                    offsets=x["offsets"], state=x["state"], dfinal_state=x["dfinal"],
+                    dstate=x["dstate"])
+    for n in ("to_out", "to_dq", "to_dk", "to_dv"):
+        bad = b[n].t.isnan()
+        assert bool(bad[50:300, 1].any()), n
+        bad[50:300, 1] = False
+        assert not bool(bad.any()), n
+        for s in (slice(0, 50), slice(300, 420)):
+            assert torch.equal(a[n].t[s], b[n].t[s]), n
+        assert torch.equal(a[n].t[:, 0], b[n].t[:, 0]) and torch.equal(a[n].t[:, 2], b[n].t[:, 2]), n
+    # causal: the first of them is at token 60, in its own row only
+    assert torch.equal(a["to_out"].t[50:60], b["to_out"].t[50:60])
+    for n in ("final", "dstate"):
+        assert torch.equal(a[n][0], b[n][0]) and torch.equal(a[n][2], b[n][2])
+        assert bool(b[n][1, 1].isnan().any()) and torch.equal(a[n][1, 0], b[n][1, 0])
+
+
+def test_linattn_offsets_out_of_range_are_cut(dm):
+    c = mix_case(13, 200, 2, 64, 64, [-5, 90, 500], False)
+    want = mix_case(13, 200, 2, 64, 64, [0, 90, 200], False)
+    op = dm.LinearAttention(200, 2, 64, max_sequences=2)
+    for x in (c, want):
+        op.forward(x["q"].t, x["k"].t, x["v"].t, x["g"], x["to_out"].t, offsets=x["offsets"])
+    assert torch.equal(c["to_out"].t, want["to_out"].t)
+    down = torch.tensor([150, 20, 60], dtype=torch.int32, device="cuda")   # the first is empty
+    op.forward(c["q"].t, c["k"].t, c["v"].t, c["g"], c["to_out"].t, offsets=down)
+    torch.cuda.synchronize()
+    assert op.status() == dm.OK
+
+
+def test_linattn_no_tokens(dm):
+    op = dm.LinearAttention(10, 2, 64, 32, max_sequences=2)
+    e, ev = (torch.empty((0, 2, w), dtype=torch.bfloat16, device="cuda") for w in (64, 32))
+    st = Draw(14)((2, 2, 64, 32), 1.0, torch.float32)
+    out, g = torch.empty_like(st), torch.zeros(2, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    op.forward(e, e, ev, g, ev, offsets=off)
+    op.forward(e, e, ev, g, ev, offsets=off, state=st, final_state=out)
+    assert torch.equal(out, st)
+    op.forward(e, e, ev, g, ev, offsets=off, final_state=out)
+    assert not out.any()
+    op.backward(ev, e, e, ev, g, e, e, ev, offsets=off, dfinal_state=st, dstate=out)
+    assert torch.allclose(out, st, rtol=2 ** -22, atol=0)
+
+
+# ------------------------------------------------------------------ single tokens
+@pytest.mark.parametrize("rows,heads,dk,dv", [(1, 32, 128, 128), (3, 5, 64, 64), (17, 2, 8, 8),
+                                              (5, 3, 40, 96), (130, 1, 120, 24), (2, 4, 72, 128)])
+@pytest.mark.parametrize("layout", [("rows", 0, 0), ("heads", 1, 3)])
+def test_step_matches_the_recurrence(dm, rows, heads, dk, dv, layout):
+    c = mix_case(rows + dk, rows, heads, dk, dv, None, False, layout)
+    st = Draw(15)((rows + 1, heads, dk, dv), 2.0, torch.float32)
+    op = dm.LinearAttention(rows, heads, dk, dv, scale=0.3)
+    q, k, v = (c[x].t for x in ("q", "k", "v"))
+    new = torch.full_like(st, SENTINEL)
+    op.step(q, k, v, c["g"], st, c["to_out"].t, new_state=new)
+    each = list(range(rows + 1))
+    ref = oracle.linattn(np64(q), np64(k), np64(v), np64(c["g"]), 0.3, each, np64(st)[:rows])
+    mass = oracle.linattn(*(np.abs(np64(x)) for x in (q, k, v)), np64(c["g"]), 0.3, each,
+                          np.abs(np64(st))[:rows])
+    no_worse(new[:rows], ref["state"], 2.0 ** -22 * mass["state"] + 2.0 ** -100, "state")
+    no_worse(c["to_out"].t, ref["out"], U * np.abs(ref["out"]) + 2.0 ** -17 * mass["out"], "out")
+    assert bool((new[rows] == SENTINEL).all()) and c["to_out"].intact()
+    keep, out = st.clone(), torch.empty_like(v)
+    op.step(q, k, v, c["g"], st, out)                                   # in place
+    assert torch.equal(st[:rows], new[:rows]) and torch.equal(out, c["to_out"].t)
+    assert torch.equal(st[rows], keep[rows])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_step_slots(dm, in_place):
+    """Rows name their slots; padding rows are skipped, shared slots taken in order."""
+    rows, heads, dk, dv, slots = 300, 3, 64, 40, 9
+    c = mix_case(16, rows, heads, dk, dv, None, False)
+    st = Draw(17)((slots, heads, dk, dv), 1.0, torch.float32)
+    rng = np.random.default_rng(18)
+    names = rng.integers(-2, slots + 2, rows)
+    names[names == 4] = 3
+    op = dm.LinearAttention(rows, heads, dk, dv)
+    q, k, v = (c[x].t for x in ("q", "k", "v"))
+    new = st.clone() if in_place else torch.full_like(st, SENTINEL)
+    op.step(q, k, v, c["g"], new if in_place else st, c["to_out"].t,
+            new_state=None if in_place else new,
+            slots=torch.tensor(names, dtype=torch.int32, device="cuda"))
+    out = c["to_out"].t
+    for s in range(slots):
+        at = np.nonzero(names == s)[0]
+        if len(at) == 0:
+            assert s == 4 and torch.equal(new[s], st[s] if in_place else torch.full_like(st[s], SENTINEL))
+            continue
+        want_new, w = st[s:s + 1].clone(), []
+        for r in at:                               # one row after another
+            o = torch.empty_like(v[r:r + 1])
+            op.step(q[r:r + 1], k[r:r + 1], v[r:r + 1], c["g"], want_new, o)
+            w.append(o)
+        assert torch.equal(new[s], want_new[0])
+        assert torch.equal(out[torch.from_numpy(at).cuda()], torch.cat(w))
+    pad = (names < 0) | (names >= slots)
+    assert bool((out[torch.from_numpy(pad).cuda()] == SENTINEL).all())
+
+
+def test_prompt_then_steps_equal_the_whole(dm):
+    """A state from forward carries on token by token."""
+    heads, d, n, more = 4, 128, 260, 5
+    c = mix_case(19, n + more, heads, d, d, None, False)
+    c["g"].fill_(-0.02)
+    op = dm.LinearAttention(n + more, heads, d)
+    q, k, v = (c[x].t for x in ("q", "k", "v"))
+    st = torch.empty((1, heads, d, d), device="cuda")
+    op.forward(q[:n], k[:n], v[:n], c["g"], c["to_out"].t[:n], final_state=st)
+    for t in range(n, n + more):
+        op.step(q[t:t + 1], k[t:t + 1], v[t:t + 1], c["g"], st, c["to_out"].t[t:t + 1])
+    ref = oracle.linattn(np64(q), np64(k), np64(v), np64(c["g"]), d ** -0.5)
+    mass = oracle.linattn(*(np.abs(np64(x)) for x in (q, k, v)), np64(c["g"]), d ** -0.5)
+    near_mix(c["to_out"].t, ref["out"], mass["out"], "prompt and steps")
+    no_worse(st, ref["state"], 1.5 * 2.0 ** -16 * mass["state"], "state")
+
+
+# ------------------------------------------------------------------ repeats, streams, graphs
+def test_results_repeat_bit_for_bit(dm):
+    c = mix_case(20, 3000, 6, 128, 128, [0, 900, 1000, 3000], True)
+    op = dm.LinearAttention(3000, 6, 128, max_sequences=3)
+    rope = dm.QKNormRope(3000, 6, 6, 128)
+    f, pos = rope_reference(128, 128), torch.arange(3000, device="cuda", dtype=torch.int32)
+    w = Draw(21)((128,))
+    seen = []
+    for _ in range(3):
+        args = [c[x].t for x in ("q", "k", "v")] + [c["g"]]
+        out, fin, dst = torch.empty_like(c["v"].t), torch.empty_like(c["state"]), \
+            torch.empty_like(c["state"])
+        gr = [torch.empty_like(c["q"].t) for _ in range(3)]
+        op.forward(*args, out, offsets=c["offsets"], state=c["state"], final_state=fin)
+        op.backward(c["dout"].t, *args, *gr, offsets=c["offsets"], state=c["state"],
+                    dfinal_state=c["dfinal"], dstate=dst)
+        dx, dw = [torch.empty_like(gr[0]) for _ in range(2)], [torch.empty_like(w) for _ in range(2)]
+        rope.backward(gr[0], gr[1], c["q"].t, c["k"].t, w, w, f, pos, *dx, *dw)
+        seen.append([out, fin, dst] + gr + dx + dw)
+    for other in seen[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(seen[0], other))
+
+
+def mixer(dm, t, hidden, heads, d):
+    """A layer as a model runs it: one projection, norms and rotation where q and k lie, mixing,
+    the feed-forward block, the head's loss, and everything's gradients."""
+    r = Draw(22)
+    f = 192
+    s = {"x": r((t, hidden)), "w_qkv": r((3 * heads * d, hidden), hidden ** -0.5),
+         "w_o": r((hidden, heads * d), (heads * d) ** -0.5), "w_q": 1 + r((d,), 0.1),
+         "w_k": 1 + r((d,), 0.1), "ffn": [r((f, hidden), hidden ** -0.5), r((f, hidden), hidden ** -0.5),
+                                          r((hidden, f), f ** -0.5)], "head": r((500, hidden), 0.1)}
+    s["g"] = -torch.exp2(-torch.arange(1, heads + 1, device="cuda").float())
+    s["off"] = torch.tensor([0, t // 3, t // 3, t - 4], dtype=torch.int32, device="cuda")
+    s["pos"] = torch.arange(t, device="cuda", dtype=torch.int32)
+    s["f"] = rope_reference(d, d)
+    s["target"] = torch.randint(500, (t,), generator=r.g, device="cuda")
+    s["target"][t - 4:] = -100                                 # the padding is not learnt from
+    s["rope"] = dm.QKNormRope(t, heads, heads, d)
+    s["mix"] = dm.LinearAttention(t, heads, d, max_sequences=3)
+    s["block"] = dm.GatedFFN(t, hidden, f, save=dm.SAVE_BF16)
+    s["loss"] = dm.LinearXent(t, hidden, 500)
+    e = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    s["o"], s["do"] = e(t, heads, d), e(t, heads, d)
+    s["qk"], s["dqkv"], s["dqk"] = e(2, t, heads, d), e(t, 3 * heads * d), e(2, t, heads, d)
+    s["y"], s["dh"], s["dx"] = e(t, hidden), e(t, hidden), e(t, hidden)
+    s["saved"] = s["block"].empty_saved(t)
+    s["dw"] = [torch.empty_like(w) for w in s["ffn"]]
+    s["dhead"], s["dw_q"], s["dw_k"] = e(500, hidden), e(d), e(d)
+    s["l"], s["lse"] = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+    s["gl"] = torch.full((t,), 1.0 / t, device="cuda")
+
+    def run():
+        qkv = s["x"] @ s["w_qkv"].t()
+        q, k, v = (qkv[:, i * heads * d:(i + 1) * heads * d].view(t, heads, d) for i in range(3))
+        s["rope"].forward(q, k, s["w_q"], s["w_k"], s["f"], s["pos"], s["qk"][0], s["qk"][1])
+        s["mix"].forward(s["qk"][0], s["qk"][1], v, s["g"], s["o"], offsets=s["off"])
+        h = s["x"] + s["o"].view(t, -1) @ s["w_o"].t()
+        s["block"].forward(h, *s["ffn"], s["y"], s["saved"])
+        s["loss"].loss_and_grads(h + s["y"], s["head"], s["target"], s["gl"], s["l"], s["lse"],
+                                 s["dh"], s["dhead"])
+        s["block"].backward(s["dh"], h, *s["ffn"], s["saved"], s["dx"], *s["dw"])
+        dhid = s["dh"] + s["dx"]
+        s["do"].copy_((dhid @ s["w_o"]).view(t, heads, d))
+        dv = s["dqkv"][:, 2 * heads * d:].view(t, heads, d)
+        s["mix"].backward(s["do"], s["qk"][0], s["qk"][1], v, s["g"], s["dqk"][0], s["dqk"][1], dv,
+                          offsets=s["off"])
+        dq, dk = (s["dqkv"][:, i * heads * d:(i + 1) * heads * d].view(t, heads, d) for i in (0, 1))
+        s["rope"].backward(s["dqk"][0], s["dqk"][1], q, k, s["w_q"], s["w_k"], s["f"], s["pos"], dq,
+                           dk, s["dw_q"], s["dw_k"])
+        s["dw_qkv"] = s["dqkv"].t() @ s["x"]
+        return [s["l"], s["dw_qkv"], s["dw_q"], s["dw_k"], s["dhead"], *s["dw"], s["dqkv"]]
+    return s, run
+
+
+def test_a_layer_and_its_gradients(dm):
+    """The operators together against the same layer in fp64 through autograd: gradients of the
+    projection, of the gains and of the feed-forward weights.  Each is a chain of about ten bf16
+    roundings (u each, independent): relative Frobenius error at most 10 u."""
+    t, hidden, heads, d = 391, 128, 3, 64
+    s, run = mixer(dm, t, hidden, heads, d)
+    got = [x.clone() for x in run()]
+    leaf = {n: s[n].double().requires_grad_() for n in ("w_qkv", "w_q", "w_k", "head")}
+    ffn = [w.double().requires_grad_() for w in s["ffn"]]
+    x, w_o = s["x"].double(), s["w_o"].double()
+    qkv = x @ leaf["w_qkv"].t()
+    q, k, v = (qkv[:, i * heads * d:(i + 1) * heads * d].view(t, heads, d) for i in range(3))
+    ang = torch.outer(s["pos"].double(), s["f"].double())[:, None]
+
+    def nr(z, w):
+        z = z / torch.sqrt(z.square().mean(-1, keepdim=True) + 1e-6) * w
+        a, b = z[..., :d // 2], z[..., d // 2:]
+        return torch.cat((a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos()), -1)
+
+    q, k = nr(q, leaf["w_q"]), nr(k, leaf["w_k"])
+    i = torch.arange(t, device="cuda")
+    seq = torch.bucketize(i, s["off"][1:].long(), right=True)
+    gap = i[:, None] - i
+    see = (gap >= 0) & (seq[:, None] == seq) & (i < t - 4)[:, None]
+    wgt = torch.where(see, torch.exp(s["g"].double()[:, None, None] * gap.clamp_min(0)), 0.0)
+    p = torch.einsum("ihd,jhd->hij", q, k) * wgt * d ** -0.5
+    o = torch.einsum("hij,jhd->ihd", p, v).reshape(t, -1)
+    h = x + o @ w_o.t()
+    gate, up = h @ ffn[0].t(), h @ ffn[1].t()
+    h = h + (torch.nn.functional.silu(gate) * up) @ ffn[2].t()
+    lsm = torch.log_softmax(h @ leaf["head"].t(), -1)
+    live = torch.arange(t - 4, device="cuda")
+    loss = -(lsm[live, s["target"][live]]).sum() / t
+    want = torch.autograd.grad(loss, [leaf["w_qkv"], leaf["w_q"], leaf["w_k"], leaf["head"], *ffn])
+    for name, a, b in zip(["dw_qkv", "dw_q", "dw_k", "dhead", "gate", "up", "down"], got[1:], want):
+        err = float((a.double() - b).norm() / b.norm())
+        assert err <= 10 * U, (name, err)
+    for op in ("rope", "mix", "block", "loss"):
+        assert s[op].status() == dm.OK
+
+
+def test_a_layer_captured_into_a_graph_replays(dm):
+    s, run = mixer(dm, 300, 64, 2, 32)
+    want = [x.clone() for x in run()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = run()
+    for _ in range(2):
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    # other inputs in the same memory
+    s["x"].mul_(-0.5)
+    fresh = [x.clone() for x in run()]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, fresh))
+
+
+def test_two_streams_with_their_own_handles(dm):
+    cases = [mix_case(23 + i, 1800, 4, 128, 64, [0, 700, 1800], True) for i in range(2)]
+    ops = [dm.LinearAttention(1800, 4, 128, 64, max_sequences=2) for _ in cases]
+
+    def go(c, op, stream=None):
+        args = [c[x].t for x in ("q", "k", "v")] + [c["g"]]
+        op.forward(*args, c["to_out"].t, offsets=c["offsets"], state=c["state"],
+                   final_state=c["final"], stream=stream)
+        op.backward(c["dout"].t, *args, *(c[n].t for n in ("to_dq", "to_dk", "to_dv")),
+                    offsets=c["offsets"], state=c["state"], dfinal_state=c["dfinal"],
+                    dstate=c["dstate"], stream=stream)
+        return [c[n].t for n in ("to_out", "to_dq", "to_dk", "to_dv")] + [c["final"], c["dstate"]]
+
+    want = [[x.clone() for x in go(c, op)] for c, op in zip(cases, ops)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for c, op, st in zip(cases, ops, streams):
+        go(c, op, st.cuda_stream)
+    torch.cuda.synchronize()
+    for c, w, op in zip(cases, want, ops):
+        have = [c[n].t for n in ("to_out", "to_dq", "to_dk", "to_dv")] + [c["final"], c["dstate"]]
+        assert all(torch.equal(a, b) for a, b in zip(have, w)) and op.status() == dm.OK

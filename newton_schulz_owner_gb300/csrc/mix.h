@@ -27,7 +27,7 @@ struct RopeArgs {
   const int32_t* position;
   int tokens, heads[2], dim, rotary;
   float eps;
-  int parts;                  // warps that share a token's heads
+  int per, parts;             // chunks of heads that a warp takes, warps of a token
   float* partial;             // backward: sums of the gains' gradients, one row per block
   __nv_bfloat16* dw[2];       // or null
 };
@@ -52,14 +52,17 @@ struct LinAttnArgs {
   float in_scale, out_scale;  // of the state on its way in and out
   int st_row, st_col;         // element strides of a state (row: the keys' side)
   Heads out;
-  int split;                  // CTAs of a cluster, which share a sequence of a head
-  float* local;               // their states on the way to one another
+  int groups;                 // runs that a head's sequences are cut into, a cluster each
+  int split;                  // CTAs of a cluster
+  int exact;                  // keys are kept to 16 bits in the state
+  float* local;               // states on the way from CTA to CTA
   int* err;
 };
 constexpr int kMixBlock = 128;   // tokens taken at a time
 constexpr int kMixMaxSplit = 8;
-constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a CTA
-constexpr int64_t kMixMaxLocals = 640;  // CTAs of a launch whose sequences are shared
+constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a state
+constexpr int kMixSlots = 3;            // states of a CTA in the workspace
+constexpr int64_t kMixMaxCtas = 320;    // of a launch whose sequences are shared
 cudaError_t linattn_prepare();  // once per device
 cudaError_t launch_linattn(const LinAttnArgs& g, cudaStream_t s);
 

@@ -158,6 +158,9 @@ int qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* const x[2],
     }
   }
   if (s.tokens == 0 && !backward) return DMUON_OK;
+  // a warp takes 4 heads at least
+  if (s.tokens * (ceil_div(heads[0], 4) + ceil_div(heads[1], 4)) > INT32_MAX)
+    return DMUON_ERR_UNSUPPORTED;
   int sms = 0;
   const int e = device_ready(&sms);
   if (e != DMUON_OK) return e;
@@ -187,27 +190,36 @@ bool linattn_shape_ok(const dmuon_linattn_shape* s) {
          s->scale != 0.f && s->sequences * s->heads <= (int64_t(1) << 27);
 }
 
-// CTAs that share a sequence of a head.
-int choose_split(const dmuon_linattn_shape& s, int sms) {
-  const int64_t blocks = ceil_div(ceil_div(s.tokens, s.sequences), kMixBlock);
-  const int64_t items = s.sequences * s.heads;
-  int best = 1;
+// How a head's packed batch is shared: `groups` clusters of `split` CTAs.
+struct Share {
+  int groups, split;
+};
+Share choose_share(const dmuon_linattn_shape& s, int sms) {
+  const int64_t blocks = s.tokens / kMixBlock + std::min(s.sequences, s.tokens);  // at most
+  Share best{1, 1};
   double least = 0;
-  for (int c = 1; c <= kMixMaxSplit; c *= 2) {
-    if (c > 1 && (c > blocks || items * c > kMixMaxLocals)) break;
-    const double per = double(ceil_div(blocks, c));
-    const double cost = double(ceil_div(items * c, sms)) * (per * (c > 1 ? 1.5 : 1.0) + 2);
-    if (c == 1 || cost < least) {
-      best = c;
-      least = cost;
+  for (int64_t groups = 1; groups <= s.sequences && groups <= 64; ++groups) {
+    for (int split = 1; split <= kMixMaxSplit; ++split) {
+      const int64_t ctas = s.heads * groups * split;
+      if (groups * split > blocks && groups * split > 1) break;
+      if (split > 1 && ctas > kMixMaxCtas) break;
+      // clusters end where sequences do: the largest has about a sequence more than its part
+      const double part = double(blocks) / groups + (groups > 1 ? double(blocks) / s.sequences : 0.0);
+      const double cost = double(ceil_div(ctas, sms)) *
+                          (std::ceil(part / split) * (split > 1 ? 1.5 : 1.0) + 2);
+      if (least == 0 || cost < least) {
+        best = {int(groups), split};
+        least = cost;
+      }
     }
+    if (s.heads * groups >= sms) break;
   }
   return best;
 }
-// The workspace serves any split of any number of tokens and sequences up to the shape's.
+// The workspace serves any way to share any number of tokens and sequences up to the shape's.
 size_t linattn_workspace(const dmuon_linattn_shape& s) {
-  const int64_t locals = std::min(s.sequences * s.heads * kMixMaxSplit, kMixMaxLocals);
-  return kHdrBytes + size_t(locals) * kMixLocalBytes;
+  const int64_t ctas = std::min(s.sequences * s.heads * kMixMaxSplit, kMixMaxCtas);
+  return kHdrBytes + size_t(ctas) * kMixSlots * kMixLocalBytes;
 }
 
 bool tile_map(CUtensorMap* m, const Rows& r, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
@@ -231,7 +243,7 @@ struct Sweep {
   float in_scale, out_scale;
 };
 int run_sweep(const dmuon_linattn_shape& s, const Sweep& w, const float* log_decay,
-              const int32_t* offsets, int split, void* ws, cudaStream_t st) {
+              const int32_t* offsets, Share share, void* ws, cudaStream_t st) {
   LinAttnArgs g{};
   if (!tile_map(&g.q, *w.q, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tile_map(&g.k, *w.k, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -254,7 +266,9 @@ int run_sweep(const dmuon_linattn_shape& s, const Sweep& w, const float* log_dec
   g.st_row = w.transposed ? 1 : g.dv;
   g.st_col = w.transposed ? g.dk : 1;
   g.out = device_heads(*w.out);
-  g.split = split;
+  g.groups = share.groups;
+  g.split = share.split;
+  g.exact = w.state_out != nullptr;
   g.err = static_cast<int*>(ws);
   g.local = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHdrBytes);
   return launch_linattn(g, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
@@ -348,7 +362,7 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
   e = device_ready(&sms);
   if (e != DMUON_OK) return e;
   const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, 1.f, 1.f};
-  return run_sweep(s, w, log_decay, offsets, choose_split(s, sms), workspace, stream);
+  return run_sweep(s, w, log_decay, offsets, choose_share(s, sms), workspace, stream);
 }
 
 int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* dout,
@@ -382,7 +396,7 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
   int sms = 0;
   e = device_ready(&sms);
   if (e != DMUON_OK) return e;
-  const int split = choose_split(s, sms);
+  const Share share = choose_share(s, sms);
   const float inv = 1.f / s.scale;
   // dk reads dfinal_state before dv's sweep may write dstate over it
   const Sweep sweeps[3] = {
@@ -390,7 +404,7 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
       {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, inv, 1.f},
       {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, inv, s.scale}};
   for (int i = s.tokens > 0 ? 0 : 2; i < 3; ++i) {
-    e = run_sweep(s, sweeps[i], log_decay, offsets, split, workspace, stream);
+    e = run_sweep(s, sweeps[i], log_decay, offsets, share, workspace, stream);
     if (e != DMUON_OK) return e;
   }
   return DMUON_OK;

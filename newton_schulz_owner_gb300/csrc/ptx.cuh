@@ -405,6 +405,17 @@ DM_DEV void umma_commit_pair(uint64_t* bar, uint16_t cta_mask) {
       : "memory");
 }
 
+// Give up registers, or take up those that other warpgroups of the block gave up (waits until they
+// have).  N a multiple of 8, executed by all warps of a warpgroup.
+template <int N>
+DM_DEV void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+DM_DEV void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // True in one lane of a converged warp.  A branch on it tells the compiler that a single
 // thread issues what follows (MMAs, TMA copies), so their operands need no loop over the
 // lanes: four MMAs of 32 columns take about 290 cycles of issuing instead of 580 behind a

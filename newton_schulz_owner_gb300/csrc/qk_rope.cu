@@ -2,16 +2,21 @@
 // position, forward and backward, in one pass over the heads.
 //
 // Bound by HBM: 4 bytes an element forward (read and write bf16), 6 backward.  A head is
-// spread over LANES lanes of a warp, 8 elements each, as two runs of four: in the split form
-// the runs are elements 4l .. 4l + 3 of each half of the rotated part, so that a lane holds
-// both sides of its pairs and nothing but the sums of squares crosses lanes; in the
-// interleaved form, and past the rotated part, they are neighbours.
+// spread over LANES lanes of a warp, 8 elements each, as four pairs: in the split form elements
+// 4l .. 4l + 3 of each half of the rotated part, in the interleaved form (and past the rotated
+// part) eight neighbours.  Both sides of a pair lie in one lane, so that only the sums of squares
+// cross lanes.  A warp loads all heads that it takes of a token before it computes on the first.
+//
+// What limits it besides is issuing: about 130 instructions for 2 x 128 elements of a head a warp
+// leave HBM idle half the time.  Hence pairs go two at a time (fma.rn.f32x2), and the gains are
+// folded into the sines and cosines once per token:
+//   n_a w_a cos - n_b w_b sin = r (x_a (w_a cos) - x_b (w_b sin))
 //
 // Angles.  t = position * inv_freq radians is needed modulo a turn only, and in fp32 a
-// position of 10^5 would leave a third of the digits.  f / 2 pi as a 64-bit fraction of a turn
-// times the position, modulo 2^64, is exact but for the fraction's rounding (2^-53 of it): the
-// top 32 bits are the angle.  A lane forms its four fractions once and keeps them over all its
-// tokens; a token's four sines and cosines serve all heads that the lane takes of it.
+// position of 10^5 would leave a third of the digits.  inv_freq / 2 pi as a 64-bit fraction of a
+// turn (an exact 24 x 128-bit product, cut) times the position, modulo 2^64, has an error of
+// 2^-33 turns at most; its top 32 bits are the angle.
+#include "f32x2.cuh"
 #include "mix.h"
 #include "ptx.cuh"
 
@@ -20,34 +25,14 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
-template <bool VEC>
-DM_DEV void load4(const __nv_bfloat16* p, float (&v)[4]) {
-  if (VEC) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __bfloat162float(p[i]);
-  }
-}
-template <bool VEC>
-DM_DEV void store4(__nv_bfloat16* p, const float (&v)[4]) {
-  if (VEC) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t*>(&a);
-    w.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __float2bfloat16_rn(v[i]);
-  }
-}
-
-// The lane's share of a head.
+// ------------------------------------------------------------------ a lane's share of a head
+// Four pairs (x, y), two to a word of each.
+struct Pairs {
+  F2 x[2], y[2];
+};
+struct Raw {  // eight bf16: the lane's two runs of four
+  uint2 a, b;
+};
 struct Share {
   int a, b;      // first elements of its two runs
   bool in;       // it has elements
@@ -68,54 +53,104 @@ DM_DEV Share share_of(int l, int dim, int rotary) {
   return s;
 }
 
-// The four angles of a lane as fractions of a turn per position, in 2^-64.
-struct Turns {
-  unsigned long long f[4];
-  float bad[4];  // 0, or NaN for a frequency that is not finite
-};
-DM_DEV Turns turns_of(const float* inv_freq, int l, bool turned) {
-  Turns t;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    double f = turned ? double(inv_freq[4 * l + i]) * 0.15915494309189533577 : 0.0;
-    f -= floor(f);
-    t.bad[i] = float(f - f);
-    t.f[i] = static_cast<unsigned long long>(f * 18446744073709551616.0);
-  }
-  return t;
+template <bool VEC>
+DM_DEV uint2 load4(const __nv_bfloat16* p) {
+  if (VEC) return *reinterpret_cast<const uint2*>(p);
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+  return make_uint2(uint32_t(h[0]) | uint32_t(h[1]) << 16, uint32_t(h[2]) | uint32_t(h[3]) << 16);
 }
-DM_DEV void angles(const Turns& t, int position, float (&c)[4], float (&s)[4]) {
+template <bool VEC>
+DM_DEV void store4(__nv_bfloat16* p, uint2 v) {
+  if (VEC) {
+    *reinterpret_cast<uint2*>(p) = v;
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+    h[0] = uint16_t(v.x);
+    h[1] = uint16_t(v.x >> 16);
+    h[2] = uint16_t(v.y);
+    h[3] = uint16_t(v.y >> 16);
+  }
+}
+template <bool ILV>
+DM_DEV Pairs unpack(const Raw& r) {
+  Pairs p;
+  if (ILV) {
+    p.x[0] = f2(bf16_lo(r.a.x), bf16_lo(r.a.y));
+    p.y[0] = f2(bf16_hi(r.a.x), bf16_hi(r.a.y));
+    p.x[1] = f2(bf16_lo(r.b.x), bf16_lo(r.b.y));
+    p.y[1] = f2(bf16_hi(r.b.x), bf16_hi(r.b.y));
+  } else {
+    p.x[0] = f2(bf16_lo(r.a.x), bf16_hi(r.a.x));
+    p.x[1] = f2(bf16_lo(r.a.y), bf16_hi(r.a.y));
+    p.y[0] = f2(bf16_lo(r.b.x), bf16_hi(r.b.x));
+    p.y[1] = f2(bf16_lo(r.b.y), bf16_hi(r.b.y));
+  }
+  return p;
+}
+// The eight values in the order of the lane's elements.
+template <bool ILV>
+DM_DEV void in_order(const Pairs& p, float (&v)[8]) {
+  float x[4], y[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f2_split(p.x[i], x[2 * i], x[2 * i + 1]);
+    f2_split(p.y[i], y[2 * i], y[2 * i + 1]);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned long long at = t.f[i] * static_cast<unsigned long long>((long long)position);
-    const float half_turns = float(int(at >> 32)) * 4.656612873077393e-10f + t.bad[i];
-    sincospif(half_turns, &s[i], &c[i]);
+    v[ILV ? 2 * i : i] = x[i];
+    v[ILV ? 2 * i + 1 : i + 4] = y[i];
   }
+}
+template <bool ILV, bool VEC>
+DM_DEV void store(__nv_bfloat16* p, const Share& sh, const Pairs& v) {
+  float o[8];
+  in_order<ILV>(v, o);
+  store4<VEC>(p + sh.a, make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])));
+  store4<VEC>(p + sh.b, make_uint2(pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])));
 }
 
-// (a, b) of a lane turned by its angles (back: by minus them).
-template <bool ILV, bool BACK>
-DM_DEV void turn(float (&a)[4], float (&b)[4], const float (&c)[4], const float (&s0)[4]) {
-  float s[4];
+// ------------------------------------------------------------------ angles
+// inv_freq radians as a fraction of a turn in 2^-64 (whole turns dropped).
+DM_DEV unsigned long long turn_of(float inv_freq) {
+  // 2^128 / 2 pi
+  constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;
+  const uint32_t bits = __float_as_uint(inv_freq);
+  const int expo = int(bits >> 23) & 255;
+  unsigned long long m = bits & 0x7FFFFFu;
+  if (expo != 0) m |= 0x800000u;
+  // |f| = m 2^(e - 150), so the fraction is m (2^128 / 2 pi) 2^(e - 214) modulo 2^64
+  const int shift = 214 - (expo == 0 ? 1 : expo);
+  const unsigned long long w0 = m * kLo, c = __umul64hi(m, kLo), lo = m * kHi;
+  const unsigned long long w1 = lo + c, w2 = __umul64hi(m, kHi) + (w1 < lo ? 1 : 0);
+  unsigned long long f;
+  if (shift >= 192) f = 0;
+  else if (shift >= 128) f = w2 >> (shift - 128);
+  else if (shift > 64) f = w1 >> (shift - 64) | w2 << (128 - shift);
+  else if (shift == 64) f = w1;
+  else if (shift > 0) f = w0 >> shift | w1 << (64 - shift);
+  else f = shift > -64 ? w0 << -shift : 0;
+  return (bits >> 31) != 0 ? 0ull - f : f;
+}
+
+// Sines and cosines of a lane's four angles; one and zero where nothing turns.
+DM_DEV void angles(const float* inv_freq, int l, bool turned, int position, F2 (&c)[2], F2 (&s)[2]) {
+  float co[4], si[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = BACK ? -s0[i] : s0[i];
-  if (ILV) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = a[2 * i], y = a[2 * i + 1];
-      a[2 * i] = x * c[i] - y * s[i];
-      a[2 * i + 1] = x * s[i] + y * c[i];
-      const float u = b[2 * i], v = b[2 * i + 1];
-      b[2 * i] = u * c[2 + i] - v * s[2 + i];
-      b[2 * i + 1] = u * s[2 + i] + v * c[2 + i];
+  for (int i = 0; i < 4; ++i) {
+    co[i] = 1.f;
+    si[i] = 0.f;
+    if (turned) {
+      const float f = inv_freq[4 * l + i];
+      const unsigned long long at = turn_of(f) * static_cast<unsigned long long>((long long)position);
+      // a frequency that is no number leaves none
+      sincospif(fmaf(float(int(at >> 32)), 4.656612873077393e-10f, f - f), &si[i], &co[i]);
     }
-  } else {
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = x * c[i] - y * s[i];
-      b[i] = x * s[i] + y * c[i];
-    }
+  for (int i = 0; i < 2; ++i) {
+    c[i] = f2(co[2 * i], co[2 * i + 1]);
+    s[i] = f2(si[2 * i], si[2 * i + 1]);
   }
 }
 
@@ -125,126 +160,207 @@ DM_DEV float group_sum(float v) {
   for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
-
-DM_DEV float square_sum(const float (&a)[4], const float (&b)[4]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
-  return s;
+DM_DEV float dot(const Pairs& a, const Pairs& b) {
+  F2 t = mul2(a.x[0], b.x[0]);
+  t = fma2(a.x[1], b.x[1], t);
+  t = fma2(a.y[0], b.y[0], t);
+  t = fma2(a.y[1], b.y[1], t);
+  float lo, hi;
+  f2_split(t, lo, hi);
+  return lo + hi;
 }
 
-template <int LANES, bool ILV, bool VEC, bool BACK>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs g) {
-  constexpr int kGroups = 32 / LANES;  // heads that a warp takes at once
-  constexpr int kDepth = BACK ? 2 : 4;  // and how many times it loads before it computes
-  grid_launch_dependents();
-  grid_wait();
+// A lane's gains.
+template <bool ILV>
+DM_DEV Pairs gains(const __nv_bfloat16* w, const Share& sh) {
+  Raw r{make_uint2(0x3F803F80u, 0x3F803F80u), make_uint2(0x3F803F80u, 0x3F803F80u)};
+  if (w != nullptr && sh.in) {
+    r.a = load4<false>(w + sh.a);
+    r.b = load4<false>(w + sh.b);
+  }
+  return unpack<ILV>(r);
+}
+
+// ------------------------------------------------------------------ kernels
+// A chunk is kGroups * kDepth heads of queries or keys; a warp takes `per` chunks of a token.
+template <int LANES>
+struct Chunk {
+  static constexpr int kGroups = 32 / LANES, kDepth = 4, kHeads = kGroups * kDepth;
+};
+constexpr int kBlocks = 7, kGradBlocks = 4;  // resident on an SM
+
+template <int LANES, bool ILV, bool VEC>
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeArgs g) {
+  using C = Chunk<LANES>;
   const int lane = threadIdx.x & 31, l = lane % LANES, group = lane / LANES;
   const Share sh = share_of<ILV>(l, g.dim, g.rotary);
-  const Turns turns = turns_of(g.inv_freq, l, sh.turned);
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = int(u / unsigned(g.parts)), part = int(u - unsigned(t) * unsigned(g.parts));
+  grid_launch_dependents();
+  grid_wait();
+  if (t >= g.tokens) return;
   const float inv_dim = 1.f / float(g.dim);
-  float wa[2][4], wb[2][4], da[2][4], db[2][4];
+  const int q_chunks = (g.heads[0] + C::kHeads - 1) / C::kHeads;
+  const int chunks = q_chunks + (g.heads[1] + C::kHeads - 1) / C::kHeads;
+  const int position = g.rotary > 0 ? g.position[t] : 0;
+  F2 c[2], s[2];
+  bool fresh = true;
+  for (int n = part * g.per; n < min(chunks, (part + 1) * g.per); ++n) {
+    const int x = n >= q_chunks ? 1 : 0;
+    const int h0 = (n - x * q_chunks) * C::kHeads + group;
+    const __nv_bfloat16* in = g.x[x].p + t * g.x[x].ts + h0 * g.x[x].hs;
+    __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts + h0 * g.out[x].hs;
+    Raw raw[C::kDepth];
+#pragma unroll
+    for (int d = 0; d < C::kDepth; ++d) {
+      raw[d] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+      if (sh.in && h0 + d * C::kGroups < g.heads[x]) {
+        const __nv_bfloat16* p = in + (long long)d * C::kGroups * g.x[x].hs;
+        raw[d].a = load4<VEC>(p + sh.a);
+        raw[d].b = load4<VEC>(p + sh.b);
+      }
+    }
+    if (fresh) angles(g.inv_freq, l, sh.turned, position, c, s);
+    fresh = false;
+    const Pairs w = gains<ILV>(g.w[x], sh);
+    Pairs wc, ws;  // x_out = r (x wc.x - y ws.y), y_out = r (x ws.x + y wc.y)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      wc.x[i] = mul2(w.x[i], c[i]);
+      wc.y[i] = mul2(w.y[i], c[i]);
+      ws.x[i] = mul2(w.x[i], s[i]);
+      ws.y[i] = negate2(mul2(w.y[i], s[i]));
+    }
+#pragma unroll
+    for (int d = 0; d < C::kDepth; ++d) {
+      const Pairs v = unpack<ILV>(raw[d]);
+      const float r = rsqrtf(fmaf(group_sum<LANES>(dot(v, v)), inv_dim, g.eps));
+      const F2 rr = f2(r, r);
+      Pairs o;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o.x[i] = mul2(rr, fma2(v.x[i], wc.x[i], mul2(v.y[i], ws.y[i])));
+        o.y[i] = mul2(rr, fma2(v.x[i], ws.x[i], mul2(v.y[i], wc.y[i])));
+      }
+      if (sh.in && h0 + d * C::kGroups < g.heads[x])
+        store<ILV, VEC>(out + (long long)d * C::kGroups * g.out[x].hs, sh, o);
+    }
+  }
+}
+
+// Gradients.  With SUMS the gains' too: a block sums its own, for rope_gains_kernel.
+template <int LANES, bool ILV, bool VEC>
+__global__ void __launch_bounds__(kThreads, kGradBlocks) rope_grad_kernel(const __grid_constant__ RopeArgs g) {
+  using C = Chunk<LANES>;
+  const int lane = threadIdx.x & 31, l = lane % LANES, group = lane / LANES;
+  const Share sh = share_of<ILV>(l, g.dim, g.rotary);
+  grid_launch_dependents();
+  grid_wait();
+  const float inv_dim = 1.f / float(g.dim);
+  const int q_chunks = (g.heads[0] + C::kHeads - 1) / C::kHeads;
+  const int chunks = q_chunks + (g.heads[1] + C::kHeads - 1) / C::kHeads;
+  Pairs dw[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool has = g.w[x] != nullptr && sh.in && g.heads[x] > 0;
-      wa[x][i] = has ? __bfloat162float(g.w[x][sh.a + i]) : 1.f;
-      wb[x][i] = has ? __bfloat162float(g.w[x][sh.b + i]) : 1.f;
-      da[x][i] = db[x][i] = 0.f;
-    }
-  const long long units = (long long)g.tokens * g.parts;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * kWarps) {
-    const int t = int(u / g.parts), part = int(u - (long long)t * g.parts);
-    float c[4], s[4];
-    if (g.rotary > 0) angles(turns, g.position[t], c, s);
+    for (int i = 0; i < 2; ++i) dw[x].x[i] = dw[x].y[i] = 0;
+  const unsigned units = unsigned(g.tokens) * unsigned(g.parts);
+  for (unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
+    const int t = int(u / unsigned(g.parts)), part = int(u - unsigned(t) * unsigned(g.parts));
+    const int position = g.rotary > 0 ? g.position[t] : 0;
+    F2 c[2], s[2];
+    bool fresh = true;
+    for (int n = part * g.per; n < min(chunks, (part + 1) * g.per); ++n) {
+      const int x = n >= q_chunks ? 1 : 0;
+      const int h0 = (n - x * q_chunks) * C::kHeads + group;
+      const __nv_bfloat16* in = g.x[x].p + t * g.x[x].ts + h0 * g.x[x].hs;
+      const __nv_bfloat16* dy = g.dy[x].p + t * g.dy[x].ts + h0 * g.dy[x].hs;
+      __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts + h0 * g.out[x].hs;
+      Raw raw[C::kDepth], grad[C::kDepth];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const __nv_bfloat16* xin = g.x[x].p + t * g.x[x].ts;
-      const __nv_bfloat16* dyin = BACK ? g.dy[x].p + t * g.dy[x].ts : nullptr;
-      __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts;
-      // every lane of the warp goes round equally often: the sums cross lanes
-      for (int h0 = part * kGroups * kDepth; h0 < g.heads[x]; h0 += g.parts * kGroups * kDepth) {
-        float a[kDepth][4], b[kDepth][4], ga[kDepth][4], gb[kDepth][4];
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          const int h = h0 + d * kGroups + group;
-          const bool has = sh.in && h < g.heads[x];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[d][i] = b[d][i] = ga[d][i] = gb[d][i] = 0.f;
-          if (has) {
-            load4<VEC>(xin + h * g.x[x].hs + sh.a, a[d]);
-            load4<VEC>(xin + h * g.x[x].hs + sh.b, b[d]);
-            if (BACK) {
-              load4<VEC>(dyin + h * g.dy[x].hs + sh.a, ga[d]);
-              load4<VEC>(dyin + h * g.dy[x].hs + sh.b, gb[d]);
-            }
-          }
+      for (int d = 0; d < C::kDepth; ++d) {
+        raw[d] = grad[d] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+        if (sh.in && h0 + d * C::kGroups < g.heads[x]) {
+          const __nv_bfloat16* p = in + (long long)d * C::kGroups * g.x[x].hs;
+          raw[d].a = load4<VEC>(p + sh.a);
+          raw[d].b = load4<VEC>(p + sh.b);
+          p = dy + (long long)d * C::kGroups * g.dy[x].hs;
+          grad[d].a = load4<VEC>(p + sh.a);
+          grad[d].b = load4<VEC>(p + sh.b);
         }
+      }
+      if (fresh) angles(g.inv_freq, l, sh.turned, position, c, s);
+      fresh = false;
+      const Pairs w = gains<ILV>(g.w[x], sh);
+      Pairs sum;
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          const int h = h0 + d * kGroups + group;
-          const bool has = sh.in && h < g.heads[x];
-          const float r = rsqrtf(group_sum<LANES>(square_sum(a[d], b[d])) * inv_dim + g.eps);
-          if (!BACK) {
+      for (int i = 0; i < 2; ++i) sum.x[i] = sum.y[i] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[d][i] = a[d][i] * r * wa[x][i];
-              b[d][i] = b[d][i] * r * wb[x][i];
-            }
-            if (sh.turned) turn<ILV, false>(a[d], b[d], c, s);
-          } else {
-            if (sh.turned) turn<ILV, true>(ga[d], gb[d], c, s);
-            float m = 0.f;
+      for (int d = 0; d < C::kDepth; ++d) {
+        const bool has = sh.in && h0 + d * C::kGroups < g.heads[x];
+        Pairs v = unpack<ILV>(raw[d]);
+        const Pairs z = unpack<ILV>(grad[d]);
+        const float r = rsqrtf(fmaf(group_sum<LANES>(dot(v, v)), inv_dim, g.eps));
+        const F2 rr = f2(r, r);
+        Pairs gw;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[d][i] *= r;  // n
-              b[d][i] *= r;
-              if (has) {
-                da[x][i] = fmaf(ga[d][i], a[d][i], da[x][i]);
-                db[x][i] = fmaf(gb[d][i], b[d][i], db[x][i]);
-              }
-              ga[d][i] *= wa[x][i];
-              gb[d][i] *= wb[x][i];
-              m = fmaf(ga[d][i], a[d][i], fmaf(gb[d][i], b[d][i], m));
-            }
-            m = group_sum<LANES>(m) * inv_dim;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[d][i] = r * fmaf(-a[d][i], m, ga[d][i]);
-              b[d][i] = r * fmaf(-b[d][i], m, gb[d][i]);
-            }
+        for (int i = 0; i < 2; ++i) {
+          const F2 gx = fma2(z.x[i], c[i], mul2(z.y[i], s[i]));
+          const F2 gy = fma2(z.y[i], c[i], negate2(mul2(z.x[i], s[i])));
+          v.x[i] = mul2(v.x[i], rr);  // n
+          v.y[i] = mul2(v.y[i], rr);
+          if (has) {  // an absent head's r may be infinite
+            sum.x[i] = fma2(gx, v.x[i], sum.x[i]);
+            sum.y[i] = fma2(gy, v.y[i], sum.y[i]);
           }
-          if (has) {
-            store4<VEC>(out + h * g.out[x].hs + sh.a, a[d]);
-            store4<VEC>(out + h * g.out[x].hs + sh.b, b[d]);
-          }
+          gw.x[i] = mul2(gx, w.x[i]);
+          gw.y[i] = mul2(gy, w.y[i]);
+        }
+        const float m = -group_sum<LANES>(dot(gw, v)) * inv_dim;
+        const F2 mm = f2(m, m);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          v.x[i] = mul2(rr, fma2(v.x[i], mm, gw.x[i]));
+          v.y[i] = mul2(rr, fma2(v.y[i], mm, gw.y[i]));
+        }
+        if (has) store<ILV, VEC>(out + (long long)d * C::kGroups * g.out[x].hs, sh, v);
+      }
+      const F2 one = f2(1.f, 1.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (x == 0) {
+          dw[0].x[i] = fma2(sum.x[i], one, dw[0].x[i]);
+          dw[0].y[i] = fma2(sum.y[i], one, dw[0].y[i]);
+        } else {
+          dw[1].x[i] = fma2(sum.x[i], one, dw[1].x[i]);
+          dw[1].y[i] = fma2(sum.y[i], one, dw[1].y[i]);
         }
       }
     }
   }
-  if (BACK && g.partial != nullptr) {
-    // the block's sums, its groups one after another
-    constexpr int kBlockGroups = kWarps * kGroups;
-    __shared__ float sums[kBlockGroups][2 * LANES * 8];
-    float* mine = sums[(threadIdx.x >> 5) * kGroups + group];
-    if (sh.in) {
+  if (g.partial == nullptr) return;
+  // the block's sums, its groups one after another
+  constexpr int kBlockGroups = kWarps * C::kGroups;
+  __shared__ float sums[kBlockGroups][2 * LANES * 8];
+  float* mine = sums[(threadIdx.x >> 5) * C::kGroups + group];
+  if (sh.in) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x) {
+      float v[8];
+      in_order<ILV>(dw[x], v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mine[x * g.dim + sh.a + i] = da[x][i];
-          mine[x * g.dim + sh.b + i] = db[x][i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        mine[x * g.dim + sh.a + i] = v[i];
+        mine[x * g.dim + sh.b + i] = v[i + 4];
+      }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * g.dim; i += kThreads) {
-      float v = 0.f;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * g.dim; i += kThreads) {
+    float v = 0.f;
 #pragma unroll 8
-      for (int k = 0; k < kBlockGroups; ++k) v += sums[k][i];
-      g.partial[(long long)blockIdx.x * 2 * g.dim + i] = v;
-    }
+    for (int k = 0; k < kBlockGroups; ++k) v += sums[k][i];
+    g.partial[(long long)blockIdx.x * 2 * g.dim + i] = v;
   }
 }
 
@@ -259,6 +375,7 @@ __global__ void __launch_bounds__(1024) rope_gains_kernel(const float* partial, 
   const int i = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (i < 2 * dim)
+#pragma unroll 8
     for (int b = row; b < blocks; b += 32) v += partial[(long long)b * 2 * dim + i];
   sums[row][lane] = v;
   __syncthreads();
@@ -275,12 +392,10 @@ using RopeKernel = void (*)(RopeArgs);
 template <int LANES>
 RopeKernel kernel_of(bool back, bool ilv, bool vec) {
   if (back)
-    return ilv ? (vec ? rope_kernel<LANES, true, true, true> : rope_kernel<LANES, true, false, true>)
-               : (vec ? rope_kernel<LANES, false, true, true>
-                      : rope_kernel<LANES, false, false, true>);
-  return ilv ? (vec ? rope_kernel<LANES, true, true, false> : rope_kernel<LANES, true, false, false>)
-             : (vec ? rope_kernel<LANES, false, true, false>
-                    : rope_kernel<LANES, false, false, false>);
+    return ilv ? (vec ? rope_grad_kernel<LANES, true, true> : rope_grad_kernel<LANES, true, false>)
+               : (vec ? rope_grad_kernel<LANES, false, true> : rope_grad_kernel<LANES, false, false>);
+  return ilv ? (vec ? rope_kernel<LANES, true, true> : rope_kernel<LANES, true, false>)
+             : (vec ? rope_kernel<LANES, false, true> : rope_kernel<LANES, false, false>);
 }
 
 }  // namespace
@@ -293,17 +408,18 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
                        : lanes == 8  ? kernel_of<8>(backward, interleaved, vec)
                        : lanes == 16 ? kernel_of<16>(backward, interleaved, vec)
                                      : kernel_of<32>(backward, interleaved, vec);
-  // A token to a warp, unless that leaves warps of the GPU idle: then its heads are shared.
-  const int most = g.heads[0] > g.heads[1] ? g.heads[0] : g.heads[1];
-  const int at_once = 32 / lanes * (backward ? 2 : 4);
-  const int max_parts = (most + at_once - 1) / at_once;
-  const long long full = (long long)sms * 8 * kWarps;
-  g.parts = 1;
-  while (g.parts < max_parts && (long long)g.tokens * g.parts < full) ++g.parts;
-  long long blocks = ((long long)g.tokens * g.parts + kWarps - 1) / kWarps;
-  const long long resident = (long long)sms * 8;
-  if (blocks > resident) blocks = resident;
-  if (blocks > kRopeBlocks) blocks = kRopeBlocks;
+  // Chunks of a warp share their token's sines; but with few tokens more warps of one chunk each
+  // fill the GPU (8192 tokens of 64 heads of 128: 52 us with 2 chunks to a warp, 48 with 8; 777 of
+  // 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take token after token, so that the
+  // gains' sums meet once a block (88 us with twice the blocks that fit, 82 with as many).
+  const int heads = 32 / lanes * 4;
+  const int chunks = (g.heads[0] + heads - 1) / heads + (g.heads[1] + heads - 1) / heads;
+  g.per = (long long)g.tokens * chunks > (long long)sms * 56 ? (backward ? 4 : 8) : 1;
+  g.parts = (chunks + g.per - 1) / g.per;
+  const long long units = (long long)g.tokens * g.parts;
+  long long blocks = (units + kWarps - 1) / kWarps;
+  if (backward && blocks > (long long)sms * kGradBlocks) blocks = (long long)sms * kGradBlocks;
+  if (backward && blocks > kRopeBlocks) blocks = kRopeBlocks;
   if (blocks > 0) {
     const cudaError_t e = launch_dependent(k, unsigned(blocks), unsigned(kThreads), s, g);
     if (e != cudaSuccess) return e;

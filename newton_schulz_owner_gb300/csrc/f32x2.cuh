@@ -46,4 +46,16 @@ DM_DEV uint32_t pack_bf16(F2 v) {
   return pack_bf16(lo, hi);
 }
 
+// Two bf16 numbers at a time: a b + c, rounded once.
+DM_DEV uint32_t bf16_fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+DM_DEV uint32_t bf16_mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 }  // namespace dm

@@ -34,11 +34,11 @@
 namespace dm {
 namespace {
 
-// Warps: states, weighted scores, outputs, loads and products (two of the last four idle: register
+// Warps: states, weighted scores, outputs, loads and products (one of the last four idles: register
 // shares are given to whole warpgroups).
 constexpr int kStateWarps = 8, kWeighWarps = 8, kOutWarps = 4, kOtherWarps = 4;
 constexpr int kWeighWarp = kStateWarps, kOutWarp = kWeighWarp + kWeighWarps;
-constexpr int kLoadWarp = kOutWarp + kOutWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kLoadWarp = kOutWarp + kOutWarps, kStateMmaWarp = kLoadWarp + 1, kMmaWarp = kLoadWarp + 2;
 constexpr int kThreads = (kStateWarps + kWeighWarps + kOutWarps + kOtherWarps) * 32;
 // Registers of a thread at launch, and what each kind takes: the shares add up to what the block
 // was launched with.
@@ -47,20 +47,20 @@ static_assert(kStateWarps * kStateRegs + kWeighWarps * kWeighRegs + kOutWarps * 
                       kOtherWarps * kOtherRegs == kThreads / 32 * kRegs, "");
 constexpr int kMaxStages = 4;
 constexpr int kSmemBytes = 232448;
-constexpr int kMiscBytes = 1536;  // barriers and powers of the decay
+constexpr int kMiscBytes = 2048;  // barriers and powers of the decay
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: scores (then the weighted ones), the block's own state, two parts of the output
 constexpr uint32_t kColScore = 0, kColState = 128, kColInner = 256, kColOuter = 384;
 constexpr long long kAbortSettleCycles = 2000000;
-constexpr int kRoundBlocks = 8;
+constexpr int kRoundBlocks = 16;
 
 // DK, DV: head sizes padded to 64 or 128 (TMA fills with zeros).
 template <int DK, int DV>
 struct Tiles {
   static constexpr int k = kMixBlock * DK * 2, v = kMixBlock * DV * 2;
-  static constexpr int q = DK > DV ? k : v;  // also holds the output on its way out
+  static constexpr int q = k > v ? k : v;  // also holds the output on its way out
   static constexpr int stage = q + k + v;
-  static constexpr int state = DK * DV * 2;
+  static constexpr int state = k;  // the entering state, or before it the keys' low parts
   static constexpr int fit = (kSmemBytes - 1024 - kMiscBytes - state) / stage;
   static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
   static_assert(stages >= 2, "two stages must fit");
@@ -68,14 +68,14 @@ struct Tiles {
 };
 
 struct Shared {
-  uint64_t full[kMaxStages];   // a stage's loads
-  uint64_t empty[kMaxStages];  // its products, and its output gone
+  uint64_t full[kMaxStages];   // a stage's keys and values are there
+  uint64_t empty[kMaxStages];  // and have been read
+  uint64_t q_full[kMaxStages], q_empty[kMaxStages];  // its queries; its output has left their place
   uint64_t score;              // scores in TMEM
   uint64_t weighted;           // weighted scores in TMEM
   uint64_t keys[2];            // keys decayed, rows past the end cleared: of even and odd blocks, as
                                // the states' warps may be one ahead of the products there
-  uint64_t half;               // the state's first product (exact states)
-  uint64_t low;                // the keys' low parts in shared memory
+  uint64_t clear;              // the same of the sweep's blocks, for the other products
   uint64_t block_state[2];     // the block's state in TMEM
   uint64_t entry;              // the entering state in shared memory
   uint64_t spent;              // weighted scores read
@@ -88,19 +88,24 @@ struct Shared {
   int place[6];                // what locate() found
   int sums[kThreads / 32];
   alignas(16) float fall[96];        // what weigh() needs of the powers of a
-  float power_[32 + kMixBlock + 1];  // a^n, n = -32 .. 128; zeros below 0
+  float near_[64];                   // scale a^n, n = -32 .. 31; zeros below 0
+  float power[kMixBlock + 1];        // a^n
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "");
 
-DM_DEV void raise_abort(int* err, volatile int* flag) {
+// What is not needed block by block stays out of line: four kinds of warps run side by side, and
+// their code has to fit the instruction cache (at 290 KB of it a block took half as long again).
+DM_DEV bool gave_up(int* err, volatile int* flag) {
   *flag = 1;
   atomicExch(err, DMUON_ERR_TIMEOUT);
+  return false;
+}
+DM_DEV bool await_long(uint64_t* bar, uint32_t parity, int* err, volatile int* flag) {
+  return mbar_wait(bar, parity, flag) || gave_up(err, flag);
 }
 // Wait of a whole warp (or one thread); false: gave up.
 DM_DEV bool await(uint64_t* bar, uint32_t parity, int* err, volatile int* flag) {
-  if (mbar_wait(bar, parity, flag)) return true;
-  raise_abort(err, flag);
-  return false;
+  return mbar_try_wait(smem_u32(bar), parity) || await_long(bar, parity, err, flag);
 }
 
 // ------------------------------------------------------------------ the packed batch
@@ -129,24 +134,29 @@ struct Cursor {
   DM_DEV int before(const LinAttnArgs& g, int n) const {
     return g.against ? x.len - min(x.len, (x.blocks - n) * kMixBlock) : min(x.len, n * kMixBlock);
   }
-  // n blocks on (past the batch's end: any block)
-  DM_DEV void skip(const LinAttnArgs& g, int n) {
-    while (n >= x.blocks - m) {
-      n -= x.blocks - m;
-      m = 0;
-      do {
-        seq += g.against ? -1 : 1;
-        if (seq < 0 || seq >= g.sequences) {
-          seq = 0;
-          x = Extent{0, 0, 0x7FFFFFFF};
-          break;
-        }
-        x = extent_of(g, seq);
-      } while (x.blocks == 0);
-    }
-    m += n;
-  }
 };
+// n blocks on (past the batch's end: any block)
+DM_DEV Cursor skipped(const LinAttnArgs& g, Cursor c, int n) {
+  while (n >= c.x.blocks - c.m) {
+    n -= c.x.blocks - c.m;
+    c.m = 0;
+    do {
+      c.seq += g.against ? -1 : 1;
+      if (c.seq < 0 || c.seq >= g.sequences) {
+        c.seq = 0;
+        c.x = Extent{0, 0, 0x7FFFFFFF};
+        break;
+      }
+      c.x = extent_of(g, c.seq);
+    } while (c.x.blocks == 0);
+  }
+  c.m += n;
+  return c;
+}
+DM_DEV void next_block(const LinAttnArgs& g, Cursor& c) {
+  if (c.m + 1 < c.x.blocks) ++c.m;
+  else c = skipped(g, c, 1);
+}
 
 // What a CTA does: stretches of `per` blocks, one in each round, of the nb blocks that its cluster
 // takes.
@@ -267,29 +277,28 @@ struct Round {
   int lo, n, ahead;
   Cursor at, share;
 };
-DM_DEV void fill_round(const LinAttnArgs& g, const Work& w, Round& r) {
-  r.n = max(0, min(w.per, w.nb - r.lo));
+DM_DEV Round round_of(const LinAttnArgs& g, const Work w, Cursor at, int lo) {
+  Round r;
+  r.lo = lo;
+  r.at = r.share = at;
+  r.n = max(0, min(w.per, w.nb - lo));
   r.ahead = 0;
   if (w.rank + 1 < g.split && r.n > 0) {
-    r.share = r.at;
-    r.share.skip(g, r.n - 1);
+    r.share = skipped(g, at, r.n - 1);
     if (r.share.m + 1 < r.share.x.blocks) {
       r.ahead = min(r.share.m + 1, r.n);
       r.share.m -= r.ahead - 1;
     }
   }
-}
-DM_DEV Round first_round(const LinAttnArgs& g, const Work& w) {
-  Round r;
-  r.lo = w.rank * w.per;
-  r.at = w.start;
-  fill_round(g, w, r);
   return r;
 }
+DM_DEV Round first_round(const LinAttnArgs& g, const Work& w) {
+  return round_of(g, w, w.start, w.rank * w.per);
+}
 DM_DEV void next_round(const LinAttnArgs& g, const Work& w, Round& r) {
-  if (r.lo + g.split * w.per < w.nb) r.at.skip(g, g.split * w.per);
-  r.lo += g.split * w.per;
-  fill_round(g, w, r);
+  const int lo = r.lo + g.split * w.per;
+  if (lo < w.nb) r.at = skipped(g, r.at, g.split * w.per);
+  r = round_of(g, w, r.at, lo);
 }
 
 // ------------------------------------------------------------------ loads
@@ -300,18 +309,26 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
   int it = 0;
   auto load = [&](int row, bool queries) {
     const int s = it % T::stages;
-    if (!await(&sh->empty[s], ((it / T::stages) & 1) ^ 1, g.err, flag)) return false;
+    const uint32_t parity = ((it / T::stages) & 1) ^ 1;
     uint8_t* q = smem + s * T::stage;
     uint8_t *k = q + T::q, *v = k + T::k;
-    uint64_t* bar = &sh->full[s];
-    mbar_arrive_expect_tx(bar, uint32_t(T::k + T::v + (queries ? T::k : 0)));
+    if (!await(&sh->empty[s], parity, g.err, flag)) return false;
+    mbar_arrive_expect_tx(&sh->full[s], uint32_t(T::k + T::v));
 #pragma unroll
-    for (int p = 0; p < DK / 64; ++p) {
-      if (queries) tma_load_3d(q + p * 16384, &g.q, bar, p * 64, head, row);
-      tma_load_3d(k + p * 16384, &g.k, bar, p * 64, head, row);
+    for (int p = 0; p < DK / 64; ++p)
+      tma_load_3d(k + p * 16384, &g.k, &sh->full[s], p * 64, head, row);
+#pragma unroll
+    for (int p = 0; p < DV / 64; ++p)
+      tma_load_3d(v + p * 16384, &g.v, &sh->full[s], p * 64, head, row);
+    if (!await(&sh->q_empty[s], parity, g.err, flag)) return false;
+    if (queries) {
+      mbar_arrive_expect_tx(&sh->q_full[s], uint32_t(T::k));
+#pragma unroll
+      for (int p = 0; p < DK / 64; ++p)
+        tma_load_3d(q + p * 16384, &g.q, &sh->q_full[s], p * 64, head, row);
+    } else {
+      mbar_arrive(&sh->q_full[s]);
     }
-#pragma unroll
-    for (int p = 0; p < DV / 64; ++p) tma_load_3d(v + p * 16384, &g.v, bar, p * 64, head, row);
     ++it;
     return true;
   };
@@ -321,117 +338,120 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
     for (int i = 0; i < r.ahead; ++i, ++c.m)
       if (!load(c.row(g), false)) return;
     c = r.at;
-    for (int i = 0; i < r.n; ++i, c.skip(g, 1))
+    for (int i = 0; i < r.n; ++i, next_block(g, c))
       if (!load(c.row(g), true)) return;
     next_round(g, w, r);
   }
 }
 
 // ------------------------------------------------------------------ products
-template <int DK, int DV>
-DM_DEV void mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state, Shared* sh) {
+// Two threads issue them, as issuing (about 75 cycles a product of 16 K-elements) takes as long as
+// computing: one the blocks' own states, one the rest.
+template <int DK, int DV, bool EXACT>
+DM_DEV void state_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state,
+                           Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
   const uint32_t tmem = sh->tmem;
-  const bool exact = g.exact != 0;
-  constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
-  constexpr uint32_t id_inner = idesc_bf16(128, DV, false, true);
-  constexpr uint32_t id_state = idesc_bf16(128, DV, true, true);
+  constexpr uint32_t id = idesc_bf16(128, DV, true, true);
   // (a^..k)^T V, rows of K in steps of 16 tokens.  With 64 key elements the upper half of the
   // 128 rows reads what follows the tile; those lanes of the result are not used.
-  auto block_state = [&](uint32_t to, uint32_t k, uint32_t v, bool accumulate) {
+  auto product = [&](uint32_t to, uint32_t k, uint32_t v, bool accumulate) {
     const uint64_t a = sdesc_sw128(k, 16384, 1024), b = sdesc_sw128(v, 16384, 1024);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      umma_bf16(tmem + to, a + uint64_t(j) * 128, b + uint64_t(j) * 128, id_state,
-                accumulate || j > 0);
+      umma_bf16(to, a + uint64_t(j) * 128, b + uint64_t(j) * 128, id, accumulate || j > 0);
   };
   int it = 0, swept = 0;
-  // ahead of the sweep: the state alone, into two places in turn
-  auto share = [&]() {
-    const int s = it % T::stages;
-    const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
-    if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return false;
-    if (!await(&sh->keys[it & 1], it >> 1 & 1, g.err, flag)) return false;
-    tc_fence_after();
-    const uint32_t to = (it & 1) != 0 ? kColInner : kColState;
-    block_state(to, k, v, false);
-    if (exact) block_state(to, q, v, true);  // the keys' low parts lie where queries would
-    umma_commit(&sh->block_state[it & 1]);
-    umma_commit(&sh->empty[s]);
-    mbar_arrive_n(&sh->empty[s], kOutWarps);
-    ++it;
-    return true;
-  };
-  auto block = [&]() {
-    const int s = it % T::stages;
-    const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
-    if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return false;
-    // the last block's weighted scores have been read (no order is promised between products of
-    // unlike shape); its output is on its way meanwhile
-    if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return false;
-    tc_fence_after();
-    {
-      const uint64_t a = sdesc_sw128(q, 16, 1024), b = sdesc_sw128(k, 16, 1024);
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j) {
-        const uint64_t at = uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2;
-        umma_bf16(tmem + kColScore, a + at, b + at, id_score, j > 0);
-      }
-      umma_commit(&sh->score);
-    }
-    if (!await(&sh->keys[it & 1], it >> 1 & 1, g.err, flag)) return false;
-    tc_fence_after();
-    block_state(kColState, k, v, false);
-    umma_commit(exact ? &sh->half : &sh->block_state[it & 1]);
-    if (!await(&sh->weighted, swept & 1, g.err, flag)) return false;
-    if (swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return false;
-    tc_fence_after();
-    {
-      const uint64_t b = sdesc_sw128(v, 16384, 1024);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)  // 8 columns of weighted scores a step, in two halves
-        umma_bf16_ts(tmem + kColInner, tmem + kColScore + (j >> 2) * 64 + (j & 3) * 8,
-                     b + uint64_t(j) * 128, id_inner, j > 0);
-      umma_commit(&sh->spent);
-    }
-    if (!await(&sh->entry, swept & 1, g.err, flag)) return false;
-    tc_fence_after();
-    {
-      const uint64_t a = sdesc_sw128(q, 16, 1024);
-      const uint64_t e = sdesc_sw128(smem_u32(state), DK * 128, 1024);
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j)
-        umma_bf16(tmem + kColOuter, a + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
-                  e + uint64_t(j) * 128, id_inner, j > 0);
-      umma_commit(&sh->out);
-    }
-    if (exact) {
-      if (!await(&sh->low, swept & 1, g.err, flag)) return false;
-      tc_fence_after();
-      block_state(kColState, k, v, true);
-      umma_commit(&sh->block_state[it & 1]);
-    }
-    umma_commit(&sh->empty[s]);
-    ++swept;
-    ++it;
-    return true;
-  };
   Round r = first_round(g, w);
   for (int round = 0; round < w.rounds; ++round) {
     // the last output of the round before, read by then, makes room for every other share
     if (r.ahead > 0 && swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
-    for (int i = 0; i < r.ahead; ++i)
-      if (!share()) return;
-    for (int i = 0; i < r.n; ++i)
-      if (!block()) return;
+    for (int i = 0; i < r.ahead + r.n; ++i, ++it) {
+      const bool share = i < r.ahead;
+      const int s = it % T::stages;
+      const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
+      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
+      if (!await(&sh->keys[it & 1], it >> 1 & 1, g.err, flag)) return;
+      tc_fence_after();
+      const uint32_t to = tmem + (share && (it & 1) != 0 ? kColOuter : kColState);
+      product(to, k, v, false);
+      // the keys' low parts lie where queries would, or the state that enters will
+      if (EXACT) product(to, share ? q : smem_u32(state), v, true);
+      umma_commit(&sh->block_state[it & 1]);
+      umma_commit(&sh->empty[s]);
+      if (share) {  // in the place of the output's warps
+#pragma unroll
+        for (int n = 0; n < kOutWarps; ++n) umma_commit(&sh->q_empty[s]);
+      } else {
+        ++swept;
+      }
+    }
+    next_round(g, w, r);
+  }
+}
+template <int DK, int DV>
+DM_DEV void out_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state,
+                         Shared* sh) {
+  using T = Tiles<DK, DV>;
+  volatile int* flag = &sh->abort;
+  const uint32_t tmem = sh->tmem;
+  constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t id_out = idesc_bf16(128, DV, false, true);
+  int it = 0, swept = 0;
+  Round r = first_round(g, w);
+  for (int round = 0; round < w.rounds; ++round) {
+    // a stage's loads are waited for in turn, whatever they are for: no wait misses a phase
+    for (int i = 0; i < r.ahead; ++i, ++it) {
+      const int s = it % T::stages;
+      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
+      if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
+      mbar_arrive(&sh->empty[s]);
+    }
+    for (int i = 0; i < r.n; ++i, ++it, ++swept) {
+      const int s = it % T::stages;
+      const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
+      const uint64_t qd = sdesc_sw128(q, 16, 1024);
+      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
+      if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
+      // the last block's weighted scores have been read (no order is promised between products
+      // of unlike shape); its output is on its way meanwhile
+      if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return;
+      tc_fence_after();
+      const uint64_t kd = sdesc_sw128(k, 16, 1024);
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) {
+        const uint64_t at = uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2;
+        umma_bf16(tmem + kColScore, qd + at, kd + at, id_score, j > 0);
+      }
+      umma_commit(&sh->score);
+      if (swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
+      if (!await(&sh->clear, swept & 1, g.err, flag)) return;
+      if (!await(&sh->weighted, swept & 1, g.err, flag)) return;
+      tc_fence_after();
+      const uint64_t vd = sdesc_sw128(v, 16384, 1024);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // 8 columns of weighted scores a step, in two halves
+        umma_bf16_ts(tmem + kColInner, tmem + kColScore + (j >> 2) * 64 + (j & 3) * 8,
+                     vd + uint64_t(j) * 128, id_out, j > 0);
+      umma_commit(&sh->spent);
+      umma_commit(&sh->empty[s]);
+      if (!await(&sh->entry, swept & 1, g.err, flag)) return;
+      tc_fence_after();
+      const uint64_t ed = sdesc_sw128(smem_u32(state), DK * 128, 1024);
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j)
+        umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
+                  ed + uint64_t(j) * 128, id_out, j > 0);
+      umma_commit(&sh->out);
+    }
     next_round(g, w, r);
   }
 }
 
 // ------------------------------------------------------------------ states
 // Thread (warp w, lane) keeps row 32 (w % 4) + lane of the state, columns DV / 2 (w / 4) on.
-template <int DK, int DV>
+template <int DK, int DV, bool EXACT>
 struct StateRole {
   static constexpr int kCols = DV / 2, kThreadsHere = kStateWarps * 32;
   static constexpr int kUnits = kMixBlock * DK / 8 / kThreadsHere;  // 16 bytes of keys each
@@ -444,45 +464,36 @@ struct StateRole {
   float log_decay;
   int head, cluster, tid, lane, row, col;
   F2 st[kCols / 2];
-  float full_weight[4];  // of this thread's four rows of keys in a whole block
 
-  DM_DEV const float* power() const { return sh->power_ + 32; }
   DM_DEV bool wait(uint64_t* bar, int n) { return await(bar, n & 1, g.err, &sh->abort); }
   DM_DEV void zero() {
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) st[i] = 0;
   }
-  DM_DEV long long state_at(int seq) const {
-    return ((long long)seq * g.heads + head) * g.dk * g.dv + (long long)row * g.st_row;
-  }
+  DM_DEV long long state_at(int seq) const { return ((long long)seq * g.heads + head) * g.dk * g.dv; }
   DM_DEV void read_initial(int seq) {
-    zero();
     if (g.state_in == nullptr || row >= g.dk) return;
-    const float* p = g.state_in + state_at(seq);
+    const float* p = g.state_in + state_at(seq) + row * g.st_row + col * g.st_col;
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) {
-      const int c = col + 2 * i;
-      if (c < g.dv)
-        st[i] = f2(g.in_scale * p[(long long)c * g.st_col], g.in_scale * p[(long long)(c + 1) * g.st_col]);
-    }
+    for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col)
+      if (col + 2 * i < g.dv) st[i] = f2(g.in_scale * p[0], g.in_scale * p[g.st_col]);
   }
   DM_DEV void write_final(int seq) {
     if (row >= g.dk) return;
-    float* p = g.state_out + state_at(seq);
+    float* p = g.state_out + state_at(seq) + row * g.st_row + col * g.st_col;
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) {
-      const int c = col + 2 * i;
+    for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col) {
       float a, b;
       f2_split(st[i], a, b);
-      if (c < g.dv) {
-        p[(long long)c * g.st_col] = g.out_scale * a;
-        p[(long long)(c + 1) * g.st_col] = g.out_scale * b;
+      if (col + 2 * i < g.dv) {
+        p[0] = g.out_scale * a;
+        p[g.st_col] = g.out_scale * b;
       }
     }
   }
   // A state in the workspace, four columns at a time so that a warp's rows lie together.  Slots of
   // a CTA: its share of even and of odd rounds (the last CTA's: what the round leaves to the
-  // next), and a copy of a sequence's first state.
+  // next), and a copy of the first state of the sequence that it begins and others end.
   DM_DEV float4* slot(int rank, int which) const {
     return reinterpret_cast<float4*>(g.local) +
            (((size_t)cluster * g.split + rank) * kMixSlots + which) * (kMixLocalBytes / 16) +
@@ -507,18 +518,41 @@ struct StateRole {
       st[2 * i + 1] = fma2(ff, st[2 * i + 1], f2(v.z, v.w));
     }
   }
-  // The state before this CTA's stretch of a round, inside sequence c.seq: what the rounds before
-  // left, and the shares of the CTAs before it.
-  DM_DEV void gather(const Cursor& c, int round) {
+  // A final state may be written over the first one while other CTAs have yet to read that.
+  DM_DEV bool over() const { return g.split > 1 && g.state_in != nullptr && g.state_in == g.state_out; }
+  DM_DEV void keep_initial(int seq) {
+    float4* to = slot(w.rank, 2);
+    const float* p = g.state_in + state_at(seq) + row * g.st_row + col * g.st_col;
+#pragma unroll 1
+    for (int i = 0; i < kCols / 4; ++i, p += 4 * g.st_col) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < g.dk && col + 4 * i < g.dv)
+        v = make_float4(g.in_scale * p[0], g.in_scale * p[g.st_col], g.in_scale * p[2 * g.st_col],
+                        g.in_scale * p[3 * g.st_col]);
+      __stcg(to + i * 128, v);
+    }
+  }
+  // The state before block c: a sequence's first state, or (the first block of a CTA's round, inside
+  // a sequence) that of its start or of the round's, and the shares of the CTAs before this one.
+  DM_DEV void enter(const Cursor& c, int round, const Round& mine) {
+    const int base = round * g.split * w.per;      // sweep's number of the round's first block
+    const int start = mine.lo - c.m;                // and of the sequence's, if c is the CTA's first
+    const bool inside = c.m > 0, older = inside && start < base;
+    const int from = older ? 0 : inside ? (start - base) / w.per : w.rank;
     zero();
-    const int base = round * g.split * w.per;              // sweep's number of the round's first block
-    const int start = base + w.rank * w.per - c.m;          // and of the sequence's
-    int from = 0;
-    if (start < base) take(slot(g.split - 1, round & 1), 1.f);
-    else from = (start - base) / w.per;
-    for (int r = from; r < w.rank; ++r) {
-      const int n0 = max(base + r * w.per - start, 0), n1 = base + (r + 1) * w.per - start;
-      take(slot(r, round & 1), expf(log_decay * float(c.before(g, n1) - c.before(g, n0))));
+    const float4* p = nullptr;
+    if (older) p = slot(g.split - 1, round & 1);
+    else if (over() && (inside || (mine.ahead > 0 && c.seq == mine.share.seq))) p = slot(from, 2);
+    else read_initial(c.seq);
+    float f = 0.f;
+#pragma unroll 1
+    for (int r = from - 1; r < w.rank; ++r) {
+      if (r >= from) {
+        p = slot(r, round & 1);
+        const int n0 = max(base + r * w.per - start, 0), n1 = base + (r + 1) * w.per - start;
+        f = expf(log_decay * float(c.before(g, n1) - c.before(g, n0)));
+      }
+      if (p != nullptr) take(p, f);
     }
   }
   // The state as the operand of Q S: rows of 64 bf16, 128-byte swizzle.
@@ -544,49 +578,57 @@ struct StateRole {
   // The thread's unit n of the keys, its token
   DM_DEV int token_of(int n) const { return ((tid >> 3) + 32 * n) & (kMixBlock - 1); }
   DM_DEV float key_weight(int j, int live) const {
-    return j >= live ? 0.f : power()[g.against ? j + 1 : live - 1 - j];
+    return j >= live ? 0.f : sh->power[g.against ? j + 1 : live - 1 - j];
   }
-  // Keys of block `it` times their decay, in place; what bf16 drops of them (EXACT) to low[], or
-  // (TO_QUERIES) to where the stage's queries would lie.  Rows past the end hold another sequence's
-  // tokens, or anything: they become zeros, here and in V.
-  template <bool EXACT, bool TO_QUERIES, bool WHOLE>
-  DM_DEV void decay_keys(int it, int live, uint32_t (&low)[EXACT && !TO_QUERIES ? kUnits * 4 : 1]) {
+  // Keys of block `it` times their decay, in place; what bf16 drops of them (EXACT) to `low`.  The
+  // decay is kept as a sum of two bf16 numbers, so that k a = k a_0 + k a_1 is rounded like an fp32
+  // product, two elements at a time, and what its rounding drops comes with two more products.
+  // Rows past the end hold another sequence's tokens, or anything: they become zeros, here and in V.
+  DM_DEV void keys(int it, int live, uint32_t low) {
     const uint32_t stage = smem_u32(smem) + (it % T::stages) * T::stage + tid * 16;
+    constexpr int kBatch = 4;  // loads in flight, and rows of a thread
+    uint32_t w0[kBatch], w1[kBatch], mask[kBatch];
 #pragma unroll
-    for (int n = 0; n < kUnits; ++n) {
-      const uint32_t at = stage + T::q + n * kThreadsHere * 16;
-      const int j = token_of(n);
-      const float f = WHOLE ? full_weight[n & 3] : key_weight(j, live);
-      const F2 ff = f2(f, f);
-      uint32_t x[4], y[4];
-      ld_shared_v4(at, x[0], x[1], x[2], x[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 v = WHOLE || j < live ? mul2(bf16_pair(x[i]), ff) : 0;
-        x[i] = pack_bf16(v);
-        y[i] = EXACT ? pack_bf16(add2(v, negate2(bf16_pair(x[i])))) : 0;
-        if constexpr (EXACT && !TO_QUERIES) low[n * 4 + i] = y[i];
-      }
-      st_shared_v4(at, x[0], x[1], x[2], x[3]);
-      if (EXACT && TO_QUERIES) st_shared_v4(at - T::q, y[0], y[1], y[2], y[3]);
+    for (int b = 0; b < kBatch; ++b) {
+      const float f = key_weight(token_of(b), live);
+      w0[b] = pack_bf16(f, f);
+      const float rest = f - bf16_lo(w0[b]);
+      w1[b] = pack_bf16(rest, rest);
+      mask[b] = token_of(b) < live ? 0xFFFFFFFFu : 0u;
     }
-    if (!WHOLE) {
 #pragma unroll
+    for (int n0 = 0; n0 < kUnits; n0 += kBatch) {
+      uint32_t x[kBatch][4];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        ld_shared_v4(stage + T::q + (n0 + b) * kThreadsHere * 16, x[b][0], x[b][1], x[b][2], x[b][3]);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k = x[b][i] & mask[b];
+          x[b][i] = bf16_fma2(k, w0[b], bf16_mul2(k, w1[b]));
+          if (EXACT) y[i] = bf16_fma2(k, w1[b], bf16_fma2(k, w0[b], x[b][i] ^ 0x80008000u));
+        }
+        if (EXACT) st_shared_v4(low + tid * 16 + (n0 + b) * kThreadsHere * 16, y[0], y[1], y[2], y[3]);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        st_shared_v4(stage + T::q + (n0 + b) * kThreadsHere * 16, x[b][0], x[b][1], x[b][2], x[b][3]);
+    }
+    if (live < kMixBlock) {
+#pragma unroll 1
       for (int n = 0; n < kMixBlock * DV / 8 / kThreadsHere; ++n)
         if (token_of(n) >= live) st_shared_v4(stage + T::q + T::k + n * kThreadsHere * 16, 0, 0, 0, 0);
     }
-  }
-  template <bool EXACT, bool TO_QUERIES>
-  DM_DEV void keys(int it, int live, uint32_t (&low)[EXACT && !TO_QUERIES ? kUnits * 4 : 1]) {
-    if (live == kMixBlock) decay_keys<EXACT, TO_QUERIES, true>(it, live, low);
-    else decay_keys<EXACT, TO_QUERIES, false>(it, live, low);
     announce(&sh->keys[it & 1]);
   }
+  DM_DEV bool block_done(int it) { return wait(&sh->block_state[it & 1], it >> 1); }
   // Block `it`, of `live` tokens, joins the state.
-  DM_DEV bool add_block(int it, int live, uint32_t from) {
-    if (!wait(&sh->block_state[it & 1], it >> 1)) return false;
+  DM_DEV void add_block(int live, uint32_t from) {
     tc_fence_after();
-    const float f = power()[live];
+    const float f = sh->power[live];
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(row & ~31) << 16) + from + col;
 #pragma unroll
@@ -599,7 +641,6 @@ struct StateRole {
     }
     if (row >= g.dk) zero();  // of keys past the head's size: 0 times an infinity of V may be there
     tc_fence_before();
-    return true;
   }
   DM_DEV bool loaded(int it) { return wait(&sh->full[it % T::stages], it / T::stages); }
   // The share of this round is in memory (or was not asked for): tell the cluster.
@@ -614,91 +655,67 @@ struct StateRole {
     return true;
   }
   DM_DEV bool all_arrived(int round) {
-    if (mbar_wait_cluster(&sh->shares, round & 1, &sh->abort)) return true;
-    raise_abort(g.err, &sh->abort);
-    return false;
+    return mbar_wait_cluster(&sh->shares, round & 1, &sh->abort) || gave_up(g.err, &sh->abort);
   }
   // This CTA's share, from the start of its last sequence or of its stretch: each block's keys while
   // the product of the block before runs.
-  template <bool EXACT>
   DM_DEV bool sum_share(const Round& r, int& it) {
     Cursor c = r.share;
-    uint32_t none[1];
     int before = 0;
+    zero();
+#pragma unroll 1
     for (int i = 0; i <= r.ahead; ++i, ++c.m) {
       int live = 0;
       if (i < r.ahead) {
         live = c.live(g);
         if (!loaded(it + i)) return false;
-        keys<EXACT, true>(it + i, live, none);
+        // the low parts go where queries would be
+        if (EXACT && !wait(&sh->q_full[(it + i) % T::stages], (it + i) / T::stages)) return false;
+        keys(it + i, live, smem_u32(smem) + ((it + i) % T::stages) * T::stage);
       }
-      if (i > 0 && !add_block(it + i - 1, before, ((it + i - 1) & 1) != 0 ? kColInner : kColState))
-        return false;
+      if (i > 0) {
+        if (!block_done(it + i - 1)) return false;
+        add_block(before, ((it + i - 1) & 1) != 0 ? kColOuter : kColState);
+      }
       before = live;
     }
     it += r.ahead;
     return true;
   }
-  template <bool EXACT>
+  DM_DEV bool sweep_block(const Cursor& c, int i, int it, int swept, int round, const Round& r) {
+    const int live = c.live(g);
+    if (i == 0 && g.split > 1 && !all_arrived(round)) return false;
+    if (c.m == 0 || (i == 0 && g.split > 1)) enter(c, round, r);
+    if (!loaded(it) || !wait(&sh->score, swept)) return false;
+    // exact: the low parts take the place of the state that entered the last block, and the one
+    // that enters this block theirs
+    if (EXACT && swept > 0 && !wait(&sh->out, swept - 1)) return false;
+    keys(it, live, smem_u32(entry));
+    if (lane == 0) mbar_arrive(&sh->clear);
+    if (EXACT ? !block_done(it) : swept > 0 && !wait(&sh->out, swept - 1)) return false;
+    write_entry();
+    if (!EXACT && !block_done(it)) return false;
+    add_block(live, kColState);
+    if (EXACT && g.state_out != nullptr && c.m + 1 == c.x.blocks) write_final(c.seq);
+    return true;
+  }
   DM_DEV void run() {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) full_weight[n] = key_weight(token_of(n), kMixBlock);
     zero();
-    const bool over = g.state_in != nullptr && g.state_in == g.state_out;
     int it = 0, swept = 0;
     bool ok = true;
     Round r = first_round(g, w);
+#pragma unroll 1
     for (int round = 0; ok && round < w.rounds; ++round) {
-      bool kept = false;
       if (r.ahead > 0) {
-        if (r.share.m == 0) {
-          read_initial(r.share.seq);
-          // another CTA may write the final state over it before this one's sweep is there
-          if (over) put(slot(w.rank, 2));
-          kept = over;
-        } else {
-          zero();
-        }
-        ok = sum_share<EXACT>(r, it);
+        if (over() && r.share.m == 0) keep_initial(r.share.seq);
+        ok = sum_share(r, it);
         put(slot(w.rank, round & 1));
       }
       if (g.split > 1) ok = arrive(round) && ok;
       Cursor c = r.at;
-      for (int i = 0; ok && i < r.n; ++i, c.skip(g, 1), ++it, ++swept) {
-        const int live = c.live(g);
-        uint32_t low[EXACT ? kUnits * 4 : 1];
-        ok = loaded(it) && wait(&sh->score, swept);
-        if (!ok) break;
-        keys<EXACT, false>(it, live, low);
-        if (i == 0 && g.split > 1) {
-          ok = all_arrived(round);
-          if (!ok) break;
-          if (c.m > 0) gather(c, round);
-        }
-        if (c.m == 0) {
-          if (kept && c.seq == r.share.seq) {
-            zero();
-            take(slot(w.rank, 2), 0.f);
-          } else {
-            read_initial(c.seq);
-          }
-        }
-        ok = swept == 0 || wait(&sh->out, swept - 1);
-        if (!ok) break;
-        write_entry();
-        if constexpr (EXACT) {
-          ok = wait(&sh->half, swept);
-          if (!ok) break;
-          const uint32_t k = smem_u32(smem) + (it % T::stages) * T::stage + T::q + tid * 16;
-#pragma unroll
-          for (int n = 0; n < kUnits; ++n)
-            st_shared_v4(k + n * kThreadsHere * 16, low[4 * n], low[4 * n + 1], low[4 * n + 2],
-                         low[4 * n + 3]);
-          announce(&sh->low);
-        }
-        ok = add_block(it, live, kColState);
-        if (g.state_out != nullptr && c.m + 1 == c.x.blocks) write_final(c.seq);
-      }
+#pragma unroll 1
+      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++it, ++swept)
+        ok = sweep_block(c, i, it, swept, round, r);
       if (r.n == 0 && g.split > 1) ok = ok && all_arrived(round);
       if (w.rank + 1 == g.split && round + 1 < w.rounds) put(slot(w.rank, (round + 1) & 1));
       next_round(g, w, r);
@@ -706,10 +723,13 @@ struct StateRole {
   }
   // Sequences without tokens: their states pass through.
   DM_DEV void pass_through(int first, int stride) {
+#pragma unroll 1
     for (int s = first; s < g.sequences; s += stride) {
       if (extent_of(g, s).blocks != 0) continue;
-      read_initial(s);
-      write_final(s);
+      const long long at = state_at(s);
+#pragma unroll 1
+      for (int i = tid; i < g.dk * g.dv; i += kThreadsHere)
+        g.state_out[at + i] = g.state_in == nullptr ? 0.f : g.out_scale * (g.in_scale * g.state_in[at + i]);
     }
   }
 };
@@ -732,18 +752,12 @@ struct WeighRole {
   template <bool AGAINST>
   DM_DEV void weigh(const float (&x)[32], int q, int j0, int live, F2 own, uint32_t (&p)[16]) {
     const int b = j0 >> 5;
-    if (b == q || (AGAINST && j0 + 32 > live)) {
-      const int row = q * 32 + lane;
-      const float* t = sh->power_ + 32 + (AGAINST ? j0 - row : row - j0);
-      // columns that row sees, a bit each
-      uint32_t see = b == q ? (AGAINST ? 0xFFFFFFFFu << lane : 0xFFFFFFFFu >> (31 - lane)) : 0xFFFFFFFFu;
-      if (AGAINST && j0 + 32 > live) see &= 0xFFFFFFFFu >> (j0 + 32 - live);
+    if (b == q) {
+      const float* t = sh->near_ + 32 + (AGAINST ? -lane : lane);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float u = x[2 * i] * t[AGAINST ? 2 * i : -2 * i];
-        const float v = x[2 * i + 1] * t[AGAINST ? 2 * i + 1 : -2 * i - 1];
-        p[i] = pack_bf16((see >> (2 * i) & 1) != 0 ? u : 0.f, (see >> (2 * i + 1) & 1) != 0 ? v : 0.f);
-      }
+      for (int i = 0; i < 16; ++i)
+        p[i] = pack_bf16(x[2 * i] * t[AGAINST ? 2 * i : -2 * i],
+                         x[2 * i + 1] * t[AGAINST ? 2 * i + 1 : -2 * i - 1]);
     } else {
       const int at = AGAINST ? 32 * (b - q) - 32 : 96 - 32 * (q - b);
       const float4* t = reinterpret_cast<const float4*>(sh->fall + at);
@@ -752,6 +766,17 @@ struct WeighRole {
         const float4 f = t[i];
         p[2 * i] = pack_bf16(mul2(mul2(f2(x[4 * i], x[4 * i + 1]), own), f2(f.x, f.y)));
         p[2 * i + 1] = pack_bf16(mul2(mul2(f2(x[4 * i + 2], x[4 * i + 3]), own), f2(f.z, f.w)));
+      }
+    }
+    if (b == q || (AGAINST && j0 + 32 > live)) {
+      // columns that the row sees, a bit each: whatever the others hold becomes 0
+      uint32_t see = b != q ? 0xFFFFFFFFu : AGAINST ? 0xFFFFFFFFu << lane : 0xFFFFFFFFu >> (31 - lane);
+      if (AGAINST && j0 + 32 > live) see &= 0xFFFFFFFFu >> (j0 + 32 - live);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        // two bits to a mask of two halves
+        const uint32_t two = see >> (2 * i) & 3u;
+        p[i] &= (two & 1u) * 0xFFFFu + (two >> 1) * 0xFFFF0000u;
       }
     }
   }
@@ -786,12 +811,12 @@ struct WeighRole {
   DM_DEV void run() {
     int swept = 0;
     bool ok = true;
-    const float f = sh->power_[32 + (g.against ? 31 - lane : lane)];
+    const float f = g.scale * sh->power[g.against ? 31 - lane : lane];
     const F2 own = f2(f, f);
     Round r = first_round(g, w);
     for (int round = 0; ok && round < w.rounds; ++round) {
       Cursor c = r.at;
-      for (int i = 0; ok && i < r.n; ++i, c.skip(g, 1), ++swept) {
+      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++swept) {
         const int live = c.live(g);
         ok = g.against ? block<true>(live, swept, own) : block<false>(live, swept, own);
       }
@@ -801,7 +826,7 @@ struct WeighRole {
 };
 
 // ------------------------------------------------------------------ outputs
-// Thread (warp w, lane) has row 32 w + lane.
+// Thread (warp w, lane) has row 32 w + lane.  The weighted scores carry the scale already.
 template <int DK, int DV>
 struct OutRole {
   using T = Tiles<DK, DV>;
@@ -812,10 +837,17 @@ struct OutRole {
   int head, warp, lane;
 
   DM_DEV bool wait(uint64_t* bar, int n) { return await(bar, n & 1, g.err, &sh->abort); }
+  // The store of the last block has left stage s.
+  DM_DEV void release(int s) {
+    if (lane == 0) {
+      bulk_wait_read<0>();
+      mbar_arrive(&sh->q_empty[s]);
+    }
+  }
   DM_DEV bool block(int row0, int live, int it, int swept) {
     const int row = warp * 32 + lane, s = it % T::stages;
-    const float f = row < live ? sh->power_[32 + (g.against ? live - 1 - row : row + 1)] : 0.f;
-    const F2 fs = f2(f * g.scale, f * g.scale), ss = f2(g.scale, g.scale);
+    const float f = row < live ? g.scale * sh->power[g.against ? live - 1 - row : row + 1] : 0.f;
+    const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(warp * 32) << 16);
     // 32 columns to a piece of 2 KB, rows of 64 bytes
     const uint32_t tile = smem_u32(smem) + s * T::stage + warp * (DV / 32) * 2048 + lane * 64;
@@ -830,7 +862,7 @@ struct OutRole {
       uint32_t o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        o[e] = pack_bf16(fma2(fs, f2(y[2 * e], y[2 * e + 1]), mul2(ss, f2(x[2 * e], x[2 * e + 1]))));
+        o[e] = pack_bf16(fma2(ff, f2(y[2 * e], y[2 * e + 1]), f2(x[2 * e], x[2 * e + 1])));
       const uint32_t to = tile + (n >> 1) * 2048;
       const int swizzle = (lane >> 1) & 3;
       st_shared_v4(to + (((2 * (n & 1)) ^ swizzle) << 4), o[0], o[1], o[2], o[3]);
@@ -849,12 +881,12 @@ struct OutRole {
         for (int n = 0; n < DV / 32; ++n)
           if (n * 32 < g.dv) tma_store_3d(&g.o, tile + n * 2048, n * 32, head, first);
         bulk_commit();
-        bulk_wait_read<0>();
       }
     } else {
       // the end of a sequence: what lies behind it is not this one's to write
       __syncwarp();
       const uint32_t base = tile - lane * 64;
+#pragma unroll 1
       for (int u = lane; u < 32 * (DV / 8); u += 32) {
         const int r = u / (DV / 8), n = u % (DV / 8);
         if (r < rows && n * 8 < g.dv) {
@@ -866,8 +898,7 @@ struct OutRole {
       }
       __syncwarp();
     }
-    if (lane == 0) mbar_arrive(&sh->empty[s]);
-    __syncwarp();
+    release(s);
     return true;
   }
   DM_DEV void run() {
@@ -877,7 +908,7 @@ struct OutRole {
     for (int round = 0; ok && round < w.rounds; ++round) {
       it += r.ahead;
       Cursor c = r.at;
-      for (int i = 0; ok && i < r.n; ++i, c.skip(g, 1), ++it, ++swept)
+      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++it, ++swept)
         ok = block(c.row(g), c.live(g), it, swept);
       next_round(g, w, r);
     }
@@ -886,22 +917,28 @@ struct OutRole {
   }
 };
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant__ LinAttnArgs g) {
+template <int DK, int DV, bool EXACT>
+__global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant__ LinAttnSweeps sweeps) {
   extern __shared__ uint8_t smem_raw[];
   using T = Tiles<DK, DV>;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* state = smem + T::stages * T::stage;
-  Shared* sh = reinterpret_cast<Shared*>(state + T::state);
+  // the state's tile, the stages (of which products read when they run past that tile's end), the rest
+  uint8_t* state = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint8_t* smem = state + T::state;
+  Shared* sh = reinterpret_cast<Shared*>(smem + T::stages * T::stage);
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
-  const int cluster = int(blockIdx.x) / g.split, rank = int(blockIdx.x) - cluster * g.split;
-  const int group = cluster / g.heads, head = cluster - group * g.heads;
+  const int split = sweeps.sweep[0].split;
+  const int cluster = int(blockIdx.x) / split, rank = int(blockIdx.x) - cluster * split;
+  const int of_sweep = sweeps.sweep[0].groups * sweeps.sweep[0].heads;
+  const LinAttnArgs& g = sweeps.sweep[cluster / of_sweep];
+  const int group = cluster % of_sweep / g.heads, head = cluster % of_sweep - group * g.heads;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], kOutWarps + 1);
+      mbar_init(&sh->empty[s], 2);
+      mbar_init(&sh->q_full[s], 1);
+      mbar_init(&sh->q_empty[s], kOutWarps);
     }
     mbar_init(&sh->score, 1);
     mbar_init(&sh->weighted, kWeighWarps);
@@ -912,8 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
       mbar_init(&sh->block_state[i], 1);
     }
     mbar_init(&sh->put, kStateWarps);
-    mbar_init(&sh->half, 1);
-    mbar_init(&sh->low, kStateWarps);
+    mbar_init(&sh->clear, kStateWarps);
     mbar_init(&sh->entry, kStateWarps);
     mbar_init(&sh->out, 1);
     mbar_init(&sh->shares, uint32_t(g.split));
@@ -934,12 +970,18 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   grid_wait();
   grid_launch_dependents();
   const float log_decay = g.log_decay[head];
-  if (threadIdx.x < 32 + kMixBlock + 1) {
-    const int n = int(threadIdx.x) - 32;
-    sh->power_[threadIdx.x] = n < 0 ? 0.f : n == 0 ? 1.f : expf(log_decay * float(n));
+  {
+    const int t = int(threadIdx.x);
+    if (t <= kMixBlock) {
+      sh->power[t] = t == 0 ? 1.f : expf(log_decay * float(t));
+    } else if (t < kMixBlock + 1 + 64) {
+      const int n = t - kMixBlock - 1 - 32;
+      sh->near_[n + 32] = n < 0 ? 0.f : g.scale * (n == 0 ? 1.f : expf(log_decay * float(n)));
+    } else if (t < kMixBlock + 1 + 64 + 96) {
+      const int n = t - kMixBlock - 1 - 64;
+      sh->fall[n] = expf(log_decay * float(g.against ? n + 1 : 96 - n));
+    }
   }
-  if (threadIdx.x < 96)
-    sh->fall[threadIdx.x] = expf(log_decay * float(g.against ? threadIdx.x + 1 : 96 - threadIdx.x));
   const Work w = g.sequences <= 32 ? locate_few(g, group, rank) : locate(g, group, rank, sh);
   tc_fence_before();
   __syncthreads();
@@ -947,12 +989,11 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
 
   if (warp < kStateWarps) {
     regs_inc<kStateRegs>();
-    StateRole<DK, DV> r{g, w, sh, smem, state, log_decay, head, cluster, int(threadIdx.x),
-                        int(threadIdx.x & 31), int((warp & 3) * 32 + (threadIdx.x & 31)),
-                        int(warp >> 2) * (DV / 2)};
-    if (g.exact) r.template run<true>();
-    else r.template run<false>();
-    if (g.state_out != nullptr) r.pass_through(group * g.split + rank, g.groups * g.split);
+    StateRole<DK, DV, EXACT> r{g, w, sh, smem, state, log_decay, head, cluster, int(threadIdx.x),
+                               int(threadIdx.x & 31), int((warp & 3) * 32 + (threadIdx.x & 31)),
+                               int(warp >> 2) * (DV / 2)};
+    r.run();
+    if (EXACT && g.state_out != nullptr) r.pass_through(group * g.split + rank, g.groups * g.split);
   } else if (warp < kOutWarp) {
     regs_dec<kWeighRegs>();
     WeighRole r{g, w, sh, warp - kWeighWarp, int(threadIdx.x & 31)};
@@ -964,7 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   } else {
     regs_dec<kOtherRegs>();
     if (warp == kLoadWarp && elect_one()) load_role<DK, DV>(g, w, head, smem, sh);
-    if (warp == kMmaWarp && elect_one()) mma_role<DK, DV>(g, w, smem, state, sh);
+    if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(g, w, smem, state, sh);
+    if (warp == kMmaWarp && elect_one()) out_mma_role<DK, DV>(g, w, smem, state, sh);
     __syncwarp();
   }
   __syncthreads();
@@ -983,22 +1025,23 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   if (g.split > 1) cluster_sync();  // no CTA leaves while another may still arrive on its barrier
 }
 
-using MixKernel = void (*)(LinAttnArgs);
-MixKernel kernel_for(int dk, int dv, int* smem) {
-  if (dk <= 64) {
-    *smem = dv <= 64 ? Tiles<64, 64>::bytes : Tiles<64, 128>::bytes;
-    return dv <= 64 ? mix_kernel<64, 64> : mix_kernel<64, 128>;
-  }
-  *smem = dv <= 64 ? Tiles<128, 64>::bytes : Tiles<128, 128>::bytes;
-  return dv <= 64 ? mix_kernel<128, 64> : mix_kernel<128, 128>;
+using MixKernel = void (*)(LinAttnSweeps);
+template <int DK, int DV>
+MixKernel kernel_of(bool exact, int* smem) {
+  *smem = Tiles<DK, DV>::bytes;
+  return exact ? mix_kernel<DK, DV, true> : mix_kernel<DK, DV, false>;
+}
+MixKernel kernel_for(int dk, int dv, bool exact, int* smem) {
+  if (dk <= 64) return dv <= 64 ? kernel_of<64, 64>(exact, smem) : kernel_of<64, 128>(exact, smem);
+  return dv <= 64 ? kernel_of<128, 64>(exact, smem) : kernel_of<128, 128>(exact, smem);
 }
 
 }  // namespace
 
 cudaError_t linattn_prepare() {
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     int smem = 0;
-    const MixKernel k = kernel_for(i & 1 ? 128 : 64, i & 2 ? 128 : 64, &smem);
+    const MixKernel k = kernel_for(i & 1 ? 128 : 64, i & 2 ? 128 : 64, (i & 4) != 0, &smem);
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     cudaFuncAttributes a{};
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k);
@@ -1009,11 +1052,12 @@ cudaError_t linattn_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t launch_linattn(const LinAttnArgs& g, cudaStream_t s) {
+cudaError_t launch_linattn(const LinAttnSweeps& g, int sweeps, cudaStream_t s) {
+  const LinAttnArgs& one = g.sweep[0];
   int smem = 0;
-  const MixKernel k = kernel_for(g.dk, g.dv, &smem);
+  const MixKernel k = kernel_for(one.dk, one.dv, one.exact != 0, &smem);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(g.groups * g.heads * g.split), 1, 1);
+  cfg.gridDim = dim3(unsigned(sweeps * one.groups * one.heads * one.split), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = s;
@@ -1021,11 +1065,11 @@ cudaError_t launch_linattn(const LinAttnArgs& g, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(g.split);
+  attr[1].val.clusterDim.x = unsigned(one.split);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = g.split > 1 ? 2 : 1;
+  cfg.numAttrs = one.split > 1 ? 2 : 1;
   return counted(cudaLaunchKernelEx(&cfg, k, g));
 }
 

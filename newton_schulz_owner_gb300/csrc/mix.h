@@ -64,7 +64,11 @@ constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a state
 constexpr int kMixSlots = 3;            // states of a CTA in the workspace
 constexpr int64_t kMixMaxCtas = 320;    // of a launch whose sequences are shared
 cudaError_t linattn_prepare();  // once per device
-cudaError_t launch_linattn(const LinAttnArgs& g, cudaStream_t s);
+// Sweeps of one launch: of the same sizes (padded to 64 or 128), sharing and precision.
+struct LinAttnSweeps {
+  LinAttnArgs sweep[3];
+};
+cudaError_t launch_linattn(const LinAttnSweeps& g, int sweeps, cudaStream_t s);
 
 struct LinStepArgs {
   Heads q, k, v, out;

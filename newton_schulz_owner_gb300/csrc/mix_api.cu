@@ -194,43 +194,49 @@ bool linattn_shape_ok(const dmuon_linattn_shape* s) {
 struct Share {
   int groups, split;
 };
-Share choose_share(const dmuon_linattn_shape& s, int sms) {
+// Microseconds, measured with 128 elements to a head: a block takes 3 (exact states 3.8), 1.5 more
+// (2) where a CTA sums its share ahead; a launch 6, an exchange of shares 5 (8192 tokens of 32 heads:
+// 97 with four CTAs to a head, 205 with one).
+Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, int sms) {
   const int64_t blocks = s.tokens / kMixBlock + std::min(s.sequences, s.tokens);  // at most
+  const double sweep = exact ? 3.8 : 3.0, ahead = exact ? 2.0 : 1.5;
   Share best{1, 1};
   double least = 0;
   for (int64_t groups = 1; groups <= s.sequences && groups <= 64; ++groups) {
     for (int split = 1; split <= kMixMaxSplit; ++split) {
-      const int64_t ctas = s.heads * groups * split;
+      const int64_t ctas = sweeps * s.heads * groups * split;
       if (groups * split > blocks && groups * split > 1) break;
       if (split > 1 && ctas > kMixMaxCtas) break;
       // clusters end where sequences do: the largest has about a sequence more than its part
       const double part = double(blocks) / groups + (groups > 1 ? double(blocks) / s.sequences : 0.0);
       const double cost = double(ceil_div(ctas, sms)) *
-                          (std::ceil(part / split) * (split > 1 ? 1.5 : 1.0) + 2);
+                          (std::ceil(part / split) * (sweep + (split > 1 ? ahead : 0.0)) + 6 +
+                           (split > 1 ? 5 : 0));
       if (least == 0 || cost < least) {
         best = {int(groups), split};
         least = cost;
       }
     }
-    if (s.heads * groups >= sms) break;
+    if (sweeps * s.heads * groups >= sms) break;
   }
   return best;
 }
 // The workspace serves any way to share any number of tokens and sequences up to the shape's.
 size_t linattn_workspace(const dmuon_linattn_shape& s) {
-  const int64_t ctas = std::min(s.sequences * s.heads * kMixMaxSplit, kMixMaxCtas);
+  const int64_t ctas = std::min(3 * s.sequences * s.heads * kMixMaxSplit, kMixMaxCtas);
   return kHdrBytes + size_t(ctas) * kMixSlots * kMixLocalBytes;
 }
 
-bool tile_map(CUtensorMap* m, const Rows& r, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+bool tile_map(CUtensorMap* m, const Rows& r, bool output = false) {
   const TensorMapEncode enc = library_tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {cuuint64_t(r.dim), cuuint64_t(r.heads), cuuint64_t(r.tokens)};
   const cuuint64_t strides[2] = {cuuint64_t(r.hs) * 2, cuuint64_t(r.ts) * 2};
-  const cuuint32_t box[3] = {cuuint32_t(box_cols), 1, cuuint32_t(box_rows)}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {output ? 32u : 64u, 1, output ? 32u : unsigned(kMixBlock)}, es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, reinterpret_cast<void*>(r.p), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             output ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // One sweep: out of (q, k, v), key width q.dim, value width v.dim.
@@ -242,36 +248,40 @@ struct Sweep {
   bool transposed;  // the caller's state is (value, key)
   float in_scale, out_scale;
 };
-int run_sweep(const dmuon_linattn_shape& s, const Sweep& w, const float* log_decay,
-              const int32_t* offsets, Share share, void* ws, cudaStream_t st) {
-  LinAttnArgs g{};
-  if (!tile_map(&g.q, *w.q, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tile_map(&g.k, *w.k, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tile_map(&g.v, *w.v, 64, kMixBlock, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tile_map(&g.o, *w.out, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-    return DMUON_ERR_CUDA;
-  g.log_decay = log_decay;
-  g.offsets = offsets;
-  g.sequences = int(s.sequences);
-  g.heads = int(s.heads);
-  g.tokens = int(s.tokens);
-  g.dk = int(w.q->dim);
-  g.dv = int(w.v->dim);
-  g.scale = s.scale;
-  g.against = w.against;
-  g.state_in = w.state_in;
-  g.state_out = w.state_out;
-  g.in_scale = w.in_scale;
-  g.out_scale = w.out_scale;
-  g.st_row = w.transposed ? 1 : g.dv;
-  g.st_col = w.transposed ? g.dk : 1;
-  g.out = device_heads(*w.out);
-  g.groups = share.groups;
-  g.split = share.split;
-  g.exact = w.state_out != nullptr;
-  g.err = static_cast<int*>(ws);
-  g.local = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHdrBytes);
-  return launch_linattn(g, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
+int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const float* log_decay,
+               const int32_t* offsets, int sms, void* ws, cudaStream_t st) {
+  bool exact = false;
+  for (int i = 0; i < sweeps; ++i) exact = exact || w[i].state_out != nullptr;
+  const Share share = choose_share(s, sweeps, exact, sms);
+  LinAttnSweeps all{};
+  for (int i = 0; i < sweeps; ++i, ++w) {
+    LinAttnArgs& g = all.sweep[i];
+    if (!tile_map(&g.q, *w->q) || !tile_map(&g.k, *w->k) || !tile_map(&g.v, *w->v) ||
+        !tile_map(&g.o, *w->out, true))
+      return DMUON_ERR_CUDA;
+    g.log_decay = log_decay;
+    g.offsets = offsets;
+    g.sequences = int(s.sequences);
+    g.heads = int(s.heads);
+    g.tokens = int(s.tokens);
+    g.dk = int(w->q->dim);
+    g.dv = int(w->v->dim);
+    g.scale = s.scale;
+    g.against = w->against;
+    g.state_in = w->state_in;
+    g.state_out = w->state_out;
+    g.in_scale = w->in_scale;
+    g.out_scale = w->out_scale;
+    g.st_row = w->transposed ? 1 : g.dv;
+    g.st_col = w->transposed ? g.dk : 1;
+    g.out = device_heads(*w->out);
+    g.groups = share.groups;
+    g.split = share.split;
+    g.exact = exact;
+    g.err = static_cast<int*>(ws);
+    g.local = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHdrBytes);
+  }
+  return launch_linattn(all, sweeps, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
 }
 
 // Rows of a tensor of the call, checked; `status` keeps the first failure.
@@ -362,7 +372,7 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
   e = device_ready(&sms);
   if (e != DMUON_OK) return e;
   const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, 1.f, 1.f};
-  return run_sweep(s, w, log_decay, offsets, choose_share(s, sms), workspace, stream);
+  return run_sweeps(s, &w, 1, log_decay, offsets, sms, workspace, stream);
 }
 
 int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* dout,
@@ -396,18 +406,19 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
   int sms = 0;
   e = device_ready(&sms);
   if (e != DMUON_OK) return e;
-  const Share share = choose_share(s, sms);
   const float inv = 1.f / s.scale;
-  // dk reads dfinal_state before dv's sweep may write dstate over it
   const Sweep sweeps[3] = {
       {&dor, &vr, &kr, &dqr, false, state, nullptr, true, 1.f, 1.f},
       {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, inv, 1.f},
       {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, inv, s.scale}};
-  for (int i = s.tokens > 0 ? 0 : 2; i < 3; ++i) {
-    e = run_sweep(s, sweeps[i], log_decay, offsets, share, workspace, stream);
-    if (e != DMUON_OK) return e;
-  }
-  return DMUON_OK;
+  if (s.tokens == 0) return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, sms, workspace, stream);
+  // The three side by side fill the GPU without cutting sequences as finely (8192 tokens of 32 heads:
+  // 285 us one after another, 204 together).  Apart where dv's sweep is another kernel, or writes
+  // dstate, perhaps over the dfinal_state that dk's reads.
+  const bool apart = dstate != nullptr || (s.key_dim <= 64) != (s.value_dim <= 64);
+  e = run_sweeps(s, sweeps, apart ? 2 : 3, log_decay, offsets, sms, workspace, stream);
+  if (e != DMUON_OK || !apart) return e;
+  return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, sms, workspace, stream);
 }
 
 int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,

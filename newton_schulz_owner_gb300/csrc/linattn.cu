@@ -34,11 +34,12 @@
 namespace dm {
 namespace {
 
-// Warps: states, weighted scores, outputs, loads and products (one of the last four idles: register
-// shares are given to whole warpgroups).
+// Warps: states, weighted scores, outputs, then loads and two that issue products (one of the last
+// four idles: register shares are given to whole warpgroups).
 constexpr int kStateWarps = 8, kWeighWarps = 8, kOutWarps = 4, kOtherWarps = 4;
 constexpr int kWeighWarp = kStateWarps, kOutWarp = kWeighWarp + kWeighWarps;
-constexpr int kLoadWarp = kOutWarp + kOutWarps, kStateMmaWarp = kLoadWarp + 1, kMmaWarp = kLoadWarp + 2;
+constexpr int kLoadWarp = kOutWarp + kOutWarps, kStateMmaWarp = kLoadWarp + 1,
+              kOutMmaWarp = kLoadWarp + 2;
 constexpr int kThreads = (kStateWarps + kWeighWarps + kOutWarps + kOtherWarps) * 32;
 // Registers of a thread at launch, and what each kind takes: the shares add up to what the block
 // was launched with.
@@ -73,12 +74,11 @@ struct Shared {
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];  // its queries; its output has left their place
   uint64_t score;              // scores in TMEM
   uint64_t weighted;           // weighted scores in TMEM
-  uint64_t keys[2];            // keys decayed, rows past the end cleared: of even and odd blocks, as
-                               // the states' warps may be one ahead of the products there
-  uint64_t clear;              // the same of the sweep's blocks, for the other products
-  uint64_t block_state[2];     // the block's state in TMEM
+  uint64_t spent;              // and read
+  uint64_t keys;               // keys decayed, rows past the end cleared
+  uint64_t clear;              // the same of the sweep's blocks, for the output's products
+  uint64_t block_state;        // the block's state in TMEM
   uint64_t entry;              // the entering state in shared memory
-  uint64_t spent;              // weighted scores read
   uint64_t out;                // both parts of the output in TMEM
   uint64_t taken;              // and out of it again
   uint64_t put;                // this CTA's share of the round in memory
@@ -345,14 +345,13 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
 }
 
 // ------------------------------------------------------------------ products
-// Two threads issue them, as issuing (about 75 cycles a product of 16 K-elements) takes as long as
-// computing: one the blocks' own states, one the rest.
+// Two threads issue them, as issuing takes about as long as computing: one the blocks' own states,
+// one the rest.
 template <int DK, int DV, bool EXACT>
 DM_DEV void state_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state,
                            Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
-  const uint32_t tmem = sh->tmem;
   constexpr uint32_t id = idesc_bf16(128, DV, true, true);
   // (a^..k)^T V, rows of K in steps of 16 tokens.  With 64 key elements the upper half of the
   // 128 rows reads what follows the tile; those lanes of the result are not used.
@@ -362,29 +361,25 @@ DM_DEV void state_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, u
     for (int j = 0; j < 8; ++j)
       umma_bf16(to, a + uint64_t(j) * 128, b + uint64_t(j) * 128, id, accumulate || j > 0);
   };
-  int it = 0, swept = 0;
+  int it = 0;
   Round r = first_round(g, w);
   for (int round = 0; round < w.rounds; ++round) {
-    // the last output of the round before, read by then, makes room for every other share
-    if (r.ahead > 0 && swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
     for (int i = 0; i < r.ahead + r.n; ++i, ++it) {
       const bool share = i < r.ahead;
       const int s = it % T::stages;
       const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
       if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
-      if (!await(&sh->keys[it & 1], it >> 1 & 1, g.err, flag)) return;
+      if (!await(&sh->keys, it & 1, g.err, flag)) return;  // the last block's state is added by then
       tc_fence_after();
-      const uint32_t to = tmem + (share && (it & 1) != 0 ? kColOuter : kColState);
+      const uint32_t to = sh->tmem + kColState;
       product(to, k, v, false);
       // the keys' low parts lie where queries would, or the state that enters will
       if (EXACT) product(to, share ? q : smem_u32(state), v, true);
-      umma_commit(&sh->block_state[it & 1]);
+      umma_commit(&sh->block_state);
       umma_commit(&sh->empty[s]);
       if (share) {  // in the place of the output's warps
 #pragma unroll
         for (int n = 0; n < kOutWarps; ++n) umma_commit(&sh->q_empty[s]);
-      } else {
-        ++swept;
       }
     }
     next_round(g, w, r);
@@ -398,27 +393,24 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uin
   const uint32_t tmem = sh->tmem;
   constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
   constexpr uint32_t id_out = idesc_bf16(128, DV, false, true);
+  const uint64_t ed = sdesc_sw128(smem_u32(state), DK * 128, 1024);
   int it = 0, swept = 0;
   Round r = first_round(g, w);
   for (int round = 0; round < w.rounds; ++round) {
-    // a stage's loads are waited for in turn, whatever they are for: no wait misses a phase
-    for (int i = 0; i < r.ahead; ++i, ++it) {
-      const int s = it % T::stages;
-      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
-      if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
-      mbar_arrive(&sh->empty[s]);
-    }
-    for (int i = 0; i < r.n; ++i, ++it, ++swept) {
+    for (int i = 0; i < r.ahead + r.n; ++i, ++it) {
       const int s = it % T::stages;
       const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
-      const uint64_t qd = sdesc_sw128(q, 16, 1024);
+      const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
       if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
       if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
-      // the last block's weighted scores have been read (no order is promised between products
-      // of unlike shape); its output is on its way meanwhile
+      if (i < r.ahead) {
+        mbar_arrive(&sh->empty[s]);  // waited for all the same: a wait misses no phase
+        continue;
+      }
+      // the last block's weighted scores have been read (no order is promised between products of
+      // unlike shape)
       if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return;
       tc_fence_after();
-      const uint64_t kd = sdesc_sw128(k, 16, 1024);
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j) {
         const uint64_t at = uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2;
@@ -438,12 +430,12 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uin
       umma_commit(&sh->empty[s]);
       if (!await(&sh->entry, swept & 1, g.err, flag)) return;
       tc_fence_after();
-      const uint64_t ed = sdesc_sw128(smem_u32(state), DK * 128, 1024);
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j)
         umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
                   ed + uint64_t(j) * 128, id_out, j > 0);
       umma_commit(&sh->out);
+      ++swept;
     }
     next_round(g, w, r);
   }
@@ -622,15 +614,15 @@ struct StateRole {
       for (int n = 0; n < kMixBlock * DV / 8 / kThreadsHere; ++n)
         if (token_of(n) >= live) st_shared_v4(stage + T::q + T::k + n * kThreadsHere * 16, 0, 0, 0, 0);
     }
-    announce(&sh->keys[it & 1]);
+    announce(&sh->keys);
   }
-  DM_DEV bool block_done(int it) { return wait(&sh->block_state[it & 1], it >> 1); }
+  DM_DEV bool block_done(int it) { return wait(&sh->block_state, it); }
   // Block `it`, of `live` tokens, joins the state.
-  DM_DEV void add_block(int live, uint32_t from) {
+  DM_DEV void add_block(int live) {
     tc_fence_after();
     const float f = sh->power[live];
     const F2 ff = f2(f, f);
-    const uint32_t at = sh->tmem + (uint32_t(row & ~31) << 16) + from + col;
+    const uint32_t at = sh->tmem + (uint32_t(row & ~31) << 16) + kColState + col;
 #pragma unroll
     for (int c = 0; c < kCols / 16; ++c) {
       float x[16];
@@ -657,29 +649,19 @@ struct StateRole {
   DM_DEV bool all_arrived(int round) {
     return mbar_wait_cluster(&sh->shares, round & 1, &sh->abort) || gave_up(g.err, &sh->abort);
   }
-  // This CTA's share, from the start of its last sequence or of its stretch: each block's keys while
-  // the product of the block before runs.
+  // This CTA's share, from the start of its last sequence or of its stretch.
   DM_DEV bool sum_share(const Round& r, int& it) {
     Cursor c = r.share;
-    int before = 0;
     zero();
 #pragma unroll 1
-    for (int i = 0; i <= r.ahead; ++i, ++c.m) {
-      int live = 0;
-      if (i < r.ahead) {
-        live = c.live(g);
-        if (!loaded(it + i)) return false;
-        // the low parts go where queries would be
-        if (EXACT && !wait(&sh->q_full[(it + i) % T::stages], (it + i) / T::stages)) return false;
-        keys(it + i, live, smem_u32(smem) + ((it + i) % T::stages) * T::stage);
-      }
-      if (i > 0) {
-        if (!block_done(it + i - 1)) return false;
-        add_block(before, ((it + i - 1) & 1) != 0 ? kColOuter : kColState);
-      }
-      before = live;
+    for (int i = 0; i < r.ahead; ++i, ++c.m, ++it) {
+      const int live = c.live(g), s = it % T::stages;
+      // the low parts go where queries would be, once the output before them has left
+      if (!loaded(it) || !wait(&sh->q_full[s], it / T::stages)) return false;
+      keys(it, live, smem_u32(smem) + s * T::stage);
+      if (!block_done(it)) return false;
+      add_block(live);
     }
-    it += r.ahead;
     return true;
   }
   DM_DEV bool sweep_block(const Cursor& c, int i, int it, int swept, int round, const Round& r) {
@@ -695,7 +677,7 @@ struct StateRole {
     if (EXACT ? !block_done(it) : swept > 0 && !wait(&sh->out, swept - 1)) return false;
     write_entry();
     if (!EXACT && !block_done(it)) return false;
-    add_block(live, kColState);
+    add_block(live);
     if (EXACT && g.state_out != nullptr && c.m + 1 == c.x.blocks) write_final(c.seq);
     return true;
   }
@@ -940,23 +922,21 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
       mbar_init(&sh->q_full[s], 1);
       mbar_init(&sh->q_empty[s], kOutWarps);
     }
+    mbar_init(&sh->keys, kStateWarps);
+    mbar_init(&sh->block_state, 1);
     mbar_init(&sh->score, 1);
     mbar_init(&sh->weighted, kWeighWarps);
     mbar_init(&sh->spent, 1);
-    mbar_init(&sh->taken, kOutWarps);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->keys[i], kStateWarps);
-      mbar_init(&sh->block_state[i], 1);
-    }
-    mbar_init(&sh->put, kStateWarps);
     mbar_init(&sh->clear, kStateWarps);
     mbar_init(&sh->entry, kStateWarps);
     mbar_init(&sh->out, 1);
+    mbar_init(&sh->taken, kOutWarps);
+    mbar_init(&sh->put, kStateWarps);
     mbar_init(&sh->shares, uint32_t(g.split));
     sh->abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kOutMmaWarp) {
     tmem_alloc(&sh->tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -1006,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     regs_dec<kOtherRegs>();
     if (warp == kLoadWarp && elect_one()) load_role<DK, DV>(g, w, head, smem, sh);
     if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(g, w, smem, state, sh);
-    if (warp == kMmaWarp && elect_one()) out_mma_role<DK, DV>(g, w, smem, state, sh);
+    if (warp == kOutMmaWarp && elect_one()) out_mma_role<DK, DV>(g, w, smem, state, sh);
     __syncwarp();
   }
   __syncthreads();
@@ -1018,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kOutMmaWarp) {
     tc_fence_after();
     tmem_dealloc(sh->tmem, kTmemCols);
   }

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -119,7 +120,7 @@ _lib.dmuon_xent_workspace_bytes.restype = _sz
 _lib.dmuon_xent.argtypes = [_XentP, _vp, _int64, _vp, _vp, _vp, _vp, _vp, _vp, _int64, _vp, _vp, _sz,
                             _vp]
 _lib.dmuon_xent.restype = _i
-# a dmuon_heads is three 64-bit words; a call's tensors are passed from one array of them
+# a dmuon_heads goes by the bytes of its three 64-bit words
 _lib.dmuon_qk_norm_rope.argtypes = [_vp] * 9 + [_vp]
 _lib.dmuon_qk_norm_rope.restype = _i
 _lib.dmuon_qk_norm_rope_workspace_bytes.argtypes = [_vp]
@@ -652,21 +653,29 @@ class LinearXent:
 
 
 # ------------------------------------------------------------------ token mixing
-_HEADS = {n: ctypes.c_int64 * (3 * n) for n in (4, 6, 7)}      # n dmuon_heads
+_pack_heads = struct.Struct("3q").pack
+_BF16 = torch.bfloat16
 
 
-def _heads(t: torch.Tensor, shape, what: str, dev: int):
-    """Check a (tokens, heads, dim) bf16 tensor on device `dev`; the words of its dmuon_heads."""
-    if t.dtype != torch.bfloat16:
+def _heads(t: torch.Tensor, shape, what: str, dev: int) -> bytes:
+    """Check a (tokens, heads, dim) bf16 tensor on device `dev`; its dmuon_heads."""
+    token, head, unit = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is _BF16 and unit == 1 and t.get_device() == dev and t.shape == shape:
+        return _pack_heads(t.data_ptr(), token, head)
+    if t.dtype != _BF16:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}: expected bfloat16")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise _elsewhere(t, dev, what)
-    token, head, unit = t.stride()
-    if unit != 1:
-        raise ValueError(f"{what}: the elements of a head must be contiguous")
-    return t.data_ptr(), token, head
+    raise ValueError(f"{what}: the elements of a head must be contiguous")
+
+
+def _flat(t: torch.Tensor, dtype, shape, what: str, dev: int) -> int:
+    """_dense, with one test where all is well."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _dense(t, dtype, shape, what, dev)
 
 
 class QKNormRope:
@@ -686,6 +695,7 @@ class QKNormRope:
         self.head_dim = int(head_dim)
         self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
         self.eps, self.interleaved, self.with_backward = float(eps), bool(interleaved), bool(backward)
+        self._last = (-1,)
         shape = self._shape(self.max_tokens)
         nbytes = int(_lib.dmuon_qk_norm_rope_workspace_bytes(ctypes.byref(shape)))
         if nbytes == 0:
@@ -704,33 +714,37 @@ class QKNormRope:
             raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.q_heads}, "
                              f"{self.head_dim}), got {tuple(q.shape)}")
         dev = _launch_device(self.workspace, "the workspace")
-        return t, dev, (t, self.q_heads, self.head_dim), (t, self.k_heads, self.head_dim)
+        last = self._last          # shapes of the last number of tokens
+        if last[0] != t:
+            last = self._last = (t, self._shape(t), (t, self.q_heads, self.head_dim),
+                                 (t, self.k_heads, self.head_dim))
+        return last + (dev,)
 
     def _key(self, k, shape, what, dev):
         if self.k_heads == 0:
             if k is not None:
                 raise ValueError(f"{what}: expected None without key heads")
-            return 0, 0, 0
+            return None
         return _heads(k, shape, what, dev)
 
     def _rest(self, w_q, w_k, inv_freq, position, t, dev):
         d = self.head_dim
-        wq = None if w_q is None else _dense(w_q, torch.bfloat16, (d,), "w_q", dev)
-        wk = None if w_k is None else _dense(w_k, torch.bfloat16, (d,), "w_k", dev)
+        wq = None if w_q is None else _flat(w_q, torch.bfloat16, (d,), "w_q", dev)
+        wk = None if w_k is None else _flat(w_k, torch.bfloat16, (d,), "w_k", dev)
         if self.rotary_dim == 0:
             return wq, wk, None, None
-        return (wq, wk, _dense(inv_freq, torch.float32, (self.rotary_dim // 2,), "inv_freq", dev),
-                _dense(position, torch.int32, (t,), "position", dev))
+        return (wq, wk, _flat(inv_freq, torch.float32, (self.rotary_dim // 2,), "inv_freq", dev),
+                _flat(position, torch.int32, (t,), "position", dev))
 
     def forward(self, q, k, w_q, w_k, inv_freq, position, q_out, k_out, stream=None) -> None:
         """q_out, k_out <- the normalised and rotated q and k."""
-        t, dev, qs, ks = self._begin(q)
-        h = _HEADS[4](*_heads(q, qs, "q", dev), *self._key(k, ks, "k", dev),
-                      *_heads(q_out, qs, "q_out", dev), *self._key(k_out, ks, "k_out", dev))
-        at = ctypes.addressof(h)
-        _check(_lib.dmuon_qk_norm_rope(ctypes.byref(self._shape(t)), at, at + 24,
-                                       *self._rest(w_q, w_k, inv_freq, position, t, dev), at + 48,
-                                       at + 72, _launch_stream(stream, dev)), "dmuon_qk_norm_rope")
+        t, shape, qs, ks, dev = self._begin(q)
+        _check(_lib.dmuon_qk_norm_rope(ctypes.byref(shape), _heads(q, qs, "q", dev),
+                                       self._key(k, ks, "k", dev),
+                                       *self._rest(w_q, w_k, inv_freq, position, t, dev),
+                                       _heads(q_out, qs, "q_out", dev),
+                                       self._key(k_out, ks, "k_out", dev),
+                                       _launch_stream(stream, dev)), "dmuon_qk_norm_rope")
 
     def backward(self, dq_out, dk_out, q, k, w_q, w_k, inv_freq, position, dq, dk, dw_q=None,
                  dw_k=None, stream=None) -> None:
@@ -738,18 +752,16 @@ class QKNormRope:
         gradient may be None (not wanted)."""
         if not self.with_backward:
             raise ValueError("this QKNormRope was made without a backward pass")
-        t, dev, qs, ks = self._begin(q)
-        h = _HEADS[6](*_heads(dq_out, qs, "dq_out", dev), *self._key(dk_out, ks, "dk_out", dev),
-                      *_heads(q, qs, "q", dev), *self._key(k, ks, "k", dev),
-                      *_heads(dq, qs, "dq", dev), *self._key(dk, ks, "dk", dev))
-        at, d = ctypes.addressof(h), self.head_dim
-        gq = None if dw_q is None else _dense(dw_q, torch.bfloat16, (d,), "dw_q", dev)
-        gk = None if dw_k is None else _dense(dw_k, torch.bfloat16, (d,), "dw_k", dev)
+        t, shape, qs, ks, dev = self._begin(q)
+        d = self.head_dim
+        gq = None if dw_q is None else _flat(dw_q, _BF16, (d,), "dw_q", dev)
+        gk = None if dw_k is None else _flat(dw_k, _BF16, (d,), "dw_k", dev)
         _check(_lib.dmuon_qk_norm_rope_backward(
-            ctypes.byref(self._shape(t)), at, at + 24, at + 48, at + 72,
-            *self._rest(w_q, w_k, inv_freq, position, t, dev), at + 96, at + 120, gq, gk,
-            self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
-            "dmuon_qk_norm_rope_backward")
+            ctypes.byref(shape), _heads(dq_out, qs, "dq_out", dev),
+            self._key(dk_out, ks, "dk_out", dev), _heads(q, qs, "q", dev), self._key(k, ks, "k", dev),
+            *self._rest(w_q, w_k, inv_freq, position, t, dev), _heads(dq, qs, "dq", dev),
+            self._key(dk, ks, "dk", dev), gq, gk, self.workspace.data_ptr(), self.workspace.numel(),
+            _launch_stream(stream, dev)), "dmuon_qk_norm_rope_backward")
 
     def status(self, stream=None) -> int:
         return stream_status(self.workspace, stream)
@@ -773,6 +785,7 @@ class LinearAttention:
         self.value_dim = self.key_dim if value_dim is None else int(value_dim)
         self.max_sequences, self.with_backward = int(max_sequences), bool(backward)
         self.scale = max(1, self.key_dim) ** -0.5 if scale is None else float(scale)
+        self._last = (-1, -1)
         shape = self._shape(self.max_tokens, self.max_sequences)
         nbytes = int(_lib.dmuon_linattn_workspace_bytes(ctypes.byref(shape), int(self.with_backward)))
         if nbytes == 0:
@@ -795,27 +808,28 @@ class LinearAttention:
             if n < 1 or n > self.max_sequences:
                 raise ValueError(f"offsets: expected (sequences + 1 <= {self.max_sequences + 1},), "
                                  f"got {tuple(offsets.shape)}")
-            off = _dense(offsets, torch.int32, (n + 1,), "offsets", dev)
-        return t, n, off, dev, (t, self.heads, self.key_dim), (t, self.heads, self.value_dim)
+            off = _flat(offsets, torch.int32, (n + 1,), "offsets", dev)
+        last = self._last          # shapes of the last numbers of tokens and sequences
+        if last[0] != t or last[1] != n:
+            last = self._last = (t, n, self._shape(t, n), (t, self.heads, self.key_dim),
+                                 (t, self.heads, self.value_dim))
+        return last + (off, dev)
 
     def _state(self, state, n, what, dev):
-        return None if state is None else _dense(
+        return None if state is None else _flat(
             state, torch.float32, (n, self.heads, self.key_dim, self.value_dim), what, dev)
 
     def forward(self, q, k, v, log_decay, out, offsets=None, state=None, final_state=None,
                 stream=None) -> None:
         """out <- the mixed values; from `state` (None: zeros) and to `final_state` if given
         (which may be `state`)."""
-        t, n, off, dev, ks, vs = self._begin(q, offsets)
-        h = _HEADS[4](*_heads(q, ks, "q", dev), *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev),
-                      *_heads(out, vs, "out", dev))
-        at = ctypes.addressof(h)
+        t, n, shape, ks, vs, off, dev = self._begin(q, offsets)
         _check(_lib.dmuon_linattn_forward(
-            ctypes.byref(self._shape(t, n)), at, at + 24, at + 48,
-            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), off,
-            self._state(state, n, "state", dev), self._state(final_state, n, "final_state", dev),
-            at + 72, self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
-            "dmuon_linattn_forward")
+            ctypes.byref(shape), _heads(q, ks, "q", dev), _heads(k, ks, "k", dev),
+            _heads(v, vs, "v", dev), _flat(log_decay, torch.float32, (self.heads,), "log_decay", dev),
+            off, self._state(state, n, "state", dev), self._state(final_state, n, "final_state", dev),
+            _heads(out, vs, "out", dev), self.workspace.data_ptr(), self.workspace.numel(),
+            _launch_stream(stream, dev)), "dmuon_linattn_forward")
 
     def backward(self, dout, q, k, v, log_decay, dq, dk, dv, offsets=None, state=None,
                  dfinal_state=None, dstate=None, stream=None) -> None:
@@ -823,37 +837,32 @@ class LinearAttention:
         (None: zeros) of final_state."""
         if not self.with_backward:
             raise ValueError("this LinearAttention was made without a backward pass")
-        t, n, off, dev, ks, vs = self._begin(q, offsets)
-        h = _HEADS[7](*_heads(dout, vs, "dout", dev), *_heads(q, ks, "q", dev),
-                      *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev), *_heads(dq, ks, "dq", dev),
-                      *_heads(dk, ks, "dk", dev), *_heads(dv, vs, "dv", dev))
-        at = ctypes.addressof(h)
+        t, n, shape, ks, vs, off, dev = self._begin(q, offsets)
         _check(_lib.dmuon_linattn_backward(
-            ctypes.byref(self._shape(t, n)), at, at + 24, at + 48, at + 72,
-            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), off,
+            ctypes.byref(shape), _heads(dout, vs, "dout", dev), _heads(q, ks, "q", dev),
+            _heads(k, ks, "k", dev), _heads(v, vs, "v", dev),
+            _flat(log_decay, torch.float32, (self.heads,), "log_decay", dev), off,
             self._state(state, n, "state", dev), self._state(dfinal_state, n, "dfinal_state", dev),
-            at + 96, at + 120, at + 144, self._state(dstate, n, "dstate", dev),
-            self.workspace.data_ptr(), self.workspace.numel(), _launch_stream(stream, dev)),
-            "dmuon_linattn_backward")
+            _heads(dq, ks, "dq", dev), _heads(dk, ks, "dk", dev), _heads(dv, vs, "dv", dev),
+            self._state(dstate, n, "dstate", dev), self.workspace.data_ptr(), self.workspace.numel(),
+            _launch_stream(stream, dev)), "dmuon_linattn_backward")
 
     def step(self, q, k, v, log_decay, state, out, new_state=None, slots=None, stream=None) -> None:
         """One token for each of q.shape[0] streams: row r reads state[slots[r]] (None: state[r])
         and writes the state after its token to the same place of `new_state` (None: of `state`).
         A slot outside the states skips its row; rows that share one are taken in their order."""
-        t, _, _, dev, ks, vs = self._begin(q)
+        t, _, shape, ks, vs, _, dev = self._begin(q)
         if state.dim() != 4:
             raise ValueError(f"state: expected 4 dimensions, got {tuple(state.shape)}")
         n = state.shape[0]
         st = self._state(state, n, "state", dev)
         new = st if new_state is None else self._state(new_state, n, "new_state", dev)
-        sl = None if slots is None else _dense(slots, torch.int32, (t,), "slots", dev)
-        h = _HEADS[4](*_heads(q, ks, "q", dev), *_heads(k, ks, "k", dev), *_heads(v, vs, "v", dev),
-                      *_heads(out, vs, "out", dev))
-        at = ctypes.addressof(h)
+        sl = None if slots is None else _flat(slots, torch.int32, (t,), "slots", dev)
         _check(_lib.dmuon_linattn_step(
-            ctypes.byref(self._shape(t, 1)), at, at + 24, at + 48,
-            _dense(log_decay, torch.float32, (self.heads,), "log_decay", dev), sl, n, st, new,
-            at + 72, _launch_stream(stream, dev)), "dmuon_linattn_step")
+            ctypes.byref(shape), _heads(q, ks, "q", dev), _heads(k, ks, "k", dev),
+            _heads(v, vs, "v", dev), _flat(log_decay, torch.float32, (self.heads,), "log_decay", dev),
+            sl, n, st, new, _heads(out, vs, "out", dev), _launch_stream(stream, dev)),
+            "dmuon_linattn_step")
 
     def status(self, stream=None) -> int:
         return stream_status(self.workspace, stream)

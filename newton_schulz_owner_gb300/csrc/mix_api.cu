@@ -139,6 +139,7 @@ int qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* const x[2],
     g.x[i] = device_heads(xr[i]);
     g.out[i] = device_heads(orow[i]);
     if (backward) g.dy[i] = device_heads(dr[i]);
+    vec = vec && aligned(w[i], 8);
   }
   // an output is its own input, or apart from every input and the other output
   if (s.tokens > 0) {

@@ -7,10 +7,13 @@
 // part) eight neighbours.  Both sides of a pair lie in one lane, so that only the sums of squares
 // cross lanes.  A warp loads all heads that it takes of a token before it computes on the first.
 //
-// What limits it besides is issuing: about 130 instructions for 2 x 128 elements of a head a warp
-// leave HBM idle half the time.  Hence pairs go two at a time (fma.rn.f32x2), and the gains are
-// folded into the sines and cosines once per token:
+// What limits it besides is issuing: with 130 instructions for 2 x 128 elements of a head a warp left
+// HBM idle half the time.  Hence pairs go two at a time (fma.rn.f32x2), and the gains are folded
+// into the sines and cosines once per token:
 //   n_a w_a cos - n_b w_b sin = r (x_a (w_a cos) - x_b (w_b sin))
+// Measured, 8192 tokens of 64 heads of 128: 44 us forward (6.1 TB/s, 0.90 of the copy rate; 111
+// with one element at a time), 79 us backward (5.1 TB/s, 0.75; 148 so, and with twice as many
+// registers a thread as forward it has half the warps to hide its 4 shuffles a sum).
 //
 // Angles.  t = position * inv_freq radians is needed modulo a turn only, and in fp32 a
 // position of 10^5 would leave a third of the digits.  inv_freq / 2 pi as a 64-bit fraction of a
@@ -171,12 +174,12 @@ DM_DEV float dot(const Pairs& a, const Pairs& b) {
 }
 
 // A lane's gains.
-template <bool ILV>
+template <bool ILV, bool VEC>
 DM_DEV Pairs gains(const __nv_bfloat16* w, const Share& sh) {
   Raw r{make_uint2(0x3F803F80u, 0x3F803F80u), make_uint2(0x3F803F80u, 0x3F803F80u)};
   if (w != nullptr && sh.in) {
-    r.a = load4<false>(w + sh.a);
-    r.b = load4<false>(w + sh.b);
+    r.a = load4<VEC>(w + sh.a);
+    r.b = load4<VEC>(w + sh.b);
   }
   return unpack<ILV>(r);
 }
@@ -210,19 +213,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     const int h0 = (n - x * q_chunks) * C::kHeads + group;
     const __nv_bfloat16* in = g.x[x].p + t * g.x[x].ts + h0 * g.x[x].hs;
     __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts + h0 * g.out[x].hs;
+    const long long in_step = C::kGroups * g.x[x].hs, out_step = C::kGroups * g.out[x].hs;
+    const int left = sh.in ? (g.heads[x] - h0 + C::kGroups - 1) / C::kGroups : 0;  // heads from h0 on
     Raw raw[C::kDepth];
 #pragma unroll
-    for (int d = 0; d < C::kDepth; ++d) {
+    for (int d = 0; d < C::kDepth; ++d, in += in_step) {
       raw[d] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-      if (sh.in && h0 + d * C::kGroups < g.heads[x]) {
-        const __nv_bfloat16* p = in + (long long)d * C::kGroups * g.x[x].hs;
-        raw[d].a = load4<VEC>(p + sh.a);
-        raw[d].b = load4<VEC>(p + sh.b);
+      if (d < left) {
+        raw[d].a = load4<VEC>(in + sh.a);
+        raw[d].b = load4<VEC>(in + sh.b);
       }
     }
     if (fresh) angles(g.inv_freq, l, sh.turned, position, c, s);
     fresh = false;
-    const Pairs w = gains<ILV>(g.w[x], sh);
+    const Pairs w = gains<ILV, VEC>(g.w[x], sh);
     Pairs wc, ws;  // x_out = r (x wc.x - y ws.y), y_out = r (x ws.x + y wc.y)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
       ws.y[i] = negate2(mul2(w.y[i], s[i]));
     }
 #pragma unroll
-    for (int d = 0; d < C::kDepth; ++d) {
+    for (int d = 0; d < C::kDepth; ++d, out += out_step) {
       const Pairs v = unpack<ILV>(raw[d]);
       const float r = rsqrtf(fmaf(group_sum<LANES>(dot(v, v)), inv_dim, g.eps));
       const F2 rr = f2(r, r);
@@ -242,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         o.x[i] = mul2(rr, fma2(v.x[i], wc.x[i], mul2(v.y[i], ws.y[i])));
         o.y[i] = mul2(rr, fma2(v.x[i], ws.x[i], mul2(v.y[i], wc.y[i])));
       }
-      if (sh.in && h0 + d * C::kGroups < g.heads[x])
-        store<ILV, VEC>(out + (long long)d * C::kGroups * g.out[x].hs, sh, o);
+      if (d < left) store<ILV, VEC>(out, sh, o);
     }
   }
 }
@@ -268,72 +271,63 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) rope_grad_kernel(const 
   for (unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     const int t = int(u / unsigned(g.parts)), part = int(u - unsigned(t) * unsigned(g.parts));
     const int position = g.rotary > 0 ? g.position[t] : 0;
-    F2 c[2], s[2];
-    bool fresh = true;
-    for (int n = part * g.per; n < min(chunks, (part + 1) * g.per); ++n) {
-      const int x = n >= q_chunks ? 1 : 0;
-      const int h0 = (n - x * q_chunks) * C::kHeads + group;
-      const __nv_bfloat16* in = g.x[x].p + t * g.x[x].ts + h0 * g.x[x].hs;
-      const __nv_bfloat16* dy = g.dy[x].p + t * g.dy[x].ts + h0 * g.dy[x].hs;
-      __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts + h0 * g.out[x].hs;
-      Raw raw[C::kDepth], grad[C::kDepth];
+    F2 c[2], s[2], minus_s[2];
+    angles(g.inv_freq, l, sh.turned, position, c, s);
 #pragma unroll
-      for (int d = 0; d < C::kDepth; ++d) {
-        raw[d] = grad[d] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-        if (sh.in && h0 + d * C::kGroups < g.heads[x]) {
-          const __nv_bfloat16* p = in + (long long)d * C::kGroups * g.x[x].hs;
-          raw[d].a = load4<VEC>(p + sh.a);
-          raw[d].b = load4<VEC>(p + sh.b);
-          p = dy + (long long)d * C::kGroups * g.dy[x].hs;
-          grad[d].a = load4<VEC>(p + sh.a);
-          grad[d].b = load4<VEC>(p + sh.b);
-        }
-      }
-      if (fresh) angles(g.inv_freq, l, sh.turned, position, c, s);
-      fresh = false;
-      const Pairs w = gains<ILV>(g.w[x], sh);
-      Pairs sum;
+    for (int i = 0; i < 2; ++i) minus_s[i] = negate2(s[i]);
+    const int end = min(chunks, (part + 1) * g.per);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sum.x[i] = sum.y[i] = 0;
+    for (int x = 0; x < 2; ++x) {
+      const Pairs w = gains<ILV, VEC>(g.heads[x] > 0 ? g.w[x] : nullptr, sh);
+      const long long in_step = C::kGroups * g.x[x].hs, dy_step = C::kGroups * g.dy[x].hs,
+                      out_step = C::kGroups * g.out[x].hs;
+#pragma unroll 1
+      for (int n = x == 0 ? part * g.per : max(part * g.per, q_chunks);
+           n < (x == 0 ? min(end, q_chunks) : end); ++n) {
+        const int h0 = (n - x * q_chunks) * C::kHeads + group;
+        const __nv_bfloat16* in = g.x[x].p + t * g.x[x].ts + h0 * g.x[x].hs;
+        const __nv_bfloat16* dy = g.dy[x].p + t * g.dy[x].ts + h0 * g.dy[x].hs;
+        __nv_bfloat16* out = g.out[x].p + t * g.out[x].ts + h0 * g.out[x].hs;
+        const int left = sh.in ? (g.heads[x] - h0 + C::kGroups - 1) / C::kGroups : 0;
+        Raw raw[C::kDepth], grad[C::kDepth];
 #pragma unroll
-      for (int d = 0; d < C::kDepth; ++d) {
-        const bool has = sh.in && h0 + d * C::kGroups < g.heads[x];
-        Pairs v = unpack<ILV>(raw[d]);
-        const Pairs z = unpack<ILV>(grad[d]);
-        const float r = rsqrtf(fmaf(group_sum<LANES>(dot(v, v)), inv_dim, g.eps));
-        const F2 rr = f2(r, r);
-        Pairs gw;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const F2 gx = fma2(z.x[i], c[i], mul2(z.y[i], s[i]));
-          const F2 gy = fma2(z.y[i], c[i], negate2(mul2(z.x[i], s[i])));
-          v.x[i] = mul2(v.x[i], rr);  // n
-          v.y[i] = mul2(v.y[i], rr);
-          if (has) {  // an absent head's r may be infinite
-            sum.x[i] = fma2(gx, v.x[i], sum.x[i]);
-            sum.y[i] = fma2(gy, v.y[i], sum.y[i]);
+        for (int d = 0; d < C::kDepth; ++d, in += in_step, dy += dy_step) {
+          raw[d] = grad[d] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+          if (d < left) {
+            raw[d].a = load4<VEC>(in + sh.a);
+            raw[d].b = load4<VEC>(in + sh.b);
+            grad[d].a = load4<VEC>(dy + sh.a);
+            grad[d].b = load4<VEC>(dy + sh.b);
           }
-          gw.x[i] = mul2(gx, w.x[i]);
-          gw.y[i] = mul2(gy, w.y[i]);
         }
-        const float m = -group_sum<LANES>(dot(gw, v)) * inv_dim;
-        const F2 mm = f2(m, m);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          v.x[i] = mul2(rr, fma2(v.x[i], mm, gw.x[i]));
-          v.y[i] = mul2(rr, fma2(v.y[i], mm, gw.y[i]));
-        }
-        if (has) store<ILV, VEC>(out + (long long)d * C::kGroups * g.out[x].hs, sh, v);
-      }
-      const F2 one = f2(1.f, 1.f);
+        for (int d = 0; d < C::kDepth; ++d, out += out_step) {
+          Pairs v = unpack<ILV>(raw[d]);
+          const Pairs z = unpack<ILV>(grad[d]);
+          // (of an absent head 1: with eps = 0 its root would be infinite)
+          const float square = fmaf(group_sum<LANES>(dot(v, v)), inv_dim, g.eps);
+          const float r = rsqrtf(d < left ? square : 1.f);
+          const F2 rr = f2(r, r);
+          Pairs gw;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (x == 0) {
-          dw[0].x[i] = fma2(sum.x[i], one, dw[0].x[i]);
-          dw[0].y[i] = fma2(sum.y[i], one, dw[0].y[i]);
-        } else {
-          dw[1].x[i] = fma2(sum.x[i], one, dw[1].x[i]);
-          dw[1].y[i] = fma2(sum.y[i], one, dw[1].y[i]);
+          for (int i = 0; i < 2; ++i) {
+            const F2 gx = fma2(z.x[i], c[i], mul2(z.y[i], s[i]));
+            const F2 gy = fma2(z.y[i], c[i], mul2(z.x[i], minus_s[i]));
+            v.x[i] = mul2(v.x[i], rr);  // n
+            v.y[i] = mul2(v.y[i], rr);
+            dw[x].x[i] = fma2(gx, v.x[i], dw[x].x[i]);
+            dw[x].y[i] = fma2(gy, v.y[i], dw[x].y[i]);
+            gw.x[i] = mul2(gx, w.x[i]);
+            gw.y[i] = mul2(gy, w.y[i]);
+          }
+          const float m = -group_sum<LANES>(dot(gw, v)) * inv_dim;
+          const F2 mm = f2(m, m);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            v.x[i] = mul2(rr, fma2(v.x[i], mm, gw.x[i]));
+            v.y[i] = mul2(rr, fma2(v.y[i], mm, gw.y[i]));
+          }
+          if (d < left) store<ILV, VEC>(out, sh, v);
         }
       }
     }
@@ -411,7 +405,8 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
   // Chunks of a warp share their token's sines; but with few tokens more warps of one chunk each
   // fill the GPU (8192 tokens of 64 heads of 128: 52 us with 2 chunks to a warp, 48 with 8; 777 of
   // 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take token after token, so that the
-  // gains' sums meet once a block (88 us with twice the blocks that fit, 82 with as many).
+  // gains' sums meet once a block (88 us with twice the blocks that fit, 82 with as many; 4 chunks to
+  // a warp 79, 2 87, 8 83).
   const int heads = 32 / lanes * 4;
   const int chunks = (g.heads[0] + heads - 1) / heads + (g.heads[1] + heads - 1) / heads;
   g.per = (long long)g.tokens * chunks > (long long)sms * 56 ? (backward ? 4 : 8) : 1;

@@ -463,24 +463,36 @@ struct StateRole {
     for (int i = 0; i < kCols / 2; ++i) st[i] = 0;
   }
   DM_DEV long long state_at(int seq) const { return ((long long)seq * g.heads + head) * g.dk * g.dv; }
+  // A caller's state: four elements of a row at a time, or (transposed) one, rows side by side.
   DM_DEV void read_initial(int seq) {
     if (g.state_in == nullptr || row >= g.dk) return;
     const float* p = g.state_in + state_at(seq) + row * g.st_row + col * g.st_col;
+    const F2 f = f2(g.in_scale, g.in_scale);
+    if (g.st_col == 1) {
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col)
-      if (col + 2 * i < g.dv) st[i] = f2(g.in_scale * p[0], g.in_scale * p[g.st_col]);
+      for (int i = 0; i < kCols / 4; ++i)
+        if (col + 4 * i < g.dv) {
+          const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+          st[2 * i] = mul2(f, f2(v.x, v.y));
+          st[2 * i + 1] = mul2(f, f2(v.z, v.w));
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col)
+        if (col + 2 * i < g.dv) st[i] = mul2(f, f2(p[0], p[g.st_col]));
+    }
   }
-  DM_DEV void write_final(int seq) {
+  DM_DEV void write_final(int seq) {  // of the gradients' sweeps only dv's has one: never transposed
     if (row >= g.dk) return;
-    float* p = g.state_out + state_at(seq) + row * g.st_row + col * g.st_col;
+    float* p = g.state_out + state_at(seq) + row * g.st_row + col;
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col) {
-      float a, b;
-      f2_split(st[i], a, b);
-      if (col + 2 * i < g.dv) {
-        p[0] = g.out_scale * a;
-        p[g.st_col] = g.out_scale * b;
-      }
+    for (int i = 0; i < kCols / 4; ++i) {
+      float4 v;
+      f2_split(st[2 * i], v.x, v.y);
+      f2_split(st[2 * i + 1], v.z, v.w);
+      if (col + 4 * i < g.dv)
+        *reinterpret_cast<float4*>(p + 4 * i) = make_float4(g.out_scale * v.x, g.out_scale * v.y,
+                                                            g.out_scale * v.z, g.out_scale * v.w);
     }
   }
   // A state in the workspace, four columns at a time so that a warp's rows lie together.  Slots of

@@ -512,16 +512,6 @@ struct StateRole {
       __stcg(p + i * 128, v);
     }
   }
-  // st <- f st + what lies there
-  DM_DEV void take(const float4* p, float f) {
-    const F2 ff = f2(f, f);
-#pragma unroll
-    for (int i = 0; i < kCols / 4; ++i) {
-      const float4 v = __ldcg(p + i * 128);
-      st[2 * i] = fma2(ff, st[2 * i], f2(v.x, v.y));
-      st[2 * i + 1] = fma2(ff, st[2 * i + 1], f2(v.z, v.w));
-    }
-  }
   // A final state may be written over the first one while other CTAs have yet to read that.
   DM_DEV bool over() const { return g.split > 1 && g.state_in != nullptr && g.state_in == g.state_out; }
   DM_DEV void keep_initial(int seq) {
@@ -548,15 +538,33 @@ struct StateRole {
     if (older) p = slot(g.split - 1, round & 1);
     else if (over() && (inside || (mine.ahead > 0 && c.seq == mine.share.seq))) p = slot(from, 2);
     else read_initial(c.seq);
-    float f = 0.f;
-#pragma unroll 1
-    for (int r = from - 1; r < w.rank; ++r) {
-      if (r >= from) {
-        p = slot(r, round & 1);
-        const int n0 = max(base + r * w.per - start, 0), n1 = base + (r + 1) * w.per - start;
-        f = expf(log_decay * float(c.before(g, n1) - c.before(g, n0)));
+    // lane r: the decay over rank r's part of the sequence
+    const int n0 = max(base + lane * w.per - start, 0), n1 = base + (lane + 1) * w.per - start;
+    const float decay =
+        lane >= from && lane < w.rank ? expf(log_decay * float(c.before(g, n1) - c.before(g, n0))) : 0.f;
+    constexpr int kPart = 4;  // of 4 columns each, so that several ranks' loads are in flight
+#pragma unroll
+    for (int i0 = 0; i0 < kCols / 4; i0 += kPart) {
+      if (p != nullptr) {
+#pragma unroll
+        for (int i = i0; i < i0 + kPart; ++i) {
+          const float4 v = __ldcg(p + i * 128);
+          st[2 * i] = f2(v.x, v.y);
+          st[2 * i + 1] = f2(v.z, v.w);
+        }
       }
-      if (p != nullptr) take(p, f);
+#pragma unroll 2
+      for (int r = from; r < w.rank; ++r) {
+        const float f = __shfl_sync(0xffffffffu, decay, r);
+        const F2 ff = f2(f, f);
+        const float4* q = slot(r, round & 1);
+#pragma unroll
+        for (int i = i0; i < i0 + kPart; ++i) {
+          const float4 v = __ldcg(q + i * 128);
+          st[2 * i] = fma2(ff, st[2 * i], f2(v.x, v.y));
+          st[2 * i + 1] = fma2(ff, st[2 * i + 1], f2(v.z, v.w));
+        }
+      }
     }
   }
   // The state as the operand of Q S: rows of 64 bf16, 128-byte swizzle.

@@ -68,6 +68,20 @@ struct Tiles {
   static constexpr int bytes = 1024 + kMiscBytes + state + stages * stage;
 };
 
+// What the warps need of a block, in the order of the CTA's work: written with its loads.
+enum BlockKind {
+  kSweep = 1,  // swept; without it only summed, for the CTAs behind this one
+  kFirst = 2,  // of its kind in its round
+  kLast = 4,
+  kEnd = 8     // no block: all are done
+};
+struct Block {
+  int kind, row, live;       // first token, tokens
+  int seq, m, blocks, len;   // number m of a sequence's blocks in the order of the sweep, its tokens
+  int it;                    // number among the CTA's blocks
+};
+constexpr int kRing = 8;  // more than stages and the warps' distances from the loads together
+
 struct Shared {
   uint64_t full[kMaxStages];   // a stage's keys and values are there
   uint64_t empty[kMaxStages];  // and have been read
@@ -83,6 +97,8 @@ struct Shared {
   uint64_t taken;              // and out of it again
   uint64_t put;                // this CTA's share of the round in memory
   uint64_t shares;             // the round's shares of all CTAs of the cluster
+  Block block[kRing];          // by number
+  Block sweep[kRing];          // the swept ones by theirs
   uint32_t tmem;
   int abort;
   int place[6];                // what locate() found
@@ -130,10 +146,6 @@ struct Cursor {
   DM_DEV int place(const LinAttnArgs& g) const { return g.against ? x.blocks - 1 - m : m; }
   DM_DEV int row(const LinAttnArgs& g) const { return x.begin + place(g) * kMixBlock; }
   DM_DEV int live(const LinAttnArgs& g) const { return min(kMixBlock, x.len - place(g) * kMixBlock); }
-  // tokens of the sequence's first n blocks of the sweep
-  DM_DEV int before(const LinAttnArgs& g, int n) const {
-    return g.against ? x.len - min(x.len, (x.blocks - n) * kMixBlock) : min(x.len, n * kMixBlock);
-  }
 };
 // n blocks on (past the batch's end: any block)
 DM_DEV Cursor skipped(const LinAttnArgs& g, Cursor c, int n) {
@@ -153,11 +165,6 @@ DM_DEV Cursor skipped(const LinAttnArgs& g, Cursor c, int n) {
   c.m += n;
   return c;
 }
-DM_DEV void next_block(const LinAttnArgs& g, Cursor& c) {
-  if (c.m + 1 < c.x.blocks) ++c.m;
-  else c = skipped(g, c, 1);
-}
-
 // What a CTA does: stretches of `per` blocks, one in each round, of the nb blocks that its cluster
 // takes.
 struct Work {
@@ -271,173 +278,165 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
   return w;
 }
 
-// A CTA's part of a round: n blocks from `at` on, before them the last `ahead` of those, from
-// `share` on, for the state that they leave to the next CTA.
-struct Round {
-  int lo, n, ahead;
-  Cursor at, share;
-};
-DM_DEV Round round_of(const LinAttnArgs& g, const Work w, Cursor at, int lo) {
-  Round r;
-  r.lo = lo;
-  r.at = r.share = at;
-  r.n = max(0, min(w.per, w.nb - lo));
-  r.ahead = 0;
-  if (w.rank + 1 < g.split && r.n > 0) {
-    r.share = skipped(g, at, r.n - 1);
-    if (r.share.m + 1 < r.share.x.blocks) {
-      r.ahead = min(r.share.m + 1, r.n);
-      r.share.m -= r.ahead - 1;
-    }
-  }
-  return r;
-}
-DM_DEV Round first_round(const LinAttnArgs& g, const Work& w) {
-  return round_of(g, w, w.start, w.rank * w.per);
-}
-DM_DEV void next_round(const LinAttnArgs& g, const Work& w, Round& r) {
-  const int lo = r.lo + g.split * w.per;
-  if (lo < w.nb) r.at = skipped(g, r.at, g.split * w.per);
-  r = round_of(g, w, r.at, lo);
+// Blocks that a CTA sweeps in all rounds.
+DM_DEV int sweeps_of(const LinAttnArgs& g, const Work& w) {
+  int n = 0;
+  for (int r = 0; r < w.rounds; ++r)
+    n += max(0, min(w.per, w.nb - (r * g.split + w.rank) * w.per));
+  return n;
 }
 
 // ------------------------------------------------------------------ loads
+// The one walk through the batch: in each round the CTA's stretch from its last sequence on, if that
+// goes on in the next CTA's, and then the whole stretch.
 template <int DK, int DV>
 DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* smem, Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
-  int it = 0;
-  auto load = [&](int row, bool queries) {
+  int it = 0, swept = 0;
+  auto load = [&](const Cursor& c, int kind) {
     const int s = it % T::stages;
     const uint32_t parity = ((it / T::stages) & 1) ^ 1;
     uint8_t* q = smem + s * T::stage;
     uint8_t *k = q + T::q, *v = k + T::k;
     if (!await(&sh->empty[s], parity, g.err, flag)) return false;
-    mbar_arrive_expect_tx(&sh->full[s], uint32_t(T::k + T::v));
+    const Block b{kind, c.row(g), c.live(g), c.seq, c.m, c.x.blocks, c.x.len, it};
+    sh->block[it % kRing] = b;
+    if (kind & kSweep) sh->sweep[swept++ % kRing] = b;
+    if (kind & kEnd) {
+      mbar_arrive(&sh->full[s]);
+    } else {
+      mbar_arrive_expect_tx(&sh->full[s], uint32_t(T::k + T::v));
 #pragma unroll
-    for (int p = 0; p < DK / 64; ++p)
-      tma_load_3d(k + p * 16384, &g.k, &sh->full[s], p * 64, head, row);
+      for (int p = 0; p < DK / 64; ++p)
+        tma_load_3d(k + p * 16384, &g.k, &sh->full[s], p * 64, head, b.row);
 #pragma unroll
-    for (int p = 0; p < DV / 64; ++p)
-      tma_load_3d(v + p * 16384, &g.v, &sh->full[s], p * 64, head, row);
+      for (int p = 0; p < DV / 64; ++p)
+        tma_load_3d(v + p * 16384, &g.v, &sh->full[s], p * 64, head, b.row);
+    }
     if (!await(&sh->q_empty[s], parity, g.err, flag)) return false;
-    if (queries) {
+    if (kind & kSweep) {
       mbar_arrive_expect_tx(&sh->q_full[s], uint32_t(T::k));
 #pragma unroll
       for (int p = 0; p < DK / 64; ++p)
-        tma_load_3d(q + p * 16384, &g.q, &sh->q_full[s], p * 64, head, row);
+        tma_load_3d(q + p * 16384, &g.q, &sh->q_full[s], p * 64, head, b.row);
     } else {
       mbar_arrive(&sh->q_full[s]);
     }
     ++it;
     return true;
   };
-  Round r = first_round(g, w);
-  for (int round = 0; round < w.rounds; ++round) {
-    Cursor c = r.share;
-    for (int i = 0; i < r.ahead; ++i, ++c.m)
-      if (!load(c.row(g), false)) return;
-    c = r.at;
-    for (int i = 0; i < r.n; ++i, next_block(g, c))
-      if (!load(c.row(g), true)) return;
-    next_round(g, w, r);
+  Cursor at = w.start;
+  for (int lo = w.rank * w.per; lo < w.nb; lo += g.split * w.per) {
+    const int n = min(w.per, w.nb - lo);
+    if (w.rank + 1 < g.split) {
+      Cursor c = skipped(g, at, n - 1);
+      if (c.m + 1 < c.x.blocks) {
+        const int ahead = min(c.m + 1, n);
+        c.m -= ahead - 1;
+        for (int i = 0; i < ahead; ++i, ++c.m)
+          if (!load(c, (i == 0 ? kFirst : 0) | (i + 1 == ahead ? kLast : 0))) return;
+      }
+    }
+    for (int i = 0; i < n; ++i) {
+      if (!load(at, kSweep | (i == 0 ? kFirst : 0) | (i + 1 == n ? kLast : 0))) return;
+      const bool more = i + 1 < n || lo + g.split * w.per < w.nb;
+      if (more) at = skipped(g, at, i + 1 < n ? 1 : 1 + g.split * w.per - n);
+    }
   }
+  (void)load(at, kEnd);
 }
 
 // ------------------------------------------------------------------ products
 // Two threads issue them, as issuing takes about as long as computing: one the blocks' own states,
 // one the rest.
 template <int DK, int DV, bool EXACT>
-DM_DEV void state_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state,
-                           Shared* sh) {
+DM_DEV void state_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
   constexpr uint32_t id = idesc_bf16(128, DV, true, true);
+  const uint32_t to = sh->tmem + kColState;
   // (a^..k)^T V, rows of K in steps of 16 tokens.  With 64 key elements the upper half of the
   // 128 rows reads what follows the tile; those lanes of the result are not used.
-  auto product = [&](uint32_t to, uint32_t k, uint32_t v, bool accumulate) {
+  auto product = [&](uint32_t k, uint32_t v, bool accumulate) {
     const uint64_t a = sdesc_sw128(k, 16384, 1024), b = sdesc_sw128(v, 16384, 1024);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       umma_bf16(to, a + uint64_t(j) * 128, b + uint64_t(j) * 128, id, accumulate || j > 0);
   };
-  int it = 0;
-  Round r = first_round(g, w);
-  for (int round = 0; round < w.rounds; ++round) {
-    for (int i = 0; i < r.ahead + r.n; ++i, ++it) {
-      const bool share = i < r.ahead;
-      const int s = it % T::stages;
-      const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
-      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
-      if (!await(&sh->keys, it & 1, g.err, flag)) return;  // the last block's state is added by then
-      tc_fence_after();
-      const uint32_t to = sh->tmem + kColState;
-      product(to, k, v, false);
-      // the keys' low parts lie where queries would, or the state that enters will
-      if (EXACT) product(to, share ? q : smem_u32(state), v, true);
-      umma_commit(&sh->block_state);
-      umma_commit(&sh->empty[s]);
-      if (share) {  // in the place of the output's warps
+#pragma unroll 1
+  for (int it = 0;; ++it) {
+    const int s = it % T::stages;
+    const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
+    if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
+    const int kind = sh->block[it % kRing].kind;
+    if (kind & kEnd) return;
+    if (!await(&sh->keys, it & 1, g.err, flag)) return;  // the last block's state is added by then
+    tc_fence_after();
+    product(k, v, false);
+    // the keys' low parts lie where queries would, or the state that enters will
+    if (EXACT) product(kind & kSweep ? smem_u32(state) : q, v, true);
+    umma_commit(&sh->block_state);
+    umma_commit(&sh->empty[s]);
+    if (!(kind & kSweep)) {  // in the place of the output's warps
 #pragma unroll
-        for (int n = 0; n < kOutWarps; ++n) umma_commit(&sh->q_empty[s]);
-      }
+      for (int n = 0; n < kOutWarps; ++n) umma_commit(&sh->q_empty[s]);
     }
-    next_round(g, w, r);
   }
 }
 template <int DK, int DV>
-DM_DEV void out_mma_role(const LinAttnArgs& g, const Work& w, uint8_t* smem, uint8_t* state,
-                         Shared* sh) {
+DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
   const uint32_t tmem = sh->tmem;
   constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
   constexpr uint32_t id_out = idesc_bf16(128, DV, false, true);
   const uint64_t ed = sdesc_sw128(smem_u32(state), DK * 128, 1024);
-  int it = 0, swept = 0;
-  Round r = first_round(g, w);
-  for (int round = 0; round < w.rounds; ++round) {
-    for (int i = 0; i < r.ahead + r.n; ++i, ++it) {
-      const int s = it % T::stages;
-      const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
-      const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
-      if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
-      if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
-      if (i < r.ahead) {
-        mbar_arrive(&sh->empty[s]);  // waited for all the same: a wait misses no phase
-        continue;
-      }
-      // the last block's weighted scores have been read (no order is promised between products of
-      // unlike shape)
-      if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return;
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j) {
-        const uint64_t at = uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2;
-        umma_bf16(tmem + kColScore, qd + at, kd + at, id_score, j > 0);
-      }
-      umma_commit(&sh->score);
-      if (swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
-      if (!await(&sh->clear, swept & 1, g.err, flag)) return;
-      if (!await(&sh->weighted, swept & 1, g.err, flag)) return;
-      tc_fence_after();
-      const uint64_t vd = sdesc_sw128(v, 16384, 1024);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)  // 8 columns of weighted scores a step, in two halves
-        umma_bf16_ts(tmem + kColInner, tmem + kColScore + (j >> 2) * 64 + (j & 3) * 8,
-                     vd + uint64_t(j) * 128, id_out, j > 0);
-      umma_commit(&sh->spent);
-      umma_commit(&sh->empty[s]);
-      if (!await(&sh->entry, swept & 1, g.err, flag)) return;
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j)
-        umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
-                  ed + uint64_t(j) * 128, id_out, j > 0);
-      umma_commit(&sh->out);
-      ++swept;
+  int swept = 0;
+#pragma unroll 1
+  for (int it = 0;; ++it) {
+    const int s = it % T::stages;
+    const uint32_t q = smem_u32(smem) + s * T::stage, k = q + T::q, v = k + T::k;
+    const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
+    if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
+    const int kind = sh->block[it % kRing].kind;
+    if (kind & kEnd) return;
+    if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
+    if (!(kind & kSweep)) {
+      mbar_arrive(&sh->empty[s]);  // waited for all the same: a wait misses no phase
+      continue;
     }
-    next_round(g, w, r);
+    // the last block's weighted scores have been read (no order is promised between products of
+    // unlike shape)
+    if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j) {
+      const uint64_t at = uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2;
+      umma_bf16(tmem + kColScore, qd + at, kd + at, id_score, j > 0);
+    }
+    umma_commit(&sh->score);
+    mbar_arrive(&sh->score);  // and with it what lies in sh->sweep, seen by this thread
+    if (swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
+    if (!await(&sh->clear, swept & 1, g.err, flag)) return;
+    if (!await(&sh->weighted, swept & 1, g.err, flag)) return;
+    tc_fence_after();
+    const uint64_t vd = sdesc_sw128(v, 16384, 1024);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // 8 columns of weighted scores a step, in two halves
+      umma_bf16_ts(tmem + kColInner, tmem + kColScore + (j >> 2) * 64 + (j & 3) * 8,
+                   vd + uint64_t(j) * 128, id_out, j > 0);
+    umma_commit(&sh->spent);
+    umma_commit(&sh->empty[s]);
+    if (!await(&sh->entry, swept & 1, g.err, flag)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j)
+      umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
+                ed + uint64_t(j) * 128, id_out, j > 0);
+    umma_commit(&sh->out);
+    mbar_arrive(&sh->out);
+    ++swept;
   }
 }
 
@@ -526,22 +525,26 @@ struct StateRole {
       __stcg(to + i * 128, v);
     }
   }
-  // The state before block c: a sequence's first state, or (the first block of a CTA's round, inside
+  // tokens of the first n of a sequence's blocks in the order of the sweep
+  DM_DEV int before(const Block& b, int n) const {
+    return g.against ? b.len - min(b.len, (b.blocks - n) * kMixBlock) : min(b.len, n * kMixBlock);
+  }
+  // The state before block b: a sequence's first state, or (the first block of a CTA's round, inside
   // a sequence) that of its start or of the round's, and the shares of the CTAs before this one.
-  DM_DEV void enter(const Cursor& c, int round, const Round& mine) {
-    const int base = round * g.split * w.per;      // sweep's number of the round's first block
-    const int start = mine.lo - c.m;                // and of the sequence's, if c is the CTA's first
-    const bool inside = c.m > 0, older = inside && start < base;
+  DM_DEV void enter(const Block& b, int round, int share_seq) {
+    const int base = round * g.split * w.per;            // sweep's number of the round's first block
+    const int start = base + w.rank * w.per - b.m;        // and of the sequence's, if b is the CTA's first
+    const bool inside = b.m > 0, older = inside && start < base;
     const int from = older ? 0 : inside ? (start - base) / w.per : w.rank;
     zero();
     const float4* p = nullptr;
     if (older) p = slot(g.split - 1, round & 1);
-    else if (over() && (inside || (mine.ahead > 0 && c.seq == mine.share.seq))) p = slot(from, 2);
-    else read_initial(c.seq);
+    else if (over() && (inside || b.seq == share_seq)) p = slot(from, 2);
+    else read_initial(b.seq);
     // lane r: the decay over rank r's part of the sequence
     const int n0 = max(base + lane * w.per - start, 0), n1 = base + (lane + 1) * w.per - start;
     const float decay =
-        lane >= from && lane < w.rank ? expf(log_decay * float(c.before(g, n1) - c.before(g, n0))) : 0.f;
+        lane >= from && lane < w.rank ? expf(log_decay * float(before(b, n1) - before(b, n0))) : 0.f;
     constexpr int kPart = 4;  // of 4 columns each, so that several ranks' loads are in flight
 #pragma unroll
     for (int i0 = 0; i0 < kCols / 4; i0 += kPart) {
@@ -654,7 +657,6 @@ struct StateRole {
     if (row >= g.dk) zero();  // of keys past the head's size: 0 times an infinity of V may be there
     tc_fence_before();
   }
-  DM_DEV bool loaded(int it) { return wait(&sh->full[it % T::stages], it / T::stages); }
   // The share of this round is in memory (or was not asked for): tell the cluster.
   DM_DEV bool arrive(int round) {
     __syncwarp();
@@ -669,59 +671,63 @@ struct StateRole {
   DM_DEV bool all_arrived(int round) {
     return mbar_wait_cluster(&sh->shares, round & 1, &sh->abort) || gave_up(g.err, &sh->abort);
   }
-  // This CTA's share, from the start of its last sequence or of its stretch.
-  DM_DEV bool sum_share(const Round& r, int& it) {
-    Cursor c = r.share;
-    zero();
-#pragma unroll 1
-    for (int i = 0; i < r.ahead; ++i, ++c.m, ++it) {
-      const int live = c.live(g), s = it % T::stages;
-      // the low parts go where queries would be, once the output before them has left
-      if (!loaded(it) || !wait(&sh->q_full[s], it / T::stages)) return false;
-      keys(it, live, smem_u32(smem) + s * T::stage);
-      if (!block_done(it)) return false;
-      add_block(live);
+  DM_DEV bool share_block(const Block& b, int round) {
+    if (b.kind & kFirst) {
+      if (over() && b.m == 0) keep_initial(b.seq);
+      zero();
     }
-    return true;
+    // the low parts go where queries would be, once the output before them has left
+    const int s = b.it % T::stages;
+    if (!wait(&sh->q_full[s], b.it / T::stages)) return false;
+    keys(b.it, b.live, smem_u32(smem) + s * T::stage);
+    if (!block_done(b.it)) return false;
+    add_block(b.live);
+    if (!(b.kind & kLast)) return true;
+    put(slot(w.rank, round & 1));
+    return arrive(round);
   }
-  DM_DEV bool sweep_block(const Cursor& c, int i, int it, int swept, int round, const Round& r) {
-    const int live = c.live(g);
-    if (i == 0 && g.split > 1 && !all_arrived(round)) return false;
-    if (c.m == 0 || (i == 0 && g.split > 1)) enter(c, round, r);
-    if (!loaded(it) || !wait(&sh->score, swept)) return false;
+  DM_DEV bool sweep_block(const Block& b, int swept, int round, int share_seq) {
+    const bool first = (b.kind & kFirst) != 0 && g.split > 1;
+    if (first && ((share_seq < 0 && !arrive(round)) || !all_arrived(round))) return false;
+    if (b.m == 0 || first) enter(b, round, share_seq);
+    if (!wait(&sh->score, swept)) return false;
     // exact: the low parts take the place of the state that entered the last block, and the one
     // that enters this block theirs
     if (EXACT && swept > 0 && !wait(&sh->out, swept - 1)) return false;
-    keys(it, live, smem_u32(entry));
+    keys(b.it, b.live, smem_u32(entry));
     if (lane == 0) mbar_arrive(&sh->clear);
-    if (EXACT ? !block_done(it) : swept > 0 && !wait(&sh->out, swept - 1)) return false;
+    if (EXACT ? !block_done(b.it) : swept > 0 && !wait(&sh->out, swept - 1)) return false;
     write_entry();
-    if (!EXACT && !block_done(it)) return false;
-    add_block(live);
-    if (EXACT && g.state_out != nullptr && c.m + 1 == c.x.blocks) write_final(c.seq);
+    if (!EXACT && !block_done(b.it)) return false;
+    add_block(b.live);
+    if (EXACT && g.state_out != nullptr && b.m + 1 == b.blocks) write_final(b.seq);
     return true;
   }
   DM_DEV void run() {
     zero();
-    int it = 0, swept = 0;
-    bool ok = true;
-    Round r = first_round(g, w);
+    int swept = 0, round = 0, share_seq = -1;
 #pragma unroll 1
-    for (int round = 0; ok && round < w.rounds; ++round) {
-      if (r.ahead > 0) {
-        if (over() && r.share.m == 0) keep_initial(r.share.seq);
-        ok = sum_share(r, it);
-        put(slot(w.rank, round & 1));
+    for (int it = 0;; ++it) {
+      if (!wait(&sh->full[it % T::stages], it / T::stages)) return;
+      const Block b = sh->block[it % kRing];
+      if (b.kind & kEnd) break;
+      if (b.kind & kSweep) {
+        if (!sweep_block(b, swept, round, share_seq)) return;
+        ++swept;
+        if (b.kind & kLast) {
+          ++round;
+          share_seq = -1;
+          // what the round leaves to the next
+          if (w.rank + 1 == g.split && round < w.rounds) put(slot(w.rank, round & 1));
+        }
+      } else {
+        if (!share_block(b, round)) return;
+        share_seq = b.seq;
       }
-      if (g.split > 1) ok = arrive(round) && ok;
-      Cursor c = r.at;
-#pragma unroll 1
-      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++it, ++swept)
-        ok = sweep_block(c, i, it, swept, round, r);
-      if (r.n == 0 && g.split > 1) ok = ok && all_arrived(round);
-      if (w.rank + 1 == g.split && round + 1 < w.rounds) put(slot(w.rank, (round + 1) & 1));
-      next_round(g, w, r);
     }
+    // rounds in which only CTAs before this one have blocks
+    for (; g.split > 1 && round < w.rounds; ++round)
+      if (!arrive(round) || !all_arrived(round)) return;
   }
   // Sequences without tokens: their states pass through.
   DM_DEV void pass_through(int first, int stride) {
@@ -783,11 +789,12 @@ struct WeighRole {
     }
   }
   template <bool AGAINST>
-  DM_DEV bool block(int live, int swept, F2 own) {
+  DM_DEV bool block(int swept, F2 own) {
     const int q = warp & 3, c0 = (warp >> 2) * 64;
     const uint32_t at = sh->tmem + (uint32_t(q * 32) << 16) + kColScore + c0;
     if (!wait(&sh->score, swept)) return false;
     tc_fence_after();
+    const int live = sh->sweep[swept % kRing].live;
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       const int j0 = c0 + n * 32;
@@ -811,18 +818,17 @@ struct WeighRole {
     return true;
   }
   DM_DEV void run() {
-    int swept = 0;
-    bool ok = true;
     const float f = g.scale * sh->power[g.against ? 31 - lane : lane];
     const F2 own = f2(f, f);
-    Round r = first_round(g, w);
-    for (int round = 0; ok && round < w.rounds; ++round) {
-      Cursor c = r.at;
-      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++swept) {
-        const int live = c.live(g);
-        ok = g.against ? block<true>(live, swept, own) : block<false>(live, swept, own);
+    const int n = sweeps_of(g, w);
+    if (g.against) {
+#pragma unroll 1
+      for (int swept = 0; swept < n && block<true>(swept, own); ++swept) {
       }
-      next_round(g, w, r);
+    } else {
+#pragma unroll 1
+      for (int swept = 0; swept < n && block<false>(swept, own); ++swept) {
+      }
     }
   }
 };
@@ -846,15 +852,16 @@ struct OutRole {
       mbar_arrive(&sh->q_empty[s]);
     }
   }
-  DM_DEV bool block(int row0, int live, int it, int swept) {
-    const int row = warp * 32 + lane, s = it % T::stages;
+  DM_DEV bool block(int swept) {
+    if (!wait(&sh->out, swept)) return false;
+    tc_fence_after();
+    const Block& b = sh->sweep[swept % kRing];
+    const int live = b.live, row0 = b.row, s = b.it % T::stages, row = warp * 32 + lane;
     const float f = row < live ? g.scale * sh->power[g.against ? live - 1 - row : row + 1] : 0.f;
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(warp * 32) << 16);
     // 32 columns to a piece of 2 KB, rows of 64 bytes
     const uint32_t tile = smem_u32(smem) + s * T::stage + warp * (DV / 32) * 2048 + lane * 64;
-    if (!wait(&sh->out, swept)) return false;
-    tc_fence_after();
 #pragma unroll 1
     for (int n = 0; n < DV / 16; ++n) {
       float x[16], y[16];
@@ -904,15 +911,9 @@ struct OutRole {
     return true;
   }
   DM_DEV void run() {
-    int it = 0, swept = 0;
-    bool ok = true;
-    Round r = first_round(g, w);
-    for (int round = 0; ok && round < w.rounds; ++round) {
-      it += r.ahead;
-      Cursor c = r.at;
-      for (int i = 0; ok && i < r.n; ++i, next_block(g, c), ++it, ++swept)
-        ok = block(c.row(g), c.live(g), it, swept);
-      next_round(g, w, r);
+    const int n = sweeps_of(g, w);
+#pragma unroll 1
+    for (int swept = 0; swept < n && block(swept); ++swept) {
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -944,12 +945,12 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     }
     mbar_init(&sh->keys, kStateWarps);
     mbar_init(&sh->block_state, 1);
-    mbar_init(&sh->score, 1);
+    mbar_init(&sh->score, 2);
     mbar_init(&sh->weighted, kWeighWarps);
     mbar_init(&sh->spent, 1);
     mbar_init(&sh->clear, kStateWarps);
     mbar_init(&sh->entry, kStateWarps);
-    mbar_init(&sh->out, 1);
+    mbar_init(&sh->out, 2);
     mbar_init(&sh->taken, kOutWarps);
     mbar_init(&sh->put, kStateWarps);
     mbar_init(&sh->shares, uint32_t(g.split));
@@ -1005,8 +1006,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   } else {
     regs_dec<kOtherRegs>();
     if (warp == kLoadWarp && elect_one()) load_role<DK, DV>(g, w, head, smem, sh);
-    if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(g, w, smem, state, sh);
-    if (warp == kOutMmaWarp && elect_one()) out_mma_role<DK, DV>(g, w, smem, state, sh);
+    if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(g, smem, state, sh);
+    if (warp == kOutMmaWarp && elect_one()) out_mma_role<DK, DV>(g, smem, state, sh);
     __syncwarp();
   }
   __syncthreads();

@@ -42,9 +42,13 @@ constexpr int kLoadWarp = kOutWarp + kOutWarps, kStateMmaWarp = kLoadWarp + 1,
               kOutMmaWarp = kLoadWarp + 2;
 constexpr int kThreads = (kStateWarps + kWeighWarps + kOutWarps + kOtherWarps) * 32;
 // Registers of a thread at launch, and what each kind takes: the shares add up to what the block
-// was launched with.
-constexpr int kRegs = 80, kStateRegs = 120, kWeighRegs = 64, kOutRegs = 64, kOtherRegs = 48;
-static_assert(kStateWarps * kStateRegs + kWeighWarps * kWeighRegs + kOutWarps * kOutRegs +
+// was launched with.  (Exact states keep more at hand; the others gain 1 to 4% by the weights'.)
+constexpr int kRegs = 80, kOutRegs = 64, kOtherRegs = 48;
+__host__ __device__ constexpr int state_regs(bool exact) { return exact ? 120 : 112; }
+__host__ __device__ constexpr int weigh_regs(bool exact) { return exact ? 64 : 72; }
+static_assert(kStateWarps * state_regs(false) + kWeighWarps * weigh_regs(false) + kOutWarps * kOutRegs +
+                      kOtherWarps * kOtherRegs == kThreads / 32 * kRegs, "");
+static_assert(kStateWarps * state_regs(true) + kWeighWarps * weigh_regs(true) + kOutWarps * kOutRegs +
                       kOtherWarps * kOtherRegs == kThreads / 32 * kRegs, "");
 constexpr int kMaxStages = 4;
 constexpr int kSmemBytes = 232448;
@@ -989,14 +993,14 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   tc_fence_after();
 
   if (warp < kStateWarps) {
-    regs_inc<kStateRegs>();
+    regs_inc<state_regs(EXACT)>();
     StateRole<DK, DV, EXACT> r{g, w, sh, smem, state, log_decay, head, cluster, int(threadIdx.x),
                                int(threadIdx.x & 31), int((warp & 3) * 32 + (threadIdx.x & 31)),
                                int(warp >> 2) * (DV / 2)};
     r.run();
     if (EXACT && g.state_out != nullptr) r.pass_through(group * g.split + rank, g.groups * g.split);
   } else if (warp < kOutWarp) {
-    regs_dec<kWeighRegs>();
+    regs_dec<weigh_regs(EXACT)>();
     WeighRole r{g, w, sh, warp - kWeighWarp, int(threadIdx.x & 31)};
     r.run();
   } else if (warp < kLoadWarp) {

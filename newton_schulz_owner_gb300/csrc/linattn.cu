@@ -92,12 +92,12 @@ struct Shared {
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];  // its queries; its output has left their place
   uint64_t score;              // scores in TMEM
   uint64_t weighted;           // weighted scores in TMEM
-  uint64_t spent;              // and read
   uint64_t keys;               // keys decayed, rows past the end cleared
-  uint64_t clear;              // the same of the sweep's blocks, for the output's products
+  uint64_t clear;              // rows past the end cleared in a sweep's block of values
   uint64_t block_state;        // the block's state in TMEM
   uint64_t entry;              // the entering state in shared memory
-  uint64_t out;                // both parts of the output in TMEM
+  uint64_t outer;              // queries times that state in TMEM
+  uint64_t out;                // and the other part of the output; the weighted scores are read
   uint64_t taken;              // and out of it again
   uint64_t put;                // this CTA's share of the round in memory
   uint64_t shares;             // the round's shares of all CTAs of the cluster
@@ -125,7 +125,8 @@ DM_DEV bool await_long(uint64_t* bar, uint32_t parity, int* err, volatile int* f
 }
 // Wait of a whole warp (or one thread); false: gave up.
 DM_DEV bool await(uint64_t* bar, uint32_t parity, int* err, volatile int* flag) {
-  return mbar_try_wait(smem_u32(bar), parity) || await_long(bar, parity, err, flag);
+  return __builtin_expect(mbar_try_wait(smem_u32(bar), parity), 1) ||
+         await_long(bar, parity, err, flag);
 }
 
 // ------------------------------------------------------------------ the packed batch
@@ -228,6 +229,7 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
   const int run = (g.sequences + kThreads - 1) / kThreads;
   const int s0 = min(tid * run, g.sequences), s1 = min(s0 + run, g.sequences);
   int mine = 0;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) mine += extent_of(g, s).blocks;
   int upto = mine;
 #pragma unroll
@@ -250,6 +252,7 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
     const int cut[2] = {int((long long)total * group / g.groups),
                         int((long long)total * (group + 1) / g.groups)};
     int at = first;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const int n = extent_of(g, s).blocks;
 #pragma unroll
@@ -266,6 +269,7 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
   const int flat = g.against ? hi - 1 - i : lo + i;
   if (i < w.nb) {
     int at = first;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const int n = extent_of(g, s).blocks;
       if (at <= flat && flat < at + n) {
@@ -285,6 +289,7 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
 // Blocks that a CTA sweeps in all rounds.
 DM_DEV int sweeps_of(const LinAttnArgs& g, const Work& w) {
   int n = 0;
+#pragma unroll 1
   for (int r = 0; r < w.rounds; ++r)
     n += max(0, min(w.per, w.nb - (r * g.split + w.rank) * w.per));
   return n;
@@ -338,10 +343,12 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
       if (c.m + 1 < c.x.blocks) {
         const int ahead = min(c.m + 1, n);
         c.m -= ahead - 1;
+#pragma unroll 1
         for (int i = 0; i < ahead; ++i, ++c.m)
           if (!load(c, (i == 0 ? kFirst : 0) | (i + 1 == ahead ? kLast : 0))) return;
       }
     }
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       if (!load(at, kSweep | (i == 0 ? kFirst : 0) | (i + 1 == n ? kLast : 0))) return;
       const bool more = i + 1 < n || lo + g.split * w.per < w.nb;
@@ -412,7 +419,7 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Sh
     }
     // the last block's weighted scores have been read (no order is promised between products of
     // unlike shape)
-    if (swept > 0 && !await(&sh->spent, (swept - 1) & 1, g.err, flag)) return;
+    if (swept > 0 && !await(&sh->out, (swept - 1) & 1, g.err, flag)) return;
     tc_fence_after();
 #pragma unroll
     for (int j = 0; j < DK / 16; ++j) {
@@ -421,7 +428,15 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Sh
     }
     umma_commit(&sh->score);
     mbar_arrive(&sh->score);  // and with it what lies in sh->sweep, seen by this thread
+    // the state's part while the scores are weighted
     if (swept > 0 && !await(&sh->taken, (swept - 1) & 1, g.err, flag)) return;
+    if (!await(&sh->entry, swept & 1, g.err, flag)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j)
+      umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
+                ed + uint64_t(j) * 128, id_out, j > 0);
+    umma_commit(&sh->outer);
     if (!await(&sh->clear, swept & 1, g.err, flag)) return;
     if (!await(&sh->weighted, swept & 1, g.err, flag)) return;
     tc_fence_after();
@@ -430,16 +445,9 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Sh
     for (int j = 0; j < 8; ++j)  // 8 columns of weighted scores a step, in two halves
       umma_bf16_ts(tmem + kColInner, tmem + kColScore + (j >> 2) * 64 + (j & 3) * 8,
                    vd + uint64_t(j) * 128, id_out, j > 0);
-    umma_commit(&sh->spent);
-    umma_commit(&sh->empty[s]);
-    if (!await(&sh->entry, swept & 1, g.err, flag)) return;
-    tc_fence_after();
-#pragma unroll
-    for (int j = 0; j < DK / 16; ++j)
-      umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
-                ed + uint64_t(j) * 128, id_out, j > 0);
     umma_commit(&sh->out);
     mbar_arrive(&sh->out);
+    umma_commit(&sh->empty[s]);
     ++swept;
   }
 }
@@ -602,7 +610,7 @@ struct StateRole {
   // Keys of block `it` times their decay, in place; what bf16 drops of them (EXACT) to `low`.  The
   // decay is kept as a sum of two bf16 numbers, so that k a = k a_0 + k a_1 is rounded like an fp32
   // product, two elements at a time, and what its rounding drops comes with two more products.
-  // Rows past the end hold another sequence's tokens, or anything: they become zeros, here and in V.
+  // Rows past the end hold another sequence's tokens, or anything: they become zeros.
   DM_DEV void keys(int it, int live, uint32_t low) {
     const uint32_t stage = smem_u32(smem) + (it % T::stages) * T::stage + tid * 16;
     constexpr int kBatch = 4;  // loads in flight, and rows of a thread
@@ -636,12 +644,15 @@ struct StateRole {
       for (int b = 0; b < kBatch; ++b)
         st_shared_v4(stage + T::q + (n0 + b) * kThreadsHere * 16, x[b][0], x[b][1], x[b][2], x[b][3]);
     }
-    if (live < kMixBlock) {
-#pragma unroll 1
-      for (int n = 0; n < kMixBlock * DV / 8 / kThreadsHere; ++n)
-        if (token_of(n) >= live) st_shared_v4(stage + T::q + T::k + n * kThreadsHere * 16, 0, 0, 0, 0);
-    }
     announce(&sh->keys);
+  }
+  // Rows of values past a sequence's end become zeros, too.
+  DM_DEV void clear_values(const Block& b) {
+    if (__builtin_expect(b.live == kMixBlock, 1)) return;
+    const uint32_t at = smem_u32(smem) + (b.it % T::stages) * T::stage + T::q + T::k + tid * 16;
+#pragma unroll 1
+    for (int n = 0; n < kMixBlock * DV / 8 / kThreadsHere; ++n)
+      if (token_of(n) >= b.live) st_shared_v4(at + n * kThreadsHere * 16, 0, 0, 0, 0);
   }
   DM_DEV bool block_done(int it) { return wait(&sh->block_state, it); }
   // Block `it`, of `live` tokens, joins the state.
@@ -675,61 +686,65 @@ struct StateRole {
   DM_DEV bool all_arrived(int round) {
     return mbar_wait_cluster(&sh->shares, round & 1, &sh->abort) || gave_up(g.err, &sh->abort);
   }
-  DM_DEV bool share_block(const Block& b, int round) {
+  // What a block needs before its keys, ahead of the sweep and in it.
+  DM_DEV bool begin_share(const Block& b) {
     if (b.kind & kFirst) {
       if (over() && b.m == 0) keep_initial(b.seq);
       zero();
     }
+    clear_values(b);
     // the low parts go where queries would be, once the output before them has left
-    const int s = b.it % T::stages;
-    if (!wait(&sh->q_full[s], b.it / T::stages)) return false;
-    keys(b.it, b.live, smem_u32(smem) + s * T::stage);
-    if (!block_done(b.it)) return false;
-    add_block(b.live);
-    if (!(b.kind & kLast)) return true;
-    put(slot(w.rank, round & 1));
-    return arrive(round);
+    return wait(&sh->q_full[b.it % T::stages], b.it / T::stages);
   }
-  DM_DEV bool sweep_block(const Block& b, int swept, int round, int share_seq) {
+  DM_DEV bool begin_sweep(const Block& b, int swept, int round, int share_seq) {
     const bool first = (b.kind & kFirst) != 0 && g.split > 1;
-    if (first && ((share_seq < 0 && !arrive(round)) || !all_arrived(round))) return false;
-    if (b.m == 0 || first) enter(b, round, share_seq);
-    if (!wait(&sh->score, swept)) return false;
-    // exact: the low parts take the place of the state that entered the last block, and the one
-    // that enters this block theirs
-    if (EXACT && swept > 0 && !wait(&sh->out, swept - 1)) return false;
-    keys(b.it, b.live, smem_u32(entry));
-    if (lane == 0) mbar_arrive(&sh->clear);
-    if (EXACT ? !block_done(b.it) : swept > 0 && !wait(&sh->out, swept - 1)) return false;
+    if (__builtin_expect(b.m == 0 || first, 0)) {
+      if (first && ((share_seq < 0 && !arrive(round)) || !all_arrived(round))) return false;
+      enter(b, round, share_seq);
+    }
+    // the place of the state that enters is free (exact: since the low parts there were read)
+    if (!EXACT && swept > 0 && !wait(&sh->outer, swept - 1)) return false;
     write_entry();
-    if (!EXACT && !block_done(b.it)) return false;
-    add_block(b.live);
-    if (EXACT && g.state_out != nullptr && b.m + 1 == b.blocks) write_final(b.seq);
-    return true;
+    clear_values(b);
+    announce(&sh->clear);
+    if (!wait(&sh->score, swept)) return false;
+    return !EXACT || wait(&sh->outer, swept);  // the low parts take that place
   }
   DM_DEV void run() {
     zero();
     int swept = 0, round = 0, share_seq = -1;
 #pragma unroll 1
     for (int it = 0;; ++it) {
-      if (!wait(&sh->full[it % T::stages], it / T::stages)) return;
+      const int s = it % T::stages;
+      if (!wait(&sh->full[s], it / T::stages)) return;
       const Block b = sh->block[it % kRing];
-      if (b.kind & kEnd) break;
-      if (b.kind & kSweep) {
-        if (!sweep_block(b, swept, round, share_seq)) return;
+      if (__builtin_expect((b.kind & kEnd) != 0, 0)) break;
+      const bool sweep = (b.kind & kSweep) != 0;
+      if (__builtin_expect(sweep, 1)) {
+        if (!begin_sweep(b, swept, round, share_seq)) return;
         ++swept;
-        if (b.kind & kLast) {
+      } else {
+        if (!begin_share(b)) return;
+        share_seq = b.seq;
+      }
+      keys(it, b.live, sweep ? smem_u32(entry) : smem_u32(smem) + s * T::stage);
+      if (!block_done(it)) return;
+      add_block(b.live);
+      if (EXACT && __builtin_expect(sweep && g.state_out != nullptr && b.m + 1 == b.blocks, 0))
+        write_final(b.seq);
+      if (__builtin_expect((b.kind & kLast) != 0, 0)) {
+        // its share, or the last CTA's: what the round leaves to the next
+        const bool leaves = w.rank + 1 == g.split && round + 1 < w.rounds;
+        if (!sweep || leaves) put(slot(w.rank, (round + (sweep ? 1 : 0)) & 1));
+        if (!sweep && !arrive(round)) return;
+        if (sweep) {
           ++round;
           share_seq = -1;
-          // what the round leaves to the next
-          if (w.rank + 1 == g.split && round < w.rounds) put(slot(w.rank, round & 1));
         }
-      } else {
-        if (!share_block(b, round)) return;
-        share_seq = b.seq;
       }
     }
     // rounds in which only CTAs before this one have blocks
+#pragma unroll 1
     for (; g.split > 1 && round < w.rounds; ++round)
       if (!arrive(round) || !all_arrived(round)) return;
   }
@@ -886,7 +901,7 @@ struct OutRole {
     if (lane == 0) mbar_arrive(&sh->taken);
     const int first = row0 + warp * 32;
     const int rows = live - warp * 32;  // of this warp that exist
-    if (rows >= 32) {
+    if (__builtin_expect(rows >= 32, 1)) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -951,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     mbar_init(&sh->block_state, 1);
     mbar_init(&sh->score, 2);
     mbar_init(&sh->weighted, kWeighWarps);
-    mbar_init(&sh->spent, 1);
+    mbar_init(&sh->outer, 1);
     mbar_init(&sh->clear, kStateWarps);
     mbar_init(&sh->entry, kStateWarps);
     mbar_init(&sh->out, 2);

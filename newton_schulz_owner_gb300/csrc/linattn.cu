@@ -92,10 +92,9 @@ struct Shared {
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];  // its queries; its output has left their place
   uint64_t score;              // scores in TMEM
   uint64_t weighted;           // weighted scores in TMEM
-  uint64_t keys;               // keys decayed, rows past the end cleared
-  uint64_t clear;              // rows past the end cleared in a sweep's block of values
+  uint64_t keys[2];            // keys of the first and last 64 tokens decayed, rows past the end cleared
   uint64_t block_state;        // the block's state in TMEM
-  uint64_t entry;              // the entering state in shared memory
+  uint64_t entry;              // the entering state in shared memory (and values past the end cleared)
   uint64_t outer;              // queries times that state in TMEM
   uint64_t out;                // and the other part of the output; the weighted scores are read
   uint64_t taken;              // and out of it again
@@ -369,10 +368,11 @@ DM_DEV void state_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, 
   const uint32_t to = sh->tmem + kColState;
   // (a^..k)^T V, rows of K in steps of 16 tokens.  With 64 key elements the upper half of the
   // 128 rows reads what follows the tile; those lanes of the result are not used.
-  auto product = [&](uint32_t k, uint32_t v, bool accumulate) {
-    const uint64_t a = sdesc_sw128(k, 16384, 1024), b = sdesc_sw128(v, 16384, 1024);
+  auto product = [&](uint32_t k, uint32_t v, int half, bool accumulate) {
+    const uint64_t a = sdesc_sw128(k, 16384, 1024) + uint64_t(half) * 512,
+                   b = sdesc_sw128(v, 16384, 1024) + uint64_t(half) * 512;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
       umma_bf16(to, a + uint64_t(j) * 128, b + uint64_t(j) * 128, id, accumulate || j > 0);
   };
 #pragma unroll 1
@@ -382,11 +382,16 @@ DM_DEV void state_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, 
     if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
     const int kind = sh->block[it % kRing].kind;
     if (kind & kEnd) return;
-    if (!await(&sh->keys, it & 1, g.err, flag)) return;  // the last block's state is added by then
-    tc_fence_after();
-    product(k, v, false);
-    // the keys' low parts lie where queries would, or the state that enters will
-    if (EXACT) product(kind & kSweep ? smem_u32(state) : q, v, true);
+    // the keys' low parts lie where queries would, or the state that enters did
+    const uint32_t low = kind & kSweep ? smem_u32(state) : q;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      // the last block's state is added by then
+      if (!await(&sh->keys[half], it & 1, g.err, flag)) return;
+      tc_fence_after();
+      product(k, v, half, half > 0);
+      if (EXACT) product(low, v, half, true);
+    }
     umma_commit(&sh->block_state);
     umma_commit(&sh->empty[s]);
     if (!(kind & kSweep)) {  // in the place of the output's warps
@@ -437,7 +442,6 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Sh
       umma_bf16(tmem + kColOuter, qd + uint64_t(j >> 2) * 1024 + uint64_t(j & 3) * 2,
                 ed + uint64_t(j) * 128, id_out, j > 0);
     umma_commit(&sh->outer);
-    if (!await(&sh->clear, swept & 1, g.err, flag)) return;
     if (!await(&sh->weighted, swept & 1, g.err, flag)) return;
     tc_fence_after();
     const uint64_t vd = sdesc_sw128(v, 16384, 1024);
@@ -613,38 +617,38 @@ struct StateRole {
   // Rows past the end hold another sequence's tokens, or anything: they become zeros.
   DM_DEV void keys(int it, int live, uint32_t low) {
     const uint32_t stage = smem_u32(smem) + (it % T::stages) * T::stage + tid * 16;
-    constexpr int kBatch = 4;  // loads in flight, and rows of a thread
-    uint32_t w0[kBatch], w1[kBatch], mask[kBatch];
+    low += tid * 16;
+    // tokens 0 .. 63, then the rest: the products of the first half start while the second is made
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const float f = key_weight(token_of(b), live);
-      w0[b] = pack_bf16(f, f);
-      const float rest = f - bf16_lo(w0[b]);
-      w1[b] = pack_bf16(rest, rest);
-      mask[b] = token_of(b) < live ? 0xFFFFFFFFu : 0u;
-    }
-#pragma unroll
-    for (int n0 = 0; n0 < kUnits; n0 += kBatch) {
+    for (int half = 0; half < 2; ++half) {
+      constexpr int kBatch = kUnits / 2;  // loads in flight: two tokens, in one or two panels
       uint32_t x[kBatch][4];
+      auto unit = [&](int b) { return (half * 2 + (b & 1) + (b >> 1) * 4) * kThreadsHere * 16; };
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
-        ld_shared_v4(stage + T::q + (n0 + b) * kThreadsHere * 16, x[b][0], x[b][1], x[b][2], x[b][3]);
+        ld_shared_v4(stage + T::q + unit(b), x[b][0], x[b][1], x[b][2], x[b][3]);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        uint32_t y[4];
+      for (int e = 0; e < 2; ++e) {
+        const int j = token_of(half * 2 + e);
+        const float f = key_weight(j, live);
+        const uint32_t w0 = pack_bf16(f, f), mask = j < live ? 0xFFFFFFFFu : 0u;
+        const float rest = f - bf16_lo(w0);
+        const uint32_t w1 = pack_bf16(rest, rest);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t k = x[b][i] & mask[b];
-          x[b][i] = bf16_fma2(k, w0[b], bf16_mul2(k, w1[b]));
-          if (EXACT) y[i] = bf16_fma2(k, w1[b], bf16_fma2(k, w0[b], x[b][i] ^ 0x80008000u));
+        for (int b = e; b < kBatch; b += 2) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t k = x[b][i] & mask;
+            x[b][i] = bf16_fma2(k, w0, bf16_mul2(k, w1));
+            if (EXACT) y[i] = bf16_fma2(k, w1, bf16_fma2(k, w0, x[b][i] ^ 0x80008000u));
+          }
+          st_shared_v4(stage + T::q + unit(b), x[b][0], x[b][1], x[b][2], x[b][3]);
+          if (EXACT) st_shared_v4(low + unit(b), y[0], y[1], y[2], y[3]);
         }
-        if (EXACT) st_shared_v4(low + tid * 16 + (n0 + b) * kThreadsHere * 16, y[0], y[1], y[2], y[3]);
       }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        st_shared_v4(stage + T::q + (n0 + b) * kThreadsHere * 16, x[b][0], x[b][1], x[b][2], x[b][3]);
+      announce(&sh->keys[half]);
     }
-    announce(&sh->keys);
   }
   // Rows of values past a sequence's end become zeros, too.
   DM_DEV void clear_values(const Block& b) {
@@ -661,13 +665,15 @@ struct StateRole {
     const float f = sh->power[live];
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(row & ~31) << 16) + kColState + col;
+    float x[2][16];
+    tmem_ld16(at, x[0]);
 #pragma unroll
     for (int c = 0; c < kCols / 16; ++c) {
-      float x[16];
-      tmem_ld16(at + c * 16, x);
       tmem_ld_wait();
+      if (c + 1 < kCols / 16) tmem_ld16(at + (c + 1) * 16, x[(c + 1) & 1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) st[c * 8 + i] = fma2(ff, st[c * 8 + i], f2(x[2 * i], x[2 * i + 1]));
+      for (int i = 0; i < 8; ++i)
+        st[c * 8 + i] = fma2(ff, st[c * 8 + i], f2(x[c & 1][2 * i], x[c & 1][2 * i + 1]));
     }
     if (row >= g.dk) zero();  // of keys past the head's size: 0 times an infinity of V may be there
     tc_fence_before();
@@ -702,23 +708,21 @@ struct StateRole {
       if (first && ((share_seq < 0 && !arrive(round)) || !all_arrived(round))) return false;
       enter(b, round, share_seq);
     }
-    // the place of the state that enters is free (exact: since the low parts there were read)
-    if (!EXACT && swept > 0 && !wait(&sh->outer, swept - 1)) return false;
-    write_entry();
     clear_values(b);
-    announce(&sh->clear);
+    // The scores are there, so the last block's products are done and with them (exact: since its
+    // low parts were read) the place of the state that enters is free.
     if (!wait(&sh->score, swept)) return false;
+    write_entry();
     return !EXACT || wait(&sh->outer, swept);  // the low parts take that place
   }
   DM_DEV void run() {
     zero();
     int swept = 0, round = 0, share_seq = -1;
+    if (!wait(&sh->full[0], 0)) return;
+    Block b = sh->block[0];
 #pragma unroll 1
-    for (int it = 0;; ++it) {
-      const int s = it % T::stages;
-      if (!wait(&sh->full[s], it / T::stages)) return;
-      const Block b = sh->block[it % kRing];
-      if (__builtin_expect((b.kind & kEnd) != 0, 0)) break;
+    for (int it = 0; (b.kind & kEnd) == 0; ++it) {
+      const int s = it % T::stages, s1 = (it + 1) % T::stages;
       const bool sweep = (b.kind & kSweep) != 0;
       if (__builtin_expect(sweep, 1)) {
         if (!begin_sweep(b, swept, round, share_seq)) return;
@@ -728,6 +732,9 @@ struct StateRole {
         share_seq = b.seq;
       }
       keys(it, b.live, sweep ? smem_u32(entry) : smem_u32(smem) + s * T::stage);
+      // while the product runs, the next block
+      if (!wait(&sh->full[s1], (it + 1) / T::stages)) return;
+      const Block next = sh->block[(it + 1) % kRing];
       if (!block_done(it)) return;
       add_block(b.live);
       if (EXACT && __builtin_expect(sweep && g.state_out != nullptr && b.m + 1 == b.blocks, 0))
@@ -742,6 +749,7 @@ struct StateRole {
           share_seq = -1;
         }
       }
+      b = next;
     }
     // rounds in which only CTAs before this one have blocks
 #pragma unroll 1
@@ -962,12 +970,12 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
       mbar_init(&sh->q_full[s], 1);
       mbar_init(&sh->q_empty[s], kOutWarps);
     }
-    mbar_init(&sh->keys, kStateWarps);
+    mbar_init(&sh->keys[0], kStateWarps);
+    mbar_init(&sh->keys[1], kStateWarps);
     mbar_init(&sh->block_state, 1);
     mbar_init(&sh->score, 2);
     mbar_init(&sh->weighted, kWeighWarps);
     mbar_init(&sh->outer, 1);
-    mbar_init(&sh->clear, kStateWarps);
     mbar_init(&sh->entry, kStateWarps);
     mbar_init(&sh->out, 2);
     mbar_init(&sh->taken, kOutWarps);

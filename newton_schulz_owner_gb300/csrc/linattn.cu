@@ -24,8 +24,9 @@
 // cut evenly into stretches of blocks wherever sequences begin and end.  A CTA whose last sequence
 // goes on in the next one's stretch first sums that sequence's share of the state alone (keys and
 // values), the shares go to the CTAs behind it through memory, and then each CTA sweeps its
-// stretch, keys and values coming from L2 the second time.  Long batches go in rounds of at most
-// kRoundBlocks blocks a CTA, so that a round's keys and values stay in L2.
+// stretch.  (Sharing again and again, in rounds short enough for keys and values to stay in L2, was
+// slower the shorter the rounds: 65536 tokens of 32 heads 829 us in rounds of 12 blocks a CTA, 797
+// of 16, 747 of 64, 738 in one.)
 #include "dmuon.h"
 #include "f32x2.cuh"
 #include "mix.h"
@@ -57,7 +58,6 @@ constexpr uint32_t kTmemCols = 512;
 // TMEM columns: scores (then the weighted ones), the block's own state, two parts of the output
 constexpr uint32_t kColScore = 0, kColState = 128, kColInner = 256, kColOuter = 384;
 constexpr long long kAbortSettleCycles = 2000000;
-constexpr int kRoundBlocks = 16;
 
 // DK, DV: head sizes padded to 64 or 128 (TMA fills with zeros).
 template <int DK, int DV>
@@ -75,7 +75,7 @@ struct Tiles {
 // What the warps need of a block, in the order of the CTA's work: written with its loads.
 enum BlockKind {
   kSweep = 1,  // swept; without it only summed, for the CTAs behind this one
-  kFirst = 2,  // of its kind in its round
+  kFirst = 2,  // of its kind
   kLast = 4,
   kEnd = 8     // no block: all are done
 };
@@ -98,8 +98,8 @@ struct Shared {
   uint64_t outer;              // queries times that state in TMEM
   uint64_t out;                // and the other part of the output; the weighted scores are read
   uint64_t taken;              // and out of it again
-  uint64_t put;                // this CTA's share of the round in memory
-  uint64_t shares;             // the round's shares of all CTAs of the cluster
+  uint64_t put;                // this CTA's share in memory
+  uint64_t shares;             // those of all CTAs of the cluster
   Block block[kRing];          // by number
   Block sweep[kRing];          // the swept ones by theirs
   uint32_t tmem;
@@ -169,11 +169,11 @@ DM_DEV Cursor skipped(const LinAttnArgs& g, Cursor c, int n) {
   c.m += n;
   return c;
 }
-// What a CTA does: stretches of `per` blocks, one in each round, of the nb blocks that its cluster
-// takes.
+// What a CTA does: n blocks from `start` on, of the nb blocks that its cluster takes in stretches of
+// `per`.
 struct Work {
-  int nb, per, rounds, rank;
-  Cursor start;  // the first round's
+  int nb, per, n, rank;
+  Cursor start;
 };
 // Blocks of all sequences are numbered in their order; sequences are dealt to the clusters of a
 // head by the block that they start with, and the blocks of a cluster evenly to its CTAs.  Every
@@ -182,8 +182,8 @@ DM_DEV Work divide(const LinAttnArgs& g, int rank, int nb) {
   Work w;
   w.nb = nb;
   w.rank = rank;
-  w.rounds = g.split == 1 ? 1 : max(1, (nb + g.split * kRoundBlocks - 1) / (g.split * kRoundBlocks));
-  w.per = (nb + g.split * w.rounds - 1) / (g.split * w.rounds);
+  w.per = (nb + g.split - 1) / g.split;
+  w.n = max(0, min(w.per, nb - rank * w.per));
   w.start.seq = 0;
   w.start.m = 0;
   w.start.x = Extent{0, 0, 0x7FFFFFFF};
@@ -209,8 +209,8 @@ DM_DEV Work locate_few(const LinAttnArgs& g, int group, int rank) {
     hi = __reduce_min_sync(0xffffffffu, x.blocks > 0 && first >= b ? first : total);
   }
   Work w = divide(g, rank, hi - lo);
-  const int i = min(rank * w.per, w.nb);
-  if (i < w.nb) {
+  const int i = rank * w.per;
+  if (w.n > 0) {
     const int flat = g.against ? hi - 1 - i : lo + i;
     const unsigned has = __ballot_sync(0xffffffffu, first <= flat && flat < first + x.blocks);
     const int s = __ffs(has) - 1;
@@ -264,9 +264,9 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
     hi = sh->place[1];
   }
   Work w = divide(g, rank, hi - lo);
-  const int i = min(rank * w.per, w.nb);
+  const int i = rank * w.per;
   const int flat = g.against ? hi - 1 - i : lo + i;
-  if (i < w.nb) {
+  if (w.n > 0) {
     int at = first;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
@@ -285,18 +285,9 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
   return w;
 }
 
-// Blocks that a CTA sweeps in all rounds.
-DM_DEV int sweeps_of(const LinAttnArgs& g, const Work& w) {
-  int n = 0;
-#pragma unroll 1
-  for (int r = 0; r < w.rounds; ++r)
-    n += max(0, min(w.per, w.nb - (r * g.split + w.rank) * w.per));
-  return n;
-}
-
 // ------------------------------------------------------------------ loads
-// The one walk through the batch: in each round the CTA's stretch from its last sequence on, if that
-// goes on in the next CTA's, and then the whole stretch.
+// The one walk through the batch: the CTA's stretch from its last sequence on, if that goes on in
+// the next CTA's, and then the whole stretch.
 template <int DK, int DV>
 DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* smem, Shared* sh) {
   using T = Tiles<DK, DV>;
@@ -335,24 +326,20 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
     return true;
   };
   Cursor at = w.start;
-  for (int lo = w.rank * w.per; lo < w.nb; lo += g.split * w.per) {
-    const int n = min(w.per, w.nb - lo);
-    if (w.rank + 1 < g.split) {
-      Cursor c = skipped(g, at, n - 1);
-      if (c.m + 1 < c.x.blocks) {
-        const int ahead = min(c.m + 1, n);
-        c.m -= ahead - 1;
+  if (w.rank + 1 < g.split && w.n > 0) {
+    Cursor c = skipped(g, at, w.n - 1);
+    if (c.m + 1 < c.x.blocks) {
+      const int ahead = min(c.m + 1, w.n);
+      c.m -= ahead - 1;
 #pragma unroll 1
-        for (int i = 0; i < ahead; ++i, ++c.m)
-          if (!load(c, (i == 0 ? kFirst : 0) | (i + 1 == ahead ? kLast : 0))) return;
-      }
+      for (int i = 0; i < ahead; ++i, ++c.m)
+        if (!load(c, (i == 0 ? kFirst : 0) | (i + 1 == ahead ? kLast : 0))) return;
     }
+  }
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      if (!load(at, kSweep | (i == 0 ? kFirst : 0) | (i + 1 == n ? kLast : 0))) return;
-      const bool more = i + 1 < n || lo + g.split * w.per < w.nb;
-      if (more) at = skipped(g, at, i + 1 < n ? 1 : 1 + g.split * w.per - n);
-    }
+  for (int i = 0; i < w.n; ++i) {
+    if (!load(at, kSweep | (i == 0 ? kFirst : 0))) return;
+    if (i + 1 < w.n) at = skipped(g, at, 1);
   }
   (void)load(at, kEnd);
 }
@@ -511,8 +498,7 @@ struct StateRole {
     }
   }
   // A state in the workspace, four columns at a time so that a warp's rows lie together.  Slots of
-  // a CTA: its share of even and of odd rounds (the last CTA's: what the round leaves to the
-  // next), and a copy of the first state of the sequence that it begins and others end.
+  // a CTA: its share, and a copy of the first state of the sequence that it begins and others end.
   DM_DEV float4* slot(int rank, int which) const {
     return reinterpret_cast<float4*>(g.local) +
            (((size_t)cluster * g.split + rank) * kMixSlots + which) * (kMixLocalBytes / 16) +
@@ -530,7 +516,7 @@ struct StateRole {
   // A final state may be written over the first one while other CTAs have yet to read that.
   DM_DEV bool over() const { return g.split > 1 && g.state_in != nullptr && g.state_in == g.state_out; }
   DM_DEV void keep_initial(int seq) {
-    float4* to = slot(w.rank, 2);
+    float4* to = slot(w.rank, 1);
     const float* p = g.state_in + state_at(seq) + row * g.st_row + col * g.st_col;
 #pragma unroll 1
     for (int i = 0; i < kCols / 4; ++i, p += 4 * g.st_col) {
@@ -545,20 +531,18 @@ struct StateRole {
   DM_DEV int before(const Block& b, int n) const {
     return g.against ? b.len - min(b.len, (b.blocks - n) * kMixBlock) : min(b.len, n * kMixBlock);
   }
-  // The state before block b: a sequence's first state, or (the first block of a CTA's round, inside
-  // a sequence) that of its start or of the round's, and the shares of the CTAs before this one.
-  DM_DEV void enter(const Block& b, int round, int share_seq) {
-    const int base = round * g.split * w.per;            // sweep's number of the round's first block
-    const int start = base + w.rank * w.per - b.m;        // and of the sequence's, if b is the CTA's first
-    const bool inside = b.m > 0, older = inside && start < base;
-    const int from = older ? 0 : inside ? (start - base) / w.per : w.rank;
+  // The state before block b: a sequence's first state, and for a CTA that begins inside the
+  // sequence the shares of the CTAs before it.
+  DM_DEV void enter(const Block& b, bool first, int share_seq) {
+    const bool inside = first && b.m > 0;
+    const int start = w.rank * w.per - b.m;  // sweep's number of the sequence's first block
+    const int from = inside ? start / w.per : w.rank;
     zero();
     const float4* p = nullptr;
-    if (older) p = slot(g.split - 1, round & 1);
-    else if (over() && (inside || b.seq == share_seq)) p = slot(from, 2);
+    if (over() && (inside || b.seq == share_seq)) p = slot(from, 1);
     else read_initial(b.seq);
     // lane r: the decay over rank r's part of the sequence
-    const int n0 = max(base + lane * w.per - start, 0), n1 = base + (lane + 1) * w.per - start;
+    const int n0 = max(lane * w.per - start, 0), n1 = (lane + 1) * w.per - start;
     const float decay =
         lane >= from && lane < w.rank ? expf(log_decay * float(before(b, n1) - before(b, n0))) : 0.f;
     constexpr int kPart = 4;  // of 4 columns each, so that several ranks' loads are in flight
@@ -576,7 +560,7 @@ struct StateRole {
       for (int r = from; r < w.rank; ++r) {
         const float f = __shfl_sync(0xffffffffu, decay, r);
         const F2 ff = f2(f, f);
-        const float4* q = slot(r, round & 1);
+        const float4* q = slot(r, 0);
 #pragma unroll
         for (int i = i0; i < i0 + kPart; ++i) {
           const float4 v = __ldcg(q + i * 128);
@@ -678,19 +662,19 @@ struct StateRole {
     if (row >= g.dk) zero();  // of keys past the head's size: 0 times an infinity of V may be there
     tc_fence_before();
   }
-  // The share of this round is in memory (or was not asked for): tell the cluster.
-  DM_DEV bool arrive(int round) {
+  // This CTA's share is in memory (or it has none): tell the cluster.
+  DM_DEV bool arrive() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->put);
     if (tid < 32) {
-      if (!wait(&sh->put, round)) return false;
+      if (!wait(&sh->put, 0)) return false;
       if (tid < g.split) mbar_arrive_cluster(mapa_shared(smem_u32(&sh->shares), uint32_t(tid)));
       __syncwarp();
     }
     return true;
   }
-  DM_DEV bool all_arrived(int round) {
-    return mbar_wait_cluster(&sh->shares, round & 1, &sh->abort) || gave_up(g.err, &sh->abort);
+  DM_DEV bool all_arrived() {
+    return mbar_wait_cluster(&sh->shares, 0, &sh->abort) || gave_up(g.err, &sh->abort);
   }
   // What a block needs before its keys, ahead of the sweep and in it.
   DM_DEV bool begin_share(const Block& b) {
@@ -702,11 +686,11 @@ struct StateRole {
     // the low parts go where queries would be, once the output before them has left
     return wait(&sh->q_full[b.it % T::stages], b.it / T::stages);
   }
-  DM_DEV bool begin_sweep(const Block& b, int swept, int round, int share_seq) {
-    const bool first = (b.kind & kFirst) != 0 && g.split > 1;
+  DM_DEV bool begin_sweep(const Block& b, int swept, int share_seq) {
+    const bool first = (b.kind & kFirst) != 0;
     if (__builtin_expect(b.m == 0 || first, 0)) {
-      if (first && ((share_seq < 0 && !arrive(round)) || !all_arrived(round))) return false;
-      enter(b, round, share_seq);
+      if (first && b.m > 0 && !all_arrived()) return false;
+      enter(b, first, share_seq);
     }
     clear_values(b);
     // The scores are there, so the last block's products are done and with them (exact: since its
@@ -717,15 +701,16 @@ struct StateRole {
   }
   DM_DEV void run() {
     zero();
-    int swept = 0, round = 0, share_seq = -1;
+    int swept = 0, share_seq = -1;
     if (!wait(&sh->full[0], 0)) return;
     Block b = sh->block[0];
+    if (g.split > 1 && (b.kind == kEnd || (b.kind & kSweep)) && !arrive()) return;  // it has no share
 #pragma unroll 1
     for (int it = 0; (b.kind & kEnd) == 0; ++it) {
       const int s = it % T::stages, s1 = (it + 1) % T::stages;
       const bool sweep = (b.kind & kSweep) != 0;
       if (__builtin_expect(sweep, 1)) {
-        if (!begin_sweep(b, swept, round, share_seq)) return;
+        if (!begin_sweep(b, swept, share_seq)) return;
         ++swept;
       } else {
         if (!begin_share(b)) return;
@@ -740,21 +725,11 @@ struct StateRole {
       if (EXACT && __builtin_expect(sweep && g.state_out != nullptr && b.m + 1 == b.blocks, 0))
         write_final(b.seq);
       if (__builtin_expect((b.kind & kLast) != 0, 0)) {
-        // its share, or the last CTA's: what the round leaves to the next
-        const bool leaves = w.rank + 1 == g.split && round + 1 < w.rounds;
-        if (!sweep || leaves) put(slot(w.rank, (round + (sweep ? 1 : 0)) & 1));
-        if (!sweep && !arrive(round)) return;
-        if (sweep) {
-          ++round;
-          share_seq = -1;
-        }
+        put(slot(w.rank, 0));
+        if (!arrive()) return;
       }
       b = next;
     }
-    // rounds in which only CTAs before this one have blocks
-#pragma unroll 1
-    for (; g.split > 1 && round < w.rounds; ++round)
-      if (!arrive(round) || !all_arrived(round)) return;
   }
   // Sequences without tokens: their states pass through.
   DM_DEV void pass_through(int first, int stride) {
@@ -847,7 +822,7 @@ struct WeighRole {
   DM_DEV void run() {
     const float f = g.scale * sh->power[g.against ? 31 - lane : lane];
     const F2 own = f2(f, f);
-    const int n = sweeps_of(g, w);
+    const int n = w.n;
     if (g.against) {
 #pragma unroll 1
       for (int swept = 0; swept < n && block<true>(swept, own); ++swept) {
@@ -938,7 +913,7 @@ struct OutRole {
     return true;
   }
   DM_DEV void run() {
-    const int n = sweeps_of(g, w);
+    const int n = w.n;
 #pragma unroll 1
     for (int swept = 0; swept < n && block(swept); ++swept) {
     }

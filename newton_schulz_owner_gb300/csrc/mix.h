@@ -61,7 +61,7 @@ struct LinAttnArgs {
 constexpr int kMixBlock = 128;   // tokens taken at a time
 constexpr int kMixMaxSplit = 8;
 constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a state
-constexpr int kMixSlots = 3;            // states of a CTA in the workspace
+constexpr int kMixSlots = 2;            // states of a CTA in the workspace
 constexpr int64_t kMixMaxCtas = 320;    // of a launch whose sequences are shared
 cudaError_t linattn_prepare();  // once per device
 // Sweeps of one launch: of the same sizes (padded to 64 or 128), sharing and precision.

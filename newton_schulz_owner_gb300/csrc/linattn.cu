@@ -1041,7 +1041,7 @@ MixKernel kernel_for(int dk, int dv, bool exact, int* smem) {
 
 }  // namespace
 
-cudaError_t linattn_prepare() {
+cudaError_t linattn_prepare(int (&fit)[kMixMaxSplit + 1]) {
   for (int i = 0; i < 8; ++i) {
     int smem = 0;
     const MixKernel k = kernel_for(i & 1 ? 128 : 64, i & 2 ? 128 : 64, (i & 4) != 0, &smem);
@@ -1051,6 +1051,24 @@ cudaError_t linattn_prepare() {
     if (e != cudaSuccess) return e;
     // launched with fewer, the states' warps would wait for theirs forever
     if (a.numRegs != kRegs) return cudaErrorInvalidKernelImage;
+    if (i > 0) continue;
+    fit[0] = 0;
+    for (int split = 1; split <= kMixMaxSplit; ++split) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(unsigned(split), 1, 1);
+      cfg.blockDim = dim3(kThreads, 1, 1);
+      cfg.dynamicSmemBytes = size_t(smem);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = unsigned(split);
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit[split], k, &cfg);
+      if (e != cudaSuccess) return e;
+      if (fit[split] < 1) return cudaErrorInvalidConfiguration;
+    }
   }
   return cudaSuccess;
 }

@@ -63,7 +63,8 @@ constexpr int kMixMaxSplit = 8;
 constexpr size_t kMixLocalBytes = size_t(128) * 128 * 4;  // of a state
 constexpr int kMixSlots = 2;            // states of a CTA in the workspace
 constexpr int64_t kMixMaxCtas = 320;    // of a launch whose sequences are shared
-cudaError_t linattn_prepare();  // once per device
+// Once per device: shared memory opt-in; fit[n] is how many clusters of n CTAs run at once.
+cudaError_t linattn_prepare(int (&fit)[kMixMaxSplit + 1]);
 // Sweeps of one launch: of the same sizes (padded to 64 or 128), sharing and precision.
 struct LinAttnSweeps {
   LinAttnArgs sweep[3];

@@ -24,18 +24,25 @@ using bf16 = __nv_bfloat16;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Ready the current device: the kernels' shared memory opt-in, once.
-int device_ready(int* sms) {
-  int d = 0, clusters = 0;
-  const int st = library_device(&d, sms, &clusters);
+// Ready the current device, once: the kernels' shared memory opt-in, and how many clusters fit.
+struct Device {
+  int sms;
+  int fit[kMixMaxSplit + 1];
+};
+int device_ready(Device* device) {
+  int d = 0, clusters = 0, sms = 0;
+  const int st = library_device(&d, &sms, &clusters);
   if (st != DMUON_OK) return st;
   static std::mutex mu;
   static bool ready[kMaxDevices] = {};
+  static Device known[kMaxDevices];
   std::lock_guard<std::mutex> lk(mu);
   if (!ready[d]) {
-    if (linattn_prepare() != cudaSuccess) return DMUON_ERR_CUDA;
+    if (linattn_prepare(known[d].fit) != cudaSuccess) return DMUON_ERR_CUDA;
+    known[d].sms = sms;
     ready[d] = true;
   }
+  *device = known[d];
   return DMUON_OK;
 }
 
@@ -162,8 +169,8 @@ int qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* const x[2],
   // a warp takes 4 heads at least
   if (s.tokens * (ceil_div(heads[0], 4) + ceil_div(heads[1], 4)) > INT32_MAX)
     return DMUON_ERR_UNSUPPORTED;
-  int sms = 0;
-  const int e = device_ready(&sms);
+  Device device;
+  const int e = device_ready(&device);
   if (e != DMUON_OK) return e;
   for (int i = 0; i < 2; ++i) {
     g.w[i] = static_cast<const bf16*>(w[i]);
@@ -177,7 +184,7 @@ int qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* const x[2],
   g.rotary = int(s.rotary_dim);
   g.eps = s.eps;
   g.partial = dw[0] != nullptr || dw[1] != nullptr ? partial : nullptr;
-  return launch_rope(g, backward, s.interleaved != 0, vec, sms, st) == cudaSuccess
+  return launch_rope(g, backward, s.interleaved != 0, vec, device.sms, st) == cudaSuccess
              ? DMUON_OK
              : DMUON_ERR_CUDA;
 }
@@ -196,29 +203,33 @@ struct Share {
   int groups, split;
 };
 // Microseconds, measured with 128 elements to a head: a block takes 3 (exact states 3.8), 1.5 more
-// (2) where a CTA sums its share ahead; a launch 6, an exchange of shares 5 (8192 tokens of 32 heads:
-// 97 with four CTAs to a head, 205 with one).
-Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, int sms) {
+// (2) where a CTA sums its share ahead; a launch 6, sharing 5.  Clusters of a size that the GPU's
+// groups of SMs do not divide into run fewer at a time (gradients of 8192 tokens of 8 heads: 24
+// clusters of 6 111 us, of 4 77).
+Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const Device& device) {
   const int64_t blocks = s.tokens / kMixBlock + std::min(s.sequences, s.tokens);  // at most
+  const double one = double(blocks) / double(s.sequences);
   const double sweep = exact ? 3.8 : 3.0, ahead = exact ? 2.0 : 1.5;
   Share best{1, 1};
   double least = 0;
   for (int64_t groups = 1; groups <= s.sequences && groups <= 64; ++groups) {
+    const int64_t clusters = sweeps * s.heads * groups;
     for (int split = 1; split <= kMixMaxSplit; ++split) {
-      const int64_t ctas = sweeps * s.heads * groups * split;
       if (groups * split > blocks && groups * split > 1) break;
-      if (split > 1 && ctas > kMixMaxCtas) break;
-      // clusters end where sequences do: the largest has about a sequence more than its part
-      const double part = double(blocks) / groups + (groups > 1 ? double(blocks) / s.sequences : 0.0);
-      const double cost = double(ceil_div(ctas, sms)) *
-                          (std::ceil(part / split) * (sweep + (split > 1 ? ahead : 0.0)) + 6 +
-                           (split > 1 ? 5 : 0));
+      if (split > 1 && clusters * split > kMixMaxCtas) break;
+      // clusters end where sequences do: the largest has about half a sequence more than its part
+      const double part = double(blocks) / groups + (groups > 1 ? one / 2 : 0.0);
+      const double stretch = std::ceil(part / split);
+      // what a CTA sums ahead: its last sequence, about half of one of many
+      const double summed = split == 1 ? 0.0 : s.sequences > split ? std::min(stretch, one / 2) : stretch;
+      const double cost = double(ceil_div(clusters, device.fit[split])) *
+                          (stretch * sweep + summed * ahead + 6 + (split > 1 ? 5 : 0));
       if (least == 0 || cost < least) {
         best = {int(groups), split};
         least = cost;
       }
     }
-    if (sweeps * s.heads * groups >= sms) break;
+    if (clusters >= device.sms) break;
   }
   return best;
 }
@@ -250,10 +261,10 @@ struct Sweep {
   float in_scale, out_scale;
 };
 int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const float* log_decay,
-               const int32_t* offsets, int sms, void* ws, cudaStream_t st) {
+               const int32_t* offsets, const Device& device, void* ws, cudaStream_t st) {
   bool exact = false;
   for (int i = 0; i < sweeps; ++i) exact = exact || w[i].state_out != nullptr;
-  const Share share = choose_share(s, sweeps, exact, sms);
+  const Share share = choose_share(s, sweeps, exact, device);
   LinAttnSweeps all{};
   for (int i = 0; i < sweeps; ++i, ++w) {
     LinAttnArgs& g = all.sweep[i];
@@ -369,11 +380,11 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
   if (e != DMUON_OK) return e;
   if (s.tokens > 0 && (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)))
     return DMUON_ERR_INVALID_ARG;
-  int sms = 0;
-  e = device_ready(&sms);
+  Device device;
+  e = device_ready(&device);
   if (e != DMUON_OK) return e;
   const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, 1.f, 1.f};
-  return run_sweeps(s, &w, 1, log_decay, offsets, sms, workspace, stream);
+  return run_sweeps(s, &w, 1, log_decay, offsets, device, workspace, stream);
 }
 
 int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* dout,
@@ -404,22 +415,22 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
         if (overlap(*o, *i)) return DMUON_ERR_INVALID_ARG;
     if (overlap(dqr, dkr) || overlap(dqr, dvr) || overlap(dkr, dvr)) return DMUON_ERR_INVALID_ARG;
   }
-  int sms = 0;
-  e = device_ready(&sms);
+  Device device;
+  e = device_ready(&device);
   if (e != DMUON_OK) return e;
   const float inv = 1.f / s.scale;
   const Sweep sweeps[3] = {
       {&dor, &vr, &kr, &dqr, false, state, nullptr, true, 1.f, 1.f},
       {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, inv, 1.f},
       {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, inv, s.scale}};
-  if (s.tokens == 0) return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, sms, workspace, stream);
+  if (s.tokens == 0) return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, device, workspace, stream);
   // The three side by side fill the GPU without cutting sequences as finely (8192 tokens of 32 heads:
   // 285 us one after another, 204 together).  Apart where dv's sweep is another kernel, or writes
   // dstate, perhaps over the dfinal_state that dk's reads.
   const bool apart = dstate != nullptr || (s.key_dim <= 64) != (s.value_dim <= 64);
-  e = run_sweeps(s, sweeps, apart ? 2 : 3, log_decay, offsets, sms, workspace, stream);
+  e = run_sweeps(s, sweeps, apart ? 2 : 3, log_decay, offsets, device, workspace, stream);
   if (e != DMUON_OK || !apart) return e;
-  return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, sms, workspace, stream);
+  return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, device, workspace, stream);
 }
 
 int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
@@ -447,8 +458,8 @@ int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
                   bytes = uintptr_t(slots) * uintptr_t(s.heads * s.key_dim * s.value_dim) * 4;
   if (a != b && a < b + bytes && b < a + bytes) return DMUON_ERR_INVALID_ARG;
   if (s.tokens * s.heads * ceil_div(s.value_dim, 32) > INT32_MAX) return DMUON_ERR_UNSUPPORTED;
-  int sms = 0;
-  const int e = device_ready(&sms);
+  Device device;
+  const int e = device_ready(&device);
   if (e != DMUON_OK) return e;
   g.q = device_heads(qr);
   g.k = device_heads(kr);

@@ -661,3 +661,72 @@ def test_two_streams_with_their_own_handles(dm):
     for c, w, op in zip(cases, want, ops):
         have = [c[n].t for n in ("to_out", "to_dq", "to_dk", "to_dv")] + [c["final"], c["dstate"]]
         assert all(torch.equal(a, b) for a, b in zip(have, w)) and op.status() == dm.OK
+
+
+# ------------------------------------------------------------------ many sequences, far addresses
+@pytest.mark.parametrize("heads,sequences,tokens", [(2, 100, 6000), (1, 33, 9000), (12, 70, 3000),
+                                                    (3, 800, 2500)])
+def test_linattn_many_sequences_of_few_heads(dm, heads, sequences, tokens):
+    """More sequences than a warp has lanes, shared among clusters and CTAs wherever they end, the
+    states over themselves; every output against the fp64 recurrence."""
+    rng = np.random.default_rng(tokens)
+    cuts = np.sort(rng.integers(0, tokens, sequences - 1))
+    cuts[: sequences // 4] = cuts[sequences // 4]                # a run of empty ones
+    off = [0] + np.sort(cuts).tolist() + [tokens]
+    c = mix_case(31, tokens, heads, 64, 128, off, True)
+    mix_check(dm, c, 0.3, f"{heads} {sequences}")
+    op = dm.LinearAttention(tokens, heads, 64, 128, max_sequences=sequences, scale=0.3)
+    args = [c[x].t for x in ("q", "k", "v")] + [c["g"]]
+    s, out = c["state"].clone(), torch.empty_like(c["v"].t)
+    op.forward(*args, out, offsets=c["offsets"], state=s, final_state=s)
+    assert torch.equal(s, c["final"]) and torch.equal(out, c["to_out"].t)
+
+
+def test_rows_past_2_to_the_32_elements(dm):
+    """Tokens so far apart that offsets pass 32 bits give the bits of the same tokens side by side."""
+    tokens, heads, d, apart = 300, 2, 64, 1 << 24
+    far = [torch.empty(tokens * apart, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    f, pos = rope_reference(d, d), torch.arange(tokens, device="cuda", dtype=torch.int32)
+
+    def at(buf, i):       # five tensors to a buffer
+        return buf.as_strided((tokens, heads, d), (apart, d, 1), i * heads * d)
+
+    def run(place):
+        draw = Draw(32)
+        q, k, v, dout = (place(0, i).copy_(draw((tokens, heads, d))) for i in range(4))
+        qo, ko = place(1, 0), place(1, 1)
+        dm.QKNormRope(tokens, heads, heads, d).forward(q, k, None, None, f, pos, qo, ko)
+        op, g = dm.LinearAttention(tokens, heads, d), torch.full((heads,), -0.01, device="cuda")
+        out = place(1, 2)
+        op.forward(qo, ko, v, g, out)
+        grads = [place(1, 3), place(1, 4), place(0, 4)]
+        op.backward(dout, qo, ko, v, g, *grads)
+        dx, dw = [place(1, 0), place(1, 1)], [torch.empty(d, dtype=torch.bfloat16, device="cuda")] * 2
+        rows = [x.clone() for x in (qo, ko, out, *grads)]
+        dm.QKNormRope(tokens, heads, heads, d).backward(grads[0], grads[1], q, k, None, None, f, pos, *dx,
+                                                        None, None)
+        return rows + [x.clone() for x in dx]
+
+    near = {}
+    want = run(lambda b, i: near.setdefault((b, i), torch.empty((tokens, heads, d), dtype=torch.bfloat16,
+                                                                device="cuda")))
+    assert (tokens - 1) * apart > 1 << 32
+    assert all(torch.equal(a, b) for a, b in zip(run(lambda b, i: at(far[b], i)), want))
+
+
+def test_step_states_past_2_to_the_32_elements(dm):
+    heads, d, slots, rows = 2, 128, 140000, 5
+    pool = torch.empty((slots, heads, d, d), device="cuda")
+    assert pool.numel() > 1 << 32
+    names = torch.tensor([slots - 1, 3, 131080, 70000, slots - 2], dtype=torch.int32, device="cuda")
+    small = Draw(33)((rows, heads, d, d), 1.0, torch.float32)
+    for i, n in enumerate(names.tolist()):
+        pool[n] = small[i]
+    draw = Draw(34)
+    q, k, v = (draw((rows, heads, d)) for _ in range(3))
+    g = torch.full((heads,), -0.1, device="cuda")
+    op, want, out = dm.LinearAttention(rows, heads, d), torch.empty_like(v), torch.empty_like(v)
+    op.step(q, k, v, g, small, want)
+    op.step(q, k, v, g, pool, out, slots=names)
+    assert torch.equal(out, want)
+    assert all(torch.equal(pool[n], small[i]) for i, n in enumerate(names.tolist()))

@@ -1458,7 +1458,7 @@ const char* dmuon_status_string(int status) {
   }
 }
 
-int dmuon_version(void) { return 200; }
+int dmuon_version(void) { return 300; }
 
 long long dmuon_launch_count(int reset) {
   const long long n = t_launches;

@@ -195,8 +195,19 @@ bool linattn_shape_ok(const dmuon_linattn_shape* s) {
          s->sequences <= kMaxSequences && s->heads >= 1 && s->heads <= kMaxHeads &&
          s->key_dim >= 8 && s->key_dim <= 128 && s->key_dim % 8 == 0 && s->value_dim >= 8 &&
          s->value_dim <= 128 && s->value_dim % 8 == 0 && std::isfinite(s->scale) &&
-         s->scale != 0.f && s->sequences * s->heads <= (int64_t(1) << 27);
+         std::isfinite(1.f / s->scale) && s->sequences * s->heads <= (int64_t(1) << 27);
 }
+// States of the call: of so many sequences, or slots.
+struct States {
+  uintptr_t p, bytes;
+  States(const float* at, const dmuon_linattn_shape& s, int64_t n)
+      : p(reinterpret_cast<uintptr_t>(at)),
+        bytes(at == nullptr ? 0 : uintptr_t(n) * uintptr_t(s.heads * s.key_dim * s.value_dim) * 4) {}
+  bool meets(uintptr_t from, uintptr_t to) const { return bytes > 0 && p < to && from < p + bytes; }
+  bool meets(const Rows& r) const { return meets(r.p, r.end()); }
+  // Written states are the read ones or lie apart from them.
+  bool beside(const States& read) const { return p == read.p || !meets(read.p, read.p + read.bytes); }
+};
 
 // How a head's packed batch is shared: `groups` clusters of `split` CTAs.
 struct Share {
@@ -378,8 +389,14 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
   const Rows qr = checked(q, one, s.key_dim, &e), kr = checked(k, one, s.key_dim, &e),
              vr = checked(v, one, s.value_dim, &e), orow = checked(out, one, s.value_dim, &e);
   if (e != DMUON_OK) return e;
-  if (s.tokens > 0 && (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)))
-    return DMUON_ERR_INVALID_ARG;
+  const States first(state, s, s.sequences), last(final_state, s, s.sequences);
+  if (!last.beside(first)) return DMUON_ERR_INVALID_ARG;
+  if (s.tokens > 0) {
+    if (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr) || first.meets(orow))
+      return DMUON_ERR_INVALID_ARG;
+    for (const Rows* r : {&qr, &kr, &vr, &orow})
+      if (last.meets(*r)) return DMUON_ERR_INVALID_ARG;
+  }
   Device device;
   e = device_ready(&device);
   if (e != DMUON_OK) return e;
@@ -409,10 +426,17 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
              dqr = checked(dq, one, s.key_dim, &e), dkr = checked(dk, one, s.key_dim, &e),
              dvr = checked(dv, one, s.value_dim, &e);
   if (e != DMUON_OK) return e;
+  const States first(state, s, s.sequences), dlast(dfinal_state, s, s.sequences),
+      dfirst(dstate, s, s.sequences);
+  if (!dfirst.beside(dlast)) return DMUON_ERR_INVALID_ARG;
   if (s.tokens > 0) {
-    for (const Rows* o : {&dqr, &dkr, &dvr})
+    for (const Rows* o : {&dqr, &dkr, &dvr}) {
+      if (first.meets(*o) || dlast.meets(*o)) return DMUON_ERR_INVALID_ARG;
       for (const Rows* i : {&dor, &qr, &kr, &vr})
         if (overlap(*o, *i)) return DMUON_ERR_INVALID_ARG;
+    }
+    for (const Rows* r : {&dor, &qr, &kr, &vr, &dqr, &dkr, &dvr})
+      if (dfirst.meets(*r)) return DMUON_ERR_INVALID_ARG;
     if (overlap(dqr, dkr) || overlap(dqr, dvr) || overlap(dkr, dvr)) return DMUON_ERR_INVALID_ARG;
   }
   Device device;
@@ -453,11 +477,13 @@ int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
     return DMUON_ERR_INVALID_ARG;
   for (const Rows* r : {&qr, &kr, &vr, &orow})
     if (r->p % 2 != 0) return DMUON_ERR_ALIGNMENT;
-  if (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)) return DMUON_ERR_INVALID_ARG;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(state), b = reinterpret_cast<uintptr_t>(new_state),
-                  bytes = uintptr_t(slots) * uintptr_t(s.heads * s.key_dim * s.value_dim) * 4;
-  if (a != b && a < b + bytes && b < a + bytes) return DMUON_ERR_INVALID_ARG;
   if (s.tokens * s.heads * ceil_div(s.value_dim, 32) > INT32_MAX) return DMUON_ERR_UNSUPPORTED;
+  if (overlap(orow, qr) || overlap(orow, kr) || overlap(orow, vr)) return DMUON_ERR_INVALID_ARG;
+  const int64_t reached = std::min(slots, int64_t(1) << 31);  // by int32 slots
+  const States before(state, s, reached), after(new_state, s, reached);
+  if (!after.beside(before) || before.meets(orow)) return DMUON_ERR_INVALID_ARG;
+  for (const Rows* r : {&qr, &kr, &vr, &orow})
+    if (after.meets(*r)) return DMUON_ERR_INVALID_ARG;
   Device device;
   const int e = device_ready(&device);
   if (e != DMUON_OK) return e;

@@ -195,6 +195,57 @@ def test_step_refuses_bad_arguments(dm):
                 slots=1 << 22, new=1 << 60) == dm.ERR_UNSUPPORTED
 
 
+def test_states_lie_apart_from_what_is_written(dm):
+    """States that are written may be the ones read, or lie apart from them and from every tensor."""
+    bad = dm.ERR_INVALID_ARG
+    n = 4 * 64 * 64 * 4                    # bytes of a sequence's states; tensors take 2048 here
+    assert lin(dm, st=W, fin=W) not in ARGUMENT and lin_back(dm, dfin=W, dst=W) not in ARGUMENT
+    for off in (16, n - 16, 16 - n):
+        assert lin(dm, st=W, fin=W + off) == bad and lin_back(dm, dfin=W, dst=W + off) == bad
+        # dstate is written after the last read of state
+        assert lin_back(dm, st=W, dst=W + off) not in ARGUMENT
+    empty = (0, 1, 4, 64, 64, 0.5)
+    assert lin(dm, shape=empty, t=[None] * 4, st=W, fin=W + 16) == bad
+    for off in (n, -n):
+        assert lin(dm, st=W, fin=W + off) not in ARGUMENT
+        assert lin_back(dm, dfin=W, dst=W + off) not in ARGUMENT
+    for off in (0, 1024, 16 - n, 2032):
+        for i in range(4):
+            assert lin(dm, fin=P + i * GAP + off) == bad
+            assert (lin(dm, st=P + i * GAP + off) == bad) == (i == 3)
+        for i in range(7):
+            assert lin_back(dm, dst=P + i * GAP + off) == bad
+            assert (lin_back(dm, dfin=P + i * GAP + off) == bad) == (i > 3)
+            assert (lin_back(dm, st=P + i * GAP + off) == bad) == (i > 3)
+    for off in (2048, -n):
+        assert lin(dm, fin=P + 3 * GAP + off) not in ARGUMENT
+        assert lin_back(dm, dst=P + 6 * GAP + off) not in ARGUMENT
+
+
+def test_step_states_lie_apart_from_what_is_written(dm):
+    n = 4 * 4 * 64 * 64 * 4
+
+    def step(st, new):
+        h = [place(i) for i in range(4)]
+        return dm.lib().dmuon_linattn_step(ctypes.byref(dm.LinattnShape(4, 1, 4, 64, 64, 0.5)),
+                                           *(ref(x) for x in h[:3]), W, None, 4, st, new, ref(h[3]), None)
+
+    for off in (0, 1024, 16 - n, 2032):
+        for i in range(4):
+            assert step(W, P + i * GAP + off) == dm.ERR_INVALID_ARG
+            assert (step(P + i * GAP + off, W) == dm.ERR_INVALID_ARG) == (i == 3)
+    for off in (2048, -n):
+        assert step(P + 3 * GAP + off, P + 3 * GAP + off) not in ARGUMENT
+
+
+def test_scales_whose_inverse_overflows_are_refused(dm):
+    """The gradients' sweeps take the final states' gradient divided by the scale."""
+    for scale, ok in ((1e-38, True), (-1e-38, True), (3e38, True), (2e-39, False), (1e-45, False)):
+        s = (4, 1, 4, 64, 64, scale)
+        assert (dm.lib().dmuon_linattn_workspace_bytes(ctypes.byref(dm.LinattnShape(*s)), 1) > 0) == ok
+        assert (lin(dm, shape=s) == dm.ERR_INVALID_ARG) == (not ok)
+
+
 def test_workspaces_stay_bounded(dm):
     """Sequences are shared among CTAs only where there are few of them."""
     one = lambda *s: dm.lib().dmuon_linattn_workspace_bytes(ctypes.byref(dm.LinattnShape(*s)), 1)

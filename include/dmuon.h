@@ -419,8 +419,9 @@ typedef struct {
  * The angle is taken modulo a turn in 64-bit fixed point, so that far positions lose nothing:
  * sines and cosines are within 2^-21 for any position.  Squares are summed in fp32 (elements
  * beyond 1e18 overflow).  An output may be its own input (q_out = q, k_out = k); a NaN or an
- * infinity reaches its own head only.  One launch; no workspace.  Rows at 8-byte addresses move
- * in 8-byte pieces, others element by element.
+ * infinity reaches its own head only.  One launch; no workspace.  Where all rows and gains lie at
+ * 8-byte addresses they move in 8-byte pieces, else element by element.  More than 2^31 - 1 groups
+ * of 4 heads in all tokens together: DMUON_ERR_UNSUPPORTED.
  */
 int dmuon_qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* q, const dmuon_heads* k,
                        const void* w_q, const void* w_k, const float* inv_freq,
@@ -449,7 +450,7 @@ typedef struct {
   int64_t tokens, sequences;     /* of all sequences together; 1 <= sequences <= 65536 */
   int64_t heads;
   int64_t key_dim, value_dim;    /* multiples of 8, at most 128 */
-  float scale;                   /* not 0 */
+  float scale;                   /* its inverse is finite, too */
 } dmuon_linattn_shape;
 
 /*
@@ -462,15 +463,16 @@ typedef struct {
  *                offsets are cut to 0 .. tokens.
  *   state        device, fp32, contiguous (sequences, heads, key_dim, value_dim): S before the
  *                first token of each sequence; NULL: zeros
- *   final_state  the same after the last token; NULL: not wanted.  May be `state`.
+ *   final_state  the same after the last token; NULL: not wanted.  May be `state`; otherwise it
+ *                lies apart from it, as it and out do from all that is read.
  * Tokens are taken in blocks of 128 counted from their sequence's start.  The weighted scores of
  * a block, the state that enters it and the keys times their decay are rounded to bf16 as
  * operands of products that accumulate in fp32; with final_state the keys are kept to 16 bits, so
- * that the state is within 2^-16 of the sum of its terms' magnitudes.
+ * that the state is within 2^-15 of the sum of its terms' magnitudes.
  * A NaN or an infinity in v reaches all tokens of its block of its sequence and those after it
  * (one in k its own token and those after, one in q its own); no other sequence or head.
  * Rows of heads are 16-byte aligned (strides multiples of 8 elements), DMUON_ERR_ALIGNMENT
- * otherwise; so are states.
+ * otherwise; so are states.  The workspace, the same for both directions, serves one call at a time.
  */
 size_t dmuon_linattn_workspace_bytes(const dmuon_linattn_shape* shape, int backward);
 int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q,
@@ -482,7 +484,8 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
 /*
  * dmuon_linattn_backward -- its gradients (nothing is kept by forward):
  *   dfinal_state  gradient of final_state, or NULL for zeros
- *   dstate        gradient of state, or NULL: not wanted.  May be dfinal_state.
+ *   dstate        gradient of state, or NULL: not wanted (kept like final_state).  May be
+ *                 dfinal_state.
  * With g_t = scale dout_t and D_t the gradient of S_t, both along the sequence:
  *   D_t = q_t g_t^T + exp(log_decay) D_{t+1},   dq_t = S_t g_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
  * A NaN or an infinity in q, k, v or dout may reach all gradients of its sequence and head.
@@ -503,7 +506,9 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
  *              slot are taken one after another in their order.
  *   state      device, fp32, contiguous (slots, heads, key_dim, value_dim)
  *   new_state  the same; may be `state` (in place).  Slots that no row names are not written.
- * One launch; no workspace.
+ * Any element address will do for rows of heads; states are 16-byte aligned.  One launch; no
+ * workspace.  More than 2^31 - 1 pieces of 32 value elements (rows x heads x pieces):
+ * DMUON_ERR_UNSUPPORTED.
  */
 int dmuon_linattn_step(const dmuon_linattn_shape* shape, const dmuon_heads* q,
                        const dmuon_heads* k, const dmuon_heads* v, const float* log_decay,

@@ -25,11 +25,6 @@ DM_DEV F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-DM_DEV F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 DM_DEV F2 negate2(F2 v) { return v ^ 0x8000000080000000ull; }
 
 DM_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -27,6 +27,14 @@
 // stretch.  (Sharing again and again, in rounds short enough for keys and values to stay in L2, was
 // slower the shorter the rounds: 65536 tokens of 32 heads 829 us in rounds of 12 blocks a CTA, 797
 // of 16, 747 of 64, 738 in one.)
+//
+// Bound, with a head to each SM, by HBM and by the SM's shared memory at once: of the 5500 cycles of
+// a block of 128 x 128 heads about 2450 go to the warps' reads and writes there, 1800 to operands of
+// products, 1000 to copies, and little else can run beside them; the tensor cores are busy for 30%.
+// 152 heads of 5120 tokens take 123 us, 6.4 TB/s of q, k, v and out, 0.95 of the copy rate (155 us
+// where a final state is written, 75 us of 64 elements: 5.3 TB/s).  With fewer heads, keys and values
+// are read twice and not all SMs take part: 8192 tokens of 32 heads 86 us (40 at the copy rate),
+// their gradients 180 (69), 65536 tokens with states 750 (318).
 #include "dmuon.h"
 #include "f32x2.cuh"
 #include "mix.h"
@@ -112,8 +120,6 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "");
 
-// What is not needed block by block stays out of line: four kinds of warps run side by side, and
-// their code has to fit the instruction cache (at 290 KB of it a block took half as long again).
 DM_DEV bool gave_up(int* err, volatile int* flag) {
   *flag = 1;
   atomicExch(err, DMUON_ERR_TIMEOUT);
@@ -346,7 +352,8 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
 
 // ------------------------------------------------------------------ products
 // Two threads issue them, as issuing takes about as long as computing: one the blocks' own states,
-// one the rest.
+// one the rest.  (A third for the scores alone: 140 us where two took 131, 152 heads of 5120
+// tokens; scores in two TMEM buffers, the next ones multiplied while these are weighted: 143.)
 template <int DK, int DV, bool EXACT>
 DM_DEV void state_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Shared* sh) {
   using T = Tiles<DK, DV>;

@@ -37,9 +37,11 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
                         cudaStream_t s);
 
 // ------------------------------------------------------------------ linear attention
-// One sweep over every sequence, along time or against it (mix_kernel in linattn.cu):
-//   along:    S_t = a S_{t-1} + k_t v_t^T,  out_t = scale q_t S_t         a = exp(log_decay)
-//   against:  R_t = a R_{t+1} + ...,        out_t = scale q_t (R_{t+1} a^0 + k_t v_t^T ...)
+// One sweep over every sequence, along time or against it (mix_kernel in linattn.cu), with
+// a = exp(log_decay):
+//   along:    S_t = a S_{t-1} + k_t v_t^T,      out_t = scale q_t S_t       state_out = S behind the last
+//   against:  R_t = R_{t+1} + k_t v_t^T,        out_t = scale q_t R_t,
+//             then decayed on its way to t - 1:  R_t <- a R_t               state_out = R before the first
 struct LinAttnArgs {
   CUtensorMap q, k, v, o;     // loads: 64 x 1 x 128 boxes; o: stores of 32 x 1 x 32
   const float* log_decay;

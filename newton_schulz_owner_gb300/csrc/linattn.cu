@@ -26,15 +26,17 @@
 // values), the shares go to the CTAs behind it through memory, and then each CTA sweeps its
 // stretch.  (Sharing again and again, in rounds short enough for keys and values to stay in L2, was
 // slower the shorter the rounds: 65536 tokens of 32 heads 829 us in rounds of 12 blocks a CTA, 797
-// of 16, 747 of 64, 738 in one.)
+// of 16, 747 of 64, 738 in one.)  Where that would leave a CTA to a head, or a head's gradient, and
+// SMs without one or a last wave of few, sequences are instead dealt whole to all SMs (deal()).
 //
 // Bound, with a head to each SM, by HBM and by the SM's shared memory at once: of the 5500 cycles of
 // a block of 128 x 128 heads about 2450 go to the warps' reads and writes there, 1800 to operands of
 // products, 1000 to copies, and little else can run beside them; the tensor cores are busy for 30%.
-// 152 heads of 5120 tokens take 123 us, 6.4 TB/s of q, k, v and out, 0.95 of the copy rate (155 us
-// where a final state is written, 75 us of 64 elements: 5.3 TB/s).  With fewer heads, keys and values
-// are read twice and not all SMs take part: 8192 tokens of 32 heads 86 us (40 at the copy rate),
-// their gradients 180 (69), 65536 tokens with states 750 (318).
+// 152 heads of 5120 tokens take 124 us, 6.4 TB/s of q, k, v and out, 0.95 of the copy rate (145 us
+// where a final state is written, 74 us of 64 elements: 5.4 TB/s).  With fewer heads, keys and values
+// are read twice and not all SMs take part: 8192 tokens of 32 heads 85 us (40 at the copy rate),
+// 65536 tokens with states 676 (318).  The gradients of 8192 tokens of 32 heads in 5 sequences take
+// 149 us (69), dealt: 44 to 49 blocks to each SM, 3.1 us a block.
 #include "dmuon.h"
 #include "f32x2.cuh"
 #include "mix.h"
@@ -112,8 +114,13 @@ struct Shared {
   Block sweep[kRing];          // the swept ones by theirs
   uint32_t tmem;
   int abort;
-  int place[6];                // what locate() found
-  int sums[kThreads / 32];
+  union {
+    struct {
+      int place[6];            // what locate() found
+      int sums[kThreads / 32];
+    };
+    int list[kMixDealt];       // sequences that the CTA was dealt: 32 pair + sequence, or -1
+  };
   alignas(16) float fall[96];        // what weigh() needs of the powers of a
   float near_[64];                   // scale a^n, n = -32 .. 31; zeros below 0
   float power[kMixBlock + 1];        // a^n
@@ -291,11 +298,86 @@ DM_DEV Work locate(const LinAttnArgs& g, int group, int rank, Shared* sh) {
   return w;
 }
 
+// Sequences of all heads and sweeps ("pairs"), dealt whole to `ctas` CTAs: the longest sequence's of all
+// pairs first, each to the CTA with the least to do so far, then the next one's.  CTAs with equally
+// much to do are runs of their numbers, a lane each: one at first, and one more for every sequence at
+// most.  The first warp of each CTA deals for all; list: what its own gets.
+DM_DEV void deal(const LinAttnArgs& g, int pairs, int ctas, int* list) {
+  constexpr int kStart = 1;  // blocks' time that a sequence takes besides
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = int(threadIdx.x) & 31, cta = int(blockIdx.x);
+  list[lane] = -1;
+  __syncwarp();
+  const int blocks = lane < g.sequences ? extent_of(g, lane).blocks : 0;
+  int place = 0;  // among the sequences
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int other = __shfl_sync(kAll, blocks, i);
+    place += other > blocks || (other == blocks && i < lane);
+  }
+  auto sum_upto = [&](int v) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kAll, v, d);
+      if (lane >= d) v += u;
+    }
+    return v;
+  };
+  int runs = 1, first = 0, count = lane == 0 ? ctas : 0, load = 0, left = kMixDealt;
+#pragma unroll 1
+  for (int n = 0; n < g.sequences; ++n) {
+    const int s = __ffs(__ballot_sync(kAll, place == n)) - 1;
+    const int cost = __shfl_sync(kAll, blocks, s) + kStart;
+    if (cost == kStart) break;
+    // sequences of a CTA of the run that start before `level`, and of all
+    auto taken = [&](int level) { return level > load ? min((level - load + cost - 1) / cost, left) : 0; };
+    auto total = [&](int level) { return __reduce_add_sync(kAll, count * taken(level)); };
+    int lo = __reduce_min_sync(kAll, count > 0 ? load : 0x7FFFFFFF);
+    int hi = __reduce_max_sync(kAll, count > 0 ? load : 0) + (pairs / ctas + 1) * cost;
+    if (total(hi) < pairs) hi += pairs * cost;
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (total(mid) >= pairs) hi = mid;
+      else lo = mid;
+    }
+    // those that start before lo, and as many that start there as are left
+    int takes = taken(lo);
+    const int able = taken(hi) > takes ? count : 0;
+    const int rest = pairs - __reduce_add_sync(kAll, count * takes);
+    int more = min(max(rest - (sum_upto(able) - able), 0), able);
+    const unsigned cut = __ballot_sync(kAll, more > 0 && more < count);
+    if (cut != 0) {  // the one run of which some do
+      const int from = __ffs(cut) - 1;
+      const int m = __shfl_sync(kAll, more, from), f = __shfl_sync(kAll, first, from),
+                c = __shfl_sync(kAll, count, from), l = __shfl_sync(kAll, load, from),
+                e = __shfl_sync(kAll, left, from), t = __shfl_sync(kAll, takes, from);
+      if (lane == from) count = m;
+      if (lane == runs) {
+        first = f + m;
+        count = c - m;
+        load = l;
+        left = e;
+        takes = t;
+        more = 0;
+      }
+      ++runs;
+    }
+    takes += more > 0;
+    const int pair = sum_upto(count * takes) - count * takes + (cta - first) * takes;
+    if (cta >= first && cta < first + count)
+      for (int i = 0; i < takes; ++i) list[kMixDealt - left + i] = 32 * (pair + i) + s;
+    load += takes * cost;
+    left -= takes;
+  }
+}
+
 // ------------------------------------------------------------------ loads
 // The one walk through the batch: the CTA's stretch from its last sequence on, if that goes on in
 // the next CTA's, and then the whole stretch.
 template <int DK, int DV>
-DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* smem, Shared* sh) {
+DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, bool again, uint8_t* smem,
+                      Shared* sh) {
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
   int it = 0, swept = 0;
@@ -347,7 +429,14 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, uint8_t* sm
     if (!load(at, kSweep | (i == 0 ? kFirst : 0))) return;
     if (i + 1 < w.n) at = skipped(g, at, 1);
   }
-  (void)load(at, kEnd);
+  if (!load(at, kEnd) || !again) return;
+  // all of the stages have been read: what arrives on their barriers has
+#pragma unroll 1
+  for (int i = max(0, it - 1 - T::stages); i < it - 1; ++i) {
+    const int s = i % T::stages;
+    if (!await(&sh->empty[s], (i / T::stages) & 1, g.err, flag)) return;
+    if (!await(&sh->q_empty[s], (i / T::stages) & 1, g.err, flag)) return;
+  }
 }
 
 // ------------------------------------------------------------------ products
@@ -410,7 +499,10 @@ DM_DEV void out_mma_role(const LinAttnArgs& g, uint8_t* smem, uint8_t* state, Sh
     const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
     if (!await(&sh->full[s], (it / T::stages) & 1, g.err, flag)) return;
     const int kind = sh->block[it % kRing].kind;
-    if (kind & kEnd) return;
+    if (kind & kEnd) {
+      if (swept > 0) (void)await(&sh->outer, (swept - 1) & 1, g.err, flag);
+      return;
+    }
     if (!await(&sh->q_full[s], (it / T::stages) & 1, g.err, flag)) return;
     if (!(kind & kSweep)) {
       mbar_arrive(&sh->empty[s]);  // waited for all the same: a wait misses no phase
@@ -929,6 +1021,9 @@ struct OutRole {
   }
 };
 
+// All warps, each from its own branch.
+DM_DEV void sync_roles() { asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 template <int DK, int DV, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant__ LinAttnSweeps sweeps) {
   extern __shared__ uint8_t smem_raw[];
@@ -940,12 +1035,13 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   Shared* sh = reinterpret_cast<Shared*>(smem + T::stages * T::stage);
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
-  const int split = sweeps.sweep[0].split;
-  const int cluster = int(blockIdx.x) / split, rank = int(blockIdx.x) - cluster * split;
-  const int of_sweep = sweeps.sweep[0].groups * sweeps.sweep[0].heads;
-  const LinAttnArgs& g = sweeps.sweep[cluster / of_sweep];
-  const int group = cluster % of_sweep / g.heads, head = cluster % of_sweep - group * g.heads;
-  if (threadIdx.x == 0) {
+  const int split = sweeps.sweep[0].split, heads = sweeps.sweep[0].heads, ctas = sweeps.deal;
+  const int cluster = ctas > 0 ? 0 : int(blockIdx.x) / split, rank = int(blockIdx.x) - cluster * split;
+  const int of_sweep = sweeps.sweep[0].groups * heads;
+  const LinAttnArgs* at = &sweeps.sweep[cluster / of_sweep];
+  const int group = cluster % of_sweep / heads;
+  int head = cluster % of_sweep - group * heads;
+  auto init_barriers = [&]() {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 2);
@@ -962,25 +1058,48 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     mbar_init(&sh->out, 2);
     mbar_init(&sh->taken, kOutWarps);
     mbar_init(&sh->put, kStateWarps);
-    mbar_init(&sh->shares, uint32_t(g.split));
-    sh->abort = 0;
+    mbar_init(&sh->shares, uint32_t(split));
     fence_barrier_init();
+  };
+  if (threadIdx.x == 0) {
+    sh->abort = 0;
+    init_barriers();
   }
   if (warp == kOutMmaWarp) {
     tmem_alloc(&sh->tmem, kTmemCols);
     tmem_relinquish();
   }
   if (warp == kLoadWarp && elect_one()) {
-    prefetch_tensormap(&g.q);
-    prefetch_tensormap(&g.k);
-    prefetch_tensormap(&g.v);
-    prefetch_tensormap(&g.o);
+    prefetch_tensormap(&at->q);
+    prefetch_tensormap(&at->k);
+    prefetch_tensormap(&at->v);
+    prefetch_tensormap(&at->o);
   }
-  if (g.split > 1) cluster_sync();  // barriers of all CTAs stand before one arrives on another's
+  if (split > 1) cluster_sync();  // barriers of all CTAs stand before one arrives on another's
   grid_wait();
   grid_launch_dependents();
-  const float log_decay = g.log_decay[head];
-  {
+  Work w;
+  if (ctas > 0) {
+    if (warp == 0) deal(*at, sweeps.count * heads, ctas, sh->list);
+    __syncthreads();
+  } else {
+    w = at->sequences <= 32 ? locate_few(*at, group, rank) : locate(*at, group, rank, sh);
+  }
+  float log_decay = 0.f;
+  auto begin = [&](int unit) {
+    if (ctas > 0) {
+      const int u = sh->list[unit];
+      const int pair = max(u, 0) >> 5, sweep = pair / heads;
+      at = &sweeps.sweep[sweep];
+      head = pair - sweep * heads;
+      w.start.seq = u & 31;
+      w.start.m = 0;
+      w.start.x = u < 0 ? Extent{0, 0, 0x7FFFFFFF} : extent_of(*at, u & 31);
+      w.nb = w.per = w.n = u < 0 ? 0 : w.start.x.blocks;
+      w.rank = 0;
+    }
+    const LinAttnArgs& g = *at;
+    log_decay = g.log_decay[head];
     const int t = int(threadIdx.x);
     if (t <= kMixBlock) {
       sh->power[t] = t == 0 ? 1.f : expf(log_decay * float(t));
@@ -991,33 +1110,59 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
       const int n = t - kMixBlock - 1 - 64;
       sh->fall[n] = expf(log_decay * float(g.against ? n + 1 : 96 - n));
     }
-  }
-  const Work w = g.sequences <= 32 ? locate_few(g, group, rank) : locate(g, group, rank, sh);
+  };
+  begin(0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
+  // Between sequences that a CTA was dealt everything stops, and starts as in a new launch.
+  auto more = [&](int unit) { return ctas > 0 && unit < kMixDealt && sh->list[unit] >= 0; };
+  auto next = [&](int unit) {
+    if (!more(unit)) return false;
+    tc_fence_before();
+    sync_roles();
+    if (*const_cast<volatile int*>(&sh->abort) != 0) return false;
+    if (threadIdx.x == 0) {
+      for (uint64_t* bar = sh->full; bar <= &sh->shares; ++bar) mbar_inval(bar);
+      init_barriers();
+    }
+    begin(unit);
+    sync_roles();
+    tc_fence_after();
+    return true;
+  };
+  int unit = 0;
   if (warp < kStateWarps) {
     regs_inc<state_regs(EXACT)>();
-    StateRole<DK, DV, EXACT> r{g, w, sh, smem, state, log_decay, head, cluster, int(threadIdx.x),
-                               int(threadIdx.x & 31), int((warp & 3) * 32 + (threadIdx.x & 31)),
-                               int(warp >> 2) * (DV / 2)};
-    r.run();
-    if (EXACT && g.state_out != nullptr) r.pass_through(group * g.split + rank, g.groups * g.split);
+    do {
+      StateRole<DK, DV, EXACT> r{*at, w, sh, smem, state, log_decay, head, cluster, int(threadIdx.x),
+                                 int(threadIdx.x & 31), int((warp & 3) * 32 + (threadIdx.x & 31)),
+                                 int(warp >> 2) * (DV / 2)};
+      r.run();
+      if (EXACT && ctas == 0 && at->state_out != nullptr)
+        r.pass_through(group * split + rank, at->groups * split);
+    } while (next(++unit));
   } else if (warp < kOutWarp) {
     regs_dec<weigh_regs(EXACT)>();
-    WeighRole r{g, w, sh, warp - kWeighWarp, int(threadIdx.x & 31)};
-    r.run();
+    do {
+      WeighRole r{*at, w, sh, warp - kWeighWarp, int(threadIdx.x & 31)};
+      r.run();
+    } while (next(++unit));
   } else if (warp < kLoadWarp) {
     regs_dec<kOutRegs>();
-    OutRole<DK, DV> r{g, w, sh, smem, head, warp - kOutWarp, int(threadIdx.x & 31)};
-    r.run();
+    do {
+      OutRole<DK, DV> r{*at, w, sh, smem, head, warp - kOutWarp, int(threadIdx.x & 31)};
+      r.run();
+    } while (next(++unit));
   } else {
     regs_dec<kOtherRegs>();
-    if (warp == kLoadWarp && elect_one()) load_role<DK, DV>(g, w, head, smem, sh);
-    if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(g, smem, state, sh);
-    if (warp == kOutMmaWarp && elect_one()) out_mma_role<DK, DV>(g, smem, state, sh);
-    __syncwarp();
+    do {
+      if (warp == kLoadWarp && elect_one()) load_role<DK, DV>(*at, w, head, more(unit + 1), smem, sh);
+      if (warp == kStateMmaWarp && elect_one()) state_mma_role<DK, DV, EXACT>(*at, smem, state, sh);
+      if (warp == kOutMmaWarp && elect_one()) out_mma_role<DK, DV>(*at, smem, state, sh);
+      __syncwarp();
+    } while (next(++unit));
   }
   __syncthreads();
   if (*const_cast<volatile int*>(&sh->abort) != 0) {
@@ -1032,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     tc_fence_after();
     tmem_dealloc(sh->tmem, kTmemCols);
   }
-  if (g.split > 1) cluster_sync();  // no CTA leaves while another may still arrive on its barrier
+  if (split > 1) cluster_sync();  // no CTA leaves while another may still arrive on its barrier
 }
 
 using MixKernel = void (*)(LinAttnSweeps);
@@ -1080,12 +1225,12 @@ cudaError_t linattn_prepare(int (&fit)[kMixMaxSplit + 1]) {
   return cudaSuccess;
 }
 
-cudaError_t launch_linattn(const LinAttnSweeps& g, int sweeps, cudaStream_t s) {
+cudaError_t launch_linattn(const LinAttnSweeps& g, cudaStream_t s) {
   const LinAttnArgs& one = g.sweep[0];
   int smem = 0;
   const MixKernel k = kernel_for(one.dk, one.dv, one.exact != 0, &smem);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(sweeps * one.groups * one.heads * one.split), 1, 1);
+  cfg.gridDim = dim3(unsigned(g.deal > 0 ? g.deal : g.count * one.groups * one.heads * one.split), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = s;

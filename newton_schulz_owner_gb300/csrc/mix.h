@@ -70,8 +70,11 @@ cudaError_t linattn_prepare(int (&fit)[kMixMaxSplit + 1]);
 // Sweeps of one launch: of the same sizes (padded to 64 or 128), sharing and precision.
 struct LinAttnSweeps {
   LinAttnArgs sweep[3];
+  int count;
+  int deal;  // CTAs that all sequences of all heads and sweeps are dealt to whole, 0: not dealt
 };
-cudaError_t launch_linattn(const LinAttnSweeps& g, int sweeps, cudaStream_t s);
+constexpr int kMixDealt = 32;  // most sequences that a CTA is dealt
+cudaError_t launch_linattn(const LinAttnSweeps& g, cudaStream_t s);
 
 struct LinStepArgs {
   Heads q, k, v, out;

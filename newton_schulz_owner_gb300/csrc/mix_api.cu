@@ -209,9 +209,10 @@ struct States {
   bool beside(const States& read) const { return p == read.p || !meets(read.p, read.p + read.bytes); }
 };
 
-// How a head's packed batch is shared: `groups` clusters of `split` CTAs.
+// How a head's packed batch is shared: `groups` clusters of `split` CTAs, or whole sequences of all heads
+// and sweeps dealt to `deal` CTAs.
 struct Share {
-  int groups, split;
+  int groups, split, deal;
 };
 // Microseconds, measured with 128 elements to a head: a block takes 3 (exact states 3.8), 1.5 more
 // (2) where a CTA sums its share ahead; a launch 6, sharing 5.  Clusters of a size that the GPU's
@@ -221,8 +222,8 @@ Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const D
   const int64_t blocks = s.tokens / kMixBlock + std::min(s.sequences, s.tokens);  // at most
   const double one = double(blocks) / double(s.sequences);
   const double sweep = exact ? 3.8 : 3.0, ahead = exact ? 2.0 : 1.5;
-  Share best{1, 1};
-  double least = 0;
+  Share best{1, 1, 0};
+  double least = 0, whole = 0;
   for (int64_t groups = 1; groups <= s.sequences && groups <= 64; ++groups) {
     const int64_t clusters = sweeps * s.heads * groups;
     for (int split = 1; split <= kMixMaxSplit; ++split) {
@@ -235,12 +236,26 @@ Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const D
       const double summed = split == 1 ? 0.0 : s.sequences > split ? std::min(stretch, one / 2) : stretch;
       const double cost = double(ceil_div(clusters, device.fit[split])) *
                           (stretch * sweep + summed * ahead + 6 + (split > 1 ? 5 : 0));
+      if (whole == 0) whole = cost;  // a CTA to a head
       if (least == 0 || cost < least) {
-        best = {int(groups), split};
+        best = {int(groups), split, 0};
         least = cost;
       }
     }
     if (clusters >= device.sms) break;
+  }
+  // Dealing whole sequences: the longest of n, cut at random, is H_n / n of the batch; each takes 4 us to
+  // begin.  (Gradients of 8192 tokens of 32 heads in 5 sequences: a CTA to a head and gradient 180 us,
+  // dealt 149; of 4096 tokens of 28 heads, 3 CTAs to each 110 to 124, dealt 79 to 84; 30 sequences of 40
+  // heads 250 and 312.)  Not where one long sequence among short ones would lose much by it.
+  const int64_t pairs = sweeps * s.heads, ctas = std::min(int64_t(device.sms), pairs * s.sequences);
+  if (whole <= 1.25 * least && !exact && s.sequences > 1 && s.sequences < 32 &&
+      pairs * s.sequences <= ctas * (kMixDealt / 2)) {
+    double longest = 0;
+    for (int64_t i = 1; i <= s.sequences; ++i) longest += one / double(i);
+    const double each = std::max(longest, double(blocks * pairs) / double(ctas));
+    const double begun = std::ceil(double(pairs * s.sequences) / double(ctas));
+    if (each * sweep + begun * 4 + 6 < least) best = {1, 1, int(ctas)};
   }
   return best;
 }
@@ -277,6 +292,8 @@ int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const f
   for (int i = 0; i < sweeps; ++i) exact = exact || w[i].state_out != nullptr;
   const Share share = choose_share(s, sweeps, exact, device);
   LinAttnSweeps all{};
+  all.count = sweeps;
+  all.deal = share.deal;
   for (int i = 0; i < sweeps; ++i, ++w) {
     LinAttnArgs& g = all.sweep[i];
     if (!tile_map(&g.q, *w->q) || !tile_map(&g.k, *w->k) || !tile_map(&g.v, *w->v) ||
@@ -304,7 +321,7 @@ int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const f
     g.err = static_cast<int*>(ws);
     g.local = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHdrBytes);
   }
-  return launch_linattn(all, sweeps, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
+  return launch_linattn(all, st) == cudaSuccess ? DMUON_OK : DMUON_ERR_CUDA;
 }
 
 // Rows of a tensor of the call, checked; `status` keeps the first failure.

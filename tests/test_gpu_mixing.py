@@ -730,3 +730,38 @@ def test_step_states_past_2_to_the_32_elements(dm):
     op.step(q, k, v, g, pool, out, slots=names)
     assert torch.equal(out, want)
     assert all(torch.equal(pool[n], small[i]) for i, n in enumerate(names.tolist()))
+
+
+# ------------------------------------------------------------------ sequences dealt whole
+@pytest.mark.parametrize("heads,cuts,dk,dv", [(160, [0, 700, 700, 701, 1100, 1500], 24, 40),
+                                              (57, [3, 303, 304, 304, 433, 590], 128, 128),
+                                              (170, [0, 130, 260, 400], 64, 128),
+                                              (101, list(range(0, 600, 37)), 64, 64)])
+def test_linattn_sequences_of_many_heads(dm, heads, cuts, dk, dv):
+    """More heads, or heads and gradients, than SMs: a CTA takes sequences of several of them, one
+    after another.  From states, but to none."""
+    tokens = max(600, cuts[-1])
+    c = mix_case(41, tokens, heads, dk, dv, cuts, False)
+    mix_check(dm, c, 0.3, f"{heads}")
+    first = [c[x].t.clone() for x in ("to_out", "to_dq", "to_dk", "to_dv")]
+    op = mix_check(dm, c, 0.3, f"{heads} again")
+    assert all(torch.equal(a, c[x].t) for a, x in zip(first, ("to_out", "to_dq", "to_dk", "to_dv")))
+
+    n = len(cuts) - 1
+    state, dfinal = (torch.randn(n, heads, dk, dv, device="cuda") for _ in range(2))
+    q, k, v, dout = (c[x].t for x in ("q", "k", "v", "dout"))
+    op.forward(q, k, v, c["g"], c["to_out"].t, offsets=c["offsets"], state=state)
+    op.backward(dout, q, k, v, c["g"], c["to_dq"].t, c["to_dk"].t, c["to_dv"].t, offsets=c["offsets"],
+                state=state, dfinal_state=dfinal)
+    assert op.status() == dm.OK
+    a, g = [np64(x) for x in (q, k, v, dout)], np64(c["g"])
+    st, df = np64(state), np64(dfinal)
+    mag = [np.abs(x) for x in a]
+    live = np.zeros(tokens, bool)
+    live[cuts[0]:cuts[-1]] = True
+    near_mix(c["to_out"].t, oracle.linattn(a[0], a[1], a[2], g, 0.3, cuts, st)["out"],
+             oracle.linattn(mag[0], mag[1], mag[2], g, 0.3, cuts, np.abs(st))["out"], "out", live)
+    back = oracle.linattn_backward(a[3], a[0], a[1], a[2], g, 0.3, cuts, st, df)
+    mass = oracle.linattn_backward(mag[3], mag[0], mag[1], mag[2], g, 0.3, cuts, np.abs(st), np.abs(df))
+    for x in ("dq", "dk", "dv"):
+        near_mix(c["to_" + x].t, back[x], mass[x], x, live)

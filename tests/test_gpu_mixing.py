@@ -736,6 +736,8 @@ def test_step_states_past_2_to_the_32_elements(dm):
 @pytest.mark.parametrize("heads,cuts,dk,dv", [(160, [0, 700, 700, 701, 1100, 1500], 24, 40),
                                               (57, [3, 303, 304, 304, 433, 590], 128, 128),
                                               (170, [0, 130, 260, 400], 64, 128),
+                                              (160, [5, 5, 5, 5], 64, 64),
+                                              (160, [0, 0, 600, 600], 128, 64),
                                               (101, list(range(0, 600, 37)), 64, 64)])
 def test_linattn_sequences_of_many_heads(dm, heads, cuts, dk, dv):
     """More heads, or heads and gradients, than SMs: a CTA takes sequences of several of them, one

@@ -12,8 +12,9 @@
 // into the sines and cosines once per token:
 //   n_a w_a cos - n_b w_b sin = r (x_a (w_a cos) - x_b (w_b sin))
 // Measured, 8192 tokens of 64 heads of 128: 44 us forward (6.1 TB/s, 0.90 of the copy rate; 111
-// with one element at a time), 79 us backward (5.1 TB/s, 0.75; 148 so, and with twice as many
-// registers a thread as forward it has half the warps to hide its 4 shuffles a sum).
+// with one element at a time), 73 us backward (5.5 TB/s, 0.81; 148 so).  With twice as many registers a
+// thread as forward it has half the warps to wait for memory with, hence the next chunk is brought to L2
+// while one is computed (79 us without; 77 two chunks ahead).
 //
 // Angles.  t = position * inv_freq radians is needed modulo a turn only, and in fp32 a
 // position of 10^5 would leave a third of the digits.  inv_freq / 2 pi as a 64-bit fraction of a
@@ -251,7 +252,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
   }
 }
 
-// Gradients.  With SUMS the gains' too: a block sums its own, for rope_gains_kernel.
+// Brings a lane's part of a chunk of heads to L2: by one lane of eight, whose elements share a line.
+template <int LANES>
+DM_DEV void fetch_ahead(const Heads& h, const Share& sh, int l, int t, int h0, int heads) {
+  using C = Chunk<LANES>;
+  if ((l & 7) != 0 || !sh.in) return;
+  const __nv_bfloat16* p = h.p + t * h.ts + h0 * h.hs + 8 * l;
+#pragma unroll
+  for (int d = 0; d < C::kDepth; ++d)
+    if (h0 + d * C::kGroups < heads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + d * C::kGroups * h.hs));
+}
+
+// Gradients; where they are wanted (partial) the gains' too: a block sums its own, for rope_gains_kernel.
 template <int LANES, bool ILV, bool VEC>
 __global__ void __launch_bounds__(kThreads, kGradBlocks) rope_grad_kernel(const __grid_constant__ RopeArgs g) {
   using C = Chunk<LANES>;
@@ -298,6 +311,20 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) rope_grad_kernel(const 
             raw[d].b = load4<VEC>(in + sh.b);
             grad[d].a = load4<VEC>(dy + sh.a);
             grad[d].b = load4<VEC>(dy + sh.b);
+          }
+        }
+        {
+          // the next chunk, of this token or of the warp's next one
+          int t1 = t, n1 = n + 1;
+          if (n1 >= end) {
+            const unsigned u1 = u + gridDim.x * kWarps;
+            t1 = u1 < units ? int(u1 / unsigned(g.parts)) : -1;
+            n1 = int(u1 - unsigned(t1) * unsigned(g.parts)) * g.per;
+          }
+          if (t1 >= 0) {
+            const int x1 = n1 >= q_chunks ? 1 : 0, h1 = (n1 - x1 * q_chunks) * C::kHeads + group;
+            fetch_ahead<LANES>(x1 ? g.x[1] : g.x[0], sh, l, t1, h1, x1 ? g.heads[1] : g.heads[0]);
+            fetch_ahead<LANES>(x1 ? g.dy[1] : g.dy[0], sh, l, t1, h1, x1 ? g.heads[1] : g.heads[0]);
           }
         }
 #pragma unroll
@@ -403,13 +430,13 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
                        : lanes == 16 ? kernel_of<16>(backward, interleaved, vec)
                                      : kernel_of<32>(backward, interleaved, vec);
   // Chunks of a warp share their token's sines; but with few tokens more warps of one chunk each
-  // fill the GPU (8192 tokens of 64 heads of 128: 52 us with 2 chunks to a warp, 48 with 8; 777 of
-  // 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take token after token, so that the
-  // gains' sums meet once a block (88 us with twice the blocks that fit, 82 with as many; 4 chunks to
-  // a warp 79, 2 87, 8 83).
+  // fill the GPU (8192 tokens of 64 heads of 128: 52 us with 2 chunks to a warp, 48 with 8, backward 82
+  // with 2, 75 with 4, 73 with 8; 777 of 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take
+  // token after token, so that the gains' sums meet once a block (88 us with twice the blocks that
+  // fit, 82 with as many).
   const int heads = 32 / lanes * 4;
   const int chunks = (g.heads[0] + heads - 1) / heads + (g.heads[1] + heads - 1) / heads;
-  g.per = (long long)g.tokens * chunks > (long long)sms * 56 ? (backward ? 4 : 8) : 1;
+  g.per = (long long)g.tokens * chunks > (long long)sms * 56 ? 8 : 1;
   g.parts = (chunks + g.per - 1) / g.per;
   const long long units = (long long)g.tokens * g.parts;
   long long blocks = (units + kWarps - 1) / kWarps;

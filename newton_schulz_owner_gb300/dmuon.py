@@ -775,7 +775,8 @@ class LinearAttention:
     q and k are (tokens, heads, key_dim), v and out (tokens, heads, value_dim), bf16, any strides
     between tokens and heads; `log_decay` fp32 (heads,), <= 0; states fp32
     (sequences, heads, key_dim, value_dim).  `offsets` int32 (sequences + 1,) says where sequences
-    begin and end; None: one sequence.  `scale` is key_dim ** -0.5 unless given.
+    begin and end; None: one sequence.  `scale` is key_dim ** -0.5 unless given.  The workspace serves
+    one forward or backward at a time: an object for each stream, or graph, that runs beside another.
     """
 
     def __init__(self, max_tokens: int, heads: int, key_dim: int, value_dim: Optional[int] = None,

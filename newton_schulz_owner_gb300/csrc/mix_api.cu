@@ -245,9 +245,9 @@ Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const D
     if (clusters >= device.sms) break;
   }
   // Dealing whole sequences: the longest of n, cut at random, is H_n / n of the batch; each takes 4 us to
-  // begin.  (Gradients of 8192 tokens of 32 heads in 5 sequences: a CTA to a head and gradient 180 us,
-  // dealt 149; of 4096 tokens of 28 heads, 3 CTAs to each 110 to 124, dealt 79 to 84; 30 sequences of 40
-  // heads 250 and 312.)  Not where one long sequence among short ones would lose much by it.
+  // begin, and with all SMs busy a block takes longer.  (Gradients of 8192 tokens of 32 heads in 5 sequences: a CTA to a head and gradient 180 us,
+  // dealt 149; of 4096 tokens of 28 heads, 3 CTAs to each 110 to 124, dealt 79 to 84, but in 2 equal
+  // sequences 87 and 93; 8192 of 40 heads in 30 sequences 250 and 312.)  Not where one long sequence among short ones would lose much by it.
   const int64_t pairs = sweeps * s.heads, ctas = std::min(int64_t(device.sms), pairs * s.sequences);
   if (whole <= 1.25 * least && !exact && s.sequences > 1 && s.sequences < 32 &&
       pairs * s.sequences <= ctas * (kMixDealt / 2)) {
@@ -255,7 +255,7 @@ Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const D
     for (int64_t i = 1; i <= s.sequences; ++i) longest += one / double(i);
     const double each = std::max(longest, double(blocks * pairs) / double(ctas));
     const double begun = std::ceil(double(pairs * s.sequences) / double(ctas));
-    if (each * sweep + begun * 4 + 6 < least) best = {1, 1, int(ctas)};
+    if (1.2 * (each * sweep + begun * 4 + 6) < least) best = {1, 1, int(ctas)};
   }
   return best;
 }

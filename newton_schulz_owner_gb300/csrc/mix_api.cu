@@ -70,9 +70,10 @@ bool rows_of(const dmuon_heads* h, int64_t tokens, int64_t heads, int64_t dim, R
 // Whether two tensors of the same tokens (heads and dims may differ) may share an element.
 bool overlap(const Rows& a, const Rows& b) {
   if (a.end() <= b.p || b.end() <= a.p) return false;
-  // a stride over one row is any stride
+  // a stride over one row is any stride that neither's row passes
   if ((a.tokens > 1 && a.ts != b.ts) || (a.heads > 1 && b.heads > 1 && a.hs != b.hs)) return true;
-  const int64_t ts = a.tokens > 1 ? a.ts : int64_t(1) << 40, hs = a.heads > 1 ? a.hs : b.hs;
+  const int64_t ts = a.tokens > 1 ? a.ts : int64_t(1) << 40,
+                hs = a.heads > 1 ? a.hs : b.heads > 1 ? b.hs : std::max(a.dim, b.dim);
   // parts of one packed tensor: b's place against a's as whole strides, outer and inner, and a
   // rest.  Element (t, h, x) of a is (t', h', x') of b where
   //   apart = (t - t') ts + (h - h') hs + (x - x')

@@ -268,6 +268,34 @@ def test_overlap_is_found_as_element_sets_have_it(dm):
             assert (got == dm.ERR_INVALID_ARG) == share, (tokens, heads, ts, hs, apart)
 
 
+def test_overlap_of_unequal_head_sizes_is_found_as_element_sets_have_it(dm):
+    """The same with keys wider or narrower than values, the output against the query (and the query
+    against the output: the one that lies first changes with the sign of the distance) and, for
+    gradients, those of queries and values against one another."""
+    for tokens, heads, ts, hs in [(1, 1, 0, 0), (3, 1, 40, 0), (3, 1, 24, 0), (1, 2, 0, 32),
+                                  (3, 2, 72, 24), (3, 2, 24, 80)]:
+        for dk, dv in [(8, 24), (24, 8), (16, 24), (24, 16)]:
+            def cells(d):
+                return {t * ts + h * hs + x for t in range(tokens) for h in range(heads) for x in range(d)}
+            s = dm.LinattnShape(tokens, 1, heads, dk, dv, 1.0)
+            need = dm.lib().dmuon_linattn_workspace_bytes(ctypes.byref(s), 1)
+            for apart in range(-240, 241, 8):
+                h = [Heads(P + GAP + i, ts, hs) for i in (0, GAP, 2 * GAP, 2 * apart)]
+                step = dm.lib().dmuon_linattn_step(ctypes.byref(s), ref(h[0]), ref(h[1]), ref(h[2]), W, None,
+                                                   tokens, W, W, ref(h[3]), None)
+                fwd = dm.lib().dmuon_linattn_forward(ctypes.byref(s), ref(h[0]), ref(h[1]), ref(h[2]), W, None,
+                                                     None, None, ref(h[3]), W, need, None)
+                t = [place(i + 4, ts, hs) for i in range(7)]           # dout, q, k, v, dq, dk, dv
+                t[4], t[6] = h[0], h[3]
+                back = dm.lib().dmuon_linattn_backward(ctypes.byref(s), *(ref(x) for x in t[:4]), W, None,
+                                                       None, None, *(ref(x) for x in t[4:]), None, W, need,
+                                                       None)
+                at = cells(dk)
+                share = any(c + apart in at for c in cells(dv))
+                for got in (step, fwd, back):
+                    assert (got == dm.ERR_INVALID_ARG) == share, (tokens, heads, ts, hs, dk, dv, apart)
+
+
 def test_binding_refuses_bad_tensors(dm):
     """Types, shapes, devices and handles, as far as they show without a GPU."""
     with pytest.raises(dm.DMuonError):

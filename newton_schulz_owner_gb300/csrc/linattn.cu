@@ -983,8 +983,9 @@ struct OutRole {
     if (lane == 0) mbar_arrive(&sh->taken);
     const int first = row0 + warp * 32;
     const int rows = live - warp * 32;  // of this warp that exist
+    // TMA reads what was written, or (all rows or some past the end) writes queries over it
+    fence_proxy_async_smem();
     if (__builtin_expect(rows >= 32, 1)) {
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
 #pragma unroll

@@ -769,3 +769,32 @@ def test_linattn_sequences_of_many_heads(dm, heads, cuts, dk, dv):
     mass = oracle.linattn_backward(mag[3], mag[0], mag[1], mag[2], g, 0.3, cuts, np.abs(st), np.abs(df))
     for x in ("dq", "dk", "dv"):
         near_mix(c["to_" + x].t, back[x], mass[x], x, live)
+
+
+# ------------------------------------------------------------------ ends inside blocks
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+def test_linattn_queries_after_the_ends_of_sequences(dm, dk, dv):
+    """A CTA walks 40 sequences that end inside blocks, some of one row only: the queries that are
+    loaded over such an end's output are whole.  Bit for bit what each sequence gives alone, which is
+    too short for any place in shared memory to be used twice."""
+    heads, lengths = 160, [1, 129, 33, 200, 95, 130, 0, 255, 64, 3] * 4
+    cuts = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    c = mix_case(43, cuts[-1], heads, dk, dv, cuts, False)
+    op = dm.LinearAttention(cuts[-1], heads, dk, dv, max_sequences=len(lengths), scale=0.2)
+    names = ("q", "k", "v", "dout")
+    outs = ("to_out", "to_dq", "to_dk", "to_dv")
+
+    def run(offsets, at):
+        q, k, v, dout = (c[x].t[at] for x in names)
+        out, dq, dkk, dvv = (torch.zeros_like(x) for x in (v, q, k, v))
+        op.forward(q, k, v, c["g"], out, offsets=offsets)
+        op.backward(dout, q, k, v, c["g"], dq, dkk, dvv, offsets=offsets)
+        return out, dq, dkk, dvv
+
+    whole = run(c["offsets"], slice(None))
+    assert op.status() == dm.OK
+    for b, e in sorted(set(zip(cuts, cuts[1:]))):
+        if b == e:
+            continue
+        for n, x, y in zip(outs, whole, run(None, slice(b, e))):
+            assert torch.equal(x[b:e], y), (n, b, e)

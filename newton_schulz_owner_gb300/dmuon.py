@@ -695,7 +695,7 @@ class QKNormRope:
         self.head_dim = int(head_dim)
         self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
         self.eps, self.interleaved, self.with_backward = float(eps), bool(interleaved), bool(backward)
-        self._last = (-1,)
+        self._last = (None,)
         shape = self._shape(self.max_tokens)
         nbytes = int(_lib.dmuon_qk_norm_rope_workspace_bytes(ctypes.byref(shape)))
         if nbytes == 0:
@@ -714,11 +714,13 @@ class QKNormRope:
             raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.q_heads}, "
                              f"{self.head_dim}), got {tuple(q.shape)}")
         dev = _launch_device(self.workspace, "the workspace")
-        last = self._last          # shapes of the last number of tokens
-        if last[0] != t:
-            last = self._last = (t, self._shape(t), (t, self.q_heads, self.head_dim),
+        # shapes of the last call, unless a size or another attribute is not what it was then
+        key = (t, self.q_heads, self.k_heads, self.head_dim, self.rotary_dim, self.interleaved, self.eps)
+        last = self._last
+        if last[0] != key:
+            last = self._last = (key, t, self._shape(t), (t, self.q_heads, self.head_dim),
                                  (t, self.k_heads, self.head_dim))
-        return last + (dev,)
+        return last[1:] + (dev,)
 
     def _key(self, k, shape, what, dev):
         if self.k_heads == 0:
@@ -786,7 +788,7 @@ class LinearAttention:
         self.value_dim = self.key_dim if value_dim is None else int(value_dim)
         self.max_sequences, self.with_backward = int(max_sequences), bool(backward)
         self.scale = max(1, self.key_dim) ** -0.5 if scale is None else float(scale)
-        self._last = (-1, -1)
+        self._last = (None,)
         shape = self._shape(self.max_tokens, self.max_sequences)
         nbytes = int(_lib.dmuon_linattn_workspace_bytes(ctypes.byref(shape), int(self.with_backward)))
         if nbytes == 0:
@@ -810,11 +812,13 @@ class LinearAttention:
                 raise ValueError(f"offsets: expected (sequences + 1 <= {self.max_sequences + 1},), "
                                  f"got {tuple(offsets.shape)}")
             off = _flat(offsets, torch.int32, (n + 1,), "offsets", dev)
-        last = self._last          # shapes of the last numbers of tokens and sequences
-        if last[0] != t or last[1] != n:
-            last = self._last = (t, n, self._shape(t, n), (t, self.heads, self.key_dim),
+        # shapes of the last call, unless a size or another attribute is not what it was then
+        key = (t, n, self.heads, self.key_dim, self.value_dim, self.scale)
+        last = self._last
+        if last[0] != key:
+            last = self._last = (key, t, n, self._shape(t, n), (t, self.heads, self.key_dim),
                                  (t, self.heads, self.value_dim))
-        return last + (off, dev)
+        return last[1:] + (off, dev)
 
     def _state(self, state, n, what, dev):
         return None if state is None else _flat(

@@ -798,3 +798,35 @@ def test_linattn_queries_after_the_ends_of_sequences(dm, dk, dv):
             continue
         for n, x, y in zip(outs, whole, run(None, slice(b, e))):
             assert torch.equal(x[b:e], y), (n, b, e)
+
+
+# ------------------------------------------------------------------ the binding
+def test_attributes_changed_after_a_call_hold(dm):
+    """What a handle says of itself is what its next call does."""
+    draw = Draw(48)
+    q, k, v = (draw((9, 2, 64)) for _ in range(3))
+    f, pos = rope_reference(64, 64), torch.arange(9, device="cuda", dtype=torch.int32)
+    rope = dm.QKNormRope(9, 2, 2, 64)
+    rope.forward(q, k, None, None, f, pos, torch.empty_like(q), torch.empty_like(k))
+    for name, value in (("eps", 0.5), ("interleaved", True), ("rotary_dim", 32)):
+        setattr(rope, name, value)
+        fresh = dm.QKNormRope(9, 2, 2, 64, rope.rotary_dim, rope.eps, rope.interleaved)
+        got, want = ([torch.empty_like(q), torch.empty_like(k)] for _ in range(2))
+        freq = f[:rope.rotary_dim // 2].contiguous()
+        rope.forward(q, k, None, None, freq, pos, *got)
+        fresh.forward(q, k, None, None, freq, pos, *want)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+    g = torch.full((2,), -0.1, device="cuda")
+    mix, got, want = dm.LinearAttention(9, 2, 64), torch.empty_like(v), torch.empty_like(v)
+    mix.forward(q, k, v, g, want)
+    mix.scale *= 2
+    mix.forward(q, k, v, g, got)
+    assert torch.equal(got, want * 2)
+    one = mix.heads = rope.q_heads = 1
+    out = torch.empty_like(v[:, :one])
+    mix.forward(q[:, :one], k[:, :one], v[:, :one], g[:one], out)
+    assert torch.equal(out, got[:, :one])
+    with pytest.raises(ValueError):
+        mix.forward(q, k, v, g, got)
+    with pytest.raises(ValueError):
+        rope.forward(q, k, None, None, freq, pos, q, k)

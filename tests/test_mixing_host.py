@@ -321,3 +321,23 @@ def test_binding_refuses_bad_tensors(dm):
         dm.LinearAttention(4, 2, 64, backward=False, device="cpu").backward(x, x, x, x, g, x, x, x)
     with pytest.raises(ValueError):
         dm.QKNormRope(4, 2, 2, 64, backward=False, device="cpu").backward(x, x, x, x, None, None, g, g, x, x)
+
+
+def test_shapes_of_a_call_follow_the_attributes(dm, monkeypatch):
+    """A handle keeps the shapes of its last call, and makes new ones once it says something else."""
+    monkeypatch.setattr(dm, "_launch_device", lambda t, what: 0)
+    q = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    rope, mix = dm.QKNormRope(4, 2, 2, 64, device="cpu"), dm.LinearAttention(4, 2, 64, device="cpu")
+    same = rope._begin(q)[1], mix._begin(q)[2]
+    assert rope._begin(q)[1] is same[0] and mix._begin(q)[2] is same[1]
+    for name, value in (("eps", 0.25), ("interleaved", True), ("rotary_dim", 32), ("head_dim", 32),
+                        ("q_heads", 3), ("k_heads", 1)):
+        setattr(rope, name, value)
+        t, shape, qs, ks, _ = rope._begin(q)
+        assert getattr(shape, name) == value and t == 4, name
+        assert qs == (4, rope.q_heads, rope.head_dim) and ks == (4, rope.k_heads, rope.head_dim)
+    for name, value in (("scale", 0.25), ("key_dim", 32), ("value_dim", 16), ("heads", 3)):
+        setattr(mix, name, value)
+        t, n, shape, ks, vs, _, _ = mix._begin(q)
+        assert getattr(shape, name) == value and (t, n) == (4, 1), name
+        assert ks == (4, mix.heads, mix.key_dim) and vs == (4, mix.heads, mix.value_dim)

@@ -463,8 +463,9 @@ typedef struct {
  *                offsets are cut to 0 .. tokens.
  *   state        device, fp32, contiguous (sequences, heads, key_dim, value_dim): S before the
  *                first token of each sequence; NULL: zeros
- *   final_state  the same after the last token; NULL: not wanted.  May be `state`; otherwise it
- *                lies apart from it, as it and out do from all that is read.
+ *   final_state  the same after the last token (without tokens `state`, bit for bit); NULL: not
+ *                wanted.  May be `state`; otherwise it lies apart from it, as it and out do from
+ *                all that is read.
  * Tokens are taken in blocks of 128 counted from their sequence's start.  The weighted scores of
  * a block, the state that enters it and the keys times their decay are rounded to bf16 as
  * operands of products that accumulate in fp32; with final_state the keys are kept to 16 bits, so
@@ -485,7 +486,8 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
  * dmuon_linattn_backward -- its gradients (nothing is kept by forward):
  *   dfinal_state  gradient of final_state, or NULL for zeros
  *   dstate        gradient of state, or NULL: not wanted (kept like final_state).  May be
- *                 dfinal_state.
+ *                 dfinal_state.  With either, 2^-64 <= |scale| <= 2^64, DMUON_ERR_UNSUPPORTED
+ *                 otherwise.  Of a sequence without tokens it is dfinal_state, bit for bit.
  * With g_t = scale dout_t and D_t the gradient of S_t, both along the sequence:
  *   D_t = q_t g_t^T + exp(log_decay) D_{t+1},   dq_t = S_t g_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
  * A NaN or an infinity in q, k, v or dout may reach all gradients of its sequence and head.

@@ -568,19 +568,18 @@ struct StateRole {
   DM_DEV void read_initial(int seq) {
     if (g.state_in == nullptr || row >= g.dk) return;
     const float* p = g.state_in + state_at(seq) + row * g.st_row + col * g.st_col;
-    const F2 f = f2(g.in_scale, g.in_scale);
     if (g.st_col == 1) {
 #pragma unroll
       for (int i = 0; i < kCols / 4; ++i)
         if (col + 4 * i < g.dv) {
           const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
-          st[2 * i] = mul2(f, f2(v.x, v.y));
-          st[2 * i + 1] = mul2(f, f2(v.z, v.w));
+          st[2 * i] = f2(v.x, v.y);
+          st[2 * i + 1] = f2(v.z, v.w);
         }
     } else {
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i, p += 2 * g.st_col)
-        if (col + 2 * i < g.dv) st[i] = mul2(f, f2(p[0], p[g.st_col]));
+        if (col + 2 * i < g.dv) st[i] = f2(p[0], p[g.st_col]);
     }
   }
   DM_DEV void write_final(int seq) {  // of the gradients' sweeps only dv's has one: never transposed
@@ -591,9 +590,7 @@ struct StateRole {
       float4 v;
       f2_split(st[2 * i], v.x, v.y);
       f2_split(st[2 * i + 1], v.z, v.w);
-      if (col + 4 * i < g.dv)
-        *reinterpret_cast<float4*>(p + 4 * i) = make_float4(g.out_scale * v.x, g.out_scale * v.y,
-                                                            g.out_scale * v.z, g.out_scale * v.w);
+      if (col + 4 * i < g.dv) *reinterpret_cast<float4*>(p + 4 * i) = v;
     }
   }
   // A state in the workspace, four columns at a time so that a warp's rows lie together.  Slots of
@@ -621,8 +618,7 @@ struct StateRole {
     for (int i = 0; i < kCols / 4; ++i, p += 4 * g.st_col) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < g.dk && col + 4 * i < g.dv)
-        v = make_float4(g.in_scale * p[0], g.in_scale * p[g.st_col], g.in_scale * p[2 * g.st_col],
-                        g.in_scale * p[3 * g.st_col]);
+        v = make_float4(p[0], p[g.st_col], p[2 * g.st_col], p[3 * g.st_col]);
       __stcg(to + i * 128, v);
     }
   }
@@ -692,7 +688,7 @@ struct StateRole {
   // The thread's unit n of the keys, its token
   DM_DEV int token_of(int n) const { return ((tid >> 3) + 32 * n) & (kMixBlock - 1); }
   DM_DEV float key_weight(int j, int live) const {
-    return j >= live ? 0.f : sh->power[g.against ? j + 1 : live - 1 - j];
+    return j >= live ? 0.f : g.key_scale * sh->power[g.against ? j + 1 : live - 1 - j];
   }
   // Keys of block `it` times their decay, in place; what bf16 drops of them (EXACT) to `low`.  The
   // decay is kept as a sum of two bf16 numbers, so that k a = k a_0 + k a_1 is rounded like an fp32
@@ -838,7 +834,7 @@ struct StateRole {
       const long long at = state_at(s);
 #pragma unroll 1
       for (int i = tid; i < g.dk * g.dv; i += kThreadsHere)
-        g.state_out[at + i] = g.state_in == nullptr ? 0.f : g.out_scale * (g.in_scale * g.state_in[at + i]);
+        g.state_out[at + i] = g.state_in == nullptr ? 0.f : g.state_in[at + i];
     }
   }
 };
@@ -958,7 +954,7 @@ struct OutRole {
     tc_fence_after();
     const Block& b = sh->sweep[swept % kRing];
     const int live = b.live, row0 = b.row, s = b.it % T::stages, row = warp * 32 + lane;
-    const float f = row < live ? g.scale * sh->power[g.against ? live - 1 - row : row + 1] : 0.f;
+    const float f = row < live ? g.state_scale * sh->power[g.against ? live - 1 - row : row + 1] : 0.f;
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(warp * 32) << 16);
     // 32 columns to a piece of 2 KB, rows of 64 bytes

@@ -42,6 +42,7 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
 //   along:    S_t = a S_{t-1} + k_t v_t^T,      out_t = scale q_t S_t       state_out = S behind the last
 //   against:  R_t = R_{t+1} + k_t v_t^T,        out_t = scale q_t R_t,
 //             then decayed on its way to t - 1:  R_t <- a R_t               state_out = R before the first
+// state_in and state_out are what the sweep keeps: S, or with key_scale = scale, scale S (R alike).
 struct LinAttnArgs {
   CUtensorMap q, k, v, o;     // loads: 64 x 1 x 128 boxes; o: stores of 32 x 1 x 32
   const float* log_decay;
@@ -51,7 +52,9 @@ struct LinAttnArgs {
   int against;
   const float* state_in;      // or null
   float* state_out;           // or null
-  float in_scale, out_scale;  // of the state on its way in and out
+  // The state kept is S or R itself (1 and scale), or scale times it (scale and 1): what the keys are
+  // multiplied by on the way to it, and the queries' product with it on its way out.
+  float key_scale, state_scale;
   int st_row, st_col;         // element strides of a state (row: the keys' side)
   Heads out;
   int groups;                 // runs that a head's sequences are cut into, a cluster each

@@ -285,7 +285,7 @@ struct Sweep {
   const float* state_in;
   float* state_out;
   bool transposed;  // the caller's state is (value, key)
-  float in_scale, out_scale;
+  bool scaled;      // and scale times the sum
 };
 int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const float* log_decay,
                const int32_t* offsets, const Device& device, void* ws, cudaStream_t st) {
@@ -311,8 +311,8 @@ int run_sweeps(const dmuon_linattn_shape& s, const Sweep* w, int sweeps, const f
     g.against = w->against;
     g.state_in = w->state_in;
     g.state_out = w->state_out;
-    g.in_scale = w->in_scale;
-    g.out_scale = w->out_scale;
+    g.key_scale = w->scaled ? s.scale : 1.f;
+    g.state_scale = w->scaled ? 1.f : s.scale;
     g.st_row = w->transposed ? 1 : g.dv;
     g.st_col = w->transposed ? g.dk : 1;
     g.out = device_heads(*w->out);
@@ -418,7 +418,7 @@ int dmuon_linattn_forward(const dmuon_linattn_shape* shape, const dmuon_heads* q
   Device device;
   e = device_ready(&device);
   if (e != DMUON_OK) return e;
-  const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, 1.f, 1.f};
+  const Sweep w{&qr, &kr, &vr, &orow, false, state, final_state, false, false};
   return run_sweeps(s, &w, 1, log_decay, offsets, device, workspace, stream);
 }
 
@@ -447,6 +447,11 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
   const States first(state, s, s.sequences), dlast(dfinal_state, s, s.sequences),
       dfirst(dstate, s, s.sequences);
   if (!dfirst.beside(dlast)) return DMUON_ERR_INVALID_ARG;
+  // the scale is a factor of q and dout then, on their way to the states' gradients: a range in which
+  // elements up to 2^63 do not overflow by it
+  if ((dfinal_state != nullptr || dstate != nullptr) &&
+      !(std::fabs(s.scale) >= 0x1p-64f && std::fabs(s.scale) <= 0x1p64f))
+    return DMUON_ERR_UNSUPPORTED;
   if (s.tokens > 0) {
     for (const Rows* o : {&dqr, &dkr, &dvr}) {
       if (first.meets(*o) || dlast.meets(*o)) return DMUON_ERR_INVALID_ARG;
@@ -460,11 +465,11 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
   Device device;
   e = device_ready(&device);
   if (e != DMUON_OK) return e;
-  const float inv = 1.f / s.scale;
-  const Sweep sweeps[3] = {
-      {&dor, &vr, &kr, &dqr, false, state, nullptr, true, 1.f, 1.f},
-      {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, inv, 1.f},
-      {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, inv, s.scale}};
+  // The states' gradients hold the scale, dout and q as they are read do not.
+  const bool scaled = dfinal_state != nullptr || dstate != nullptr;
+  const Sweep sweeps[3] = {{&dor, &vr, &kr, &dqr, false, state, nullptr, true, false},
+                           {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, scaled},
+                           {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, scaled}};
   if (s.tokens == 0) return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, device, workspace, stream);
   // The three side by side fill the GPU without cutting sequences as finely (8192 tokens of 32 heads:
   // 285 us one after another, 204 together).  Apart where dv's sweep is another kernel, or writes

@@ -830,3 +830,39 @@ def test_attributes_changed_after_a_call_hold(dm):
         mix.forward(q, k, v, g, got)
     with pytest.raises(ValueError):
         rope.forward(q, k, None, None, freq, pos, q, k)
+
+
+# ------------------------------------------------------------------ gradients of states
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (72, 40)])
+def test_linattn_gradients_of_states_keep_their_size(dm, dk, dv):
+    """The final states' gradient is large and the scale small: nothing on the way leaves fp32."""
+    tokens, heads, off, scale = 300, 3, [0, 0, 140, 300, 300], 2.0 ** -60
+    c = mix_case(46, tokens, heads, dk, dv, off, True)
+    c["dfinal"] *= 2.0 ** 70
+    op = dm.LinearAttention(tokens, heads, dk, dv, max_sequences=4, scale=scale)
+    q, k, v, dout = (c[x].t for x in ("q", "k", "v", "dout"))
+    dq, dkk, dvv = (c[x].t for x in ("to_dq", "to_dk", "to_dv"))
+    args = [np64(x) for x in (dout, q, k, v, c["g"])] + [scale, off, np64(c["state"]), np64(c["dfinal"])]
+    ref = oracle.linattn_backward(*args)
+    mass = oracle.linattn_backward(*(np.abs(x) for x in args[:4]), *args[4:7], *(np.abs(x) for x in args[7:]))
+    for want_dstate in (True, False):
+        op.backward(dout, q, k, v, c["g"], dq, dkk, dvv, offsets=c["offsets"], state=c["state"],
+                    dfinal_state=c["dfinal"], dstate=c["dstate"] if want_dstate else None)
+        for n, got in (("dq", dq), ("dk", dkk), ("dv", dvv)):
+            near_mix(got, ref[n], mass[n], n)
+    no_worse(c["dstate"], ref["dstate"], 1.25 * 2.0 ** -16 * mass["dstate"] + 2.0 ** -30, "dstate")
+
+
+@pytest.mark.parametrize("scale", [0.3, -7.0, 2.0 ** -64])
+def test_linattn_states_pass_empty_sequences_bit_for_bit(dm, scale):
+    heads, d, off = 3, 64, [0, 0, 140, 140]
+    c = mix_case(47, 140, heads, d, d, off, True)
+    c["dfinal"][0] *= 1e30
+    c["dfinal"][2] *= 1e-37
+    op = dm.LinearAttention(140, heads, d, max_sequences=3, scale=scale)
+    q, k, v, dout = (c[x].t for x in ("q", "k", "v", "dout"))
+    op.forward(q, k, v, c["g"], c["to_out"].t, offsets=c["offsets"], state=c["state"], final_state=c["final"])
+    op.backward(dout, q, k, v, c["g"], *(c[x].t for x in ("to_dq", "to_dk", "to_dv")), offsets=c["offsets"],
+                state=c["state"], dfinal_state=c["dfinal"], dstate=c["dstate"])
+    for i in (0, 2):
+        assert torch.equal(c["final"][i], c["state"][i]) and torch.equal(c["dstate"][i], c["dfinal"][i])

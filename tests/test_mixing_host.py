@@ -341,3 +341,13 @@ def test_shapes_of_a_call_follow_the_attributes(dm, monkeypatch):
         t, n, shape, ks, vs, _, _ = mix._begin(q)
         assert getattr(shape, name) == value and (t, n) == (4, 1), name
         assert ks == (4, mix.heads, mix.key_dim) and vs == (4, mix.heads, mix.value_dim)
+
+
+def test_gradients_of_states_refuse_far_scales(dm):
+    """With states' gradients the scale is a factor of operands."""
+    for scale, ok in ((2.0 ** -64, True), (-2.0 ** 64, True), (2.0 ** -65, False), (-2.0 ** 65, False),
+                      (1e-38, False), (3e38, False)):
+        s = (4, 1, 4, 64, 64, scale)
+        assert lin_back(dm, shape=s) not in ARGUMENT
+        for states in (dict(dfin=W), dict(dst=W), dict(dfin=W, dst=W)):
+            assert (lin_back(dm, shape=s, **states) == dm.ERR_UNSUPPORTED) == (not ok), (scale, states)

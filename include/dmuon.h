@@ -469,7 +469,9 @@ typedef struct {
  * Tokens are taken in blocks of 128 counted from their sequence's start.  The weighted scores of
  * a block, the state that enters it and the keys times their decay are rounded to bf16 as
  * operands of products that accumulate in fp32; with final_state the keys are kept to 16 bits, so
- * that the state is within 2^-15 of the sum of its terms' magnitudes.
+ * that the state is within 2^-15 + n 2^-24 of the sum of its terms' magnitudes after n blocks (the
+ * second part where every rounding of a fp32 sum falls to one side, as for equal terms; what rounds
+ * in the decays does not add up).  With final_state, out may differ in its last bits.
  * A NaN or an infinity in v reaches all tokens of its block of its sequence and those after it
  * (one in k its own token and those after, one in q its own); no other sequence or head.
  * Rows of heads are 16-byte aligned (strides multiples of 8 elements), DMUON_ERR_ALIGNMENT

@@ -87,7 +87,8 @@ enum BlockKind {
   kSweep = 1,  // swept; without it only summed, for the CTAs behind this one
   kFirst = 2,  // of its kind
   kLast = 4,
-  kEnd = 8     // no block: all are done
+  kEnd = 8,    // no block: all are done
+  kAbove = 16  // which of two numbers decays the state over a whole one
 };
 struct Block {
   int kind, row, live;       // first token, tokens
@@ -123,10 +124,14 @@ struct Shared {
   };
   alignas(16) float fall[96];        // what weigh() needs of the powers of a
   float near_[64];                   // scale a^n, n = -32 .. 31; zeros below 0
-  float power[kMixBlock + 1];        // a^n
+  uint32_t key[kMixBlock + 1];       // key_scale a^n as the sum of two bf16
+  float whole[2];                    // the fp32 numbers below and above a^128,
+  uint32_t above;                    // and how often a block takes the latter, in 2^-32
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "");
 
+// a^n; 1 for n = 0 however fast the head forgets.
+DM_DEV float power_of(float log_decay, int n) { return n == 0 ? 1.f : expf(log_decay * float(n)); }
 DM_DEV bool gave_up(int* err, volatile int* flag) {
   *flag = 1;
   atomicExch(err, DMUON_ERR_TIMEOUT);
@@ -381,15 +386,21 @@ DM_DEV void load_role(const LinAttnArgs& g, const Work& w, int head, bool again,
   using T = Tiles<DK, DV>;
   volatile int* flag = &sh->abort;
   int it = 0, swept = 0;
+  // A slow head multiplies its state by a^128 thousands of times, and an error of 2^-25 with one sign
+  // would add up (2^20 tokens, log_decay -1e-6: 7e-5 of the state).  So whole blocks take the fp32
+  // numbers below and above a^128 in turn, as often as their mean asks for: the product of any run of
+  // them is within 2^-23.
+  const uint32_t above = sh->above;
   auto load = [&](const Cursor& c, int kind) {
     const int s = it % T::stages;
     const uint32_t parity = ((it / T::stages) & 1) ^ 1;
     uint8_t* q = smem + s * T::stage;
     uint8_t *k = q + T::q, *v = k + T::k;
-    if (!await(&sh->empty[s], parity, g.err, flag)) return false;
-    const Block b{kind, c.row(g), c.live(g), c.seq, c.m, c.x.blocks, c.x.len, it};
+    const Block b{kind | (uint32_t(c.m + 1) * above < above ? kAbove : 0), c.row(g), c.live(g), c.seq, c.m,
+                  c.x.blocks, c.x.len, it};
     sh->block[it % kRing] = b;
     if (kind & kSweep) sh->sweep[swept++ % kRing] = b;
+    if (!await(&sh->empty[s], parity, g.err, flag)) return false;
     if (kind & kEnd) {
       mbar_arrive(&sh->full[s]);
     } else {
@@ -687,8 +698,8 @@ struct StateRole {
   }
   // The thread's unit n of the keys, its token
   DM_DEV int token_of(int n) const { return ((tid >> 3) + 32 * n) & (kMixBlock - 1); }
-  DM_DEV float key_weight(int j, int live) const {
-    return j >= live ? 0.f : g.key_scale * sh->power[g.against ? j + 1 : live - 1 - j];
+  DM_DEV uint32_t key_weight(int j, int live) const {
+    return j >= live ? 0u : sh->key[g.against ? j + 1 : live - 1 - j];
   }
   // Keys of block `it` times their decay, in place; what bf16 drops of them (EXACT) to `low`.  The
   // decay is kept as a sum of two bf16 numbers, so that k a = k a_0 + k a_1 is rounded like an fp32
@@ -709,10 +720,8 @@ struct StateRole {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = token_of(half * 2 + e);
-        const float f = key_weight(j, live);
-        const uint32_t w0 = pack_bf16(f, f), mask = j < live ? 0xFFFFFFFFu : 0u;
-        const float rest = f - bf16_lo(w0);
-        const uint32_t w1 = pack_bf16(rest, rest);
+        const uint32_t w = key_weight(j, live), mask = j < live ? 0xFFFFFFFFu : 0u;
+        const uint32_t w0 = __byte_perm(w, 0, 0x1010), w1 = __byte_perm(w, 0, 0x3232);
 #pragma unroll
         for (int b = e; b < kBatch; b += 2) {
           uint32_t y[4];
@@ -738,10 +747,10 @@ struct StateRole {
       if (token_of(n) >= b.live) st_shared_v4(at + n * kThreadsHere * 16, 0, 0, 0, 0);
   }
   DM_DEV bool block_done(int it) { return wait(&sh->block_state, it); }
-  // Block `it`, of `live` tokens, joins the state.
-  DM_DEV void add_block(int live) {
+  // A block joins the state.
+  DM_DEV void add_block(const Block& b) {
     tc_fence_after();
-    const float f = sh->power[live];
+    const float f = b.live == kMixBlock ? sh->whole[(b.kind & kAbove) != 0] : expf(log_decay * float(b.live));
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(row & ~31) << 16) + kColState + col;
     float x[2][16];
@@ -799,7 +808,7 @@ struct StateRole {
     int swept = 0, share_seq = -1;
     if (!wait(&sh->full[0], 0)) return;
     Block b = sh->block[0];
-    if (g.split > 1 && (b.kind == kEnd || (b.kind & kSweep)) && !arrive()) return;  // it has no share
+    if (g.split > 1 && (b.kind & (kEnd | kSweep)) != 0 && !arrive()) return;  // it has no share
 #pragma unroll 1
     for (int it = 0; (b.kind & kEnd) == 0; ++it) {
       const int s = it % T::stages, s1 = (it + 1) % T::stages;
@@ -816,7 +825,7 @@ struct StateRole {
       if (!wait(&sh->full[s1], (it + 1) / T::stages)) return;
       const Block next = sh->block[(it + 1) % kRing];
       if (!block_done(it)) return;
-      add_block(b.live);
+      add_block(b);
       if (EXACT && __builtin_expect(sweep && g.state_out != nullptr && b.m + 1 == b.blocks, 0))
         write_final(b.seq);
       if (__builtin_expect((b.kind & kLast) != 0, 0)) {
@@ -850,6 +859,7 @@ struct WeighRole {
   const LinAttnArgs& g;
   const Work& w;
   Shared* sh;
+  float log_decay;
   int warp, lane;
 
   DM_DEV bool wait(uint64_t* bar, int n) { return await(bar, n & 1, g.err, &sh->abort); }
@@ -915,7 +925,7 @@ struct WeighRole {
     return true;
   }
   DM_DEV void run() {
-    const float f = g.scale * sh->power[g.against ? 31 - lane : lane];
+    const float f = g.scale * power_of(log_decay, g.against ? 31 - lane : lane);
     const F2 own = f2(f, f);
     const int n = w.n;
     if (g.against) {
@@ -939,9 +949,16 @@ struct OutRole {
   const Work& w;
   Shared* sh;
   uint8_t* smem;
+  float log_decay;
   int head, warp, lane;
+  float whole;  // weight of a whole block
 
   DM_DEV bool wait(uint64_t* bar, int n) { return await(bar, n & 1, g.err, &sh->abort); }
+  // of the entering state in the thread's row of a block of `live` tokens
+  DM_DEV float weight(int live) const {
+    const int row = warp * 32 + lane;
+    return row < live ? g.state_scale * power_of(log_decay, g.against ? live - 1 - row : row + 1) : 0.f;
+  }
   // The store of the last block has left stage s.
   DM_DEV void release(int s) {
     if (lane == 0) {
@@ -953,8 +970,8 @@ struct OutRole {
     if (!wait(&sh->out, swept)) return false;
     tc_fence_after();
     const Block& b = sh->sweep[swept % kRing];
-    const int live = b.live, row0 = b.row, s = b.it % T::stages, row = warp * 32 + lane;
-    const float f = row < live ? g.state_scale * sh->power[g.against ? live - 1 - row : row + 1] : 0.f;
+    const int live = b.live, row0 = b.row, s = b.it % T::stages;
+    const float f = __builtin_expect(live == kMixBlock, 1) ? whole : weight(live);
     const F2 ff = f2(f, f);
     const uint32_t at = sh->tmem + (uint32_t(warp * 32) << 16);
     // 32 columns to a piece of 2 KB, rows of 64 bytes
@@ -1010,6 +1027,7 @@ struct OutRole {
   }
   DM_DEV void run() {
     const int n = w.n;
+    whole = weight(kMixBlock);
 #pragma unroll 1
     for (int swept = 0; swept < n && block(swept); ++swept) {
     }
@@ -1099,13 +1117,28 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
     log_decay = g.log_decay[head];
     const int t = int(threadIdx.x);
     if (t <= kMixBlock) {
-      sh->power[t] = t == 0 ? 1.f : expf(log_decay * float(t));
+      const float f = g.key_scale * power_of(log_decay, t), high = bf16_lo(pack_bf16(f, f));
+      sh->key[t] = pack_bf16(high, f - high);
     } else if (t < kMixBlock + 1 + 64) {
       const int n = t - kMixBlock - 1 - 32;
-      sh->near_[n + 32] = n < 0 ? 0.f : g.scale * (n == 0 ? 1.f : expf(log_decay * float(n)));
+      sh->near_[n + 32] = n < 0 ? 0.f : g.scale * power_of(log_decay, n);
     } else if (t < kMixBlock + 1 + 64 + 96) {
       const int n = t - kMixBlock - 1 - 64;
       sh->fall[n] = expf(log_decay * float(g.against ? n + 1 : 96 - n));
+    } else if (t == kMixBlock + 1 + 64 + 96) {
+      // a^128 = 1 + e = f + rest, exactly; a rounding below 0.57 does not outlast a few blocks
+      const float z = log_decay * float(kMixBlock), e = expm1f(z);
+      float f = 1.f + e, above = 0.f;
+      if (z <= 0.f && f > 0.57f) {
+        const float rest = e - (f - 1.f);
+        if (rest < 0.f) f -= 0x1p-24f;
+        above = fminf((rest < 0.f ? rest + 0x1p-24f : rest) * 0x1p56f, 0x1.fffffep31f);
+      } else {
+        f = expf(z);
+      }
+      sh->whole[0] = f;
+      sh->whole[1] = f + 0x1p-24f;
+      sh->above = uint32_t(above);
     }
   };
   begin(0);
@@ -1143,13 +1176,13 @@ __global__ void __launch_bounds__(kThreads, 1) mix_kernel(const __grid_constant_
   } else if (warp < kOutWarp) {
     regs_dec<weigh_regs(EXACT)>();
     do {
-      WeighRole r{*at, w, sh, warp - kWeighWarp, int(threadIdx.x & 31)};
+      WeighRole r{*at, w, sh, log_decay, warp - kWeighWarp, int(threadIdx.x & 31)};
       r.run();
     } while (next(++unit));
   } else if (warp < kLoadWarp) {
     regs_dec<kOutRegs>();
     do {
-      OutRole<DK, DV> r{*at, w, sh, smem, head, warp - kOutWarp, int(threadIdx.x & 31)};
+      OutRole<DK, DV> r{*at, w, sh, smem, log_decay, head, warp - kOutWarp, int(threadIdx.x & 31)};
       r.run();
     } while (next(++unit));
   } else {

@@ -866,3 +866,34 @@ def test_linattn_states_pass_empty_sequences_bit_for_bit(dm, scale):
                 state=c["state"], dfinal_state=c["dfinal"], dstate=c["dstate"])
     for i in (0, 2):
         assert torch.equal(c["final"][i], c["state"][i]) and torch.equal(c["dstate"][i], c["dfinal"][i])
+
+
+# ------------------------------------------------------------------ slow heads
+def test_states_of_slow_heads_do_not_drift(dm):
+    """2^20 tokens in one chain of blocks (a CTA to a head), terms of one sign: what a decay loses when
+    it is rounded to fp32 must not add up over the blocks that a slow head remembers.  A term is within
+    1.25 * 2^-16; two roundings of 2^-24 a block fall to either side (terms are random): six deviations
+    of their sum, at most sqrt(2 blocks / 3) * 2^-24, two blocks' worth of a state that grew to its size
+    over all of them counting for no more than their average of a third."""
+    tokens, heads, d = 1 << 20, 152, 8
+    g = torch.tensor([-1e-6, -2e-7, -5e-8, -5e-7, -2e-3, 0.0, -7e-9, -3.3e-5], device="cuda")
+    draw = Draw(44)
+    k, v = (draw((tokens, heads, d)).abs_() for _ in range(2))
+    final = torch.empty((1, heads, d, d), device="cuda")
+    op, out = dm.LinearAttention(tokens, heads, d), torch.empty_like(v)
+    op.forward(k, k, v, g.repeat(heads // 8), out, final_state=final)
+    assert op.status() == dm.OK
+    far = torch.arange(tokens - 1, -1, -1, device="cuda", dtype=torch.float64)
+    tolerance = 1.25 * 2.0 ** -16 + 6 * 2.0 ** -24 * (2 * tokens / 128 / 9) ** 0.5
+    for h in range(8):
+        want = (k[:, h].double() * torch.exp(g[h].double() * far)[:, None]).T @ v[:, h].double()
+        err = float((final[0, h].double() / want - 1).abs().max())
+        assert err <= tolerance, (float(g[h]), err)
+    # against time, k for queries: the first state's gradient, every term decayed once more
+    op.backward(v, k, k, v, g.repeat(heads // 8), *(torch.empty_like(v) for _ in range(3)), dstate=final)
+    assert op.status() == dm.OK
+    for h in range(8):
+        weight = d ** -0.5 * torch.exp(g[h].double() * (far.flip(0) + 1))
+        want = (k[:, h].double() * weight[:, None]).T @ v[:, h].double()
+        err = float((final[0, h].double() / want - 1).abs().max())
+        assert err <= tolerance, ("dstate", float(g[h]), err)

@@ -504,7 +504,7 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
 /*
  * dmuon_linattn_step -- one token for each of `tokens` streams (shape.sequences is not used):
  * row r reads the state of slot[r], writes the state after its token and its output, all in
- * fp32 but for the bf16 output.
+ * fp32 but for the bf16 output (and exp(log_decay) to more, so that many steps of a slow head keep it).
  *   slot       device, int32 per row, or NULL: row r has slot r.  A slot outside [0, slots)
  *              skips its row (padding): nothing of it is read or written.  Rows that share a
  *              slot are taken one after another in their order.

@@ -5,7 +5,7 @@
 // pieces of 32 (128 bytes of a row), a block takes the key_dim rows of one piece, all its
 // loads in flight at once, and no block waits for another.  8 lanes hold a row, 16 rows at a
 // time; the 16 sums of a column meet by shuffles and through shared memory, in that order.
-// Measured, 250 streams of 32 heads of 128 x 128: 155 to 158 us, 6.7 TB/s, the copy rate; one stream 3.5 us,
+// Measured, 250 streams of 32 heads of 128 x 128: 155 us a pass, 6.8 TB/s, the copy rate; one stream 3.5 us,
 // a launch's latency.
 #include "mix.h"
 #include "ptx.cuh"
@@ -18,7 +18,7 @@ constexpr int kPasses = 128 / kRowsAtOnce;
 
 __global__ void __launch_bounds__(kThreads) linattn_step_kernel(const __grid_constant__ LinStepArgs g,
                                                                 int pieces) {
-  __shared__ float sq[128], sk[128], part[kThreads / 32][kCols];
+  __shared__ float sq[128], sk[128], part[kThreads / 32][kCols], decay[2];
   grid_launch_dependents();
   grid_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) linattn_step_kernel(const __grid_con
   }
   const int c0 = piece * kCols + (lane & 7) * 4, r0 = tid >> 3;
   const bool in = c0 < g.dv;
-  const float a = expf(g.log_decay[head]);
+  const float log_decay = g.log_decay[head];
   const long long at = ((slot * g.heads + head) * g.dk + r0) * g.dv + c0;
   const long long step = (long long)kRowsAtOnce * g.dv;
   float4 st[kPasses];
@@ -56,17 +56,39 @@ __global__ void __launch_bounds__(kThreads) linattn_step_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __bfloat162float(vp[i]);
     }
+    // a and, of a slow head, what its rounding drops: over thousands of steps an error with one sign
+    // would add up (8000 of log_decay -1e-6: 3e-4 of the state).  a rounded down, so that the rest of
+    // an infinity has its sign.  By one thread, with all loads on their way: 250 streams 155 us, 164
+    // to 177 by each.
+    if (tid == kThreads - 1) {
+      const float e = expm1f(log_decay);
+      float a = expf(log_decay), rest = 0.f;
+      if (log_decay <= 0.f && e > -0.4375f) {
+        a = 1.f + e;
+        rest = e - (a - 1.f);  // exact
+        if (rest < 0.f) {
+          a -= 0x1p-24f;
+          rest += 0x1p-24f;
+        }
+      }
+      decay[0] = a;
+      decay[1] = rest;
+    }
     __syncthreads();
+    // k v is exact; what is left of a joins it, as a state that decays by less than its last bit
+    // would else stay as it is
+    const float a = decay[0], rest = decay[1];
+    auto stepped = [&](float x, float kv) { return fmaf(a, x, rest > 0.f ? fmaf(rest, x, kv) : kv); };
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       const int i = r0 + p * kRowsAtOnce;
       if (i < g.dk) {
         const float k = sk[i], q = sq[i];
-        st[p].x = fmaf(k, v[0], a * st[p].x);
-        st[p].y = fmaf(k, v[1], a * st[p].y);
-        st[p].z = fmaf(k, v[2], a * st[p].z);
-        st[p].w = fmaf(k, v[3], a * st[p].w);
+        st[p].x = stepped(st[p].x, k * v[0]);
+        st[p].y = stepped(st[p].y, k * v[1]);
+        st[p].z = stepped(st[p].z, k * v[2]);
+        st[p].w = stepped(st[p].w, k * v[3]);
         o[0] = fmaf(q, st[p].x, o[0]);
         o[1] = fmaf(q, st[p].y, o[1]);
         o[2] = fmaf(q, st[p].z, o[2]);

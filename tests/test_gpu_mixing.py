@@ -897,3 +897,33 @@ def test_states_of_slow_heads_do_not_drift(dm):
         want = (k[:, h].double() * weight[:, None]).T @ v[:, h].double()
         err = float((final[0, h].double() / want - 1).abs().max())
         assert err <= tolerance, ("dstate", float(g[h]), err)
+
+
+def test_steps_of_slow_heads_do_not_drift(dm):
+    """8000 single tokens of one sign: what exp(log_decay) loses when it is rounded to fp32 must not add
+    up.  Three roundings of 2^-24 a step fall to either side (terms are random): six deviations of
+    their sum, each counting as the state's size then did, a third of its last on average."""
+    heads, d, n = 8, 64, 8000
+    g = torch.tensor([-1e-6, -2e-7, -4.5e-8, -1e-7, -2e-4, 0.0, -7e-9, -3.3e-5], device="cuda")
+    draw = Draw(45)
+    k, v = (draw((n, heads, d)).abs_() for _ in range(2))
+    s, op = torch.zeros((1, heads, d, d), device="cuda"), dm.LinearAttention(1, heads, d)
+    out = torch.empty_like(v[:1])
+    for t in range(n):
+        op.step(k[t:t + 1], k[t:t + 1], v[t:t + 1], g, s, out)
+    w = torch.exp(g.double() * torch.arange(n - 1, -1, -1, device="cuda").double()[:, None])
+    want = torch.einsum("th,thi,thj->hij", w, k.double(), v.double())
+    err = (s[0].double() / want - 1).abs().amax(dim=(1, 2))
+    assert float(err.max()) <= 6 * 2.0 ** -24 * (3 * n / 9) ** 0.5, err.tolist()
+
+
+def test_steps_keep_infinities(dm):
+    """An infinity in a state stays one in slow and in fast heads, and a zero a zero."""
+    heads, d = 4, 32
+    g = torch.tensor([-1e-6, 0.0, -3.0, -0.3], device="cuda")
+    z = torch.zeros((1, heads, d), dtype=torch.bfloat16, device="cuda")
+    s = torch.zeros((1, heads, d, d), device="cuda")
+    s[0, :, 3, 5], s[0, :, 7, 9] = float("inf"), -float("inf")
+    want = s.clone()
+    dm.LinearAttention(1, heads, d).step(z, z, z, g, s, torch.empty_like(z))
+    assert torch.equal(s, want)

@@ -657,8 +657,14 @@ _pack_heads = struct.Struct("3q").pack
 _BF16 = torch.bfloat16
 
 
+def _required(t: Optional[torch.Tensor], what: str) -> None:
+    if t is None:
+        raise TypeError(f"{what}: expected a tensor, got None")
+
+
 def _heads(t: torch.Tensor, shape, what: str, dev: int) -> bytes:
     """Check a (tokens, heads, dim) bf16 tensor on device `dev`; its dmuon_heads."""
+    _required(t, what)
     token, head, unit = t.stride() if t.dim() == 3 else (0, 0, 0)
     if t.dtype is _BF16 and unit == 1 and t.get_device() == dev and t.shape == shape:
         return _pack_heads(t.data_ptr(), token, head)
@@ -673,6 +679,7 @@ def _heads(t: torch.Tensor, shape, what: str, dev: int) -> bytes:
 
 def _flat(t: torch.Tensor, dtype, shape, what: str, dev: int) -> int:
     """_dense, with one test where all is well."""
+    _required(t, what)
     if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     return _dense(t, dtype, shape, what, dev)
@@ -709,6 +716,7 @@ class QKNormRope:
                        self.interleaved, self.eps)
 
     def _begin(self, q):
+        _required(q, "q")
         t = q.shape[0] if q.dim() == 3 else -1
         if t < 0 or t > self.max_tokens:
             raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.q_heads}, "
@@ -800,6 +808,7 @@ class LinearAttention:
         return LinattnShape(tokens, sequences, self.heads, self.key_dim, self.value_dim, self.scale)
 
     def _begin(self, q, offsets=None):
+        _required(q, "q")
         t = q.shape[0] if q.dim() == 3 else -1
         if t < 0 or t > self.max_tokens:
             raise ValueError(f"q: expected (tokens <= {self.max_tokens}, {self.heads}, "
@@ -855,8 +864,10 @@ class LinearAttention:
     def step(self, q, k, v, log_decay, state, out, new_state=None, slots=None, stream=None) -> None:
         """One token for each of q.shape[0] streams: row r reads state[slots[r]] (None: state[r])
         and writes the state after its token to the same place of `new_state` (None: of `state`).
-        A slot outside the states skips its row; rows that share one are taken in their order."""
+        A slot outside the states skips its row; rows that share one are taken in their order.
+        The workspace is not used."""
         t, _, shape, ks, vs, _, dev = self._begin(q)
+        _required(state, "state")
         if state.dim() != 4:
             raise ValueError(f"state: expected 4 dimensions, got {tuple(state.shape)}")
         n = state.shape[0]

@@ -927,3 +927,25 @@ def test_steps_keep_infinities(dm):
     want = s.clone()
     dm.LinearAttention(1, heads, d).step(z, z, z, g, s, torch.empty_like(z))
     assert torch.equal(s, want)
+
+
+def test_required_tensors_may_not_be_none(dm):
+    draw = Draw(49)
+    q, k, v = (draw((4, 2, 64)) for _ in range(3))
+    f, pos = rope_reference(64, 64), torch.arange(4, device="cuda", dtype=torch.int32)
+    rope, mix, g = dm.QKNormRope(4, 2, 2, 64), dm.LinearAttention(4, 2, 64), torch.zeros(2, device="cuda")
+    state = torch.zeros((4, 2, 64, 64), device="cuda")
+    e = [torch.empty_like(q) for _ in range(3)]
+
+    def each(call, args, optional=()):
+        for i in range(len(args)):
+            if i not in optional:
+                with pytest.raises(TypeError):
+                    call(*args[:i], None, *args[i + 1:])
+        call(*args)
+
+    each(rope.forward, [q, k, None, None, f, pos, e[0], e[1]], (2, 3))
+    each(rope.backward, [q, k, q, k, None, None, f, pos, e[0], e[1]], (4, 5))
+    each(mix.forward, [q, k, v, g, e[0]])
+    each(mix.backward, [v, q, k, v, g, *e])
+    each(mix.step, [q, k, v, g, state, e[0]])

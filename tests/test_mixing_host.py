@@ -351,3 +351,25 @@ def test_gradients_of_states_refuse_far_scales(dm):
         assert lin_back(dm, shape=s) not in ARGUMENT
         for states in (dict(dfin=W), dict(dst=W), dict(dfin=W, dst=W)):
             assert (lin_back(dm, shape=s, **states) == dm.ERR_UNSUPPORTED) == (not ok), (scale, states)
+
+
+def test_required_tensors_may_not_be_none(dm, monkeypatch):
+    """Every tensor that a call cannot do without is refused by its name."""
+    monkeypatch.setattr(dm, "_launch_device", lambda t, what: -1)
+    monkeypatch.setattr(dm, "_launch_stream", lambda stream, dev: 0)
+    x, g, f, pos = torch.zeros((4, 2, 64), dtype=torch.bfloat16), torch.zeros(2), torch.zeros(32), torch.zeros(4).int()
+    rope, mix = dm.QKNormRope(4, 2, 2, 64, device="cpu"), dm.LinearAttention(4, 2, 64, device="cpu")
+    calls = [(rope.forward, [("q", x), ("k", x), (None, None), (None, None), ("inv_freq", f), ("position", pos),
+                             ("q_out", x), ("k_out", x)]),
+             (rope.backward, [("dq_out", x), ("dk_out", x), ("q", x), ("k", x), (None, None), (None, None),
+                              ("inv_freq", f), ("position", pos), ("dq", x), ("dk", x)]),
+             (mix.forward, [("q", x), ("k", x), ("v", x), ("log_decay", g), ("out", x)]),
+             (mix.backward, [("dout", x), ("q", x), ("k", x), ("v", x), ("log_decay", g), ("dq", x), ("dk", x),
+                             ("dv", x)]),
+             (mix.step, [("q", x), ("k", x), ("v", x), ("log_decay", g), ("state", torch.zeros(4, 2, 64, 64)),
+                         ("out", x)])]
+    for call, args in calls:
+        for i, (name, _) in enumerate(args):
+            if name is not None:
+                with pytest.raises(TypeError, match=f"^{name}: expected a tensor, got None"):
+                    call(*(None if j == i else v for j, (_, v) in enumerate(args)))

@@ -949,3 +949,23 @@ def test_required_tensors_may_not_be_none(dm):
     each(mix.forward, [q, k, v, g, e[0]])
     each(mix.backward, [v, q, k, v, g, *e])
     each(mix.step, [q, k, v, g, state, e[0]])
+
+
+def test_gains_gradients_at_far_addresses(dm):
+    """Tokens so far apart that offsets pass 32 bits give the gains' gradients of the same tokens
+    side by side."""
+    tokens, heads, d, apart = 300, 2, 64, 1 << 24
+    far = torch.empty(tokens * apart, dtype=torch.bfloat16, device="cuda")
+    f, pos = rope_reference(d, d), torch.arange(tokens, device="cuda", dtype=torch.int32)
+    w, seen = [Draw(50 + i)((d,)) for i in range(2)], []
+    for i in range(2):
+        draw = Draw(52)
+        rows = [draw((tokens, heads, d)) for _ in range(4)]
+        to = [torch.empty_like(rows[0]) for _ in range(2)]
+        if i == 1:
+            place = [far.as_strided((tokens, heads, d), (apart, d, 1), j * heads * d) for j in range(6)]
+            rows, to = [p.copy_(r) for p, r in zip(place, rows)], place[4:]
+        dw = [torch.full((d,), SENTINEL, dtype=torch.bfloat16, device="cuda") for _ in w]
+        dm.QKNormRope(tokens, heads, heads, d).backward(*rows, *w, f, pos, *to, *dw)
+        seen.append([x.clone() for x in to] + dw)
+    assert all(torch.equal(a, b) for a, b in zip(*seen))

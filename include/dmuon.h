@@ -416,12 +416,13 @@ typedef struct {
  *   w_q, w_k   device, bf16 gains, head_dim each; NULL: gains of 1
  *   inv_freq   device, fp32, rotary_dim / 2 angles per position
  *   position   device, int32 per token (any value)
- * The angle is taken modulo a turn in 64-bit fixed point, so that far positions lose nothing:
- * sines and cosines are within 2^-21 for any position.  Squares are summed in fp32 (elements
- * beyond 1e18 overflow).  An output may be its own input (q_out = q, k_out = k); a NaN or an
- * infinity reaches its own head only.  One launch; no workspace.  Where all rows and gains lie at
- * 8-byte addresses they move in 8-byte pieces, else element by element.  More than 2^31 - 1 groups
- * of 4 heads in all tokens together: DMUON_ERR_UNSUPPORTED.
+ * The angle is taken modulo a turn in 64-bit fixed point, so that far positions lose nothing: sines
+ * and cosines are within 2^-21 for any position.  Squares are summed in fp32 (elements beyond 1e18
+ * overflow, and without eps heads of elements below 1e-19 lose their size).  An output may be its
+ * own input (q_out = q, k_out = k); a NaN or an infinity reaches its own head only.  One launch; no
+ * workspace.  Where all rows and gains lie at 8-byte addresses they move in 8-byte pieces, else
+ * element by element.  More than 2^31 - 1 groups of 4 heads in all tokens together:
+ * DMUON_ERR_UNSUPPORTED.
  */
 int dmuon_qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* q, const dmuon_heads* k,
                        const void* w_q, const void* w_k, const float* inv_freq,
@@ -434,7 +435,8 @@ int dmuon_qk_norm_rope(const dmuon_qk_shape* shape, const dmuon_heads* q, const 
  *   dw = sum over tokens and heads of g n
  *   dx = (g w - n mean(g w n)) / sqrt(mean(x^2) + eps)
  *   dw_q, dw_k  device, bf16, head_dim each, written, not added to; NULL: not wanted
- * dq may be dq_out, and dk dk_out.  tokens == 0 sets dw_q and dw_k to zero.
+ * dq may be dq_out, and dk dk_out.  tokens == 0 sets dw_q and dw_k to zero.  The workspace serves
+ * one call at a time.
  */
 size_t dmuon_qk_norm_rope_workspace_bytes(const dmuon_qk_shape* shape);
 int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const dmuon_heads* dq_out,
@@ -448,7 +450,7 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const dmuon_heads* 
 /* Sizes of a linear attention. */
 typedef struct {
   int64_t tokens, sequences;     /* of all sequences together; 1 <= sequences <= 65536 */
-  int64_t heads;
+  int64_t heads;                 /* sequences x heads <= 2^27 */
   int64_t key_dim, value_dim;    /* multiples of 8, at most 128 */
   float scale;                   /* its inverse is finite, too */
 } dmuon_linattn_shape;
@@ -502,9 +504,10 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
                            void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /*
- * dmuon_linattn_step -- one token for each of `tokens` streams (shape.sequences is not used):
+ * dmuon_linattn_step -- one token for each of `tokens` streams (shape.sequences is 1, or any
+ * number within its limits):
  * row r reads the state of slot[r], writes the state after its token and its output, all in
- * fp32 but for the bf16 output (and exp(log_decay) to more, so that many steps of a slow head keep it).
+ * fp32 but for the bf16 output (exp(log_decay) to more, so that many steps of a slow head keep it).
  *   slot       device, int32 per row, or NULL: row r has slot r.  A slot outside [0, slots)
  *              skips its row (padding): nothing of it is read or written.  Rows that share a
  *              slot are taken one after another in their order.

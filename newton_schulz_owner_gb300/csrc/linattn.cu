@@ -20,23 +20,32 @@
 // over the head's elements and an MN-major one where it runs over tokens, so nothing is
 // transposed.  Keys take their decay in place once the scores have read them.
 //
-// A cluster of up to 8 CTAs takes the whole packed batch of a head (or a run of its sequences),
-// cut evenly into stretches of blocks wherever sequences begin and end.  A CTA whose last sequence
-// goes on in the next one's stretch first sums that sequence's share of the state alone (keys and
+// Three operands are rounded to bf16 because the tensor core takes them so: weighted scores, the state
+// that enters a block and the decayed keys.  Outputs and gradients are 0.0026 from 64 bits by it, where
+// rounding the result alone gives 0.0017.  A second part of each would take a product and a pass of its
+// own: the keys' costs a fifth (152 heads of 5120 tokens: 125 us, 150 with it), and is taken where a
+// state is an output, which then keeps 16 bits of every term.
+//
+// A cluster of up to 8 CTAs takes the whole packed batch of a head (or a run of its sequences), cut
+// evenly into stretches of blocks wherever sequences begin and end.  A CTA whose last sequence goes
+// on in the next one's stretch first sums that sequence's share of the state alone (keys and
 // values), the shares go to the CTAs behind it through memory, and then each CTA sweeps its
 // stretch.  (Sharing again and again, in rounds short enough for keys and values to stay in L2, was
 // slower the shorter the rounds: 65536 tokens of 32 heads 829 us in rounds of 12 blocks a CTA, 797
-// of 16, 747 of 64, 738 in one.)  Where that would leave a CTA to a head, or a head's gradient, and
-// SMs without one or a last wave of few, sequences are instead dealt whole to all SMs (deal()).
+// of 16, 747 of 64, 738 in one, which is 675 to 690 now.)  Where that would leave a CTA to a head,
+// or a head's gradient, and SMs without one or a last wave of few, sequences are instead dealt
+// whole to all SMs (deal()).
 //
-// Bound, with a head to each SM, by HBM and by the SM's shared memory at once: of the 5500 cycles of
-// a block of 128 x 128 heads about 2450 go to the warps' reads and writes there, 1800 to operands of
-// products, 1000 to copies, and little else can run beside them; the tensor cores are busy for 30%.
-// 152 heads of 5120 tokens take 124 us, 6.4 TB/s of q, k, v and out, 0.95 of the copy rate (145 us
-// where a final state is written, 74 us of 64 elements: 5.4 TB/s).  With fewer heads, keys and values
-// are read twice and not all SMs take part: 8192 tokens of 32 heads 85 us (40 at the copy rate),
-// 65536 tokens with states 676 (318).  The gradients of 8192 tokens of 32 heads in 5 sequences take
-// 149 us (69), dealt: 44 to 49 blocks to each SM, 3.1 us a block.
+// Bound, with a head to each SM, by HBM and by the SM's shared memory at once: of the 5500 cycles
+// of a block of 128 x 128 heads about 2450 go to the warps' reads and writes there, 1800 to
+// operands of products, 1000 to copies, and little else can run beside them; the tensor cores are
+// busy for 30%. 152 heads of 5120 tokens take 125 us, 6.4 TB/s of q, k, v and out, 0.94 of the copy
+// rate (150 us where a final state is written, 74 us of 64 elements: 5.4 TB/s).  With fewer heads,
+// keys and values are read twice and not all SMs take part: 8192 tokens of 32 heads 85 us (40 at
+// the copy rate), 65536 tokens with states 675 to 690 (318).  Where a final state is written,
+// the warps of a CTA load and store spilled registers about 300 times a block, next to never
+// elsewhere.  The gradients of 8192 tokens of 32 heads in 5 sequences take 149 us
+// (69), dealt: 44 to 49 blocks to each SM, 3.1 us a block.
 #include "dmuon.h"
 #include "f32x2.cuh"
 #include "mix.h"
@@ -1233,7 +1242,7 @@ cudaError_t linattn_prepare(int (&fit)[kMixMaxSplit + 1]) {
     if (e != cudaSuccess) return e;
     // launched with fewer, the states' warps would wait for theirs forever
     if (a.numRegs != kRegs) return cudaErrorInvalidKernelImage;
-    if (i > 0) continue;
+    if (i > 0) continue;  // one CTA to an SM in all of them, so as many clusters fit
     fit[0] = 0;
     for (int split = 1; split <= kMixMaxSplit; ++split) {
       cudaLaunchConfig_t cfg{};

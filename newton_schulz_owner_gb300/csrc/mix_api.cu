@@ -215,10 +215,10 @@ struct States {
 struct Share {
   int groups, split, deal;
 };
-// Microseconds, measured with 128 elements to a head: a block takes 3 (exact states 3.8), 1.5 more
-// (2) where a CTA sums its share ahead; a launch 6, sharing 5.  Clusters of a size that the GPU's
-// groups of SMs do not divide into run fewer at a time (gradients of 8192 tokens of 8 heads: 24
-// clusters of 6 111 us, of 4 77).
+// Microseconds, measured with 128 elements to a head and taken for fewer, too (a block of 64 takes
+// 1.9): a block takes 3 (exact states 3.8), 1.5 more (2) where a CTA sums its share ahead; a launch
+// 6, sharing 5.  Clusters of a size that the GPU's groups of SMs do not divide into run fewer at a
+// time (gradients of 8192 tokens of 8 heads: 24 clusters of 6 111 us, of 4 77).
 Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const Device& device) {
   const int64_t blocks = s.tokens / kMixBlock + std::min(s.sequences, s.tokens);  // at most
   const double one = double(blocks) / double(s.sequences);
@@ -245,10 +245,12 @@ Share choose_share(const dmuon_linattn_shape& s, int sweeps, bool exact, const D
     }
     if (clusters >= device.sms) break;
   }
-  // Dealing whole sequences: the longest of n, cut at random, is H_n / n of the batch; each takes 4 us to
-  // begin, and with all SMs busy a block takes longer.  (Gradients of 8192 tokens of 32 heads in 5 sequences: a CTA to a head and gradient 180 us,
-  // dealt 149; of 4096 tokens of 28 heads, 3 CTAs to each 110 to 124, dealt 79 to 84, but in 2 equal
-  // sequences 87 and 93; 8192 of 40 heads in 30 sequences 250 and 312.)  Not where one long sequence among short ones would lose much by it.
+  // Dealing whole sequences: the longest of n, cut at random, is H_n / n of the batch; each takes 4
+  // us to begin, and with all SMs busy a block takes longer.  (Gradients of 8192 tokens of 32 heads
+  // in 5 sequences: a CTA to a head and gradient 180 us, dealt 149; of 4096 tokens of 28 heads, 3
+  // CTAs to each 110 to 124, dealt 79 to 84, but in 2 equal sequences 87 and 93; 8192 of 40 heads
+  // in 30 sequences 250 and 312.)  Not where one long sequence among short ones would lose much by
+  // it.
   const int64_t pairs = sweeps * s.heads, ctas = std::min(int64_t(device.sms), pairs * s.sequences);
   if (whole <= 1.25 * least && !exact && s.sequences > 1 && s.sequences < 32 &&
       pairs * s.sequences <= ctas * (kMixDealt / 2)) {
@@ -471,9 +473,10 @@ int dmuon_linattn_backward(const dmuon_linattn_shape* shape, const dmuon_heads* 
                            {&vr, &dor, &qr, &dkr, true, dfinal_state, nullptr, true, scaled},
                            {&kr, &qr, &dor, &dvr, true, dfinal_state, dstate, false, scaled}};
   if (s.tokens == 0) return run_sweeps(s, sweeps + 2, 1, log_decay, offsets, device, workspace, stream);
-  // The three side by side fill the GPU without cutting sequences as finely (8192 tokens of 32 heads:
-  // 285 us one after another, 204 together).  Apart where dv's sweep is another kernel, or writes
-  // dstate, perhaps over the dfinal_state that dk's reads.
+  // The three side by side fill the GPU without cutting sequences as finely (8192 tokens of 32
+  // heads in 5 sequences: 149 us; with dstate, in two launches with keys kept to 16 bits, 285).
+  // Apart where dv's sweep is another kernel, or writes dstate, perhaps over the dfinal_state that
+  // dk's reads.
   const bool apart = dstate != nullptr || (s.key_dim <= 64) != (s.value_dim <= 64);
   e = run_sweeps(s, sweeps, apart ? 2 : 3, log_decay, offsets, device, workspace, stream);
   if (e != DMUON_OK || !apart) return e;

@@ -30,11 +30,12 @@ DM_DEV void mbar_init(uint64_t* bar, uint32_t count) {
                : "memory");
 }
 
-// Make barrier initialisation visible to the async proxy (TMA, tcgen05).
 // Ends a barrier's life: its memory may then be initialised again.
 DM_DEV void mbar_inval(uint64_t* bar) {
   asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+
+// Make barrier initialisation visible to the async proxy (TMA, tcgen05).
 DM_DEV void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

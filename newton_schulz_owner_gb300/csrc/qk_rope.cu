@@ -430,8 +430,8 @@ cudaError_t launch_rope(RopeArgs& g, bool backward, bool interleaved, bool vec, 
                        : lanes == 16 ? kernel_of<16>(backward, interleaved, vec)
                                      : kernel_of<32>(backward, interleaved, vec);
   // Chunks of a warp share their token's sines; but with few tokens more warps of one chunk each
-  // fill the GPU (8192 tokens of 64 heads of 128: 52 us with 2 chunks to a warp, 48 with 8, backward 82
-  // with 2, 75 with 4, 73 with 8; 777 of 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take
+  // fill the GPU (8192 tokens of 64 heads of 128, an earlier kernel: 52 us with 2 chunks to a warp, 48 with
+  // 8, which is 44 now; backward 82 with 2, 75 with 4, 73 with 8; 777 of 32: 5.1 with one, 6.2 with 2).  Backward, blocks stay and take
   // token after token, so that the gains' sums meet once a block (88 us with twice the blocks that
   // fit, 82 with as many).
   const int heads = 32 / lanes * 4;

@@ -5,7 +5,7 @@
 // pieces of 32 (128 bytes of a row), a block takes the key_dim rows of one piece, all its
 // loads in flight at once, and no block waits for another.  8 lanes hold a row, 16 rows at a
 // time; the 16 sums of a column meet by shuffles and through shared memory, in that order.
-// Measured, 250 streams of 32 heads of 128 x 128: 155 us a pass, 6.8 TB/s, the copy rate; one stream 3.5 us,
+// Measured, 250 streams of 32 heads of 128 x 128: 155 us a pass, 6.8 TB/s, the copy rate; one stream 3.8 us,
 // a launch's latency.
 #include "mix.h"
 #include "ptx.cuh"

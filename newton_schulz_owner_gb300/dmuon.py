@@ -692,7 +692,8 @@ class QKNormRope:
     Queries are (tokens, q_heads, head_dim), keys (tokens, k_heads, head_dim), bf16, any strides
     between tokens and heads (slices of one packed projection, say); outputs may be the inputs.
     Gains are bf16 (head_dim,) or None for ones, `inv_freq` fp32 (rotary_dim / 2,), positions
-    int32 (tokens,).  `k_heads` = 0 takes queries alone (pass None for keys).
+    int32 (tokens,).  `k_heads` = 0 takes queries alone (pass None for keys).  The workspace serves
+    one backward at a time.
     """
 
     def __init__(self, max_tokens: int, q_heads: int, k_heads: int, head_dim: int,
@@ -848,7 +849,8 @@ class LinearAttention:
     def backward(self, dout, q, k, v, log_decay, dq, dk, dv, offsets=None, state=None,
                  dfinal_state=None, dstate=None, stream=None) -> None:
         """Gradients of q, k, v and (if `dstate` is given) of `state`, from those of out and
-        (None: zeros) of final_state."""
+        (None: zeros) of final_state; with either of the states' gradients the scale lies between
+        2 ** -64 and 2 ** 64."""
         if not self.with_backward:
             raise ValueError("this LinearAttention was made without a backward pass")
         t, n, shape, ks, vs, off, dev = self._begin(q, offsets)
